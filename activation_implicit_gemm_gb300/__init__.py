@@ -4,6 +4,10 @@ A thin Python binding over the C ABI of libfconv.so (include/fconv.h). PyTorch o
 provides device memory and streams; every step of the convolution runs in the
 library's CUDA kernels. There is no CPU path: without the built library every call
 raises.
+
+Beside it, the operators that follow a patch embedding (include/fconv_ops.h): layer_norm over
+rows or channels-first features, rope (rotary positions with one to three axes) and attention,
+each with its gradient.
 """
 from __future__ import annotations
 
@@ -14,14 +18,18 @@ from . import _lib
 from ._lib import ROUTES, ROUTE_NAMES, STATUS
 
 __all__ = ["FconvError", "FusedConvPlan", "fused_conv", "conv_transpose", "plan_for", "load_library",
-           "build"]
+           "build", "LayerNormPlan", "RopePlan", "AttentionPlan", "layer_norm",
+           "layer_norm_backward", "rope", "rope_frequencies", "attention",
+           "attention_backward"]
 
 
 class FconvError(RuntimeError):
     def __init__(self, status: int, where: str = ""):
         self.status = status
         self.code = STATUS.get(status, str(status))
-        msg = _lib.load().fconv_status_string(status).decode()
+        lib = _lib.load()
+        text = lib.fconv_status_string if status < 32 else _ops.load().fconv_ops_status_string
+        msg = text(status).decode()
         super().__init__(f"{where}: {self.code} ({msg})" if where else f"{self.code} ({msg})")
 
 
@@ -209,3 +217,8 @@ def conv_transpose(x, w, b=None, z=None, *, group: int = 1, strides=None, dilati
                  activation=activation, activation_params=activation_params, transposed=True,
                  output_padding=output_padding)
     return p.run(x, w, b, z, y=out)
+
+
+from . import _ops  # noqa: E402
+from ._ops import (AttentionPlan, LayerNormPlan, RopePlan, attention,  # noqa: E402
+                   attention_backward, layer_norm, layer_norm_backward, rope, rope_frequencies)

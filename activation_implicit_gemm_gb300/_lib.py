@@ -20,7 +20,8 @@ STATUS = {0: "OK", 1: "E_NULL", 2: "E_RANK", 3: "E_ATTR_LENGTH", 4: "E_ATTR_VALU
           5: "E_PADS_WITH_AUTOPAD", 6: "E_KERNEL_SHAPE", 7: "E_GROUP", 8: "E_BIAS_SHAPE",
           9: "E_Z_SHAPE", 10: "E_ACT_PARAMS", 11: "E_ACTIVATION", 12: "E_OUTPUT_EMPTY",
           13: "E_WORKSPACE", 14: "E_UNSUPPORTED", 15: "E_CUDA", 16: "E_DEVICE_TIMEOUT",
-          17: "E_NOMEM", 18: "E_ALIGNMENT", 19: "E_ALIAS"}
+          17: "E_NOMEM", 18: "E_ALIGNMENT", 19: "E_ALIAS",
+          32: "E_EXTENT", 33: "E_STRIDE", 34: "E_MASK"}
 
 I64 = ctypes.c_int64
 

@@ -1,0 +1,510 @@
+"""Token-side operators over the C ABI in include/fconv_ops.h: layer norm, rotary positions
+with several axes, and attention, each with its gradient.
+
+As with the convolution, PyTorch only provides device memory and streams: plans are cached by
+shape and strides, arguments are checked here and in the library, and every step runs in the
+library's CUDA kernels on the current stream of the tensors' device (or the one given).
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional, Sequence
+
+from . import FconvError, _lib
+
+I64, I32, F32 = ctypes.c_int64, ctypes.c_int, ctypes.c_float
+VP, SZ = ctypes.c_void_p, ctypes.c_size_t
+BF16 = 2
+PAIRINGS = {"interleaved": 0, "half": 1, "half_per_axis": 2}
+ATTN_ROUTES = {"auto": 0, "simple": 1, "tc": 2}
+ATTN_ROUTE_NAMES = {v: k for k, v in ATTN_ROUTES.items()}
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("dtype", I32), ("param_dtype", I32), ("outer", I64), ("channels", I64),
+                ("inner", I64), ("has_weight", I32), ("has_bias", I32), ("eps", F32)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("dtype", I32), ("batch", I64), ("len", I64), ("heads_q", I64),
+                ("heads_k", I64), ("head_dim", I64), ("q_stride", I64 * 3),
+                ("k_stride", I64 * 3), ("q_out_stride", I64 * 3), ("k_out_stride", I64 * 3),
+                ("axes", I32), ("section", I64 * 3), ("pairing", I32), ("pos_type", I32),
+                ("pos_batch", I64), ("inverse", I32)]
+
+
+class AttnDesc(ctypes.Structure):
+    _fields_ = [("dtype", I32), ("batch", I64), ("len_q", I64), ("len_k", I64),
+                ("heads_q", I64), ("heads_kv", I64), ("head_dim", I64), ("q_stride", I64 * 3),
+                ("k_stride", I64 * 3), ("v_stride", I64 * 3), ("out_stride", I64 * 3),
+                ("dout_stride", I64 * 3), ("dq_stride", I64 * 3), ("dk_stride", I64 * 3),
+                ("dv_stride", I64 * 3), ("scale", F32), ("causal", I32), ("has_q_lens", I32),
+                ("has_kv_lens", I32), ("training", I32)]
+
+
+_PROTOS = {
+    "fconv_norm_plan_create": [ctypes.POINTER(NormDesc), I32, ctypes.POINTER(VP)],
+    "fconv_norm_workspace_size": [VP, ctypes.POINTER(SZ)],
+    "fconv_norm_forward": [VP] * 8,
+    "fconv_norm_backward": [VP] * 10 + [SZ, VP],
+    "fconv_norm_destroy": [VP],
+    "fconv_rope_plan_create": [ctypes.POINTER(RopeDesc), I32, ctypes.POINTER(VP)],
+    "fconv_rope_run": [VP] * 8,
+    "fconv_rope_destroy": [VP],
+    "fconv_attn_plan_create": [ctypes.POINTER(AttnDesc), I32, I32, ctypes.POINTER(VP)],
+    "fconv_attn_plan_route": [VP, ctypes.POINTER(I32)],
+    "fconv_attn_forward_workspace": [VP, ctypes.POINTER(SZ)],
+    "fconv_attn_backward_workspace": [VP, ctypes.POINTER(SZ)],
+    "fconv_attn_forward": [VP] * 9 + [SZ, VP],
+    "fconv_attn_backward": [VP] * 13 + [SZ, VP],
+    "fconv_attn_destroy": [VP],
+    "fconv_ops_check_device": [VP],
+    "fconv_ops_status_string": [I32],
+}
+_ready = None
+
+
+def load() -> ctypes.CDLL:
+    """The library with these operators' prototypes set."""
+    global _ready
+    if _ready is None:
+        lib = _lib.load()
+        for name, args in _PROTOS.items():
+            f = getattr(lib, name)
+            f.argtypes = args
+            f.restype = I32
+        for name in ("fconv_norm_destroy", "fconv_rope_destroy", "fconv_attn_destroy"):
+            getattr(lib, name).restype = None
+        lib.fconv_ops_status_string.restype = ctypes.c_char_p
+        _ready = lib
+    return _ready
+
+
+def _check(status: int, where: str):
+    if status:
+        raise FconvError(status, where)
+
+
+def check_device(stream=None) -> None:
+    """Synchronise `stream` and raise if a kernel of these operators gave up a wait."""
+    _check(load().fconv_ops_check_device(None if stream is None else stream.cuda_stream),
+           "check_device")
+
+
+def _code(dtype) -> int:
+    import torch
+    code = {torch.float32: _lib.F32, torch.float16: _lib.F16, torch.bfloat16: BF16}.get(dtype)
+    if code is None:
+        raise FconvError(14, f"dtype {dtype}")
+    return code
+
+
+class _Plan:
+    """Owns a plan of the C library; `kind` names its entry points."""
+
+    kind = ""
+
+    def _create(self, desc, device, *extra):
+        self._lib = load()
+        self._ptr = VP()
+        create = getattr(self._lib, f"fconv_{self.kind}_plan_create")
+        _check(create(ctypes.byref(desc), device, *extra, ctypes.byref(self._ptr)),
+               f"fconv_{self.kind}_plan_create")
+
+    def _bytes(self, name) -> int:
+        n = SZ()
+        _check(getattr(self._lib, name)(self._ptr, ctypes.byref(n)), name)
+        return n.value
+
+    def __del__(self):
+        try:
+            if self._ptr:
+                getattr(self._lib, f"fconv_{self.kind}_destroy")(self._ptr)
+                self._ptr = VP()
+        except Exception:
+            pass
+
+
+def _on_cuda(who: str, *tensors) -> None:
+    device = tensors[0].device
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device != device):
+            raise ValueError(f"{who} runs on tensors of one CUDA device only")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+class _Stream:
+    """The stream of a call: the given one, or the current one of the tensors' device. Inside
+    the block new tensors belong to that stream."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.stream = torch.cuda.current_stream(device) if stream is None else stream
+        self.ctx = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _workspace(nbytes: int, device):
+    import torch
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+# -------------------------------------------------------------------------------- layer norm
+
+class LayerNormPlan(_Plan):
+    """A validated layer norm: x (outer, channels, inner) normalised over channels."""
+
+    kind = "norm"
+
+    def __init__(self, dtype: int, outer: int, channels: int, inner: int = 1, *,
+                 param_dtype: Optional[int] = None, has_weight: bool = True,
+                 has_bias: bool = True, eps: float = 1e-5, device: int = -1):
+        desc = NormDesc(dtype, dtype if param_dtype is None else param_dtype, outer, channels,
+                        inner, int(has_weight), int(has_bias), eps)
+        self._create(desc, device)
+        self.workspace_bytes = self._bytes("fconv_norm_workspace_size")
+
+    def forward_ptrs(self, x, w, b, y, mean, rstd, stream) -> None:
+        """Enqueue on raw device pointers (ints or None)."""
+        _check(self._lib.fconv_norm_forward(self._ptr, x, w, b, y, mean, rstd, stream),
+               "fconv_norm_forward")
+
+    def backward_ptrs(self, dy, x, w, mean, rstd, dx, dw, db, ws, ws_bytes, stream) -> None:
+        _check(self._lib.fconv_norm_backward(self._ptr, dy, x, w, mean, rstd, dx, dw, db, ws,
+                                             ws_bytes, stream), "fconv_norm_backward")
+
+
+_norm_plans: dict = {}
+
+
+def _norm_plan(who, x, weight, bias, axis, eps):
+    key = (x.dtype, x.shape, axis, None if weight is None else weight.dtype,
+           None if bias is None else bias.dtype, eps, x.device)
+    p = _norm_plans.get(key)
+    if p is None:
+        if not -x.dim() <= axis < x.dim():
+            raise ValueError(f"{who}: axis {axis} of a tensor with {x.dim()} axes")
+        axis %= x.dim()
+        param = weight if weight is not None else bias
+        if weight is not None and bias is not None and weight.dtype != bias.dtype:
+            raise ValueError(f"{who}: weight and bias must have one type")
+        p = LayerNormPlan(_code(x.dtype), math.prod(x.shape[:axis]), x.shape[axis],
+                          math.prod(x.shape[axis + 1:]),
+                          param_dtype=None if param is None else _code(param.dtype),
+                          has_weight=weight is not None, has_bias=bias is not None, eps=eps,
+                          device=x.device.index)
+        p.channels = x.shape[axis]
+        p.stat_shape = x.shape[:axis] + x.shape[axis + 1:]
+        _norm_plans[key] = p
+    for t in (weight, bias):
+        if t is not None and (t.dim() != 1 or t.shape[0] != p.channels or not t.is_contiguous()):
+            raise ValueError(f"{who}: weight and bias are vectors of {p.channels} values")
+    return p
+
+
+def layer_norm(x, weight=None, bias=None, *, axis: int = -1, eps: float = 1e-5, out=None,
+               return_stats: bool = False, stream=None):
+    """(x - mean) * rstd * weight + bias over one axis of a contiguous tensor: axis -1 for token
+    rows, axis 1 for channels-first features (N, C, D1..Dn). weight and bias have x's type or
+    float32. With return_stats also mean and rstd (float32), which the gradient takes. `out`
+    may be x."""
+    import torch
+    _on_cuda("layer_norm", x, weight, bias, out)
+    p = _norm_plan("layer_norm", x, weight, bias, axis, eps)
+    if not x.is_contiguous() or (out is not None and not out.is_contiguous()):
+        raise ValueError("layer_norm tensors must be contiguous")
+    if out is not None and (out.shape != x.shape or out.dtype != x.dtype):
+        raise ValueError("layer_norm: out must be like x")
+    with _Stream(x.device, stream) as s:
+        y = torch.empty_like(x) if out is None else out
+        mean = rstd = None
+        if return_stats:
+            mean = torch.empty(p.stat_shape, dtype=torch.float32, device=x.device)
+            rstd = torch.empty_like(mean)
+        p.forward_ptrs(_ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd), s)
+    return (y, mean, rstd) if return_stats else y
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, bias=None, *, axis: int = -1,
+                        param_grads: bool = True, stream=None):
+    """Gradients (dx, dweight, dbias) of layer_norm. mean and rstd are the forward pass's; of
+    bias only its presence and type matter. dweight and dbias are None for an absent weight or
+    bias, or without param_grads."""
+    import torch
+    _on_cuda("layer_norm_backward", dy, x, mean, rstd, weight, bias)
+    p = _norm_plan("layer_norm_backward", x, weight, bias, axis, 1e-5)
+    if dy.shape != x.shape or dy.dtype != x.dtype:
+        raise ValueError("layer_norm_backward: dy must be like x")
+    for t in (mean, rstd):
+        if t.shape != p.stat_shape or t.dtype != torch.float32:
+            raise ValueError("layer_norm_backward: mean and rstd are float32 of shape "
+                             f"{tuple(p.stat_shape)}")
+    if not all(t.is_contiguous() for t in (dy, x, mean, rstd)):
+        raise ValueError("layer_norm_backward tensors must be contiguous")
+    with _Stream(x.device, stream) as s:
+        dx = torch.empty_like(x)
+        dw = torch.empty_like(weight) if weight is not None and param_grads else None
+        db = torch.empty_like(bias) if bias is not None and param_grads else None
+        n = p.workspace_bytes if dw is not None or db is not None else 0
+        ws = _workspace(n, x.device)
+        p.backward_ptrs(_ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx),
+                        _ptr(dw), _ptr(db), _ptr(ws), n, s)
+    return dx, dw, db
+
+
+# ---------------------------------------------------------------------------------- positions
+
+
+def _heads(who: str, name: str, t) -> None:
+    if t.dim() != 4:
+        raise ValueError(f"{who}: {name} must be (batch, tokens, heads, head_dim)")
+    if t.stride(3) != 1 and t.shape[3] > 1:
+        raise ValueError(f"{who}: the last axis of {name} must be contiguous")
+
+
+class RopePlan(_Plan):
+    """A validated rotary-position call; strides are (batch, token, head) in elements."""
+
+    kind = "rope"
+
+    def __init__(self, dtype: int, batch: int, length: int, heads_q: int, heads_k: int,
+                 head_dim: int, *, q_stride, k_stride=(0, 0, 0), q_out_stride,
+                 k_out_stride=(0, 0, 0), sections: Sequence[int], pairing: str = "half",
+                 pos_type: int = 0, pos_batch: int = 1, inverse: bool = False,
+                 device: int = -1):
+        if pairing not in PAIRINGS:
+            raise ValueError(f"pairing must be one of {list(PAIRINGS)}")
+        sec = list(sections)
+        v = (I64 * 3)(*(sec + [0, 0, 0])[:3])
+        s3 = lambda s: (I64 * 3)(*s)  # noqa: E731
+        desc = RopeDesc(dtype, batch, length, heads_q, heads_k, head_dim, s3(q_stride),
+                        s3(k_stride), s3(q_out_stride), s3(k_out_stride), len(sec), v,
+                        PAIRINGS[pairing], pos_type, pos_batch, int(inverse))
+        self._create(desc, device)
+
+    def run_ptrs(self, q, k, positions, inv_freq, q_out, k_out, stream) -> None:
+        _check(self._lib.fconv_rope_run(self._ptr, q, k, positions, inv_freq, q_out, k_out,
+                                        stream), "fconv_rope_run")
+
+
+_rope_plans: dict = {}
+
+
+def rope_frequencies(sections: Sequence[int], theta: float = 10000.0, shared: bool = False,
+                     device="cuda"):
+    """inv_freq for `rope`: each axis counts its own frequencies theta^(-i / n) over its n
+    pairs, or with `shared` the axes split one sequence over all pairs."""
+    import torch
+    total = sum(sections)
+    values = []
+    for n in sections:
+        base, size = (len(values), total) if shared else (0, n)
+        values += [theta ** -((base + i) / size) for i in range(n)]
+    return torch.tensor(values, dtype=torch.float32, device=device)
+
+
+def rope(q, k=None, *, positions, inv_freq, sections: Optional[Sequence[int]] = None,
+         pairing: str = "half", inverse: bool = False, out=None, k_out=None, stream=None):
+    """Turn the pairs of q (batch, tokens, heads, head_dim), and of k in the same launch, by
+    positions * inv_freq. positions is (tokens, axes), (1, tokens, axes) or (batch, tokens,
+    axes) of int32, int64 or float32, or without the last axis for one axis; sections gives the
+    pairs of each axis in order (default: all pairs on one axis). `inverse` turns back, which
+    is the gradient. q and k may be strided views with a contiguous last axis; out and k_out
+    may be q and k. Returns q', or (q', k')."""
+    import torch
+    _on_cuda("rope", q, k, positions, inv_freq, out, k_out)
+    _heads("rope", "q", q)
+    if sections is None:
+        sections = (inv_freq.numel(),)
+        if positions.dim() in (1, 2):
+            positions = positions.unsqueeze(-1)
+    sections = tuple(sections)
+    if positions.dim() == 2:
+        positions = positions.unsqueeze(0)
+    pos_type = {torch.int32: 0, torch.int64: 1, torch.float32: 2}.get(positions.dtype)
+    if pos_type is None:
+        raise FconvError(14, f"positions of {positions.dtype}")
+    if (positions.dim() != 3 or positions.shape[0] not in (1, q.shape[0])
+            or positions.shape[1] != q.shape[1] or positions.shape[2] != len(sections)
+            or not positions.is_contiguous()):
+        raise ValueError("rope: positions must be contiguous (1 or batch, tokens, axes)")
+    if (inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous()
+            or inv_freq.numel() != sum(sections)):
+        raise ValueError("rope: inv_freq must be float32 with one value per pair")
+    if k is not None:
+        _heads("rope", "k", k)
+        if k.dtype != q.dtype or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3]:
+            raise ValueError("rope: k must have q's type, batch, tokens and head_dim")
+    for name, t, like in (("out", out, q), ("k_out", k_out, k)):
+        if t is not None:
+            if like is None or t.shape != like.shape or t.dtype != like.dtype:
+                raise ValueError(f"rope: {name} must be like its input")
+            _heads("rope", name, t)
+    with _Stream(q.device, stream) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        key = (q.dtype, q.shape, q.stride(), out.stride(), positions.shape, pos_type, sections,
+               pairing, inverse, q.device,
+               None if k is None else (k.shape, k.stride(), k_out.stride()))
+        p = _rope_plans.get(key)
+        if p is None:
+            b, t, h, d = q.shape
+            none = (0, 0, 0)
+            p = _rope_plans[key] = RopePlan(
+                _code(q.dtype), b, t, h, 0 if k is None else k.shape[2], d,
+                q_stride=q.stride()[:3], q_out_stride=out.stride()[:3],
+                k_stride=none if k is None else k.stride()[:3],
+                k_out_stride=none if k is None else k_out.stride()[:3], sections=sections,
+                pairing=pairing, pos_type=pos_type, pos_batch=positions.shape[0],
+                inverse=inverse, device=q.device.index)
+        p.run_ptrs(_ptr(q), _ptr(k), _ptr(positions), _ptr(inv_freq), _ptr(out), _ptr(k_out), s)
+    return out if k is None else (out, k_out)
+
+
+# ---------------------------------------------------------------------------------- attention
+
+class AttentionPlan(_Plan):
+    """A validated attention call; strides are (batch, token, head) in elements. A plan made
+    with `training` (and the gradients' strides) also runs the backward pass."""
+
+    kind = "attn"
+
+    def __init__(self, dtype: int, batch: int, len_q: int, len_k: int, heads_q: int,
+                 heads_kv: int, head_dim: int, *, q_stride, k_stride, v_stride, out_stride,
+                 dout_stride=(0, 0, 0), dq_stride=(0, 0, 0), dk_stride=(0, 0, 0),
+                 dv_stride=(0, 0, 0), scale: Optional[float] = None, causal: bool = False,
+                 has_q_lens: bool = False, has_kv_lens: bool = False, training: bool = False,
+                 route: str = "auto", device: int = -1):
+        if scale is None:
+            scale = 1.0 / math.sqrt(head_dim) if head_dim > 0 else 1.0
+        s3 = lambda s: (I64 * 3)(*s)  # noqa: E731
+        desc = AttnDesc(dtype, batch, len_q, len_k, heads_q, heads_kv, head_dim, s3(q_stride),
+                        s3(k_stride), s3(v_stride), s3(out_stride), s3(dout_stride),
+                        s3(dq_stride), s3(dk_stride), s3(dv_stride), scale, int(causal),
+                        int(has_q_lens), int(has_kv_lens), int(training))
+        self._create(desc, device, ATTN_ROUTES[route])
+        self.forward_workspace = self._bytes("fconv_attn_forward_workspace")
+        self.backward_workspace = self._bytes("fconv_attn_backward_workspace")
+        r = I32()
+        _check(self._lib.fconv_attn_plan_route(self._ptr, ctypes.byref(r)), "route")
+        self.route = ATTN_ROUTE_NAMES[r.value]
+
+    def forward_ptrs(self, q, k, v, q_lens, kv_lens, out, lse, ws, ws_bytes, stream) -> None:
+        _check(self._lib.fconv_attn_forward(self._ptr, q, k, v, q_lens, kv_lens, out, lse, ws,
+                                            ws_bytes, stream), "fconv_attn_forward")
+
+    def backward_ptrs(self, dout, q, k, v, out, lse, q_lens, kv_lens, dq, dk, dv, ws, ws_bytes,
+                      stream) -> None:
+        _check(self._lib.fconv_attn_backward(self._ptr, dout, q, k, v, out, lse, q_lens, kv_lens,
+                                             dq, dk, dv, ws, ws_bytes, stream),
+               "fconv_attn_backward")
+
+
+_attn_plans: dict = {}
+
+
+def _attn_args(who, q, k, v, q_lens, kv_lens):
+    import torch
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _heads(who, name, t)
+    if (k.shape != v.shape or k.dtype != q.dtype or v.dtype != q.dtype
+            or k.shape[0] != q.shape[0] or k.shape[3] != q.shape[3]):
+        raise ValueError(f"{who}: k and v must be (batch, keys, kv_heads, head_dim) of q's type")
+    for name, t in (("q_lens", q_lens), ("kv_lens", kv_lens)):
+        if t is not None and (t.dtype != torch.int32 or t.shape != q.shape[:1]
+                              or not t.is_contiguous()):
+            raise ValueError(f"{who}: {name} must be contiguous int32 with one value a sequence")
+
+
+def attention(q, k, v, *, causal: bool = False, scale: Optional[float] = None, q_lens=None,
+              kv_lens=None, out=None, return_lse: bool = False, route: str = "auto",
+              stream=None):
+    """softmax(scale * q k^T) v for q (batch, queries, heads, head_dim) and k, v (batch, keys,
+    kv_heads, head_dim); heads is a multiple of kv_heads. scale defaults to head_dim^-1/2.
+    q_lens and kv_lens (int32, one value a sequence) cut sequences short; causal lets query i
+    see keys up to i + kv_len - q_len. A query that sees no key gives 0. With return_lse also
+    the log of the softmax sums (batch, heads, queries) in float32, which the gradient takes."""
+    import torch
+    _on_cuda("attention", q, k, v, q_lens, kv_lens, out)
+    _attn_args("attention", q, k, v, q_lens, kv_lens)
+    if out is not None:
+        if out.shape != q.shape or out.dtype != q.dtype:
+            raise ValueError("attention: out must be like q")
+        _heads("attention", "out", out)
+    with _Stream(q.device, stream) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        key = (q.dtype, q.shape, k.shape, q.stride(), k.stride(), v.stride(), out.stride(),
+               causal, scale, q_lens is None, kv_lens is None, route, q.device)
+        p = _attn_plans.get(key)
+        if p is None:
+            b, lq, h, d = q.shape
+            p = _attn_plans[key] = AttentionPlan(
+                _code(q.dtype), b, lq, k.shape[1], h, k.shape[2], d, q_stride=q.stride()[:3],
+                k_stride=k.stride()[:3], v_stride=v.stride()[:3], out_stride=out.stride()[:3],
+                scale=scale, causal=causal, has_q_lens=q_lens is not None,
+                has_kv_lens=kv_lens is not None, route=route, device=q.device.index)
+        lse = None
+        if return_lse:
+            lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32,
+                              device=q.device)
+        n = p.forward_workspace
+        ws = _workspace(n, q.device)
+        p.forward_ptrs(_ptr(q), _ptr(k), _ptr(v), _ptr(q_lens), _ptr(kv_lens), _ptr(out),
+                       _ptr(lse), _ptr(ws), n, s)
+    return (out, lse) if return_lse else out
+
+
+def attention_backward(dout, q, k, v, out, lse, *, causal: bool = False,
+                       scale: Optional[float] = None, q_lens=None, kv_lens=None, dq=None,
+                       dk=None, dv=None, route: str = "auto", stream=None):
+    """Gradients (dq, dk, dv) of attention, its probabilities made again from lse. out and lse
+    are the forward pass's; dq, dk, dv may be given (strided views of one buffer, say)."""
+    import torch
+    _on_cuda("attention_backward", q, k, v, dout, out, lse, q_lens, kv_lens, dq, dk, dv)
+    _attn_args("attention_backward", q, k, v, q_lens, kv_lens)
+    for name, t, like in (("dout", dout, q), ("out", out, q), ("dq", dq, q), ("dk", dk, k),
+                          ("dv", dv, v)):
+        if t is not None:
+            if t.shape != like.shape or t.dtype != like.dtype:
+                raise ValueError(f"attention_backward: {name} has another shape or type")
+            _heads("attention_backward", name, t)
+    if (lse.shape != (q.shape[0], q.shape[2], q.shape[1]) or lse.dtype != torch.float32
+            or not lse.is_contiguous()):
+        raise ValueError("attention_backward: lse must be float32 (batch, heads, queries)")
+    with _Stream(q.device, stream) as s:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
+        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
+        dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
+        key = (q.dtype, q.shape, k.shape, q.stride(), k.stride(), v.stride(), out.stride(),
+               causal, scale, q_lens is None, kv_lens is None, route, q.device, dout.stride(),
+               dq.stride(), dk.stride(), dv.stride())
+        p = _attn_plans.get(key)
+        if p is None:
+            b, lq, h, d = q.shape
+            p = _attn_plans[key] = AttentionPlan(
+                _code(q.dtype), b, lq, k.shape[1], h, k.shape[2], d, q_stride=q.stride()[:3],
+                k_stride=k.stride()[:3], v_stride=v.stride()[:3], out_stride=out.stride()[:3],
+                dout_stride=dout.stride()[:3], dq_stride=dq.stride()[:3],
+                dk_stride=dk.stride()[:3], dv_stride=dv.stride()[:3], scale=scale,
+                causal=causal, has_q_lens=q_lens is not None, has_kv_lens=kv_lens is not None,
+                training=True, route=route, device=q.device.index)
+        n = p.backward_workspace
+        ws = _workspace(n, q.device)
+        p.backward_ptrs(_ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
+                        _ptr(q_lens), _ptr(kv_lens), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), n, s)
+    return dq, dk, dv

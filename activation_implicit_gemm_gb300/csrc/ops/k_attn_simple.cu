@@ -1,0 +1,516 @@
+// Attention forward and backward on CUDA cores (include/fconv_ops.h): every type, head length
+// up to 256 and stride.
+//
+//   s = scale q k^T,  p = softmax(s),  out = p v,  lse = log sum exp s
+// Forward: a block owns BT query rows of one head and walks the keys in tiles of BT with the
+// running maximum m and sum l of the softmax; when m grows, l and the accumulator shrink by
+// exp(m_old - m_new), so one pass suffices.
+// Backward, with p = exp(s - lse) recomputed and delta_i = sum_d dout_id out_id:
+//   dv = p^T dout,  ds = scale p (dout v^T - delta),  dq = ds k,  dk = ds^T q
+// One kernel owns query tiles (dq) and one owns key tiles (dk, dv; it walks the queries of all
+// the heads that share the key head), so every gradient has one writer and no atomics.
+//
+// Tiles lie in shared memory as f32 with rows of D + 4 floats: the 16 threads that read 16
+// neighbouring rows with 16-byte loads then touch all banks evenly. Rows past a sequence's
+// length are stored as zeros, so what the tensors hold there never enters a product. Each of
+// the 16 x 16 threads computes an R x R piece of the BT x BT scores (R = BT / 16). Bound: the
+// f32 FMA lanes (4 D FLOPs a pair forward, 14 D backward with the scores made twice).
+#include "ops_common.cuh"
+#include "ops_internal.h"
+
+#include <cmath>
+
+namespace fconv {
+namespace ops {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Geom {
+  int64_t B, Lq, Lk;
+  int Hq, Hk, G, D, Dp;  // Dp: D rounded up to 4
+  int64_t q[3], k[3], v[3], o[3], g[3], dq[3], dk[3], dv[3];
+  float scale;
+  int causal;
+  const int32_t* q_lens;
+  const int32_t* kv_lens;
+};
+
+struct Lens {
+  int64_t q, k, shift;  // causal: query i sees keys j <= i + shift
+};
+__device__ __forceinline__ Lens lens_of(const Geom& g, int64_t b) {
+  Lens l;
+  l.q = g.q_lens ? g.q_lens[b] : g.Lq;
+  l.k = g.kv_lens ? g.kv_lens[b] : g.Lk;
+  l.q = l.q < 0 ? 0 : l.q > g.Lq ? g.Lq : l.q;
+  l.k = l.k < 0 ? 0 : l.k > g.Lk ? g.Lk : l.k;
+  l.shift = l.k - l.q;
+  return l;
+}
+
+// BT rows of (row0..) of one head into shared memory; rows outside [lo, hi) become zeros.
+template <typename T, int BT>
+__device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t row_stride,
+                                          int64_t row0, int64_t lo, int64_t hi, const Geom& g) {
+  const int pitch = g.Dp + 4;
+  for (int e = threadIdx.x; e < BT * g.Dp; e += 256) {
+    const int r = e / g.Dp, d = e - r * g.Dp;
+    const int64_t row = row0 + r;
+    dst[r * pitch + d] =
+        row >= lo && row < hi && d < g.D ? to_f(src[row * row_stride + d]) : 0.0f;
+  }
+}
+
+// acc[r][c] = sum_d a[ty R + r][d] * b[tx + 16 c][d]
+template <int R>
+__device__ __forceinline__ void dot_tile(const float* a, const float* b, int Dp, int ty, int tx,
+                                         float (&acc)[R][R]) {
+  const int pitch = Dp + 4;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < R; ++c) acc[r][c] = 0.0f;
+  for (int d = 0; d < Dp; d += 4) {
+    float4 x[R], y[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      x[r] = *reinterpret_cast<const float4*>(a + (ty * R + r) * pitch + d);
+#pragma unroll
+    for (int c = 0; c < R; ++c)
+      y[c] = *reinterpret_cast<const float4*>(b + (tx + 16 * c) * pitch + d);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int c = 0; c < R; ++c) {
+        float s = acc[r][c];
+        s = fmaf(x[r].x, y[c].x, s);
+        s = fmaf(x[r].y, y[c].y, s);
+        s = fmaf(x[r].z, y[c].z, s);
+        acc[r][c] = fmaf(x[r].w, y[c].w, s);
+      }
+  }
+}
+
+// acc[r][e] += sum_j p[ty R + r][j] * t[j][tx 4 + 64 e ..]; TR: p is read transposed
+template <int BT, int NE, bool TR>
+__device__ __forceinline__ void mix_tile(const float* p, const float* t, int Dp, int ty, int tx,
+                                         float4 (&acc)[BT / 16][NE]) {
+  constexpr int R = BT / 16;
+  const int pitch = Dp + 4;
+  for (int j = 0; j < BT; ++j) {
+    float w[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      w[r] = TR ? p[j * (BT + 4) + ty * R + r] : p[(ty * R + r) * (BT + 4) + j];
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+      const int d = tx * 4 + 64 * e;
+      if (d >= Dp) break;
+      const float4 y = *reinterpret_cast<const float4*>(t + j * pitch + d);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        acc[r][e].x = fmaf(w[r], y.x, acc[r][e].x);
+        acc[r][e].y = fmaf(w[r], y.y, acc[r][e].y);
+        acc[r][e].z = fmaf(w[r], y.z, acc[r][e].z);
+        acc[r][e].w = fmaf(w[r], y.w, acc[r][e].w);
+      }
+    }
+  }
+}
+
+template <typename T, int BT, int NE>
+__device__ __forceinline__ void store_rows(T* dst, int64_t row_stride, int64_t row0, int64_t rows,
+                                           const float4 (&acc)[BT / 16][NE], const float* mul,
+                                           int D, int ty, int tx) {
+  constexpr int R = BT / 16;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t row = row0 + ty * R + r;
+    if (row >= rows) continue;
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+      const int d = tx * 4 + 64 * e;
+      const float v[4] = {acc[r][e].x, acc[r][e].y, acc[r][e].z, acc[r][e].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (d + i < D) dst[row * row_stride + d + i] = from_f<T>(v[i] * mul[r]);
+    }
+  }
+}
+
+template <int R, int NE>
+__device__ __forceinline__ void clear(float4 (&acc)[R][NE]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int e = 0; e < NE; ++e) acc[r][e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+}
+
+template <typename T, int BT, int NE>
+__global__ void __launch_bounds__(256, 1)
+    attn_simple_forward(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                        T* __restrict__ o, float* __restrict__ lse, const Geom g) {
+  constexpr int R = BT / 16;
+  extern __shared__ float4 smem4[];
+  float* qs = reinterpret_cast<float*>(smem4);
+  const int pitch = g.Dp + 4;
+  float* ks = qs + BT * pitch;
+  float* vs = ks + BT * pitch;
+  float* ps = vs + BT * pitch;
+  const int64_t tiles = (g.Lq + BT - 1) / BT;
+  int64_t u = blockIdx.x;
+  const int64_t i0 = u % tiles * BT;
+  u /= tiles;
+  const int h = (int)(u % g.Hq);
+  const int64_t b = u / g.Hq;
+  const Lens L = lens_of(g, b);
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+
+  int64_t nk = i0 < L.q ? L.k : 0;
+  if (g.causal && nk > 0) {
+    const int64_t last = (i0 + BT < L.q ? i0 + BT : L.q) - 1 + L.shift;  // last key seen
+    nk = last + 1 < nk ? last + 1 : nk;
+  }
+  float4 acc[R][NE];
+  clear(acc);
+  float m[R], l[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.0f;
+  }
+  const T* qp = q + b * g.q[0] + h * g.q[2];
+  const T* kp = k + b * g.k[0] + (h / g.G) * g.k[2];
+  const T* vp = v + b * g.v[0] + (h / g.G) * g.v[2];
+  load_tile<T, BT>(qs, qp, g.q[1], i0, 0, L.q, g);
+  const float c = g.scale * kLog2e;
+  for (int64_t j0 = 0; j0 < nk; j0 += BT) {
+    __syncthreads();
+    load_tile<T, BT>(ks, kp, g.k[1], j0, 0, L.k, g);
+    load_tile<T, BT>(vs, vp, g.v[1], j0, 0, L.k, g);
+    __syncthreads();
+    float s[R][R];
+    dot_tile<R>(qs, ks, g.Dp, ty, tx, s);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t i = i0 + ty * R + r;
+      float top = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < R; ++e) {
+        const int64_t j = j0 + tx + 16 * e;
+        const bool ok = i < L.q && j < L.k && (!g.causal || j <= i + L.shift);
+        s[r][e] = ok ? s[r][e] * c : -INFINITY;
+        top = fmaxf(top, s[r][e]);
+      }
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+      const float mn = fmaxf(m[r], top);
+      const float ref = mn == -INFINITY ? 0.0f : mn;  // a row without keys so far
+      const float shrink = exp2f(m[r] - ref);
+      float sum = 0.0f;
+#pragma unroll
+      for (int e = 0; e < R; ++e) {
+        const float p = exp2f(s[r][e] - ref);
+        sum += p;
+        ps[(ty * R + r) * (BT + 4) + tx + 16 * e] = p;
+      }
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+      l[r] = l[r] * shrink + sum;
+      m[r] = mn;
+#pragma unroll
+      for (int e = 0; e < NE; ++e) {
+        acc[r][e].x *= shrink;
+        acc[r][e].y *= shrink;
+        acc[r][e].z *= shrink;
+        acc[r][e].w *= shrink;
+      }
+    }
+    __syncwarp();  // a warp reads back only the rows of p that it wrote
+    mix_tile<BT, NE, false>(ps, vs, g.Dp, ty, tx, acc);
+  }
+  float mul[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    mul[r] = l[r] == 0.0f ? 0.0f : 1.0f / l[r];
+    const int64_t i = i0 + ty * R + r;
+    if (lse && tx == 0 && i < g.Lq)
+      lse[(b * g.Hq + h) * g.Lq + i] = l[r] == 0.0f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
+  }
+  store_rows<T, BT, NE>(o + b * g.o[0] + h * g.o[2], g.o[1], i0, g.Lq, acc, mul, g.D, ty, tx);
+}
+
+// delta = sum_d dout out, one warp per (b, h, i); rows past the length get 0.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    attn_simple_delta(const T* __restrict__ o, const T* __restrict__ dout, float* delta,
+                      const Geom g) {
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= g.B * g.Hq * g.Lq) return;
+  const int64_t i = row % g.Lq, bh = row / g.Lq;
+  const int h = (int)(bh % g.Hq);
+  const int64_t b = bh / g.Hq;
+  float s = 0.0f;
+  if (i < lens_of(g, b).q)
+    for (int d = threadIdx.x & 31; d < g.D; d += 32)
+      s = fmaf(to_f(o[b * g.o[0] + i * g.o[1] + h * g.o[2] + d]),
+               to_f(dout[b * g.g[0] + i * g.g[1] + h * g.g[2] + d]), s);
+  s = warp_sum(s);
+  if ((threadIdx.x & 31) == 0) delta[row] = s;
+}
+
+// p and ds of one tile pair (query rows ty R + r, keys tx + 16 e): s holds the scores and dp
+// the products dout v^T; both are replaced.
+template <int R>
+__device__ __forceinline__ void grad_tile(float (&s)[R][R], float (&dp)[R][R], int64_t i0,
+                                          int64_t j0, const Lens& L, const Geom& g,
+                                          const float* lse_row, const float* delta_row, int ty,
+                                          int tx) {
+  const float c = g.scale * kLog2e;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t i = i0 + ty * R + r;
+    const float lse = i < L.q ? lse_row[i] * kLog2e : 0.0f, delta = i < L.q ? delta_row[i] : 0.0f;
+#pragma unroll
+    for (int e = 0; e < R; ++e) {
+      const int64_t j = j0 + tx + 16 * e;
+      const bool ok = i < L.q && j < L.k && (!g.causal || j <= i + L.shift);
+      const float p = ok ? exp2f(s[r][e] * c - lse) : 0.0f;
+      s[r][e] = p;
+      dp[r][e] = ok ? p * (dp[r][e] - delta) : 0.0f;
+    }
+  }
+}
+
+template <typename T, int BT, int NE>
+__global__ void __launch_bounds__(256, 1)
+    attn_simple_dq(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                   const T* __restrict__ dout, const float* __restrict__ lse,
+                   const float* __restrict__ delta, T* __restrict__ dq, const Geom g) {
+  constexpr int R = BT / 16;
+  extern __shared__ float4 smem4[];
+  float* qs = reinterpret_cast<float*>(smem4);
+  const int pitch = g.Dp + 4;
+  float* gs = qs + BT * pitch;
+  float* ks = gs + BT * pitch;
+  float* vs = ks + BT * pitch;
+  float* ps = vs + BT * pitch;
+  const int64_t tiles = (g.Lq + BT - 1) / BT;
+  int64_t u = blockIdx.x;
+  const int64_t i0 = u % tiles * BT;
+  u /= tiles;
+  const int h = (int)(u % g.Hq);
+  const int64_t b = u / g.Hq;
+  const Lens L = lens_of(g, b);
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  int64_t nk = i0 < L.q ? L.k : 0;
+  if (g.causal && nk > 0) {
+    const int64_t last = (i0 + BT < L.q ? i0 + BT : L.q) - 1 + L.shift;
+    nk = last + 1 < nk ? last + 1 : nk;
+  }
+  float4 acc[R][NE];
+  clear(acc);
+  load_tile<T, BT>(qs, q + b * g.q[0] + h * g.q[2], g.q[1], i0, 0, L.q, g);
+  load_tile<T, BT>(gs, dout + b * g.g[0] + h * g.g[2], g.g[1], i0, 0, L.q, g);
+  const T* kp = k + b * g.k[0] + (h / g.G) * g.k[2];
+  const T* vp = v + b * g.v[0] + (h / g.G) * g.v[2];
+  const float* lse_row = lse + (b * g.Hq + h) * g.Lq;
+  const float* delta_row = delta + (b * g.Hq + h) * g.Lq;
+  for (int64_t j0 = 0; j0 < nk; j0 += BT) {
+    __syncthreads();
+    load_tile<T, BT>(ks, kp, g.k[1], j0, 0, L.k, g);
+    load_tile<T, BT>(vs, vp, g.v[1], j0, 0, L.k, g);
+    __syncthreads();
+    float s[R][R], dp[R][R];
+    dot_tile<R>(qs, ks, g.Dp, ty, tx, s);
+    dot_tile<R>(gs, vs, g.Dp, ty, tx, dp);
+    grad_tile<R>(s, dp, i0, j0, L, g, lse_row, delta_row, ty, tx);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < R; ++e) ps[(ty * R + r) * (BT + 4) + tx + 16 * e] = dp[r][e];
+    __syncwarp();
+    mix_tile<BT, NE, false>(ps, ks, g.Dp, ty, tx, acc);
+  }
+  float mul[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) mul[r] = g.scale;
+  store_rows<T, BT, NE>(dq + b * g.dq[0] + h * g.dq[2], g.dq[1], i0, g.Lq, acc, mul, g.D, ty, tx);
+}
+
+template <typename T, int BT, int NE>
+__global__ void __launch_bounds__(256, 1)
+    attn_simple_dkv(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                    const T* __restrict__ dout, const float* __restrict__ lse,
+                    const float* __restrict__ delta, T* __restrict__ dk, T* __restrict__ dv,
+                    const Geom g) {
+  constexpr int R = BT / 16;
+  extern __shared__ float4 smem4[];
+  float* qs = reinterpret_cast<float*>(smem4);
+  const int pitch = g.Dp + 4;
+  float* gs = qs + BT * pitch;
+  float* ks = gs + BT * pitch;
+  float* vs = ks + BT * pitch;
+  float* ps = vs + BT * pitch;
+  float* ds = ps + BT * (BT + 4);
+  const int64_t tiles = (g.Lk + BT - 1) / BT;
+  int64_t u = blockIdx.x;
+  const int64_t j0 = u % tiles * BT;
+  u /= tiles;
+  const int hk = (int)(u % g.Hk);
+  const int64_t b = u / g.Hk;
+  const Lens L = lens_of(g, b);
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  float4 ak[R][NE], av[R][NE];
+  clear(ak);
+  clear(av);
+  load_tile<T, BT>(ks, k + b * g.k[0] + hk * g.k[2], g.k[1], j0, 0, L.k, g);
+  load_tile<T, BT>(vs, v + b * g.v[0] + hk * g.v[2], g.v[1], j0, 0, L.k, g);
+  int64_t first = 0;                                 // first query that sees key j0
+  if (g.causal) first = j0 - L.shift;
+  if (first < 0) first = 0;
+  // queries that see no key at all take no part either (their scores are all hidden)
+  const int64_t lead = g.causal && L.shift < 0 ? -L.shift : 0;
+  const int64_t end = j0 < L.k ? L.q : 0;
+  for (int h = hk * g.G; h < (hk + 1) * g.G; ++h)
+    for (int64_t i0 = first / BT * BT; i0 < end; i0 += BT) {
+      __syncthreads();
+      load_tile<T, BT>(qs, q + b * g.q[0] + h * g.q[2], g.q[1], i0, lead, L.q, g);
+      load_tile<T, BT>(gs, dout + b * g.g[0] + h * g.g[2], g.g[1], i0, lead, L.q, g);
+      __syncthreads();
+      float s[R][R], dp[R][R];
+      dot_tile<R>(qs, ks, g.Dp, ty, tx, s);
+      dot_tile<R>(gs, vs, g.Dp, ty, tx, dp);
+      const int64_t row = (b * g.Hq + h) * g.Lq;
+      grad_tile<R>(s, dp, i0, j0, L, g, lse + row, delta + row, ty, tx);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < R; ++e) {
+          ps[(ty * R + r) * (BT + 4) + tx + 16 * e] = s[r][e];
+          ds[(ty * R + r) * (BT + 4) + tx + 16 * e] = dp[r][e];
+        }
+      __syncthreads();
+      mix_tile<BT, NE, true>(ps, gs, g.Dp, ty, tx, av);
+      mix_tile<BT, NE, true>(ds, qs, g.Dp, ty, tx, ak);
+    }
+  float one[R], mul[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    one[r] = 1.0f;
+    mul[r] = g.scale;
+  }
+  store_rows<T, BT, NE>(dk + b * g.dk[0] + hk * g.dk[2], g.dk[1], j0, g.Lk, ak, mul, g.D, ty, tx);
+  store_rows<T, BT, NE>(dv + b * g.dv[0] + hk * g.dv[2], g.dv[1], j0, g.Lk, av, one, g.D, ty, tx);
+}
+
+Geom geom_of(const fconv_attn_desc& d, const AttnArgs& a) {
+  Geom g{};
+  g.B = d.batch;
+  g.Lq = d.len_q;
+  g.Lk = d.len_k;
+  g.Hq = (int)d.heads_q;
+  g.Hk = (int)d.heads_kv;
+  g.G = g.Hq / g.Hk;
+  g.D = (int)d.head_dim;
+  g.Dp = (g.D + 3) / 4 * 4;
+  for (int i = 0; i < 3; ++i) {
+    g.q[i] = d.q_stride[i];
+    g.k[i] = d.k_stride[i];
+    g.v[i] = d.v_stride[i];
+    g.o[i] = d.out_stride[i];
+    g.g[i] = d.dout_stride[i];
+    g.dq[i] = d.dq_stride[i];
+    g.dk[i] = d.dk_stride[i];
+    g.dv[i] = d.dv_stride[i];
+  }
+  g.scale = d.scale;
+  g.causal = d.causal;
+  g.q_lens = a.q_lens;
+  g.kv_lens = a.kv_lens;
+  return g;
+}
+
+size_t tile_bytes(const Geom& g, int BT, int tiles, int squares) {
+  return sizeof(float) * ((size_t)tiles * BT * (g.Dp + 4) + (size_t)squares * BT * (BT + 4));
+}
+
+template <typename K>
+int allow_smem(K kernel, size_t bytes) {
+  return (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   (int)bytes);
+}
+
+template <typename T, int BT, int NE>
+int forward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
+  const long long blocks = g.B * g.Hq * ((g.Lq + BT - 1) / BT);
+  if (!grid_ok(blocks)) return (int)cudaErrorInvalidValue;
+  const size_t smem = tile_bytes(g, BT, 3, 1);
+  auto kern = attn_simple_forward<T, BT, NE>;
+  const int e = allow_smem(kern, smem);
+  if (e) return e;
+  kern<<<(unsigned)blocks, 256, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v, (T*)a.o,
+                                           a.lse, g);
+  return (int)cudaGetLastError();
+}
+
+template <typename T, int BT, int NE>
+int backward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
+  const long long rows = g.B * g.Hq * g.Lq;
+  const long long bq = g.B * g.Hq * ((g.Lq + BT - 1) / BT);
+  const long long bk = g.B * g.Hk * ((g.Lk + BT - 1) / BT);
+  float* delta = (float*)a.ws;
+  if (rows > 0) {
+    const size_t smem = tile_bytes(g, BT, 4, 1);
+    auto kern = attn_simple_dq<T, BT, NE>;
+    const int e = allow_smem(kern, smem);
+    if (e) return e;
+    if (!grid_ok((rows + 7) / 8) || !grid_ok(bq)) return (int)cudaErrorInvalidValue;
+    attn_simple_delta<T><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>((const T*)a.out,
+                                                                    (const T*)a.dout, delta, g);
+    kern<<<(unsigned)bq, 256, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v,
+                                         (const T*)a.dout, a.lse, delta, (T*)a.dq, g);
+  }
+  if (bk > 0) {
+    const size_t smem = tile_bytes(g, BT, 4, 2);
+    auto kern = attn_simple_dkv<T, BT, NE>;
+    const int e = allow_smem(kern, smem);
+    if (e) return e;
+    if (!grid_ok(bk)) return (int)cudaErrorInvalidValue;
+    kern<<<(unsigned)bk, 256, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v,
+                                         (const T*)a.dout, a.lse, delta, (T*)a.dk, (T*)a.dv, g);
+  }
+  return (int)cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attn_simple_backward_workspace(const fconv_attn_desc& d) {
+  return (size_t)d.batch * (size_t)d.heads_q * (size_t)d.len_q * sizeof(float);
+}
+
+int launch_attn_simple_forward(const fconv_attn_desc& d, const AttnArgs& a, cudaStream_t s) {
+  const Geom g = geom_of(d, a);
+  if (g.B * g.Lq == 0) return 0;
+#define FCONV_M(T)                                        \
+  return g.Dp <= 64    ? forward_t<T, 64, 1>(g, a, s)     \
+         : g.Dp <= 128 ? forward_t<T, 64, 2>(g, a, s)     \
+                       : forward_t<T, 32, 4>(g, a, s)
+  FCONV_OPS_TYPE(d.dtype, FCONV_M)
+#undef FCONV_M
+}
+
+int launch_attn_simple_backward(const fconv_attn_desc& d, const AttnArgs& a, cudaStream_t s) {
+  const Geom g = geom_of(d, a);
+#define FCONV_M(T)                                         \
+  return g.Dp <= 64    ? backward_t<T, 64, 1>(g, a, s)     \
+         : g.Dp <= 128 ? backward_t<T, 64, 2>(g, a, s)     \
+                       : backward_t<T, 32, 4>(g, a, s)
+  FCONV_OPS_TYPE(d.dtype, FCONV_M)
+#undef FCONV_M
+}
+
+}  // namespace ops
+}  // namespace fconv

@@ -1,0 +1,78 @@
+// Element types, 16-byte vectors and block reductions shared by the token-side operators.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace fconv {
+namespace ops {
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+// N consecutive elements as one aligned access (N * sizeof(T) a power of two up to 16).
+template <typename T, int N>
+struct alignas(sizeof(T) * N) Vec {
+  T v[N];
+};
+
+template <typename T, int N>
+__device__ __forceinline__ void load_f(const T* p, float (&f)[N]) {
+  const Vec<T, N> x = *reinterpret_cast<const Vec<T, N>*>(p);
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = to_f(x.v[i]);
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_f(T* p, const float (&f)[N]) {
+  Vec<T, N> x;
+#pragma unroll
+  for (int i = 0; i < N; ++i) x.v[i] = from_f<T>(f[i]);
+  *reinterpret_cast<Vec<T, N>*>(p) = x;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sum over a block of NT threads (a multiple of 32), the same value in every thread; `red`
+// has NT / 32 floats. Ends with a barrier, so `red` can be used again at once.
+template <int NT>
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  if (NT == 32) return warp_sum(v);
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NT / 32; ++i) s += red[i];
+  __syncthreads();
+  return s;
+}
+
+}  // namespace ops
+}  // namespace fconv
+
+// Calls M(T) with T the C++ type of a dtype code.
+#define FCONV_OPS_TYPE(dtype, M)            \
+  switch (dtype) {                          \
+    case FCONV_F32: { M(float); break; }    \
+    case FCONV_F16: { M(__half); break; }   \
+    default: { M(__nv_bfloat16); break; }   \
+  }

@@ -1,0 +1,66 @@
+// Internal interface between the token-side operators' planner (ops_api.cpp) and their
+// CUDA launchers.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "../../../include/fconv_ops.h"
+
+namespace fconv {
+namespace ops {
+
+// Launchers return a cudaError_t as int (0 = success).
+
+struct NormArgs {
+  const void* x;
+  const void* dy;
+  const void* w;
+  const void* b;
+  void* y;  // y, or dx
+  void* dw;
+  void* db;
+  float* mean;
+  float* rstd;
+  float* ws;
+};
+int launch_norm_forward(const fconv_norm_desc& d, int sms, const NormArgs& a, cudaStream_t s);
+int launch_norm_backward(const fconv_norm_desc& d, int sms, const NormArgs& a, cudaStream_t s);
+size_t norm_workspace(const fconv_norm_desc& d, int sms);
+
+struct RopeArgs {
+  const void* q;
+  const void* k;
+  const void* pos;
+  const float* inv_freq;
+  void* q_out;
+  void* k_out;
+};
+int launch_rope(const fconv_rope_desc& d, int sms, const RopeArgs& a, cudaStream_t s);
+
+struct AttnArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* out;  // backward
+  const void* dout;
+  const int32_t* q_lens;
+  const int32_t* kv_lens;
+  void* o;  // forward
+  float* lse;
+  void* dq;
+  void* dk;
+  void* dv;
+  void* ws;
+};
+int launch_attn_simple_forward(const fconv_attn_desc& d, const AttnArgs& a, cudaStream_t s);
+int launch_attn_simple_backward(const fconv_attn_desc& d, const AttnArgs& a, cudaStream_t s);
+size_t attn_simple_backward_workspace(const fconv_attn_desc& d);
+
+// Whether a launch's block count fits the grid's first axis.
+inline bool grid_ok(long long blocks) { return blocks > 0 && blocks <= 0x7fffffffLL; }
+
+}  // namespace ops
+}  // namespace fconv

@@ -33,8 +33,9 @@
 extern "C" {
 #endif
 
-/* Element type T of X, W, B, Z and Y (manifest "typeConstraints"). */
-typedef enum { FCONV_F32 = 0, FCONV_F16 = 1 } fconv_dtype;
+/* Element type T of X, W, B, Z and Y (manifest "typeConstraints"). FCONV_BF16 is a type of the
+ * operators in fconv_ops.h only; a convolution refuses it with FCONV_E_UNSUPPORTED. */
+typedef enum { FCONV_F32 = 0, FCONV_F16 = 1, FCONV_BF16 = 2 } fconv_dtype;
 
 /* auto_pad (README "Attributes": NOTSET uses pads; SAME_UPPER / SAME_LOWER pick pads so
  * each output size is ceil(input / stride), the odd pixel at the end / the beginning;
@@ -95,7 +96,11 @@ typedef enum {
   FCONV_E_DEVICE_TIMEOUT = 16,   /* a kernel gave up a bounded wait (device error word) */
   FCONV_E_NOMEM = 17,            /* host allocation failed */
   FCONV_E_ALIGNMENT = 18,        /* a device pointer is not 16-byte aligned */
-  FCONV_E_ALIAS = 19             /* Y equals X, W, B, Z or the workspace */
+  FCONV_E_ALIAS = 19,            /* Y equals X, W, B, Z or the workspace */
+  /* of the operators in fconv_ops.h (fconv_ops_status_string gives their texts) */
+  FCONV_E_EXTENT = 32,           /* an extent below its minimum, or sizes that do not fit */
+  FCONV_E_STRIDE = 33,           /* a negative stride, or elements of an output that overlap */
+  FCONV_E_MASK = 34              /* lengths given where the plan has none, or the reverse */
 } fconv_status;
 
 /* Kernel routes a plan can take. */
