@@ -1,0 +1,301 @@
+// Pieces shared by the tensor-core attention kernels: instruction wrappers beyond ../ptx.cuh,
+// bounded waits, the packing of query rows, tensor maps.
+//
+// Everything with state has internal linkage: each translation unit has its own error word.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../fconv_internal.h"
+#include "../ptx.cuh"
+#include "ops_internal.h"
+
+namespace fconv {
+namespace ops {
+namespace {
+
+constexpr int kTile = 128;                 // rows of a query tile, keys of a key tile
+constexpr uint32_t kHalfBytes = kTile * 128;  // 128 rows of 64 elements: one 128-byte-row box
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t kDrainLimitNs = 200000000ull;
+
+__device__ unsigned g_attn_error = 0;
+
+// Wait for a phase of an mbarrier, for at most kWaitLimitNs; gives up early when another warp
+// of the block has. A wait that runs out sets the flag and the error word.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (ptx::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0) {
+      if (*abort_flag) return false;
+      if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        atomicOr(&g_attn_error, 1u);
+        return false;
+      }
+    }
+  }
+}
+
+// Wait for operations this block has already issued (they always complete).
+__device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity) {
+  if (ptx::mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (ptx::mbar_try_wait(bar, parity)) return;
+    if ((i & 63u) == 0 && ptx::globaltimer_ns() - t0 > kDrainLimitNs) {
+      atomicOr(&g_attn_error, 1u);
+      return;
+    }
+  }
+}
+
+// ------------------------------------------------------------------------- instructions
+
+// K-major operand in the 128-byte swizzle (64 elements a row): ptx::desc_sw128.
+// MN-major operand in the same tiles, its rows now running along K: 64 elements along M or N
+// are 128 contiguous bytes, 8 rows (K) an atom of 1024 bytes (stride offset), and the next 64
+// elements along M or N lie one box further (leading offset).
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kHalfBytes >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// Instruction descriptor of kind::f16: f32 accumulator, A and B both f16 (0) or both bf16 (1),
+// B K-major or (bmn) MN-major.
+__host__ __device__ constexpr uint32_t idesc_16(bool bf16, int M, int N, bool bmn) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (bmn ? 1u << 16 : 0u) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: A's rows are TMEM lanes, two 16-bit elements a column.
+__device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 4-D tiled TMA load (c0 innermost).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int c0, int c1, int c2,
+                                            int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"((uint64_t)tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+
+// Contiguous copy of `bytes` (a multiple of 16, both addresses 16-byte aligned).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+#define FCONV_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), \
+                       "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
+#define FCONV_I8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), \
+                       "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
+#define FCONV_P8(r, o) "+r"(r[o]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]), \
+                       "+r"(r[o + 4]), "+r"(r[o + 5]), "+r"(r[o + 6]), "+r"(r[o + 7])
+
+// Whole warp: starts the load of 32 lanes x 32 columns (thread t gets lane base + t). The
+// registers hold the values only after tmem_arrived() on them.
+__device__ __forceinline__ void tmem_fetch32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : FCONV_R8(r, 0), FCONV_R8(r, 8), FCONV_R8(r, 16), FCONV_R8(r, 24)
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// Ties the registers to the wait that precedes: no use of them moves above it.
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32]) {
+  asm volatile("" : FCONV_P8(r, 0), FCONV_P8(r, 8), FCONV_P8(r, 16), FCONV_P8(r, 24)::"memory");
+}
+__device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::FCONV_I8(
+          r, 0),
+      FCONV_I8(r, 8), FCONV_I8(r, 16), FCONV_I8(r, 24), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::FCONV_I8(r, 0),
+      FCONV_I8(r, 8), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Registers a thread of the calling warpgroup may use from here on (all its warps call it).
+template <int N>
+__device__ __forceinline__ void regs_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_fewer() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// 2^x by the special-function unit (within 2 ulp; results below 2^-126 become 0).
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two values rounded to 16 bits, the first in the low half.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  uint32_t r;
+  if (BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// ------------------------------------------------------------------------------ geometry
+
+// Query rows are packed: a tile of key head hk takes `toks` tokens of all G heads that read it,
+// row r = token * G + head in group, so shared heads fill a tile together and read each key
+// tile once. toks = 128 / G; rows toks * G .. 127 (G not a power of two) stay empty.
+struct TcGeom {
+  int64_t B, Lq, Lk;
+  int Hq, Hk, G, D;
+  int toks, rows;              // tokens and rows of a query tile
+  int qtiles;                  // query tiles of a (batch, key head)
+  int ktiles;                  // key tiles of the longest sequence
+  float scale;
+  int causal;
+  const int32_t* q_lens;
+  const int32_t* kv_lens;
+  int kb, kh, vb, vh, qb, gb;  // coordinate multipliers: 0 where a tensor broadcasts the axis
+};
+
+struct TcLens {
+  int q, k, shift;  // causal: query i sees keys j <= i + shift
+  int lead;         // queries before it see no key (causal order with more queries than keys)
+};
+__device__ __forceinline__ TcLens tc_lens(const TcGeom& g, int b) {
+  TcLens l;
+  l.q = (int)g.Lq;
+  l.k = (int)g.Lk;
+  if (g.q_lens) l.q = min(max(g.q_lens[b], 0), (int)g.Lq);
+  if (g.kv_lens) l.k = min(max(g.kv_lens[b], 0), (int)g.Lk);
+  l.shift = l.k - l.q;
+  l.lead = g.causal && l.shift < 0 ? -l.shift : 0;
+  if (l.k == 0) l.lead = l.q;
+  return l;
+}
+// Keys that query i sees: [0, limit). Queries outside [lead, q) see none.
+__device__ __forceinline__ int key_limit(const TcGeom& g, const TcLens& l, int i) {
+  if (i < l.lead || i >= l.q) return 0;
+  return g.causal ? min(l.k, i + l.shift + 1) : l.k;
+}
+// Key tiles that the query tile starting at token t0 needs.
+__device__ __forceinline__ int key_tiles(const TcGeom& g, const TcLens& l, int t0) {
+  if (t0 >= l.q) return 0;
+  const int last = min(t0 + g.toks, l.q) - 1;
+  return (key_limit(g, l, last) + kTile - 1) / kTile;
+}
+
+// Zeroes rows [lo, hi) of a tile made of `halves` boxes of 128-byte rows (the swizzle moves
+// 16-byte units within a row only). Whole warp.
+__device__ __forceinline__ void zero_rows(uint32_t tile, int halves, int lo, int hi, int lane) {
+  for (int h = 0; h < halves; ++h)
+    for (int e = lo * 8 + lane; e < hi * 8; e += 32)
+      ptx::st_shared_v4(tile + h * kHalfBytes + (uint32_t)e * 16, 0, 0, 0, 0);
+}
+
+// ------------------------------------------------------------------------------ host side
+
+// Tensor map of a (batch, token, head, D) tensor seen as (D, head, token, batch), with boxes
+// of 64 elements x `heads` x `toks`. An axis with stride 0 gets extent 1 and multiplier 0.
+inline bool make_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, int dtype, int64_t D,
+                     int64_t heads, int64_t len, int64_t batch, const int64_t st[3], int box_heads,
+                     int box_toks, int* mul_head, int* mul_batch) {
+  if (mul_head) {
+    *mul_head = st[2] == 0 ? 0 : 1;
+    if (!*mul_head) heads = 1;
+  }
+  *mul_batch = st[0] == 0 ? 0 : 1;
+  if (!*mul_batch) batch = 1;
+  auto bytes = [&](int64_t stride, int64_t extent) {
+    return (cuuint64_t)(extent > 1 ? stride * 2 : 16);
+  };
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)len,
+                              (cuuint64_t)batch};
+  const cuuint64_t strides[3] = {bytes(st[2], heads), bytes(st[1], len), bytes(st[0], batch)};
+  const cuuint32_t box[4] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_toks, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return enc(m,
+             dtype == FCONV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+             4, const_cast<void*>(base), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+inline TcGeom tc_geom(const fconv_attn_desc& d, const AttnArgs& a) {
+  TcGeom g{};
+  g.B = d.batch;
+  g.Lq = d.len_q;
+  g.Lk = d.len_k;
+  g.Hq = (int)d.heads_q;
+  g.Hk = (int)d.heads_kv;
+  g.G = g.Hq / g.Hk;
+  g.D = (int)d.head_dim;
+  g.toks = kTile / g.G;
+  g.rows = g.toks * g.G;
+  g.qtiles = (int)((g.Lq + g.toks - 1) / g.toks);
+  g.ktiles = (int)((g.Lk + kTile - 1) / kTile);
+  g.scale = d.scale;
+  g.causal = d.causal;
+  g.q_lens = a.q_lens;
+  g.kv_lens = a.kv_lens;
+  return g;
+}
+
+inline int read_and_clear_error(cudaStream_t s, unsigned* value) {
+  unsigned v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_attn_error, sizeof(v), 0,
+                                            cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && v)
+    e = cudaMemcpyToSymbolAsync(g_attn_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  *value = v;
+  return (int)e;
+}
+
+}  // namespace
+}  // namespace ops
+}  // namespace fconv

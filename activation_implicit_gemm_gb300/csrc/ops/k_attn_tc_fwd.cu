@@ -1,0 +1,575 @@
+// Attention forward on the tcgen05 tensor cores (f16 and bf16, head_dim a multiple of 8 up to
+// 128).
+//
+// A persistent block (one per SM) owns a pair of 128-row query tiles of one (batch, key head)
+// and walks the keys in tiles of 128:
+//   S_t = Q_t K^T (both operands in shared memory), 128 x 128 f32 in TMEM
+//   P_t = exp2(scale log2e S_t - m)  rounded to 16 bits, written over S_t in TMEM
+//   O_t += P_t V (P from TMEM, V from shared memory as the MN-major operand)
+// The two tiles share every K and V tile and take turns: while the 128 softmax threads of one
+// tile work (a thread owns a row: no shuffles), the tensor core runs P V and the next Q K^T of
+// the other. m is the running row maximum; O and the row sum are rescaled only when it grew by
+// more than 8 in log2 (the sums stay below 2^8 times their final size, far inside f32, and P
+// below 2^8, inside f16), which is exact in the same way as rescaling always: m cancels in O / l.
+// P's rounding is the only one before the output's; the row sum adds the unrounded values.
+//
+// Roles: warps 0-3 and 4-7 softmax and epilogue of tile 0 and 1, warp 8 MMA, warp 9 TMA (10 and
+// 11 only complete the warpgroup).
+// TMEM: S0 S1 O0 O1, 128 columns each. Shared memory: two Q tiles, a ring of K and V tiles.
+// When there are fewer blocks than SMs the keys are split; partial O (normalised, f32) and the
+// log2 of their sums go to the workspace and attn_tc_join adds them in order.
+//
+// Bound: tensor (4 D FLOPs a pair) for long queries, HBM (K and V) for few.
+#include "attn_tc.cuh"
+
+#include <climits>
+#include <cmath>
+#include <cstring>
+
+namespace fconv {
+namespace ops {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+// A softmax thread holds a row of 128 scores; three warps a scheduler leave 168 registers a
+// thread, so the third warpgroup hands some over: 2 * 216 + 72 = 3 * 168.
+constexpr int kLaunchRegs = 168, kSoftmaxRegs = 216, kOtherRegs = 72;
+static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "within the launch's registers");
+
+struct FwdArgs {
+  TcGeom g;
+  int pairs, splits, per;  // query tile pairs; key splits and key tiles of a split
+  int items;
+  int64_t o[3];
+  void* out;
+  float* lse;
+  float* part;      // splits > 1: [split][B][Hq][Lq][D]
+  float* part_lse;  // [split][B][Hq][Lq], log2
+};
+
+struct FwdItem {
+  int b, hk, split, t0[2], n[2], jb;
+  TcLens l;
+};
+
+// Item k of a block: rounds run forwards and backwards in turn, and in causal order the long
+// query tiles come first, so that the blocks' sums of work come out even. Without causal order
+// neighbouring blocks share a head's keys in L2.
+__device__ __forceinline__ bool fwd_item(const FwdArgs& a, int k, FwdItem& it) {
+  const int grid = gridDim.x, bid = blockIdx.x;
+  const int at = k * grid + ((k & 1) ? grid - 1 - bid : bid);
+  if (at >= a.items) return false;
+  int u = at;
+  it.split = u % a.splits;
+  u /= a.splits;
+  const int bh = (int)a.g.B * a.g.Hk;
+  int pair;
+  if (a.g.causal) {
+    pair = a.pairs - 1 - u / bh;
+    u %= bh;
+  } else {
+    pair = u % a.pairs;
+    u /= a.pairs;
+  }
+  it.hk = u % a.g.Hk;
+  it.b = u / a.g.Hk;
+  it.l = tc_lens(a.g, it.b);
+  it.jb = it.split * a.per;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    it.t0[t] = (2 * pair + t) * a.g.toks;
+    it.n[t] = max(min(key_tiles(a.g, it.l, it.t0[t]) - it.jb, a.per), 0);
+  }
+  return true;
+}
+
+template <int H>
+struct FwdPlan {
+  static constexpr uint32_t tile_bytes = H * kHalfBytes;
+  static constexpr int slots = H == 2 ? 5 : 8;
+  static constexpr uint32_t smem = (2 + slots) * tile_bytes + 1024;
+};
+
+template <int H>
+struct FwdCtl {
+  uint64_t full[FwdPlan<H>::slots], empty[FwdPlan<H>::slots];
+  uint64_t q_full, q_empty, tail, drain;
+  uint64_t s_full[2], p_ready[2], o_done[2];
+  uint32_t tmem;
+  int abort_flag;
+};
+
+template <bool BF16, int H>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tc_forward(const FwdArgs a, const __grid_constant__ CUtensorMap tm_q,
+                    const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v) {
+  using Plan = FwdPlan<H>;
+  extern __shared__ uint8_t dsmem[];
+  __shared__ FwdCtl<H> ctl;
+  const TcGeom& g = a.g;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t qbase = (ptx::smem_addr(dsmem) + 1023u) & ~1023u;
+  const uint32_t ring = qbase + 2 * Plan::tile_bytes;
+  volatile int* abort_flag = &ctl.abort_flag;
+
+  if (tid == 0) {
+    for (int i = 0; i < Plan::slots; ++i) {
+      ptx::mbar_init(ptx::smem_addr(&ctl.full[i]), 1);
+      ptx::mbar_init(ptx::smem_addr(&ctl.empty[i]), 1);
+    }
+    ptx::mbar_init(ptx::smem_addr(&ctl.q_full), 1);
+    ptx::mbar_init(ptx::smem_addr(&ctl.q_empty), 1);
+    ptx::mbar_init(ptx::smem_addr(&ctl.tail), 1);
+    ptx::mbar_init(ptx::smem_addr(&ctl.drain), 1);
+    for (int t = 0; t < 2; ++t) {
+      ptx::mbar_init(ptx::smem_addr(&ctl.s_full[t]), 1);
+      ptx::mbar_init(ptx::smem_addr(&ctl.p_ready[t]), 4);
+      ptx::mbar_init(ptx::smem_addr(&ctl.o_done[t]), 1);
+    }
+    ctl.abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(ptx::smem_addr(&ctl.tmem), 512);
+    ptx::tmem_relinquish();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    ptx::prefetch_tmap(&tm_q);
+    ptx::prefetch_tmap(&tm_k);
+    ptx::prefetch_tmap(&tm_v);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  ptx::pdl_wait();
+
+  if (warp >= 8) {
+   regs_fewer<kOtherRegs>();
+   if (warp == kLoadWarp) {
+    // ------------------------------------------------------------------ TMA producer
+    uint32_t c = 0, q_items = 0, tails = 0;
+    FwdItem it;
+    bool stop = false;
+    for (int k = 0; !stop && fwd_item(a, k, it); ++k) {
+      const int n = max(it.n[0], it.n[1]);
+      if (n == 0) continue;
+      if (!wait_bar(ptx::smem_addr(&ctl.q_empty), (q_items & 1) ^ 1, abort_flag)) break;
+      ++q_items;
+      if (lane == 0) {
+        const uint32_t bar = ptx::smem_addr(&ctl.q_full);
+        const uint32_t box = (uint32_t)g.rows * 128;
+        ptx::mbar_arrive_expect_tx(bar, ((it.n[0] > 0) + (it.n[1] > 0)) * H * box);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (it.n[t] > 0)
+            for (int h = 0; h < H; ++h)
+              tma_load_4d(qbase + t * Plan::tile_bytes + h * kHalfBytes, &tm_q, h * 64,
+                          it.hk * g.G, it.t0[t], it.b * g.qb, bar);
+      }
+      for (int j = 0; j < 2 * n; ++j, ++c) {
+        const uint32_t s = c % Plan::slots, ph = (c / Plan::slots) & 1;
+        if (!wait_bar(ptx::smem_addr(&ctl.empty[s]), ph ^ 1, abort_flag)) {
+          stop = true;
+          break;
+        }
+        const int key0 = (it.jb + (j >> 1)) * kTile;
+        const uint32_t dst = ring + s * Plan::tile_bytes;
+        const bool is_v = j & 1;
+        // rows of V past the sequence would meet P = 0: a NaN there must not reach the product
+        const bool ragged = is_v && key0 + kTile > it.l.k && it.l.k < g.Lk;
+        const uint32_t full = ptx::smem_addr(&ctl.full[s]);
+        const uint32_t bar = ragged ? ptx::smem_addr(&ctl.tail) : full;
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(bar, Plan::tile_bytes);
+          for (int h = 0; h < H; ++h)
+            tma_load_4d(dst + h * kHalfBytes, is_v ? &tm_v : &tm_k, h * 64,
+                        it.hk * (is_v ? g.vh : g.kh), key0, it.b * (is_v ? g.vb : g.kb), bar);
+        }
+        if (ragged) {
+          if (!wait_bar(bar, tails & 1, abort_flag)) {
+            drain_bar(bar, tails & 1);
+            stop = true;
+            break;
+          }
+          ++tails;
+          zero_rows(dst, H, it.l.k - key0, kTile, lane);
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(full);
+        }
+      }
+    }
+    if (*abort_flag) {
+      // loads in flight land before the block's shared memory is given back
+      for (uint32_t i = c > Plan::slots ? c - Plan::slots : 0; i < c; ++i)
+        drain_bar(ptx::smem_addr(&ctl.full[i % Plan::slots]), (i / Plan::slots) & 1);
+      if (q_items) drain_bar(ptx::smem_addr(&ctl.q_full), (q_items - 1) & 1);
+    }
+   } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------------ MMA issue
+    if (lane == 0) {
+      const uint32_t id_s = idesc_16(BF16, kTile, kTile, false);
+      const int dk = (g.D + 15) / 16;  // K steps of Q K^T, N / 16 of P V
+      const uint32_t id_o = idesc_16(BF16, kTile, dk * 16, true);
+      uint32_t c = 0, q_items = 0, pv[2] = {0, 0};
+      FwdItem it;
+      bool stop = false;
+      auto scores = [&](int t, uint32_t ktile) {
+        const uint32_t q = qbase + t * Plan::tile_bytes;
+#pragma unroll
+        for (int d = 0; d < 4 * H; ++d)
+          if (d < dk) {
+            const uint32_t o = (d >> 2) * kHalfBytes + (d & 3) * 32;
+            ptx::mma_f16(tmem + t * 128, ptx::desc_sw128(q + o), ptx::desc_sw128(ktile + o), id_s,
+                         d > 0);
+          }
+        ptx::mma_commit(ptx::smem_addr(&ctl.s_full[t]));
+      };
+      for (int k = 0; !stop && fwd_item(a, k, it); ++k) {
+        const int n = max(it.n[0], it.n[1]);
+        if (n == 0) continue;
+        if (!wait_bar(ptx::smem_addr(&ctl.q_full), q_items & 1, abort_flag)) break;
+        ++q_items;
+        if (!wait_bar(ptx::smem_addr(&ctl.full[c % Plan::slots]), (c / Plan::slots) & 1,
+                      abort_flag))
+          break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (it.n[t] > 0) scores(t, ring + c % Plan::slots * Plan::tile_bytes);
+        ptx::mma_commit(ptx::smem_addr(&ctl.empty[c % Plan::slots]));
+        if (n == 1) ptx::mma_commit(ptx::smem_addr(&ctl.q_empty));
+        for (int j = 0; j < n; ++j, c += 2) {
+          const uint32_t vs = (c + 1) % Plan::slots, ks = (c + 2) % Plan::slots;
+          if (!wait_bar(ptx::smem_addr(&ctl.full[vs]), ((c + 1) / Plan::slots) & 1, abort_flag) ||
+              (j + 1 < n && !wait_bar(ptx::smem_addr(&ctl.full[ks]),
+                                      ((c + 2) / Plan::slots) & 1, abort_flag))) {
+            stop = true;
+            break;
+          }
+          const uint32_t v = ring + vs * Plan::tile_bytes;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (j >= it.n[t]) continue;
+            if (!wait_bar(ptx::smem_addr(&ctl.p_ready[t]), pv[t] & 1, abort_flag)) {
+              stop = true;
+              break;
+            }
+            ++pv[t];
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int s = 0; s < kTile / 16; ++s)
+              mma_ts(tmem + 256 + t * 128, tmem + t * 128 + s * 8, desc_mn_sw128(v + s * 2048),
+                     id_o, j > 0 || s > 0);
+            if (j == it.n[t] - 1) ptx::mma_commit(ptx::smem_addr(&ctl.o_done[t]));
+            if (j + 1 < it.n[t]) scores(t, ring + ks * Plan::tile_bytes);
+          }
+          if (stop) break;
+          ptx::mma_commit(ptx::smem_addr(&ctl.empty[vs]));
+          if (j + 1 < n) ptx::mma_commit(ptx::smem_addr(&ctl.empty[ks]));
+          if (j + 2 == n) ptx::mma_commit(ptx::smem_addr(&ctl.q_empty));
+        }
+      }
+      ptx::mma_commit(ptx::smem_addr(&ctl.drain));
+      drain_bar(ptx::smem_addr(&ctl.drain), 0);
+    }
+   }
+  } else {
+    // ------------------------------------------------------------------ softmax, epilogue
+    regs_more<kSoftmaxRegs>();
+    const int t = warp >> 2;
+    const int row = tid & 127, tok = row / g.G, head = row - tok * g.G;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
+    const uint32_t s_at = tmem + t * 128 + lanes, o_at = tmem + 256 + t * 128 + lanes;
+    const float c = g.scale * kLog2e;
+    uint32_t steps = 0, done = 0;
+    FwdItem it;
+    for (int k = 0; fwd_item(a, k, it); ++k) {
+      const int n = t ? it.n[1] : it.n[0], i = (t ? it.t0[1] : it.t0[0]) + tok;
+      const int limit = row < g.rows ? key_limit(g, it.l, i) : 0;
+      float m = -INFINITY, l = 0.0f;
+      bool stop = false;
+      for (int j = 0; j < n; ++j) {
+        if (!wait_bar(ptx::smem_addr(&ctl.s_full[t]), steps & 1, abort_flag)) {
+          stop = true;
+          break;
+        }
+        ++steps;
+        ptx::tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_fetch32(s_at + q * 32, s[q]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_arrived(s[q]);
+        const int seen = limit - (it.jb + j) * kTile;  // columns of this tile that the row sees
+        if (__any_sync(0xffffffffu, seen < kTile)) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (q * 32 + e >= seen) s[q][e] = 0xff800000u;  // -inf
+        }
+        float top[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          top[q] = __uint_as_float(s[q][0]);
+#pragma unroll
+          for (int e = 1; e < 32; ++e) top[q] = fmaxf(top[q], __uint_as_float(s[q][e]));
+        }
+        const float mn = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c);
+        if (__any_sync(0xffffffffu, mn > m + 8.0f)) {
+          // the scores of this tile are complete, so every earlier P V is too
+          const float f = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
+          l *= f;
+          m = mn;
+          if (j > 0)
+            for (int q = 0; q < (g.D + 31) / 32; ++q) {
+              uint32_t o[32];
+              tmem_fetch32(o_at + q * 32, o);
+              tmem_wait_ld();
+              tmem_arrived(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_store32(o_at + q * 32, o);
+            }
+        }
+        const float ref = m == -INFINITY ? 0.0f : m;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float x = exp2_fast(fmaf(__uint_as_float(s[q][2 * e]), c, -ref));
+            const float y = exp2_fast(fmaf(__uint_as_float(s[q][2 * e + 1]), c, -ref));
+            sum[q] += x + y;
+            p[e] = pack2<BF16>(x, y);
+          }
+          tmem_store16(s_at + q * 16, p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl.p_ready[t]));
+      }
+      if (stop) break;
+      if (n > 0) {
+        if (!wait_bar(ptx::smem_addr(&ctl.o_done[t]), done & 1, abort_flag)) break;
+        ++done;
+        ptx::tc_fence_after();
+      }
+      const bool live = row < g.rows && i < g.Lq;
+      const int64_t h = (int64_t)it.hk * g.G + head;
+      const int64_t at = ((int64_t)it.b * g.Hq + h) * g.Lq + i;
+      const bool any = n > 0 && limit > 0 && l != 0.0f;  // l: NaN counts as present
+      const float inv = any ? 1.0f / l : 0.0f;
+      const float lse2 = any ? m + log2f(l) : -INFINITY;
+      const int64_t rows = g.B * g.Hq * g.Lq;
+      if (live) {
+        if (a.splits > 1) a.part_lse[(int64_t)it.split * rows + at] = lse2;
+        else if (a.lse) a.lse[at] = lse2 * kLn2;
+      }
+      uint16_t* out = (uint16_t*)a.out + it.b * a.o[0] + i * a.o[1] + h * a.o[2];
+      float* part = a.part + ((int64_t)it.split * rows + at) * g.D;
+      for (int q = 0; q < (g.D + 31) / 32; ++q) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_fetch32(o_at + q * 32, o);
+          tmem_wait_ld();
+          tmem_arrived(o);
+        }
+        if (!live) continue;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = any ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+        if (a.splits > 1) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            if (q * 32 + e < g.D)
+              ptx::st_global_v4(part + q * 32 + e, make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            if (q * 32 + e < g.D) {
+              uint4 w;
+              w.x = pack2<BF16>(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
+              w.y = pack2<BF16>(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+              w.z = pack2<BF16>(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]));
+              w.w = pack2<BF16>(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7]));
+              ptx::st_global_v4(out + q * 32 + e, w);
+            }
+        }
+      }
+    }
+  }
+
+  ptx::pdl_trigger();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the key splits of a row: out = sum_s w_s part_s / sum_s w_s, w_s = 2^(lse_s - max).
+// One warp per row, splits in order.
+template <bool BF16>
+__global__ void __launch_bounds__(256) attn_tc_join(const FwdArgs a) {
+  ptx::pdl_wait();
+  ptx::pdl_trigger();
+  const TcGeom& g = a.g;
+  const int64_t rows = g.B * g.Hq * g.Lq;
+  const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (at >= rows) return;
+  float top = -INFINITY;
+  for (int s = lane; s < a.splits; s += 32) top = fmaxf(top, a.part_lse[(int64_t)s * rows + at]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float ref = top == -INFINITY ? 0.0f : top;
+  float total = 0.0f;
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int d = lane * 4;
+  for (int s = 0; s < a.splits; ++s) {
+    const float lse = a.part_lse[(int64_t)s * rows + at];
+    if (lse == -INFINITY) continue;
+    const float w = exp2f(lse - ref);
+    total += w;
+    if (d < g.D) {
+      const float4 p =
+          *reinterpret_cast<const float4*>(a.part + ((int64_t)s * rows + at) * g.D + d);
+      acc[0] = fmaf(w, p.x, acc[0]);
+      acc[1] = fmaf(w, p.y, acc[1]);
+      acc[2] = fmaf(w, p.z, acc[2]);
+      acc[3] = fmaf(w, p.w, acc[3]);
+    }
+  }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  const int64_t i = at % g.Lq, bh = at / g.Lq, h = bh % g.Hq, b = bh / g.Hq;
+  if (d < g.D) {
+    uint16_t* out = (uint16_t*)a.out + b * a.o[0] + i * a.o[1] + h * a.o[2] + d;
+    const uint2 v = make_uint2(pack2<BF16>(acc[0] * inv, acc[1] * inv),
+                               pack2<BF16>(acc[2] * inv, acc[3] * inv));
+    *reinterpret_cast<uint2*>(out) = v;
+  }
+  if (a.lse && lane == 0)
+    a.lse[at] = total == 0.0f ? -INFINITY : (ref + log2f(total)) * kLn2;
+}
+
+// Key splits: the count with the shortest schedule, in key-tile steps. A block's item costs its
+// tiles and about 1.5 steps of loading and writing; the join about 2. With ragged lengths the
+// longest item rather than a full round ends the schedule.
+int split_count(const TcGeom& g, bool ragged, int sms, int pairs) {
+  const long long base = (long long)g.B * g.Hk * pairs;
+  int best = 1;
+  double least = 1e30;
+  for (int s = 1; s <= g.ktiles && s <= 64; ++s) {
+    const int per = (g.ktiles + s - 1) / s;
+    if ((g.ktiles + per - 1) / per != s) continue;
+    double cost;
+    if (ragged)
+      cost = (double)base * (g.ktiles * 0.75 + 1.5 * s) / sms + per;
+    else
+      cost = (double)((base * s + sms - 1) / sms) * (per + 1.5);
+    if (s > 1) cost += 2.0 + (double)s * g.Lq * g.G * g.B * g.Hk / 4.0 / (128.0 * sms);
+    if (cost < least - 1e-9) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+FwdArgs fwd_args(const fconv_attn_desc& d, int sms, const AttnArgs& a) {
+  FwdArgs f{};
+  f.g = tc_geom(d, a);
+  f.pairs = (f.g.qtiles + 1) / 2;
+  f.splits = split_count(f.g, d.has_kv_lens != 0, sms, f.pairs);
+  f.per = (f.g.ktiles + f.splits - 1) / f.splits;
+  f.items = (int)((long long)f.g.B * f.g.Hk * f.pairs * f.splits);
+  for (int i = 0; i < 3; ++i) f.o[i] = d.out_stride[i];
+  f.out = a.o;
+  f.lse = a.lse;
+  const size_t rows = (size_t)f.g.B * f.g.Hq * f.g.Lq;
+  f.part_lse = (float*)a.ws;
+  f.part = f.part_lse ? f.part_lse + ((size_t)f.splits * rows + 3) / 4 * 4 : nullptr;
+  return f;
+}
+
+template <bool BF16, int H>
+int launch_t(const FwdArgs& f, int sms, const CUtensorMap* m, cudaStream_t s) {
+  auto kern = attn_tc_forward<BF16, H>;
+  const int e = (int)cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          (int)FwdPlan<H>::smem);
+  if (e) return e;
+  const int grid = f.items < sms ? f.items : sms;
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), FwdPlan<H>::smem, s, f, m[0], m[1], m[2]);
+}
+
+}  // namespace
+
+// Strides of axes that are walked must be whole 16-byte units; 0 only on an axis of K or V
+// that a block does not walk (batch, head).
+bool attn_tc_supported(const fconv_attn_desc& d) {
+  if (d.dtype == FCONV_F32 || d.head_dim % 8 != 0 || d.head_dim > 128) return false;
+  if (d.heads_q / d.heads_kv > kTile || d.len_q == 0 || d.len_k == 0 || d.batch == 0) return false;
+  auto unit = [](int64_t stride, int64_t extent, bool zero) {
+    return extent == 1 || (stride % 8 == 0 && stride < (int64_t)1 << 38 && (stride > 0 || zero));
+  };
+  auto ok = [&](const int64_t st[3], int64_t len, int64_t heads, bool zero_head) {
+    return unit(st[0], d.batch, true) && unit(st[1], len, false) && unit(st[2], heads, zero_head);
+  };
+  const int64_t h = d.heads_q, kh = d.heads_kv;
+  if (!ok(d.q_stride, d.len_q, h, false) || !ok(d.k_stride, d.len_k, kh, true) ||
+      !ok(d.v_stride, d.len_k, kh, true) || !ok(d.out_stride, d.len_q, h, false))
+    return false;
+  // blocks' items, up to 64 key splits each, count in 32 bits
+  const int64_t toks = kTile / (h / kh);
+  return d.batch * kh * ((d.len_q + toks - 1) / toks / 2 + 1) <= INT_MAX / 128;
+}
+
+size_t attn_tc_forward_workspace(const fconv_attn_desc& d, int sms) {
+  const FwdArgs f = fwd_args(d, sms, AttnArgs{});
+  if (f.splits == 1) return 0;
+  const size_t rows = (size_t)d.batch * d.heads_q * d.len_q;
+  return (((size_t)f.splits * rows + 3) / 4 * 4 + (size_t)f.splits * rows * d.head_dim) *
+         sizeof(float);
+}
+
+int launch_attn_tc_forward(const fconv_attn_desc& d, int sms, const AttnArgs& a, cudaStream_t s) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (!enc) return (int)cudaErrorNotSupported;
+  FwdArgs f = fwd_args(d, sms, a);
+  CUtensorMap m[3];
+  std::memset(m, 0, sizeof(m));
+  if (!make_map(enc, &m[0], a.q, d.dtype, d.head_dim, d.heads_q, d.len_q, d.batch, d.q_stride,
+                f.g.G, f.g.toks, nullptr, &f.g.qb) ||
+      !make_map(enc, &m[1], a.k, d.dtype, d.head_dim, d.heads_kv, d.len_k, d.batch, d.k_stride, 1,
+                kTile, &f.g.kh, &f.g.kb) ||
+      !make_map(enc, &m[2], a.v, d.dtype, d.head_dim, d.heads_kv, d.len_k, d.batch, d.v_stride, 1,
+                kTile, &f.g.vh, &f.g.vb))
+    return (int)cudaErrorInvalidValue;
+  const bool bf = d.dtype == FCONV_BF16;
+  int e;
+  if (d.head_dim <= 64)
+    e = bf ? launch_t<true, 1>(f, sms, m, s) : launch_t<false, 1>(f, sms, m, s);
+  else
+    e = bf ? launch_t<true, 2>(f, sms, m, s) : launch_t<false, 2>(f, sms, m, s);
+  if (e || f.splits == 1) return e;
+  const long long rows = (long long)f.g.B * f.g.Hq * f.g.Lq;
+  return launch_pdl(bf ? attn_tc_join<true> : attn_tc_join<false>, dim3((unsigned)((rows + 7) / 8)),
+                    dim3(256), 0, s, f);
+}
+
+int read_and_clear_attn_forward_error(cudaStream_t s, unsigned* v) {
+  return read_and_clear_error(s, v);
+}
+
+}  // namespace ops
+}  // namespace fconv

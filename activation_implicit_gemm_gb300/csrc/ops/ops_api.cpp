@@ -183,7 +183,9 @@ const char* fconv_ops_status_string(int s) {
 }
 
 fconv_status fconv_ops_check_device(void* stream) {
-  return cudaStreamSynchronize((cudaStream_t)stream) == cudaSuccess ? FCONV_OK : FCONV_E_CUDA;
+  unsigned v = 0;
+  if (read_and_clear_attn_forward_error((cudaStream_t)stream, &v) != 0) return FCONV_E_CUDA;
+  return v ? FCONV_E_DEVICE_TIMEOUT : FCONV_OK;
 }
 
 // ---------------------------------------------------------------------------- layer norm
@@ -295,14 +297,15 @@ fconv_status fconv_attn_plan_create(const fconv_attn_desc* desc, int device, int
   const fconv_status st = new_plan(desc, device, check_attn, out);
   if (st != FCONV_OK) return st;
   fconv_attn_plan* p = *out;
-  p->want = route;
-  p->route = FCONV_ATTN_SIMPLE;
-  if (route != FCONV_ATTN_AUTO && route != p->route) {
+  const bool tc = attn_tc_supported(p->d);
+  if (route < FCONV_ATTN_AUTO || route > FCONV_ATTN_TC || (route == FCONV_ATTN_TC && !tc)) {
     delete p;
     *out = nullptr;
     return FCONV_E_UNSUPPORTED;
   }
-  p->fwd_ws = 0;
+  p->want = route;
+  p->route = tc && route != FCONV_ATTN_SIMPLE ? FCONV_ATTN_TC : FCONV_ATTN_SIMPLE;
+  p->fwd_ws = p->route == FCONV_ATTN_TC ? attn_tc_forward_workspace(p->d, p->sms) : 0;
   p->bwd_ws = attn_simple_backward_workspace(p->d);
   return FCONV_OK;
 }
@@ -349,6 +352,11 @@ fconv_status fconv_attn_forward(const fconv_attn_plan* p, const void* q, const v
   a.o = out;
   a.lse = lse;
   a.ws = workspace;
+  if (p->route == FCONV_ATTN_TC) {
+    if (!misaligned(q, 16) && !misaligned(k, 16) && !misaligned(v, 16) && !misaligned(out, 16))
+      return done(launch_attn_tc_forward(d, p->sms, a, (cudaStream_t)stream));
+    if (p->want == FCONV_ATTN_TC) return FCONV_E_ALIGNMENT;
+  }
   return done(launch_attn_simple_forward(d, a, (cudaStream_t)stream));
 }
 

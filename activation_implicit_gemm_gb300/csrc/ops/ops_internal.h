@@ -59,6 +59,12 @@ int launch_attn_simple_forward(const fconv_attn_desc& d, const AttnArgs& a, cuda
 int launch_attn_simple_backward(const fconv_attn_desc& d, const AttnArgs& a, cudaStream_t s);
 size_t attn_simple_backward_workspace(const fconv_attn_desc& d);
 
+// Tensor-core route (k_attn_tc_*.cu): addresses must be 16-byte aligned.
+bool attn_tc_supported(const fconv_attn_desc& d);
+size_t attn_tc_forward_workspace(const fconv_attn_desc& d, int sms);
+int launch_attn_tc_forward(const fconv_attn_desc& d, int sms, const AttnArgs& a, cudaStream_t s);
+int read_and_clear_attn_forward_error(cudaStream_t s, unsigned* value);
+
 // Whether a launch's block count fits the grid's first axis.
 inline bool grid_ok(long long blocks) { return blocks > 0 && blocks <= 0x7fffffffLL; }
 
