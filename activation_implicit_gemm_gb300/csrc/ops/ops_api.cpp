@@ -24,8 +24,8 @@ struct fconv_rope_plan {
 struct fconv_attn_plan {
   fconv_attn_desc d;
   int sms;
-  int want;   // the route asked for
-  int route;  // the route of a call with aligned addresses
+  int want;            // the route asked for
+  bool fwd_tc, bwd_tc;  // tensor cores for calls with aligned addresses
   size_t fwd_ws, bwd_ws;
 };
 
@@ -183,9 +183,11 @@ const char* fconv_ops_status_string(int s) {
 }
 
 fconv_status fconv_ops_check_device(void* stream) {
-  unsigned v = 0;
-  if (read_and_clear_attn_forward_error((cudaStream_t)stream, &v) != 0) return FCONV_E_CUDA;
-  return v ? FCONV_E_DEVICE_TIMEOUT : FCONV_OK;
+  unsigned f = 0, b = 0;
+  if (read_and_clear_attn_forward_error((cudaStream_t)stream, &f) != 0 ||
+      read_and_clear_attn_backward_error((cudaStream_t)stream, &b) != 0)
+    return FCONV_E_CUDA;
+  return f || b ? FCONV_E_DEVICE_TIMEOUT : FCONV_OK;
 }
 
 // ---------------------------------------------------------------------------- layer norm
@@ -297,22 +299,31 @@ fconv_status fconv_attn_plan_create(const fconv_attn_desc* desc, int device, int
   const fconv_status st = new_plan(desc, device, check_attn, out);
   if (st != FCONV_OK) return st;
   fconv_attn_plan* p = *out;
-  const bool tc = attn_tc_supported(p->d);
-  if (route < FCONV_ATTN_AUTO || route > FCONV_ATTN_TC || (route == FCONV_ATTN_TC && !tc)) {
+  const bool fwd = attn_tc_supported(p->d);
+  const bool bwd = p->d.training && attn_tc_backward_supported(p->d);
+  if (route < FCONV_ATTN_AUTO || route > FCONV_ATTN_TC ||
+      (route == FCONV_ATTN_TC && (!fwd || (p->d.training && !bwd)))) {
     delete p;
     *out = nullptr;
     return FCONV_E_UNSUPPORTED;
   }
   p->want = route;
-  p->route = tc && route != FCONV_ATTN_SIMPLE ? FCONV_ATTN_TC : FCONV_ATTN_SIMPLE;
-  p->fwd_ws = p->route == FCONV_ATTN_TC ? attn_tc_forward_workspace(p->d, p->sms) : 0;
-  p->bwd_ws = attn_simple_backward_workspace(p->d);
+  p->fwd_tc = fwd && route != FCONV_ATTN_SIMPLE;
+  p->bwd_tc = bwd && route != FCONV_ATTN_SIMPLE;
+  p->fwd_ws = p->fwd_tc ? attn_tc_forward_workspace(p->d, p->sms) : 0;
+  if (p->d.training) {
+    p->bwd_ws = attn_simple_backward_workspace(p->d);
+    if (p->bwd_tc) {  // a call with unaligned addresses takes the simple route
+      const size_t n = attn_tc_backward_workspace(p->d, p->sms);
+      if (n > p->bwd_ws) p->bwd_ws = n;
+    }
+  }
   return FCONV_OK;
 }
 
 fconv_status fconv_attn_plan_route(const fconv_attn_plan* p, int* route) {
   if (!p || !route) return FCONV_E_NULL;
-  *route = p->route;
+  *route = (p->d.training ? p->bwd_tc : p->fwd_tc) ? FCONV_ATTN_TC : FCONV_ATTN_SIMPLE;
   return FCONV_OK;
 }
 
@@ -352,7 +363,7 @@ fconv_status fconv_attn_forward(const fconv_attn_plan* p, const void* q, const v
   a.o = out;
   a.lse = lse;
   a.ws = workspace;
-  if (p->route == FCONV_ATTN_TC) {
+  if (p->fwd_tc) {
     if (!misaligned(q, 16) && !misaligned(k, 16) && !misaligned(v, 16) && !misaligned(out, 16))
       return done(launch_attn_tc_forward(d, p->sms, a, (cudaStream_t)stream));
     if (p->want == FCONV_ATTN_TC) return FCONV_E_ALIGNMENT;
@@ -399,6 +410,13 @@ fconv_status fconv_attn_backward(const fconv_attn_plan* p, const void* dout, con
   a.dk = dk;
   a.dv = dv;
   a.ws = workspace;
+  if (p->bwd_tc) {
+    bool whole = true;
+    for (const void* x : {dout, q, k, v, out, (const void*)dq, (const void*)dk, (const void*)dv})
+      whole = whole && !misaligned(x, 16);
+    if (whole) return done(launch_attn_tc_backward(d, p->sms, a, (cudaStream_t)stream));
+    if (p->want == FCONV_ATTN_TC) return FCONV_E_ALIGNMENT;
+  }
   return done(launch_attn_simple_backward(d, a, (cudaStream_t)stream));
 }
 

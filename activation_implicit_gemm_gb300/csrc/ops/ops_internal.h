@@ -64,6 +64,10 @@ bool attn_tc_supported(const fconv_attn_desc& d);
 size_t attn_tc_forward_workspace(const fconv_attn_desc& d, int sms);
 int launch_attn_tc_forward(const fconv_attn_desc& d, int sms, const AttnArgs& a, cudaStream_t s);
 int read_and_clear_attn_forward_error(cudaStream_t s, unsigned* value);
+bool attn_tc_backward_supported(const fconv_attn_desc& d);
+size_t attn_tc_backward_workspace(const fconv_attn_desc& d, int sms);
+int launch_attn_tc_backward(const fconv_attn_desc& d, int sms, const AttnArgs& a, cudaStream_t s);
+int read_and_clear_attn_backward_error(cudaStream_t s, unsigned* value);
 
 // Whether a launch's block count fits the grid's first axis.
 inline bool grid_ok(long long blocks) { return blocks > 0 && blocks <= 0x7fffffffLL; }

@@ -136,9 +136,9 @@ typedef struct fconv_attn_plan fconv_attn_plan;
 /* route: FCONV_ATTN_AUTO, or one that must run the request (else FCONV_E_UNSUPPORTED). */
 fconv_status fconv_attn_plan_create(const fconv_attn_desc* desc, int device, int route,
                                     fconv_attn_plan** out);
-/* The route of a call whose device addresses are 16-byte aligned (a call with others runs on
- * FCONV_ATTN_SIMPLE, unless the plan was made for FCONV_ATTN_TC: then it is refused with
- * FCONV_E_ALIGNMENT). */
+/* The route of a call whose device addresses are 16-byte aligned, of the backward pass in a
+ * training plan (a call with others runs on FCONV_ATTN_SIMPLE, unless the plan was made for
+ * FCONV_ATTN_TC: then it is refused with FCONV_E_ALIGNMENT). */
 fconv_status fconv_attn_plan_route(const fconv_attn_plan* plan, int* route);
 fconv_status fconv_attn_forward_workspace(const fconv_attn_plan* plan, size_t* bytes);
 fconv_status fconv_attn_backward_workspace(const fconv_attn_plan* plan, size_t* bytes);

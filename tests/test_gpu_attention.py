@@ -259,3 +259,22 @@ def test_offsets_past_32_bits(dtype):
         return x
 
     run_and_check(q, k, v, g, causal=True, place=place)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("size", [2.0 ** -13, 1.0, 256.0])
+def test_gradients_of_every_size(dtype, size):
+    """Small output gradients over long sequences (score gradients far below f16's smallest
+    normal value) and large ones (score gradients past f16's largest value times the keys)
+    keep the relative accuracy of the type."""
+    q, k, v, g = tensors(1, 260, 1300, 2, 1, 64, dtype)
+    T = R.TYPES[dtype]
+    g, v = (g.float() * size).to(T), (v.float() * 8).to(T)
+    out, lse = fc.attention(q.cuda(), k.cuda(), v.cuda(), return_lse=True)
+    got = fc.attention_backward(g.cuda(), q.cuda(), k.cuda(), v.cuda(), out, lse)
+    want = R.attention(q, k, v, dout=g)
+    for name, t in zip(("dq", "dk", "dv"), got):
+        ref = want[name][0]
+        floor = R.TINY[T] * ref.numel() ** 0.5  # the output's own rounding near zero
+        off = (t.double().cpu() - ref).norm()
+        assert off <= 3 * R.U[T] * ref.norm() + floor, (name, float(off / ref.norm()))
