@@ -63,6 +63,7 @@ _PROTOS = {
     "fconv_ops_status_string": [I32],
 }
 _ready = None
+torch = None  # imported with the first call: the plans alone need no PyTorch
 
 
 def load() -> ctypes.CDLL:
@@ -86,6 +87,14 @@ def _check(status: int, where: str):
         raise FconvError(status, where)
 
 
+def _start():
+    """First call of an operator: PyTorch and the library."""
+    global torch
+    import torch as t
+    load()
+    torch = t
+
+
 def check_device(stream=None) -> None:
     """Synchronise `stream` and raise if a kernel of these operators gave up a wait."""
     _check(load().fconv_ops_check_device(None if stream is None else stream.cuda_stream),
@@ -93,7 +102,6 @@ def check_device(stream=None) -> None:
 
 
 def _code(dtype) -> int:
-    import torch
     code = {torch.float32: _lib.F32, torch.float16: _lib.F16, torch.bfloat16: BF16}.get(dtype)
     if code is None:
         raise FconvError(14, f"dtype {dtype}")
@@ -126,39 +134,29 @@ class _Plan:
             pass
 
 
-def _on_cuda(who: str, *tensors) -> None:
-    device = tensors[0].device
-    for t in tensors:
-        if t is not None and (not t.is_cuda or t.device != device):
-            raise ValueError(f"{who} runs on tensors of one CUDA device only")
+def _on_cuda(who: str, device: int, *tensors) -> None:
+    """All tensors that are there lie on one CUDA device."""
+    if device >= 0:
+        for t in tensors:
+            if t is not None and t.get_device() != device:
+                break
+        else:
+            return
+    raise ValueError(f"{who} runs on tensors of one CUDA device only")
+
+
+def _current_stream(device: int) -> int:
+    """The handle of the device's current stream; the plain handle spares building a Stream
+    object (2 us of the call's 10)."""
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _workspace(nbytes: int, like):
+    return torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes else None
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
-
-
-class _Stream:
-    """The stream of a call: the given one, or the current one of the tensors' device. Inside
-    the block new tensors belong to that stream."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.stream = torch.cuda.current_stream(device) if stream is None else stream
-        self.ctx = None if stream is None else torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-
-
-def _workspace(nbytes: int, device):
-    import torch
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
 # -------------------------------------------------------------------------------- layer norm
@@ -189,9 +187,9 @@ class LayerNormPlan(_Plan):
 _norm_plans: dict = {}
 
 
-def _norm_plan(who, x, weight, bias, axis, eps):
+def _norm_plan(who, x, weight, bias, axis, eps, device):
     key = (x.dtype, x.shape, axis, None if weight is None else weight.dtype,
-           None if bias is None else bias.dtype, eps, x.device)
+           None if bias is None else bias.dtype, eps, device)
     p = _norm_plans.get(key)
     if p is None:
         if not -x.dim() <= axis < x.dim():
@@ -204,13 +202,13 @@ def _norm_plan(who, x, weight, bias, axis, eps):
                           math.prod(x.shape[axis + 1:]),
                           param_dtype=None if param is None else _code(param.dtype),
                           has_weight=weight is not None, has_bias=bias is not None, eps=eps,
-                          device=x.device.index)
-        p.channels = x.shape[axis]
+                          device=device)
+        p.param_shape = x.shape[axis:axis + 1]
         p.stat_shape = x.shape[:axis] + x.shape[axis + 1:]
         _norm_plans[key] = p
     for t in (weight, bias):
-        if t is not None and (t.dim() != 1 or t.shape[0] != p.channels or not t.is_contiguous()):
-            raise ValueError(f"{who}: weight and bias are vectors of {p.channels} values")
+        if t is not None and (t.shape != p.param_shape or not t.is_contiguous()):
+            raise ValueError(f"{who}: weight and bias are vectors of {p.param_shape[0]} values")
     return p
 
 
@@ -220,21 +218,28 @@ def layer_norm(x, weight=None, bias=None, *, axis: int = -1, eps: float = 1e-5, 
     rows, axis 1 for channels-first features (N, C, D1..Dn). weight and bias have x's type or
     float32. With return_stats also mean and rstd (float32), which the gradient takes. `out`
     may be x."""
-    import torch
-    _on_cuda("layer_norm", x, weight, bias, out)
-    p = _norm_plan("layer_norm", x, weight, bias, axis, eps)
-    if not x.is_contiguous() or (out is not None and not out.is_contiguous()):
+    if torch is None:
+        _start()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layer_norm(x, weight, bias, axis=axis, eps=eps, out=out,
+                              return_stats=return_stats)
+    device = x.get_device()
+    _on_cuda("layer_norm", device, weight, bias, out)
+    p = _norm_plan("layer_norm", x, weight, bias, axis, eps, device)
+    if not x.is_contiguous():
         raise ValueError("layer_norm tensors must be contiguous")
-    if out is not None and (out.shape != x.shape or out.dtype != x.dtype):
-        raise ValueError("layer_norm: out must be like x")
-    with _Stream(x.device, stream) as s:
-        y = torch.empty_like(x) if out is None else out
-        mean = rstd = None
-        if return_stats:
-            mean = torch.empty(p.stat_shape, dtype=torch.float32, device=x.device)
-            rstd = torch.empty_like(mean)
-        p.forward_ptrs(_ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd), s)
-    return (y, mean, rstd) if return_stats else y
+    if out is None:
+        out = torch.empty_like(x)
+    elif out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous():
+        raise ValueError("layer_norm: out must be like x and contiguous")
+    mean = rstd = None
+    if return_stats:
+        mean = torch.empty(p.stat_shape, dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+    p.forward_ptrs(x.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(), _ptr(mean), _ptr(rstd),
+                   _current_stream(device))
+    return (out, mean, rstd) if return_stats else out
 
 
 def layer_norm_backward(dy, x, mean, rstd, weight=None, bias=None, *, axis: int = -1,
@@ -242,25 +247,31 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, bias=None, *, axis: int 
     """Gradients (dx, dweight, dbias) of layer_norm. mean and rstd are the forward pass's; of
     bias only its presence and type matter. dweight and dbias are None for an absent weight or
     bias, or without param_grads."""
-    import torch
-    _on_cuda("layer_norm_backward", dy, x, mean, rstd, weight, bias)
-    p = _norm_plan("layer_norm_backward", x, weight, bias, axis, 1e-5)
+    if torch is None:
+        _start()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layer_norm_backward(dy, x, mean, rstd, weight, bias, axis=axis,
+                                       param_grads=param_grads)
+    device = x.get_device()
+    _on_cuda("layer_norm_backward", device, dy, mean, rstd, weight, bias)
+    p = _norm_plan("layer_norm_backward", x, weight, bias, axis, 1e-5, device)
     if dy.shape != x.shape or dy.dtype != x.dtype:
         raise ValueError("layer_norm_backward: dy must be like x")
     for t in (mean, rstd):
         if t.shape != p.stat_shape or t.dtype != torch.float32:
             raise ValueError("layer_norm_backward: mean and rstd are float32 of shape "
                              f"{tuple(p.stat_shape)}")
-    if not all(t.is_contiguous() for t in (dy, x, mean, rstd)):
+    if not (dy.is_contiguous() and x.is_contiguous() and mean.is_contiguous()
+            and rstd.is_contiguous()):
         raise ValueError("layer_norm_backward tensors must be contiguous")
-    with _Stream(x.device, stream) as s:
-        dx = torch.empty_like(x)
-        dw = torch.empty_like(weight) if weight is not None and param_grads else None
-        db = torch.empty_like(bias) if bias is not None and param_grads else None
-        n = p.workspace_bytes if dw is not None or db is not None else 0
-        ws = _workspace(n, x.device)
-        p.backward_ptrs(_ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx),
-                        _ptr(dw), _ptr(db), _ptr(ws), n, s)
+    dx = torch.empty_like(x)
+    dw = torch.empty_like(weight) if weight is not None and param_grads else None
+    db = torch.empty_like(bias) if bias is not None and param_grads else None
+    n = p.workspace_bytes if dw is not None or db is not None else 0
+    ws = _workspace(n, x)
+    p.backward_ptrs(dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(),
+                    dx.data_ptr(), _ptr(dw), _ptr(db), _ptr(ws), n, _current_stream(device))
     return dx, dw, db
 
 
@@ -306,7 +317,8 @@ def rope_frequencies(sections: Sequence[int], theta: float = 10000.0, shared: bo
                      device="cuda"):
     """inv_freq for `rope`: each axis counts its own frequencies theta^(-i / n) over its n
     pairs, or with `shared` the axes split one sequence over all pairs."""
-    import torch
+    if torch is None:
+        _start()
     total = sum(sections)
     values = []
     for n in sections:
@@ -323,22 +335,49 @@ def rope(q, k=None, *, positions, inv_freq, sections: Optional[Sequence[int]] = 
     pairs of each axis in order (default: all pairs on one axis). `inverse` turns back, which
     is the gradient. q and k may be strided views with a contiguous last axis; out and k_out
     may be q and k. Returns q', or (q', k')."""
-    import torch
-    _on_cuda("rope", q, k, positions, inv_freq, out, k_out)
+    if torch is None:
+        _start()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rope(q, k, positions=positions, inv_freq=inv_freq, sections=sections,
+                        pairing=pairing, inverse=inverse, out=out, k_out=k_out)
+    device = q.get_device()
+    _on_cuda("rope", device, k, positions, inv_freq, out, k_out)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    sections = None if sections is None else tuple(sections)
+    # everything the checks look at is in the key: a call like an earlier one has passed them
+    key = (q.dtype, q.shape, q.stride(), out.dtype, out.shape, out.stride(), positions.dtype,
+           positions.shape, positions.is_contiguous(), inv_freq.dtype, inv_freq.shape,
+           inv_freq.is_contiguous(), sections, pairing, inverse, device)
+    if k is not None or k_out is not None:
+        key += (None,) if k is None else (k.dtype, k.shape, k.stride(), k_out.dtype, k_out.shape,
+                                          k_out.stride())
+    p = _rope_plans.get(key)
+    if p is None:
+        p = _rope_plans[key] = _rope_plan(q, k, positions, inv_freq, sections, pairing, inverse,
+                                          out, k_out, device)
+    p.run_ptrs(q.data_ptr(), _ptr(k), positions.data_ptr(), inv_freq.data_ptr(), out.data_ptr(),
+               _ptr(k_out), _current_stream(device))
+    return out if k is None else (out, k_out)
+
+
+def _rope_plan(q, k, positions, inv_freq, sections, pairing, inverse, out, k_out, device):
     _heads("rope", "q", q)
-    if sections is None:
-        sections = (inv_freq.numel(),)
-        if positions.dim() in (1, 2):
-            positions = positions.unsqueeze(-1)
-    sections = tuple(sections)
-    if positions.dim() == 2:
-        positions = positions.unsqueeze(0)
     pos_type = {torch.int32: 0, torch.int64: 1, torch.float32: 2}.get(positions.dtype)
     if pos_type is None:
         raise FconvError(14, f"positions of {positions.dtype}")
-    if (positions.dim() != 3 or positions.shape[0] not in (1, q.shape[0])
-            or positions.shape[1] != q.shape[1] or positions.shape[2] != len(sections)
-            or not positions.is_contiguous()):
+    shape = tuple(positions.shape)
+    if sections is None:
+        sections = (inv_freq.numel(),)
+        if len(shape) in (1, 2):
+            shape += (1,)
+    if len(shape) == 2:
+        shape = (1,) + shape
+    if (len(shape) != 3 or shape[0] not in (1, q.shape[0]) or shape[1] != q.shape[1]
+            or shape[2] != len(sections) or not positions.is_contiguous()):
         raise ValueError("rope: positions must be contiguous (1 or batch, tokens, axes)")
     if (inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous()
             or inv_freq.numel() != sum(sections)):
@@ -352,27 +391,14 @@ def rope(q, k=None, *, positions, inv_freq, sections: Optional[Sequence[int]] = 
             if like is None or t.shape != like.shape or t.dtype != like.dtype:
                 raise ValueError(f"rope: {name} must be like its input")
             _heads("rope", name, t)
-    with _Stream(q.device, stream) as s:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        key = (q.dtype, q.shape, q.stride(), out.stride(), positions.shape, pos_type, sections,
-               pairing, inverse, q.device,
-               None if k is None else (k.shape, k.stride(), k_out.stride()))
-        p = _rope_plans.get(key)
-        if p is None:
-            b, t, h, d = q.shape
-            none = (0, 0, 0)
-            p = _rope_plans[key] = RopePlan(
-                _code(q.dtype), b, t, h, 0 if k is None else k.shape[2], d,
-                q_stride=q.stride()[:3], q_out_stride=out.stride()[:3],
-                k_stride=none if k is None else k.stride()[:3],
-                k_out_stride=none if k is None else k_out.stride()[:3], sections=sections,
-                pairing=pairing, pos_type=pos_type, pos_batch=positions.shape[0],
-                inverse=inverse, device=q.device.index)
-        p.run_ptrs(_ptr(q), _ptr(k), _ptr(positions), _ptr(inv_freq), _ptr(out), _ptr(k_out), s)
-    return out if k is None else (out, k_out)
+    b, t, h, d = q.shape
+    none = (0, 0, 0)
+    return RopePlan(_code(q.dtype), b, t, h, 0 if k is None else k.shape[2], d,
+                    q_stride=q.stride()[:3], q_out_stride=out.stride()[:3],
+                    k_stride=none if k is None else k.stride()[:3],
+                    k_out_stride=none if k is None else k_out.stride()[:3], sections=sections,
+                    pairing=pairing, pos_type=pos_type, pos_batch=shape[0], inverse=inverse,
+                    device=device)
 
 
 # ---------------------------------------------------------------------------------- attention
@@ -417,8 +443,20 @@ class AttentionPlan(_Plan):
 _attn_plans: dict = {}
 
 
-def _attn_args(who, q, k, v, q_lens, kv_lens):
-    import torch
+def _attn_plan(who, q, k, v, out, causal, scale, q_lens, kv_lens, route, device, grads=None):
+    """The cached plan of a call. Everything the checks look at is in the key, so a call like
+    an earlier one has passed them. grads: (dout, dq, dk, dv) of a backward pass."""
+    key = (q.dtype, k.dtype, v.dtype, out.dtype, q.shape, k.shape, v.shape, out.shape, q.stride(),
+           k.stride(), v.stride(), out.stride(), causal, scale, route, device)
+    if q_lens is not None or kv_lens is not None:
+        for t in (q_lens, kv_lens):
+            key += (None,) if t is None else (t.dtype, t.shape, t.is_contiguous())
+    if grads is not None:
+        for t in grads:
+            key += (t.dtype, t.shape, t.stride())
+    p = _attn_plans.get(key)
+    if p is not None:
+        return p
     for name, t in (("q", q), ("k", k), ("v", v)):
         _heads(who, name, t)
     if (k.shape != v.shape or k.dtype != q.dtype or v.dtype != q.dtype
@@ -428,6 +466,26 @@ def _attn_args(who, q, k, v, q_lens, kv_lens):
         if t is not None and (t.dtype != torch.int32 or t.shape != q.shape[:1]
                               or not t.is_contiguous()):
             raise ValueError(f"{who}: {name} must be contiguous int32 with one value a sequence")
+    named = [("out", out, q)]
+    if grads is not None:
+        named += zip(("dout", "dq", "dk", "dv"), grads, (q, q, k, v))
+    for name, t, like in named:
+        if t.shape != like.shape or t.dtype != like.dtype:
+            raise ValueError(f"{who}: {name} has another shape or type than its tensor")
+        _heads(who, name, t)
+    b, lq, h, d = q.shape
+    strides = {}
+    if grads is not None:
+        strides = {n + "_stride": t.stride()[:3]
+                   for n, t in zip(("dout", "dq", "dk", "dv"), grads)}
+    p = _attn_plans[key] = AttentionPlan(
+        _code(q.dtype), b, lq, k.shape[1], h, k.shape[2], d, q_stride=q.stride()[:3],
+        k_stride=k.stride()[:3], v_stride=v.stride()[:3], out_stride=out.stride()[:3],
+        scale=scale, causal=causal, has_q_lens=q_lens is not None,
+        has_kv_lens=kv_lens is not None, training=grads is not None, route=route, device=device,
+        **strides)
+    p.lse_shape = (b, h, lq)
+    return p
 
 
 def attention(q, k, v, *, causal: bool = False, scale: Optional[float] = None, q_lens=None,
@@ -438,34 +496,24 @@ def attention(q, k, v, *, causal: bool = False, scale: Optional[float] = None, q
     q_lens and kv_lens (int32, one value a sequence) cut sequences short; causal lets query i
     see keys up to i + kv_len - q_len. A query that sees no key gives 0. With return_lse also
     the log of the softmax sums (batch, heads, queries) in float32, which the gradient takes."""
-    import torch
-    _on_cuda("attention", q, k, v, q_lens, kv_lens, out)
-    _attn_args("attention", q, k, v, q_lens, kv_lens)
-    if out is not None:
-        if out.shape != q.shape or out.dtype != q.dtype:
-            raise ValueError("attention: out must be like q")
-        _heads("attention", "out", out)
-    with _Stream(q.device, stream) as s:
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        key = (q.dtype, q.shape, k.shape, q.stride(), k.stride(), v.stride(), out.stride(),
-               causal, scale, q_lens is None, kv_lens is None, route, q.device)
-        p = _attn_plans.get(key)
-        if p is None:
-            b, lq, h, d = q.shape
-            p = _attn_plans[key] = AttentionPlan(
-                _code(q.dtype), b, lq, k.shape[1], h, k.shape[2], d, q_stride=q.stride()[:3],
-                k_stride=k.stride()[:3], v_stride=v.stride()[:3], out_stride=out.stride()[:3],
-                scale=scale, causal=causal, has_q_lens=q_lens is not None,
-                has_kv_lens=kv_lens is not None, route=route, device=q.device.index)
-        lse = None
-        if return_lse:
-            lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32,
-                              device=q.device)
-        n = p.forward_workspace
-        ws = _workspace(n, q.device)
-        p.forward_ptrs(_ptr(q), _ptr(k), _ptr(v), _ptr(q_lens), _ptr(kv_lens), _ptr(out),
-                       _ptr(lse), _ptr(ws), n, s)
+    if torch is None:
+        _start()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return attention(q, k, v, causal=causal, scale=scale, q_lens=q_lens, kv_lens=kv_lens,
+                             out=out, return_lse=return_lse, route=route)
+    device = q.get_device()
+    _on_cuda("attention", device, k, v, q_lens, kv_lens, out)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    p = _attn_plan("attention", q, k, v, out, causal, scale, q_lens, kv_lens, route, device)
+    lse = None
+    if return_lse:
+        lse = torch.empty(p.lse_shape, dtype=torch.float32, device=q.device)
+    n = p.forward_workspace
+    ws = _workspace(n, q)
+    p.forward_ptrs(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(q_lens), _ptr(kv_lens),
+                   out.data_ptr(), _ptr(lse), _ptr(ws), n, _current_stream(device))
     return (out, lse) if return_lse else out
 
 
@@ -474,37 +522,25 @@ def attention_backward(dout, q, k, v, out, lse, *, causal: bool = False,
                        dk=None, dv=None, route: str = "auto", stream=None):
     """Gradients (dq, dk, dv) of attention, its probabilities made again from lse. out and lse
     are the forward pass's; dq, dk, dv may be given (strided views of one buffer, say)."""
-    import torch
-    _on_cuda("attention_backward", q, k, v, dout, out, lse, q_lens, kv_lens, dq, dk, dv)
-    _attn_args("attention_backward", q, k, v, q_lens, kv_lens)
-    for name, t, like in (("dout", dout, q), ("out", out, q), ("dq", dq, q), ("dk", dk, k),
-                          ("dv", dv, v)):
-        if t is not None:
-            if t.shape != like.shape or t.dtype != like.dtype:
-                raise ValueError(f"attention_backward: {name} has another shape or type")
-            _heads("attention_backward", name, t)
-    if (lse.shape != (q.shape[0], q.shape[2], q.shape[1]) or lse.dtype != torch.float32
-            or not lse.is_contiguous()):
+    if torch is None:
+        _start()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return attention_backward(dout, q, k, v, out, lse, causal=causal, scale=scale,
+                                      q_lens=q_lens, kv_lens=kv_lens, dq=dq, dk=dk, dv=dv,
+                                      route=route)
+    device = q.get_device()
+    _on_cuda("attention_backward", device, k, v, dout, out, lse, q_lens, kv_lens, dq, dk, dv)
+    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
+    dk = torch.empty(k.shape, dtype=k.dtype, device=q.device) if dk is None else dk
+    dv = torch.empty(v.shape, dtype=v.dtype, device=q.device) if dv is None else dv
+    p = _attn_plan("attention_backward", q, k, v, out, causal, scale, q_lens, kv_lens, route,
+                   device, (dout, dq, dk, dv))
+    if lse.shape != p.lse_shape or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("attention_backward: lse must be float32 (batch, heads, queries)")
-    with _Stream(q.device, stream) as s:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
-        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
-        dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
-        key = (q.dtype, q.shape, k.shape, q.stride(), k.stride(), v.stride(), out.stride(),
-               causal, scale, q_lens is None, kv_lens is None, route, q.device, dout.stride(),
-               dq.stride(), dk.stride(), dv.stride())
-        p = _attn_plans.get(key)
-        if p is None:
-            b, lq, h, d = q.shape
-            p = _attn_plans[key] = AttentionPlan(
-                _code(q.dtype), b, lq, k.shape[1], h, k.shape[2], d, q_stride=q.stride()[:3],
-                k_stride=k.stride()[:3], v_stride=v.stride()[:3], out_stride=out.stride()[:3],
-                dout_stride=dout.stride()[:3], dq_stride=dq.stride()[:3],
-                dk_stride=dk.stride()[:3], dv_stride=dv.stride()[:3], scale=scale,
-                causal=causal, has_q_lens=q_lens is not None, has_kv_lens=kv_lens is not None,
-                training=True, route=route, device=q.device.index)
-        n = p.backward_workspace
-        ws = _workspace(n, q.device)
-        p.backward_ptrs(_ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
-                        _ptr(q_lens), _ptr(kv_lens), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), n, s)
+    n = p.backward_workspace
+    ws = _workspace(n, q)
+    p.backward_ptrs(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                    lse.data_ptr(), _ptr(q_lens), _ptr(kv_lens), dq.data_ptr(), dk.data_ptr(),
+                    dv.data_ptr(), _ptr(ws), n, _current_stream(device))
     return dq, dk, dv

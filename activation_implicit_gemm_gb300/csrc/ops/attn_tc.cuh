@@ -1,7 +1,5 @@
 // Pieces shared by the tensor-core attention kernels: instruction wrappers beyond ../ptx.cuh,
-// bounded waits, the packing of query rows, tensor maps.
-//
-// Everything with state has internal linkage: each translation unit has its own error word.
+// the packing of query rows, tensor maps.
 #pragma once
 
 #include <cuda.h>
@@ -14,6 +12,7 @@
 #include "../fconv_internal.h"
 #include "../ptx.cuh"
 #include "ops_internal.h"
+#include "waits.cuh"
 
 namespace fconv {
 namespace ops {
@@ -23,41 +22,6 @@ constexpr int kTile = 128;                 // rows of a query tile, keys of a ke
 constexpr uint32_t kHalfBytes = kTile * 128;  // 128 rows of 64 elements: one 128-byte-row box
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
-constexpr uint64_t kDrainLimitNs = 200000000ull;
-
-__device__ unsigned g_attn_error = 0;
-
-// Wait for a phase of an mbarrier, for at most kWaitLimitNs; gives up early when another warp
-// of the block has. A wait that runs out sets the flag and the error word.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  if (ptx::mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = ptx::globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    if ((i & 63u) == 0) {
-      if (*abort_flag) return false;
-      if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
-        *abort_flag = 1;
-        atomicOr(&g_attn_error, 1u);
-        return false;
-      }
-    }
-  }
-}
-
-// Wait for operations this block has already issued (they always complete).
-__device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity) {
-  if (ptx::mbar_try_wait(bar, parity)) return;
-  const uint64_t t0 = ptx::globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (ptx::mbar_try_wait(bar, parity)) return;
-    if ((i & 63u) == 0 && ptx::globaltimer_ns() - t0 > kDrainLimitNs) {
-      atomicOr(&g_attn_error, 1u);
-      return;
-    }
-  }
-}
 
 // ------------------------------------------------------------------------- instructions
 
@@ -95,16 +59,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int 
       "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
       "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"((uint64_t)tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
-      : "memory");
-}
-
-// Contiguous copy of `bytes` (a multiple of 16, both addresses 16-byte aligned).
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
 
@@ -282,18 +236,6 @@ inline TcGeom tc_geom(const fconv_attn_desc& d, const AttnArgs& a) {
   g.q_lens = a.q_lens;
   g.kv_lens = a.kv_lens;
   return g;
-}
-
-inline int read_and_clear_error(cudaStream_t s, unsigned* value) {
-  unsigned v = 0, zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_attn_error, sizeof(v), 0,
-                                            cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && v)
-    e = cudaMemcpyToSymbolAsync(g_attn_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  *value = v;
-  return (int)e;
 }
 
 }  // namespace

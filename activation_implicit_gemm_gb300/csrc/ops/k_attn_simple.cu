@@ -437,19 +437,13 @@ size_t tile_bytes(const Geom& g, int BT, int tiles, int squares) {
   return sizeof(float) * ((size_t)tiles * BT * (g.Dp + 4) + (size_t)squares * BT * (BT + 4));
 }
 
-template <typename K>
-int allow_smem(K kernel, size_t bytes) {
-  return (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   (int)bytes);
-}
-
 template <typename T, int BT, int NE>
 int forward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
   const long long blocks = g.B * g.Hq * ((g.Lq + BT - 1) / BT);
   if (!grid_ok(blocks)) return (int)cudaErrorInvalidValue;
   const size_t smem = tile_bytes(g, BT, 3, 1);
   auto kern = attn_simple_forward<T, BT, NE>;
-  const int e = allow_smem(kern, smem);
+  const int e = allow_smem((const void*)kern, smem);
   if (e) return e;
   kern<<<(unsigned)blocks, 256, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v, (T*)a.o,
                                            a.lse, g);
@@ -465,7 +459,7 @@ int backward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
   if (rows > 0) {
     const size_t smem = tile_bytes(g, BT, 4, 1);
     auto kern = attn_simple_dq<T, BT, NE>;
-    const int e = allow_smem(kern, smem);
+    const int e = allow_smem((const void*)kern, smem);
     if (e) return e;
     if (!grid_ok((rows + 7) / 8) || !grid_ok(bq)) return (int)cudaErrorInvalidValue;
     attn_simple_delta<T><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>((const T*)a.out,
@@ -476,7 +470,7 @@ int backward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
   if (bk > 0) {
     const size_t smem = tile_bytes(g, BT, 4, 2);
     auto kern = attn_simple_dkv<T, BT, NE>;
-    const int e = allow_smem(kern, smem);
+    const int e = allow_smem((const void*)kern, smem);
     if (e) return e;
     if (!grid_ok(bk)) return (int)cudaErrorInvalidValue;
     kern<<<(unsigned)bk, 256, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v,

@@ -183,7 +183,7 @@ __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t
 // A block's dynamic shared memory must start on the swizzle atom's 1024 bytes.
 __device__ __forceinline__ bool smem_ok(const uint8_t* p) {
   if ((ptx::smem_addr(p) & 1023u) == 0) return true;
-  if (threadIdx.x == 0) atomicOr(&g_attn_error, 2u);
+  if (threadIdx.x == 0) atomicOr(&g_wait_error, 2u);
   return false;
 }
 
@@ -1069,8 +1069,7 @@ BwdPlan bwd_plan(const fconv_attn_desc& d, int sms, const AttnArgs& a) {
 template <typename K>
 int start(K kern, uint32_t smem, int items, int sms, const BwdArgs& b, const CUtensorMap* m,
           cudaStream_t s) {
-  const int e = (int)cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          (int)smem);
+  const int e = allow_smem((const void*)kern, smem);
   if (e) return e;
   return launch_pdl(kern, dim3(items < sms ? items : sms), dim3(kThreads), smem, s, b, m[0], m[1],
                     m[2], m[3]);

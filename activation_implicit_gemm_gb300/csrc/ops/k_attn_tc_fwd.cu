@@ -505,8 +505,7 @@ FwdArgs fwd_args(const fconv_attn_desc& d, int sms, const AttnArgs& a) {
 template <bool BF16, int H>
 int launch_t(const FwdArgs& f, int sms, const CUtensorMap* m, cudaStream_t s) {
   auto kern = attn_tc_forward<BF16, H>;
-  const int e = (int)cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          (int)FwdPlan<H>::smem);
+  const int e = allow_smem((const void*)kern, FwdPlan<H>::smem);
   if (e) return e;
   const int grid = f.items < sms ? f.items : sms;
   return launch_pdl(kern, dim3(grid), dim3(kThreads), FwdPlan<H>::smem, s, f, m[0], m[1], m[2]);

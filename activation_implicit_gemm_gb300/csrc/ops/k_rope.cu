@@ -1,31 +1,34 @@
-// Rotary positions with one to three axes (include/fconv_ops.h), simple form: one thread per
-// (token, pair) turns that pair in every head.
+// Rotary positions with one to three axes (include/fconv_ops.h).
 //
-// The angle is position * inv_freq. Its f32 product p alone is off by up to p * 2^-24 radians,
-// 0.004 at 65536; the exact remainder of the product (one FMA) is kept and added after p has
-// been reduced by whole turns with 2 pi in two parts (Cody and Waite, "Software Manual for the
-// Elementary Functions", 1980), so sine and cosine see an angle within about pi that is right
-// to 2^-22 or so at every position up to 2^23.
+//   angle = position[axis(p)] * inv_freq[p],  (u, v) -> (u cos - v sin, v cos + u sin)
+// A thread owns VEC neighbouring pairs of one token, makes their sines and cosines once and
+// turns them in every head of q and k (or of its share of the heads when there are few tokens),
+// several heads in flight at a time. Bound: HBM, q and k in and out; 36864 tokens of 40 heads of
+// 128 in bf16 move 1.51 GB.
+//
+// The angle in turns is position * inv_freq / (2 pi). The f32 product alone would be off by up
+// to 2^-24 of its size (0.004 radians at an angle of 65536), so the products are kept with
+// their exact remainders (one FMA each) until the whole turns are gone; what is left, within
+// half a turn, is right to about 2^-24 turns at every position up to 2^23.
 #include "ops_common.cuh"
 #include "ops_internal.h"
+
+#include "../fconv_internal.h"
+#include "../ptx.cuh"
 
 namespace fconv {
 namespace ops {
 namespace {
 
-// p - k * kHi is exact: kHi is a multiple of 2^-21, so both terms are multiples of
-// min(2^-21, ulp(p)) and the difference, at most 4, fits 24 bits. What kHi + kMid lack of
-// 2 pi (1e-14) stays below 2e-8 for every k up to 2^21.
+constexpr int kHeads = 4;
+
 __device__ __forceinline__ void turn_of(float pos, float freq, float& sn, float& cs) {
-  constexpr double kTwoPi = 6.283185307179586476925286766559;
-  constexpr float kHi = (float)kTwoPi;
-  constexpr float kMid = (float)(kTwoPi - (double)kHi);
-  constexpr float kInv = (float)(1.0 / kTwoPi);
-  const float p = pos * freq;
-  const float e = fmaf(pos, freq, -p);  // p + e is the exact product
-  const float k = rintf(p * kInv);
-  const float r = fmaf(-k, kHi, p);     // exact: |r| is small against p
-  sincosf(fmaf(-k, kMid, r) + e, &sn, &cs);
+  constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
+  constexpr float kHi = (float)kTurn, kLo = (float)(kTurn - (double)kHi);
+  const float p = pos * freq, e = fmaf(pos, freq, -p);  // p + e is the exact product
+  const float t = p * kHi, f = fmaf(p, kHi, -t);        // t + f is p kHi exactly
+  const float rest = fmaf(p, kLo, fmaf(e, kHi, f));
+  sincospif(2.0f * ((t - rintf(t)) + rest), &sn, &cs);
 }
 
 __device__ __forceinline__ float position(const void* pos, int type, int64_t at) {
@@ -35,75 +38,155 @@ __device__ __forceinline__ float position(const void* pos, int type, int64_t at)
 }
 
 struct RopeGeom {
+  const void* q;
+  const void* k;
+  const void* pos;
+  const float* inv_freq;
+  void* q_out;
+  void* k_out;
   int64_t len, pos_batch, tokens;
-  int heads_q, heads_k, head_dim, pairs, axes, sec0, sec1, pairing, pos_type, inverse;
+  int heads_q, heads, per;  // heads: of q and k together; per: heads of a block row
+  int pairs, chunks, axes, sec0, sec1, pairing, pos_type, inverse;
   int64_t q_stride[3], k_stride[3], q_out_stride[3], k_out_stride[3];
 };
 
-template <typename T>
-__device__ __forceinline__ void turn_head(const T* x, T* y, int lo, int hi, float cs, float sn) {
-  const float u = to_f(x[lo]), v = to_f(x[hi]);
-  y[lo] = from_f<T>(u * cs - v * sn);
-  y[hi] = from_f<T>(v * cs + u * sn);
-}
-
-// Elements [0, pairs) of the walk are pairs; [pairs, head_dim - pairs) copy element
-// pairs + index (the tail past the last pair).
-template <typename T>
-__global__ void __launch_bounds__(256)
-    rope_simple(const T* q, const T* k, const void* pos, const float* __restrict__ inv_freq, T* qo,
-                T* ko, const RopeGeom g) {
-  const int work = g.head_dim - g.pairs;
+// VEC: pairs a thread, one access of VEC elements each for the first and the second members
+// with HEADS heads in flight; interleaved pairs are one access of 2 VEC elements (IL). Chunks
+// past the last pair copy the elements that no pair covers.
+template <typename T, int VEC, bool IL, int HEADS>
+__global__ void __launch_bounds__(256) rope_kernel(const RopeGeom g) {
+  constexpr int N = IL ? 2 * VEC : VEC;  // elements of an access
+  using V = Vec<T, N>;
+  ptx::pdl_wait();
+  ptx::pdl_trigger();
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t token = at / work;
-  const int p = (int)(at - token * work);
+  const int64_t token = at / g.chunks;
+  const int chunk = (int)(at - token * g.chunks);
   if (token >= g.tokens) return;
   const int64_t b = token / g.len, t = token - b * g.len;
-  const T* qp = q + b * g.q_stride[0] + t * g.q_stride[1];
-  T* qw = qo + b * g.q_out_stride[0] + t * g.q_out_stride[1];
-  const T* kp = k + b * g.k_stride[0] + t * g.k_stride[1];
-  T* kw = ko + b * g.k_out_stride[0] + t * g.k_out_stride[1];
-  if (p >= g.pairs) {
-    const int d = g.pairs + p;
-    for (int h = 0; h < g.heads_q; ++h) qw[h * g.q_out_stride[2] + d] = qp[h * g.q_stride[2] + d];
-    for (int h = 0; h < g.heads_k; ++h) kw[h * g.k_out_stride[2] + d] = kp[h * g.k_stride[2] + d];
-    return;
+  const int p0 = chunk * VEC;
+  const bool copy = p0 >= g.pairs;
+  float cs[VEC], sn[VEC];
+  int lo = 2 * g.pairs + (chunk - g.pairs / VEC) * N, hi = lo;
+  if (!copy) {
+    const int64_t pt = ((g.pos_batch == 1 ? 0 : b) * g.len + t) * g.axes;
+    float pos[3];
+#pragma unroll
+    for (int a = 0; a < 3; ++a) pos[a] = a < g.axes ? position(g.pos, g.pos_type, pt + a) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      const int p = p0 + i;
+      const float x = p < g.sec0 ? pos[0] : p < g.sec0 + g.sec1 ? pos[1] : pos[2];
+      turn_of(x, g.inv_freq[p], sn[i], cs[i]);
+      if (g.inverse) sn[i] = -sn[i];
+    }
+    if (IL) {
+      lo = 2 * p0;
+    } else if (g.pairing == FCONV_ROPE_INTERLEAVED) {
+      lo = 2 * p0;  // VEC is 1
+      hi = lo + 1;
+    } else if (g.pairing == FCONV_ROPE_HALF) {
+      lo = p0;
+      hi = p0 + g.pairs;
+    } else {
+      const int s1 = g.sec0 + g.sec1;
+      const int start = p0 < g.sec0 ? 0 : p0 < s1 ? g.sec0 : s1;
+      const int size = p0 < g.sec0 ? g.sec0 : p0 < s1 ? g.sec1 : g.pairs - s1;
+      lo = start + p0;
+      hi = lo + size;
+    }
   }
-  const int axis = p < g.sec0 ? 0 : p < g.sec0 + g.sec1 ? 1 : 2;
-  const int64_t pb = g.pos_batch == 1 ? 0 : b;
-  float sn, cs;
-  turn_of(position(pos, g.pos_type, (pb * g.len + t) * g.axes + axis), inv_freq[p], sn, cs);
-  if (g.inverse) sn = -sn;
-  int lo, hi;
-  if (g.pairing == FCONV_ROPE_INTERLEAVED) {
-    lo = 2 * p;
-    hi = lo + 1;
-  } else if (g.pairing == FCONV_ROPE_HALF) {
-    lo = p;
-    hi = p + g.pairs;
-  } else {
-    const int start = axis == 0 ? 0 : axis == 1 ? g.sec0 : g.sec0 + g.sec1;
-    const int size = axis == 0 ? g.sec0 : axis == 1 ? g.sec1 : g.pairs - g.sec0 - g.sec1;
-    lo = start + p;
-    hi = lo + size;
+  const T* qp = (const T*)g.q + b * g.q_stride[0] + t * g.q_stride[1];
+  const T* kp = (const T*)g.k + b * g.k_stride[0] + t * g.k_stride[1];
+  T* qw = (T*)g.q_out + b * g.q_out_stride[0] + t * g.q_out_stride[1];
+  T* kw = (T*)g.k_out + b * g.k_out_stride[0] + t * g.k_out_stride[1];
+  const int h0 = blockIdx.y * g.per, h1 = min(h0 + g.per, g.heads);
+  for (int h = h0; h < h1; h += HEADS) {
+    V x[HEADS], y[IL ? 1 : HEADS];
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i) {
+      const int n = h + i;
+      if (n >= h1) break;
+      const T* p = n < g.heads_q ? qp + n * g.q_stride[2] : kp + (n - g.heads_q) * g.k_stride[2];
+      x[i] = *reinterpret_cast<const V*>(p + lo);
+      if (!IL && !copy) y[i] = *reinterpret_cast<const V*>(p + hi);
+    }
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i) {
+      const int n = h + i;
+      if (n >= h1) break;
+      T* p = n < g.heads_q ? qw + n * g.q_out_stride[2]
+                           : kw + (n - g.heads_q) * g.k_out_stride[2];
+      if (!copy) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          T& u = IL ? x[i].v[2 * e] : x[i].v[e];
+          T& v = IL ? x[i].v[2 * e + 1] : y[IL ? 0 : i].v[e];
+          const float a = to_f(u), c = to_f(v);
+          u = from_f<T>(a * cs[e] - c * sn[e]);
+          v = from_f<T>(c * cs[e] + a * sn[e]);
+        }
+        if (!IL) *reinterpret_cast<V*>(p + hi) = y[IL ? 0 : i];
+      }
+      *reinterpret_cast<V*>(p + lo) = x[i];
+    }
   }
-  for (int h = 0; h < g.heads_q; ++h)
-    turn_head(qp + h * g.q_stride[2], qw + h * g.q_out_stride[2], lo, hi, cs, sn);
-  for (int h = 0; h < g.heads_k; ++h)
-    turn_head(kp + h * g.k_stride[2], kw + h * g.k_out_stride[2], lo, hi, cs, sn);
+}
+
+// Elements of an access: as many as every pair's members allow. Sections (or all pairs) and the
+// tail are whole chunks, and every row and tensor starts at a multiple of it.
+int width(const fconv_rope_desc& d, const RopeArgs& a, int pairs) {
+  const int size = d.dtype == FCONV_F32 ? 4 : 2;
+  int64_t units = d.head_dim - 2 * pairs;
+  units |= d.pairing == FCONV_ROPE_INTERLEAVED ? 2 * pairs : pairs;
+  if (d.pairing == FCONV_ROPE_HALF_PER_AXIS)
+    for (int i = 0; i < d.axes; ++i) units |= d.section[i];
+  const int64_t ext[3] = {d.batch, d.len, d.heads_q};
+  for (int i = 0; i < 3; ++i) {
+    if (ext[i] > 1) units |= d.q_stride[i] | d.q_out_stride[i];
+    if (d.heads_k && (i < 2 ? ext[i] : d.heads_k) > 1) units |= d.k_stride[i] | d.k_out_stride[i];
+  }
+  const uintptr_t addr = (uintptr_t)a.q | (uintptr_t)a.k | (uintptr_t)a.q_out | (uintptr_t)a.k_out;
+  int n = 16 / size;
+  while (n > 1 && (units % n != 0 || addr % (n * size) != 0)) n /= 2;
+  return n;
+}
+
+// Interleaved pairs that no access holds whole (odd strides) take two accesses of one element.
+template <typename T, int N>
+int start(const RopeGeom& g, dim3 grid, cudaStream_t s) {
+  if constexpr (N > 1) {
+    if (g.pairing == FCONV_ROPE_INTERLEAVED)
+      return launch_pdl(rope_kernel<T, N / 2, true, 2 * kHeads>, grid, dim3(256), 0, s, g);
+  }
+  return launch_pdl(rope_kernel<T, N, false, kHeads>, grid, dim3(256), 0, s, g);
+}
+
+template <typename T>
+int start_t(const RopeGeom& g, int n, dim3 grid, cudaStream_t s) {
+  if constexpr (sizeof(T) == 2) {
+    if (n == 8) return start<T, 8>(g, grid, s);
+  }
+  if (n == 4) return start<T, 4>(g, grid, s);
+  if (n == 2) return start<T, 2>(g, grid, s);
+  return start<T, 1>(g, grid, s);
 }
 
 }  // namespace
 
 int launch_rope(const fconv_rope_desc& d, int sms, const RopeArgs& a, cudaStream_t s) {
-  (void)sms;
   RopeGeom g{};
+  g.q = a.q;
+  g.k = a.k;
+  g.pos = a.pos;
+  g.inv_freq = a.inv_freq;
+  g.q_out = a.q_out;
+  g.k_out = a.k_out;
   g.len = d.len;
   g.pos_batch = d.pos_batch;
   g.tokens = d.batch * d.len;
   g.heads_q = (int)d.heads_q;
-  g.heads_k = (int)d.heads_k;
-  g.head_dim = (int)d.head_dim;
+  g.heads = (int)(d.heads_q + d.heads_k);
   g.axes = d.axes;
   for (int i = 0; i < d.axes; ++i) g.pairs += (int)d.section[i];
   g.sec0 = (int)d.section[0];
@@ -117,15 +200,22 @@ int launch_rope(const fconv_rope_desc& d, int sms, const RopeArgs& a, cudaStream
     g.q_out_stride[i] = d.q_out_stride[i];
     g.k_out_stride[i] = d.k_out_stride[i];
   }
-  const long long blocks = (long long)((g.tokens * (g.head_dim - g.pairs) + 255) / 256);
-  if (blocks == 0) return 0;
+  const int n = width(d, a, g.pairs);
+  const bool whole = d.pairing == FCONV_ROPE_INTERLEAVED && n > 1;  // an access holds both members
+  const int in_flight = whole ? 2 * kHeads : kHeads;
+  g.chunks = (whole ? (int)d.head_dim : (int)d.head_dim - g.pairs) / n;
+  const long long blocks = (g.tokens * g.chunks + 255) / 256;
   if (!grid_ok(blocks)) return (int)cudaErrorInvalidValue;
-#define FCONV_M(T)                                                                          \
-  rope_simple<T><<<(unsigned)blocks, 256, 0, s>>>((const T*)a.q, (const T*)a.k, a.pos,      \
-                                                  a.inv_freq, (T*)a.q_out, (T*)a.k_out, g)
+  // few tokens: the heads are shared out too, down to one group in flight a block, until there
+  // are about four blocks an SM
+  const int groups = (g.heads + in_flight - 1) / in_flight;
+  const long long want = (4LL * sms + blocks - 1) / blocks;
+  const int rows = (int)(want < groups ? want : groups);
+  g.per = (groups + rows - 1) / rows * in_flight;
+  const dim3 grid((unsigned)blocks, (unsigned)((g.heads + g.per - 1) / g.per));
+#define FCONV_M(T) return start_t<T>(g, n, grid, s)
   FCONV_OPS_TYPE(d.dtype, FCONV_M)
 #undef FCONV_M
-  return (int)cudaGetLastError();
 }
 
 }  // namespace ops

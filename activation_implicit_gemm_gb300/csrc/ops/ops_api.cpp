@@ -5,6 +5,7 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <mutex>
 #include <new>
 #include <utility>
 
@@ -72,7 +73,11 @@ bool same_strides(const int64_t a[3], const int64_t b[3]) {
   return a[0] == b[0] && a[1] == b[1] && a[2] == b[2];
 }
 
-fconv_status done(int err) { return err == 0 ? FCONV_OK : FCONV_E_CUDA; }
+fconv_status done(int err) {
+  if (err == 0) return FCONV_OK;
+  cudaGetLastError();  // reported here, not by the caller's next check
+  return FCONV_E_CUDA;
+}
 
 fconv_status check_norm(const fconv_norm_desc& d) {
   if (!known_type(d.dtype) || !known_type(d.param_dtype) ||
@@ -168,6 +173,41 @@ fconv_status attn_inputs(const fconv_attn_desc& d, const void* q, const void* k,
 
 }  // namespace
 
+namespace fconv {
+namespace ops {
+
+int allow_smem(const void* kernel, size_t bytes) {
+  if (bytes <= 24 * 1024) return 0;  // with static shared memory within the default 48 KB
+  struct Seen {
+    const void* kernel;
+    int device;
+    size_t bytes;
+  };
+  static std::mutex mu;
+  static Seen seen[256];
+  static int count = 0;
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return (int)e;
+  std::lock_guard<std::mutex> lock(mu);
+  Seen* at = nullptr;
+  for (int i = 0; i < count && !at; ++i)
+    if (seen[i].kernel == kernel && seen[i].device == device) at = &seen[i];
+  if (at && at->bytes >= bytes) return 0;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess) return (int)e;
+  if (!at && count < 256) {
+    at = &seen[count++];
+    at->kernel = kernel;
+    at->device = device;
+  }
+  if (at) at->bytes = bytes;
+  return 0;
+}
+
+}  // namespace ops
+}  // namespace fconv
+
 extern "C" {
 
 const char* fconv_ops_status_string(int s) {
@@ -183,11 +223,12 @@ const char* fconv_ops_status_string(int s) {
 }
 
 fconv_status fconv_ops_check_device(void* stream) {
-  unsigned f = 0, b = 0;
-  if (read_and_clear_attn_forward_error((cudaStream_t)stream, &f) != 0 ||
+  unsigned n = 0, f = 0, b = 0;
+  if (read_and_clear_norm_error((cudaStream_t)stream, &n) != 0 ||
+      read_and_clear_attn_forward_error((cudaStream_t)stream, &f) != 0 ||
       read_and_clear_attn_backward_error((cudaStream_t)stream, &b) != 0)
     return FCONV_E_CUDA;
-  return f || b ? FCONV_E_DEVICE_TIMEOUT : FCONV_OK;
+  return n || f || b ? FCONV_E_DEVICE_TIMEOUT : FCONV_OK;
 }
 
 // ---------------------------------------------------------------------------- layer norm

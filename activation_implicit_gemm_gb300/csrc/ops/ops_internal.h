@@ -29,6 +29,7 @@ struct NormArgs {
 int launch_norm_forward(const fconv_norm_desc& d, int sms, const NormArgs& a, cudaStream_t s);
 int launch_norm_backward(const fconv_norm_desc& d, int sms, const NormArgs& a, cudaStream_t s);
 size_t norm_workspace(const fconv_norm_desc& d, int sms);
+int read_and_clear_norm_error(cudaStream_t s, unsigned* value);
 
 struct RopeArgs {
   const void* q;
@@ -68,6 +69,10 @@ bool attn_tc_backward_supported(const fconv_attn_desc& d);
 size_t attn_tc_backward_workspace(const fconv_attn_desc& d, int sms);
 int launch_attn_tc_backward(const fconv_attn_desc& d, int sms, const AttnArgs& a, cudaStream_t s);
 int read_and_clear_attn_backward_error(cudaStream_t s, unsigned* value);
+
+// Lets a kernel use more shared memory than the default 48 KB; asks the runtime once for each
+// (kernel, device, larger size).
+int allow_smem(const void* kernel, size_t bytes);
 
 // Whether a launch's block count fits the grid's first axis.
 inline bool grid_ok(long long blocks) { return blocks > 0 && blocks <= 0x7fffffffLL; }
