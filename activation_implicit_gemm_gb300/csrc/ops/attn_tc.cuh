@@ -25,13 +25,18 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 // ------------------------------------------------------------------------- instructions
 
-// K-major operand in the 128-byte swizzle (64 elements a row): ptx::desc_sw128.
-// MN-major operand in the same tiles, its rows now running along K: 64 elements along M or N
-// are 128 contiguous bytes, 8 rows (K) an atom of 1024 bytes (stride offset), and the next 64
-// elements along M or N lie one box further (leading offset).
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kHalfBytes >> 4) << 16) |
-         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// Shared-memory descriptors in the 128-byte swizzle, 8-row atoms of 1024 bytes. The upper word
+// is the same for all (stride offset 1024 >> 4, version 1, layout 2), so only the lower one is
+// kept and advanced: the issuing thread has few registers, and 64-bit descriptors kept for
+// every step of an unrolled product made it spill. K-major (64 elements of a row along K): the
+// leading offset is unused. MN-major (rows run along K, 64 elements along M or N contiguous):
+// it leads to the next 64 elements along M or N, one box further.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t saddr) {
+  return ((saddr & 0x3FFFFu) >> 4) | (1u << 16);
+}
+__device__ __forceinline__ uint32_t desc_mn(uint32_t saddr) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((kHalfBytes >> 4) << 16);
 }
 
 // Instruction descriptor of kind::f16: f32 accumulator, A and B both f16 (0) or both bf16 (1),
@@ -41,15 +46,32 @@ __host__ __device__ constexpr uint32_t idesc_16(bool bf16, int M, int N, bool bm
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// D[tmem] (+)= A[smem] * B[smem]^T, lower descriptor words; issued by one thread.
+__device__ __forceinline__ void mma_ss(uint32_t tmem_d, uint32_t a, uint32_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+      : "memory");
+}
 // D[tmem] (+)= A[tmem] * B[smem]: A's rows are TMEM lanes, two 16-bit elements a column.
-__device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+__device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint32_t b,
                                        uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
       : "memory");
+}
+// Byte offset of K step s (16 elements) in a K-major tile of 64-element boxes, in descriptor
+// units of 16 bytes.
+__host__ __device__ constexpr uint32_t k_step(int s) {
+  return (uint32_t)(s >> 2) * (kHalfBytes >> 4) + (uint32_t)(s & 3) * 2;
 }
 
 // 4-D tiled TMA load (c0 innermost).
@@ -80,21 +102,29 @@ __device__ __forceinline__ void tmem_fetch32(uint32_t taddr, uint32_t (&r)[32]) 
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_fetch8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : FCONV_R8(r, 0)
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[8]) {
+  asm volatile("" : FCONV_P8(r, 0)::"memory");
+}
+__device__ __forceinline__ void tmem_store8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::FCONV_I8(
+          r, 0),
+      "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 // Ties the registers to the wait that precedes: no use of them moves above it.
 __device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32]) {
   asm volatile("" : FCONV_P8(r, 0), FCONV_P8(r, 8), FCONV_P8(r, 16), FCONV_P8(r, 24)::"memory");
-}
-__device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::FCONV_I8(
-          r, 0),
-      FCONV_I8(r, 8), FCONV_I8(r, 16), FCONV_I8(r, 24), "r"(taddr)
-      : "memory");
 }
 __device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(

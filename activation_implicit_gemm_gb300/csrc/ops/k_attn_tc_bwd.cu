@@ -191,22 +191,20 @@ __device__ __forceinline__ bool smem_ok(const uint8_t* p) {
 template <int H>
 __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, int dk,
                                            uint32_t idesc) {
+  const uint32_t x = desc_k(a), y = desc_k(b);
 #pragma unroll
   for (int s = 0; s < 4 * H; ++s)
-    if (s < dk) {
-      const uint32_t o = (s >> 2) * kHalfBytes + (s & 3) * 32;
-      ptx::mma_f16(d, ptx::desc_sw128(a + o), ptx::desc_sw128(b + o), idesc, s > 0);
-    }
+    if (s < dk) mma_ss(d, x + k_step(s), y + k_step(s), idesc, s > 0);
 }
 
 // D[128 x head_dim] (+)= A B over the 128 columns of a score tile: A in TMEM, its two column
 // halves 64 columns apart, B a tile read MN-major.
 __device__ __forceinline__ void mma_grads(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                           bool first) {
+  const uint32_t y = desc_mn(b);
 #pragma unroll
   for (int s = 0; s < kTile / 16; ++s)
-    mma_ts(d, a + (s >> 2) * 64 + (s & 3) * 8, desc_mn_sw128(b + s * 2048), idesc,
-           !first || s > 0);
+    mma_ts(d, a + (s >> 2) * 64 + (s & 3) * 8, y + s * (2048 >> 4), idesc, !first || s > 0);
 }
 
 // One thread's row of an accumulator, columns [c0, c0 + 32 H), times mul: to a 16-bit row or

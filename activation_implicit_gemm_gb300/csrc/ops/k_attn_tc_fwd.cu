@@ -218,14 +218,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       FwdItem it;
       bool stop = false;
       auto scores = [&](int t, uint32_t ktile) {
-        const uint32_t q = qbase + t * Plan::tile_bytes;
+        const uint32_t q = desc_k(qbase + t * Plan::tile_bytes), kt = desc_k(ktile);
 #pragma unroll
         for (int d = 0; d < 4 * H; ++d)
-          if (d < dk) {
-            const uint32_t o = (d >> 2) * kHalfBytes + (d & 3) * 32;
-            ptx::mma_f16(tmem + t * 128, ptx::desc_sw128(q + o), ptx::desc_sw128(ktile + o), id_s,
-                         d > 0);
-          }
+          if (d < dk) mma_ss(tmem + t * 128, q + k_step(d), kt + k_step(d), id_s, d > 0);
         ptx::mma_commit(ptx::smem_addr(&ctl.s_full[t]));
       };
       for (int k = 0; !stop && fwd_item(a, k, it); ++k) {
@@ -250,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             stop = true;
             break;
           }
-          const uint32_t v = ring + vs * Plan::tile_bytes;
+          const uint32_t v = desc_mn(ring + vs * Plan::tile_bytes);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (j >= it.n[t]) continue;
@@ -262,8 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tc_fence_after();
 #pragma unroll
             for (int s = 0; s < kTile / 16; ++s)
-              mma_ts(tmem + 256 + t * 128, tmem + t * 128 + s * 8, desc_mn_sw128(v + s * 2048),
-                     id_o, j > 0 || s > 0);
+              mma_ts(tmem + 256 + t * 128, tmem + t * 128 + s * 8, v + s * (2048 >> 4), id_o,
+                     j > 0 || s > 0);
             if (j == it.n[t] - 1) ptx::mma_commit(ptx::smem_addr(&ctl.o_done[t]));
             if (j + 1 < it.n[t]) scores(t, ring + ks * Plan::tile_bytes);
           }
@@ -327,14 +323,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           l *= f;
           m = mn;
           if (j > 0)
-            for (int q = 0; q < (g.D + 31) / 32; ++q) {
-              uint32_t o[32];
-              tmem_fetch32(o_at + q * 32, o);
+#pragma unroll 1
+            for (int q = 0; q < (g.D + 7) / 8; ++q) {
+              uint32_t o[8];
+              tmem_fetch8(o_at + q * 8, o);
               tmem_wait_ld();
               tmem_arrived(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_store32(o_at + q * 32, o);
+              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_store8(o_at + q * 8, o);
             }
         }
         const float ref = m == -INFINITY ? 0.0f : m;

@@ -2,9 +2,8 @@
 //
 //   angle = position[axis(p)] * inv_freq[p],  (u, v) -> (u cos - v sin, v cos + u sin)
 // A thread owns VEC neighbouring pairs of one token, makes their sines and cosines once and
-// turns them in every head of q and k (or of its share of the heads when there are few tokens),
-// several heads in flight at a time. Bound: HBM, q and k in and out; 36864 tokens of 40 heads of
-// 128 in bf16 move 1.51 GB.
+// turns them in every head of q and k (or of its share of the heads when there are few tokens).
+// Bound: HBM, q and k in and out; 36864 tokens of 40 heads of 128 in bf16 move 1.51 GB.
 //
 // The angle in turns is position * inv_freq / (2 pi). The f32 product alone would be off by up
 // to 2^-24 of its size (0.004 radians at an angle of 65536), so the products are kept with
@@ -19,8 +18,6 @@
 namespace fconv {
 namespace ops {
 namespace {
-
-constexpr int kHeads = 4;
 
 __device__ __forceinline__ void turn_of(float pos, float freq, float& sn, float& cs) {
   constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
@@ -51,10 +48,12 @@ struct RopeGeom {
 };
 
 // VEC: pairs a thread, one access of VEC elements each for the first and the second members
-// with HEADS heads in flight; interleaved pairs are one access of 2 VEC elements (IL). Chunks
-// past the last pair copy the elements that no pair covers.
-template <typename T, int VEC, bool IL, int HEADS>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeGeom g) {
+// of a head; interleaved pairs are one access of 2 VEC elements (IL). Chunks past the last pair
+// copy the elements that no pair covers. One head at a time and as many threads as registers
+// allow (64 a thread with two accesses, 32 with one) beat more heads in flight in fewer threads:
+// at the size above 244 and 253 us (6.2 and 6.0 TB/s) against 340 and 382 us with two.
+template <typename T, int VEC, bool IL>
+__global__ void __launch_bounds__(256, IL ? 8 : 4) rope_kernel(const RopeGeom g) {
   constexpr int N = IL ? 2 * VEC : VEC;  // elements of an access
   using V = Vec<T, N>;
   ptx::pdl_wait();
@@ -101,35 +100,24 @@ __global__ void __launch_bounds__(256) rope_kernel(const RopeGeom g) {
   T* qw = (T*)g.q_out + b * g.q_out_stride[0] + t * g.q_out_stride[1];
   T* kw = (T*)g.k_out + b * g.k_out_stride[0] + t * g.k_out_stride[1];
   const int h0 = blockIdx.y * g.per, h1 = min(h0 + g.per, g.heads);
-  for (int h = h0; h < h1; h += HEADS) {
-    V x[HEADS], y[IL ? 1 : HEADS];
+  for (int h = h0; h < h1; ++h) {
+    const bool is_q = h < g.heads_q;
+    const T* p = is_q ? qp + h * g.q_stride[2] : kp + (h - g.heads_q) * g.k_stride[2];
+    T* w = is_q ? qw + h * g.q_out_stride[2] : kw + (h - g.heads_q) * g.k_out_stride[2];
+    V x = *reinterpret_cast<const V*>(p + lo), y;
+    if (!copy) {
+      if (!IL) y = *reinterpret_cast<const V*>(p + hi);
 #pragma unroll
-    for (int i = 0; i < HEADS; ++i) {
-      const int n = h + i;
-      if (n >= h1) break;
-      const T* p = n < g.heads_q ? qp + n * g.q_stride[2] : kp + (n - g.heads_q) * g.k_stride[2];
-      x[i] = *reinterpret_cast<const V*>(p + lo);
-      if (!IL && !copy) y[i] = *reinterpret_cast<const V*>(p + hi);
-    }
-#pragma unroll
-    for (int i = 0; i < HEADS; ++i) {
-      const int n = h + i;
-      if (n >= h1) break;
-      T* p = n < g.heads_q ? qw + n * g.q_out_stride[2]
-                           : kw + (n - g.heads_q) * g.k_out_stride[2];
-      if (!copy) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          T& u = IL ? x[i].v[2 * e] : x[i].v[e];
-          T& v = IL ? x[i].v[2 * e + 1] : y[IL ? 0 : i].v[e];
-          const float a = to_f(u), c = to_f(v);
-          u = from_f<T>(a * cs[e] - c * sn[e]);
-          v = from_f<T>(c * cs[e] + a * sn[e]);
-        }
-        if (!IL) *reinterpret_cast<V*>(p + hi) = y[IL ? 0 : i];
+      for (int e = 0; e < VEC; ++e) {
+        T& u = IL ? x.v[2 * e] : x.v[e];
+        T& v = IL ? x.v[2 * e + 1] : y.v[e];
+        const float a = to_f(u), c = to_f(v);
+        u = from_f<T>(a * cs[e] - c * sn[e]);
+        v = from_f<T>(c * cs[e] + a * sn[e]);
       }
-      *reinterpret_cast<V*>(p + lo) = x[i];
+      if (!IL) *reinterpret_cast<V*>(w + hi) = y;
     }
+    *reinterpret_cast<V*>(w + lo) = x;
   }
 }
 
@@ -157,9 +145,9 @@ template <typename T, int N>
 int start(const RopeGeom& g, dim3 grid, cudaStream_t s) {
   if constexpr (N > 1) {
     if (g.pairing == FCONV_ROPE_INTERLEAVED)
-      return launch_pdl(rope_kernel<T, N / 2, true, 2 * kHeads>, grid, dim3(256), 0, s, g);
+      return launch_pdl(rope_kernel<T, N / 2, true>, grid, dim3(256), 0, s, g);
   }
-  return launch_pdl(rope_kernel<T, N, false, kHeads>, grid, dim3(256), 0, s, g);
+  return launch_pdl(rope_kernel<T, N, false>, grid, dim3(256), 0, s, g);
 }
 
 template <typename T>
@@ -202,16 +190,13 @@ int launch_rope(const fconv_rope_desc& d, int sms, const RopeArgs& a, cudaStream
   }
   const int n = width(d, a, g.pairs);
   const bool whole = d.pairing == FCONV_ROPE_INTERLEAVED && n > 1;  // an access holds both members
-  const int in_flight = whole ? 2 * kHeads : kHeads;
   g.chunks = (whole ? (int)d.head_dim : (int)d.head_dim - g.pairs) / n;
   const long long blocks = (g.tokens * g.chunks + 255) / 256;
   if (!grid_ok(blocks)) return (int)cudaErrorInvalidValue;
-  // few tokens: the heads are shared out too, down to one group in flight a block, until there
-  // are about four blocks an SM
-  const int groups = (g.heads + in_flight - 1) / in_flight;
+  // few tokens: the heads are shared out too, until there are about four blocks an SM
   const long long want = (4LL * sms + blocks - 1) / blocks;
-  const int rows = (int)(want < groups ? want : groups);
-  g.per = (groups + rows - 1) / rows * in_flight;
+  const int shares = (int)(want < g.heads ? want : g.heads);
+  g.per = (g.heads + shares - 1) / shares;
   const dim3 grid((unsigned)blocks, (unsigned)((g.heads + g.per - 1) / g.per));
 #define FCONV_M(T) return start_t<T>(g, n, grid, s)
   FCONV_OPS_TYPE(d.dtype, FCONV_M)
