@@ -3,7 +3,7 @@
 //   p = exp(scale q k^T - lse),  dp = dout v^T,  ds = p (dp - delta),  delta_i = dout_i . out_i
 //   dv = p^T dout,  dk = scale ds^T q,  dq = scale ds k
 //
-// Three launches. attn_tc_delta writes lse (in log2) and delta per packed query row.
+// Three launches. attn_tc_delta writes -lse (in log2) and -delta per packed query row.
 // attn_tc_dkv owns 128 keys of a (batch, key head) and walks the query tiles of all the heads
 // that share them; attn_tc_dq owns 128 packed query rows and walks the key tiles. Every
 // gradient element has one writer that adds in a fixed order: no atomics, the same bits every
@@ -49,7 +49,7 @@ struct BwdArgs {
   TcGeom g;
   int splits, per;   // splits of the walked axis, tiles of a split
   int items;
-  const float* stat;   // [b][hk][query tile]: 128 lse (log2), 128 delta
+  const float* stat;   // [b][hk][query tile]: 128 of -lse (log2, with p's scale), 128 of -delta
   const float* gmax;   // f16: [b][hk][query tile] largest |dout row|^2
   const float* vmax;   // f16: [b][hk][key tile] largest |v row|^2
   int64_t o1[3], o2[3];
@@ -119,14 +119,15 @@ __global__ void __launch_bounds__(256) attn_tc_delta(const DeltaArgs a) {
       }
       most = fmaxf(most, n);
       if (d == 0) {
-        // a row that sees nothing (or only scores of -inf) gets +inf: its p is 0
-        float lse = INFINITY;
+        // added to the scores; a row that sees nothing (or only scores of -inf) gets -inf: its p
+        // is 0
+        float x = -INFINITY;
         if (live) {
-          lse = a.lse[((int64_t)b * g.Hq + h) * g.Lq + i];
-          lse = lse == -INFINITY ? INFINITY : lse * kLog2e;
+          x = a.lse[((int64_t)b * g.Hq + h) * g.Lq + i];
+          if (x != -INFINITY) x = (BF16 ? 0.0f : (float)kPShift) - x * kLog2e;
         }
-        stat[r] = lse;
-        stat[kTile + r] = live ? s : 0.0f;
+        stat[r] = x;
+        stat[kTile + r] = live ? -s : 0.0f;
       }
     }
   } else {
@@ -198,13 +199,17 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, i
 }
 
 // D[128 x head_dim] (+)= A B over the 128 columns of a score tile: A in TMEM, its two column
-// halves 64 columns apart, B a tile read MN-major.
+// halves 64 columns apart, B a tile read MN-major. PART 0 and 1: the first and the last 32 of
+// each half's columns.
+template <int PART>
 __device__ __forceinline__ void mma_grads(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                           bool first) {
   const uint32_t y = desc_mn(b);
 #pragma unroll
-  for (int s = 0; s < kTile / 16; ++s)
-    mma_ts(d, a + (s >> 2) * 64 + (s & 3) * 8, y + s * (2048 >> 4), idesc, !first || s > 0);
+  for (int n = 0; n < 4; ++n) {
+    const int h = n >> 1, s = PART * 2 + (n & 1);  // half, K step of the half
+    mma_ts(d, a + h * 64 + s * 8, y + (h * 4 + s) * (2048 >> 4), idesc, !first || PART || n);
+  }
 }
 
 // One thread's row of an accumulator, columns [c0, c0 + 32 H), times mul: to a 16-bit row or
@@ -287,7 +292,8 @@ template <int H>
 struct DqCtl {
   uint64_t full[DqPlan<H>::slots], empty[DqPlan<H>::slots];
   uint64_t own_full[2], own_empty[2];
-  uint64_t tail, drain, s_full[2], dp_full, ds_ready, done;
+  uint64_t tail, drain, s_full[2], dp_full, dp_free, done;
+  uint64_t ds_ready[2][2];  // [step's parity][column part]: a warp may be a step ahead of another
   uint32_t tmem;
   int abort_flag;
 };
@@ -307,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!smem_ok(dsmem)) return;
   DqCtl<H>& ctl = *reinterpret_cast<DqCtl<H>*>(dsmem + (2 * Plan::own + Plan::slots) * Plan::tile);
   const TcGeom& g = a.g;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uni(tid >> 5), lane = tid & 31;
   const uint32_t own = ptx::smem_addr(dsmem), ring = own + 2 * Plan::own * Plan::tile;
   volatile int* abort_flag = &ctl.abort_flag;
 
@@ -324,7 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(ptx::smem_addr(&ctl.tail), 1);
     ptx::mbar_init(ptx::smem_addr(&ctl.drain), 1);
     ptx::mbar_init(ptx::smem_addr(&ctl.dp_full), 1);
-    ptx::mbar_init(ptx::smem_addr(&ctl.ds_ready), 8);
+    ptx::mbar_init(ptx::smem_addr(&ctl.dp_free), 8);
+    for (int i = 0; i < 4; ++i) ptx::mbar_init(ptx::smem_addr(&ctl.ds_ready[i >> 1][i & 1]), 8);
     ptx::mbar_init(ptx::smem_addr(&ctl.done), 1);
     ctl.abort_flag = 0;
     ptx::fence_mbar_init();
@@ -342,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = ctl.tmem;
+  const uint32_t tmem = uni(ctl.tmem);
   ptx::pdl_wait();
 
   if (warp >= 8) {
@@ -407,8 +414,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t i = items > Plan::own ? items - Plan::own : 0; i < items; ++i)
           drain_bar(ptx::smem_addr(&ctl.own_full[i % Plan::own]), (i / Plan::own) & 1);
       }
-    } else if (warp == kMmaWarp && lane == 0) {
+    } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------------- MMA issue
+      const bool leader = elect_lane();
       const int dk = (g.D + 15) / 16;
       const uint32_t id_s = idesc_16(BF16, kTile, kTile, false);
       const uint32_t id_g = idesc_16(BF16, kTile, dk * 16, true);
@@ -416,60 +424,72 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t c = 0, items = 0, steps = 0;
       DqItem it;
       bool stop = false;
+      auto wait = [&](uint64_t& bar, uint32_t parity) {
+        return all_lanes(wait_bar(ptx::smem_addr(&bar), parity, abort_flag));
+      };
+      auto commit = [&](uint64_t& bar) {
+        if (leader) ptx::mma_commit(ptx::smem_addr(&bar));
+      };
       auto wait_slot = [&](uint32_t i) {
-        return wait_bar(ptx::smem_addr(&ctl.full[i % Plan::slots]), (i / Plan::slots) & 1,
-                        abort_flag);
+        return wait(ctl.full[i % Plan::slots], (i / Plan::slots) & 1);
       };
       auto slot = [&](uint32_t i) { return ring + i % Plan::slots * Plan::tile; };
-      auto free_slot = [&](uint32_t i) {
-        ptx::mma_commit(ptx::smem_addr(&ctl.empty[i % Plan::slots]));
-      };
+      auto free_slot = [&](uint32_t i) { commit(ctl.empty[i % Plan::slots]); };
       for (int k = 0; !stop && dq_item(a, k, it); ++k) {
-        if (it.n == 0) continue;
+        const int n = uni(it.n);
+        if (n == 0) continue;
         const uint32_t ob = items % Plan::own;
-        if (!wait_bar(ptx::smem_addr(&ctl.own_full[ob]), (items / Plan::own) & 1, abort_flag) ||
-            !wait_slot(c) || !wait_slot(c + 1))
+        if (!wait(ctl.own_full[ob], (items / Plan::own) & 1) || !wait_slot(c) || !wait_slot(c + 1))
           break;
         ++items;
         const uint32_t q = own + ob * 2 * Plan::tile, go = q + Plan::tile;
         ptx::tc_fence_after();
-        mma_scores<H>(tmem + (steps & 1) * 128, q, slot(c), dk, id_s);
-        ptx::mma_commit(ptx::smem_addr(&ctl.s_full[steps & 1]));
-        mma_scores<H>(dp, go, slot(c + 1), dk, id_s);
-        ptx::mma_commit(ptx::smem_addr(&ctl.dp_full));
+        if (leader) mma_scores<H>(tmem + (steps & 1) * 128, q, slot(c), dk, id_s);
+        commit(ctl.s_full[steps & 1]);
+        if (leader) mma_scores<H>(dp, go, slot(c + 1), dk, id_s);
+        commit(ctl.dp_full);
         free_slot(c + 1);
-        for (int j = 0; j < it.n; ++j, c += 2, ++steps) {
-          const bool more = j + 1 < it.n;
+        for (int j = 0; j < n; ++j, c += 2, ++steps) {
+          const bool more = j + 1 < n;
           if (more) {
             if (!wait_slot(c + 2)) {
               stop = true;
               break;
             }
             ptx::tc_fence_after();
-            mma_scores<H>(tmem + ((steps + 1) & 1) * 128, q, slot(c + 2), dk, id_s);
-            ptx::mma_commit(ptx::smem_addr(&ctl.s_full[(steps + 1) & 1]));
+            if (leader) mma_scores<H>(tmem + ((steps + 1) & 1) * 128, q, slot(c + 2), dk, id_s);
+            commit(ctl.s_full[(steps + 1) & 1]);
+            if (!wait(ctl.dp_free, steps & 1) || !wait_slot(c + 3)) {
+              stop = true;
+              break;
+            }
+            ptx::tc_fence_after();
+            if (leader) mma_scores<H>(dp, go, slot(c + 3), dk, id_s);
+            commit(ctl.dp_full);
+            free_slot(c + 3);
           }
-          if (!wait_bar(ptx::smem_addr(&ctl.ds_ready), steps & 1, abort_flag) ||
-              (more && !wait_slot(c + 3))) {
+          const uint32_t ds = tmem + (steps & 1) * 128;
+          if (!wait(ctl.ds_ready[steps & 1][0], (steps >> 1) & 1)) {
             stop = true;
             break;
           }
           ptx::tc_fence_after();
-          if (more) {
-            mma_scores<H>(dp, go, slot(c + 3), dk, id_s);
-            ptx::mma_commit(ptx::smem_addr(&ctl.dp_full));
-            free_slot(c + 3);
+          if (leader) mma_grads<0>(dq, ds, slot(c), id_g, j == 0);
+          if (!wait(ctl.ds_ready[steps & 1][1], (steps >> 1) & 1)) {
+            stop = true;
+            break;
           }
-          mma_grads(dq, tmem + (steps & 1) * 128, slot(c), id_g, j == 0);
+          ptx::tc_fence_after();
+          if (leader) mma_grads<1>(dq, ds, slot(c), id_g, j == 0);
           free_slot(c);
           // Q and dO were read last by the products before this one
           if (!more) {
-            ptx::mma_commit(ptx::smem_addr(&ctl.own_empty[ob]));
-            ptx::mma_commit(ptx::smem_addr(&ctl.done));
+            commit(ctl.own_empty[ob]);
+            commit(ctl.done);
           }
         }
       }
-      ptx::mma_commit(ptx::smem_addr(&ctl.drain));
+      commit(ctl.drain);
       drain_bar(ptx::smem_addr(&ctl.drain), 0);
     }
   } else {
@@ -477,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_more<kWorkRegs>();
     const int half = warp >> 2, row = tid & 127, tok = row / g.G, head = row - tok * g.G;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const float c = g.scale * kLog2e;
+    const uint64_t c2 = pair(g.scale * kLog2e, g.scale * kLog2e);
     uint32_t steps = 0, items = 0;
     int shift = 0, last_bh = -1;
     DqItem it;
@@ -485,57 +505,75 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int i = it.t0 + tok, bh = it.b * g.Hk + it.hk;
       const int limit = row < g.rows ? key_limit(g, it.l, i) : 0;
       const float* stat = a.stat + ((int64_t)bh * g.qtiles + it.tile) * (2 * kTile);
-      const float lse = stat[row], delta = stat[kTile + row];
+      const uint64_t nlse = pair(stat[row], stat[row]);
       if (!BF16 && bh != last_bh) {
         shift = grad_shift(a, bh, lane);
         last_bh = bh;
       }
-      const float gs = BF16 ? 1.0f : pow2i(shift), gd = -delta * gs;
+      const float gs = BF16 ? 1.0f : pow2i(shift - kPShift), nd = stat[kTile + row] * gs;
+      const uint64_t gs2 = pair(gs, gs), nd2 = pair(nd, nd);
       bool stop = false;
       for (int j = 0; j < it.n; ++j, ++steps) {
         const uint32_t s_at = tmem + (steps & 1) * 128 + half * 64 + lanes;
         const uint32_t dp_at = tmem + 256 + half * 64 + lanes;
-        if (!wait_bar(ptx::smem_addr(&ctl.s_full[steps & 1]), (steps >> 1) & 1, abort_flag) ||
-            !wait_bar(ptx::smem_addr(&ctl.dp_full), steps & 1, abort_flag)) {
+        if (!wait_bar(ptx::smem_addr(&ctl.s_full[steps & 1]), (steps >> 1) & 1, abort_flag)) {
           stop = true;
           break;
         }
         ptx::tc_fence_after();
         uint32_t s[2][32], dp[2][32];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          tmem_fetch32(s_at + q * 32, s[q]);
-          tmem_fetch32(dp_at + q * 32, dp[q]);
-        }
+        for (int q = 0; q < 2; ++q) tmem_fetch32(s_at + q * 32, s[q]);
         tmem_wait_ld();
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           tmem_arrived(s[q]);
-          tmem_arrived(dp[q]);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const uint64_t x = fma2(pair(s[q][e], s[q][e + 1]), c2, nlse);
+            s[q][e] = __float_as_uint(exp2_fast(low(x)));
+            s[q][e + 1] = __float_as_uint(exp2_fast(high(x)));
+          }
         }
+        if (!wait_bar(ptx::smem_addr(&ctl.dp_full), steps & 1, abort_flag)) {
+          stop = true;
+          break;
+        }
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) tmem_fetch32(dp_at + q * 32, dp[q]);
+        tmem_wait_ld();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl.dp_free));
         const int seen = limit - (it.jb + j) * kTile - half * 64;
         const bool masked = __any_sync(0xffffffffu, seen < 64);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
+          tmem_arrived(dp[q]);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            uint64_t x = pair(dp[q][e], dp[q][e + 1]);
+            x = BF16 ? add2(x, nd2) : fma2(x, gs2, nd2);
+            x = mul2(x, pair(s[q][e], s[q][e + 1]));
+            dp[q][e] = (uint32_t)x;
+            dp[q][e + 1] = (uint32_t)(x >> 32);
+          }
+          if (masked) {  // hidden columns, whatever their scores and products are
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (q * 32 + e >= seen) dp[q][e] = 0;
+          }
           uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float d[2];
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-              const int x = 2 * e + f;
-              const float p = exp2_fast(fmaf(__uint_as_float(s[q][x]), c, -lse));
-              d[f] = p * fmaf(__uint_as_float(dp[q][x]), gs, gd);
-              if (masked && q * 32 + x >= seen) d[f] = 0.0f;
-            }
-            w[e] = pack2<BF16>(d[0], d[1]);
-          }
+          for (int e = 0; e < 16; ++e)
+            w[e] = pack2<BF16>(__uint_as_float(dp[q][2 * e]), __uint_as_float(dp[q][2 * e + 1]));
           tmem_store16(s_at + q * 16, w);
+          tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl.ds_ready[steps & 1][q]));
         }
-        tmem_wait_st();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl.ds_ready));
       }
       if (stop) break;
       if (it.n > 0) {
@@ -613,7 +651,7 @@ struct DkvCtl {
   uint64_t g_full[DkvPlan<H>::gs], g_empty[DkvPlan<H>::gs];
   uint64_t st_full[2], st_empty[2];
   uint64_t own_full[2], own_empty[2];
-  uint64_t tail, drain, s_full, dp_full, p_ready, ds_ready, done;
+  uint64_t tail, drain, s_full, dp_full, p_ready[2], ds_ready[2], done;
   uint32_t tmem;
   int abort_flag;
 };
@@ -633,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!smem_ok(dsmem)) return;
   DkvCtl<H>& ctl = *reinterpret_cast<DkvCtl<H>*>(dsmem + Plan::ctl_at);
   const TcGeom& g = a.g;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uni(tid >> 5), lane = tid & 31;
   const uint32_t own = ptx::smem_addr(dsmem);
   const uint32_t qring = own + 2 * Plan::own * Plan::tile, gring = qring + Plan::qs * Plan::tile;
   const uint32_t stats = own + Plan::stat_at;
@@ -658,8 +696,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(ptx::smem_addr(&ctl.drain), 1);
     ptx::mbar_init(ptx::smem_addr(&ctl.s_full), 1);
     ptx::mbar_init(ptx::smem_addr(&ctl.dp_full), 1);
-    ptx::mbar_init(ptx::smem_addr(&ctl.p_ready), 8);
-    ptx::mbar_init(ptx::smem_addr(&ctl.ds_ready), 8);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(ptx::smem_addr(&ctl.p_ready[i]), 8);
+      ptx::mbar_init(ptx::smem_addr(&ctl.ds_ready[i]), 8);
+    }
     ptx::mbar_init(ptx::smem_addr(&ctl.done), 1);
     ctl.abort_flag = 0;
     ptx::fence_mbar_init();
@@ -684,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = ctl.tmem;
+  const uint32_t tmem = uni(ctl.tmem);
   ptx::pdl_wait();
 
   if (warp >= 8) {
@@ -769,8 +809,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t i = items > Plan::own ? items - Plan::own : 0; i < items; ++i)
           drain_bar(ptx::smem_addr(&ctl.own_full[i % Plan::own]), (i / Plan::own) & 1);
       }
-    } else if (warp == kMmaWarp && lane == 0) {
+    } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------------- MMA issue
+      const bool leader = elect_lane();
       const int dk = (g.D + 15) / 16;
       const uint32_t id_s = idesc_16(BF16, kTile, kTile, false);
       const uint32_t id_g = idesc_16(BF16, kTile, dk * 16, true);
@@ -778,69 +819,82 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t c = 0, items = 0;
       DkvItem it;
       bool stop = false;
-      auto wait_q = [&](uint32_t i) {
-        return wait_bar(ptx::smem_addr(&ctl.q_full[i % Plan::qs]), (i / Plan::qs) & 1, abort_flag);
+      auto wait = [&](uint64_t& bar, uint32_t parity) {
+        return all_lanes(wait_bar(ptx::smem_addr(&bar), parity, abort_flag));
       };
-      auto wait_g = [&](uint32_t i) {
-        return wait_bar(ptx::smem_addr(&ctl.g_full[i % Plan::gs]), (i / Plan::gs) & 1, abort_flag);
+      auto commit = [&](uint64_t& bar) {
+        if (leader) ptx::mma_commit(ptx::smem_addr(&bar));
       };
+      auto wait_q = [&](uint32_t i) { return wait(ctl.q_full[i % Plan::qs], (i / Plan::qs) & 1); };
+      auto wait_g = [&](uint32_t i) { return wait(ctl.g_full[i % Plan::gs], (i / Plan::gs) & 1); };
       auto q_tile = [&](uint32_t i) { return qring + i % Plan::qs * Plan::tile; };
       auto g_tile = [&](uint32_t i) { return gring + i % Plan::gs * Plan::tile; };
       for (int k = 0; !stop && dkv_item(a, k, it); ++k) {
-        if (it.n == 0) continue;
+        const int n = uni(it.n);
+        if (n == 0) continue;
         const uint32_t ob = items % Plan::own;
-        if (!wait_bar(ptx::smem_addr(&ctl.own_full[ob]), (items / Plan::own) & 1, abort_flag) ||
-            !wait_q(c))
-          break;
+        if (!wait(ctl.own_full[ob], (items / Plan::own) & 1) || !wait_q(c)) break;
         ++items;
         const uint32_t kt = own + ob * 2 * Plan::tile, vt = kt + Plan::tile;
         ptx::tc_fence_after();
-        mma_scores<H>(st, kt, q_tile(c), dk, id_s);
-        ptx::mma_commit(ptx::smem_addr(&ctl.s_full));
+        if (leader) mma_scores<H>(st, kt, q_tile(c), dk, id_s);
+        commit(ctl.s_full);
         if (!wait_g(c)) break;
         ptx::tc_fence_after();
-        mma_scores<H>(dp, vt, g_tile(c), dk, id_s);
-        ptx::mma_commit(ptx::smem_addr(&ctl.dp_full));
-        for (int i = 0; i < it.n; ++i, ++c) {
-          const bool more = i + 1 < it.n;
-          if (!wait_bar(ptx::smem_addr(&ctl.p_ready), c & 1, abort_flag)) {
+        if (leader) mma_scores<H>(dp, vt, g_tile(c), dk, id_s);
+        commit(ctl.dp_full);
+        for (int i = 0; i < n; ++i, ++c) {
+          const bool more = i + 1 < n;
+          if (!wait(ctl.p_ready[0], c & 1)) {
             stop = true;
             break;
           }
           ptx::tc_fence_after();
-          mma_grads(dv, st, g_tile(c), id_g, i == 0);
-          ptx::mma_commit(ptx::smem_addr(&ctl.g_empty[c % Plan::gs]));
+          if (leader) mma_grads<0>(dv, st, g_tile(c), id_g, i == 0);
+          if (!wait(ctl.p_ready[1], c & 1)) {
+            stop = true;
+            break;
+          }
+          ptx::tc_fence_after();
+          if (leader) mma_grads<1>(dv, st, g_tile(c), id_g, i == 0);
+          commit(ctl.g_empty[c % Plan::gs]);
           if (more) {
             if (!wait_q(c + 1)) {
               stop = true;
               break;
             }
             ptx::tc_fence_after();
-            mma_scores<H>(st, kt, q_tile(c + 1), dk, id_s);
-            ptx::mma_commit(ptx::smem_addr(&ctl.s_full));
+            if (leader) mma_scores<H>(st, kt, q_tile(c + 1), dk, id_s);
+            commit(ctl.s_full);
           }
-          if (!wait_bar(ptx::smem_addr(&ctl.ds_ready), c & 1, abort_flag)) {
+          if (!wait(ctl.ds_ready[0], c & 1)) {
             stop = true;
             break;
           }
           ptx::tc_fence_after();
-          mma_grads(dkk, dp, q_tile(c), id_g, i == 0);
-          ptx::mma_commit(ptx::smem_addr(&ctl.q_empty[c % Plan::qs]));
+          if (leader) mma_grads<0>(dkk, dp, q_tile(c), id_g, i == 0);
+          if (!wait(ctl.ds_ready[1], c & 1)) {
+            stop = true;
+            break;
+          }
+          ptx::tc_fence_after();
+          if (leader) mma_grads<1>(dkk, dp, q_tile(c), id_g, i == 0);
+          commit(ctl.q_empty[c % Plan::qs]);
           if (more) {
             if (!wait_g(c + 1)) {
               stop = true;
               break;
             }
             ptx::tc_fence_after();
-            mma_scores<H>(dp, vt, g_tile(c + 1), dk, id_s);
-            ptx::mma_commit(ptx::smem_addr(&ctl.dp_full));
+            if (leader) mma_scores<H>(dp, vt, g_tile(c + 1), dk, id_s);
+            commit(ctl.dp_full);
           } else {
-            ptx::mma_commit(ptx::smem_addr(&ctl.own_empty[ob]));
-            ptx::mma_commit(ptx::smem_addr(&ctl.done));
+            commit(ctl.own_empty[ob]);
+            commit(ctl.done);
           }
         }
       }
-      ptx::mma_commit(ptx::smem_addr(&ctl.drain));
+      commit(ctl.drain);
       drain_bar(ptx::smem_addr(&ctl.drain), 0);
     }
   } else {
@@ -849,8 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t s_at = tmem + half * 64 + lanes, dp_at = s_at + 128;
-    const float c = g.scale * kLog2e;
-    const float shift_p = BF16 ? 0.0f : (float)kPShift;
+    const uint64_t c2 = pair(g.scale * kLog2e, g.scale * kLog2e);
     uint32_t steps = 0, items = 0;
     int shift = 0, last_bh = -1;
     DkvItem it;
@@ -861,86 +914,107 @@ __global__ void __launch_bounds__(kThreads, 1)
         last_bh = bh;
       }
       const float gs = BF16 ? 1.0f : pow2i(shift - kPShift);
+      const uint64_t gs2 = pair(gs, gs);
       bool stop = false;
       for (int i = 0; i < it.n; ++i, ++steps) {
         const uint32_t ss = steps & 1;
-        const float4* lse4 = reinterpret_cast<const float4*>(dsmem + Plan::stat_at + ss * kStatBytes);
-        const float4* del4 = lse4 + kTile / 4;
-        if (!wait_bar(ptx::smem_addr(&ctl.st_full[ss]), (steps >> 1) & 1, abort_flag) ||
-            !wait_bar(ptx::smem_addr(&ctl.s_full), steps & 1, abort_flag)) {
+        const ulonglong2* nlse = reinterpret_cast<const ulonglong2*>(dsmem + Plan::stat_at +
+                                                                     ss * kStatBytes) + half * 16;
+        const ulonglong2* ndelta = nlse + kTile / 4;
+        if (!wait_bar(ptx::smem_addr(&ctl.st_full[ss]), (steps >> 1) & 1, abort_flag)) {
+          stop = true;
+          break;
+        }
+        // the columns' statistics are in registers before the scores are there
+        ulonglong2 n[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) n[e] = nlse[e];
+        if (!wait_bar(ptx::smem_addr(&ctl.s_full), steps & 1, abort_flag)) {
           stop = true;
           break;
         }
         ptx::tc_fence_after();
         uint32_t s[2][32];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) tmem_fetch32(s_at + q * 32, s[q]);
+        tmem_fetch32(s_at, s[0]);
         // columns [0, hide) are queries before the first that sees key j
         int hide = 0;
         if (g.causal)
           hide = min(max(j - it.l.shift - (it.ib + i) * g.toks, 0), g.toks) * g.G - half * 64;
-        tmem_wait_ld();
-#pragma unroll
-        for (int q = 0; q < 2; ++q) tmem_arrived(s[q]);
         const bool masked = __any_sync(0xffffffffu, hide > 0);
+        tmem_wait_ld();
+        tmem_arrived(s[0]);
+        tmem_fetch32(s_at + 32, s[1]);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          uint32_t w[16];
+          if (q == 1) {
+            tmem_wait_ld();
+            tmem_arrived(s[1]);
+          }
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const float4 l4 = lse4[half * 16 + q * 8 + e / 4];
-            const float ls[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              float p = exp2_fast(fmaf(__uint_as_float(s[q][e + f]), c, shift_p - ls[f]));
-              if (masked && q * 32 + e + f < hide) p = 0.0f;
-              s[q][e + f] = __float_as_uint(p);
-            }
-            w[e / 2] = pack2<BF16>(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
-            w[e / 2 + 1] = pack2<BF16>(__uint_as_float(s[q][e + 2]), __uint_as_float(s[q][e + 3]));
+            const uint64_t x = fma2(pair(s[q][e], s[q][e + 1]), c2, n[q * 8 + e / 4].x);
+            const uint64_t y = fma2(pair(s[q][e + 2], s[q][e + 3]), c2, n[q * 8 + e / 4].y);
+            s[q][e] = __float_as_uint(exp2_fast(low(x)));
+            s[q][e + 1] = __float_as_uint(exp2_fast(high(x)));
+            s[q][e + 2] = __float_as_uint(exp2_fast(low(y)));
+            s[q][e + 3] = __float_as_uint(exp2_fast(high(y)));
           }
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (q * 32 + e < hide) s[q][e] = 0;
+          }
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[e] = pack2<BF16>(__uint_as_float(s[q][2 * e]), __uint_as_float(s[q][2 * e + 1]));
           tmem_store16(s_at + q * 16, w);
+          tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl.p_ready[q]));
         }
-        tmem_wait_st();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl.p_ready));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) n[e] = ndelta[e];
         if (!wait_bar(ptx::smem_addr(&ctl.dp_full), steps & 1, abort_flag)) {
           stop = true;
           break;
         }
         ptx::tc_fence_after();
         uint32_t dp[2][32];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) tmem_fetch32(dp_at + q * 32, dp[q]);
+        tmem_fetch32(dp_at, dp[0]);
         tmem_wait_ld();
-#pragma unroll
-        for (int q = 0; q < 2; ++q) tmem_arrived(dp[q]);
+        tmem_arrived(dp[0]);
+        tmem_fetch32(dp_at + 32, dp[1]);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
+          if (q == 1) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) n[e] = ndelta[8 + e];
+            tmem_wait_ld();
+            tmem_arrived(dp[1]);
+          }
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const float4 d4 = del4[half * 16 + q * 8 + e / 4];
-            const float ds[4] = {d4.x, d4.y, d4.z, d4.w};
-            float r[4];
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              r[f] = __uint_as_float(s[q][e + f]) * (__uint_as_float(dp[q][e + f]) - ds[f]);
-              if (!BF16) r[f] *= gs;
+            uint64_t x = add2(pair(dp[q][e], dp[q][e + 1]), n[e / 4].x);
+            uint64_t y = add2(pair(dp[q][e + 2], dp[q][e + 3]), n[e / 4].y);
+            x = mul2(x, pair(s[q][e], s[q][e + 1]));
+            y = mul2(y, pair(s[q][e + 2], s[q][e + 3]));
+            if (!BF16) {
+              x = mul2(x, gs2);
+              y = mul2(y, gs2);
             }
-            w[e / 2] = pack2<BF16>(r[0], r[1]);
-            w[e / 2 + 1] = pack2<BF16>(r[2], r[3]);
+            w[e / 2] = pack2<BF16>(low(x), high(x));
+            w[e / 2 + 1] = pack2<BF16>(low(y), high(y));
           }
           tmem_store16(dp_at + q * 16, w);
+          tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl.ds_ready[q]));
         }
-        tmem_wait_st();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(ptx::smem_addr(&ctl.st_empty[ss]));
-          ptx::mbar_arrive(ptx::smem_addr(&ctl.ds_ready));
-        }
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl.st_empty[ss]));
       }
       if (stop) break;
       if (it.n > 0) {

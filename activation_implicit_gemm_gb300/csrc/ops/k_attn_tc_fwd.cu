@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t dsmem[];
   __shared__ FwdCtl<H> ctl;
   const TcGeom& g = a.g;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uni(tid >> 5), lane = tid & 31;
   const uint32_t qbase = (ptx::smem_addr(dsmem) + 1023u) & ~1023u;
   const uint32_t ring = qbase + 2 * Plan::tile_bytes;
   volatile int* abort_flag = &ctl.abort_flag;
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const uint32_t tmem = ctl.tmem;
+  const uint32_t tmem = uni(ctl.tmem);
   ptx::pdl_wait();
 
   if (warp >= 8) {
@@ -210,68 +210,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
    } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ MMA issue
-    if (lane == 0) {
-      const uint32_t id_s = idesc_16(BF16, kTile, kTile, false);
-      const int dk = (g.D + 15) / 16;  // K steps of Q K^T, N / 16 of P V
-      const uint32_t id_o = idesc_16(BF16, kTile, dk * 16, true);
-      uint32_t c = 0, q_items = 0, pv[2] = {0, 0};
-      FwdItem it;
-      bool stop = false;
-      auto scores = [&](int t, uint32_t ktile) {
-        const uint32_t q = desc_k(qbase + t * Plan::tile_bytes), kt = desc_k(ktile);
+    const bool leader = elect_lane();
+    const uint32_t id_s = idesc_16(BF16, kTile, kTile, false);
+    const int dk = (g.D + 15) / 16;  // K steps of Q K^T, N / 16 of P V
+    const uint32_t id_o = idesc_16(BF16, kTile, dk * 16, true);
+    uint32_t c = 0, q_items = 0, pv0 = 0, pv1 = 0;
+    FwdItem it;
+    bool stop = false;
+    auto wait = [&](uint64_t& bar, uint32_t parity) {
+      return all_lanes(wait_bar(ptx::smem_addr(&bar), parity, abort_flag));
+    };
+    auto commit = [&](uint64_t& bar) {
+      if (leader) ptx::mma_commit(ptx::smem_addr(&bar));
+    };
+    auto scores = [&](int t, uint32_t ktile) {
+      const uint32_t q = desc_k(qbase + t * Plan::tile_bytes), kt = desc_k(ktile);
+      if (leader) {
 #pragma unroll
         for (int d = 0; d < 4 * H; ++d)
           if (d < dk) mma_ss(tmem + t * 128, q + k_step(d), kt + k_step(d), id_s, d > 0);
-        ptx::mma_commit(ptx::smem_addr(&ctl.s_full[t]));
-      };
-      for (int k = 0; !stop && fwd_item(a, k, it); ++k) {
-        const int n = max(it.n[0], it.n[1]);
-        if (n == 0) continue;
-        if (!wait_bar(ptx::smem_addr(&ctl.q_full), q_items & 1, abort_flag)) break;
-        ++q_items;
-        if (!wait_bar(ptx::smem_addr(&ctl.full[c % Plan::slots]), (c / Plan::slots) & 1,
-                      abort_flag))
+      }
+      commit(ctl.s_full[t]);
+    };
+    for (int k = 0; !stop && fwd_item(a, k, it); ++k) {
+      const int n0 = uni(it.n[0]), n1 = uni(it.n[1]), n = max(n0, n1);
+      if (n == 0) continue;
+      if (!wait(ctl.q_full, q_items & 1)) break;
+      ++q_items;
+      if (!wait(ctl.full[c % Plan::slots], (c / Plan::slots) & 1)) break;
+      ptx::tc_fence_after();
+      if (n0 > 0) scores(0, ring + c % Plan::slots * Plan::tile_bytes);
+      if (n1 > 0) scores(1, ring + c % Plan::slots * Plan::tile_bytes);
+      commit(ctl.empty[c % Plan::slots]);
+      if (n == 1) commit(ctl.q_empty);
+      for (int j = 0; j < n; ++j, c += 2) {
+        const uint32_t vs = (c + 1) % Plan::slots, ks = (c + 2) % Plan::slots;
+        if (!wait(ctl.full[vs], ((c + 1) / Plan::slots) & 1) ||
+            (j + 1 < n && !wait(ctl.full[ks], ((c + 2) / Plan::slots) & 1))) {
+          stop = true;
           break;
-        ptx::tc_fence_after();
+        }
+        const uint32_t v = desc_mn(ring + vs * Plan::tile_bytes);
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (it.n[t] > 0) scores(t, ring + c % Plan::slots * Plan::tile_bytes);
-        ptx::mma_commit(ptx::smem_addr(&ctl.empty[c % Plan::slots]));
-        if (n == 1) ptx::mma_commit(ptx::smem_addr(&ctl.q_empty));
-        for (int j = 0; j < n; ++j, c += 2) {
-          const uint32_t vs = (c + 1) % Plan::slots, ks = (c + 2) % Plan::slots;
-          if (!wait_bar(ptx::smem_addr(&ctl.full[vs]), ((c + 1) / Plan::slots) & 1, abort_flag) ||
-              (j + 1 < n && !wait_bar(ptx::smem_addr(&ctl.full[ks]),
-                                      ((c + 2) / Plan::slots) & 1, abort_flag))) {
+        for (int t = 0; t < 2; ++t) {
+          const int nt = t ? n1 : n0;
+          if (j >= nt) continue;
+          if (!wait(ctl.p_ready[t], (t ? pv1 : pv0) & 1)) {
             stop = true;
             break;
           }
-          const uint32_t v = desc_mn(ring + vs * Plan::tile_bytes);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (j >= it.n[t]) continue;
-            if (!wait_bar(ptx::smem_addr(&ctl.p_ready[t]), pv[t] & 1, abort_flag)) {
-              stop = true;
-              break;
-            }
-            ++pv[t];
-            ptx::tc_fence_after();
+          ++(t ? pv1 : pv0);
+          ptx::tc_fence_after();
+          if (leader) {
 #pragma unroll
             for (int s = 0; s < kTile / 16; ++s)
               mma_ts(tmem + 256 + t * 128, tmem + t * 128 + s * 8, v + s * (2048 >> 4), id_o,
                      j > 0 || s > 0);
-            if (j == it.n[t] - 1) ptx::mma_commit(ptx::smem_addr(&ctl.o_done[t]));
-            if (j + 1 < it.n[t]) scores(t, ring + ks * Plan::tile_bytes);
           }
-          if (stop) break;
-          ptx::mma_commit(ptx::smem_addr(&ctl.empty[vs]));
-          if (j + 1 < n) ptx::mma_commit(ptx::smem_addr(&ctl.empty[ks]));
-          if (j + 2 == n) ptx::mma_commit(ptx::smem_addr(&ctl.q_empty));
+          if (j == nt - 1) commit(ctl.o_done[t]);
+          if (j + 1 < nt) scores(t, ring + ks * Plan::tile_bytes);
         }
+        if (stop) break;
+        commit(ctl.empty[vs]);
+        if (j + 1 < n) commit(ctl.empty[ks]);
+        if (j + 2 == n) commit(ctl.q_empty);
       }
-      ptx::mma_commit(ptx::smem_addr(&ctl.drain));
-      drain_bar(ptx::smem_addr(&ctl.drain), 0);
     }
+    commit(ctl.drain);
+    drain_bar(ptx::smem_addr(&ctl.drain), 0);
    }
   } else {
     // ------------------------------------------------------------------ softmax, epilogue
@@ -335,20 +341,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         const float ref = m == -INFINITY ? 0.0f : m;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint64_t c2 = pair(c, c), r2 = pair(-ref, -ref);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t p[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float x = exp2_fast(fmaf(__uint_as_float(s[q][2 * e]), c, -ref));
-            const float y = exp2_fast(fmaf(__uint_as_float(s[q][2 * e + 1]), c, -ref));
-            sum[q] += x + y;
-            p[e] = pack2<BF16>(x, y);
+            const uint64_t x = fma2(pair(s[q][2 * e], s[q][2 * e + 1]), c2, r2);
+            const float u = exp2_fast(low(x)), v = exp2_fast(high(x));
+            sum[e & 1] = add2(sum[e & 1], pair(u, v));
+            p[e] = pack2<BF16>(u, v);
           }
           tmem_store16(s_at + q * 16, p);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        sum[0] = add2(sum[0], sum[1]);
+        l += low(sum[0]) + high(sum[0]);
         tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
