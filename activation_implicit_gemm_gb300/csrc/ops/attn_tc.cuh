@@ -101,6 +101,33 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int 
       : "memory");
 }
 
+// 4-D tiled TMA store of a box from shared memory (elements outside the tensor are left out),
+// its group, and the wait until the group's boxes have been read / written.
+__device__ __forceinline__ void tma_store_4d(const void* tmap, uint32_t src, int c0, int c1, int c2,
+                                             int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+          (uint64_t)tmap),
+      "r"(src), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+// One thread's 16-bit row of 32 columns (64 bytes) of a swizzled box of 128-byte rows.
+__device__ __forceinline__ void stage_row(uint32_t box, int row, int c0, const uint32_t (&w)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    ptx::st_shared_v4(box + row * 128 + (((c0 / 8 + i) ^ (row & 7)) << 4), w[4 * i], w[4 * i + 1],
+                      w[4 * i + 2], w[4 * i + 3]);
+}
+
 #define FCONV_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), \
                        "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
 #define FCONV_I8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), \
@@ -250,6 +277,66 @@ __device__ __forceinline__ int key_tiles(const TcGeom& g, const TcLens& l, int t
   if (t0 >= l.q) return 0;
   const int last = min(t0 + g.toks, l.q) - 1;
   return (key_limit(g, l, last) + kTile - 1) / kTile;
+}
+
+// A block's dynamic shared memory must start on the swizzle atom's 1024 bytes.
+__device__ __forceinline__ bool smem_ok(const uint8_t* p) {
+  if ((ptx::smem_addr(p) & 1023u) == 0) return true;
+  if (threadIdx.x == 0) atomicOr(&g_wait_error, 2u);
+  return false;
+}
+
+// Work items on their way from the load warp, which makes them (a running counter in global
+// memory where items differ in length, else a fixed order; lengths and index divisions), to
+// the MMA warp and the eight others, two ahead.
+template <typename Item>
+struct Sched {
+  uint64_t full[2], empty[2];
+  Item slot[2];
+};
+constexpr int kSchedReaders = 9;  // warps
+template <typename Item>
+__device__ __forceinline__ void sched_init(Sched<Item>& s) {
+  for (int i = 0; i < 2; ++i) {
+    ptx::mbar_init(ptx::smem_addr(&s.full[i]), 1);
+    ptx::mbar_init(ptx::smem_addr(&s.empty[i]), kSchedReaders);
+  }
+}
+// Whole load warp: makes and hands on item k; false at the end (handed on as well).
+template <typename Item, typename Make>
+__device__ __forceinline__ bool sched_make(Sched<Item>& s, int k, Item& it, int* counter, int lane,
+                                           volatile int* abort_flag, Make make) {
+  const int i = k & 1;
+  if (!all_lanes(wait_bar(ptx::smem_addr(&s.empty[i]), ((k >> 1) & 1) ^ 1, abort_flag)))
+    return false;
+  if (lane == 0) {
+    // rounds run forwards and backwards in turn: the blocks' sums come out even
+    const int at = counter ? atomicAdd(counter, 1)
+                           : k * (int)gridDim.x + ((k & 1) ? (int)(gridDim.x - 1 - blockIdx.x)
+                                                           : (int)blockIdx.x);
+    Item x;
+    make(at, x);
+    s.slot[i] = x;
+  }
+  __syncwarp();
+  it = s.slot[i];
+  __syncwarp();
+  if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&s.full[i]));
+  return it.valid;
+}
+template <typename Item>
+__device__ __forceinline__ bool sched_take(Sched<Item>& s, int k, Item& it, int lane,
+                                           volatile int* abort_flag) {
+  const int i = k & 1;
+  if (!all_lanes(wait_bar(ptx::smem_addr(&s.full[i]), (k >> 1) & 1, abort_flag))) return false;
+  it = s.slot[i];
+  __syncwarp();
+  if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&s.empty[i]));
+  return it.valid;
+}
+// Whether items differ enough in length for a running counter.
+inline bool sched_dynamic(const fconv_attn_desc& d, long long items, int sms) {
+  return items > sms && (d.causal || d.has_q_lens || d.has_kv_lens);
 }
 
 // Zeroes rows [lo, hi) of a tile made of `halves` boxes of 128-byte rows (the swizzle moves

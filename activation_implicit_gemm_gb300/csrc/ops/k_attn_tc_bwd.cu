@@ -49,6 +49,7 @@ struct BwdArgs {
   TcGeom g;
   int splits, per;   // splits of the walked axis, tiles of a split
   int items;
+  int* counter;      // of the items handed out, or null
   const float* stat;   // [b][hk][query tile]: 128 of -lse (log2, with p's scale), 128 of -delta
   const float* gmax;   // f16: [b][hk][query tile] largest |dout row|^2
   const float* vmax;   // f16: [b][hk][key tile] largest |v row|^2
@@ -71,6 +72,7 @@ struct DeltaArgs {
   float* stat;
   float* gmax;
   float* vmax;
+  int* counters;  // two, set to zero for the kernels that follow
 };
 
 template <bool BF16>
@@ -86,6 +88,7 @@ __global__ void __launch_bounds__(256) attn_tc_delta(const DeltaArgs a) {
   __shared__ float top[16];
   ptx::pdl_wait();
   ptx::pdl_trigger();
+  if (blockIdx.x == 0 && threadIdx.x < 2) a.counters[threadIdx.x] = 0;
   const TcGeom& g = a.g;
   const int per = g.qtiles + (BF16 ? 0 : g.ktiles);
   const int bh = blockIdx.x / per, tile = blockIdx.x - bh * per;
@@ -181,13 +184,6 @@ __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t
 
 // ------------------------------------------------------------------------------ shared parts
 
-// A block's dynamic shared memory must start on the swizzle atom's 1024 bytes.
-__device__ __forceinline__ bool smem_ok(const uint8_t* p) {
-  if ((ptx::smem_addr(p) & 1023u) == 0) return true;
-  if (threadIdx.x == 0) atomicOr(&g_wait_error, 2u);
-  return false;
-}
-
 // D[128 x 128] = A B^T over head_dim, both K-major tiles in shared memory.
 template <int H>
 __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, int dk,
@@ -249,20 +245,46 @@ __device__ __forceinline__ void store_grad(uint32_t at, int c0, int D, float mul
   }
 }
 
+// One thread's half row of an accumulator, columns [32 H half, 32 H (half + 1)), times mul, into
+// a staged tile of H boxes of 64 columns.
+template <bool BF16, int H>
+__device__ __forceinline__ void stage_grad(uint32_t at, int half, int row, float mul, bool keep,
+                                           uint32_t tile) {
+#pragma unroll
+  for (int q = 0; q < H; ++q) {
+    const int d0 = half * 32 * H + q * 32;
+    uint32_t o[32], w[16];
+    tmem_fetch32(at + d0, o);
+    tmem_wait_ld();
+    tmem_arrived(o);
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      w[e] = keep ? pack2<BF16>(__uint_as_float(o[2 * e]) * mul, __uint_as_float(o[2 * e + 1]) * mul)
+                  : 0u;
+    stage_row(tile + (d0 >> 6) * kHalfBytes, row, d0 & 63, w);
+  }
+}
+
+// All eight warps have written what they store (or read what they free): true in warp 0 when
+// they have, in the others at once.
+__device__ __forceinline__ bool store_ready(uint64_t& bar, uint32_t n, int warp, int lane,
+                                            volatile int* abort_flag) {
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&bar));
+  return warp != 0 || wait_bar(ptx::smem_addr(&bar), n & 1, abort_flag);
+}
+
 // ------------------------------------------------------------------------------ dq
 
 struct DqItem {
-  int b, hk, split, t0, tile, jb, n;
+  int valid, b, hk, split, t0, tile, jb, n;
   TcLens l;
 };
 
-__device__ __forceinline__ int item_index(int k) {
-  return k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-}
-
-__device__ __forceinline__ bool dq_item(const BwdArgs& a, int k, DqItem& it) {
-  int u = item_index(k);
-  if (u >= a.items) return false;
+__device__ __forceinline__ void dq_item(const BwdArgs& a, int u, DqItem& it) {
+  it.valid = u < a.items;
+  if (!it.valid) return;
   it.split = u % a.splits;
   u /= a.splits;
   const int bh = (int)a.g.B * a.g.Hk;
@@ -279,7 +301,6 @@ __device__ __forceinline__ bool dq_item(const BwdArgs& a, int k, DqItem& it) {
   it.t0 = it.tile * a.g.toks;
   it.jb = it.split * a.per;
   it.n = max(min(key_tiles(a.g, it.l, it.t0) - it.jb, a.per), 0);
-  return true;
 }
 
 template <int H>
@@ -294,6 +315,8 @@ struct DqCtl {
   uint64_t own_full[2], own_empty[2];
   uint64_t tail, drain, s_full[2], dp_full, dp_free, done;
   uint64_t ds_ready[2][2];  // [step's parity][column part]: a warp may be a step ahead of another
+  uint64_t out_ready;
+  Sched<DqItem> sched;
   uint32_t tmem;
   int abort_flag;
 };
@@ -307,7 +330,8 @@ template <bool BF16, int H>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_dq(const BwdArgs a, const __grid_constant__ CUtensorMap tm_q,
                const __grid_constant__ CUtensorMap tm_g, const __grid_constant__ CUtensorMap tm_k,
-               const __grid_constant__ CUtensorMap tm_v) {
+               const __grid_constant__ CUtensorMap tm_v,
+               const __grid_constant__ CUtensorMap tm_o1) {
   using Plan = DqPlan<H>;
   extern __shared__ __align__(1024) uint8_t dsmem[];
   if (!smem_ok(dsmem)) return;
@@ -333,6 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(ptx::smem_addr(&ctl.dp_free), 8);
     for (int i = 0; i < 4; ++i) ptx::mbar_init(ptx::smem_addr(&ctl.ds_ready[i >> 1][i & 1]), 8);
     ptx::mbar_init(ptx::smem_addr(&ctl.done), 1);
+    ptx::mbar_init(ptx::smem_addr(&ctl.out_ready), 8);
+    sched_init(ctl.sched);
     ctl.abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -359,7 +385,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t c = 0, items = 0, tails = 0;
       DqItem it;
       bool stop = false;
-      for (int k = 0; !stop && dq_item(a, k, it); ++k) {
+      auto make = [&](int u, DqItem& x) { dq_item(a, u, x); };
+      for (int k = 0; !stop && sched_make(ctl.sched, k, it, a.counter, lane, abort_flag, make);
+           ++k) {
         if (it.n == 0) continue;
         const uint32_t ob = items % Plan::own;
         if (!wait_bar(ptx::smem_addr(&ctl.own_empty[ob]), ((items / Plan::own) & 1) ^ 1,
@@ -435,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto slot = [&](uint32_t i) { return ring + i % Plan::slots * Plan::tile; };
       auto free_slot = [&](uint32_t i) { commit(ctl.empty[i % Plan::slots]); };
-      for (int k = 0; !stop && dq_item(a, k, it); ++k) {
+      for (int k = 0; !stop && sched_take(ctl.sched, k, it, lane, abort_flag); ++k) {
         const int n = uni(it.n);
         if (n == 0) continue;
         const uint32_t ob = items % Plan::own;
@@ -482,11 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tc_fence_after();
           if (leader) mma_grads<1>(dq, ds, slot(c), id_g, j == 0);
           free_slot(c);
-          // Q and dO were read last by the products before this one
-          if (!more) {
-            commit(ctl.own_empty[ob]);
-            commit(ctl.done);
-          }
+          if (!more) commit(ctl.done);
         }
       }
       commit(ctl.drain);
@@ -501,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t steps = 0, items = 0;
     int shift = 0, last_bh = -1;
     DqItem it;
-    for (int k = 0; dq_item(a, k, it); ++k) {
+    for (int k = 0; sched_take(ctl.sched, k, it, lane, abort_flag); ++k) {
       const int i = it.t0 + tok, bh = it.b * g.Hk + it.hk;
       const int limit = row < g.rows ? key_limit(g, it.l, i) : 0;
       const float* stat = a.stat + ((int64_t)bh * g.qtiles + it.tile) * (2 * kTile);
@@ -581,16 +605,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++items;
         ptx::tc_fence_after();
       }
+      const bool keep = limit > 0;
+      const float mul = g.scale * (BF16 ? 1.0f : pow2i(-shift));
+      if (a.splits == 1 && it.n > 0) {
+        // over Q, which has been read last, and out as one box
+        const uint32_t ob = (items - 1) % Plan::own, box = own + ob * 2 * Plan::tile;
+        stage_grad<BF16, H>(tmem + 384 + lanes, half, row, mul, keep, box);
+        if (!store_ready(ctl.out_ready, items - 1, warp, lane, abort_flag)) break;
+        if (tid == 0) {
+          for (int x = 0; x < H; ++x)
+            tma_store_4d(&tm_o1, box + x * kHalfBytes, x * 64, it.hk * g.G, it.t0, it.b);
+          bulk_commit();
+          bulk_wait_read();
+          ptx::mbar_arrive(ptx::smem_addr(&ctl.own_empty[ob]));
+        }
+        continue;
+      }
       const bool ok = row < g.rows && i < g.Lq;
       const int64_t h = (int64_t)it.hk * g.G + head;
       uint16_t* out = (uint16_t*)a.out1 + it.b * a.o1[0] + i * a.o1[1] + h * a.o1[2];
       float* part = nullptr;
       if (a.splits > 1)
         part = a.part1 + ((((int64_t)it.split * g.B + it.b) * g.Hq + h) * g.Lq + i) * g.D;
-      store_grad<BF16, H>(tmem + 384 + lanes, half * 32 * H, g.D,
-                          g.scale * (BF16 ? 1.0f : pow2i(-shift)), ok, it.n > 0 && limit > 0,
+      store_grad<BF16, H>(tmem + 384 + lanes, half * 32 * H, g.D, mul, ok, it.n > 0 && keep,
                           it.n > 0, out, part);
+      if (it.n > 0) {  // Q and dO are free once every warp is here
+        if (!store_ready(ctl.out_ready, items - 1, warp, lane, abort_flag)) break;
+        if (tid == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl.own_empty[(items - 1) % Plan::own]));
+      }
     }
+    if (tid == 0) bulk_wait_all();
   }
 
   ptx::pdl_trigger();
@@ -606,13 +650,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------------------ dk, dv
 
 struct DkvItem {
-  int b, hk, split, tile, ib, n;  // query tiles [ib, ib + n)
+  int valid, b, hk, split, tile, ib, n;  // query tiles [ib, ib + n)
   TcLens l;
 };
 
-__device__ __forceinline__ bool dkv_item(const BwdArgs& a, int k, DkvItem& it) {
-  int u = item_index(k);
-  if (u >= a.items) return false;
+__device__ __forceinline__ void dkv_item(const BwdArgs& a, int u, DkvItem& it) {
+  it.valid = u < a.items;
+  if (!it.valid) return;
   it.split = u % a.splits;
   u /= a.splits;
   const int bh = (int)a.g.B * a.g.Hk;
@@ -633,7 +677,6 @@ __device__ __forceinline__ bool dkv_item(const BwdArgs& a, int k, DkvItem& it) {
   if (j0 >= it.l.k || first >= it.l.q) hi = lo = 0;
   it.ib = max(lo, it.split * a.per);
   it.n = max(min(hi, (it.split + 1) * a.per) - it.ib, 0);
-  return true;
 }
 
 template <int H>
@@ -652,6 +695,8 @@ struct DkvCtl {
   uint64_t st_full[2], st_empty[2];
   uint64_t own_full[2], own_empty[2];
   uint64_t tail, drain, s_full, dp_full, p_ready[2], ds_ready[2], done;
+  uint64_t out_ready;
+  Sched<DkvItem> sched;
   uint32_t tmem;
   int abort_flag;
 };
@@ -665,7 +710,9 @@ template <bool BF16, int H>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_dkv(const BwdArgs a, const __grid_constant__ CUtensorMap tm_q,
                 const __grid_constant__ CUtensorMap tm_g, const __grid_constant__ CUtensorMap tm_k,
-                const __grid_constant__ CUtensorMap tm_v) {
+                const __grid_constant__ CUtensorMap tm_v,
+                const __grid_constant__ CUtensorMap tm_o1,
+                const __grid_constant__ CUtensorMap tm_o2) {
   using Plan = DkvPlan<H>;
   extern __shared__ __align__(1024) uint8_t dsmem[];
   if (!smem_ok(dsmem)) return;
@@ -701,6 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(ptx::smem_addr(&ctl.ds_ready[i]), 8);
     }
     ptx::mbar_init(ptx::smem_addr(&ctl.done), 1);
+    ptx::mbar_init(ptx::smem_addr(&ctl.out_ready), 8);
+    sched_init(ctl.sched);
     ctl.abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -734,7 +783,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t c = 0, items = 0, tails = 0;  // c: query tiles loaded so far
       DkvItem it;
       bool stop = false;
-      for (int k = 0; !stop && dkv_item(a, k, it); ++k) {
+      auto make = [&](int u, DkvItem& x) { dkv_item(a, u, x); };
+      for (int k = 0; !stop && sched_make(ctl.sched, k, it, a.counter, lane, abort_flag, make);
+           ++k) {
         if (it.n == 0) continue;
         const uint32_t ob = items % Plan::own;
         if (!wait_bar(ptx::smem_addr(&ctl.own_empty[ob]), ((items / Plan::own) & 1) ^ 1,
@@ -829,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto wait_g = [&](uint32_t i) { return wait(ctl.g_full[i % Plan::gs], (i / Plan::gs) & 1); };
       auto q_tile = [&](uint32_t i) { return qring + i % Plan::qs * Plan::tile; };
       auto g_tile = [&](uint32_t i) { return gring + i % Plan::gs * Plan::tile; };
-      for (int k = 0; !stop && dkv_item(a, k, it); ++k) {
+      for (int k = 0; !stop && sched_take(ctl.sched, k, it, lane, abort_flag); ++k) {
         const int n = uni(it.n);
         if (n == 0) continue;
         const uint32_t ob = items % Plan::own;
@@ -889,7 +940,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (leader) mma_scores<H>(dp, vt, g_tile(c + 1), dk, id_s);
             commit(ctl.dp_full);
           } else {
-            commit(ctl.own_empty[ob]);
             commit(ctl.done);
           }
         }
@@ -907,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t steps = 0, items = 0;
     int shift = 0, last_bh = -1;
     DkvItem it;
-    for (int k = 0; dkv_item(a, k, it); ++k) {
+    for (int k = 0; sched_take(ctl.sched, k, it, lane, abort_flag); ++k) {
       const int j = it.tile * kTile + row, bh = it.b * g.Hk + it.hk;
       if (!BF16 && bh != last_bh) {
         shift = grad_shift(a, bh, lane);
@@ -1022,7 +1072,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++items;
         ptx::tc_fence_after();
       }
-      const bool ok = j < g.Lk, keep = it.n > 0 && j < it.l.k;
+      const bool keep = it.n > 0 && j < it.l.k;
+      const float mul_v = BF16 ? 1.0f : pow2i(-kPShift);
+      const float mul_k = g.scale * (BF16 ? 1.0f : pow2i(-shift));
+      if (a.splits == 1 && it.n > 0) {
+        // dk over K and dv over V, which have been read last, and out as boxes
+        const uint32_t ob = (items - 1) % Plan::own, box = own + ob * 2 * Plan::tile;
+        stage_grad<BF16, H>(tmem + 384 + lanes, half, row, mul_k, keep, box);
+        stage_grad<BF16, H>(tmem + 256 + lanes, half, row, mul_v, keep, box + Plan::tile);
+        if (!store_ready(ctl.out_ready, items - 1, warp, lane, abort_flag)) break;
+        if (tid == 0) {
+          for (int x = 0; x < H; ++x) {
+            tma_store_4d(&tm_o1, box + x * kHalfBytes, x * 64, it.hk, it.tile * kTile, it.b);
+            tma_store_4d(&tm_o2, box + Plan::tile + x * kHalfBytes, x * 64, it.hk,
+                         it.tile * kTile, it.b);
+          }
+          bulk_commit();
+          bulk_wait_read();
+          ptx::mbar_arrive(ptx::smem_addr(&ctl.own_empty[ob]));
+        }
+        continue;
+      }
+      const bool ok = j < g.Lk;
       uint16_t* o1 = (uint16_t*)a.out1 + it.b * a.o1[0] + j * a.o1[1] + it.hk * a.o1[2];
       uint16_t* o2 = (uint16_t*)a.out2 + it.b * a.o2[0] + j * a.o2[1] + it.hk * a.o2[2];
       float *p1 = nullptr, *p2 = nullptr;
@@ -1031,11 +1102,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         p1 = a.part1 + at;
         p2 = a.part2 + at;
       }
-      store_grad<BF16, H>(tmem + 256 + lanes, half * 32 * H, g.D, BF16 ? 1.0f : pow2i(-kPShift), ok,
-                          keep, it.n > 0, o2, p2);
-      store_grad<BF16, H>(tmem + 384 + lanes, half * 32 * H, g.D,
-                          g.scale * (BF16 ? 1.0f : pow2i(-shift)), ok, keep, it.n > 0, o1, p1);
+      store_grad<BF16, H>(tmem + 256 + lanes, half * 32 * H, g.D, mul_v, ok, keep, it.n > 0, o2,
+                          p2);
+      store_grad<BF16, H>(tmem + 384 + lanes, half * 32 * H, g.D, mul_k, ok, keep, it.n > 0, o1,
+                          p1);
+      if (it.n > 0) {  // K and V are free once every warp is here
+        if (!store_ready(ctl.out_ready, items - 1, warp, lane, abort_flag)) break;
+        if (tid == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl.own_empty[(items - 1) % Plan::own]));
+      }
     }
+    if (tid == 0) bulk_wait_all();
   }
 
   ptx::pdl_trigger();
@@ -1109,7 +1185,7 @@ int split_count(long long base, int tiles, int sms) {
 struct BwdPlan {
   TcGeom g;
   int dq_splits, dkv_splits;
-  size_t stat, gmax, vmax, part_q, part_k, part_v, total;  // offsets in floats
+  size_t counters, stat, gmax, vmax, part_q, part_k, part_v, total;  // offsets in floats
 };
 
 BwdPlan bwd_plan(const fconv_attn_desc& d, int sms, const AttnArgs& a) {
@@ -1125,6 +1201,7 @@ BwdPlan bwd_plan(const fconv_attn_desc& d, int sms, const AttnArgs& a) {
     at += (n + 3) / 4 * 4;
     return o;
   };
+  p.counters = take(4);
   p.stat = take((size_t)bh * p.g.qtiles * 2 * kTile);
   p.gmax = take((size_t)bh * p.g.qtiles);
   p.vmax = take((size_t)bh * p.g.ktiles);
@@ -1138,13 +1215,16 @@ BwdPlan bwd_plan(const fconv_attn_desc& d, int sms, const AttnArgs& a) {
   return p;
 }
 
-template <typename K>
+template <int OUTS, typename K>
 int start(K kern, uint32_t smem, int items, int sms, const BwdArgs& b, const CUtensorMap* m,
           cudaStream_t s) {
   const int e = allow_smem((const void*)kern, smem);
   if (e) return e;
-  return launch_pdl(kern, dim3(items < sms ? items : sms), dim3(kThreads), smem, s, b, m[0], m[1],
-                    m[2], m[3]);
+  const dim3 grid(items < sms ? items : sms);
+  if constexpr (OUTS == 1)
+    return launch_pdl(kern, grid, dim3(kThreads), smem, s, b, m[0], m[1], m[2], m[3], m[4]);
+  else
+    return launch_pdl(kern, grid, dim3(kThreads), smem, s, b, m[0], m[1], m[2], m[3], m[5], m[6]);
 }
 
 int join(bool bf, const JoinArgs& j, int sms, cudaStream_t s) {
@@ -1185,7 +1265,8 @@ int launch_attn_tc_backward(const fconv_attn_desc& d, int sms, const AttnArgs& a
   TcGeom& g = p.g;
   float* ws = (float*)a.ws;
   const bool bf = d.dtype == FCONV_BF16;
-  CUtensorMap m[4];  // q, dout, k, v
+  CUtensorMap m[7];  // q, dout, k, v, dq, dk, dv
+  int whole;
   std::memset(m, 0, sizeof(m));
   if (!make_map(enc, &m[0], a.q, d.dtype, g.D, g.Hq, g.Lq, g.B, d.q_stride, g.G, g.toks, nullptr,
                 &g.qb) ||
@@ -1194,7 +1275,13 @@ int launch_attn_tc_backward(const fconv_attn_desc& d, int sms, const AttnArgs& a
       !make_map(enc, &m[2], a.k, d.dtype, g.D, g.Hk, g.Lk, g.B, d.k_stride, 1, kTile, &g.kh,
                 &g.kb) ||
       !make_map(enc, &m[3], a.v, d.dtype, g.D, g.Hk, g.Lk, g.B, d.v_stride, 1, kTile, &g.vh,
-                &g.vb))
+                &g.vb) ||
+      !make_map(enc, &m[4], a.dq, d.dtype, g.D, g.Hq, g.Lq, g.B, d.dq_stride, g.G, g.toks, nullptr,
+                &whole) ||
+      !make_map(enc, &m[5], a.dk, d.dtype, g.D, g.Hk, g.Lk, g.B, d.dk_stride, 1, kTile, nullptr,
+                &whole) ||
+      !make_map(enc, &m[6], a.dv, d.dtype, g.D, g.Hk, g.Lk, g.B, d.dv_stride, 1, kTile, nullptr,
+                &whole))
     return (int)cudaErrorInvalidValue;
 
   DeltaArgs da{};
@@ -1211,6 +1298,7 @@ int launch_attn_tc_backward(const fconv_attn_desc& d, int sms, const AttnArgs& a
   da.stat = ws + p.stat;
   da.gmax = ws + p.gmax;
   da.vmax = ws + p.vmax;
+  da.counters = (int*)(ws + p.counters);
   const long long bh = (long long)g.B * g.Hk;
   int e = launch_pdl(bf ? attn_tc_delta<true> : attn_tc_delta<false>,
                      dim3((unsigned)(bh * (g.qtiles + (bf ? 0 : g.ktiles)))), dim3(256), 0, s, da);
@@ -1224,6 +1312,7 @@ int launch_attn_tc_backward(const fconv_attn_desc& d, int sms, const AttnArgs& a
   b.splits = p.dkv_splits;
   b.per = (g.qtiles + b.splits - 1) / b.splits;
   b.items = (int)(bh * g.ktiles * b.splits);
+  b.counter = sched_dynamic(d, b.items, sms) ? da.counters : nullptr;
   for (int i = 0; i < 3; ++i) {
     b.o1[i] = d.dk_stride[i];
     b.o2[i] = d.dv_stride[i];
@@ -1233,11 +1322,11 @@ int launch_attn_tc_backward(const fconv_attn_desc& d, int sms, const AttnArgs& a
   b.part1 = ws + p.part_k;
   b.part2 = ws + p.part_v;
   if (d.head_dim <= 64)
-    e = bf ? start(attn_tc_dkv<true, 1>, dkv_smem<1>(), b.items, sms, b, m, s)
-           : start(attn_tc_dkv<false, 1>, dkv_smem<1>(), b.items, sms, b, m, s);
+    e = bf ? start<2>(attn_tc_dkv<true, 1>, dkv_smem<1>(), b.items, sms, b, m, s)
+           : start<2>(attn_tc_dkv<false, 1>, dkv_smem<1>(), b.items, sms, b, m, s);
   else
-    e = bf ? start(attn_tc_dkv<true, 2>, dkv_smem<2>(), b.items, sms, b, m, s)
-           : start(attn_tc_dkv<false, 2>, dkv_smem<2>(), b.items, sms, b, m, s);
+    e = bf ? start<2>(attn_tc_dkv<true, 2>, dkv_smem<2>(), b.items, sms, b, m, s)
+           : start<2>(attn_tc_dkv<false, 2>, dkv_smem<2>(), b.items, sms, b, m, s);
   if (e) return e;
   if (b.splits > 1) {
     JoinArgs j{};
@@ -1262,15 +1351,16 @@ int launch_attn_tc_backward(const fconv_attn_desc& d, int sms, const AttnArgs& a
   b.splits = p.dq_splits;
   b.per = (g.ktiles + b.splits - 1) / b.splits;
   b.items = (int)(bh * g.qtiles * b.splits);
+  b.counter = sched_dynamic(d, b.items, sms) ? da.counters + 1 : nullptr;
   for (int i = 0; i < 3; ++i) b.o1[i] = d.dq_stride[i];
   b.out1 = a.dq;
   b.part1 = ws + p.part_q;
   if (d.head_dim <= 64)
-    e = bf ? start(attn_tc_dq<true, 1>, dq_smem<1>(), b.items, sms, b, m, s)
-           : start(attn_tc_dq<false, 1>, dq_smem<1>(), b.items, sms, b, m, s);
+    e = bf ? start<1>(attn_tc_dq<true, 1>, dq_smem<1>(), b.items, sms, b, m, s)
+           : start<1>(attn_tc_dq<false, 1>, dq_smem<1>(), b.items, sms, b, m, s);
   else
-    e = bf ? start(attn_tc_dq<true, 2>, dq_smem<2>(), b.items, sms, b, m, s)
-           : start(attn_tc_dq<false, 2>, dq_smem<2>(), b.items, sms, b, m, s);
+    e = bf ? start<1>(attn_tc_dq<true, 2>, dq_smem<2>(), b.items, sms, b, m, s)
+           : start<1>(attn_tc_dq<false, 2>, dq_smem<2>(), b.items, sms, b, m, s);
   if (e || b.splits == 1) return e;
   JoinArgs j{};
   j.part[0] = j.part[1] = b.part1;

@@ -15,7 +15,8 @@
 //
 // Roles: warps 0-3 and 4-7 softmax and epilogue of tile 0 and 1, warp 8 MMA, warp 9 TMA (10 and
 // 11 only complete the warpgroup).
-// TMEM: S0 S1 O0 O1, 128 columns each. Shared memory: two Q tiles, a ring of K and V tiles.
+// TMEM: S0 S1 O0 O1, 128 columns each. Shared memory: the Q tiles (of the next item too for
+// head_dim up to 64), a ring of K and V tiles, a box of output a tile.
 // When there are fewer blocks than SMs the keys are split; partial O (normalised, f32) and the
 // log2 of their sums go to the workspace and attn_tc_join adds them in order.
 //
@@ -41,26 +42,25 @@ struct FwdArgs {
   TcGeom g;
   int pairs, splits, per;  // query tile pairs; key splits and key tiles of a split
   int items;
+  int* counter;
   int64_t o[3];
   void* out;
   float* lse;
   float* part;      // splits > 1: [split][B][Hq][Lq][D]
   float* part_lse;  // [split][B][Hq][Lq], log2
+  size_t counter_floats, part_floats;  // of the workspace
 };
 
 struct FwdItem {
-  int b, hk, split, t0[2], n[2], jb;
+  int valid, b, hk, split, t0[2], n[2], jb;
   TcLens l;
 };
 
-// Item k of a block: rounds run forwards and backwards in turn, and in causal order the long
-// query tiles come first, so that the blocks' sums of work come out even. Without causal order
-// neighbouring blocks share a head's keys in L2.
-__device__ __forceinline__ bool fwd_item(const FwdArgs& a, int k, FwdItem& it) {
-  const int grid = gridDim.x, bid = blockIdx.x;
-  const int at = k * grid + ((k & 1) ? grid - 1 - bid : bid);
-  if (at >= a.items) return false;
-  int u = at;
+// In causal order the long query tiles come first; otherwise neighbouring blocks share a
+// head's keys in L2.
+__device__ __forceinline__ void fwd_item(const FwdArgs& a, int u, FwdItem& it) {
+  it.valid = u < a.items;
+  if (!it.valid) return;
   it.split = u % a.splits;
   u /= a.splits;
   const int bh = (int)a.g.B * a.g.Hk;
@@ -81,37 +81,47 @@ __device__ __forceinline__ bool fwd_item(const FwdArgs& a, int k, FwdItem& it) {
     it.t0[t] = (2 * pair + t) * a.g.toks;
     it.n[t] = max(min(key_tiles(a.g, it.l, it.t0[t]) - it.jb, a.per), 0);
   }
-  return true;
 }
 
 template <int H>
 struct FwdPlan {
   static constexpr uint32_t tile_bytes = H * kHalfBytes;
-  static constexpr int slots = H == 2 ? 5 : 8;
-  static constexpr uint32_t smem = (2 + slots) * tile_bytes + 1024;
+  static constexpr int own = H == 1 ? 2 : 1;    // buffers of the two Q tiles
+  static constexpr int slots = H == 1 ? 6 : 4;  // ring of K and V tiles
+  static constexpr uint32_t ring_at = 2 * own * tile_bytes;
+  static constexpr uint32_t out_at = ring_at + slots * tile_bytes;  // a box of 64 columns a tile
+  static constexpr uint32_t ctl_at = out_at + 2 * kHalfBytes;
 };
 
 template <int H>
 struct FwdCtl {
   uint64_t full[FwdPlan<H>::slots], empty[FwdPlan<H>::slots];
-  uint64_t q_full, q_empty, tail, drain;
-  uint64_t s_full[2], p_ready[2], o_done[2];
+  uint64_t q_full[2], q_empty[2], tail, drain;
+  uint64_t s_full[2], p_ready[2], o_done[2], out_ready[2], out_free[2];
+  Sched<FwdItem> sched;
   uint32_t tmem;
   int abort_flag;
 };
+template <int H>
+constexpr uint32_t fwd_smem() {
+  return FwdPlan<H>::ctl_at + sizeof(FwdCtl<H>);
+}
+static_assert(fwd_smem<2>() <= 232448 && fwd_smem<1>() <= 232448, "one block's shared memory");
 
 template <bool BF16, int H>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_forward(const FwdArgs a, const __grid_constant__ CUtensorMap tm_q,
                     const __grid_constant__ CUtensorMap tm_k,
-                    const __grid_constant__ CUtensorMap tm_v) {
+                    const __grid_constant__ CUtensorMap tm_v,
+                    const __grid_constant__ CUtensorMap tm_o) {
   using Plan = FwdPlan<H>;
-  extern __shared__ uint8_t dsmem[];
-  __shared__ FwdCtl<H> ctl;
+  extern __shared__ __align__(1024) uint8_t dsmem[];
+  if (!smem_ok(dsmem)) return;
+  FwdCtl<H>& ctl = *reinterpret_cast<FwdCtl<H>*>(dsmem + Plan::ctl_at);
   const TcGeom& g = a.g;
   const int tid = threadIdx.x, warp = uni(tid >> 5), lane = tid & 31;
-  const uint32_t qbase = (ptx::smem_addr(dsmem) + 1023u) & ~1023u;
-  const uint32_t ring = qbase + 2 * Plan::tile_bytes;
+  const uint32_t own = ptx::smem_addr(dsmem);
+  const uint32_t ring = own + Plan::ring_at;
   volatile int* abort_flag = &ctl.abort_flag;
 
   if (tid == 0) {
@@ -119,15 +129,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(ptx::smem_addr(&ctl.full[i]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl.empty[i]), 1);
     }
-    ptx::mbar_init(ptx::smem_addr(&ctl.q_full), 1);
-    ptx::mbar_init(ptx::smem_addr(&ctl.q_empty), 1);
     ptx::mbar_init(ptx::smem_addr(&ctl.tail), 1);
     ptx::mbar_init(ptx::smem_addr(&ctl.drain), 1);
     for (int t = 0; t < 2; ++t) {
+      ptx::mbar_init(ptx::smem_addr(&ctl.q_full[t]), 1);
+      ptx::mbar_init(ptx::smem_addr(&ctl.q_empty[t]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl.s_full[t]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl.p_ready[t]), 4);
       ptx::mbar_init(ptx::smem_addr(&ctl.o_done[t]), 1);
+      ptx::mbar_init(ptx::smem_addr(&ctl.out_ready[t]), 4);
+      ptx::mbar_init(ptx::smem_addr(&ctl.out_free[t]), 1);
     }
+    sched_init(ctl.sched);
     ctl.abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -139,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::prefetch_tmap(&tm_q);
     ptx::prefetch_tmap(&tm_k);
     ptx::prefetch_tmap(&tm_v);
+    ptx::prefetch_tmap(&tm_o);
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -147,138 +161,146 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::pdl_wait();
 
   if (warp >= 8) {
-   regs_fewer<kOtherRegs>();
-   if (warp == kLoadWarp) {
-    // ------------------------------------------------------------------ TMA producer
-    uint32_t c = 0, q_items = 0, tails = 0;
-    FwdItem it;
-    bool stop = false;
-    for (int k = 0; !stop && fwd_item(a, k, it); ++k) {
-      const int n = max(it.n[0], it.n[1]);
-      if (n == 0) continue;
-      if (!wait_bar(ptx::smem_addr(&ctl.q_empty), (q_items & 1) ^ 1, abort_flag)) break;
-      ++q_items;
-      if (lane == 0) {
-        const uint32_t bar = ptx::smem_addr(&ctl.q_full);
-        const uint32_t box = (uint32_t)g.rows * 128;
-        ptx::mbar_arrive_expect_tx(bar, ((it.n[0] > 0) + (it.n[1] > 0)) * H * box);
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (it.n[t] > 0)
-            for (int h = 0; h < H; ++h)
-              tma_load_4d(qbase + t * Plan::tile_bytes + h * kHalfBytes, &tm_q, h * 64,
-                          it.hk * g.G, it.t0[t], it.b * g.qb, bar);
-      }
-      for (int j = 0; j < 2 * n; ++j, ++c) {
-        const uint32_t s = c % Plan::slots, ph = (c / Plan::slots) & 1;
-        if (!wait_bar(ptx::smem_addr(&ctl.empty[s]), ph ^ 1, abort_flag)) {
-          stop = true;
+    regs_fewer<kOtherRegs>();
+    if (warp == kLoadWarp) {
+      // ---------------------------------------------------------------- TMA producer
+      uint32_t c = 0, q_items = 0, tails = 0;
+      FwdItem it;
+      bool stop = false;
+      auto make = [&](int u, FwdItem& x) { fwd_item(a, u, x); };
+      for (int k = 0; !stop && sched_make(ctl.sched, k, it, a.counter, lane, abort_flag, make);
+           ++k) {
+        const int n = max(it.n[0], it.n[1]);
+        if (n == 0) continue;
+        const uint32_t ob = q_items % Plan::own;
+        if (!wait_bar(ptx::smem_addr(&ctl.q_empty[ob]), ((q_items / Plan::own) & 1) ^ 1,
+                      abort_flag))
           break;
-        }
-        const int key0 = (it.jb + (j >> 1)) * kTile;
-        const uint32_t dst = ring + s * Plan::tile_bytes;
-        const bool is_v = j & 1;
-        // rows of V past the sequence would meet P = 0: a NaN there must not reach the product
-        const bool ragged = is_v && key0 + kTile > it.l.k && it.l.k < g.Lk;
-        const uint32_t full = ptx::smem_addr(&ctl.full[s]);
-        const uint32_t bar = ragged ? ptx::smem_addr(&ctl.tail) : full;
+        ++q_items;
         if (lane == 0) {
-          ptx::mbar_arrive_expect_tx(bar, Plan::tile_bytes);
-          for (int h = 0; h < H; ++h)
-            tma_load_4d(dst + h * kHalfBytes, is_v ? &tm_v : &tm_k, h * 64,
-                        it.hk * (is_v ? g.vh : g.kh), key0, it.b * (is_v ? g.vb : g.kb), bar);
+          const uint32_t bar = ptx::smem_addr(&ctl.q_full[ob]);
+          const uint32_t box = (uint32_t)g.rows * 128;
+          ptx::mbar_arrive_expect_tx(bar, ((it.n[0] > 0) + (it.n[1] > 0)) * H * box);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            if (it.n[t] > 0)
+              for (int h = 0; h < H; ++h)
+                tma_load_4d(own + (ob * 2 + t) * Plan::tile_bytes + h * kHalfBytes, &tm_q, h * 64,
+                            it.hk * g.G, it.t0[t], it.b * g.qb, bar);
         }
-        if (ragged) {
-          if (!wait_bar(bar, tails & 1, abort_flag)) {
-            drain_bar(bar, tails & 1);
+        for (int j = 0; j < 2 * n; ++j, ++c) {
+          const uint32_t s = c % Plan::slots, ph = (c / Plan::slots) & 1;
+          if (!wait_bar(ptx::smem_addr(&ctl.empty[s]), ph ^ 1, abort_flag)) {
             stop = true;
             break;
           }
-          ++tails;
-          zero_rows(dst, H, it.l.k - key0, kTile, lane);
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(full);
-        }
-      }
-    }
-    if (*abort_flag) {
-      // loads in flight land before the block's shared memory is given back
-      for (uint32_t i = c > Plan::slots ? c - Plan::slots : 0; i < c; ++i)
-        drain_bar(ptx::smem_addr(&ctl.full[i % Plan::slots]), (i / Plan::slots) & 1);
-      if (q_items) drain_bar(ptx::smem_addr(&ctl.q_full), (q_items - 1) & 1);
-    }
-   } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------------ MMA issue
-    const bool leader = elect_lane();
-    const uint32_t id_s = idesc_16(BF16, kTile, kTile, false);
-    const int dk = (g.D + 15) / 16;  // K steps of Q K^T, N / 16 of P V
-    const uint32_t id_o = idesc_16(BF16, kTile, dk * 16, true);
-    uint32_t c = 0, q_items = 0, pv0 = 0, pv1 = 0;
-    FwdItem it;
-    bool stop = false;
-    auto wait = [&](uint64_t& bar, uint32_t parity) {
-      return all_lanes(wait_bar(ptx::smem_addr(&bar), parity, abort_flag));
-    };
-    auto commit = [&](uint64_t& bar) {
-      if (leader) ptx::mma_commit(ptx::smem_addr(&bar));
-    };
-    auto scores = [&](int t, uint32_t ktile) {
-      const uint32_t q = desc_k(qbase + t * Plan::tile_bytes), kt = desc_k(ktile);
-      if (leader) {
-#pragma unroll
-        for (int d = 0; d < 4 * H; ++d)
-          if (d < dk) mma_ss(tmem + t * 128, q + k_step(d), kt + k_step(d), id_s, d > 0);
-      }
-      commit(ctl.s_full[t]);
-    };
-    for (int k = 0; !stop && fwd_item(a, k, it); ++k) {
-      const int n0 = uni(it.n[0]), n1 = uni(it.n[1]), n = max(n0, n1);
-      if (n == 0) continue;
-      if (!wait(ctl.q_full, q_items & 1)) break;
-      ++q_items;
-      if (!wait(ctl.full[c % Plan::slots], (c / Plan::slots) & 1)) break;
-      ptx::tc_fence_after();
-      if (n0 > 0) scores(0, ring + c % Plan::slots * Plan::tile_bytes);
-      if (n1 > 0) scores(1, ring + c % Plan::slots * Plan::tile_bytes);
-      commit(ctl.empty[c % Plan::slots]);
-      if (n == 1) commit(ctl.q_empty);
-      for (int j = 0; j < n; ++j, c += 2) {
-        const uint32_t vs = (c + 1) % Plan::slots, ks = (c + 2) % Plan::slots;
-        if (!wait(ctl.full[vs], ((c + 1) / Plan::slots) & 1) ||
-            (j + 1 < n && !wait(ctl.full[ks], ((c + 2) / Plan::slots) & 1))) {
-          stop = true;
-          break;
-        }
-        const uint32_t v = desc_mn(ring + vs * Plan::tile_bytes);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int nt = t ? n1 : n0;
-          if (j >= nt) continue;
-          if (!wait(ctl.p_ready[t], (t ? pv1 : pv0) & 1)) {
-            stop = true;
-            break;
+          const int key0 = (it.jb + (j >> 1)) * kTile;
+          const uint32_t dst = ring + s * Plan::tile_bytes;
+          const bool is_v = j & 1;
+          // rows of V past the sequence would meet P = 0: a NaN there must not reach the product
+          const bool ragged = is_v && key0 + kTile > it.l.k && it.l.k < g.Lk;
+          const uint32_t full = ptx::smem_addr(&ctl.full[s]);
+          const uint32_t bar = ragged ? ptx::smem_addr(&ctl.tail) : full;
+          if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(bar, Plan::tile_bytes);
+            for (int h = 0; h < H; ++h)
+              tma_load_4d(dst + h * kHalfBytes, is_v ? &tm_v : &tm_k, h * 64,
+                          it.hk * (is_v ? g.vh : g.kh), key0, it.b * (is_v ? g.vb : g.kb), bar);
           }
-          ++(t ? pv1 : pv0);
-          ptx::tc_fence_after();
+          if (ragged) {
+            if (!wait_bar(bar, tails & 1, abort_flag)) {
+              drain_bar(bar, tails & 1);
+              stop = true;
+              break;
+            }
+            ++tails;
+            zero_rows(dst, H, it.l.k - key0, kTile, lane);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(full);
+          }
+        }
+      }
+      if (*abort_flag) {
+        // loads in flight land before the block's shared memory is given back
+        for (uint32_t i = c > Plan::slots ? c - Plan::slots : 0; i < c; ++i)
+          drain_bar(ptx::smem_addr(&ctl.full[i % Plan::slots]), (i / Plan::slots) & 1);
+        for (uint32_t i = q_items > Plan::own ? q_items - Plan::own : 0; i < q_items; ++i)
+          drain_bar(ptx::smem_addr(&ctl.q_full[i % Plan::own]), (i / Plan::own) & 1);
+      }
+    } else if (warp == kMmaWarp) {
+      // ---------------------------------------------------------------- MMA issue
+      const bool leader = elect_lane();
+      const uint32_t id_s = idesc_16(BF16, kTile, kTile, false);
+      const int dk = (g.D + 15) / 16;  // K steps of Q K^T, N / 16 of P V
+      const uint32_t id_o = idesc_16(BF16, kTile, dk * 16, true);
+      uint32_t c = 0, q_items = 0, pv0 = 0, pv1 = 0;
+      FwdItem it;
+      bool stop = false;
+      auto wait = [&](uint64_t& bar, uint32_t parity) {
+        return all_lanes(wait_bar(ptx::smem_addr(&bar), parity, abort_flag));
+      };
+      auto commit = [&](uint64_t& bar) {
+        if (leader) ptx::mma_commit(ptx::smem_addr(&bar));
+      };
+      for (int k = 0; !stop && sched_take(ctl.sched, k, it, lane, abort_flag); ++k) {
+        const int n0 = uni(it.n[0]), n1 = uni(it.n[1]), n = max(n0, n1);
+        if (n == 0) continue;
+        const uint32_t ob = q_items % Plan::own;
+        const uint32_t q0 = own + ob * 2 * Plan::tile_bytes;
+        auto scores = [&](int t, uint32_t ktile) {
+          const uint32_t q = desc_k(q0 + t * Plan::tile_bytes), kt = desc_k(ktile);
           if (leader) {
 #pragma unroll
-            for (int s = 0; s < kTile / 16; ++s)
-              mma_ts(tmem + 256 + t * 128, tmem + t * 128 + s * 8, v + s * (2048 >> 4), id_o,
-                     j > 0 || s > 0);
+            for (int d = 0; d < 4 * H; ++d)
+              if (d < dk) mma_ss(tmem + t * 128, q + k_step(d), kt + k_step(d), id_s, d > 0);
           }
-          if (j == nt - 1) commit(ctl.o_done[t]);
-          if (j + 1 < nt) scores(t, ring + ks * Plan::tile_bytes);
+          commit(ctl.s_full[t]);
+        };
+        if (!wait(ctl.q_full[ob], (q_items / Plan::own) & 1)) break;
+        ++q_items;
+        if (!wait(ctl.full[c % Plan::slots], (c / Plan::slots) & 1)) break;
+        ptx::tc_fence_after();
+        if (n0 > 0) scores(0, ring + c % Plan::slots * Plan::tile_bytes);
+        if (n1 > 0) scores(1, ring + c % Plan::slots * Plan::tile_bytes);
+        commit(ctl.empty[c % Plan::slots]);
+        if (n == 1) commit(ctl.q_empty[ob]);
+        for (int j = 0; j < n; ++j, c += 2) {
+          const uint32_t vs = (c + 1) % Plan::slots, ks = (c + 2) % Plan::slots;
+          if (!wait(ctl.full[vs], ((c + 1) / Plan::slots) & 1) ||
+              (j + 1 < n && !wait(ctl.full[ks], ((c + 2) / Plan::slots) & 1))) {
+            stop = true;
+            break;
+          }
+          const uint32_t v = desc_mn(ring + vs * Plan::tile_bytes);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int nt = t ? n1 : n0;
+            if (j >= nt) continue;
+            if (!wait(ctl.p_ready[t], (t ? pv1 : pv0) & 1)) {
+              stop = true;
+              break;
+            }
+            ++(t ? pv1 : pv0);
+            ptx::tc_fence_after();
+            if (leader) {
+#pragma unroll
+              for (int s = 0; s < kTile / 16; ++s)
+                mma_ts(tmem + 256 + t * 128, tmem + t * 128 + s * 8, v + s * (2048 >> 4), id_o,
+                       j > 0 || s > 0);
+            }
+            if (j == nt - 1) commit(ctl.o_done[t]);
+            if (j + 1 < nt) scores(t, ring + ks * Plan::tile_bytes);
+          }
+          if (stop) break;
+          commit(ctl.empty[vs]);
+          if (j + 1 < n) commit(ctl.empty[ks]);
+          if (j + 2 == n) commit(ctl.q_empty[ob]);
         }
-        if (stop) break;
-        commit(ctl.empty[vs]);
-        if (j + 1 < n) commit(ctl.empty[ks]);
-        if (j + 2 == n) commit(ctl.q_empty);
       }
+      commit(ctl.drain);
+      drain_bar(ptx::smem_addr(&ctl.drain), 0);
     }
-    commit(ctl.drain);
-    drain_bar(ptx::smem_addr(&ctl.drain), 0);
-   }
   } else {
     // ------------------------------------------------------------------ softmax, epilogue
     regs_more<kSoftmaxRegs>();
@@ -286,11 +308,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = tid & 127, tok = row / g.G, head = row - tok * g.G;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
     const uint32_t s_at = tmem + t * 128 + lanes, o_at = tmem + 256 + t * 128 + lanes;
+    const uint32_t box = own + Plan::out_at + t * kHalfBytes;
     const float c = g.scale * kLog2e;
-    uint32_t steps = 0, done = 0;
+    uint32_t steps = 0, done = 0, boxes = 0;
     FwdItem it;
-    for (int k = 0; fwd_item(a, k, it); ++k) {
-      const int n = t ? it.n[1] : it.n[0], i = (t ? it.t0[1] : it.t0[0]) + tok;
+    for (int k = 0; sched_take(ctl.sched, k, it, lane, abort_flag); ++k) {
+      const int n = t ? it.n[1] : it.n[0], t0 = t ? it.t0[1] : it.t0[0], i = t0 + tok;
       const int limit = row < g.rows ? key_limit(g, it.l, i) : 0;
       float m = -INFINITY, l = 0.0f;
       bool stop = false;
@@ -379,37 +402,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (a.splits > 1) a.part_lse[(int64_t)it.split * rows + at] = lse2;
         else if (a.lse) a.lse[at] = lse2 * kLn2;
       }
-      uint16_t* out = (uint16_t*)a.out + it.b * a.o[0] + i * a.o[1] + h * a.o[2];
-      float* part = a.part + ((int64_t)it.split * rows + at) * g.D;
-      for (int q = 0; q < (g.D + 31) / 32; ++q) {
-        uint32_t o[32];
-        if (n > 0) {
-          tmem_fetch32(o_at + q * 32, o);
-          tmem_wait_ld();
-          tmem_arrived(o);
-        }
-        if (!live) continue;
+      if (a.splits > 1) {
+        float* part = a.part + ((int64_t)it.split * rows + at) * g.D;
+        for (int q = 0; q < (g.D + 31) / 32; ++q) {
+          uint32_t o[32];
+          if (n > 0) {
+            tmem_fetch32(o_at + q * 32, o);
+            tmem_wait_ld();
+            tmem_arrived(o);
+          }
+          if (!live) continue;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = any ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
-        if (a.splits > 1) {
+          for (int e = 0; e < 32; ++e)
+            o[e] = any ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             if (q * 32 + e < g.D)
               ptx::st_global_v4(part + q * 32 + e, make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
-        } else {
+        }
+        continue;
+      }
+      // 64 columns at a time through shared memory to a TMA store; a thread's own 16-byte
+      // stores, one row a lane, kept the store unit busy for 4000 cycles a tile
+      for (int x = 0; x < H; ++x, ++boxes) {
+        if (t0 >= g.Lq) break;  // the pair's second tile may not exist
+        if (!wait_bar(ptx::smem_addr(&ctl.out_free[t]), (boxes & 1) ^ 1, abort_flag)) {
+          stop = true;
+          break;
+        }
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            if (q * 32 + e < g.D) {
-              uint4 w;
-              w.x = pack2<BF16>(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
-              w.y = pack2<BF16>(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-              w.z = pack2<BF16>(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5]));
-              w.w = pack2<BF16>(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7]));
-              ptx::st_global_v4(out + q * 32 + e, w);
-            }
+        for (int q = 0; q < 2; ++q) {
+          uint32_t o[32], w[16];
+          if (n > 0) {
+            tmem_fetch32(o_at + x * 64 + q * 32, o);
+            tmem_wait_ld();
+            tmem_arrived(o);
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[e] = any ? pack2<BF16>(__uint_as_float(o[2 * e]) * inv,
+                                     __uint_as_float(o[2 * e + 1]) * inv)
+                       : 0u;
+          stage_row(box, row, q * 32, w);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl.out_ready[t]));
+        if ((warp & 3) == 0) {
+          if (!wait_bar(ptx::smem_addr(&ctl.out_ready[t]), boxes & 1, abort_flag)) {
+            stop = true;
+            break;
+          }
+          if (lane == 0) {
+            tma_store_4d(&tm_o, box, x * 64, it.hk * g.G, t0, it.b);
+            bulk_commit();
+            bulk_wait_read();
+            ptx::mbar_arrive(ptx::smem_addr(&ctl.out_free[t]));
+          }
         }
       }
+      if (stop) break;
     }
+    if ((warp & 3) == 0 && lane == 0) bulk_wait_all();
   }
 
   ptx::pdl_trigger();
@@ -502,18 +556,28 @@ FwdArgs fwd_args(const fconv_attn_desc& d, int sms, const AttnArgs& a) {
   f.out = a.o;
   f.lse = a.lse;
   const size_t rows = (size_t)f.g.B * f.g.Hq * f.g.Lq;
-  f.part_lse = (float*)a.ws;
-  f.part = f.part_lse ? f.part_lse + ((size_t)f.splits * rows + 3) / 4 * 4 : nullptr;
+  float* ws = (float*)a.ws;
+  if (sched_dynamic(d, f.items, sms)) {
+    f.counter = (int*)ws;
+    f.counter_floats = 4;
+    if (ws) ws += 4;
+  }
+  if (f.splits > 1) {
+    f.part_lse = ws;
+    f.part_floats = ((size_t)f.splits * rows + 3) / 4 * 4;
+    if (ws) f.part = ws + f.part_floats;
+    f.part_floats += (size_t)f.splits * rows * f.g.D;
+  }
   return f;
 }
 
 template <bool BF16, int H>
 int launch_t(const FwdArgs& f, int sms, const CUtensorMap* m, cudaStream_t s) {
   auto kern = attn_tc_forward<BF16, H>;
-  const int e = allow_smem((const void*)kern, FwdPlan<H>::smem);
+  const int e = allow_smem((const void*)kern, fwd_smem<H>());
   if (e) return e;
   const int grid = f.items < sms ? f.items : sms;
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), FwdPlan<H>::smem, s, f, m[0], m[1], m[2]);
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), fwd_smem<H>(), s, f, m[0], m[1], m[2], m[3]);
 }
 
 }  // namespace
@@ -540,27 +604,30 @@ bool attn_tc_supported(const fconv_attn_desc& d) {
 
 size_t attn_tc_forward_workspace(const fconv_attn_desc& d, int sms) {
   const FwdArgs f = fwd_args(d, sms, AttnArgs{});
-  if (f.splits == 1) return 0;
-  const size_t rows = (size_t)d.batch * d.heads_q * d.len_q;
-  return (((size_t)f.splits * rows + 3) / 4 * 4 + (size_t)f.splits * rows * d.head_dim) *
-         sizeof(float);
+  return (f.counter_floats + f.part_floats) * sizeof(float);
 }
 
 int launch_attn_tc_forward(const fconv_attn_desc& d, int sms, const AttnArgs& a, cudaStream_t s) {
   EncodeTiledFn enc = tensor_map_encoder();
   if (!enc) return (int)cudaErrorNotSupported;
   FwdArgs f = fwd_args(d, sms, a);
-  CUtensorMap m[3];
+  int e, whole;
+  CUtensorMap m[4];  // q, k, v, out
   std::memset(m, 0, sizeof(m));
   if (!make_map(enc, &m[0], a.q, d.dtype, d.head_dim, d.heads_q, d.len_q, d.batch, d.q_stride,
                 f.g.G, f.g.toks, nullptr, &f.g.qb) ||
       !make_map(enc, &m[1], a.k, d.dtype, d.head_dim, d.heads_kv, d.len_k, d.batch, d.k_stride, 1,
                 kTile, &f.g.kh, &f.g.kb) ||
       !make_map(enc, &m[2], a.v, d.dtype, d.head_dim, d.heads_kv, d.len_k, d.batch, d.v_stride, 1,
-                kTile, &f.g.vh, &f.g.vb))
+                kTile, &f.g.vh, &f.g.vb) ||
+      !make_map(enc, &m[3], a.o, d.dtype, d.head_dim, d.heads_q, d.len_q, d.batch, d.out_stride,
+                f.g.G, f.g.toks, nullptr, &whole))
     return (int)cudaErrorInvalidValue;
+  if (f.counter) {
+    e = (int)cudaMemsetAsync(f.counter, 0, sizeof(int), s);
+    if (e) return e;
+  }
   const bool bf = d.dtype == FCONV_BF16;
-  int e;
   if (d.head_dim <= 64)
     e = bf ? launch_t<true, 1>(f, sms, m, s) : launch_t<false, 1>(f, sms, m, s);
   else

@@ -278,3 +278,27 @@ def test_gradients_of_every_size(dtype, size):
         floor = R.TINY[T] * ref.numel() ** 0.5  # the output's own rounding near zero
         off = (t.double().cpu() - ref).norm()
         assert off <= 3 * R.U[T] * ref.norm() + floor, (name, float(off / ref.norm()))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [False, True])
+def test_many_tiles_and_items_a_block(D, causal):
+    """More work items than SMs, each of many tiles, so that every block's rings, phases and
+    accumulators go round many times: two heads of one head's data give the same bits, and a
+    head computed alone agrees with it."""
+    B, L, H = 2, 1700, 48
+    q, k, v, g = tensors(B, L, L, 1, 1, D, "bf16")
+    rep = lambda t: t.cuda().expand(B, L, H, D).contiguous()  # noqa: E731
+    kl = lens([1700, 901]).cuda()
+    out, lse = fc.attention(rep(q), rep(k), rep(v), causal=causal, kv_lens=kl, return_lse=True)
+    grads = fc.attention_backward(rep(g), rep(q), rep(k), rep(v), out, lse, causal=causal,
+                                  kv_lens=kl)
+    one, l1 = fc.attention(q.cuda(), k.cuda(), v.cuda(), causal=causal, kv_lens=kl,
+                           return_lse=True, route="simple")
+    g1 = fc.attention_backward(g.cuda(), q.cuda(), k.cuda(), v.cuda(), one, l1, causal=causal,
+                               kv_lens=kl, route="simple")
+    for name, many, single in zip(("out", "dq", "dk", "dv"), (out, *grads), (one, *g1)):
+        assert torch.equal(many, many[:, :, :1].expand_as(many)), name
+        a, b = many[:, :, :1].double(), single.double()
+        assert (a - b).norm() <= 4 * R.U[torch.bfloat16] * b.norm(), name
+    assert torch.equal(lse, lse[:, :1].expand_as(lse))
