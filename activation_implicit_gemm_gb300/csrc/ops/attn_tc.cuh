@@ -302,24 +302,22 @@ __device__ __forceinline__ void sched_init(Sched<Item>& s) {
     ptx::mbar_init(ptx::smem_addr(&s.empty[i]), kSchedReaders);
   }
 }
-// Whole load warp: makes and hands on item k; false at the end (handed on as well).
+// Whole load warp (make runs in all lanes): makes and hands on item k; false at the end (handed
+// on as well).
 template <typename Item, typename Make>
 __device__ __forceinline__ bool sched_make(Sched<Item>& s, int k, Item& it, int* counter, int lane,
                                            volatile int* abort_flag, Make make) {
   const int i = k & 1;
   if (!all_lanes(wait_bar(ptx::smem_addr(&s.empty[i]), ((k >> 1) & 1) ^ 1, abort_flag)))
     return false;
-  if (lane == 0) {
-    // rounds run forwards and backwards in turn: the blocks' sums come out even
-    const int at = counter ? atomicAdd(counter, 1)
-                           : k * (int)gridDim.x + ((k & 1) ? (int)(gridDim.x - 1 - blockIdx.x)
-                                                           : (int)blockIdx.x);
-    Item x;
-    make(at, x);
-    s.slot[i] = x;
+  // rounds run forwards and backwards in turn: the blocks' sums come out even
+  int at = k * (int)gridDim.x + ((k & 1) ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x);
+  if (counter) {
+    if (lane == 0) at = atomicAdd(counter, 1);
+    at = uni(at);
   }
-  __syncwarp();
-  it = s.slot[i];
+  make(at, it);
+  if (lane == 0) s.slot[i] = it;
   __syncwarp();
   if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&s.full[i]));
   return it.valid;

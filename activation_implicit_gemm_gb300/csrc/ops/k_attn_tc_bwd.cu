@@ -98,58 +98,75 @@ __global__ void __launch_bounds__(256) attn_tc_delta(const DeltaArgs a) {
   float most = 0.0f;
   if (tile < g.qtiles) {
     float* stat = a.stat + ((int64_t)bh * g.qtiles + tile) * (2 * kTile);
-#pragma unroll 2
-    for (int r = sub; r < kTile; r += 16) {
-      const int tok = r / g.G, i = tile * g.toks + tok;
-      const int64_t h = (int64_t)hk * g.G + (r - tok * g.G);
-      const bool live = r < g.rows && i >= l.lead && i < l.q;
-      float s = 0.0f, n = 0.0f;
-      if (live && d < g.D) {
-        const uint4 x = ptx::ldg_nc_v4(a.out + b * a.o[0] + i * a.o[1] + h * a.o[2] + d);
-        const uint4 y = ptx::ldg_nc_v4(a.dout + b * a.d[0] + i * a.d[1] + h * a.d[2] + d);
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+    // four rows a lane in flight
+    for (int r0 = sub; r0 < kTile; r0 += 64) {
+      uint4 x[4], y[4];
+      bool live[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int r = r0 + n * 16, tok = r / g.G, i = tile * g.toks + tok;
+        const int64_t h = (int64_t)hk * g.G + (r - tok * g.G);
+        live[n] = r < g.rows && i >= l.lead && i < l.q;
+        x[n] = y[n] = make_uint4(0, 0, 0, 0);
+        if (live[n] && d < g.D) {
+          x[n] = ptx::ldg_nc_v4(a.out + b * a.o[0] + i * a.o[1] + h * a.o[2] + d);
+          y[n] = ptx::ldg_nc_v4(a.dout + b * a.d[0] + i * a.d[1] + h * a.d[2] + d);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int r = r0 + n * 16, tok = r / g.G, i = tile * g.toks + tok;
+        const int64_t h = (int64_t)hk * g.G + (r - tok * g.G);
+        const uint32_t xs[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+        const uint32_t ys[4] = {y[n].x, y[n].y, y[n].z, y[n].w};
+        float s = 0.0f, z = 0.0f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 u = unpack2<BF16>(xs[e]), v = unpack2<BF16>(ys[e]);
           s = fmaf(u.x, v.x, fmaf(u.y, v.y, s));
-          n = fmaf(v.x, v.x, fmaf(v.y, v.y, n));
+          z = fmaf(v.x, v.x, fmaf(v.y, v.y, z));
         }
-      }
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, o);
-        n += __shfl_xor_sync(0xffffffffu, n, o);
-      }
-      most = fmaxf(most, n);
-      if (d == 0) {
-        // added to the scores; a row that sees nothing (or only scores of -inf) gets -inf: its p
-        // is 0
-        float x = -INFINITY;
-        if (live) {
-          x = a.lse[((int64_t)b * g.Hq + h) * g.Lq + i];
-          if (x != -INFINITY) x = (BF16 ? 0.0f : (float)kPShift) - x * kLog2e;
+        for (int o = 8; o > 0; o >>= 1) {
+          s += __shfl_xor_sync(0xffffffffu, s, o);
+          if (!BF16) z += __shfl_xor_sync(0xffffffffu, z, o);
         }
-        stat[r] = x;
-        stat[kTile + r] = live ? -s : 0.0f;
+        most = fmaxf(most, z);
+        if (d == 0) {
+          // added to the scores; a row that sees nothing (or only scores of -inf) gets -inf:
+          // its p is 0
+          float v = -INFINITY;
+          if (live[n]) {
+            v = a.lse[((int64_t)b * g.Hq + h) * g.Lq + i];
+            if (v != -INFINITY) v = (BF16 ? 0.0f : (float)kPShift) - v * kLog2e;
+          }
+          stat[r] = v;
+          stat[kTile + r] = live[n] ? -s : 0.0f;
+        }
       }
     }
   } else {
     const int j0 = (tile - g.qtiles) * kTile;
-    for (int r = sub; r < kTile; r += 16) {
-      float n = 0.0f;
-      if (j0 + r < l.k && d < g.D) {
-        const uint4 y = ptx::ldg_nc_v4(a.val + b * a.v[0] + (int64_t)(j0 + r) * a.v[1] +
-                                       hk * a.v[2] + d);
-        const uint32_t ys[4] = {y.x, y.y, y.z, y.w};
+    uint4 y[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 v = unpack2<BF16>(ys[e]);
-          n = fmaf(v.x, v.x, fmaf(v.y, v.y, n));
-        }
+    for (int n = 0; n < 8; ++n) {
+      const int j = j0 + sub + n * 16;
+      y[n] = make_uint4(0, 0, 0, 0);
+      if (j < l.k && d < g.D)
+        y[n] = ptx::ldg_nc_v4(a.val + b * a.v[0] + (int64_t)j * a.v[1] + hk * a.v[2] + d);
+    }
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const uint32_t ys[4] = {y[n].x, y[n].y, y[n].z, y[n].w};
+      float z = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 v = unpack2<BF16>(ys[e]);
+        z = fmaf(v.x, v.x, fmaf(v.y, v.y, z));
       }
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-      most = fmaxf(most, n);
+      for (int o = 8; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+      most = fmaxf(most, z);
     }
   }
   if (BF16) return;
@@ -278,7 +295,7 @@ __device__ __forceinline__ bool store_ready(uint64_t& bar, uint32_t n, int warp,
 // ------------------------------------------------------------------------------ dq
 
 struct DqItem {
-  int valid, b, hk, split, t0, tile, jb, n;
+  int valid, b, hk, split, t0, tile, jb, n, shift;  // shift: log2 of ds's scale (f16)
   TcLens l;
 };
 
@@ -385,7 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t c = 0, items = 0, tails = 0;
       DqItem it;
       bool stop = false;
-      auto make = [&](int u, DqItem& x) { dq_item(a, u, x); };
+      auto make = [&](int u, DqItem& x) {
+        dq_item(a, u, x);
+        x.shift = !BF16 && x.valid ? grad_shift(a, x.b * g.Hk + x.hk, lane) : 0;
+      };
       for (int k = 0; !stop && sched_make(ctl.sched, k, it, a.counter, lane, abort_flag, make);
            ++k) {
         if (it.n == 0) continue;
@@ -523,17 +543,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint64_t c2 = pair(g.scale * kLog2e, g.scale * kLog2e);
     uint32_t steps = 0, items = 0;
-    int shift = 0, last_bh = -1;
     DqItem it;
     for (int k = 0; sched_take(ctl.sched, k, it, lane, abort_flag); ++k) {
       const int i = it.t0 + tok, bh = it.b * g.Hk + it.hk;
       const int limit = row < g.rows ? key_limit(g, it.l, i) : 0;
       const float* stat = a.stat + ((int64_t)bh * g.qtiles + it.tile) * (2 * kTile);
       const uint64_t nlse = pair(stat[row], stat[row]);
-      if (!BF16 && bh != last_bh) {
-        shift = grad_shift(a, bh, lane);
-        last_bh = bh;
-      }
+      const int shift = it.shift;
       const float gs = BF16 ? 1.0f : pow2i(shift - kPShift), nd = stat[kTile + row] * gs;
       const uint64_t gs2 = pair(gs, gs), nd2 = pair(nd, nd);
       bool stop = false;
@@ -650,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------------------ dk, dv
 
 struct DkvItem {
-  int valid, b, hk, split, tile, ib, n;  // query tiles [ib, ib + n)
+  int valid, b, hk, split, tile, ib, n, shift;  // query tiles [ib, ib + n)
   TcLens l;
 };
 
@@ -783,7 +799,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t c = 0, items = 0, tails = 0;  // c: query tiles loaded so far
       DkvItem it;
       bool stop = false;
-      auto make = [&](int u, DkvItem& x) { dkv_item(a, u, x); };
+      auto make = [&](int u, DkvItem& x) {
+        dkv_item(a, u, x);
+        x.shift = !BF16 && x.valid ? grad_shift(a, x.b * g.Hk + x.hk, lane) : 0;
+      };
       for (int k = 0; !stop && sched_make(ctl.sched, k, it, a.counter, lane, abort_flag, make);
            ++k) {
         if (it.n == 0) continue;
@@ -955,14 +974,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_at = tmem + half * 64 + lanes, dp_at = s_at + 128;
     const uint64_t c2 = pair(g.scale * kLog2e, g.scale * kLog2e);
     uint32_t steps = 0, items = 0;
-    int shift = 0, last_bh = -1;
     DkvItem it;
     for (int k = 0; sched_take(ctl.sched, k, it, lane, abort_flag); ++k) {
       const int j = it.tile * kTile + row, bh = it.b * g.Hk + it.hk;
-      if (!BF16 && bh != last_bh) {
-        shift = grad_shift(a, bh, lane);
-        last_bh = bh;
-      }
+      const int shift = it.shift;
       const float gs = BF16 ? 1.0f : pow2i(shift - kPShift);
       const uint64_t gs2 = pair(gs, gs);
       bool stop = false;
@@ -1164,16 +1179,23 @@ __global__ void __launch_bounds__(256) attn_tc_sum(const JoinArgs a) {
 
 // ------------------------------------------------------------------------------ host side
 
-// Splits of the walked axis when the owned tiles do not fill the SMs: the count with the
-// shortest schedule, an item costing its tiles and about 2 more for its loads and epilogue.
-int split_count(long long base, int tiles, int sms) {
+// Splits of the walked axis: the count with the shortest schedule, in steps of about a
+// microsecond (a tile pair). An item costs its tiles and 2 more for its loads and epilogue; the
+// last round is whole with a fixed order, and costs about a quarter of an item with a running
+// counter (longest items first, `fill` of the tiles needed on average); partial sums of
+// `floats` values a split are written and read once.
+int split_count(long long base, int tiles, double floats, bool dynamic, double fill, int sms) {
   int best = 1;
   double least = 1e30;
   for (int s = 1; s <= tiles && s <= 64; ++s) {
     const int per = (tiles + s - 1) / s;
     if ((tiles + per - 1) / per != s) continue;
-    const double cost =
-        (double)((base * s + sms - 1) / sms) * (per + 2.0) + (s > 1 ? 3.0 + 0.25 * s : 0.0);
+    double cost;
+    if (dynamic && base * s > sms)
+      cost = (double)base * (tiles * fill + 2.0 * s) / sms + per * 0.25;
+    else
+      cost = (double)((base * s + sms - 1) / sms) * (per + 2.0);
+    if (s > 1) cost += 4.0 + s * floats * 8.0 / 6.7e6;
     if (cost < least - 1e-9) {
       least = cost;
       best = s;
@@ -1192,9 +1214,13 @@ BwdPlan bwd_plan(const fconv_attn_desc& d, int sms, const AttnArgs& a) {
   BwdPlan p{};
   p.g = tc_geom(d, a);
   const long long bh = (long long)p.g.B * p.g.Hk;
-  p.dq_splits = split_count(bh * p.g.qtiles, p.g.ktiles, sms);
-  p.dkv_splits = split_count(bh * p.g.ktiles, p.g.qtiles, sms);
   const size_t D = (size_t)p.g.D;
+  const bool dynamic = d.causal || d.has_q_lens || d.has_kv_lens;
+  const double fill = d.causal ? 0.5 : 0.75;
+  p.dq_splits = split_count(bh * p.g.qtiles, p.g.ktiles, (double)p.g.B * p.g.Hq * p.g.Lq * D,
+                            dynamic, fill, sms);
+  p.dkv_splits = split_count(bh * p.g.ktiles, p.g.qtiles, 2.0 * bh * p.g.Lk * D, dynamic, fill,
+                             sms);
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t o = at;

@@ -315,6 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; sched_take(ctl.sched, k, it, lane, abort_flag); ++k) {
       const int n = t ? it.n[1] : it.n[0], t0 = t ? it.t0[1] : it.t0[0], i = t0 + tok;
       const int limit = row < g.rows ? key_limit(g, it.l, i) : 0;
+      // a few query tokens leave most warps without a row
+      const bool warp_live = __any_sync(0xffffffffu, limit > 0);
       float m = -INFINITY, l = 0.0f;
       bool stop = false;
       for (int j = 0; j < n; ++j) {
@@ -324,6 +326,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++steps;
         ptx::tc_fence_after();
+        if (!warp_live) {  // rows that no one reads: their P is whatever lies there
+          ptx::tc_fence_before();
+          if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(&ctl.p_ready[t]));
+          continue;
+        }
         uint32_t s[4][32];
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_fetch32(s_at + q * 32, s[q]);
@@ -521,22 +528,24 @@ __global__ void __launch_bounds__(256) attn_tc_join(const FwdArgs a) {
     a.lse[at] = total == 0.0f ? -INFINITY : (ref + log2f(total)) * kLn2;
 }
 
-// Key splits: the count with the shortest schedule, in key-tile steps. A block's item costs its
-// tiles and about 1.5 steps of loading and writing; the join about 2. With ragged lengths the
-// longest item rather than a full round ends the schedule.
-int split_count(const TcGeom& g, bool ragged, int sms, int pairs) {
+// Key splits: the count with the shortest schedule, in steps of about a microsecond (a key
+// tile). An item costs its tiles and 1.5 more for its loads and epilogue; the last round is
+// whole with a fixed order, and costs about half an item with a running counter; partial sums
+// are written and read once, and joined in about 4.
+int split_count(const TcGeom& g, bool dynamic, int sms, int pairs) {
   const long long base = (long long)g.B * g.Hk * pairs;
+  const double floats = (double)g.B * g.Hq * g.Lq * g.D, fill = g.causal ? 0.5 : 0.75;
   int best = 1;
   double least = 1e30;
   for (int s = 1; s <= g.ktiles && s <= 64; ++s) {
     const int per = (g.ktiles + s - 1) / s;
     if ((g.ktiles + per - 1) / per != s) continue;
     double cost;
-    if (ragged)
-      cost = (double)base * (g.ktiles * 0.75 + 1.5 * s) / sms + per;
+    if (dynamic && base * s > sms)
+      cost = (double)base * (g.ktiles * fill + 1.5 * s) / sms + per * 0.5;
     else
       cost = (double)((base * s + sms - 1) / sms) * (per + 1.5);
-    if (s > 1) cost += 2.0 + (double)s * g.Lq * g.G * g.B * g.Hk / 4.0 / (128.0 * sms);
+    if (s > 1) cost += 4.0 + s * floats * 8.0 / 6.7e6;
     if (cost < least - 1e-9) {
       least = cost;
       best = s;
@@ -549,7 +558,7 @@ FwdArgs fwd_args(const fconv_attn_desc& d, int sms, const AttnArgs& a) {
   FwdArgs f{};
   f.g = tc_geom(d, a);
   f.pairs = (f.g.qtiles + 1) / 2;
-  f.splits = split_count(f.g, d.has_kv_lens != 0, sms, f.pairs);
+  f.splits = split_count(f.g, d.causal || d.has_q_lens || d.has_kv_lens, sms, f.pairs);
   f.per = (f.g.ktiles + f.splits - 1) / f.splits;
   f.items = (int)((long long)f.g.B * f.g.Hk * f.pairs * f.splits);
   for (int i = 0; i < 3; ++i) f.o[i] = d.out_stride[i];
