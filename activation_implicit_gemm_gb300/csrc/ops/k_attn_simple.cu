@@ -18,6 +18,8 @@
 #include "ops_common.cuh"
 #include "ops_internal.h"
 
+#include "../ptx.cuh"
+
 #include <cmath>
 
 namespace fconv {
@@ -50,17 +52,33 @@ __device__ __forceinline__ Lens lens_of(const Geom& g, int64_t b) {
   return l;
 }
 
-// BT rows of (row0..) of one head into shared memory; rows outside [lo, hi) become zeros.
-template <typename T, int BT>
+// BT rows of (row0..) of one head on their way into shared memory; rows outside [lo, hi) become
+// zeros. A warp takes every eighth row. f32 rows of whole 16-byte units are copied
+// asynchronously (VEC; complete after copies_done and a barrier), others go through registers.
+template <typename T, int BT, bool VEC>
 __device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t row_stride,
                                           int64_t row0, int64_t lo, int64_t hi, const Geom& g) {
-  const int pitch = g.Dp + 4;
-  for (int e = threadIdx.x; e < BT * g.Dp; e += 256) {
-    const int r = e / g.Dp, d = e - r * g.Dp;
+  const int pitch = g.Dp + 4, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 0; n < BT / 8; ++n) {
+    const int r = n * 8 + (threadIdx.x >> 5);
     const int64_t row = row0 + r;
-    dst[r * pitch + d] =
-        row >= lo && row < hi && d < g.D ? to_f(src[row * row_stride + d]) : 0.0f;
+    const bool ok = row >= lo && row < hi;
+    const T* p = src + (ok ? row * row_stride : 0);
+    if (VEC) {
+      for (int d = lane * 4; d < g.Dp; d += 128)
+        ptx::cp_async16(ptx::smem_addr(dst + r * pitch + d), p + d, ok ? 16 : 0);
+    } else {
+      for (int d = lane; d < g.Dp; d += 32)
+        dst[r * pitch + d] = ok && d < g.D ? to_f(p[d]) : 0.0f;
+    }
   }
+  ptx::cp_async_commit();
+}
+// At most N later tiles are still on their way.
+template <int N>
+__device__ __forceinline__ void copies_done() {
+  ptx::cp_async_wait<N>();
 }
 
 // acc[r][c] = sum_d a[ty R + r][d] * b[tx + 16 c][d]
@@ -72,6 +90,7 @@ __device__ __forceinline__ void dot_tile(const float* a, const float* b, int Dp,
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int c = 0; c < R; ++c) acc[r][c] = 0.0f;
+#pragma unroll 2
   for (int d = 0; d < Dp; d += 4) {
     float4 x[R], y[R];
 #pragma unroll
@@ -93,36 +112,46 @@ __device__ __forceinline__ void dot_tile(const float* a, const float* b, int Dp,
   }
 }
 
-// acc[r][e] += sum_j p[ty R + r][j] * t[j][tx 4 + 64 e ..]; TR: p is read transposed
+// acc[r][e] += sum_j p[ty R + r][j] * t[j][2 tx + 32 e ..]; TR: p is read transposed
 template <int BT, int NE, bool TR>
 __device__ __forceinline__ void mix_tile(const float* p, const float* t, int Dp, int ty, int tx,
-                                         float4 (&acc)[BT / 16][NE]) {
+                                         float2 (&acc)[BT / 16][NE]) {
   constexpr int R = BT / 16;
   const int pitch = Dp + 4;
-  for (int j = 0; j < BT; ++j) {
-    float w[R];
+  for (int j0 = 0; j0 < BT; j0 += 4) {
+    float w[4][R];
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      w[r] = TR ? p[j * (BT + 4) + ty * R + r] : p[(ty * R + r) * (BT + 4) + j];
+    for (int r = 0; r < R; ++r) {
+      if (!TR) {
+        const float4 v = *reinterpret_cast<const float4*>(p + (ty * R + r) * (BT + 4) + j0);
+        w[0][r] = v.x;
+        w[1][r] = v.y;
+        w[2][r] = v.z;
+        w[3][r] = v.w;
+      } else {
 #pragma unroll
-    for (int e = 0; e < NE; ++e) {
-      const int d = tx * 4 + 64 * e;
-      if (d >= Dp) break;
-      const float4 y = *reinterpret_cast<const float4*>(t + j * pitch + d);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        acc[r][e].x = fmaf(w[r], y.x, acc[r][e].x);
-        acc[r][e].y = fmaf(w[r], y.y, acc[r][e].y);
-        acc[r][e].z = fmaf(w[r], y.z, acc[r][e].z);
-        acc[r][e].w = fmaf(w[r], y.w, acc[r][e].w);
+        for (int i = 0; i < 4; ++i) w[i][r] = p[(j0 + i) * (BT + 4) + ty * R + r];
       }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < NE; ++e) {
+        const int d = tx * 2 + 32 * e;
+        if (d >= Dp) break;
+        const float2 y = *reinterpret_cast<const float2*>(t + (j0 + i) * pitch + d);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          acc[r][e].x = fmaf(w[i][r], y.x, acc[r][e].x);
+          acc[r][e].y = fmaf(w[i][r], y.y, acc[r][e].y);
+        }
+      }
   }
 }
 
 template <typename T, int BT, int NE>
 __device__ __forceinline__ void store_rows(T* dst, int64_t row_stride, int64_t row0, int64_t rows,
-                                           const float4 (&acc)[BT / 16][NE], const float* mul,
+                                           const float2 (&acc)[BT / 16][NE], const float* mul,
                                            int D, int ty, int tx) {
   constexpr int R = BT / 16;
 #pragma unroll
@@ -131,25 +160,23 @@ __device__ __forceinline__ void store_rows(T* dst, int64_t row_stride, int64_t r
     if (row >= rows) continue;
 #pragma unroll
     for (int e = 0; e < NE; ++e) {
-      const int d = tx * 4 + 64 * e;
-      const float v[4] = {acc[r][e].x, acc[r][e].y, acc[r][e].z, acc[r][e].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (d + i < D) dst[row * row_stride + d + i] = from_f<T>(v[i] * mul[r]);
+      const int d = tx * 2 + 32 * e;
+      if (d < D) dst[row * row_stride + d] = from_f<T>(acc[r][e].x * mul[r]);
+      if (d + 1 < D) dst[row * row_stride + d + 1] = from_f<T>(acc[r][e].y * mul[r]);
     }
   }
 }
 
 template <int R, int NE>
-__device__ __forceinline__ void clear(float4 (&acc)[R][NE]) {
+__device__ __forceinline__ void clear(float2 (&acc)[R][NE]) {
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int e = 0; e < NE; ++e) acc[r][e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int e = 0; e < NE; ++e) acc[r][e] = make_float2(0.0f, 0.0f);
 }
 
-template <typename T, int BT, int NE>
-__global__ void __launch_bounds__(256, 1)
+template <typename T, int BT, int NE, bool VEC>
+__global__ void __launch_bounds__(256, NE <= 3 ? 2 : 1)
     attn_simple_forward(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                         T* __restrict__ o, float* __restrict__ lse, const Geom g) {
   constexpr int R = BT / 16;
@@ -173,7 +200,7 @@ __global__ void __launch_bounds__(256, 1)
     const int64_t last = (i0 + BT < L.q ? i0 + BT : L.q) - 1 + L.shift;  // last key seen
     nk = last + 1 < nk ? last + 1 : nk;
   }
-  float4 acc[R][NE];
+  float2 acc[R][NE];
   clear(acc);
   float m[R], l[R];
 #pragma unroll
@@ -184,15 +211,19 @@ __global__ void __launch_bounds__(256, 1)
   const T* qp = q + b * g.q[0] + h * g.q[2];
   const T* kp = k + b * g.k[0] + (h / g.G) * g.k[2];
   const T* vp = v + b * g.v[0] + (h / g.G) * g.v[2];
-  load_tile<T, BT>(qs, qp, g.q[1], i0, 0, L.q, g);
+  load_tile<T, BT, VEC>(qs, qp, g.q[1], i0, 0, L.q, g);
   const float c = g.scale * kLog2e;
+  // the next keys are on their way while this tile's scores are used, the next values while
+  // the next scores are made
+  load_tile<T, BT, VEC>(ks, kp, g.k[1], 0, 0, L.k, g);
+  load_tile<T, BT, VEC>(vs, vp, g.v[1], 0, 0, L.k, g);
   for (int64_t j0 = 0; j0 < nk; j0 += BT) {
-    __syncthreads();
-    load_tile<T, BT>(ks, kp, g.k[1], j0, 0, L.k, g);
-    load_tile<T, BT>(vs, vp, g.v[1], j0, 0, L.k, g);
+    copies_done<1>();
     __syncthreads();
     float s[R][R];
     dot_tile<R>(qs, ks, g.Dp, ty, tx, s);
+    __syncthreads();
+    load_tile<T, BT, VEC>(ks, kp, g.k[1], j0 + BT, 0, L.k, g);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int64_t i = i0 + ty * R + r;
@@ -224,13 +255,15 @@ __global__ void __launch_bounds__(256, 1)
       for (int e = 0; e < NE; ++e) {
         acc[r][e].x *= shrink;
         acc[r][e].y *= shrink;
-        acc[r][e].z *= shrink;
-        acc[r][e].w *= shrink;
       }
     }
-    __syncwarp();  // a warp reads back only the rows of p that it wrote
+    copies_done<1>();
+    __syncthreads();
     mix_tile<BT, NE, false>(ps, vs, g.Dp, ty, tx, acc);
+    __syncthreads();
+    load_tile<T, BT, VEC>(vs, vp, g.v[1], j0 + BT, 0, L.k, g);
   }
+  copies_done<0>();
   float mul[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -284,8 +317,8 @@ __device__ __forceinline__ void grad_tile(float (&s)[R][R], float (&dp)[R][R], i
   }
 }
 
-template <typename T, int BT, int NE>
-__global__ void __launch_bounds__(256, 1)
+template <typename T, int BT, int NE, bool VEC>
+__global__ void __launch_bounds__(256, NE <= 3 ? 2 : 1)
     attn_simple_dq(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                    const T* __restrict__ dout, const float* __restrict__ lse,
                    const float* __restrict__ delta, T* __restrict__ dq, const Geom g) {
@@ -310,38 +343,43 @@ __global__ void __launch_bounds__(256, 1)
     const int64_t last = (i0 + BT < L.q ? i0 + BT : L.q) - 1 + L.shift;
     nk = last + 1 < nk ? last + 1 : nk;
   }
-  float4 acc[R][NE];
+  float2 acc[R][NE];
   clear(acc);
-  load_tile<T, BT>(qs, q + b * g.q[0] + h * g.q[2], g.q[1], i0, 0, L.q, g);
-  load_tile<T, BT>(gs, dout + b * g.g[0] + h * g.g[2], g.g[1], i0, 0, L.q, g);
+  load_tile<T, BT, VEC>(qs, q + b * g.q[0] + h * g.q[2], g.q[1], i0, 0, L.q, g);
+  load_tile<T, BT, VEC>(gs, dout + b * g.g[0] + h * g.g[2], g.g[1], i0, 0, L.q, g);
   const T* kp = k + b * g.k[0] + (h / g.G) * g.k[2];
   const T* vp = v + b * g.v[0] + (h / g.G) * g.v[2];
   const float* lse_row = lse + (b * g.Hq + h) * g.Lq;
   const float* delta_row = delta + (b * g.Hq + h) * g.Lq;
+  load_tile<T, BT, VEC>(vs, vp, g.v[1], 0, 0, L.k, g);
+  load_tile<T, BT, VEC>(ks, kp, g.k[1], 0, 0, L.k, g);
   for (int64_t j0 = 0; j0 < nk; j0 += BT) {
-    __syncthreads();
-    load_tile<T, BT>(ks, kp, g.k[1], j0, 0, L.k, g);
-    load_tile<T, BT>(vs, vp, g.v[1], j0, 0, L.k, g);
+    copies_done<0>();
     __syncthreads();
     float s[R][R], dp[R][R];
     dot_tile<R>(qs, ks, g.Dp, ty, tx, s);
     dot_tile<R>(gs, vs, g.Dp, ty, tx, dp);
+    __syncthreads();
+    load_tile<T, BT, VEC>(vs, vp, g.v[1], j0 + BT, 0, L.k, g);
     grad_tile<R>(s, dp, i0, j0, L, g, lse_row, delta_row, ty, tx);
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int e = 0; e < R; ++e) ps[(ty * R + r) * (BT + 4) + tx + 16 * e] = dp[r][e];
-    __syncwarp();
+    __syncwarp();  // a warp reads back only the rows that it wrote
     mix_tile<BT, NE, false>(ps, ks, g.Dp, ty, tx, acc);
+    __syncthreads();
+    load_tile<T, BT, VEC>(ks, kp, g.k[1], j0 + BT, 0, L.k, g);
   }
+  copies_done<0>();
   float mul[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) mul[r] = g.scale;
   store_rows<T, BT, NE>(dq + b * g.dq[0] + h * g.dq[2], g.dq[1], i0, g.Lq, acc, mul, g.D, ty, tx);
 }
 
-template <typename T, int BT, int NE>
-__global__ void __launch_bounds__(256, 1)
+template <typename T, int BT, int NE, bool VEC>
+__global__ void __launch_bounds__(256, NE <= 3 ? 2 : 1)
     attn_simple_dkv(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                     const T* __restrict__ dout, const float* __restrict__ lse,
                     const float* __restrict__ delta, T* __restrict__ dk, T* __restrict__ dv,
@@ -363,39 +401,57 @@ __global__ void __launch_bounds__(256, 1)
   const int64_t b = u / g.Hk;
   const Lens L = lens_of(g, b);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  float4 ak[R][NE], av[R][NE];
+  float2 ak[R][NE], av[R][NE];
   clear(ak);
   clear(av);
-  load_tile<T, BT>(ks, k + b * g.k[0] + hk * g.k[2], g.k[1], j0, 0, L.k, g);
-  load_tile<T, BT>(vs, v + b * g.v[0] + hk * g.v[2], g.v[1], j0, 0, L.k, g);
+  load_tile<T, BT, VEC>(ks, k + b * g.k[0] + hk * g.k[2], g.k[1], j0, 0, L.k, g);
+  load_tile<T, BT, VEC>(vs, v + b * g.v[0] + hk * g.v[2], g.v[1], j0, 0, L.k, g);
   int64_t first = 0;                                 // first query that sees key j0
   if (g.causal) first = j0 - L.shift;
   if (first < 0) first = 0;
   // queries that see no key at all take no part either (their scores are all hidden)
   const int64_t lead = g.causal && L.shift < 0 ? -L.shift : 0;
   const int64_t end = j0 < L.k ? L.q : 0;
-  for (int h = hk * g.G; h < (hk + 1) * g.G; ++h)
-    for (int64_t i0 = first / BT * BT; i0 < end; i0 += BT) {
-      __syncthreads();
-      load_tile<T, BT>(qs, q + b * g.q[0] + h * g.q[2], g.q[1], i0, lead, L.q, g);
-      load_tile<T, BT>(gs, dout + b * g.g[0] + h * g.g[2], g.g[1], i0, lead, L.q, g);
-      __syncthreads();
-      float s[R][R], dp[R][R];
-      dot_tile<R>(qs, ks, g.Dp, ty, tx, s);
-      dot_tile<R>(gs, vs, g.Dp, ty, tx, dp);
-      const int64_t row = (b * g.Hq + h) * g.Lq;
-      grad_tile<R>(s, dp, i0, j0, L, g, lse + row, delta + row, ty, tx);
+  const int64_t start = first / BT * BT, steps = end > start ? (end - start + BT - 1) / BT : 0;
+  const int64_t all = steps * g.G;
+  auto head_of = [&](int64_t n) { return hk * g.G + (int)(n / steps); };
+  auto row_of = [&](int64_t n) { return start + n % steps * BT; };
+  auto load_q = [&](int64_t n) {
+    if (n < all)
+      load_tile<T, BT, VEC>(qs, q + b * g.q[0] + head_of(n) * g.q[2], g.q[1], row_of(n), lead, L.q,
+                            g);
+  };
+  auto load_g = [&](int64_t n) {
+    if (n < all)
+      load_tile<T, BT, VEC>(gs, dout + b * g.g[0] + head_of(n) * g.g[2], g.g[1], row_of(n), lead,
+                            L.q, g);
+  };
+  load_q(0);
+  load_g(0);
+  for (int64_t n = 0; n < all; ++n) {
+    const int64_t i0 = row_of(n), row = (b * g.Hq + head_of(n)) * g.Lq;
+    copies_done<0>();
+    __syncthreads();
+    float s[R][R], dp[R][R];
+    dot_tile<R>(qs, ks, g.Dp, ty, tx, s);
+    dot_tile<R>(gs, vs, g.Dp, ty, tx, dp);
+    grad_tile<R>(s, dp, i0, j0, L, g, lse + row, delta + row, ty, tx);
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int e = 0; e < R; ++e) {
-          ps[(ty * R + r) * (BT + 4) + tx + 16 * e] = s[r][e];
-          ds[(ty * R + r) * (BT + 4) + tx + 16 * e] = dp[r][e];
-        }
-      __syncthreads();
-      mix_tile<BT, NE, true>(ps, gs, g.Dp, ty, tx, av);
-      mix_tile<BT, NE, true>(ds, qs, g.Dp, ty, tx, ak);
-    }
+      for (int e = 0; e < R; ++e) {
+        ps[(ty * R + r) * (BT + 4) + tx + 16 * e] = s[r][e];
+        ds[(ty * R + r) * (BT + 4) + tx + 16 * e] = dp[r][e];
+      }
+    __syncthreads();
+    mix_tile<BT, NE, true>(ps, gs, g.Dp, ty, tx, av);
+    __syncthreads();
+    load_g(n + 1);
+    mix_tile<BT, NE, true>(ds, qs, g.Dp, ty, tx, ak);
+    __syncthreads();
+    load_q(n + 1);
+  }
+  copies_done<0>();
   float one[R], mul[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -437,12 +493,12 @@ size_t tile_bytes(const Geom& g, int BT, int tiles, int squares) {
   return sizeof(float) * ((size_t)tiles * BT * (g.Dp + 4) + (size_t)squares * BT * (BT + 4));
 }
 
-template <typename T, int BT, int NE>
+template <typename T, int BT, int NE, bool VEC>
 int forward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
   const long long blocks = g.B * g.Hq * ((g.Lq + BT - 1) / BT);
   if (!grid_ok(blocks)) return (int)cudaErrorInvalidValue;
   const size_t smem = tile_bytes(g, BT, 3, 1);
-  auto kern = attn_simple_forward<T, BT, NE>;
+  auto kern = attn_simple_forward<T, BT, NE, VEC>;
   const int e = allow_smem((const void*)kern, smem);
   if (e) return e;
   kern<<<(unsigned)blocks, 256, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v, (T*)a.o,
@@ -450,7 +506,7 @@ int forward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
   return (int)cudaGetLastError();
 }
 
-template <typename T, int BT, int NE>
+template <typename T, int BT, int NE, bool VEC>
 int backward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
   const long long rows = g.B * g.Hq * g.Lq;
   const long long bq = g.B * g.Hq * ((g.Lq + BT - 1) / BT);
@@ -458,7 +514,7 @@ int backward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
   float* delta = (float*)a.ws;
   if (rows > 0) {
     const size_t smem = tile_bytes(g, BT, 4, 1);
-    auto kern = attn_simple_dq<T, BT, NE>;
+    auto kern = attn_simple_dq<T, BT, NE, VEC>;
     const int e = allow_smem((const void*)kern, smem);
     if (e) return e;
     if (!grid_ok((rows + 7) / 8) || !grid_ok(bq)) return (int)cudaErrorInvalidValue;
@@ -469,7 +525,7 @@ int backward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
   }
   if (bk > 0) {
     const size_t smem = tile_bytes(g, BT, 4, 2);
-    auto kern = attn_simple_dkv<T, BT, NE>;
+    auto kern = attn_simple_dkv<T, BT, NE, VEC>;
     const int e = allow_smem((const void*)kern, smem);
     if (e) return e;
     if (!grid_ok(bk)) return (int)cudaErrorInvalidValue;
@@ -477,6 +533,40 @@ int backward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
                                          (const T*)a.dout, a.lse, delta, (T*)a.dk, (T*)a.dv, g);
   }
   return (int)cudaGetLastError();
+}
+
+// Whether every row starts and ends on a 16-byte unit.
+bool whole_rows(const fconv_attn_desc& d, const AttnArgs& a) {
+  int64_t units = d.head_dim;
+  auto add = [&](const int64_t st[3], int64_t len, int64_t heads) {
+    const int64_t ext[3] = {d.batch, len, heads};
+    for (int i = 0; i < 3; ++i)
+      if (ext[i] > 1) units |= st[i];
+  };
+  add(d.q_stride, d.len_q, d.heads_q);
+  add(d.k_stride, d.len_k, d.heads_kv);
+  add(d.v_stride, d.len_k, d.heads_kv);
+  if (a.dout) add(d.dout_stride, d.len_q, d.heads_q);
+  const uintptr_t addr = (uintptr_t)a.q | (uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)a.dout;
+  return units % 4 == 0 && addr % 16 == 0;
+}
+
+template <typename T, int BT, int NE, bool BWD>
+int by_rows(const fconv_attn_desc& d, const Geom& g, const AttnArgs& a, cudaStream_t s) {
+  if constexpr (sizeof(T) == 4) {
+    if (whole_rows(d, a))
+      return BWD ? backward_t<T, BT, NE, true>(g, a, s) : forward_t<T, BT, NE, true>(g, a, s);
+  }
+  return BWD ? backward_t<T, BT, NE, false>(g, a, s) : forward_t<T, BT, NE, false>(g, a, s);
+}
+
+// NE: pairs of columns a thread accumulates, 32 columns apart.
+template <typename T, bool BWD>
+int by_size(const fconv_attn_desc& d, const Geom& g, const AttnArgs& a, cudaStream_t s) {
+  return g.Dp <= 64    ? by_rows<T, 64, 2, BWD>(d, g, a, s)
+         : g.Dp <= 96  ? by_rows<T, 64, 3, BWD>(d, g, a, s)
+         : g.Dp <= 128 ? by_rows<T, 64, 4, BWD>(d, g, a, s)
+                       : by_rows<T, 32, 8, BWD>(d, g, a, s);
 }
 
 }  // namespace
@@ -488,20 +578,14 @@ size_t attn_simple_backward_workspace(const fconv_attn_desc& d) {
 int launch_attn_simple_forward(const fconv_attn_desc& d, const AttnArgs& a, cudaStream_t s) {
   const Geom g = geom_of(d, a);
   if (g.B * g.Lq == 0) return 0;
-#define FCONV_M(T)                                        \
-  return g.Dp <= 64    ? forward_t<T, 64, 1>(g, a, s)     \
-         : g.Dp <= 128 ? forward_t<T, 64, 2>(g, a, s)     \
-                       : forward_t<T, 32, 4>(g, a, s)
+#define FCONV_M(T) return by_size<T, false>(d, g, a, s)
   FCONV_OPS_TYPE(d.dtype, FCONV_M)
 #undef FCONV_M
 }
 
 int launch_attn_simple_backward(const fconv_attn_desc& d, const AttnArgs& a, cudaStream_t s) {
   const Geom g = geom_of(d, a);
-#define FCONV_M(T)                                         \
-  return g.Dp <= 64    ? backward_t<T, 64, 1>(g, a, s)     \
-         : g.Dp <= 128 ? backward_t<T, 64, 2>(g, a, s)     \
-                       : backward_t<T, 32, 4>(g, a, s)
+#define FCONV_M(T) return by_size<T, true>(d, g, a, s)
   FCONV_OPS_TYPE(d.dtype, FCONV_M)
 #undef FCONV_M
 }

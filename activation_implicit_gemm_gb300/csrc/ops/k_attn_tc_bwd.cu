@@ -98,52 +98,51 @@ __global__ void __launch_bounds__(256) attn_tc_delta(const DeltaArgs a) {
   float most = 0.0f;
   if (tile < g.qtiles) {
     float* stat = a.stat + ((int64_t)bh * g.qtiles + tile) * (2 * kTile);
-    // four rows a lane in flight
-    for (int r0 = sub; r0 < kTile; r0 += 64) {
-      uint4 x[4], y[4];
-      bool live[4];
+    // all eight rows of a lane in flight at once, and the lse of its half warp's
+    uint4 x[8], y[8];
+    float lse = -INFINITY;
+    {
+      const int n = threadIdx.x & 15, r = sub + n * 16, tok = r / g.G, i = tile * g.toks + tok;
+      if (n < 8 && r < g.rows && i >= l.lead && i < l.q)
+        lse = a.lse[((int64_t)b * g.Hq + (int64_t)hk * g.G + (r - tok * g.G)) * g.Lq + i];
+    }
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int r = r0 + n * 16, tok = r / g.G, i = tile * g.toks + tok;
-        const int64_t h = (int64_t)hk * g.G + (r - tok * g.G);
-        live[n] = r < g.rows && i >= l.lead && i < l.q;
-        x[n] = y[n] = make_uint4(0, 0, 0, 0);
-        if (live[n] && d < g.D) {
-          x[n] = ptx::ldg_nc_v4(a.out + b * a.o[0] + i * a.o[1] + h * a.o[2] + d);
-          y[n] = ptx::ldg_nc_v4(a.dout + b * a.d[0] + i * a.d[1] + h * a.d[2] + d);
-        }
+    for (int n = 0; n < 8; ++n) {
+      const int r = sub + n * 16, tok = r / g.G, i = tile * g.toks + tok;
+      const int64_t h = (int64_t)hk * g.G + (r - tok * g.G);
+      x[n] = y[n] = make_uint4(0, 0, 0, 0);
+      if (r < g.rows && i >= l.lead && i < l.q && d < g.D) {
+        x[n] = ptx::ldg_nc_v4(a.out + b * a.o[0] + i * a.o[1] + h * a.o[2] + d);
+        y[n] = ptx::ldg_nc_v4(a.dout + b * a.d[0] + i * a.d[1] + h * a.d[2] + d);
+      }
+    }
+    float delta = 0.0f;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+      const uint32_t xs[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+      const uint32_t ys[4] = {y[n].x, y[n].y, y[n].z, y[n].w};
+      float s = 0.0f, z = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 u = unpack2<BF16>(xs[e]), v = unpack2<BF16>(ys[e]);
+        s = fmaf(u.x, v.x, fmaf(u.y, v.y, s));
+        z = fmaf(v.x, v.x, fmaf(v.y, v.y, z));
       }
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int r = r0 + n * 16, tok = r / g.G, i = tile * g.toks + tok;
-        const int64_t h = (int64_t)hk * g.G + (r - tok * g.G);
-        const uint32_t xs[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
-        const uint32_t ys[4] = {y[n].x, y[n].y, y[n].z, y[n].w};
-        float s = 0.0f, z = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 u = unpack2<BF16>(xs[e]), v = unpack2<BF16>(ys[e]);
-          s = fmaf(u.x, v.x, fmaf(u.y, v.y, s));
-          z = fmaf(v.x, v.x, fmaf(v.y, v.y, z));
-        }
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
-          s += __shfl_xor_sync(0xffffffffu, s, o);
-          if (!BF16) z += __shfl_xor_sync(0xffffffffu, z, o);
-        }
-        most = fmaxf(most, z);
-        if (d == 0) {
-          // added to the scores; a row that sees nothing (or only scores of -inf) gets -inf:
-          // its p is 0
-          float v = -INFINITY;
-          if (live[n]) {
-            v = a.lse[((int64_t)b * g.Hq + h) * g.Lq + i];
-            if (v != -INFINITY) v = (BF16 ? 0.0f : (float)kPShift) - v * kLog2e;
-          }
-          stat[r] = v;
-          stat[kTile + r] = live[n] ? -s : 0.0f;
-        }
+      for (int o = 8; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (!BF16) z += __shfl_xor_sync(0xffffffffu, z, o);
       }
+      most = fmaxf(most, z);
+      if ((threadIdx.x & 15) == n) delta = s;
+    }
+    const int n = threadIdx.x & 15;
+    if (n < 8) {
+      // -lse is added to the scores; a row that sees nothing (or only scores of -inf) gets
+      // -inf: its p is 0
+      stat[sub + n * 16] =
+          lse == -INFINITY ? -INFINITY : (BF16 ? 0.0f : (float)kPShift) - lse * kLog2e;
+      stat[kTile + sub + n * 16] = -delta;  // 0 where the row takes no part
     }
   } else {
     const int j0 = (tile - g.qtiles) * kTile;
