@@ -1,5 +1,6 @@
-// Attention forward and backward on CUDA cores (include/fconv_ops.h): every type, head length
-// up to 256 and stride.
+// Attention forward and backward on CUDA cores (include/fconv_ops.h): every type and stride,
+// for head lengths from 129 to 256, whose gradients of a key tile no longer fit the registers of
+// the kernels in k_attn_mma.cu.
 //
 //   s = scale q k^T,  p = softmax(s),  out = p v,  lse = log sum exp s
 // Forward: a block owns BT query rows of one head and walks the keys in tiles of BT with the
@@ -15,71 +16,11 @@
 // length are stored as zeros, so what the tensors hold there never enters a product. Each of
 // the 16 x 16 threads computes an R x R piece of the BT x BT scores (R = BT / 16). Bound: the
 // f32 FMA lanes (4 D FLOPs a pair forward, 14 D backward with the scores made twice).
-#include "ops_common.cuh"
-#include "ops_internal.h"
-
-#include "../ptx.cuh"
-
-#include <cmath>
+#include "attn_geom.cuh"
 
 namespace fconv {
 namespace ops {
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-struct Geom {
-  int64_t B, Lq, Lk;
-  int Hq, Hk, G, D, Dp;  // Dp: D rounded up to 4
-  int64_t q[3], k[3], v[3], o[3], g[3], dq[3], dk[3], dv[3];
-  float scale;
-  int causal;
-  const int32_t* q_lens;
-  const int32_t* kv_lens;
-};
-
-struct Lens {
-  int64_t q, k, shift;  // causal: query i sees keys j <= i + shift
-};
-__device__ __forceinline__ Lens lens_of(const Geom& g, int64_t b) {
-  Lens l;
-  l.q = g.q_lens ? g.q_lens[b] : g.Lq;
-  l.k = g.kv_lens ? g.kv_lens[b] : g.Lk;
-  l.q = l.q < 0 ? 0 : l.q > g.Lq ? g.Lq : l.q;
-  l.k = l.k < 0 ? 0 : l.k > g.Lk ? g.Lk : l.k;
-  l.shift = l.k - l.q;
-  return l;
-}
-
-// BT rows of (row0..) of one head on their way into shared memory; rows outside [lo, hi) become
-// zeros. A warp takes every eighth row. f32 rows of whole 16-byte units are copied
-// asynchronously (VEC; complete after copies_done and a barrier), others go through registers.
-template <typename T, int BT, bool VEC>
-__device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t row_stride,
-                                          int64_t row0, int64_t lo, int64_t hi, const Geom& g) {
-  const int pitch = g.Dp + 4, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int n = 0; n < BT / 8; ++n) {
-    const int r = n * 8 + (threadIdx.x >> 5);
-    const int64_t row = row0 + r;
-    const bool ok = row >= lo && row < hi;
-    const T* p = src + (ok ? row * row_stride : 0);
-    if (VEC) {
-      for (int d = lane * 4; d < g.Dp; d += 128)
-        ptx::cp_async16(ptx::smem_addr(dst + r * pitch + d), p + d, ok ? 16 : 0);
-    } else {
-      for (int d = lane; d < g.Dp; d += 32)
-        dst[r * pitch + d] = ok && d < g.D ? to_f(p[d]) : 0.0f;
-    }
-  }
-  ptx::cp_async_commit();
-}
-// At most N later tiles are still on their way.
-template <int N>
-__device__ __forceinline__ void copies_done() {
-  ptx::cp_async_wait<N>();
-}
 
 // acc[r][c] = sum_d a[ty R + r][d] * b[tx + 16 c][d]
 template <int R>
@@ -175,9 +116,9 @@ __device__ __forceinline__ void clear(float2 (&acc)[R][NE]) {
     for (int e = 0; e < NE; ++e) acc[r][e] = make_float2(0.0f, 0.0f);
 }
 
-template <typename T, int BT, int NE, bool VEC>
-__global__ void __launch_bounds__(256, NE <= 3 ? 2 : 1)
-    attn_simple_forward(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+template <typename T, int BT, int NE>
+__global__ void __launch_bounds__(256, 1)
+    attn_fma_forward(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                         T* __restrict__ o, float* __restrict__ lse, const Geom g) {
   constexpr int R = BT / 16;
   extern __shared__ float4 smem4[];
@@ -211,19 +152,18 @@ __global__ void __launch_bounds__(256, NE <= 3 ? 2 : 1)
   const T* qp = q + b * g.q[0] + h * g.q[2];
   const T* kp = k + b * g.k[0] + (h / g.G) * g.k[2];
   const T* vp = v + b * g.v[0] + (h / g.G) * g.v[2];
-  load_tile<T, BT, VEC>(qs, qp, g.q[1], i0, 0, L.q, g);
+  load_tile<T, BT, 8, false>(qs, qp, g.q[1], i0, 0, L.q, g);
   const float c = g.scale * kLog2e;
   // the next keys are on their way while this tile's scores are used, the next values while
   // the next scores are made
-  load_tile<T, BT, VEC>(ks, kp, g.k[1], 0, 0, L.k, g);
-  load_tile<T, BT, VEC>(vs, vp, g.v[1], 0, 0, L.k, g);
+  load_tile<T, BT, 8, false>(ks, kp, g.k[1], 0, 0, L.k, g);
+  load_tile<T, BT, 8, false>(vs, vp, g.v[1], 0, 0, L.k, g);
   for (int64_t j0 = 0; j0 < nk; j0 += BT) {
-    copies_done<1>();
-    __syncthreads();
+        __syncthreads();
     float s[R][R];
     dot_tile<R>(qs, ks, g.Dp, ty, tx, s);
     __syncthreads();
-    load_tile<T, BT, VEC>(ks, kp, g.k[1], j0 + BT, 0, L.k, g);
+    load_tile<T, BT, 8, false>(ks, kp, g.k[1], j0 + BT, 0, L.k, g);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int64_t i = i0 + ty * R + r;
@@ -257,13 +197,11 @@ __global__ void __launch_bounds__(256, NE <= 3 ? 2 : 1)
         acc[r][e].y *= shrink;
       }
     }
-    copies_done<1>();
-    __syncthreads();
+        __syncthreads();
     mix_tile<BT, NE, false>(ps, vs, g.Dp, ty, tx, acc);
     __syncthreads();
-    load_tile<T, BT, VEC>(vs, vp, g.v[1], j0 + BT, 0, L.k, g);
+    load_tile<T, BT, 8, false>(vs, vp, g.v[1], j0 + BT, 0, L.k, g);
   }
-  copies_done<0>();
   float mul[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -273,25 +211,6 @@ __global__ void __launch_bounds__(256, NE <= 3 ? 2 : 1)
       lse[(b * g.Hq + h) * g.Lq + i] = l[r] == 0.0f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
   }
   store_rows<T, BT, NE>(o + b * g.o[0] + h * g.o[2], g.o[1], i0, g.Lq, acc, mul, g.D, ty, tx);
-}
-
-// delta = sum_d dout out, one warp per (b, h, i); rows past the length get 0.
-template <typename T>
-__global__ void __launch_bounds__(256)
-    attn_simple_delta(const T* __restrict__ o, const T* __restrict__ dout, float* delta,
-                      const Geom g) {
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= g.B * g.Hq * g.Lq) return;
-  const int64_t i = row % g.Lq, bh = row / g.Lq;
-  const int h = (int)(bh % g.Hq);
-  const int64_t b = bh / g.Hq;
-  float s = 0.0f;
-  if (i < lens_of(g, b).q)
-    for (int d = threadIdx.x & 31; d < g.D; d += 32)
-      s = fmaf(to_f(o[b * g.o[0] + i * g.o[1] + h * g.o[2] + d]),
-               to_f(dout[b * g.g[0] + i * g.g[1] + h * g.g[2] + d]), s);
-  s = warp_sum(s);
-  if ((threadIdx.x & 31) == 0) delta[row] = s;
 }
 
 // p and ds of one tile pair (query rows ty R + r, keys tx + 16 e): s holds the scores and dp
@@ -317,9 +236,9 @@ __device__ __forceinline__ void grad_tile(float (&s)[R][R], float (&dp)[R][R], i
   }
 }
 
-template <typename T, int BT, int NE, bool VEC>
-__global__ void __launch_bounds__(256, NE <= 3 ? 2 : 1)
-    attn_simple_dq(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+template <typename T, int BT, int NE>
+__global__ void __launch_bounds__(256, 1)
+    attn_fma_dq(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                    const T* __restrict__ dout, const float* __restrict__ lse,
                    const float* __restrict__ delta, T* __restrict__ dq, const Geom g) {
   constexpr int R = BT / 16;
@@ -345,22 +264,21 @@ __global__ void __launch_bounds__(256, NE <= 3 ? 2 : 1)
   }
   float2 acc[R][NE];
   clear(acc);
-  load_tile<T, BT, VEC>(qs, q + b * g.q[0] + h * g.q[2], g.q[1], i0, 0, L.q, g);
-  load_tile<T, BT, VEC>(gs, dout + b * g.g[0] + h * g.g[2], g.g[1], i0, 0, L.q, g);
+  load_tile<T, BT, 8, false>(qs, q + b * g.q[0] + h * g.q[2], g.q[1], i0, 0, L.q, g);
+  load_tile<T, BT, 8, false>(gs, dout + b * g.g[0] + h * g.g[2], g.g[1], i0, 0, L.q, g);
   const T* kp = k + b * g.k[0] + (h / g.G) * g.k[2];
   const T* vp = v + b * g.v[0] + (h / g.G) * g.v[2];
   const float* lse_row = lse + (b * g.Hq + h) * g.Lq;
   const float* delta_row = delta + (b * g.Hq + h) * g.Lq;
-  load_tile<T, BT, VEC>(vs, vp, g.v[1], 0, 0, L.k, g);
-  load_tile<T, BT, VEC>(ks, kp, g.k[1], 0, 0, L.k, g);
+  load_tile<T, BT, 8, false>(vs, vp, g.v[1], 0, 0, L.k, g);
+  load_tile<T, BT, 8, false>(ks, kp, g.k[1], 0, 0, L.k, g);
   for (int64_t j0 = 0; j0 < nk; j0 += BT) {
-    copies_done<0>();
-    __syncthreads();
+      __syncthreads();
     float s[R][R], dp[R][R];
     dot_tile<R>(qs, ks, g.Dp, ty, tx, s);
     dot_tile<R>(gs, vs, g.Dp, ty, tx, dp);
     __syncthreads();
-    load_tile<T, BT, VEC>(vs, vp, g.v[1], j0 + BT, 0, L.k, g);
+    load_tile<T, BT, 8, false>(vs, vp, g.v[1], j0 + BT, 0, L.k, g);
     grad_tile<R>(s, dp, i0, j0, L, g, lse_row, delta_row, ty, tx);
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -369,18 +287,17 @@ __global__ void __launch_bounds__(256, NE <= 3 ? 2 : 1)
     __syncwarp();  // a warp reads back only the rows that it wrote
     mix_tile<BT, NE, false>(ps, ks, g.Dp, ty, tx, acc);
     __syncthreads();
-    load_tile<T, BT, VEC>(ks, kp, g.k[1], j0 + BT, 0, L.k, g);
+    load_tile<T, BT, 8, false>(ks, kp, g.k[1], j0 + BT, 0, L.k, g);
   }
-  copies_done<0>();
   float mul[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) mul[r] = g.scale;
   store_rows<T, BT, NE>(dq + b * g.dq[0] + h * g.dq[2], g.dq[1], i0, g.Lq, acc, mul, g.D, ty, tx);
 }
 
-template <typename T, int BT, int NE, bool VEC>
-__global__ void __launch_bounds__(256, NE <= 3 ? 2 : 1)
-    attn_simple_dkv(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+template <typename T, int BT, int NE>
+__global__ void __launch_bounds__(256, 1)
+    attn_fma_dkv(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                     const T* __restrict__ dout, const float* __restrict__ lse,
                     const float* __restrict__ delta, T* __restrict__ dk, T* __restrict__ dv,
                     const Geom g) {
@@ -404,8 +321,8 @@ __global__ void __launch_bounds__(256, NE <= 3 ? 2 : 1)
   float2 ak[R][NE], av[R][NE];
   clear(ak);
   clear(av);
-  load_tile<T, BT, VEC>(ks, k + b * g.k[0] + hk * g.k[2], g.k[1], j0, 0, L.k, g);
-  load_tile<T, BT, VEC>(vs, v + b * g.v[0] + hk * g.v[2], g.v[1], j0, 0, L.k, g);
+  load_tile<T, BT, 8, false>(ks, k + b * g.k[0] + hk * g.k[2], g.k[1], j0, 0, L.k, g);
+  load_tile<T, BT, 8, false>(vs, v + b * g.v[0] + hk * g.v[2], g.v[1], j0, 0, L.k, g);
   int64_t first = 0;                                 // first query that sees key j0
   if (g.causal) first = j0 - L.shift;
   if (first < 0) first = 0;
@@ -418,20 +335,19 @@ __global__ void __launch_bounds__(256, NE <= 3 ? 2 : 1)
   auto row_of = [&](int64_t n) { return start + n % steps * BT; };
   auto load_q = [&](int64_t n) {
     if (n < all)
-      load_tile<T, BT, VEC>(qs, q + b * g.q[0] + head_of(n) * g.q[2], g.q[1], row_of(n), lead, L.q,
+      load_tile<T, BT, 8, false>(qs, q + b * g.q[0] + head_of(n) * g.q[2], g.q[1], row_of(n), lead, L.q,
                             g);
   };
   auto load_g = [&](int64_t n) {
     if (n < all)
-      load_tile<T, BT, VEC>(gs, dout + b * g.g[0] + head_of(n) * g.g[2], g.g[1], row_of(n), lead,
+      load_tile<T, BT, 8, false>(gs, dout + b * g.g[0] + head_of(n) * g.g[2], g.g[1], row_of(n), lead,
                             L.q, g);
   };
   load_q(0);
   load_g(0);
   for (int64_t n = 0; n < all; ++n) {
     const int64_t i0 = row_of(n), row = (b * g.Hq + head_of(n)) * g.Lq;
-    copies_done<0>();
-    __syncthreads();
+      __syncthreads();
     float s[R][R], dp[R][R];
     dot_tile<R>(qs, ks, g.Dp, ty, tx, s);
     dot_tile<R>(gs, vs, g.Dp, ty, tx, dp);
@@ -451,7 +367,6 @@ __global__ void __launch_bounds__(256, NE <= 3 ? 2 : 1)
     __syncthreads();
     load_q(n + 1);
   }
-  copies_done<0>();
   float one[R], mul[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -462,43 +377,16 @@ __global__ void __launch_bounds__(256, NE <= 3 ? 2 : 1)
   store_rows<T, BT, NE>(dv + b * g.dv[0] + hk * g.dv[2], g.dv[1], j0, g.Lk, av, one, g.D, ty, tx);
 }
 
-Geom geom_of(const fconv_attn_desc& d, const AttnArgs& a) {
-  Geom g{};
-  g.B = d.batch;
-  g.Lq = d.len_q;
-  g.Lk = d.len_k;
-  g.Hq = (int)d.heads_q;
-  g.Hk = (int)d.heads_kv;
-  g.G = g.Hq / g.Hk;
-  g.D = (int)d.head_dim;
-  g.Dp = (g.D + 3) / 4 * 4;
-  for (int i = 0; i < 3; ++i) {
-    g.q[i] = d.q_stride[i];
-    g.k[i] = d.k_stride[i];
-    g.v[i] = d.v_stride[i];
-    g.o[i] = d.out_stride[i];
-    g.g[i] = d.dout_stride[i];
-    g.dq[i] = d.dq_stride[i];
-    g.dk[i] = d.dk_stride[i];
-    g.dv[i] = d.dv_stride[i];
-  }
-  g.scale = d.scale;
-  g.causal = d.causal;
-  g.q_lens = a.q_lens;
-  g.kv_lens = a.kv_lens;
-  return g;
-}
-
 size_t tile_bytes(const Geom& g, int BT, int tiles, int squares) {
   return sizeof(float) * ((size_t)tiles * BT * (g.Dp + 4) + (size_t)squares * BT * (BT + 4));
 }
 
-template <typename T, int BT, int NE, bool VEC>
+template <typename T, int BT, int NE>
 int forward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
   const long long blocks = g.B * g.Hq * ((g.Lq + BT - 1) / BT);
   if (!grid_ok(blocks)) return (int)cudaErrorInvalidValue;
   const size_t smem = tile_bytes(g, BT, 3, 1);
-  auto kern = attn_simple_forward<T, BT, NE, VEC>;
+  auto kern = attn_fma_forward<T, BT, NE>;
   const int e = allow_smem((const void*)kern, smem);
   if (e) return e;
   kern<<<(unsigned)blocks, 256, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v, (T*)a.o,
@@ -506,7 +394,7 @@ int forward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
   return (int)cudaGetLastError();
 }
 
-template <typename T, int BT, int NE, bool VEC>
+template <typename T, int BT, int NE>
 int backward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
   const long long rows = g.B * g.Hq * g.Lq;
   const long long bq = g.B * g.Hq * ((g.Lq + BT - 1) / BT);
@@ -514,18 +402,18 @@ int backward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
   float* delta = (float*)a.ws;
   if (rows > 0) {
     const size_t smem = tile_bytes(g, BT, 4, 1);
-    auto kern = attn_simple_dq<T, BT, NE, VEC>;
+    auto kern = attn_fma_dq<T, BT, NE>;
     const int e = allow_smem((const void*)kern, smem);
     if (e) return e;
     if (!grid_ok((rows + 7) / 8) || !grid_ok(bq)) return (int)cudaErrorInvalidValue;
-    attn_simple_delta<T><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>((const T*)a.out,
+    attn_delta<T><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>((const T*)a.out,
                                                                     (const T*)a.dout, delta, g);
     kern<<<(unsigned)bq, 256, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v,
                                          (const T*)a.dout, a.lse, delta, (T*)a.dq, g);
   }
   if (bk > 0) {
     const size_t smem = tile_bytes(g, BT, 4, 2);
-    auto kern = attn_simple_dkv<T, BT, NE, VEC>;
+    auto kern = attn_fma_dkv<T, BT, NE>;
     const int e = allow_smem((const void*)kern, smem);
     if (e) return e;
     if (!grid_ok(bk)) return (int)cudaErrorInvalidValue;
@@ -535,57 +423,18 @@ int backward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
   return (int)cudaGetLastError();
 }
 
-// Whether every row starts and ends on a 16-byte unit.
-bool whole_rows(const fconv_attn_desc& d, const AttnArgs& a) {
-  int64_t units = d.head_dim;
-  auto add = [&](const int64_t st[3], int64_t len, int64_t heads) {
-    const int64_t ext[3] = {d.batch, len, heads};
-    for (int i = 0; i < 3; ++i)
-      if (ext[i] > 1) units |= st[i];
-  };
-  add(d.q_stride, d.len_q, d.heads_q);
-  add(d.k_stride, d.len_k, d.heads_kv);
-  add(d.v_stride, d.len_k, d.heads_kv);
-  if (a.dout) add(d.dout_stride, d.len_q, d.heads_q);
-  const uintptr_t addr = (uintptr_t)a.q | (uintptr_t)a.k | (uintptr_t)a.v | (uintptr_t)a.dout;
-  return units % 4 == 0 && addr % 16 == 0;
-}
-
-template <typename T, int BT, int NE, bool BWD>
-int by_rows(const fconv_attn_desc& d, const Geom& g, const AttnArgs& a, cudaStream_t s) {
-  if constexpr (sizeof(T) == 4) {
-    if (whole_rows(d, a))
-      return BWD ? backward_t<T, BT, NE, true>(g, a, s) : forward_t<T, BT, NE, true>(g, a, s);
-  }
-  return BWD ? backward_t<T, BT, NE, false>(g, a, s) : forward_t<T, BT, NE, false>(g, a, s);
-}
-
-// NE: pairs of columns a thread accumulates, 32 columns apart.
-template <typename T, bool BWD>
-int by_size(const fconv_attn_desc& d, const Geom& g, const AttnArgs& a, cudaStream_t s) {
-  return g.Dp <= 64    ? by_rows<T, 64, 2, BWD>(d, g, a, s)
-         : g.Dp <= 96  ? by_rows<T, 64, 3, BWD>(d, g, a, s)
-         : g.Dp <= 128 ? by_rows<T, 64, 4, BWD>(d, g, a, s)
-                       : by_rows<T, 32, 8, BWD>(d, g, a, s);
-}
-
 }  // namespace
 
-size_t attn_simple_backward_workspace(const fconv_attn_desc& d) {
-  return (size_t)d.batch * (size_t)d.heads_q * (size_t)d.len_q * sizeof(float);
-}
-
-int launch_attn_simple_forward(const fconv_attn_desc& d, const AttnArgs& a, cudaStream_t s) {
+int launch_attn_fma_forward(const fconv_attn_desc& d, const AttnArgs& a, cudaStream_t s) {
   const Geom g = geom_of(d, a);
-  if (g.B * g.Lq == 0) return 0;
-#define FCONV_M(T) return by_size<T, false>(d, g, a, s)
+#define FCONV_M(T) return forward_t<T, 32, 8>(g, a, s)
   FCONV_OPS_TYPE(d.dtype, FCONV_M)
 #undef FCONV_M
 }
 
-int launch_attn_simple_backward(const fconv_attn_desc& d, const AttnArgs& a, cudaStream_t s) {
+int launch_attn_fma_backward(const fconv_attn_desc& d, const AttnArgs& a, cudaStream_t s) {
   const Geom g = geom_of(d, a);
-#define FCONV_M(T) return by_size<T, true>(d, g, a, s)
+#define FCONV_M(T) return backward_t<T, 32, 8>(g, a, s)
   FCONV_OPS_TYPE(d.dtype, FCONV_M)
 #undef FCONV_M
 }

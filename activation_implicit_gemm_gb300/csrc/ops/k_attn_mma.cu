@@ -1,0 +1,459 @@
+// Attention forward and backward with f32 operands on the warp-level tensor instructions
+// (include/fconv_ops.h): f32 up to a head length of 128, and f16 and bf16 calls that the tcgen05
+// route does not take (odd head lengths, strides or addresses).
+//
+//   s = scale q k^T,  p = softmax(s),  out = p v,  lse = log sum exp s
+//   p = exp(s - lse),  ds = p (dout v^T - delta),  dv = p^T dout,  dq = scale ds k,
+//   dk = scale ds^T q
+// An f32 value is the sum of hi, its 13 low mantissa bits cleared (a TF32 value), and lo = v - hi
+// (exact); a product is hi hi + hi lo + lo hi in three m16n8k8 TF32 instructions with f32
+// accumulators. What is dropped (lo lo, and lo's bits below TF32) is about 2^-20 of a product.
+// p and ds are split the same way: nothing is rounded to fewer bits.
+//
+// A block of four warps owns 64 rows (of queries, or of keys for dk and dv); each warp has 16 of
+// them and all 64 columns of a score tile in registers. The score accumulator is the next
+// product's A operand as it is: its column pair (2t, 2t + 1) of a lane takes the places of k = t
+// and k = t + 4, and the B operand is read with rows 2t and 2t + 1 to match. Tiles lie in shared
+// memory as f32 with rows of Dp + 4 floats, Dp a multiple of 8: both ways of reading a B operand
+// (along a row, and down two rows) then touch all 32 banks. The next tile is on its way while the
+// current one's products run. As in the other routes every gradient has one writer and no
+// atomics. Bound: the warp-level tensor rate and the shared-memory reads that feed it (one 4-byte
+// operand a lane for every 1.5 instructions).
+#include "attn_geom.cuh"
+
+namespace fconv {
+namespace ops {
+namespace {
+
+constexpr int kRows = 64, kCols = 64, kWarps = 4;
+
+struct Split4 {
+  uint32_t hi[4], lo[4];
+};
+__device__ __forceinline__ void split(float v, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(v) & 0xffffe000u;
+  lo = __float_as_uint(v - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma3(float (&d)[4], const Split4& a, float b0, float b1) {
+  uint32_t h0, l0, h1, l1;
+  split(b0, h0, l0);
+  split(b1, h1, l1);
+  mma_tf32(d, a.lo, h0, h1);
+  mma_tf32(d, a.hi, l0, l1);
+  mma_tf32(d, a.hi, h0, h1);
+}
+
+// s = a b^T over d for 16 rows of a (this warp's) and the 64 rows of b.
+__device__ __forceinline__ void scores(float (&s)[kCols / 8][4], const float* a, const float* b,
+                                       int nd, int pitch, int gr, int t) {
+#pragma unroll
+  for (int n = 0; n < kCols / 8; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
+#pragma unroll 1
+  for (int k = 0; k < nd; ++k) {
+    const float* ap = a + gr * pitch + k * 8 + t;
+    Split4 x;
+    split(ap[0], x.hi[0], x.lo[0]);
+    split(ap[8 * pitch], x.hi[1], x.lo[1]);
+    split(ap[4], x.hi[2], x.lo[2]);
+    split(ap[8 * pitch + 4], x.hi[3], x.lo[3]);
+    const float* bp = b + gr * pitch + k * 8 + t;
+#pragma unroll
+    for (int n = 0; n < kCols / 8; ++n) mma3(s[n], x, bp[n * 8 * pitch], bp[n * 8 * pitch + 4]);
+  }
+}
+
+// acc += p b: p the 16 x 64 accumulator of scores(), b's 64 rows of head_dim.
+template <int NT>
+__device__ __forceinline__ void mix(float (&acc)[NT][4], const float (&p)[kCols / 8][4],
+                                    const float* b, int nd, int pitch, int gr, int t) {
+#pragma unroll
+  for (int k = 0; k < kCols / 8; ++k) {
+    Split4 x;
+    split(p[k][0], x.hi[0], x.lo[0]);
+    split(p[k][2], x.hi[1], x.lo[1]);
+    split(p[k][1], x.hi[2], x.lo[2]);
+    split(p[k][3], x.hi[3], x.lo[3]);
+    const float* bp = b + (k * 8 + 2 * t) * pitch + gr;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (n < nd) mma3(acc[n], x, bp[n * 8], bp[pitch + n * 8]);
+  }
+}
+
+template <typename T, int NT>
+__device__ __forceinline__ void store_rows(T* dst, int64_t row_stride, int64_t row0, int64_t rows,
+                                           const float (&acc)[NT][4], const float (&mul)[2], int D,
+                                           int gr, int t) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t row = row0 + gr + 8 * h;
+    if (row >= rows) continue;
+    T* p = dst + row * row_stride;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int d = n * 8 + 2 * t;
+      if (d < D) p[d] = from_f<T>(acc[n][2 * h] * mul[h]);
+      if (d + 1 < D) p[d + 1] = from_f<T>(acc[n][2 * h + 1] * mul[h]);
+    }
+  }
+}
+template <int NT>
+__device__ __forceinline__ void clear(float (&acc)[NT][4]) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
+}
+
+// Keys [0, end) that the query rows [i0, i0 + kRows) need.
+__device__ __forceinline__ int64_t key_end(const Geom& g, const Lens& L, int64_t i0) {
+  if (i0 >= L.q) return 0;
+  if (!g.causal) return L.k;
+  const int64_t last = (i0 + kRows < L.q ? i0 + kRows : L.q) + L.shift;
+  return last < L.k ? last : L.k;
+}
+
+template <typename T, int NT, bool VEC>
+__global__ void __launch_bounds__(kWarps * 32)
+    attn_mma_forward(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                     T* __restrict__ o, float* __restrict__ lse, const Geom g) {
+  extern __shared__ float4 smem4[];
+  const int pitch = g.Dp + 4, nd = g.Dp / 8;
+  float* qs = reinterpret_cast<float*>(smem4);
+  float* ks = qs + kRows * pitch;
+  float* vs = ks + kCols * pitch;
+  const int64_t tiles = (g.Lq + kRows - 1) / kRows;
+  int64_t u = blockIdx.x;
+  const int64_t i0 = u % tiles * kRows;
+  u /= tiles;
+  const int h = (int)(u % g.Hq);
+  const int64_t b = u / g.Hq;
+  const Lens L = lens_of(g, b);
+  const int warp = threadIdx.x >> 5, gr = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  const int64_t nk = key_end(g, L, i0);
+  const T* kp = k + b * g.k[0] + (h / g.G) * g.k[2];
+  const T* vp = v + b * g.v[0] + (h / g.G) * g.v[2];
+  load_tile<T, kRows, kWarps, VEC>(qs, q + b * g.q[0] + h * g.q[2], g.q[1], i0, 0, L.q, g);
+  load_tile<T, kCols, kWarps, VEC>(ks, kp, g.k[1], 0, 0, L.k, g);
+  load_tile<T, kCols, kWarps, VEC>(vs, vp, g.v[1], 0, 0, L.k, g);
+  float acc[NT][4];
+  clear(acc);
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+  const float c = g.scale * kLog2e;
+  for (int64_t j0 = 0; j0 < nk; j0 += kCols) {
+    ptx::cp_async_wait<1>();  // all but the values
+    __syncthreads();
+    float s[kCols / 8][4];
+    scores(s, qs + warp * 16 * pitch, ks, nd, pitch, gr, t);
+    __syncthreads();
+    load_tile<T, kCols, kWarps, VEC>(ks, kp, g.k[1], j0 + kCols, 0, L.k, g);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int64_t i = i0 + warp * 16 + gr + 8 * r;
+      const int64_t end = i < L.q ? (g.causal && i + L.shift + 1 < L.k ? i + L.shift + 1 : L.k) : 0;
+      float top = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < kCols / 8; ++n)
+#pragma unroll
+        for (int e = 2 * r; e < 2 * r + 2; ++e) {
+          s[n][e] = j0 + n * 8 + 2 * t + (e & 1) < end ? s[n][e] * c : -INFINITY;
+          top = fmaxf(top, s[n][e]);
+        }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float mn = fmaxf(m[r], top);
+      const float ref = mn == -INFINITY ? 0.0f : mn;  // a row without keys so far
+      const float shrink = exp2f(m[r] - ref);
+      float sum = 0.0f;
+#pragma unroll
+      for (int n = 0; n < kCols / 8; ++n)
+#pragma unroll
+        for (int e = 2 * r; e < 2 * r + 2; ++e) {
+          s[n][e] = exp2f(s[n][e] - ref);
+          sum += s[n][e];
+        }
+      l[r] = l[r] * shrink + sum;  // the lane's columns only, joined at the end
+      m[r] = mn;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        acc[n][2 * r] *= shrink;
+        acc[n][2 * r + 1] *= shrink;
+      }
+    }
+    ptx::cp_async_wait<1>();  // all but the next keys
+    __syncthreads();
+    mix<NT>(acc, s, vs, nd, pitch, gr, t);
+    __syncthreads();
+    load_tile<T, kCols, kWarps, VEC>(vs, vp, g.v[1], j0 + kCols, 0, L.k, g);
+  }
+  ptx::cp_async_wait<0>();
+  float mul[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    mul[r] = l[r] == 0.0f ? 0.0f : 1.0f / l[r];
+    const int64_t i = i0 + warp * 16 + gr + 8 * r;
+    if (lse && t == 0 && i < g.Lq)
+      lse[(b * g.Hq + h) * g.Lq + i] = l[r] == 0.0f ? -INFINITY : (m[r] + log2f(l[r])) * kLn2;
+  }
+  store_rows<T, NT>(o + b * g.o[0] + h * g.o[2], g.o[1], i0 + warp * 16, g.Lq, acc, mul, g.D, gr,
+                    t);
+}
+
+template <typename T, int NT, bool VEC>
+__global__ void __launch_bounds__(kWarps * 32)
+    attn_mma_dq(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                const T* __restrict__ dout, const float* __restrict__ lse,
+                const float* __restrict__ delta, T* __restrict__ dq, const Geom g) {
+  extern __shared__ float4 smem4[];
+  const int pitch = g.Dp + 4, nd = g.Dp / 8;
+  float* qs = reinterpret_cast<float*>(smem4);
+  float* gs = qs + kRows * pitch;
+  float* ks = gs + kRows * pitch;
+  float* vs = ks + kCols * pitch;
+  const int64_t tiles = (g.Lq + kRows - 1) / kRows;
+  int64_t u = blockIdx.x;
+  const int64_t i0 = u % tiles * kRows;
+  u /= tiles;
+  const int h = (int)(u % g.Hq);
+  const int64_t b = u / g.Hq;
+  const Lens L = lens_of(g, b);
+  const int warp = threadIdx.x >> 5, gr = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  const int64_t nk = key_end(g, L, i0);
+  const T* kp = k + b * g.k[0] + (h / g.G) * g.k[2];
+  const T* vp = v + b * g.v[0] + (h / g.G) * g.v[2];
+  load_tile<T, kRows, kWarps, VEC>(qs, q + b * g.q[0] + h * g.q[2], g.q[1], i0, 0, L.q, g);
+  load_tile<T, kRows, kWarps, VEC>(gs, dout + b * g.g[0] + h * g.g[2], g.g[1], i0, 0, L.q, g);
+  load_tile<T, kCols, kWarps, VEC>(ks, kp, g.k[1], 0, 0, L.k, g);
+  load_tile<T, kCols, kWarps, VEC>(vs, vp, g.v[1], 0, 0, L.k, g);
+  float acc[NT][4];
+  clear(acc);
+  const float c = g.scale * kLog2e;
+  float ls[2], del[2];
+  int64_t end[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int64_t i = i0 + warp * 16 + gr + 8 * r, at = (b * g.Hq + h) * g.Lq + i;
+    const bool in = i < L.q;
+    ls[r] = in ? lse[at] * kLog2e : 0.0f;
+    del[r] = in ? delta[at] : 0.0f;
+    end[r] = in ? (g.causal && i + L.shift + 1 < L.k ? i + L.shift + 1 : L.k) : 0;
+  }
+  for (int64_t j0 = 0; j0 < nk; j0 += kCols) {
+    ptx::cp_async_wait<0>();
+    __syncthreads();
+    float s[kCols / 8][4], dp[kCols / 8][4];
+    scores(s, qs + warp * 16 * pitch, ks, nd, pitch, gr, t);
+    scores(dp, gs + warp * 16 * pitch, vs, nd, pitch, gr, t);
+    __syncthreads();
+    load_tile<T, kCols, kWarps, VEC>(vs, vp, g.v[1], j0 + kCols, 0, L.k, g);
+#pragma unroll
+    for (int n = 0; n < kCols / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = e >> 1;
+        const bool ok = j0 + n * 8 + 2 * t + (e & 1) < end[r];
+        dp[n][e] = ok ? exp2f(s[n][e] * c - ls[r]) * (dp[n][e] - del[r]) : 0.0f;
+      }
+    mix<NT>(acc, dp, ks, nd, pitch, gr, t);
+    __syncthreads();
+    load_tile<T, kCols, kWarps, VEC>(ks, kp, g.k[1], j0 + kCols, 0, L.k, g);
+  }
+  ptx::cp_async_wait<0>();
+  const float mul[2] = {g.scale, g.scale};
+  store_rows<T, NT>(dq + b * g.dq[0] + h * g.dq[2], g.dq[1], i0 + warp * 16, g.Lq, acc, mul, g.D,
+                    gr, t);
+}
+
+template <typename T, int NT, bool VEC>
+__global__ void __launch_bounds__(kWarps * 32)
+    attn_mma_dkv(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                 const T* __restrict__ dout, const float* __restrict__ lse,
+                 const float* __restrict__ delta, T* __restrict__ dk, T* __restrict__ dv,
+                 const Geom g) {
+  extern __shared__ float4 smem4[];
+  __shared__ float ls[kCols], del[kCols];  // -lse (log2) and delta of the tile's queries
+  const int pitch = g.Dp + 4, nd = g.Dp / 8;
+  float* ks = reinterpret_cast<float*>(smem4);
+  float* vs = ks + kRows * pitch;
+  float* qs = vs + kRows * pitch;
+  float* gs = qs + kCols * pitch;
+  const int64_t tiles = (g.Lk + kRows - 1) / kRows;
+  int64_t u = blockIdx.x;
+  const int64_t j0 = u % tiles * kRows;
+  u /= tiles;
+  const int hk = (int)(u % g.Hk);
+  const int64_t b = u / g.Hk;
+  const Lens L = lens_of(g, b);
+  const int warp = threadIdx.x >> 5, gr = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  load_tile<T, kRows, kWarps, VEC>(ks, k + b * g.k[0] + hk * g.k[2], g.k[1], j0, 0, L.k, g);
+  load_tile<T, kRows, kWarps, VEC>(vs, v + b * g.v[0] + hk * g.v[2], g.v[1], j0, 0, L.k, g);
+  int64_t first = g.causal ? j0 - L.shift : 0;  // first query that sees key j0
+  if (first < 0) first = 0;
+  // queries that see no key at all take no part either (their scores are all hidden)
+  const int64_t lead = g.causal && L.shift < 0 ? -L.shift : 0;
+  const int64_t end = j0 < L.k ? L.q : 0;
+  // the walk: query tiles of every head that shares the keys
+  const int64_t start = first / kCols * kCols;
+  const int64_t steps = end > start ? (end - start + kCols - 1) / kCols : 0, all = steps * g.G;
+  auto head_of = [&](int64_t n) { return hk * g.G + (int)(n / steps); };
+  auto row_of = [&](int64_t n) { return start + n % steps * kCols; };
+  auto load_q = [&](int64_t n) {
+    if (n < all)
+      load_tile<T, kCols, kWarps, VEC>(qs, q + b * g.q[0] + head_of(n) * g.q[2], g.q[1], row_of(n),
+                                       lead, L.q, g);
+  };
+  auto load_g = [&](int64_t n) {
+    if (n < all)
+      load_tile<T, kCols, kWarps, VEC>(gs, dout + b * g.g[0] + head_of(n) * g.g[2], g.g[1],
+                                       row_of(n), lead, L.q, g);
+  };
+  load_q(0);
+  load_g(0);
+  float ak[NT][4], av[NT][4];
+  clear(ak);
+  clear(av);
+  const float c = g.scale * kLog2e;
+  for (int64_t n = 0; n < all; ++n) {
+    const int64_t i0 = row_of(n);
+    if (threadIdx.x < kCols) {
+      const int64_t i = i0 + threadIdx.x, at = (b * g.Hq + head_of(n)) * g.Lq + i;
+      ls[threadIdx.x] = i < L.q ? lse[at] * kLog2e : 0.0f;
+      del[threadIdx.x] = i < L.q ? delta[at] : 0.0f;
+    }
+    ptx::cp_async_wait<0>();
+    __syncthreads();
+    float s[kCols / 8][4];
+    scores(s, ks + warp * 16 * pitch, qs, nd, pitch, gr, t);
+#pragma unroll
+    for (int x = 0; x < kCols / 8; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int col = x * 8 + 2 * t + (e & 1);
+        const int64_t i = i0 + col, j = j0 + warp * 16 + gr + 8 * (e >> 1);
+        const bool ok = i < L.q && j < L.k && (!g.causal || j <= i + L.shift);
+        s[x][e] = ok ? exp2f(s[x][e] * c - ls[col]) : 0.0f;
+      }
+    mix<NT>(av, s, gs, nd, pitch, gr, t);
+    float dp[kCols / 8][4];
+    scores(dp, vs + warp * 16 * pitch, gs, nd, pitch, gr, t);
+#pragma unroll
+    for (int x = 0; x < kCols / 8; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int col = x * 8 + 2 * t + (e & 1);
+        dp[x][e] = s[x][e] == 0.0f ? 0.0f : s[x][e] * (dp[x][e] - del[col]);
+      }
+    __syncthreads();
+    load_g(n + 1);
+    mix<NT>(ak, dp, qs, nd, pitch, gr, t);
+    __syncthreads();
+    load_q(n + 1);
+  }
+  ptx::cp_async_wait<0>();
+  const float one[2] = {1.0f, 1.0f}, mul[2] = {g.scale, g.scale};
+  store_rows<T, NT>(dk + b * g.dk[0] + hk * g.dk[2], g.dk[1], j0 + warp * 16, g.Lk, ak, mul, g.D,
+                    gr, t);
+  store_rows<T, NT>(dv + b * g.dv[0] + hk * g.dv[2], g.dv[1], j0 + warp * 16, g.Lk, av, one, g.D,
+                    gr, t);
+}
+
+size_t tile_bytes(const Geom& g, int tiles) {
+  return sizeof(float) * (size_t)tiles * kRows * (g.Dp + 4);
+}
+
+template <typename T, int NT, bool VEC>
+int forward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
+  const long long blocks = g.B * g.Hq * ((g.Lq + kRows - 1) / kRows);
+  if (!grid_ok(blocks)) return (int)cudaErrorInvalidValue;
+  const size_t smem = tile_bytes(g, 3);
+  auto kern = attn_mma_forward<T, NT, VEC>;
+  const int e = allow_smem((const void*)kern, smem);
+  if (e) return e;
+  kern<<<(unsigned)blocks, kWarps * 32, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v,
+                                                   (T*)a.o, a.lse, g);
+  return (int)cudaGetLastError();
+}
+
+template <typename T, int NT, bool VEC>
+int backward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
+  const long long rows = g.B * g.Hq * g.Lq;
+  const long long bq = g.B * g.Hq * ((g.Lq + kRows - 1) / kRows);
+  const long long bk = g.B * g.Hk * ((g.Lk + kRows - 1) / kRows);
+  float* delta = (float*)a.ws;
+  const size_t smem = tile_bytes(g, 4);
+  if (rows > 0) {
+    auto kern = attn_mma_dq<T, NT, VEC>;
+    const int e = allow_smem((const void*)kern, smem);
+    if (e) return e;
+    if (!grid_ok((rows + 7) / 8) || !grid_ok(bq)) return (int)cudaErrorInvalidValue;
+    attn_delta<T><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>((const T*)a.out, (const T*)a.dout,
+                                                             delta, g);
+    kern<<<(unsigned)bq, kWarps * 32, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v,
+                                                 (const T*)a.dout, a.lse, delta, (T*)a.dq, g);
+  }
+  if (bk > 0) {
+    auto kern = attn_mma_dkv<T, NT, VEC>;
+    const int e = allow_smem((const void*)kern, smem);
+    if (e) return e;
+    if (!grid_ok(bk)) return (int)cudaErrorInvalidValue;
+    kern<<<(unsigned)bk, kWarps * 32, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v,
+                                                 (const T*)a.dout, a.lse, delta, (T*)a.dk,
+                                                 (T*)a.dv, g);
+  }
+  return (int)cudaGetLastError();
+}
+
+// NT: 8-column tiles of head_dim in registers, fitted for f32 rows of whole 16-byte units, the
+// most for the rest.
+template <typename T, bool BWD>
+int by_size(const fconv_attn_desc& d, const Geom& g, const AttnArgs& a, cudaStream_t s) {
+#define FCONV_RUN(NT, VEC) \
+  return BWD ? backward_t<T, NT, VEC>(g, a, s) : forward_t<T, NT, VEC>(g, a, s)
+  if constexpr (sizeof(T) == 4) {
+    if (whole_rows(d, a)) {
+      if (g.Dp <= 64) FCONV_RUN(8, true);
+      if (g.Dp <= 96) FCONV_RUN(12, true);
+      FCONV_RUN(16, true);
+    }
+  }
+  FCONV_RUN(16, false);
+#undef FCONV_RUN
+}
+
+}  // namespace
+
+size_t attn_simple_backward_workspace(const fconv_attn_desc& d) {
+  return (size_t)d.batch * (size_t)d.heads_q * (size_t)d.len_q * sizeof(float);
+}
+
+int launch_attn_simple_forward(const fconv_attn_desc& d, const AttnArgs& a, cudaStream_t s) {
+  const Geom g = geom_of(d, a);
+  if (g.B * g.Lq == 0) return 0;
+  if (g.D > 128) return launch_attn_fma_forward(d, a, s);
+#define FCONV_M(T) return by_size<T, false>(d, g, a, s)
+  FCONV_OPS_TYPE(d.dtype, FCONV_M)
+#undef FCONV_M
+}
+
+int launch_attn_simple_backward(const fconv_attn_desc& d, const AttnArgs& a, cudaStream_t s) {
+  const Geom g = geom_of(d, a);
+  if (g.D > 128) return launch_attn_fma_backward(d, a, s);
+#define FCONV_M(T) return by_size<T, true>(d, g, a, s)
+  FCONV_OPS_TYPE(d.dtype, FCONV_M)
+#undef FCONV_M
+}
+
+}  // namespace ops
+}  // namespace fconv
