@@ -36,19 +36,27 @@ __device__ __forceinline__ void split(float v, uint32_t& hi, uint32_t& lo) {
 }
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma3(float (&d)[4], const Split4& a, float b0, float b1) {
-  uint32_t h0, l0, h1, l1;
-  split(b0, h0, l0);
-  split(b1, h1, l1);
-  mma_tf32(d, a.lo, h0, h1);
-  mma_tf32(d, a.hi, l0, l1);
-  mma_tf32(d, a.hi, h0, h1);
+// d[n] += a b[n] for N independent accumulators, one kind of product after the other: an
+// accumulator is used again only N instructions later.
+template <int N>
+__device__ __forceinline__ void mma3(float (*d)[4], const Split4& a, const float (&b)[N][2]) {
+  uint32_t h[N][2], l[N][2];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    split(b[n][0], h[n][0], l[n][0]);
+    split(b[n][1], h[n][1], l[n][1]);
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) mma_tf32(d[n], a.lo, h[n][0], h[n][1]);
+#pragma unroll
+  for (int n = 0; n < N; ++n) mma_tf32(d[n], a.hi, l[n][0], l[n][1]);
+#pragma unroll
+  for (int n = 0; n < N; ++n) mma_tf32(d[n], a.hi, h[n][0], h[n][1]);
 }
 
 // s = a b^T over d for 16 rows of a (this warp's) and the 64 rows of b.
@@ -58,7 +66,7 @@ __device__ __forceinline__ void scores(float (&s)[kCols / 8][4], const float* a,
   for (int n = 0; n < kCols / 8; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
-#pragma unroll 1
+#pragma unroll 2
   for (int k = 0; k < nd; ++k) {
     const float* ap = a + gr * pitch + k * 8 + t;
     Split4 x;
@@ -68,7 +76,15 @@ __device__ __forceinline__ void scores(float (&s)[kCols / 8][4], const float* a,
     split(ap[8 * pitch + 4], x.hi[3], x.lo[3]);
     const float* bp = b + gr * pitch + k * 8 + t;
 #pragma unroll
-    for (int n = 0; n < kCols / 8; ++n) mma3(s[n], x, bp[n * 8 * pitch], bp[n * 8 * pitch + 4]);
+    for (int n = 0; n < kCols / 8; n += 4) {
+      float y[4][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[i][0] = bp[(n + i) * 8 * pitch];
+        y[i][1] = bp[(n + i) * 8 * pitch + 4];
+      }
+      mma3<4>(s + n, x, y);
+    }
   }
 }
 
@@ -85,8 +101,18 @@ __device__ __forceinline__ void mix(float (&acc)[NT][4], const float (&p)[kCols 
     split(p[k][3], x.hi[3], x.lo[3]);
     const float* bp = b + (k * 8 + 2 * t) * pitch + gr;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-      if (n < nd) mma3(acc[n], x, bp[n * 8], bp[pitch + n * 8]);
+    for (int n = 0; n < NT; n += 4) {
+      if (n >= nd) break;
+      float y[4][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // past the row's end: its own first columns, into accumulators that no one reads
+        const int at = n + i < nd ? (n + i) * 8 : 0;
+        y[i][0] = bp[at];
+        y[i][1] = bp[pitch + at];
+      }
+      mma3<4>(acc + n, x, y);
+    }
   }
 }
 
