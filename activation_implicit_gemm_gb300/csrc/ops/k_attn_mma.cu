@@ -10,8 +10,9 @@
 // accumulators. What is dropped (lo lo, and lo's bits below TF32) is about 2^-20 of a product.
 // p and ds are split the same way: nothing is rounded to fewer bits.
 //
-// A block of four warps owns 64 rows (of queries, or of keys for dk and dv); each warp has 16 of
-// them and all 64 columns of a score tile in registers. The score accumulator is the next
+// A block owns 64 rows (of queries, or of keys for dk and dv), a warp 16 of them and the columns
+// of a score tile in registers: all 64 for dk and dv, half of them in the other kernels, whose
+// accumulators leave room for twice the warps (the halves are joined at the end). The score accumulator is the next
 // product's A operand as it is: its column pair (2t, 2t + 1) of a lane takes the places of k = t
 // and k = t + 4, and the B operand is read with rows 2t and 2t + 1 to match. Tiles lie in shared
 // memory as f32 with rows of Dp + 4 floats, Dp a multiple of 8: both ways of reading a B operand
@@ -25,7 +26,7 @@ namespace fconv {
 namespace ops {
 namespace {
 
-constexpr int kRows = 64, kCols = 64, kWarps = 4;
+constexpr int kRows = 64, kCols = 64;
 
 struct Split4 {
   uint32_t hi[4], lo[4];
@@ -59,11 +60,12 @@ __device__ __forceinline__ void mma3(float (*d)[4], const Split4& a, const float
   for (int n = 0; n < N; ++n) mma_tf32(d[n], a.hi, h[n][0], h[n][1]);
 }
 
-// s = a b^T over d for 16 rows of a (this warp's) and the 64 rows of b.
-__device__ __forceinline__ void scores(float (&s)[kCols / 8][4], const float* a, const float* b,
-                                       int nd, int pitch, int gr, int t) {
+// s = a b^T over d for 16 rows of a (this warp's) and 8 N rows of b.
+template <int N>
+__device__ __forceinline__ void scores(float (&s)[N][4], const float* a, const float* b, int nd,
+                                       int pitch, int gr, int t) {
 #pragma unroll
-  for (int n = 0; n < kCols / 8; ++n)
+  for (int n = 0; n < N; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
 #pragma unroll 2
@@ -76,7 +78,7 @@ __device__ __forceinline__ void scores(float (&s)[kCols / 8][4], const float* a,
     split(ap[8 * pitch + 4], x.hi[3], x.lo[3]);
     const float* bp = b + gr * pitch + k * 8 + t;
 #pragma unroll
-    for (int n = 0; n < kCols / 8; n += 4) {
+    for (int n = 0; n < N; n += 4) {
       float y[4][2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -88,12 +90,13 @@ __device__ __forceinline__ void scores(float (&s)[kCols / 8][4], const float* a,
   }
 }
 
-// acc += p b: p the 16 x 64 accumulator of scores(), b's 64 rows of head_dim.
-template <int NT>
-__device__ __forceinline__ void mix(float (&acc)[NT][4], const float (&p)[kCols / 8][4],
-                                    const float* b, int nd, int pitch, int gr, int t) {
+// acc += p b: p the 16 x 8 N accumulator of scores(), b's 8 N rows of head_dim.
+template <int NT, int N>
+__device__ __forceinline__ void mix(float (&acc)[NT][4], const float (&p)[N][4], const float* b,
+                                    int nd, int pitch, int gr, int t) {
+  constexpr int GS = NT % 3 == 0 ? 3 : 4;
 #pragma unroll
-  for (int k = 0; k < kCols / 8; ++k) {
+  for (int k = 0; k < N; ++k) {
     Split4 x;
     split(p[k][0], x.hi[0], x.lo[0]);
     split(p[k][2], x.hi[1], x.lo[1]);
@@ -101,17 +104,17 @@ __device__ __forceinline__ void mix(float (&acc)[NT][4], const float (&p)[kCols 
     split(p[k][3], x.hi[3], x.lo[3]);
     const float* bp = b + (k * 8 + 2 * t) * pitch + gr;
 #pragma unroll
-    for (int n = 0; n < NT; n += 4) {
+    for (int n = 0; n < NT; n += GS) {
       if (n >= nd) break;
-      float y[4][2];
+      float y[GS][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < GS; ++i) {
         // past the row's end: its own first columns, into accumulators that no one reads
         const int at = n + i < nd ? (n + i) * 8 : 0;
         y[i][0] = bp[at];
         y[i][1] = bp[pitch + at];
       }
-      mma3<4>(acc + n, x, y);
+      mma3<GS>(acc + n, x, y);
     }
   }
 }
@@ -150,7 +153,7 @@ __device__ __forceinline__ int64_t key_end(const Geom& g, const Lens& L, int64_t
 }
 
 template <typename T, int NT, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(256, 2)
     attn_mma_forward(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                      T* __restrict__ o, float* __restrict__ lse, const Geom g) {
   extern __shared__ float4 smem4[];
@@ -165,13 +168,13 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int h = (int)(u % g.Hq);
   const int64_t b = u / g.Hq;
   const Lens L = lens_of(g, b);
-  const int warp = threadIdx.x >> 5, gr = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  const int warp = (threadIdx.x >> 5) & 3, half = threadIdx.x >> 7, gr = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
   const int64_t nk = key_end(g, L, i0);
   const T* kp = k + b * g.k[0] + (h / g.G) * g.k[2];
   const T* vp = v + b * g.v[0] + (h / g.G) * g.v[2];
-  load_tile<T, kRows, kWarps, VEC>(qs, q + b * g.q[0] + h * g.q[2], g.q[1], i0, 0, L.q, g);
-  load_tile<T, kCols, kWarps, VEC>(ks, kp, g.k[1], 0, 0, L.k, g);
-  load_tile<T, kCols, kWarps, VEC>(vs, vp, g.v[1], 0, 0, L.k, g);
+  load_tile<T, kRows, 8, VEC>(qs, q + b * g.q[0] + h * g.q[2], g.q[1], i0, 0, L.q, g);
+  load_tile<T, kCols, 8, VEC>(ks, kp, g.k[1], 0, 0, L.k, g);
+  load_tile<T, kCols, 8, VEC>(vs, vp, g.v[1], 0, 0, L.k, g);
   float acc[NT][4];
   clear(acc);
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
@@ -179,20 +182,20 @@ __global__ void __launch_bounds__(kWarps * 32)
   for (int64_t j0 = 0; j0 < nk; j0 += kCols) {
     ptx::cp_async_wait<1>();  // all but the values
     __syncthreads();
-    float s[kCols / 8][4];
-    scores(s, qs + warp * 16 * pitch, ks, nd, pitch, gr, t);
+    float s[kCols / 16][4];
+    scores(s, qs + warp * 16 * pitch, ks + half * 32 * pitch, nd, pitch, gr, t);
     __syncthreads();
-    load_tile<T, kCols, kWarps, VEC>(ks, kp, g.k[1], j0 + kCols, 0, L.k, g);
+    load_tile<T, kCols, 8, VEC>(ks, kp, g.k[1], j0 + kCols, 0, L.k, g);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int64_t i = i0 + warp * 16 + gr + 8 * r;
       const int64_t end = i < L.q ? (g.causal && i + L.shift + 1 < L.k ? i + L.shift + 1 : L.k) : 0;
       float top = -INFINITY;
 #pragma unroll
-      for (int n = 0; n < kCols / 8; ++n)
+      for (int n = 0; n < kCols / 16; ++n)
 #pragma unroll
         for (int e = 2 * r; e < 2 * r + 2; ++e) {
-          s[n][e] = j0 + n * 8 + 2 * t + (e & 1) < end ? s[n][e] * c : -INFINITY;
+          s[n][e] = j0 + half * 32 + n * 8 + 2 * t + (e & 1) < end ? s[n][e] * c : -INFINITY;
           top = fmaxf(top, s[n][e]);
         }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -202,7 +205,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       const float shrink = exp2f(m[r] - ref);
       float sum = 0.0f;
 #pragma unroll
-      for (int n = 0; n < kCols / 8; ++n)
+      for (int n = 0; n < kCols / 16; ++n)
 #pragma unroll
         for (int e = 2 * r; e < 2 * r + 2; ++e) {
           s[n][e] = exp2f(s[n][e] - ref);
@@ -218,14 +221,41 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
     ptx::cp_async_wait<1>();  // all but the next keys
     __syncthreads();
-    mix<NT>(acc, s, vs, nd, pitch, gr, t);
+    mix(acc, s, vs + half * 32 * pitch, nd, pitch, gr, t);
     __syncthreads();
-    load_tile<T, kCols, kWarps, VEC>(vs, vp, g.v[1], j0 + kCols, 0, L.k, g);
+    load_tile<T, kCols, 8, VEC>(vs, vp, g.v[1], j0 + kCols, 0, L.k, g);
   }
   ptx::cp_async_wait<0>();
+  __syncthreads();
+  // the second half of the columns' warps hand theirs over
+  float* box = reinterpret_cast<float*>(smem4) + (threadIdx.x & 127);
+  if (half) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      box[r * 128] = m[r];
+      box[(2 + r) * 128] = l[r];
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (n < nd)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) box[(4 + n * 4 + e) * 128] = acc[n][e];
+  }
+  __syncthreads();
+  if (half) return;
   float mul[2];
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
+    const float mo = box[r * 128], mn = fmaxf(m[r], mo), ref = mn == -INFINITY ? 0.0f : mn;
+    const float f = exp2f(m[r] - ref), fo = exp2f(mo - ref);
+    l[r] = l[r] * f + box[(2 + r) * 128] * fo;
+    m[r] = mn;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (n < nd)
+#pragma unroll
+        for (int e = 2 * r; e < 2 * r + 2; ++e)
+          acc[n][e] = acc[n][e] * f + box[(4 + n * 4 + e) * 128] * fo;
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
     mul[r] = l[r] == 0.0f ? 0.0f : 1.0f / l[r];
@@ -238,7 +268,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 }
 
 template <typename T, int NT, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(256, 2)
     attn_mma_dq(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                 const T* __restrict__ dout, const float* __restrict__ lse,
                 const float* __restrict__ delta, T* __restrict__ dq, const Geom g) {
@@ -255,14 +285,14 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int h = (int)(u % g.Hq);
   const int64_t b = u / g.Hq;
   const Lens L = lens_of(g, b);
-  const int warp = threadIdx.x >> 5, gr = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  const int warp = (threadIdx.x >> 5) & 3, half = threadIdx.x >> 7, gr = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
   const int64_t nk = key_end(g, L, i0);
   const T* kp = k + b * g.k[0] + (h / g.G) * g.k[2];
   const T* vp = v + b * g.v[0] + (h / g.G) * g.v[2];
-  load_tile<T, kRows, kWarps, VEC>(qs, q + b * g.q[0] + h * g.q[2], g.q[1], i0, 0, L.q, g);
-  load_tile<T, kRows, kWarps, VEC>(gs, dout + b * g.g[0] + h * g.g[2], g.g[1], i0, 0, L.q, g);
-  load_tile<T, kCols, kWarps, VEC>(ks, kp, g.k[1], 0, 0, L.k, g);
-  load_tile<T, kCols, kWarps, VEC>(vs, vp, g.v[1], 0, 0, L.k, g);
+  load_tile<T, kRows, 8, VEC>(qs, q + b * g.q[0] + h * g.q[2], g.q[1], i0, 0, L.q, g);
+  load_tile<T, kRows, 8, VEC>(gs, dout + b * g.g[0] + h * g.g[2], g.g[1], i0, 0, L.q, g);
+  load_tile<T, kCols, 8, VEC>(ks, kp, g.k[1], 0, 0, L.k, g);
+  load_tile<T, kCols, 8, VEC>(vs, vp, g.v[1], 0, 0, L.k, g);
   float acc[NT][4];
   clear(acc);
   const float c = g.scale * kLog2e;
@@ -279,31 +309,45 @@ __global__ void __launch_bounds__(kWarps * 32)
   for (int64_t j0 = 0; j0 < nk; j0 += kCols) {
     ptx::cp_async_wait<0>();
     __syncthreads();
-    float s[kCols / 8][4], dp[kCols / 8][4];
-    scores(s, qs + warp * 16 * pitch, ks, nd, pitch, gr, t);
-    scores(dp, gs + warp * 16 * pitch, vs, nd, pitch, gr, t);
+    float s[kCols / 16][4], dp[kCols / 16][4];
+    scores(s, qs + warp * 16 * pitch, ks + half * 32 * pitch, nd, pitch, gr, t);
+    scores(dp, gs + warp * 16 * pitch, vs + half * 32 * pitch, nd, pitch, gr, t);
     __syncthreads();
-    load_tile<T, kCols, kWarps, VEC>(vs, vp, g.v[1], j0 + kCols, 0, L.k, g);
+    load_tile<T, kCols, 8, VEC>(vs, vp, g.v[1], j0 + kCols, 0, L.k, g);
 #pragma unroll
-    for (int n = 0; n < kCols / 8; ++n)
+    for (int n = 0; n < kCols / 16; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = e >> 1;
-        const bool ok = j0 + n * 8 + 2 * t + (e & 1) < end[r];
+        const bool ok = j0 + half * 32 + n * 8 + 2 * t + (e & 1) < end[r];
         dp[n][e] = ok ? exp2f(s[n][e] * c - ls[r]) * (dp[n][e] - del[r]) : 0.0f;
       }
-    mix<NT>(acc, dp, ks, nd, pitch, gr, t);
+    mix(acc, dp, ks + half * 32 * pitch, nd, pitch, gr, t);
     __syncthreads();
-    load_tile<T, kCols, kWarps, VEC>(ks, kp, g.k[1], j0 + kCols, 0, L.k, g);
+    load_tile<T, kCols, 8, VEC>(ks, kp, g.k[1], j0 + kCols, 0, L.k, g);
   }
   ptx::cp_async_wait<0>();
+  __syncthreads();
+  float* box = reinterpret_cast<float*>(smem4) + (threadIdx.x & 127);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    if (n < nd && half)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) box[(n * 4 + e) * 128] = acc[n][e];
+  __syncthreads();
+  if (half) return;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    if (n < nd)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[n][e] += box[(n * 4 + e) * 128];
   const float mul[2] = {g.scale, g.scale};
   store_rows<T, NT>(dq + b * g.dq[0] + h * g.dq[2], g.dq[1], i0 + warp * 16, g.Lq, acc, mul, g.D,
                     gr, t);
 }
 
 template <typename T, int NT, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(128)
     attn_mma_dkv(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                  const T* __restrict__ dout, const float* __restrict__ lse,
                  const float* __restrict__ delta, T* __restrict__ dk, T* __restrict__ dv,
@@ -323,8 +367,8 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int64_t b = u / g.Hk;
   const Lens L = lens_of(g, b);
   const int warp = threadIdx.x >> 5, gr = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
-  load_tile<T, kRows, kWarps, VEC>(ks, k + b * g.k[0] + hk * g.k[2], g.k[1], j0, 0, L.k, g);
-  load_tile<T, kRows, kWarps, VEC>(vs, v + b * g.v[0] + hk * g.v[2], g.v[1], j0, 0, L.k, g);
+  load_tile<T, kRows, 4, VEC>(ks, k + b * g.k[0] + hk * g.k[2], g.k[1], j0, 0, L.k, g);
+  load_tile<T, kRows, 4, VEC>(vs, v + b * g.v[0] + hk * g.v[2], g.v[1], j0, 0, L.k, g);
   int64_t first = g.causal ? j0 - L.shift : 0;  // first query that sees key j0
   if (first < 0) first = 0;
   // queries that see no key at all take no part either (their scores are all hidden)
@@ -337,12 +381,12 @@ __global__ void __launch_bounds__(kWarps * 32)
   auto row_of = [&](int64_t n) { return start + n % steps * kCols; };
   auto load_q = [&](int64_t n) {
     if (n < all)
-      load_tile<T, kCols, kWarps, VEC>(qs, q + b * g.q[0] + head_of(n) * g.q[2], g.q[1], row_of(n),
+      load_tile<T, kCols, 4, VEC>(qs, q + b * g.q[0] + head_of(n) * g.q[2], g.q[1], row_of(n),
                                        lead, L.q, g);
   };
   auto load_g = [&](int64_t n) {
     if (n < all)
-      load_tile<T, kCols, kWarps, VEC>(gs, dout + b * g.g[0] + head_of(n) * g.g[2], g.g[1],
+      load_tile<T, kCols, 4, VEC>(gs, dout + b * g.g[0] + head_of(n) * g.g[2], g.g[1],
                                        row_of(n), lead, L.q, g);
   };
   load_q(0);
@@ -371,7 +415,7 @@ __global__ void __launch_bounds__(kWarps * 32)
         const bool ok = i < L.q && j < L.k && (!g.causal || j <= i + L.shift);
         s[x][e] = ok ? exp2f(s[x][e] * c - ls[col]) : 0.0f;
       }
-    mix<NT>(av, s, gs, nd, pitch, gr, t);
+    mix(av, s, gs, nd, pitch, gr, t);
     float dp[kCols / 8][4];
     scores(dp, vs + warp * 16 * pitch, gs, nd, pitch, gr, t);
 #pragma unroll
@@ -383,7 +427,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       }
     __syncthreads();
     load_g(n + 1);
-    mix<NT>(ak, dp, qs, nd, pitch, gr, t);
+    mix(ak, dp, qs, nd, pitch, gr, t);
     __syncthreads();
     load_q(n + 1);
   }
@@ -407,7 +451,7 @@ int forward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
   auto kern = attn_mma_forward<T, NT, VEC>;
   const int e = allow_smem((const void*)kern, smem);
   if (e) return e;
-  kern<<<(unsigned)blocks, kWarps * 32, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v,
+  kern<<<(unsigned)blocks, 256, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v,
                                                    (T*)a.o, a.lse, g);
   return (int)cudaGetLastError();
 }
@@ -426,7 +470,7 @@ int backward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
     if (!grid_ok((rows + 7) / 8) || !grid_ok(bq)) return (int)cudaErrorInvalidValue;
     attn_delta<T><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>((const T*)a.out, (const T*)a.dout,
                                                              delta, g);
-    kern<<<(unsigned)bq, kWarps * 32, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v,
+    kern<<<(unsigned)bq, 256, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v,
                                                  (const T*)a.dout, a.lse, delta, (T*)a.dq, g);
   }
   if (bk > 0) {
@@ -434,7 +478,7 @@ int backward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
     const int e = allow_smem((const void*)kern, smem);
     if (e) return e;
     if (!grid_ok(bk)) return (int)cudaErrorInvalidValue;
-    kern<<<(unsigned)bk, kWarps * 32, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v,
+    kern<<<(unsigned)bk, 128, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v,
                                                  (const T*)a.dout, a.lse, delta, (T*)a.dk,
                                                  (T*)a.dv, g);
   }
