@@ -18,7 +18,10 @@
 // TMEM: S0 S1 O0 O1, 128 columns each. Shared memory: the Q tiles (of the next item too for
 // head_dim up to 64), a ring of K and V tiles, a box of output a tile.
 // When there are fewer blocks than SMs the keys are split; partial O (normalised, f32) and the
-// log2 of their sums go to the workspace and attn_tc_join adds them in order.
+// log2 of their sums go to the workspace and attn_tc_join adds them in order. With few queries
+// (one tile a key head) a split's even key tiles go through S0, P0, O0 and its odd ones through
+// S1, P1, O1 with the same Q (FOLD), two chains of products and exponentials instead of one, each
+// with a partial sum of its own.
 //
 // Bound: tensor (4 D FLOPs a pair) for long queries, HBM (K and V) for few.
 #include "attn_tc.cuh"
@@ -40,7 +43,8 @@ static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "within the laun
 
 struct FwdArgs {
   TcGeom g;
-  int pairs, splits, per;  // query tile pairs; key splits and key tiles of a split
+  int pairs, splits, per;  // query tile pairs (FOLD: tiles); key splits, key tiles of a split
+  int fold, parts;         // parts: partial sums of a row
   int items;
   int* counter;
   int64_t o[3];
@@ -78,8 +82,9 @@ __device__ __forceinline__ void fwd_item(const FwdArgs& a, int u, FwdItem& it) {
   it.jb = it.split * a.per;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    it.t0[t] = (2 * pair + t) * a.g.toks;
+    it.t0[t] = (a.fold ? pair : 2 * pair + t) * a.g.toks;
     it.n[t] = max(min(key_tiles(a.g, it.l, it.t0[t]) - it.jb, a.per), 0);
+    if (a.fold) it.n[t] = (it.n[t] + 1 - t) / 2;  // tiles jb + t, jb + t + 2, ...
   }
 }
 
@@ -91,11 +96,13 @@ struct FwdPlan {
   static constexpr uint32_t ring_at = 2 * own * tile_bytes;
   static constexpr uint32_t out_at = ring_at + slots * tile_bytes;  // a box of 64 columns a tile
   static constexpr uint32_t ctl_at = out_at + 2 * kHalfBytes;
+  // FOLD: one Q tile, and the rest of the space a ring
+  static constexpr int fold_slots = (ctl_at - tile_bytes) / tile_bytes;
 };
 
 template <int H>
 struct FwdCtl {
-  uint64_t full[FwdPlan<H>::slots], empty[FwdPlan<H>::slots];
+  uint64_t full[FwdPlan<H>::fold_slots], empty[FwdPlan<H>::fold_slots];
   uint64_t q_full[2], q_empty[2], tail, drain;
   uint64_t s_full[2], p_ready[2], o_done[2], out_ready[2], out_free[2];
   Sched<FwdItem> sched;
@@ -108,7 +115,7 @@ constexpr uint32_t fwd_smem() {
 }
 static_assert(fwd_smem<2>() <= 232448 && fwd_smem<1>() <= 232448, "one block's shared memory");
 
-template <bool BF16, int H>
+template <bool BF16, int H, bool FOLD>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_forward(const FwdArgs a, const __grid_constant__ CUtensorMap tm_q,
                     const __grid_constant__ CUtensorMap tm_k,
@@ -121,11 +128,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const TcGeom& g = a.g;
   const int tid = threadIdx.x, warp = uni(tid >> 5), lane = tid & 31;
   const uint32_t own = ptx::smem_addr(dsmem);
-  const uint32_t ring = own + Plan::ring_at;
+  constexpr int kOwn = FOLD ? 1 : Plan::own, kSlots = FOLD ? Plan::fold_slots : Plan::slots;
+  const uint32_t ring = own + (FOLD ? Plan::tile_bytes : Plan::ring_at);
   volatile int* abort_flag = &ctl.abort_flag;
 
   if (tid == 0) {
-    for (int i = 0; i < Plan::slots; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
       ptx::mbar_init(ptx::smem_addr(&ctl.full[i]), 1);
       ptx::mbar_init(ptx::smem_addr(&ctl.empty[i]), 1);
     }
@@ -172,31 +180,40 @@ __global__ void __launch_bounds__(kThreads, 1)
            ++k) {
         const int n = max(it.n[0], it.n[1]);
         if (n == 0) continue;
-        const uint32_t ob = q_items % Plan::own;
-        if (!wait_bar(ptx::smem_addr(&ctl.q_empty[ob]), ((q_items / Plan::own) & 1) ^ 1,
+        const uint32_t ob = q_items % kOwn;
+        if (!wait_bar(ptx::smem_addr(&ctl.q_empty[ob]), ((q_items / kOwn) & 1) ^ 1,
                       abort_flag))
           break;
         ++q_items;
         if (lane == 0) {
           const uint32_t bar = ptx::smem_addr(&ctl.q_full[ob]);
           const uint32_t box = (uint32_t)g.rows * 128;
-          ptx::mbar_arrive_expect_tx(bar, ((it.n[0] > 0) + (it.n[1] > 0)) * H * box);
+          const int tiles = FOLD ? 1 : (it.n[0] > 0) + (it.n[1] > 0);
+          ptx::mbar_arrive_expect_tx(bar, tiles * H * box);
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < (FOLD ? 1 : 2); ++t)
             if (it.n[t] > 0)
               for (int h = 0; h < H; ++h)
                 tma_load_4d(own + (ob * 2 + t) * Plan::tile_bytes + h * kHalfBytes, &tm_q, h * 64,
                             it.hk * g.G, it.t0[t], it.b * g.qb, bar);
         }
-        for (int j = 0; j < 2 * n; ++j, ++c) {
-          const uint32_t s = c % Plan::slots, ph = (c / Plan::slots) & 1;
+        // K, V of each step; FOLD: K, K, V, V of its two tiles (the last step may have one)
+        const int loads = FOLD ? 2 * (it.n[0] + it.n[1]) : 2 * n;
+        for (int j = 0; j < loads; ++j, ++c) {
+          const uint32_t s = c % kSlots, ph = (c / kSlots) & 1;
           if (!wait_bar(ptx::smem_addr(&ctl.empty[s]), ph ^ 1, abort_flag)) {
             stop = true;
             break;
           }
-          const int key0 = (it.jb + (j >> 1)) * kTile;
+          int tile = j >> 1;
+          bool is_v = j & 1;
+          if (FOLD) {
+            const bool two = (j >> 2) < it.n[1];
+            is_v = two ? j & 2 : j & 1;
+            tile = 2 * (j >> 2) + (two ? j & 1 : 0);
+          }
+          const int key0 = (it.jb + tile) * kTile;
           const uint32_t dst = ring + s * Plan::tile_bytes;
-          const bool is_v = j & 1;
           // rows of V past the sequence would meet P = 0: a NaN there must not reach the product
           const bool ragged = is_v && key0 + kTile > it.l.k && it.l.k < g.Lk;
           const uint32_t full = ptx::smem_addr(&ctl.full[s]);
@@ -223,10 +240,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (*abort_flag) {
         // loads in flight land before the block's shared memory is given back
-        for (uint32_t i = c > Plan::slots ? c - Plan::slots : 0; i < c; ++i)
-          drain_bar(ptx::smem_addr(&ctl.full[i % Plan::slots]), (i / Plan::slots) & 1);
-        for (uint32_t i = q_items > Plan::own ? q_items - Plan::own : 0; i < q_items; ++i)
-          drain_bar(ptx::smem_addr(&ctl.q_full[i % Plan::own]), (i / Plan::own) & 1);
+        for (uint32_t i = c > kSlots ? c - kSlots : 0; i < c; ++i)
+          drain_bar(ptx::smem_addr(&ctl.full[i % kSlots]), (i / kSlots) & 1);
+        for (uint32_t i = q_items > kOwn ? q_items - kOwn : 0; i < q_items; ++i)
+          drain_bar(ptx::smem_addr(&ctl.q_full[i % kOwn]), (i / kOwn) & 1);
       }
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------------- MMA issue
@@ -246,10 +263,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; !stop && sched_take(ctl.sched, k, it, lane, abort_flag); ++k) {
         const int n0 = uni(it.n[0]), n1 = uni(it.n[1]), n = max(n0, n1);
         if (n == 0) continue;
-        const uint32_t ob = q_items % Plan::own;
+        const uint32_t ob = q_items % kOwn;
         const uint32_t q0 = own + ob * 2 * Plan::tile_bytes;
         auto scores = [&](int t, uint32_t ktile) {
-          const uint32_t q = desc_k(q0 + t * Plan::tile_bytes), kt = desc_k(ktile);
+          const uint32_t q = desc_k(q0 + (FOLD ? 0 : t) * Plan::tile_bytes), kt = desc_k(ktile);
           if (leader) {
 #pragma unroll
             for (int d = 0; d < 4 * H; ++d)
@@ -257,18 +274,64 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           commit(ctl.s_full[t]);
         };
-        if (!wait(ctl.q_full[ob], (q_items / Plan::own) & 1)) break;
+        if (!wait(ctl.q_full[ob], (q_items / kOwn) & 1)) break;
         ++q_items;
-        if (!wait(ctl.full[c % Plan::slots], (c / Plan::slots) & 1)) break;
+        if (FOLD) {
+          auto wait_slot = [&](uint32_t i) { return wait(ctl.full[i % kSlots], (i / kSlots) & 1); };
+          auto slot = [&](uint32_t i) { return ring + i % kSlots * Plan::tile_bytes; };
+          // scores of step j, whose loads start at `at`, for chain t
+          auto fold_scores = [&](int t, uint32_t at, bool last) {
+            if (!wait_slot(at + t)) return false;
+            ptx::tc_fence_after();
+            scores(t, slot(at + t));
+            commit(ctl.empty[(at + t) % kSlots]);
+            if (last) commit(ctl.q_empty[ob]);
+            return true;
+          };
+          const int all = n0 + n1;
+          if (!fold_scores(0, c, all == 1) || (n1 > 0 && !fold_scores(1, c, all == 2))) break;
+          for (int j = 0; j < n0; ++j) {
+            const int two = j < n1 ? 2 : 1;
+            const uint32_t next = c + 2 * two;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (t >= two) continue;
+              if (!wait_slot(c + two + t) || !wait(ctl.p_ready[t], (t ? pv1 : pv0) & 1)) {
+                stop = true;
+                break;
+              }
+              ++(t ? pv1 : pv0);
+              ptx::tc_fence_after();
+              const uint32_t v = desc_mn(slot(c + two + t));
+              if (leader) {
+#pragma unroll
+                for (int s = 0; s < kTile / 16; ++s)
+                  mma_ts(tmem + 256 + t * 128, tmem + t * 128 + s * 8, v + s * (2048 >> 4), id_o,
+                         j > 0 || s > 0);
+              }
+              commit(ctl.empty[(c + two + t) % kSlots]);
+              if (j + 1 == (t ? n1 : n0)) {
+                commit(ctl.o_done[t]);
+              } else if (!fold_scores(t, next, 2 * (j + 1) + t + 1 == all)) {
+                stop = true;
+                break;
+              }
+            }
+            if (stop) break;
+            c = next;
+          }
+          continue;
+        }
+        if (!wait(ctl.full[c % kSlots], (c / kSlots) & 1)) break;
         ptx::tc_fence_after();
-        if (n0 > 0) scores(0, ring + c % Plan::slots * Plan::tile_bytes);
-        if (n1 > 0) scores(1, ring + c % Plan::slots * Plan::tile_bytes);
-        commit(ctl.empty[c % Plan::slots]);
+        if (n0 > 0) scores(0, ring + c % kSlots * Plan::tile_bytes);
+        if (n1 > 0) scores(1, ring + c % kSlots * Plan::tile_bytes);
+        commit(ctl.empty[c % kSlots]);
         if (n == 1) commit(ctl.q_empty[ob]);
         for (int j = 0; j < n; ++j, c += 2) {
-          const uint32_t vs = (c + 1) % Plan::slots, ks = (c + 2) % Plan::slots;
-          if (!wait(ctl.full[vs], ((c + 1) / Plan::slots) & 1) ||
-              (j + 1 < n && !wait(ctl.full[ks], ((c + 2) / Plan::slots) & 1))) {
+          const uint32_t vs = (c + 1) % kSlots, ks = (c + 2) % kSlots;
+          if (!wait(ctl.full[vs], ((c + 1) / kSlots) & 1) ||
+              (j + 1 < n && !wait(ctl.full[ks], ((c + 2) / kSlots) & 1))) {
             stop = true;
             break;
           }
@@ -337,7 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_arrived(s[q]);
-        const int seen = limit - (it.jb + j) * kTile;  // columns of this tile that the row sees
+        const int tile = it.jb + (FOLD ? 2 * j + t : j);
+        const int seen = limit - tile * kTile;  // columns of this tile that the row sees
         if (__any_sync(0xffffffffu, seen < kTile)) {
 #pragma unroll
           for (int q = 0; q < 4; ++q)
@@ -405,12 +469,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = any ? 1.0f / l : 0.0f;
       const float lse2 = any ? m + log2f(l) : -INFINITY;
       const int64_t rows = g.B * g.Hq * g.Lq;
+      const int64_t part_at = (int64_t)(FOLD ? 2 * it.split + t : it.split) * rows + at;
       if (live) {
-        if (a.splits > 1) a.part_lse[(int64_t)it.split * rows + at] = lse2;
+        if (a.parts > 1) a.part_lse[part_at] = lse2;
         else if (a.lse) a.lse[at] = lse2 * kLn2;
       }
-      if (a.splits > 1) {
-        float* part = a.part + ((int64_t)it.split * rows + at) * g.D;
+      if (a.parts > 1) {
+        float* part = a.part + part_at * g.D;
         for (int q = 0; q < (g.D + 31) / 32; ++q) {
           uint32_t o[32];
           if (n > 0) {
@@ -495,14 +560,14 @@ __global__ void __launch_bounds__(256) attn_tc_join(const FwdArgs a) {
   const int lane = threadIdx.x & 31;
   if (at >= rows) return;
   float top = -INFINITY;
-  for (int s = lane; s < a.splits; s += 32) top = fmaxf(top, a.part_lse[(int64_t)s * rows + at]);
+  for (int s = lane; s < a.parts; s += 32) top = fmaxf(top, a.part_lse[(int64_t)s * rows + at]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float ref = top == -INFINITY ? 0.0f : top;
   float total = 0.0f;
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   const int d = lane * 4;
-  for (int s = 0; s < a.splits; ++s) {
+  for (int s = 0; s < a.parts; ++s) {
     const float lse = a.part_lse[(int64_t)s * rows + at];
     if (lse == -INFINITY) continue;
     const float w = exp2f(lse - ref);
@@ -533,6 +598,7 @@ __global__ void __launch_bounds__(256) attn_tc_join(const FwdArgs a) {
 // whole with a fixed order, and costs about half an item with a running counter; partial sums
 // are written and read once, and joined in about 4.
 int split_count(const TcGeom& g, bool dynamic, int sms, int pairs) {
+  const double tile = g.qtiles == 1 ? 0.7 : 1.0;  // two chains
   const long long base = (long long)g.B * g.Hk * pairs;
   const double floats = (double)g.B * g.Hq * g.Lq * g.D, fill = g.causal ? 0.5 : 0.75;
   int best = 1;
@@ -542,9 +608,9 @@ int split_count(const TcGeom& g, bool dynamic, int sms, int pairs) {
     if ((g.ktiles + per - 1) / per != s) continue;
     double cost;
     if (dynamic && base * s > sms)
-      cost = (double)base * (g.ktiles * fill + 1.5 * s) / sms + per * 0.5;
+      cost = (double)base * (g.ktiles * fill * tile + 1.5 * s) / sms + per * tile * 0.5;
     else
-      cost = (double)((base * s + sms - 1) / sms) * (per + 1.5);
+      cost = (double)((base * s + sms - 1) / sms) * (per * tile + 1.5);
     if (s > 1) cost += 4.0 + s * floats * 8.0 / 6.7e6;
     if (cost < least - 1e-9) {
       least = cost;
@@ -560,6 +626,8 @@ FwdArgs fwd_args(const fconv_attn_desc& d, int sms, const AttnArgs& a) {
   f.pairs = (f.g.qtiles + 1) / 2;
   f.splits = split_count(f.g, d.causal || d.has_q_lens || d.has_kv_lens, sms, f.pairs);
   f.per = (f.g.ktiles + f.splits - 1) / f.splits;
+  f.fold = f.g.qtiles == 1 && f.splits > 1 && f.per > 1;
+  f.parts = f.splits * (f.fold ? 2 : 1);
   f.items = (int)((long long)f.g.B * f.g.Hk * f.pairs * f.splits);
   for (int i = 0; i < 3; ++i) f.o[i] = d.out_stride[i];
   f.out = a.o;
@@ -571,18 +639,18 @@ FwdArgs fwd_args(const fconv_attn_desc& d, int sms, const AttnArgs& a) {
     f.counter_floats = 4;
     if (ws) ws += 4;
   }
-  if (f.splits > 1) {
+  if (f.parts > 1) {
     f.part_lse = ws;
-    f.part_floats = ((size_t)f.splits * rows + 3) / 4 * 4;
+    f.part_floats = ((size_t)f.parts * rows + 3) / 4 * 4;
     if (ws) f.part = ws + f.part_floats;
-    f.part_floats += (size_t)f.splits * rows * f.g.D;
+    f.part_floats += (size_t)f.parts * rows * f.g.D;
   }
   return f;
 }
 
 template <bool BF16, int H>
 int launch_t(const FwdArgs& f, int sms, const CUtensorMap* m, cudaStream_t s) {
-  auto kern = attn_tc_forward<BF16, H>;
+  auto kern = f.fold ? attn_tc_forward<BF16, H, true> : attn_tc_forward<BF16, H, false>;
   const int e = allow_smem((const void*)kern, fwd_smem<H>());
   if (e) return e;
   const int grid = f.items < sms ? f.items : sms;
@@ -641,7 +709,7 @@ int launch_attn_tc_forward(const fconv_attn_desc& d, int sms, const AttnArgs& a,
     e = bf ? launch_t<true, 1>(f, sms, m, s) : launch_t<false, 1>(f, sms, m, s);
   else
     e = bf ? launch_t<true, 2>(f, sms, m, s) : launch_t<false, 2>(f, sms, m, s);
-  if (e || f.splits == 1) return e;
+  if (e || f.parts == 1) return e;
   const long long rows = (long long)f.g.B * f.g.Hq * f.g.Lq;
   return launch_pdl(bf ? attn_tc_join<true> : attn_tc_join<false>, dim3((unsigned)((rows + 7) / 8)),
                     dim3(256), 0, s, f);
