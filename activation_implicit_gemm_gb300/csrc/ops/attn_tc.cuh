@@ -11,6 +11,7 @@
 
 #include "../fconv_internal.h"
 #include "../ptx.cuh"
+#include "ops_common.cuh"
 #include "ops_internal.h"
 #include "waits.cuh"
 
@@ -196,31 +197,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// Pairs of f32 in one instruction.
-__device__ __forceinline__ uint64_t pair(float x, float y) {
-  return (uint64_t)__float_as_uint(x) | ((uint64_t)__float_as_uint(y) << 32);
-}
-__device__ __forceinline__ uint64_t pair(uint32_t x, uint32_t y) {
-  return (uint64_t)x | ((uint64_t)y << 32);
-}
-__device__ __forceinline__ float low(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float high(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
 }
 
 // Two values rounded to 16 bits, the first in the low half.

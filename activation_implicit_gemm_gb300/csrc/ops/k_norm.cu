@@ -474,34 +474,74 @@ struct TileRing {
       ptx::cp_async4(word(stage, n, c), ok ? p + ch * step : p, ok ? 4 : 0);
     }
   }
-  template <typename T, int VP>
-  __device__ __forceinline__ void get(float (&f)[VP], uint32_t stage, int n, int c) const {
-    const uint32_t raw = ptx::ld_shared_u32(word(stage, n, c));
-    const Vec<T, VP> v = *reinterpret_cast<const Vec<T, VP>*>(&raw);
-#pragma unroll
-    for (int i = 0; i < VP; ++i) f[i] = to_f(v.v[i]);
-  }
 };
+
+// The positions of a lane: one f32, or two that the packed f32 instructions work on at once.
+template <int VP>
+struct Lane;
+template <>
+struct Lane<1> {
+  using V = float;
+  static __device__ __forceinline__ V all(float x) { return x; }
+  static __device__ __forceinline__ V add(V a, V b) { return a + b; }
+  static __device__ __forceinline__ V mul(V a, V b) { return a * b; }
+  static __device__ __forceinline__ V fma(V a, V b, V c) { return fmaf(a, b, c); }
+  static __device__ __forceinline__ float sum(V a) { return a; }
+  static __device__ __forceinline__ float at(V a, int) { return a; }
+  static __device__ __forceinline__ V from(const float (&f)[1]) { return f[0]; }
+};
+template <>
+struct Lane<2> {
+  using V = uint64_t;
+  static __device__ __forceinline__ V all(float x) { return pair(x, x); }
+  static __device__ __forceinline__ V add(V a, V b) { return add2(a, b); }
+  static __device__ __forceinline__ V mul(V a, V b) { return mul2(a, b); }
+  static __device__ __forceinline__ V fma(V a, V b, V c) { return fma2(a, b, c); }
+  static __device__ __forceinline__ float sum(V a) { return low(a) + high(a); }
+  static __device__ __forceinline__ float at(V a, int i) { return i ? high(a) : low(a); }
+  static __device__ __forceinline__ V from(const float (&f)[2]) { return pair(f[0], f[1]); }
+};
+// A 4-byte word of T as the lane's values, and back.
+template <typename T, int VP>
+__device__ __forceinline__ typename Lane<VP>::V lane_get(uint32_t word) {
+  const Vec<T, VP> v = *reinterpret_cast<const Vec<T, VP>*>(&word);
+  float f[VP];
+#pragma unroll
+  for (int i = 0; i < VP; ++i) f[i] = to_f(v.v[i]);
+  return Lane<VP>::from(f);
+}
+template <typename T, int VP>
+__device__ __forceinline__ void lane_put(T* p, typename Lane<VP>::V a) {
+  Vec<T, VP> v;
+#pragma unroll
+  for (int i = 0; i < VP; ++i) v.v[i] = from_f<T>(Lane<VP>::at(a, i));
+  *reinterpret_cast<Vec<T, VP>*>(p) = v;
+}
 constexpr int kTileFwdStages = 3, kTileBwdStages = 2;
 
 // The parameters of the block's channels in shared memory, as f32.
+template <int STRIDE>
 __device__ __forceinline__ void stage_params(float* dst, const void* p, float none,
                                              const NormGeom& g) {
   for (int c = threadIdx.y * 32 + threadIdx.x; c < kStaged; c += blockDim.y * 32)
-    dst[c] = p && c < g.C ? param_at(p, g.param_f32, c, g.dtype) : none;
+    dst[c * STRIDE] = p && c < g.C ? param_at(p, g.param_f32, c, g.dtype) : none;
 }
 
 template <typename T, int VP>
 __global__ void __launch_bounds__(kPlaneWarps * 32, 2)
     norm_tiles_forward(const NormGeom g, int64_t tiles) {
   extern __shared__ __align__(16) uint8_t dsmem[];
-  __shared__ float red[kPlaneWarps * VP * 32], w[kStaged], b[kStaged];
+  __shared__ float red[kPlaneWarps * VP * 32];
+  __shared__ float2 wb[kStaged];
+  using L = Lane<VP>;
   constexpr int S = kTileFwdStages;
   ptx::pdl_wait();
   ptx::pdl_trigger();
   const int warps = blockDim.y, C = (int)g.C;
   const int64_t step = g.inner;
   const float inv = 1.0f / (float)C;
+  // channels of this warp that exist: the first `mine` of its kCpw
+  const int mine = (C - (int)threadIdx.y + warps - 1) / warps;
   TileRing<1, S> ring;
   ring.init(dsmem);
   auto ask = [&](int64_t u, uint32_t stage) {
@@ -512,36 +552,44 @@ __global__ void __launch_bounds__(kPlaneWarps * 32, 2)
     ptx::cp_async_commit();
   };
   for (int i = 0; i < S - 1; ++i) ask(blockIdx.x + (int64_t)i * gridDim.x, i);
-  stage_params(w, g.w, 1.0f, g);
-  stage_params(b, g.b, 0.0f, g);
+  stage_params<2>(&wb[0].x, g.w, 1.0f, g);
+  stage_params<2>(&wb[0].y, g.b, 0.0f, g);
   uint32_t stage = 0;
   for (int64_t u = blockIdx.x; u < tiles; u += gridDim.x) {
     ask(u + (int64_t)(S - 1) * gridDim.x, (stage + S - 1) % S);
     ptx::cp_async_wait<S - 1>();
     const Tile k = tile_of<VP>(g, u);
-    T* y = (T*)g.y + k.base;
-    float m[VP], r[VP], f[VP];
+    typename L::V f[kCpw], acc = L::all(0.0f);
+    const uint32_t word = ring.word(stage, 0, 0);
 #pragma unroll
-    for (int i = 0; i < VP; ++i) m[i] = r[i] = 0.0f;
-#pragma unroll
-    for (int c = 0; c < kCpw; ++c) {
-      ring.template get<T, VP>(f, stage, 0, c);
-#pragma unroll
-      for (int i = 0; i < VP; ++i) m[i] += f[i];
+    for (int c = 0; c < kCpw; ++c) {  // channels that do not exist arrived as zeros
+      f[c] = lane_get<T, VP>(ptx::ld_shared_u32(word + c * ring.pitch));
+      acc = L::add(acc, f[c]);
     }
+    float m[VP], r[VP];
+#pragma unroll
+    for (int i = 0; i < VP; ++i) m[i] = L::at(acc, i);
     plane_sum<VP>(m, red, warps);
 #pragma unroll
-    for (int i = 0; i < VP; ++i) m[i] *= inv;
+    for (int i = 0; i < VP; ++i) m[i] = -m[i] * inv;
+    const typename L::V nm = L::from(m);
+    acc = L::all(0.0f);
+    if (mine == kCpw) {
 #pragma unroll
-    for (int c = 0; c < kCpw; ++c) {
-      ring.template get<T, VP>(f, stage, 0, c);
-      const bool in = c * warps + (int)threadIdx.y < C;
-#pragma unroll
-      for (int i = 0; i < VP; ++i) {
-        const float d = in ? f[i] - m[i] : 0.0f;
-        r[i] = fmaf(d, d, r[i]);
+      for (int c = 0; c < kCpw; ++c) {
+        f[c] = L::add(f[c], nm);
+        acc = L::fma(f[c], f[c], acc);
       }
+    } else {
+#pragma unroll
+      for (int c = 0; c < kCpw; ++c)
+        if (c < mine) {
+          f[c] = L::add(f[c], nm);
+          acc = L::fma(f[c], f[c], acc);
+        }
     }
+#pragma unroll
+    for (int i = 0; i < VP; ++i) r[i] = L::at(acc, i);
     plane_sum<VP>(r, red, warps);
 #pragma unroll
     for (int i = 0; i < VP; ++i) r[i] = rsqrtf(r[i] * inv + g.eps);
@@ -549,18 +597,17 @@ __global__ void __launch_bounds__(kPlaneWarps * 32, 2)
       if (threadIdx.y == 0) {
 #pragma unroll
         for (int i = 0; i < VP; ++i) {
-          if (g.mean) g.mean[k.pos + i] = m[i];
+          if (g.mean) g.mean[k.pos + i] = -m[i];
           if (g.rstd) g.rstd[k.pos + i] = r[i];
         }
       }
+      const typename L::V rr = L::from(r);
+      T* y = (T*)g.y + k.base + threadIdx.y * step;
 #pragma unroll
-      for (int c = 0; c < kCpw; ++c) {
-        const int ch = c * warps + threadIdx.y;
-        if (ch >= C) break;
-        ring.template get<T, VP>(f, stage, 0, c);
-#pragma unroll
-        for (int i = 0; i < VP; ++i) f[i] = fmaf((f[i] - m[i]) * r[i], w[ch], b[ch]);
-        store_f<T, VP>(y + ch * step, f);
+      for (int c = 0; c < kCpw; ++c, y += warps * step) {
+        if (c >= mine) break;
+        const float2 p = wb[c * warps + threadIdx.y];
+        lane_put<T, VP>(y, L::fma(L::mul(f[c], rr), L::all(p.x), L::all(p.y)));
       }
     }
     stage = (stage + 1) % S;
@@ -580,6 +627,8 @@ __global__ void __launch_bounds__(kPlaneWarps * 32, 1)
   const int warps = blockDim.y, lane = threadIdx.x, C = (int)g.C;
   const int64_t step = g.inner;
   const float inv = 1.0f / (float)C;
+  const int mine = (C - (int)threadIdx.y + warps - 1) / warps;
+  using L = Lane<VP>;
   TileRing<2, S> ring;
   ring.init(dsmem);
   auto ask = [&](int64_t u, uint32_t stage) {
@@ -591,58 +640,62 @@ __global__ void __launch_bounds__(kPlaneWarps * 32, 1)
     ptx::cp_async_commit();
   };
   ask(blockIdx.x, 0);
-  stage_params(w, g.w, 1.0f, g);
+  stage_params<1>(w, g.w, 1.0f, g);
   __syncthreads();
   float aw = 0.0f, ab = 0.0f;
   uint32_t stage = 0;
   for (int64_t u = blockIdx.x; u < tiles; u += gridDim.x) {
     const Tile k = tile_of<VP>(g, u);
-    T* dx = (T*)g.y + k.base;
     float m[VP], r[VP], s[2 * VP];
 #pragma unroll
     for (int i = 0; i < VP; ++i) {
-      m[i] = k.live ? g.mean[k.pos + i] : 0.0f;
+      m[i] = k.live ? -g.mean[k.pos + i] : 0.0f;
       r[i] = k.live ? g.rstd[k.pos + i] : 0.0f;
-      s[i] = s[VP + i] = 0.0f;
     }
     ask(u + gridDim.x, stage ^ 1);
+    const typename L::V nm = L::from(m), rr = L::from(r);
     ptx::cp_async_wait<S - 1>();
+    const uint32_t wx = ring.word(stage, 0, 0), wd = ring.word(stage, 1, 0);
+    typename L::V s1 = L::all(0.0f), s2 = L::all(0.0f);
     float p[kCpw], q[kCpw];
 #pragma unroll
-    for (int c = 0; c < kCpw; ++c) {
-      float x[VP], d[VP];
-      ring.template get<T, VP>(x, stage, 0, c);
-      ring.template get<T, VP>(d, stage, 1, c);
-      const float wc = w[min(c * warps + (int)threadIdx.y, kStaged - 1)];
-      p[c] = q[c] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < VP; ++i) {
-        const float h = (x[i] - m[i]) * r[i];
-        p[c] = fmaf(d[i], h, p[c]);
-        q[c] += d[i];
-        s[i] = fmaf(d[i], wc, s[i]);
-        s[VP + i] = fmaf(d[i] * wc, h, s[VP + i]);
-      }
+    for (int c = 0; c < kCpw; ++c) {  // channels that do not exist arrived with dy = 0
+      const typename L::V x = lane_get<T, VP>(ptx::ld_shared_u32(wx + c * ring.pitch));
+      const typename L::V d = lane_get<T, VP>(ptx::ld_shared_u32(wd + c * ring.pitch));
+      const typename L::V wc = L::all(w[c * warps + threadIdx.y]);
+      const typename L::V h = L::mul(L::add(x, nm), rr), k2 = L::mul(d, wc);
+      p[c] = L::sum(L::mul(d, h));
+      q[c] = L::sum(d);
+      s1 = L::add(s1, k2);
+      s2 = L::fma(k2, h, s2);
     }
     if (g.part) {
       aw += fold<kCpw>(p);
       ab += fold<kCpw>(q);
     }
+#pragma unroll
+    for (int i = 0; i < VP; ++i) {
+      s[i] = L::at(s1, i);
+      s[VP + i] = L::at(s2, i);
+    }
     plane_sum<2 * VP>(s, red, warps);
-#pragma unroll
-    for (int i = 0; i < 2 * VP; ++i) s[i] *= inv;
     if (k.live) {
+      float a1[VP], a2[VP];
 #pragma unroll
-      for (int c = 0; c < kCpw; ++c) {
-        const int ch = c * warps + threadIdx.y;
-        if (ch >= C) break;
-        float x[VP], d[VP];
-        ring.template get<T, VP>(x, stage, 0, c);
-        ring.template get<T, VP>(d, stage, 1, c);
+      for (int i = 0; i < VP; ++i) {
+        a1[i] = -s[i] * inv;
+        a2[i] = -s[VP + i] * inv;
+      }
+      const typename L::V n1 = L::from(a1), n2 = L::from(a2);
+      T* dx = (T*)g.y + k.base + threadIdx.y * step;
 #pragma unroll
-        for (int i = 0; i < VP; ++i)
-          d[i] = r[i] * (d[i] * w[ch] - s[i] - (x[i] - m[i]) * r[i] * s[VP + i]);
-        store_f<T, VP>(dx + ch * step, d);
+      for (int c = 0; c < kCpw; ++c, dx += warps * step) {
+        if (c >= mine) break;
+        const typename L::V x = lane_get<T, VP>(ptx::ld_shared_u32(wx + c * ring.pitch));
+        const typename L::V d = lane_get<T, VP>(ptx::ld_shared_u32(wd + c * ring.pitch));
+        const typename L::V h = L::mul(L::add(x, nm), rr);
+        const typename L::V t = L::fma(d, L::all(w[c * warps + threadIdx.y]), n1);
+        lane_put<T, VP>(dx, L::mul(L::fma(h, n2, t), rr));
       }
     }
     stage ^= 1;
@@ -817,27 +870,27 @@ __global__ void __launch_bounds__(kPlaneWarps * 32, 1)
 
 // ------------------------------------------------------------------------------ join
 
-// dw (blockIdx.y 0) and db (1) from the blocks' partial sums: eight interleaved sequences a
+// dw (blockIdx.y 0) and db (1) from the blocks' partial sums: 32 interleaved sequences a
 // channel, then those in order.
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
     norm_dparam_join(const float* __restrict__ part, void* dw, void* db, int dtype, int f32,
                      int64_t C, int blocks) {
-  __shared__ float red[8][32];
+  __shared__ float red[32][32];
   ptx::pdl_wait();
   ptx::pdl_trigger();
   void* out = blockIdx.y ? db : dw;
   const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
   float s = 0.0f;
   if (c < C && out) {
-#pragma unroll 4
-    for (int i = threadIdx.y; i < blocks; i += 8) s += part[(2 * (int64_t)i + blockIdx.y) * C + c];
+#pragma unroll 8
+    for (int i = threadIdx.y; i < blocks; i += 32) s += part[(2 * (int64_t)i + blockIdx.y) * C + c];
   }
   red[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y || c >= C || !out) return;
   s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s += red[i][threadIdx.x];
+  for (int i = 0; i < 32; ++i) s += red[i][threadIdx.x];
   if (f32) ((float*)out)[c] = s;
   else if (dtype == FCONV_F16) ((__half*)out)[c] = from_f<__half>(s);
   else ((__nv_bfloat16*)out)[c] = from_f<__nv_bfloat16>(s);
@@ -1051,7 +1104,7 @@ int launch_norm_backward(const fconv_norm_desc& d, int sms, const NormArgs& a, c
   // without rows there are no partial sums and both gradients are zero
   const int blocks =
       d.outer > 0 ? (int)backward_blocks(d, sms, row_vec(d, a), plane_vp(d, a)) : 0;
-  return launch_pdl(norm_dparam_join, dim3((unsigned)((d.channels + 31) / 32), 2), dim3(32, 8), 0,
+  return launch_pdl(norm_dparam_join, dim3((unsigned)((d.channels + 31) / 32), 2), dim3(32, 32), 0,
                     s, (const float*)a.ws, a.dw, a.db, d.dtype, (int)(d.param_dtype == FCONV_F32),
                     d.channels, blocks);
 }
