@@ -82,10 +82,11 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
 }
 
 // A block per query tile of a (batch, key head); in f16 also one per key tile for the largest
-// value norm. Sixteen lanes share a row, eight elements each.
-template <bool BF16>
-__global__ void __launch_bounds__(256) attn_tc_delta(const DeltaArgs a) {
-  __shared__ float top[16];
+// value norm. LPR lanes share a row, eight elements each, so RP rows go at a time.
+template <bool BF16, int LPR>
+__global__ void __launch_bounds__(256, 4) attn_tc_delta(const DeltaArgs a) {
+  constexpr int RP = 256 / LPR, N = kTile / RP;
+  __shared__ float top[RP];
   ptx::pdl_wait();
   ptx::pdl_trigger();
   if (blockIdx.x == 0 && threadIdx.x < 2) a.counters[threadIdx.x] = 0;
@@ -94,68 +95,73 @@ __global__ void __launch_bounds__(256) attn_tc_delta(const DeltaArgs a) {
   const int bh = blockIdx.x / per, tile = blockIdx.x - bh * per;
   const int b = bh / g.Hk, hk = bh - b * g.Hk;
   const TcLens l = tc_lens(g, b);
-  const int sub = threadIdx.x >> 4, d = (threadIdx.x & 15) * 8;
+  const int sub = threadIdx.x / LPR, at = threadIdx.x % LPR, d = at * 8;
   float most = 0.0f;
   if (tile < g.qtiles) {
     float* stat = a.stat + ((int64_t)bh * g.qtiles + tile) * (2 * kTile);
-    // all eight rows of a lane in flight at once, and the lse of its half warp's
-    uint4 x[8], y[8];
+    // four rows of a lane in flight, and the lse of all that it shares
     float lse = -INFINITY;
     {
-      const int n = threadIdx.x & 15, r = sub + n * 16, tok = r / g.G, i = tile * g.toks + tok;
-      if (n < 8 && r < g.rows && i >= l.lead && i < l.q)
+      const int n = at, r = sub + n * RP, tok = r / g.G, i = tile * g.toks + tok;
+      if (n < N && r < g.rows && i >= l.lead && i < l.q)
         lse = a.lse[((int64_t)b * g.Hq + (int64_t)hk * g.G + (r - tok * g.G)) * g.Lq + i];
     }
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const int r = sub + n * 16, tok = r / g.G, i = tile * g.toks + tok;
-      const int64_t h = (int64_t)hk * g.G + (r - tok * g.G);
-      x[n] = y[n] = make_uint4(0, 0, 0, 0);
-      if (r < g.rows && i >= l.lead && i < l.q && d < g.D) {
-        x[n] = ptx::ldg_nc_v4(a.out + b * a.o[0] + i * a.o[1] + h * a.o[2] + d);
-        y[n] = ptx::ldg_nc_v4(a.dout + b * a.d[0] + i * a.d[1] + h * a.d[2] + d);
-      }
-    }
+    const uint16_t* out = a.out + b * a.o[0] + (int64_t)hk * g.G * a.o[2] + d;
+    const uint16_t* dout = a.dout + b * a.d[0] + (int64_t)hk * g.G * a.d[2] + d;
     float delta = 0.0f;
+#pragma unroll 1
+    for (int n0 = 0; n0 < N; n0 += 4) {
+      uint4 x[4], y[4];
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const uint32_t xs[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
-      const uint32_t ys[4] = {y[n].x, y[n].y, y[n].z, y[n].w};
-      float s = 0.0f, z = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 u = unpack2<BF16>(xs[e]), v = unpack2<BF16>(ys[e]);
-        s = fmaf(u.x, v.x, fmaf(u.y, v.y, s));
-        z = fmaf(v.x, v.x, fmaf(v.y, v.y, z));
+      for (int n = 0; n < 4; ++n) {
+        const int r = sub + (n0 + n) * RP, tok = r / g.G, i = tile * g.toks + tok;
+        const int64_t h = r - tok * g.G;
+        x[n] = y[n] = make_uint4(0, 0, 0, 0);
+        if (r < g.rows && i >= l.lead && i < l.q && d < g.D) {
+          x[n] = ptx::ldg_nc_v4(out + i * a.o[1] + h * a.o[2]);
+          y[n] = ptx::ldg_nc_v4(dout + i * a.d[1] + h * a.d[2]);
+        }
       }
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (!BF16) z += __shfl_xor_sync(0xffffffffu, z, o);
+      for (int n = 0; n < 4; ++n) {
+        const uint32_t xs[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+        const uint32_t ys[4] = {y[n].x, y[n].y, y[n].z, y[n].w};
+        float s = 0.0f, z = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 u = unpack2<BF16>(xs[e]), v = unpack2<BF16>(ys[e]);
+          s = fmaf(u.x, v.x, fmaf(u.y, v.y, s));
+          z = fmaf(v.x, v.x, fmaf(v.y, v.y, z));
+        }
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) {
+          s += __shfl_xor_sync(0xffffffffu, s, o);
+          if (!BF16) z += __shfl_xor_sync(0xffffffffu, z, o);
+        }
+        most = fmaxf(most, z);
+        if (at == n0 + n) delta = s;
       }
-      most = fmaxf(most, z);
-      if ((threadIdx.x & 15) == n) delta = s;
     }
-    const int n = threadIdx.x & 15;
-    if (n < 8) {
+    const int n = at;
+    if (n < N) {
       // -lse is added to the scores; a row that sees nothing (or only scores of -inf) gets
       // -inf: its p is 0
-      stat[sub + n * 16] =
+      stat[sub + n * RP] =
           lse == -INFINITY ? -INFINITY : (BF16 ? 0.0f : (float)kPShift) - lse * kLog2e;
-      stat[kTile + sub + n * 16] = -delta;  // 0 where the row takes no part
+      stat[kTile + sub + n * RP] = -delta;  // 0 where the row takes no part
     }
   } else {
     const int j0 = (tile - g.qtiles) * kTile;
-    uint4 y[8];
+    uint4 y[N];
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const int j = j0 + sub + n * 16;
+    for (int n = 0; n < N; ++n) {
+      const int j = j0 + sub + n * RP;
       y[n] = make_uint4(0, 0, 0, 0);
       if (j < l.k && d < g.D)
         y[n] = ptx::ldg_nc_v4(a.val + b * a.v[0] + (int64_t)j * a.v[1] + hk * a.v[2] + d);
     }
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
+    for (int n = 0; n < N; ++n) {
       const uint32_t ys[4] = {y[n].x, y[n].y, y[n].z, y[n].w};
       float z = 0.0f;
 #pragma unroll
@@ -164,15 +170,15 @@ __global__ void __launch_bounds__(256) attn_tc_delta(const DeltaArgs a) {
         z = fmaf(v.x, v.x, fmaf(v.y, v.y, z));
       }
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+      for (int o = LPR / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
       most = fmaxf(most, z);
     }
   }
   if (BF16) return;
-  if ((threadIdx.x & 15) == 0) top[sub] = most;
+  if (at == 0) top[sub] = most;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 16; ++i) most = fmaxf(most, top[i]);
+    for (int i = 0; i < RP; ++i) most = fmaxf(most, top[i]);
     if (tile < g.qtiles) a.gmax[(int64_t)bh * g.qtiles + tile] = most;
     else a.vmax[(int64_t)bh * g.ktiles + tile - g.qtiles] = most;
   }
@@ -1325,8 +1331,10 @@ int launch_attn_tc_backward(const fconv_attn_desc& d, int sms, const AttnArgs& a
   da.vmax = ws + p.vmax;
   da.counters = (int*)(ws + p.counters);
   const long long bh = (long long)g.B * g.Hk;
-  int e = launch_pdl(bf ? attn_tc_delta<true> : attn_tc_delta<false>,
-                     dim3((unsigned)(bh * (g.qtiles + (bf ? 0 : g.ktiles)))), dim3(256), 0, s, da);
+  auto pre = d.head_dim <= 64 ? (bf ? attn_tc_delta<true, 8> : attn_tc_delta<false, 8>)
+                              : (bf ? attn_tc_delta<true, 16> : attn_tc_delta<false, 16>);
+  int e = launch_pdl(pre, dim3((unsigned)(bh * (g.qtiles + (bf ? 0 : g.ktiles)))), dim3(256), 0, s,
+                     da);
   if (e) return e;
 
   BwdArgs b{};

@@ -115,7 +115,7 @@ struct Row {
 
 // Rows on their way to a group of TPR threads: a ring of S stages in shared memory filled by
 // bulk copies (N tensors a stage), so that the loads in flight do not depend on registers or
-// on the group's barriers. Without 16-byte rows (RING false) rows are read where they are.
+// on the group's barriers. Rows that are not whole 16-byte units do not use it (RING false).
 template <typename T, int N, int S, int TPR, bool RING>
 struct Feed {
   const T* src[N];
@@ -156,10 +156,9 @@ struct Feed {
   __device__ __forceinline__ void wait() {
     if (RING) drain_bar(bars + k % S * 8, (k / S) & 1);
   }
-  __device__ __forceinline__ const T* row(const uint8_t* dsmem, int n, const T* direct) const {
-    return RING ? reinterpret_cast<const T*>(dsmem + (ring - ptx::smem_addr(dsmem)) +
-                                             (k % S * N + n) * bytes)
-                : direct;
+  __device__ __forceinline__ const T* row(const uint8_t* dsmem, int n) const {
+    return reinterpret_cast<const T*>(dsmem + (ring - ptx::smem_addr(dsmem)) +
+                                      (k % S * N + n) * bytes);
   }
   // After a barrier of the group past the last read of the current row.
   __device__ __forceinline__ void next() {
@@ -204,10 +203,19 @@ __global__ void __launch_bounds__(row_threads<TPR>(), row_blocks(E, TPR, false))
   R::params(b, g.b, 0.0f, g, t, C);
   const float inv = 1.0f / (float)C;
   int turn = 0;
+  float ahead[VEC > 1 ? 1 : E];  // without a ring the next row waits in registers
+  if constexpr (VEC == 1)
+    if (row < g.outer) R::get(ahead, (const T*)g.x + row * C, t, C);
   for (; row < g.outer; row += step) {
     float f[E];
-    feed.wait();
-    R::get(f, feed.row(dsmem, 0, (const T*)g.x + row * C), t, C);
+    if constexpr (VEC > 1) {
+      feed.wait();
+      R::get(f, feed.row(dsmem, 0), t, C);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = ahead[e];
+      if (row + step < g.outer) R::get(ahead, (const T*)g.x + (row + step) * C, t, C);
+    }
     float s[1] = {0.0f};
 #pragma unroll
     for (int e = 0; e < E; ++e) s[0] += f[e];
@@ -256,6 +264,12 @@ __global__ void __launch_bounds__(row_threads<TPR>(), row_blocks(E, TPR, true))
   for (int e = 0; e < E; ++e) aw[e] = ab[e] = 0.0f;
   const float inv = 1.0f / (float)C;
   int turn = 0;
+  float ahead[2][VEC > 1 ? 1 : E];  // without a ring the next row waits in registers
+  if constexpr (VEC == 1)
+    if (row < g.outer) {
+      R::get(ahead[0], (const T*)g.x + row * C, t, C);
+      R::get(ahead[1], (const T*)g.dy + row * C, t, C);
+    }
   float lm = 0.0f, lr = 0.0f;  // lane i: the statistics of the row i steps past a group of 32
   for (uint32_t k = 0; row < g.outer; row += step, ++k) {
     if ((k & 31) == 0) {
@@ -265,9 +279,21 @@ __global__ void __launch_bounds__(row_threads<TPR>(), row_blocks(E, TPR, true))
     }
     const float m = __shfl_sync(0xffffffffu, lm, k & 31), r = __shfl_sync(0xffffffffu, lr, k & 31);
     float h[E], d[E];
-    feed.wait();
-    R::get(h, feed.row(dsmem, 0, (const T*)g.x + row * C), t, C);
-    R::get(d, feed.row(dsmem, 1, (const T*)g.dy + row * C), t, C);
+    if constexpr (VEC > 1) {
+      feed.wait();
+      R::get(h, feed.row(dsmem, 0), t, C);
+      R::get(d, feed.row(dsmem, 1), t, C);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        h[e] = ahead[0][e];
+        d[e] = ahead[1][e];
+      }
+      if (row + step < g.outer) {
+        R::get(ahead[0], (const T*)g.x + (row + step) * C, t, C);
+        R::get(ahead[1], (const T*)g.dy + (row + step) * C, t, C);
+      }
+    }
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int e = 0; e < E; ++e) {
