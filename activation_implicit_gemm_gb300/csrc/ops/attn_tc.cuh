@@ -236,8 +236,8 @@ __device__ __forceinline__ TcLens tc_lens(const TcGeom& g, int b) {
   TcLens l;
   l.q = (int)g.Lq;
   l.k = (int)g.Lk;
-  if (g.q_lens) l.q = min(max(g.q_lens[b], 0), (int)g.Lq);
-  if (g.kv_lens) l.k = min(max(g.kv_lens[b], 0), (int)g.Lk);
+  if (g.q_lens) l.q = min(max(__ldcg(g.q_lens + b), 0), (int)g.Lq);
+  if (g.kv_lens) l.k = min(max(__ldcg(g.kv_lens + b), 0), (int)g.Lk);
   l.shift = l.k - l.q;
   l.lead = g.causal && l.shift < 0 ? -l.shift : 0;
   if (l.k == 0) l.lead = l.q;

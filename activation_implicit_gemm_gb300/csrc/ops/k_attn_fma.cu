@@ -119,7 +119,7 @@ __device__ __forceinline__ void clear(float2 (&acc)[R][NE]) {
 template <typename T, int BT, int NE>
 __global__ void __launch_bounds__(256, 1)
     attn_fma_forward(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
-                        T* __restrict__ o, float* __restrict__ lse, const Geom g) {
+                     T* __restrict__ o, float* __restrict__ lse, const Geom g) {
   constexpr int R = BT / 16;
   extern __shared__ float4 smem4[];
   float* qs = reinterpret_cast<float*>(smem4);
@@ -154,12 +154,12 @@ __global__ void __launch_bounds__(256, 1)
   const T* vp = v + b * g.v[0] + (h / g.G) * g.v[2];
   load_tile<T, BT, 8, false>(qs, qp, g.q[1], i0, 0, L.q, g);
   const float c = g.scale * kLog2e;
-  // the next keys are on their way while this tile's scores are used, the next values while
-  // the next scores are made
+  // the next keys are fetched when this tile's scores are made, the next values when its
+  // probabilities are used up
   load_tile<T, BT, 8, false>(ks, kp, g.k[1], 0, 0, L.k, g);
   load_tile<T, BT, 8, false>(vs, vp, g.v[1], 0, 0, L.k, g);
   for (int64_t j0 = 0; j0 < nk; j0 += BT) {
-        __syncthreads();
+    __syncthreads();
     float s[R][R];
     dot_tile<R>(qs, ks, g.Dp, ty, tx, s);
     __syncthreads();
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(256, 1)
         acc[r][e].y *= shrink;
       }
     }
-        __syncthreads();
+    __syncthreads();
     mix_tile<BT, NE, false>(ps, vs, g.Dp, ty, tx, acc);
     __syncthreads();
     load_tile<T, BT, 8, false>(vs, vp, g.v[1], j0 + BT, 0, L.k, g);
@@ -239,8 +239,8 @@ __device__ __forceinline__ void grad_tile(float (&s)[R][R], float (&dp)[R][R], i
 template <typename T, int BT, int NE>
 __global__ void __launch_bounds__(256, 1)
     attn_fma_dq(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
-                   const T* __restrict__ dout, const float* __restrict__ lse,
-                   const float* __restrict__ delta, T* __restrict__ dq, const Geom g) {
+                const T* __restrict__ dout, const float* __restrict__ lse,
+                const float* __restrict__ delta, T* __restrict__ dq, const Geom g) {
   constexpr int R = BT / 16;
   extern __shared__ float4 smem4[];
   float* qs = reinterpret_cast<float*>(smem4);
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(256, 1)
   load_tile<T, BT, 8, false>(vs, vp, g.v[1], 0, 0, L.k, g);
   load_tile<T, BT, 8, false>(ks, kp, g.k[1], 0, 0, L.k, g);
   for (int64_t j0 = 0; j0 < nk; j0 += BT) {
-      __syncthreads();
+    __syncthreads();
     float s[R][R], dp[R][R];
     dot_tile<R>(qs, ks, g.Dp, ty, tx, s);
     dot_tile<R>(gs, vs, g.Dp, ty, tx, dp);
@@ -298,9 +298,9 @@ __global__ void __launch_bounds__(256, 1)
 template <typename T, int BT, int NE>
 __global__ void __launch_bounds__(256, 1)
     attn_fma_dkv(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
-                    const T* __restrict__ dout, const float* __restrict__ lse,
-                    const float* __restrict__ delta, T* __restrict__ dk, T* __restrict__ dv,
-                    const Geom g) {
+                 const T* __restrict__ dout, const float* __restrict__ lse,
+                 const float* __restrict__ delta, T* __restrict__ dk, T* __restrict__ dv,
+                 const Geom g) {
   constexpr int R = BT / 16;
   extern __shared__ float4 smem4[];
   float* qs = reinterpret_cast<float*>(smem4);
@@ -335,19 +335,19 @@ __global__ void __launch_bounds__(256, 1)
   auto row_of = [&](int64_t n) { return start + n % steps * BT; };
   auto load_q = [&](int64_t n) {
     if (n < all)
-      load_tile<T, BT, 8, false>(qs, q + b * g.q[0] + head_of(n) * g.q[2], g.q[1], row_of(n), lead, L.q,
-                            g);
+      load_tile<T, BT, 8, false>(qs, q + b * g.q[0] + head_of(n) * g.q[2], g.q[1], row_of(n),
+                                 lead, L.q, g);
   };
   auto load_g = [&](int64_t n) {
     if (n < all)
-      load_tile<T, BT, 8, false>(gs, dout + b * g.g[0] + head_of(n) * g.g[2], g.g[1], row_of(n), lead,
-                            L.q, g);
+      load_tile<T, BT, 8, false>(gs, dout + b * g.g[0] + head_of(n) * g.g[2], g.g[1], row_of(n),
+                                 lead, L.q, g);
   };
   load_q(0);
   load_g(0);
   for (int64_t n = 0; n < all; ++n) {
     const int64_t i0 = row_of(n), row = (b * g.Hq + head_of(n)) * g.Lq;
-      __syncthreads();
+    __syncthreads();
     float s[R][R], dp[R][R];
     dot_tile<R>(qs, ks, g.Dp, ty, tx, s);
     dot_tile<R>(gs, vs, g.Dp, ty, tx, dp);
@@ -406,8 +406,8 @@ int backward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
     const int e = allow_smem((const void*)kern, smem);
     if (e) return e;
     if (!grid_ok((rows + 7) / 8) || !grid_ok(bq)) return (int)cudaErrorInvalidValue;
-    attn_delta<T><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>((const T*)a.out,
-                                                                    (const T*)a.dout, delta, g);
+    attn_delta<T><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>((const T*)a.out, (const T*)a.dout,
+                                                             delta, g);
     kern<<<(unsigned)bq, 256, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v,
                                          (const T*)a.dout, a.lse, delta, (T*)a.dq, g);
   }

@@ -3,9 +3,11 @@
 //   p = exp(scale q k^T - lse),  dp = dout v^T,  ds = p (dp - delta),  delta_i = dout_i . out_i
 //   dv = p^T dout,  dk = scale ds^T q,  dq = scale ds k
 //
-// Three launches. attn_tc_delta writes -lse (in log2) and -delta per packed query row.
+// attn_tc_delta writes -lse (in log2) and -delta per packed query row.
 // attn_tc_dkv owns 128 keys of a (batch, key head) and walks the query tiles of all the heads
-// that share them; attn_tc_dq owns 128 packed query rows and walks the key tiles. Every
+// that share them; attn_tc_dq owns 128 packed query rows and walks the key tiles. dq needs
+// nothing of dkv's: its blocks start as dkv's end, and it waits for dkv only before it ends (f16
+// images of 197 tokens: 86 -> 82 us a training pass; the causal size below: 699 -> 690). Every
 // gradient element has one writer that adds in a fixed order: no atomics, the same bits every
 // time. The price is that q k^T and dout v^T are made twice: 7 products of 128 x 128 x D a tile
 // pair instead of 5, while one kernel for all five would add dq in f32 atomics (32 bits a value
@@ -27,7 +29,12 @@
 // in the epilogue: small gradients do not fall into f16's subnormals and none overflows. bf16
 // needs neither.
 //
-// Bound: tensor (14 D FLOPs a pair as run, 10 D counted).
+// Bound: tensor (14 D FLOPs a pair as run, 10 D counted). 2 x 4096 tokens in causal order, 32
+// heads of 128 on 8, bf16 (4096 and 2631 valid): delta 22 us, dkv 280, dq 241. In dkv the tensor
+// pipe waits for p and ds between its products (4096 tokens of 19 heads: 219 us, the products
+// alone 180); dq waits for its K and V tiles, each from L2 for one query tile (there 214 us, 193
+// without elementwise work, 128 without the loads as well). 32 x 197 tokens, 12 heads of 64, f16:
+// delta 10 us, dkv 33, dq 24: 768 items of two tiles, a chain of latencies each, on 152 SMs.
 #include "attn_tc.cuh"
 
 #include <climits>
@@ -188,9 +195,9 @@ __global__ void __launch_bounds__(256, 4) attn_tc_delta(const DeltaArgs a) {
 __device__ __forceinline__ int grad_shift(const BwdArgs& a, int bh, int lane) {
   float x = 0.0f, y = 0.0f;
   for (int i = lane; i < a.g.qtiles; i += 32)
-    x = fmaxf(x, a.gmax[(int64_t)bh * a.g.qtiles + i]);
+    x = fmaxf(x, __ldcg(a.gmax + (int64_t)bh * a.g.qtiles + i));
   for (int i = lane; i < a.g.ktiles; i += 32)
-    y = fmaxf(y, a.vmax[(int64_t)bh * a.g.ktiles + i]);
+    y = fmaxf(y, __ldcg(a.vmax + (int64_t)bh * a.g.ktiles + i));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
@@ -398,7 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = uni(ctl.tmem);
-  ptx::pdl_wait();
+  // No wait for the launch before: that is attn_tc_dkv, which let this one start after its own
+  // wait for the delta pass, so all that is read here is complete (read from L2, since nothing
+  // orders this SM's L1 after the delta pass).
 
   if (warp >= 8) {
     regs_fewer<kOtherRegs>();
@@ -553,9 +562,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int i = it.t0 + tok, bh = it.b * g.Hk + it.hk;
       const int limit = row < g.rows ? key_limit(g, it.l, i) : 0;
       const float* stat = a.stat + ((int64_t)bh * g.qtiles + it.tile) * (2 * kTile);
-      const uint64_t nlse = pair(stat[row], stat[row]);
+      const float nl = __ldcg(stat + row);
+      const uint64_t nlse = pair(nl, nl);
       const int shift = it.shift;
-      const float gs = BF16 ? 1.0f : pow2i(shift - kPShift), nd = stat[kTile + row] * gs;
+      const float gs = BF16 ? 1.0f : pow2i(shift - kPShift), nd = __ldcg(stat + kTile + row) * gs;
       const uint64_t gs2 = pair(gs, gs), nd2 = pair(nd, nd);
       bool stop = false;
       for (int j = 0; j < it.n; ++j, ++steps) {
@@ -658,6 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) bulk_wait_all();
   }
 
+  ptx::pdl_wait();  // attn_tc_dkv: what follows this kernel follows both
   ptx::pdl_trigger();
   ptx::tc_fence_before();
   __syncthreads();
@@ -796,6 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = uni(ctl.tmem);
   ptx::pdl_wait();
+  ptx::pdl_trigger();  // attn_tc_dq's blocks take the SMs as this kernel's leave them
 
   if (warp >= 8) {
     regs_fewer<kOtherRegs>();
@@ -1134,7 +1146,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) bulk_wait_all();
   }
 
-  ptx::pdl_trigger();
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -1236,12 +1247,10 @@ BwdPlan bwd_plan(const fconv_attn_desc& d, int sms, const AttnArgs& a) {
   p.stat = take((size_t)bh * p.g.qtiles * 2 * kTile);
   p.gmax = take((size_t)bh * p.g.qtiles);
   p.vmax = take((size_t)bh * p.g.ktiles);
-  // dq and dk/dv partial sums are alive one after the other
-  const size_t q = p.dq_splits > 1 ? (size_t)p.dq_splits * p.g.B * p.g.Hq * p.g.Lq * D : 0;
   const size_t k = p.dkv_splits > 1 ? (size_t)p.dkv_splits * bh * p.g.Lk * D : 0;
-  p.part_q = p.part_k = at;
-  p.part_v = p.part_k + (k + 3) / 4 * 4;
-  at += q > 2 * ((k + 3) / 4 * 4) ? q : 2 * ((k + 3) / 4 * 4);
+  p.part_k = take(k);
+  p.part_v = take(k);
+  p.part_q = take(p.dq_splits > 1 ? (size_t)p.dq_splits * p.g.B * p.g.Hq * p.g.Lq * D : 0);
   p.total = at;
   return p;
 }
@@ -1361,26 +1370,6 @@ int launch_attn_tc_backward(const fconv_attn_desc& d, int sms, const AttnArgs& a
     e = bf ? start<2>(attn_tc_dkv<true, 2>, dkv_smem<2>(), b.items, sms, b, m, s)
            : start<2>(attn_tc_dkv<false, 2>, dkv_smem<2>(), b.items, sms, b, m, s);
   if (e) return e;
-  if (b.splits > 1) {
-    JoinArgs j{};
-    j.part[0] = b.part1;
-    j.part[1] = b.part2;
-    j.out[0] = (uint16_t*)a.dk;
-    j.out[1] = (uint16_t*)a.dv;
-    for (int i = 0; i < 3; ++i) {
-      j.st[0][i] = d.dk_stride[i];
-      j.st[1][i] = d.dv_stride[i];
-    }
-    j.rows = bh * g.Lk;
-    j.len = g.Lk;
-    j.heads = g.Hk;
-    j.D = g.D;
-    j.splits = b.splits;
-    j.count = 2;
-    e = join(bf, j, sms, s);
-    if (e) return e;
-  }
-
   b.splits = p.dq_splits;
   b.per = (g.ktiles + b.splits - 1) / b.splits;
   b.items = (int)(bh * g.qtiles * b.splits);
@@ -1394,16 +1383,35 @@ int launch_attn_tc_backward(const fconv_attn_desc& d, int sms, const AttnArgs& a
   else
     e = bf ? start<1>(attn_tc_dq<true, 2>, dq_smem<2>(), b.items, sms, b, m, s)
            : start<1>(attn_tc_dq<false, 2>, dq_smem<2>(), b.items, sms, b, m, s);
-  if (e || b.splits == 1) return e;
+  if (e) return e;
+
   JoinArgs j{};
-  j.part[0] = j.part[1] = b.part1;
+  j.D = g.D;
+  if (p.dkv_splits > 1) {
+    j.part[0] = ws + p.part_k;
+    j.part[1] = ws + p.part_v;
+    j.out[0] = (uint16_t*)a.dk;
+    j.out[1] = (uint16_t*)a.dv;
+    for (int i = 0; i < 3; ++i) {
+      j.st[0][i] = d.dk_stride[i];
+      j.st[1][i] = d.dv_stride[i];
+    }
+    j.rows = bh * g.Lk;
+    j.len = g.Lk;
+    j.heads = g.Hk;
+    j.splits = p.dkv_splits;
+    j.count = 2;
+    e = join(bf, j, sms, s);
+    if (e) return e;
+  }
+  if (p.dq_splits == 1) return 0;
+  j.part[0] = j.part[1] = ws + p.part_q;
   j.out[0] = j.out[1] = (uint16_t*)a.dq;
   for (int i = 0; i < 3; ++i) j.st[0][i] = j.st[1][i] = d.dq_stride[i];
   j.rows = (int64_t)g.B * g.Hq * g.Lq;
   j.len = g.Lq;
   j.heads = g.Hq;
-  j.D = g.D;
-  j.splits = b.splits;
+  j.splits = p.dq_splits;
   j.count = 1;
   return join(bf, j, sms, s);
 }
