@@ -5,15 +5,19 @@
 //   s = scale q k^T,  p = softmax(s),  out = p v,  lse = log sum exp s
 //   p = exp(s - lse),  ds = p (dout v^T - delta),  dv = p^T dout,  dq = scale ds k,
 //   dk = scale ds^T q
-// An f32 value is the sum of hi, its 13 low mantissa bits cleared (a TF32 value), and lo = v - hi
-// (exact); a product is hi hi + hi lo + lo hi in three m16n8k8 TF32 instructions with f32
-// accumulators. What is dropped (lo lo, and lo's bits below TF32) is about 2^-20 of a product.
-// p and ds are split the same way: nothing is rounded to fewer bits.
+// An f32 value is the sum of hi, rounded to TF32, and lo = v - hi (exact, read as TF32); a
+// product is lo hi + hi lo + hi hi in three m16n8k8 TF32 instructions. What is dropped is about
+// 2^-23 of a product either way (hi cut off instead of rounded: 2^-21, always the same way). The
+// instructions' own f32 sums round towards zero, so they run over 16 products only and are then
+// added to the accumulator in plain f32. Against 64 bits the outputs are as near as those of
+// f32 FMAs in sequence (3e-7 to 5e-7 of their norm at the size below; 4e-6 with hi cut off and
+// one accumulator throughout, which took 435 us for a training pass instead of 461). p and ds
+// are split the same way: nothing is rounded to fewer bits.
 //
 // A block owns 64 rows (of queries, or of keys for dk and dv), a warp 16 of them and the columns
 // of a score tile in registers: all 64 for dk and dv, half of them in the other kernels, whose
-// accumulators leave room for twice the warps (the halves are joined at the end; a training
-// pass of the size below took 528 us without and takes 434). The score accumulator is the next
+// accumulators leave room for twice the warps (the halves are joined at the end; 528 -> 434 us a
+// training pass of the size below when it was made). The score accumulator is the next
 // product's A operand as it is: its column pair (2t, 2t + 1) of a lane takes the places of k = t
 // and k = t + 4, and the B operand is read with rows 2t and 2t + 1 to match. Tiles lie in shared
 // memory as f32 with rows of Dp + 4 floats, Dp a multiple of 8: both ways of reading a B operand
@@ -22,7 +26,7 @@
 // atomics.
 //
 // Bound: latency. 3 x 333 queries x 777 keys, 16 heads of 72, f32 (one sequence without keys,
-// one cut short): forward 90 us, delta 9, dq 120, dk and dv 210. A scheduler has four warps (two
+// one cut short): forward 96 us, delta 9, dq 133, dk and dv 230. A scheduler has four warps (two
 // for dk and dv, whose two accumulators fill the registers) to cover the time of the products
 // and of the shared-memory reads that feed them (a 4-byte operand a lane for 1.5 instructions).
 #include "attn_geom.cuh"
@@ -37,32 +41,48 @@ struct Split4 {
   uint32_t hi[4], lo[4];
 };
 __device__ __forceinline__ void split(float v, uint32_t& hi, uint32_t& lo) {
-  hi = __float_as_uint(v) & 0xffffe000u;
+  hi = (__float_as_uint(v) + 0x1000u) & 0xffffe000u;
   lo = __float_as_uint(v - __uint_as_float(hi));
 }
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
+                                         uint32_t b1, const float (&c)[4]) {
   asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      "{%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]),
+        "f"(c[2]), "f"(c[3]));
 }
-// d[n] += a b[n] for N independent accumulators, one kind of product after the other: an
-// accumulator is used again only N instructions later.
-template <int N>
-__device__ __forceinline__ void mma3(float (*d)[4], const Split4& a, const float (&b)[N][2]) {
+// x[n] = a b[n], or x[n] += a b[n], for N sums, one kind of product after the other: a sum is
+// used again only N instructions later.
+template <bool FIRST, int N>
+__device__ __forceinline__ void mma3(float (&x)[N][4], const Split4& a, const float (&b)[N][2]) {
   uint32_t h[N][2], l[N][2];
+  const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     split(b[n][0], h[n][0], l[n][0]);
     split(b[n][1], h[n][1], l[n][1]);
   }
 #pragma unroll
-  for (int n = 0; n < N; ++n) mma_tf32(d[n], a.lo, h[n][0], h[n][1]);
+  for (int n = 0; n < N; ++n) {
+    if (FIRST) mma_tf32(x[n], a.lo, h[n][0], h[n][1], zero);
+    else mma_tf32(x[n], a.lo, h[n][0], h[n][1], x[n]);
+  }
 #pragma unroll
-  for (int n = 0; n < N; ++n) mma_tf32(d[n], a.hi, l[n][0], l[n][1]);
+  for (int n = 0; n < N; ++n) mma_tf32(x[n], a.hi, l[n][0], l[n][1], x[n]);
 #pragma unroll
-  for (int n = 0; n < N; ++n) mma_tf32(d[n], a.hi, h[n][0], h[n][1]);
+  for (int n = 0; n < N; ++n) mma_tf32(x[n], a.hi, h[n][0], h[n][1], x[n]);
+}
+template <int N>
+__device__ __forceinline__ void add_to(float (*d)[4], const float (&x)[N][4]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      const uint64_t v = add2(pair(d[n][e], d[n][e + 1]), pair(x[n][e], x[n][e + 1]));
+      d[n][e] = low(v);
+      d[n][e + 1] = high(v);
+    }
 }
 
 // s = a b^T over d for 16 rows of a (this warp's) and 8 N rows of b.
@@ -73,24 +93,45 @@ __device__ __forceinline__ void scores(float (&s)[N][4], const float* a, const f
   for (int n = 0; n < N; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
-#pragma unroll 2
-  for (int k = 0; k < nd; ++k) {
-    const float* ap = a + gr * pitch + k * 8 + t;
-    Split4 x;
-    split(ap[0], x.hi[0], x.lo[0]);
-    split(ap[8 * pitch], x.hi[1], x.lo[1]);
-    split(ap[4], x.hi[2], x.lo[2]);
-    split(ap[8 * pitch + 4], x.hi[3], x.lo[3]);
-    const float* bp = b + gr * pitch + k * 8 + t;
+  const float* ap = a + gr * pitch + t;
+  const float* bp = b + gr * pitch + t;
+  auto rows = [&](Split4& x, int k) {
+    split(ap[k * 8], x.hi[0], x.lo[0]);
+    split(ap[8 * pitch + k * 8], x.hi[1], x.lo[1]);
+    split(ap[k * 8 + 4], x.hi[2], x.lo[2]);
+    split(ap[8 * pitch + k * 8 + 4], x.hi[3], x.lo[3]);
+  };
+  auto cols = [&](float (&y)[4][2], int n, int k) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[i][0] = bp[(n + i) * 8 * pitch + k * 8];
+      y[i][1] = bp[(n + i) * 8 * pitch + k * 8 + 4];
+    }
+  };
+  int k = 0;
+  for (; k + 1 < nd; k += 2) {
+    Split4 x[2];
+    rows(x[0], k);
+    rows(x[1], k + 1);
 #pragma unroll
     for (int n = 0; n < N; n += 4) {
-      float y[4][2];
+      float y[4][2], z[4][4];
+      cols(y, n, k);
+      mma3<true>(z, x[0], y);
+      cols(y, n, k + 1);
+      mma3<false>(z, x[1], y);
+      add_to(s + n, z);
+    }
+  }
+  if (k < nd) {
+    Split4 x;
+    rows(x, k);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        y[i][0] = bp[(n + i) * 8 * pitch];
-        y[i][1] = bp[(n + i) * 8 * pitch + 4];
-      }
-      mma3<4>(s + n, x, y);
+    for (int n = 0; n < N; n += 4) {
+      float y[4][2], z[4][4];
+      cols(y, n, k);
+      mma3<true>(z, x, y);
+      add_to(s + n, z);
     }
   }
 }
@@ -101,25 +142,34 @@ __device__ __forceinline__ void mix(float (&acc)[NT][4], const float (&p)[N][4],
                                     int nd, int pitch, int gr, int t) {
   constexpr int GS = NT % 3 == 0 ? 3 : 4;
 #pragma unroll
-  for (int k = 0; k < N; ++k) {
-    Split4 x;
-    split(p[k][0], x.hi[0], x.lo[0]);
-    split(p[k][2], x.hi[1], x.lo[1]);
-    split(p[k][1], x.hi[2], x.lo[2]);
-    split(p[k][3], x.hi[3], x.lo[3]);
+  for (int k = 0; k < N; k += 2) {
+    Split4 x[2];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      split(p[k + w][0], x[w].hi[0], x[w].lo[0]);
+      split(p[k + w][2], x[w].hi[1], x[w].lo[1]);
+      split(p[k + w][1], x[w].hi[2], x[w].lo[2]);
+      split(p[k + w][3], x[w].hi[3], x[w].lo[3]);
+    }
     const float* bp = b + (k * 8 + 2 * t) * pitch + gr;
 #pragma unroll
     for (int n = 0; n < NT; n += GS) {
       if (n >= nd) break;
-      float y[GS][2];
+      float z[GS][4];
 #pragma unroll
-      for (int i = 0; i < GS; ++i) {
-        // past the row's end: its own first columns, into accumulators that no one reads
-        const int at = n + i < nd ? (n + i) * 8 : 0;
-        y[i][0] = bp[at];
-        y[i][1] = bp[pitch + at];
+      for (int w = 0; w < 2; ++w) {
+        float y[GS][2];
+#pragma unroll
+        for (int i = 0; i < GS; ++i) {
+          // past the row's end: its own first columns, into accumulators that no one reads
+          const int at = w * 8 * pitch + (n + i < nd ? (n + i) * 8 : 0);
+          y[i][0] = bp[at];
+          y[i][1] = bp[pitch + at];
+        }
+        if (w == 0) mma3<true>(z, x[0], y);
+        else mma3<false>(z, x[1], y);
       }
-      mma3<GS>(acc + n, x, y);
+      add_to(acc + n, z);
     }
   }
 }
