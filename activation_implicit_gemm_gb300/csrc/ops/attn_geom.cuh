@@ -4,6 +4,7 @@
 
 #include <cmath>
 
+#include "../fconv_internal.h"
 #include "../ptx.cuh"
 #include "ops_common.cuh"
 #include "ops_internal.h"
@@ -30,8 +31,8 @@ struct Lens {
 };
 __device__ __forceinline__ Lens lens_of(const Geom& g, int64_t b) {
   Lens l;
-  l.q = g.q_lens ? g.q_lens[b] : g.Lq;
-  l.k = g.kv_lens ? g.kv_lens[b] : g.Lk;
+  l.q = g.q_lens ? __ldcg(g.q_lens + b) : g.Lq;
+  l.k = g.kv_lens ? __ldcg(g.kv_lens + b) : g.Lk;
   l.q = l.q < 0 ? 0 : l.q > g.Lq ? g.Lq : l.q;
   l.k = l.k < 0 ? 0 : l.k > g.Lk ? g.Lk : l.k;
   l.shift = l.k - l.q;
@@ -58,7 +59,7 @@ __device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t row_
         ptx::cp_async16(ptx::smem_addr(dst + r * pitch + d), p + d, ok && d < g.D ? 16 : 0);
     } else {
       for (int d = lane; d < g.Dp; d += 32)
-        dst[r * pitch + d] = ok && d < g.D ? to_f(p[d]) : 0.0f;
+        dst[r * pitch + d] = ok && d < g.D ? to_f(__ldcg(p + d)) : 0.0f;
     }
   }
   ptx::cp_async_commit();
@@ -68,7 +69,8 @@ __device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t row_
 template <typename T>
 __global__ void __launch_bounds__(256)
     attn_delta(const T* __restrict__ o, const T* __restrict__ dout, float* delta,
-                      const Geom g) {
+               const Geom g) {
+  ptx::pdl_wait();
   const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= g.B * g.Hq * g.Lq) return;
   const int64_t i = row % g.Lq, bh = row / g.Lq;

@@ -17,9 +17,9 @@
 // the 16 x 16 threads computes an R x R piece of the BT x BT scores (R = BT / 16). Bound: the
 // f32 FMA lanes (4 D FLOPs a pair forward, 14 D backward with the scores made twice) and the
 // shared-memory reads that feed them: an 8-byte operand for 4 FMAs. 4 x 1024 tokens of 8 heads of
-// 256, f32: forward 3.80 ms (9 TFLOP/s of 80), backward 10.9 ms (8 counted, 11 as run). No listed
-// use of these lengths has come up; a tile that is split between the warps as in k_attn_mma.cu
-// would be the next step.
+// 256, f32: forward 3.80 ms (9 TFLOP/s of 80), backward 10.9 ms (8 counted, 11 as run). Head
+// lengths over 128 are not among the measured workloads; tiles split between the warps as in
+// k_attn_mma.cu would be the next step.
 #include "attn_geom.cuh"
 
 namespace fconv {

@@ -11,8 +11,7 @@
 // instructions' own f32 sums round towards zero, so they run over 16 products only and are then
 // added to the accumulator in plain f32. Against 64 bits the outputs are as near as those of
 // f32 FMAs in sequence (3e-7 to 5e-7 of their norm at the size below; 4e-6 with hi cut off and
-// one accumulator throughout, which took 435 us for a training pass instead of 461). p and ds
-// are split the same way: nothing is rounded to fewer bits.
+// one accumulator throughout, at 0.94 of the time). p and ds are split the same way: nothing is rounded to fewer bits.
 //
 // A block owns 64 rows (of queries, or of keys for dk and dv), a warp 16 of them and the columns
 // of a score tile in registers: all 64 for dk and dv, half of them in the other kernels, whose
@@ -23,10 +22,13 @@
 // memory as f32 with rows of Dp + 4 floats, Dp a multiple of 8: both ways of reading a B operand
 // (along a row, and down two rows) then touch all 32 banks. The next tile is on its way while the
 // current one's products run. As in the other routes every gradient has one writer and no
-// atomics.
+// atomics. dq needs nothing of dk and dv: its kernel is launched after theirs but takes the SMs as
+// their blocks leave them (it reads what the delta pass wrote, which theirs has waited for, from
+// L2) and waits for them only before it ends: 461 -> 383 us a training pass of the size below.
 //
 // Bound: latency. 3 x 333 queries x 777 keys, 16 heads of 72, f32 (one sequence without keys,
-// one cut short): forward 96 us, delta 9, dq 133, dk and dv 230. A scheduler has four warps (two
+// one cut short): forward 96 us, delta 9, dk and dv 230 and
+// dq 133 alone, 383 for the pass. A scheduler has four warps (two
 // for dk and dv, whose two accumulators fill the registers) to cover the time of the products
 // and of the shared-memory reads that feed them (a 4-byte operand a lane for 1.5 instructions).
 #include "attn_geom.cuh"
@@ -359,8 +361,8 @@ __global__ void __launch_bounds__(256, 2)
   for (int r = 0; r < 2; ++r) {
     const int64_t i = i0 + warp * 16 + gr + 8 * r, at = (b * g.Hq + h) * g.Lq + i;
     const bool in = i < L.q;
-    ls[r] = in ? lse[at] * kLog2e : 0.0f;
-    del[r] = in ? delta[at] : 0.0f;
+    ls[r] = in ? __ldcg(lse + at) * kLog2e : 0.0f;
+    del[r] = in ? __ldcg(delta + at) : 0.0f;
     end[r] = in ? (g.causal && i + L.shift + 1 < L.k ? i + L.shift + 1 : L.k) : 0;
   }
   for (int64_t j0 = 0; j0 < nk; j0 += kCols) {
@@ -401,6 +403,7 @@ __global__ void __launch_bounds__(256, 2)
   const float mul[2] = {g.scale, g.scale};
   store_rows<T, NT>(dq + b * g.dq[0] + h * g.dq[2], g.dq[1], i0 + warp * 16, g.Lq, acc, mul, g.D,
                     gr, t);
+  ptx::pdl_wait();  // attn_mma_dkv: what follows this kernel follows both
 }
 
 template <typename T, int NT, bool VEC>
@@ -409,6 +412,8 @@ __global__ void __launch_bounds__(128)
                  const T* __restrict__ dout, const float* __restrict__ lse,
                  const float* __restrict__ delta, T* __restrict__ dk, T* __restrict__ dv,
                  const Geom g) {
+  ptx::pdl_wait();
+  ptx::pdl_trigger();  // attn_mma_dq's blocks fill the SMs as this kernel's leave them
   extern __shared__ float4 smem4[];
   __shared__ float ls[kCols], del[kCols];  // -lse (log2) and delta of the tile's queries
   const int pitch = g.Dp + 4, nd = g.Dp / 8;
@@ -520,26 +525,29 @@ int backward_t(const Geom& g, const AttnArgs& a, cudaStream_t s) {
   const long long bk = g.B * g.Hk * ((g.Lk + kRows - 1) / kRows);
   float* delta = (float*)a.ws;
   const size_t smem = tile_bytes(g, 4);
-  if (rows > 0) {
-    auto kern = attn_mma_dq<T, NT, VEC>;
-    const int e = allow_smem((const void*)kern, smem);
-    if (e) return e;
-    if (!grid_ok((rows + 7) / 8) || !grid_ok(bq)) return (int)cudaErrorInvalidValue;
-    attn_delta<T><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>((const T*)a.out, (const T*)a.dout,
-                                                             delta, g);
-    kern<<<(unsigned)bq, 256, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v,
-                                                 (const T*)a.dout, a.lse, delta, (T*)a.dq, g);
-  }
-  if (bk > 0) {
+  int e = 0;
+  if ((rows > 0 && (!grid_ok((rows + 7) / 8) || !grid_ok(bq))) || (bk > 0 && !grid_ok(bk)))
+    return (int)cudaErrorInvalidValue;
+  if (rows > 0)
+    e = launch_pdl(attn_delta<T>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s,
+                   (const T*)a.out, (const T*)a.dout, delta, g);
+  if (!e && bk > 0) {
     auto kern = attn_mma_dkv<T, NT, VEC>;
-    const int e = allow_smem((const void*)kern, smem);
-    if (e) return e;
-    if (!grid_ok(bk)) return (int)cudaErrorInvalidValue;
-    kern<<<(unsigned)bk, 128, smem, s>>>((const T*)a.q, (const T*)a.k, (const T*)a.v,
-                                                 (const T*)a.dout, a.lse, delta, (T*)a.dk,
-                                                 (T*)a.dv, g);
+    e = allow_smem((const void*)kern, smem);
+    if (!e)
+      e = launch_pdl(kern, dim3((unsigned)bk), dim3(128), smem, s, (const T*)a.q, (const T*)a.k,
+                     (const T*)a.v, (const T*)a.dout, (const float*)a.lse, (const float*)delta,
+                     (T*)a.dk, (T*)a.dv, g);
   }
-  return (int)cudaGetLastError();
+  if (!e && rows > 0) {
+    auto kern = attn_mma_dq<T, NT, VEC>;
+    e = allow_smem((const void*)kern, smem);
+    if (!e)
+      e = launch_pdl(kern, dim3((unsigned)bq), dim3(256), smem, s, (const T*)a.q, (const T*)a.k,
+                     (const T*)a.v, (const T*)a.dout, (const float*)a.lse, (const float*)delta,
+                     (T*)a.dq, g);
+  }
+  return e;
 }
 
 // NT: 8-column tiles of head_dim in registers, fitted for f32 rows of whole 16-byte units, the
