@@ -11,7 +11,8 @@
 // instructions' own f32 sums round towards zero, so they run over 16 products only and are then
 // added to the accumulator in plain f32. Against 64 bits the outputs are as near as those of
 // f32 FMAs in sequence (3e-7 to 5e-7 of their norm at the size below; 4e-6 with hi cut off and
-// one accumulator throughout, at 0.94 of the time). p and ds are split the same way: nothing is rounded to fewer bits.
+// one accumulator throughout, at 0.94 of the time). p and ds are split the same way: nothing is
+// rounded to fewer bits.
 //
 // A block owns 64 rows (of queries, or of keys for dk and dv), a warp 16 of them and the columns
 // of a score tile in registers: all 64 for dk and dv, half of them in the other kernels, whose
@@ -27,10 +28,10 @@
 // L2) and waits for them only before it ends: 461 -> 383 us a training pass of the size below.
 //
 // Bound: latency. 3 x 333 queries x 777 keys, 16 heads of 72, f32 (one sequence without keys,
-// one cut short): forward 96 us, delta 9, dk and dv 230 and
-// dq 133 alone, 383 for the pass. A scheduler has four warps (two
-// for dk and dv, whose two accumulators fill the registers) to cover the time of the products
-// and of the shared-memory reads that feed them (a 4-byte operand a lane for 1.5 instructions).
+// one cut short): forward 96 us, delta 9, dk and dv 230 and dq 133 by themselves, 383 for
+// the pass. A scheduler has four warps (two for dk and dv, whose two accumulators fill the
+// registers) to cover the time of the products and of the shared-memory reads that feed them (a
+// 4-byte operand a lane for 1.5 instructions).
 #include "attn_geom.cuh"
 
 namespace fconv {
