@@ -22,7 +22,7 @@ import activation_implicit_gemm_gb300 as fc  # noqa: E402
 
 
 def new_params(channels, heads, patch, seed=0, device="cuda"):
-    """Parameters in f16 as the block uses them, norms' in f32."""
+    """Parameters in f16 as the block uses them, norms' in f32, and the positions' frequencies."""
     g = torch.Generator().manual_seed(seed)
 
     def normal(*shape, scale):
@@ -35,7 +35,13 @@ def new_params(channels, heads, patch, seed=0, device="cuda"):
         "norm_w": torch.ones(c, device=device), "norm_b": torch.zeros(c, device=device),
         "qkv": normal(3 * c, c, scale=c ** -0.5), "proj": normal(c, c, scale=c ** -0.5),
         "probe": normal(1, 1, heads, c // heads, scale=1.0),
+        "freq": fc.rope_frequencies(sections(c // heads), device=device),
     }
+
+
+def sections(head_dim):
+    """The pairs of a head that turn by the row and by the column."""
+    return (head_dim // 4, head_dim // 2 - head_dim // 4)
 
 
 def grid_positions(rows, columns, device="cuda"):
@@ -58,8 +64,7 @@ def forward(p, images, heads):
     qkv = (h @ p["qkv"].t()).view(n, rows * columns, 3, heads, d)
     q, k, v = qkv.unbind(2)
     turn = {"positions": grid_positions(rows, columns, images.device),
-            "sections": (d // 4, d // 2 - d // 4)}
-    turn["inv_freq"] = fc.rope_frequencies(turn["sections"], device=images.device)
+            "inv_freq": p["freq"], "sections": sections(d)}
     fc.rope(q, k, **turn, out=q, k_out=k)
     a, lse = fc.attention(q, k, v, return_lse=True)
     y = x + a.view(n, -1, c) @ p["proj"].t()

@@ -148,7 +148,8 @@ fconv_status fconv_attn_forward(const fconv_attn_plan* plan, const void* q, cons
                                 const void* v, const int32_t* q_lens, const int32_t* kv_lens,
                                 void* out, float* lse, void* workspace, size_t workspace_bytes,
                                 void* stream);
-/* out and lse are the forward pass's. Gradients of tokens past their lengths are zero. */
+/* out and lse are the forward pass's. Gradients of tokens past their lengths are zero. dq, dk
+ * and dv must not overlap each other or an input. */
 fconv_status fconv_attn_backward(const fconv_attn_plan* plan, const void* dout, const void* q,
                                  const void* k, const void* v, const void* out, const float* lse,
                                  const int32_t* q_lens, const int32_t* kv_lens, void* dq,

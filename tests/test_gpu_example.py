@@ -92,3 +92,34 @@ def test_loss_falls(example):
     target = torch.randn(4, 64, generator=g).cuda()
     losses = [example.step(p, images, target, 2, 2.0).item() for _ in range(10)]
     assert losses[-1] < losses[0]
+
+
+def test_captured_in_a_graph(example):
+    """The block's kernels (those that start beside their predecessor too) replayed from a CUDA
+    graph on new inputs, against direct calls."""
+    p = example.new_params(128, 2, 16, seed=7)
+    g = torch.Generator().manual_seed(8)
+    images = [torch.randn(3, 3, 64, 80, generator=g).half().cuda() for _ in range(3)]
+    up = torch.randn(3, 128, generator=g).half().cuda()
+
+    def run(x):
+        pooled, kept = example.forward(p, x, 2)
+        grads = example.backward(p, kept, up)
+        return [pooled] + [grads[k] for k in sorted(grads)]
+
+    x = images[0].clone()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        for _ in range(3):
+            run(x)
+    torch.cuda.current_stream().wait_stream(stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(x)
+    for image in images:
+        x.copy_(image)
+        graph.replay()
+        got = [t.clone() for t in out]
+        for a, b in zip(got, run(image)):
+            assert torch.equal(a, b)
