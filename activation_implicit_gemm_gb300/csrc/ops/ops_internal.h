@@ -56,10 +56,10 @@ struct AttnArgs {
   void* dv;
   void* ws;
 };
-// The route without tcgen05: warp-level tensor instructions up to a head length of 128
-// (k_attn_mma.cu), CUDA cores beyond (k_attn_fma.cu).
-int launch_attn_fma_forward(const fconv_attn_desc& d, const AttnArgs& a, cudaStream_t s);
-int launch_attn_fma_backward(const fconv_attn_desc& d, const AttnArgs& a, cudaStream_t s);
+// The route without tcgen05: warp-level tensor instructions, for head lengths up to 128 in
+// k_attn_mma.cu and beyond in k_attn_mma_wide.cu.
+int launch_attn_wide_forward(const fconv_attn_desc& d, const AttnArgs& a, cudaStream_t s);
+int launch_attn_wide_backward(const fconv_attn_desc& d, const AttnArgs& a, cudaStream_t s);
 int launch_attn_simple_forward(const fconv_attn_desc& d, const AttnArgs& a, cudaStream_t s);
 int launch_attn_simple_backward(const fconv_attn_desc& d, const AttnArgs& a, cudaStream_t s);
 size_t attn_simple_backward_workspace(const fconv_attn_desc& d);

@@ -128,7 +128,7 @@ typedef struct {
 typedef enum {
   FCONV_ATTN_AUTO = 0,
   FCONV_ATTN_SIMPLE = 1, /* every type, head_dim, stride: warp-level tensor instructions in split
-                            f32 (CUDA cores for head_dim over 128) */
+                            f32 */
   FCONV_ATTN_TC = 2      /* tcgen05 tensor cores: f16 and bf16, head_dim a multiple of 8 up to
                             128, 16-byte strides and addresses */
 } fconv_attn_route;

@@ -302,3 +302,15 @@ def test_many_tiles_and_items_a_block(D, causal):
         a, b = many[:, :, :1].double(), single.double()
         assert (a - b).norm() <= 4 * R.U[torch.bfloat16] * b.norm(), name
     assert torch.equal(lse, lse[:, :1].expand_as(lse))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("B,Lq,Lk,H,K,D,causal,kl", [
+    (2, 70, 200, 4, 2, 256, True, [200, 65]), (1, 129, 129, 2, 2, 136, False, None),
+    (3, 33, 97, 3, 1, 192, False, [97, 0, 31]), (1, 1, 300, 8, 2, 256, True, None),
+    (2, 100, 40, 2, 1, 129, True, [40, 7]), (1, 65, 65, 1, 1, 251, True, None),
+])
+def test_head_lengths_over_128(B, Lq, Lk, H, K, D, causal, kl, dtype):
+    """Odd lengths, rows that are whole 16-byte units and ones that are not, several tiles of
+    queries and keys, keys cut short, queries without a key."""
+    run_and_check(*tensors(B, Lq, Lk, H, K, D, dtype), causal=causal, kv_lens=lens(kl))
