@@ -155,6 +155,14 @@ def _workspace(nbytes: int, like):
     return torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes else None
 
 
+def _new(like):
+    """An uninitialised contiguous tensor of this shape and type (empty_like is the quicker call,
+    but keeps the strides of what is not contiguous)."""
+    if like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -343,18 +351,21 @@ def rope(q, k=None, *, positions, inv_freq, sections: Optional[Sequence[int]] = 
                         pairing=pairing, inverse=inverse, out=out, k_out=k_out)
     device = q.get_device()
     _on_cuda("rope", device, k, positions, inv_freq, out, k_out)
+    given = out is not None or k_out is not None
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _new(q)
     if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        k_out = _new(k)
     sections = None if sections is None else tuple(sections)
     # everything the checks look at is in the key: a call like an earlier one has passed them
-    key = (q.dtype, q.shape, q.stride(), out.dtype, out.shape, out.stride(), positions.dtype,
-           positions.shape, positions.is_contiguous(), inv_freq.dtype, inv_freq.shape,
-           inv_freq.is_contiguous(), sections, pairing, inverse, device)
-    if k is not None or k_out is not None:
-        key += (None,) if k is None else (k.dtype, k.shape, k.stride(), k_out.dtype, k_out.shape,
-                                          k_out.stride())
+    # (new outputs follow from the inputs)
+    key = (q.dtype, q.shape, q.stride(), positions.dtype, positions.shape,
+           positions.is_contiguous(), inv_freq.dtype, inv_freq.shape, inv_freq.is_contiguous(),
+           sections, pairing, inverse, device,
+           None if k is None else (k.dtype, k.shape, k.stride()))
+    if given:
+        key += (out.dtype, out.shape, out.stride(),
+                None if k_out is None else (k_out.dtype, k_out.shape, k_out.stride()))
     p = _rope_plans.get(key)
     if p is None:
         p = _rope_plans[key] = _rope_plan(q, k, positions, inv_freq, sections, pairing, inverse,
@@ -505,7 +516,7 @@ def attention(q, k, v, *, causal: bool = False, scale: Optional[float] = None, q
     device = q.get_device()
     _on_cuda("attention", device, k, v, q_lens, kv_lens, out)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _new(q)
     p = _attn_plan("attention", q, k, v, out, causal, scale, q_lens, kv_lens, route, device)
     lse = None
     if return_lse:
@@ -531,9 +542,9 @@ def attention_backward(dout, q, k, v, out, lse, *, causal: bool = False,
                                       route=route)
     device = q.get_device()
     _on_cuda("attention_backward", device, k, v, dout, out, lse, q_lens, kv_lens, dq, dk, dv)
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
-    dk = torch.empty(k.shape, dtype=k.dtype, device=q.device) if dk is None else dk
-    dv = torch.empty(v.shape, dtype=v.dtype, device=q.device) if dv is None else dv
+    dq = _new(q) if dq is None else dq
+    dk = _new(k) if dk is None else dk
+    dv = _new(v) if dv is None else dv
     p = _attn_plan("attention_backward", q, k, v, out, causal, scale, q_lens, kv_lens, route,
                    device, (dout, dq, dk, dv))
     if lse.shape != p.lse_shape or lse.dtype != torch.float32 or not lse.is_contiguous():
