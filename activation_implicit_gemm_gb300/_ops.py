@@ -145,6 +145,15 @@ def _on_cuda(who: str, device: int, *tensors) -> None:
     raise ValueError(f"{who} runs on tensors of one CUDA device only")
 
 
+def _on_stream(stream, *tensors):
+    """The context of a call on `stream`. The tensors it is given stay allocated until the work
+    enqueued there is done, whichever stream they come from."""
+    for t in tensors:
+        if t is not None and t.is_cuda:  # the call refuses others
+            t.record_stream(stream)
+    return torch.cuda.stream(stream)
+
+
 def _current_stream(device: int) -> int:
     """The handle of the device's current stream; the plain handle spares building a Stream
     object (2 us of the call's 10)."""
@@ -229,7 +238,7 @@ def layer_norm(x, weight=None, bias=None, *, axis: int = -1, eps: float = 1e-5, 
     if torch is None:
         _start()
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, x, weight, bias, out):
             return layer_norm(x, weight, bias, axis=axis, eps=eps, out=out,
                               return_stats=return_stats)
     device = x.get_device()
@@ -258,7 +267,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, bias=None, *, axis: int 
     if torch is None:
         _start()
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, dy, x, mean, rstd, weight, bias):
             return layer_norm_backward(dy, x, mean, rstd, weight, bias, axis=axis,
                                        param_grads=param_grads)
     device = x.get_device()
@@ -346,7 +355,7 @@ def rope(q, k=None, *, positions, inv_freq, sections: Optional[Sequence[int]] = 
     if torch is None:
         _start()
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, q, k, positions, inv_freq, out, k_out):
             return rope(q, k, positions=positions, inv_freq=inv_freq, sections=sections,
                         pairing=pairing, inverse=inverse, out=out, k_out=k_out)
     device = q.get_device()
@@ -510,7 +519,7 @@ def attention(q, k, v, *, causal: bool = False, scale: Optional[float] = None, q
     if torch is None:
         _start()
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, q, k, v, q_lens, kv_lens, out):
             return attention(q, k, v, causal=causal, scale=scale, q_lens=q_lens, kv_lens=kv_lens,
                              out=out, return_lse=return_lse, route=route)
     device = q.get_device()
@@ -536,7 +545,7 @@ def attention_backward(dout, q, k, v, out, lse, *, causal: bool = False,
     if torch is None:
         _start()
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on_stream(stream, dout, q, k, v, out, lse, q_lens, kv_lens, dq, dk, dv):
             return attention_backward(dout, q, k, v, out, lse, causal=causal, scale=scale,
                                       q_lens=q_lens, kv_lens=kv_lens, dq=dq, dk=dk, dv=dv,
                                       route=route)

@@ -189,3 +189,19 @@ def test_offsets_past_32_bits():
     dy = x
     dx, _, _ = fc.layer_norm_backward(dy, x, mean, rstd)
     R.check(dx[-4:], *R.layer_norm_backward(tail, tail, None, None, -1, 1e-5)["dx"], "dx")
+
+
+def test_inputs_given_back_before_a_side_stream_runs():
+    """A call on another stream than its input's: the input may be dropped while the work still
+    waits there, and what takes the memory next does not reach the result."""
+    x = R.normal(31, (512, 1024), torch.float32).cuda()
+    want = fc.layer_norm(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    got = fc.layer_norm(x, stream=side)
+    del x
+    again = [torch.full((512, 1024), float("nan"), device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and len(again) == 4
