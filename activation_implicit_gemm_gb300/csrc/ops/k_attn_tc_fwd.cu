@@ -27,7 +27,7 @@
 // sequences. 16384 tokens, 16 heads of 128, bf16: 1.33 ms, 1660 TFLOP/s, 0.98 of what a long run
 // of library products keeps up; head length 64 has the same exponentials for half the products
 // (4 x 4096 tokens, 16 heads: 280 us, 980 TFLOP/s). One query and up to 8192 keys of 16
-// sequences, 8 key heads of 128 for 32: 63 us and 8 for the join, 5.5 TB/s. 196 tokens of 12
+// sequences, 8 key heads of 128 for 32: 64 us and 6 for the join, 5.4 TB/s. 196 tokens of 12
 // heads of 64: 8.9 us, one tile's chain of two key tiles.
 // Signalling each half of a tile's probabilities as it is ready (so that P V starts earlier) ran
 // 3 % slower at a head length of 128 and 1.5 % faster at 64: not done.
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the key splits of a row: out = sum_s w_s part_s / sum_s w_s, w_s = 2^(lse_s - max).
-// One warp per row, splits in order.
+// One warp per row, splits in order, eight at a time on their way (8.3 -> 6.1 us for 512 rows).
 template <bool BF16>
 __global__ void __launch_bounds__(256) attn_tc_join(const FwdArgs a) {
   ptx::pdl_wait();
@@ -574,18 +574,29 @@ __global__ void __launch_bounds__(256) attn_tc_join(const FwdArgs a) {
   float total = 0.0f;
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   const int d = lane * 4;
-  for (int s = 0; s < a.parts; ++s) {
-    const float lse = a.part_lse[(int64_t)s * rows + at];
-    if (lse == -INFINITY) continue;
-    const float w = exp2f(lse - ref);
-    total += w;
-    if (d < g.D) {
-      const float4 p =
-          *reinterpret_cast<const float4*>(a.part + ((int64_t)s * rows + at) * g.D + d);
-      acc[0] = fmaf(w, p.x, acc[0]);
-      acc[1] = fmaf(w, p.y, acc[1]);
-      acc[2] = fmaf(w, p.z, acc[2]);
-      acc[3] = fmaf(w, p.w, acc[3]);
+  for (int s0 = 0; s0 < a.parts; s0 += 32) {
+    const int n = min(32, a.parts - s0);
+    const float mine =
+        lane < n ? exp2f(a.part_lse[(int64_t)(s0 + lane) * rows + at] - ref) : 0.0f;
+    for (int s = 0; s < n; s += 8) {  // eight loads in flight
+      float w[8];
+      float4 p[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        w[i] = __shfl_sync(0xffffffffu, mine, s + i);
+        p[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (w[i] != 0.0f && d < g.D)  // a split without keys has written nothing
+          p[i] = *reinterpret_cast<const float4*>(a.part + ((int64_t)(s0 + s + i) * rows + at) *
+                                                               g.D + d);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        total += w[i];
+        acc[0] = fmaf(w[i], p[i].x, acc[0]);
+        acc[1] = fmaf(w[i], p[i].y, acc[1]);
+        acc[2] = fmaf(w[i], p[i].z, acc[2]);
+        acc[3] = fmaf(w[i], p[i].w, acc[3]);
+      }
     }
   }
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
