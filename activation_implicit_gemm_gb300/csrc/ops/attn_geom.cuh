@@ -43,7 +43,8 @@ __device__ __forceinline__ Lens lens_of(const Geom& g, int64_t b) {
 // rows outside [lo, hi) become zeros, so what the tensors hold there never enters a product.
 // Each of the block's WARPS warps takes every WARPS-th row. f32 rows of whole 16-byte units are
 // copied asynchronously (VEC; complete after cp_async_wait and a barrier), others go through
-// registers.
+// registers. Both read L2: attn_mma_dq loads its tiles before it waits for the launch before it,
+// and nothing orders its SM's L1 after what wrote them.
 template <typename T, int BT, int WARPS, bool VEC>
 __device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t row_stride,
                                           int64_t row0, int64_t lo, int64_t hi, const Geom& g) {
@@ -56,7 +57,7 @@ __device__ __forceinline__ void load_tile(float* dst, const T* src, int64_t row_
     const T* p = src + (ok ? row * row_stride : 0);
     if (VEC) {
       for (int d = lane * 4; d < g.Dp; d += 128)
-        ptx::cp_async16(ptx::smem_addr(dst + r * pitch + d), p + d, ok && d < g.D ? 16 : 0);
+        ptx::cp_async16_l2(ptx::smem_addr(dst + r * pitch + d), p + d, ok && d < g.D ? 16 : 0);
     } else {
       for (int d = lane; d < g.Dp; d += 32)
         dst[r * pitch + d] = ok && d < g.D ? to_f(__ldcg(p + d)) : 0.0f;
