@@ -8,10 +8,13 @@
 //   O_t += P_t V (P from TMEM, V from shared memory as the MN-major operand)
 // The two tiles share every K and V tile and take turns: while the 128 softmax threads of one
 // tile work (a thread owns a row: no shuffles), the tensor core runs P V and the next Q K^T of
-// the other. m is the running row maximum; O and the row sum are rescaled only when it grew by
-// more than 8 in log2 (the sums stay below 2^8 times their final size, far inside f32, and P
-// below 2^8, inside f16), which is exact in the same way as rescaling always: m cancels in O / l.
-// P's rounding is the only one before the output's; the row sum adds the unrounded values.
+// the other. m is the running row maximum, less kLift; O and the row sum are rescaled only when
+// it grew by more than 8 in log2 (the sums stay below 2^15 times their final size, far inside f32,
+// and P below 2^(8 + kLift), inside its type), which is exact in the same way as rescaling always:
+// m cancels in O / l. P's rounding is the only one before the output's; the row sum adds the
+// unrounded values. In f16 kLift is 7: a probability keeps all its bits down to 2^-21 of the row's
+// largest and some down to 2^-32, so that the keys under a dominant one that carries no value
+// still count (2^-14 and 2^-25 without it). bf16 has f32's range.
 //
 // Roles: warps 0-3 and 4-7 softmax and epilogue of tile 0 and 1, warp 8 MMA, warp 9 TMA (10 and
 // 11 only complete the warpgroup).
@@ -136,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = uni(tid >> 5), lane = tid & 31;
   const uint32_t own = ptx::smem_addr(dsmem);
   constexpr int kOwn = FOLD ? 1 : Plan::own, kSlots = FOLD ? Plan::fold_slots : Plan::slots;
+  constexpr float kLift = BF16 ? 0.0f : 7.0f;
   const uint32_t ring = own + (FOLD ? Plan::tile_bytes : Plan::ring_at);
   volatile int* abort_flag = &ctl.abort_flag;
 
@@ -423,7 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 1; e < 32; ++e) top[q] = fmaxf(top[q], __uint_as_float(s[q][e]));
         }
-        const float mn = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c);
+        const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        const float mn = fmaxf(m, fmaf(most, c, -kLift));
         if (__any_sync(0xffffffffu, mn > m + 8.0f)) {
           // the scores of this tile are complete, so every earlier P V is too
           const float f = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
