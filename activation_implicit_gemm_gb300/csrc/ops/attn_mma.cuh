@@ -12,7 +12,8 @@
 // added to the accumulator in plain f32. Against 64 bits the outputs are as near as those of
 // f32 FMAs in sequence (3e-7 to 5e-7 of their norm at the size below; 4e-6 with hi cut off and
 // one accumulator throughout, at 0.94 of the time). p and ds are split the same way: nothing is
-// rounded to fewer bits.
+// rounded to fewer bits, but that values under 2^-113 lose what of lo lies under TF32's smallest
+// step, 2^-136.
 //
 // A block owns 64 rows (of queries, or of keys for dk and dv), a warp 16 of them and the columns
 // of a score tile in registers: all of them for dk and dv, half in the other kernels, whose
@@ -43,12 +44,19 @@ namespace ops {
 namespace {
 
 constexpr int kRows = 64;
+constexpr float kLargestTf32 = 3.4011621342146535e38f;  // (2 - 2^-10) 2^127
 
 struct Split4 {
   uint32_t hi[4], lo[4];
 };
+// Values that would round past TF32's largest, and infinities, get the largest as hi: lo is then
+// what is missing, an infinity where v is one, and a product with it comes out infinite once
+// instead of as inf - inf (383 -> 408 us a training pass of the size above; the conversion
+// instruction that saturates took 499).
 __device__ __forceinline__ void split(float v, uint32_t& hi, uint32_t& lo) {
-  hi = (__float_as_uint(v) + 0x1000u) & 0xffffe000u;
+  float c;
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(c) : "f"(v), "f"(kLargestTf32));
+  hi = (__float_as_uint(c) + 0x1000u) & 0xffffe000u;
   lo = __float_as_uint(v - __uint_as_float(hi));
 }
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
