@@ -221,6 +221,12 @@ __device__ __forceinline__ void clear(float (&acc)[NT][4]) {
 template <int NT>
 constexpr int kColsOf = NT > 12 ? 32 : 64;
 
+// lse in log2 as the gradients subtract it. A row whose scores are all -inf has lse -inf and
+// probabilities of 0, not 2^(-inf + inf).
+__device__ __forceinline__ float lse_log2(float lse) {
+  return lse == -INFINITY ? INFINITY : lse * kLog2e;
+}
+
 // Keys [0, end) that the query rows [i0, i0 + kRows) need.
 __device__ __forceinline__ int64_t key_end(const Geom& g, const Lens& L, int64_t i0) {
   if (i0 >= L.q) return 0;
@@ -384,7 +390,7 @@ __global__ void __launch_bounds__(256, NT > 16 ? 1 : 2)
   for (int r = 0; r < 2; ++r) {
     const int64_t i = i0 + warp * 16 + gr + 8 * r, at = (b * g.Hq + h) * g.Lq + i;
     const bool in = i < L.q;
-    ls[r] = in ? __ldcg(lse + at) * kLog2e : 0.0f;
+    ls[r] = in ? lse_log2(__ldcg(lse + at)) : 0.0f;
     del[r] = in ? __ldcg(delta + at) : 0.0f;
     end[r] = in ? (g.causal && i + L.shift + 1 < L.k ? i + L.shift + 1 : L.k) : 0;
   }
@@ -441,7 +447,7 @@ __global__ void __launch_bounds__(128 * DH)
   ptx::pdl_trigger();  // attn_mma_dq's blocks fill the SMs as this kernel's leave them
   constexpr int kCols = kColsOf<NT * DH>, WARPS = 4 * DH;
   extern __shared__ float4 smem4[];
-  __shared__ float ls[kCols], del[kCols];  // -lse (log2) and delta of the tile's queries
+  __shared__ float ls[kCols], del[kCols];  // lse (log2) and delta of the tile's queries
   const int pitch = g.Dp + 4, nd = g.Dp / 8;
   float* ks = reinterpret_cast<float*>(smem4);
   float* vs = ks + kRows * pitch;
@@ -489,7 +495,7 @@ __global__ void __launch_bounds__(128 * DH)
     const int64_t i0 = row_of(n);
     if (threadIdx.x < kCols) {
       const int64_t i = i0 + threadIdx.x, at = (b * g.Hq + head_of(n)) * g.Lq + i;
-      ls[threadIdx.x] = i < L.q ? lse[at] * kLog2e : 0.0f;
+      ls[threadIdx.x] = i < L.q ? lse_log2(lse[at]) : 0.0f;
       del[threadIdx.x] = i < L.q ? delta[at] : 0.0f;
     }
     ptx::cp_async_wait<0>();

@@ -95,3 +95,22 @@ def test_queries_of_the_largest_size(B, Lq, Lk, H, K, D):
     want = R.attention(q, k, v, scale=2.0 ** -28)
     R.check(out, *want["out"], "out")
     R.check(lse, *want["lse"], "lse")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("route", ["auto", "simple"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_that_see_only_scores_of_minus_infinity(D, route, dtype):
+    """Every score of a sequence is -inf: its rows have out 0, lse -inf and no gradient, and the
+    other sequence is not touched."""
+    T = R.TYPES[dtype]
+    q, k, v, g = (t.to(T) for t in tensors(2, 70, 150, 4, 2, D))
+    q = q.abs() + 0.5
+    k[1] = -3.0e38
+    out, lse, dq, dk, dv = run(q, k, v, g, route=route)
+    want = R.attention(q[:1], k[:1], v[:1], dout=g[:1])
+    for name, t in zip(("out", "lse", "dq", "dk", "dv"), (out, lse, dq, dk, dv)):
+        R.check(t[:1], *want[name], name)
+    assert (lse[1] == -INF).all()
+    for t in (out, dq, dk, dv):
+        assert torch.count_nonzero(t[1]) == 0
