@@ -408,7 +408,8 @@ __global__ void __launch_bounds__(256, NT > 16 ? 1 : 2)
       for (int e = 0; e < 4; ++e) {
         const int r = e >> 1;
         const bool ok = j0 + half * (kCols / 2) + n * 8 + 2 * t + (e & 1) < end[r];
-        dp[n][e] = ok ? exp2f(s[n][e] * c - ls[r]) * (dp[n][e] - del[r]) : 0.0f;
+        const float p = ok ? exp2f(s[n][e] * c - ls[r]) : 0.0f;
+        dp[n][e] = p == 0.0f ? 0.0f : p * (dp[n][e] - del[r]);  // dp may not be finite there
       }
     mix(acc, dp, ks + half * (kCols / 2) * pitch, nd, pitch, gr, t);
     __syncthreads();

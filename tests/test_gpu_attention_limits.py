@@ -114,3 +114,21 @@ def test_rows_that_see_only_scores_of_minus_infinity(D, route, dtype):
     assert (lse[1] == -INF).all()
     for t in (out, dq, dk, dv):
         assert torch.count_nonzero(t[1]) == 0
+
+
+@pytest.mark.parametrize("B,Lq,Lk,H,K,D", SIZES)
+def test_keys_and_values_of_the_lowest_value(B, Lq, Lk, H, K, D):
+    """Slots filled with the lowest value in keys and values alike: probability 0, although the
+    product of the output gradient with such a value is not finite."""
+    q, k, v, g = tensors(B, Lq, Lk, H, K, D)
+    q = q.abs() + 0.5
+    hidden = torch.zeros(Lk, dtype=torch.bool)
+    hidden[10:30] = True
+    k[:, hidden], v[:, hidden] = LOWEST, LOWEST
+    got = run(q, k, v, g)
+    want = R.attention(q, k[:, ~hidden], v[:, ~hidden], dout=g)
+    for name, t in zip(("out", "lse", "dq", "dk", "dv"), got):
+        if name in ("dk", "dv"):
+            assert torch.count_nonzero(t[:, hidden]) == 0, name
+            t = t[:, ~hidden]
+        R.check(t, *want[name], name)
