@@ -215,8 +215,10 @@ def _norm_plan(who, x, weight, bias, axis, eps, device):
         param = weight if weight is not None else bias
         if weight is not None and bias is not None and weight.dtype != bias.dtype:
             raise ValueError(f"{who}: weight and bias must have one type")
-        p = LayerNormPlan(_code(x.dtype), math.prod(x.shape[:axis]), x.shape[axis],
-                          math.prod(x.shape[axis + 1:]),
+        outer, inner = math.prod(x.shape[:axis]), math.prod(x.shape[axis + 1:])
+        if inner == 0:  # no positions: as with no rows, nothing to normalise
+            outer, inner = 0, 1
+        p = LayerNormPlan(_code(x.dtype), outer, x.shape[axis], inner,
                           param_dtype=None if param is None else _code(param.dtype),
                           has_weight=weight is not None, has_bias=bias is not None, eps=eps,
                           device=device)
