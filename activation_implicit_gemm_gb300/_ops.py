@@ -350,8 +350,8 @@ def rope(q, k=None, *, positions, inv_freq, sections: Optional[Sequence[int]] = 
          pairing: str = "half", inverse: bool = False, out=None, k_out=None, stream=None):
     """Turn the pairs of q (batch, tokens, heads, head_dim), and of k in the same launch, by
     positions * inv_freq. positions is (tokens, axes), (1, tokens, axes) or (batch, tokens,
-    axes) of int32, int64 or float32, or without the last axis for one axis; sections gives the
-    pairs of each axis in order (default: all pairs on one axis). `inverse` turns back, which
+    axes) of int32, int64 or float32, the last one left out at will for one axis; sections gives
+    the pairs of each axis in order (default: all pairs on one axis). `inverse` turns back, which
     is the gradient. q and k may be strided views with a contiguous last axis; out and k_out
     may be q and k. Returns q', or (q', k')."""
     if torch is None:
@@ -391,11 +391,11 @@ def _rope_plan(q, k, positions, inv_freq, sections, pairing, inverse, out, k_out
     pos_type = {torch.int32: 0, torch.int64: 1, torch.float32: 2}.get(positions.dtype)
     if pos_type is None:
         raise FconvError(14, f"positions of {positions.dtype}")
-    shape = tuple(positions.shape)
     if sections is None:
         sections = (inv_freq.numel(),)
-        if len(shape) in (1, 2):
-            shape += (1,)
+    shape = tuple(positions.shape)
+    if len(sections) == 1 and shape in ((q.shape[1],), (1, q.shape[1]), tuple(q.shape[:2])):
+        shape += (1,)
     if len(shape) == 2:
         shape = (1,) + shape
     if (len(shape) != 3 or shape[0] not in (1, q.shape[0]) or shape[1] != q.shape[1]
