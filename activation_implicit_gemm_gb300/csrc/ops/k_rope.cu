@@ -8,7 +8,9 @@
 // The angle in turns is position * inv_freq / (2 pi). The f32 product alone would be off by up
 // to 2^-24 of its size (0.004 radians at an angle of 65536), so the products are kept with
 // their exact remainders (one FMA each) until the whole turns are gone; what is left, within
-// half a turn, is right to about 2^-24 turns at every position up to 2^23.
+// half a turn, is right to about 2^-24 turns at every position up to 2^23. Tokens with a longer
+// position (integers past 2^24 are not f32 values any more) take the same steps in f64, right to
+// that at every position up to 2^53.
 #include "ops_common.cuh"
 #include "ops_internal.h"
 
@@ -28,10 +30,30 @@ __device__ __forceinline__ void turn_of(float pos, float freq, float& sn, float&
   sincospif(2.0f * ((t - rintf(t)) + rest), &sn, &cs);
 }
 
+// The same for a position that an f32 may not hold.
+__device__ __noinline__ float2 turn_of_long(double pos, float freq) {
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;  // 1 / (2 pi)
+  const double p = pos * (double)freq, e = fma(pos, (double)freq, -p);
+  const double t = p * kHi, f = fma(p, kHi, -t);
+  const double rest = fma(p, kLo, fma(e, kHi, f));
+  double turns = (t - rint(t)) + rest;
+  turns -= rint(turns);
+  float2 v;
+  sincospif(2.0f * (float)turns, &v.x, &v.y);
+  return v;
+}
+
+constexpr float kLongPosition = 8388608.0f;  // 2^23
+
 __device__ __forceinline__ float position(const void* pos, int type, int64_t at) {
   if (type == FCONV_POS_I32) return (float)((const int32_t*)pos)[at];
   if (type == FCONV_POS_I64) return (float)((const int64_t*)pos)[at];
   return ((const float*)pos)[at];
+}
+__device__ __forceinline__ double long_position(const void* pos, int type, int64_t at) {
+  if (type == FCONV_POS_I32) return (double)((const int32_t*)pos)[at];
+  if (type == FCONV_POS_I64) return (double)((const int64_t*)pos)[at];
+  return (double)((const float*)pos)[at];
 }
 
 struct RopeGeom {
@@ -76,7 +98,14 @@ __global__ void __launch_bounds__(256, IL ? 8 : 4) rope_kernel(const RopeGeom g)
     for (int i = 0; i < VEC; ++i) {
       const int p = p0 + i;
       const float x = p < g.sec0 ? pos[0] : p < g.sec0 + g.sec1 ? pos[1] : pos[2];
-      turn_of(x, g.inv_freq[p], sn[i], cs[i]);
+      if (fabsf(x) <= kLongPosition) {
+        turn_of(x, g.inv_freq[p], sn[i], cs[i]);
+      } else {
+        const int a = p < g.sec0 ? 0 : p < g.sec0 + g.sec1 ? 1 : 2;
+        const float2 v = turn_of_long(long_position(g.pos, g.pos_type, pt + a), g.inv_freq[p]);
+        sn[i] = v.x;
+        cs[i] = v.y;
+      }
       if (g.inverse) sn[i] = -sn[i];
     }
     if (IL) {

@@ -68,8 +68,8 @@ void fconv_norm_destroy(fconv_norm_plan* plan);
  *   angle = positions[b, t, a] * inv_freq[p]
  *   (u, v) -> (u cos - v sin, v cos + u sin)        inverse: (u cos + v sin, v cos - u sin)
  * and elements past the last pair are copied. The inverse is the gradient's pass: it takes
- * dq', dk' to dq, dk. Angles are reduced modulo 2 pi with the error of the f32 product
- * corrected, so long positions keep their precision. */
+ * dq', dk' to dq, dk. Angles are reduced modulo 2 pi with the error of the product corrected, so
+ * long positions keep their precision, up to 2^53. */
 typedef enum {
   FCONV_ROPE_INTERLEAVED = 0,   /* pair p is elements (2p, 2p + 1) */
   FCONV_ROPE_HALF = 1,          /* pair p is elements (p, p + pairs) */
