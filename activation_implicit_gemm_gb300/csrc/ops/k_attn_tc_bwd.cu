@@ -893,6 +893,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           drain_bar(ptx::smem_addr(&ctl.q_full[i % Plan::qs]), (i / Plan::qs) & 1);
         for (uint32_t i = c > Plan::gs ? c - Plan::gs : 0; i < c; ++i)
           drain_bar(ptx::smem_addr(&ctl.g_full[i % Plan::gs]), (i / Plan::gs) & 1);
+        for (uint32_t i = c > 2 ? c - 2 : 0; i < c; ++i)
+          drain_bar(ptx::smem_addr(&ctl.st_full[i & 1]), (i >> 1) & 1);
         for (uint32_t i = items > Plan::own ? items - Plan::own : 0; i < items; ++i)
           drain_bar(ptx::smem_addr(&ctl.own_full[i % Plan::own]), (i / Plan::own) & 1);
       }
