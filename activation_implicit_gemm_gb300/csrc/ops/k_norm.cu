@@ -29,6 +29,7 @@
 
 #include "../fconv_internal.h"
 #include "../ptx.cuh"
+#include "row_feed.cuh"
 #include "waits.cuh"
 
 namespace fconv {
@@ -61,12 +62,12 @@ __host__ __device__ constexpr int row_threads() { return TPR == 32 ? 128 : TPR; 
 
 // Sum of N values over the TPR threads of a row. `red` has 2 * N * 16 floats and alternates
 // between its halves: a half is written again only after the barrier of the next use, by when
-// every thread has read it.
-template <int TPR, int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], float* red, int& turn) {
+// every thread has read it. ASK: whether `ok` holds in all those threads, the same answer in each.
+template <int TPR, bool ASK, int N>
+__device__ __forceinline__ bool row_sum(float (&v)[N], float* red, int& turn, bool ok) {
 #pragma unroll
   for (int n = 0; n < N; ++n) v[n] = warp_sum(v[n]);
-  if (TPR == 32) return;
+  if (TPR == 32) return !ASK || __all_sync(0xffffffffu, ok);
   float* r = red + turn * (N * 16);
   turn ^= 1;
   const int warp = threadIdx.x >> 5;
@@ -74,13 +75,15 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* red, int& turn) {
 #pragma unroll
     for (int n = 0; n < N; ++n) r[n * 16 + warp] = v[n];
   }
-  __syncthreads();
+  if (ASK) ok = __syncthreads_and(ok);
+  else __syncthreads();
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     v[n] = 0.0f;
 #pragma unroll
     for (int i = 0; i < TPR / 32; ++i) v[n] += r[n * 16 + i];
   }
+  return !ASK || ok;
 }
 
 // Thread t of a row owns chunks t, t + TPR, ... of VEC elements, E elements in all.
@@ -120,63 +123,6 @@ struct Row {
   }
 };
 
-// Rows on their way to a group of TPR threads: a ring of S stages in shared memory filled by
-// bulk copies (N tensors a stage), so that the loads in flight do not depend on registers or
-// on the group's barriers. Rows that are not whole 16-byte units do not use it (RING false).
-template <typename T, int N, int S, int TPR, bool RING>
-struct Feed {
-  const T* src[N];
-  int64_t step, C, left;  // left: rows not yet asked for
-  uint32_t ring, bars, bytes, k;
-  int t;
-  __device__ __forceinline__ void ask(uint32_t stage) {
-    const uint32_t bar = bars + stage * 8;
-    ptx::mbar_arrive_expect_tx(bar, N * bytes);
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      bulk_load(ring + (stage * N + n) * bytes, src[n], bytes, bar);
-      src[n] += step * C;
-    }
-    --left;
-  }
-  // dsmem: the block's dynamic shared memory; group: this group's index of `groups`.
-  __device__ __forceinline__ void init(uint8_t* dsmem, int group, int groups, int t_, int64_t row,
-                                       int64_t rows, int64_t step_, int64_t C_) {
-    t = t_;
-    step = step_;
-    C = C_;
-    k = 0;
-    bytes = (uint32_t)(C * sizeof(T));
-    left = row < rows ? (rows - row + step - 1) / step : 0;
-    bars = ptx::smem_addr(dsmem) + group * S * 8;
-    ring = ptx::smem_addr(dsmem) + ((groups * S * 8 + 15) & ~15) + group * S * N * bytes;
-    if (RING && t == 0) {
-      for (int i = 0; i < S; ++i) ptx::mbar_init(bars + i * 8, 1);
-      ptx::fence_mbar_init();
-    }
-  }
-  __device__ __forceinline__ void start() {
-    if (RING && t == 0)
-      for (int i = 0; i < S && left > 0; ++i) ask(i);
-  }
-  // The current row of tensor n (all threads of the group wait for it).
-  __device__ __forceinline__ void wait() {
-    if (RING) drain_bar(bars + k % S * 8, (k / S) & 1);
-  }
-  __device__ __forceinline__ const T* row(const uint8_t* dsmem, int n) const {
-    return reinterpret_cast<const T*>(dsmem + (ring - ptx::smem_addr(dsmem)) +
-                                      (k % S * N + n) * bytes);
-  }
-  // After a barrier of the group past the last read of the current row.
-  __device__ __forceinline__ void next() {
-    if (RING && t == 0 && left > 0) ask(k % S);
-    ++k;
-  }
-};
-template <int N, int S>
-size_t feed_bytes(int groups, int64_t row_bytes) {
-  return ((size_t)groups * S * 8 + 15) / 16 * 16 + (size_t)groups * S * N * row_bytes;
-}
 constexpr int kFwdStages = 4, kBwdStages = 3;
 
 // Blocks an SM holds: as many as leave a thread the registers for E values of x and of the
@@ -194,6 +140,7 @@ __global__ void __launch_bounds__(row_threads<TPR>(), row_blocks(E, TPR, false))
   constexpr int NT = row_threads<TPR>(), RPB = NT / TPR;
   extern __shared__ __align__(16) uint8_t dsmem[];
   __shared__ float red[2 * 16];
+  __shared__ int abort_flag;
   using R = Row<T, VEC, E, TPR>;
   const int t = threadIdx.x % TPR, C = (int)g.C;
   int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
@@ -201,6 +148,7 @@ __global__ void __launch_bounds__(row_threads<TPR>(), row_blocks(E, TPR, false))
   Feed<T, 1, kFwdStages, TPR, (VEC > 1)> feed;
   feed.init(dsmem, threadIdx.x / TPR, RPB, t, row, g.outer, step, C);
   feed.src[0] = (const T*)g.x + row * C;
+  if (threadIdx.x == 0) abort_flag = 0;
   __syncthreads();
   ptx::pdl_wait();
   ptx::pdl_trigger();
@@ -215,8 +163,9 @@ __global__ void __launch_bounds__(row_threads<TPR>(), row_blocks(E, TPR, false))
     if (row < g.outer) R::get(ahead, (const T*)g.x + row * C, t, C);
   for (; row < g.outer; row += step) {
     float f[E];
+    bool ok = true;
     if constexpr (VEC > 1) {
-      feed.wait();
+      ok = feed.wait(&abort_flag);
       R::get(f, feed.row(dsmem, 0), t, C);
     } else {
 #pragma unroll
@@ -226,7 +175,10 @@ __global__ void __launch_bounds__(row_threads<TPR>(), row_blocks(E, TPR, false))
     float s[1] = {0.0f};
 #pragma unroll
     for (int e = 0; e < E; ++e) s[0] += f[e];
-    row_sum<TPR>(s, red, turn);
+    if (!row_sum<TPR, (VEC > 1)>(s, red, turn, ok)) {
+      feed.drain();
+      break;
+    }
     feed.next();
     const float m = s[0] * inv;
     s[0] = 0.0f;
@@ -235,7 +187,7 @@ __global__ void __launch_bounds__(row_threads<TPR>(), row_blocks(E, TPR, false))
       f[e] = (e / VEC * TPR + t) * VEC < C ? f[e] - m : 0.0f;
       s[0] = fmaf(f[e], f[e], s[0]);
     }
-    row_sum<TPR>(s, red, turn);
+    row_sum<TPR, false>(s, red, turn, true);
     const float r = rsqrtf(s[0] * inv + g.eps);
     if (t == 0) {
       if (g.mean) g.mean[row] = m;
@@ -253,6 +205,7 @@ __global__ void __launch_bounds__(row_threads<TPR>(), row_blocks(E, TPR, true))
   constexpr int NT = row_threads<TPR>(), RPB = NT / TPR;
   extern __shared__ __align__(16) uint8_t dsmem[];
   __shared__ float red[TPR == 32 ? 2 * E * 32 : 2 * 2 * 16];
+  __shared__ int abort_flag;
   using R = Row<T, VEC, E, TPR>;
   const int t = threadIdx.x % TPR, lane = threadIdx.x & 31, C = (int)g.C;
   int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
@@ -261,6 +214,7 @@ __global__ void __launch_bounds__(row_threads<TPR>(), row_blocks(E, TPR, true))
   feed.init(dsmem, threadIdx.x / TPR, RPB, t, row, g.outer, step, C);
   feed.src[0] = (const T*)g.x + row * C;
   feed.src[1] = (const T*)g.dy + row * C;
+  if (threadIdx.x == 0) abort_flag = 0;
   __syncthreads();
   ptx::pdl_wait();
   ptx::pdl_trigger();
@@ -286,8 +240,9 @@ __global__ void __launch_bounds__(row_threads<TPR>(), row_blocks(E, TPR, true))
     }
     const float m = __shfl_sync(0xffffffffu, lm, k & 31), r = __shfl_sync(0xffffffffu, lr, k & 31);
     float h[E], d[E];
+    bool ok = true;
     if constexpr (VEC > 1) {
-      feed.wait();
+      ok = feed.wait(&abort_flag);
       R::get(h, feed.row(dsmem, 0), t, C);
       R::get(d, feed.row(dsmem, 1), t, C);
     } else {
@@ -311,7 +266,10 @@ __global__ void __launch_bounds__(row_threads<TPR>(), row_blocks(E, TPR, true))
       s[0] += d[e];
       s[1] = fmaf(d[e], h[e], s[1]);
     }
-    row_sum<TPR>(s, red, turn);
+    if (!row_sum<TPR, (VEC > 1)>(s, red, turn, ok)) {
+      feed.drain();
+      break;
+    }
     feed.next();
     const float a = s[0] * inv, c = s[1] * inv;
 #pragma unroll
