@@ -3,7 +3,8 @@ with several axes, and attention, each with its gradient.
 
 As with the convolution, PyTorch only provides device memory and streams: plans are cached by
 shape and strides, arguments are checked here and in the library, and every step runs in the
-library's CUDA kernels on the current stream of the tensors' device (or the one given).
+library's CUDA kernels on the current stream of the tensors' device (or the one given), with that
+device made current for the call.
 """
 from __future__ import annotations
 
@@ -96,9 +97,16 @@ def _start():
 
 
 def check_device(stream=None) -> None:
-    """Synchronise `stream` and raise if a kernel of these operators gave up a wait."""
-    _check(load().fconv_ops_check_device(None if stream is None else stream.cuda_stream),
-           "check_device")
+    """Synchronise `stream` (the current device's default one) and raise if a kernel of these
+    operators gave up a wait on its device."""
+    if torch is None:
+        _start()
+    check = load().fconv_ops_check_device
+    if stream is None:
+        status = check(None)
+    else:
+        status = _run(stream.device.index, check, stream.cuda_stream)
+    _check(status, "check_device")
 
 
 def _code(dtype) -> int:
@@ -149,7 +157,9 @@ def _on_stream(stream, *tensors):
     """The context of a call on `stream`. The tensors it is given stay allocated until the work
     enqueued there is done, whichever stream they come from."""
     for t in tensors:
-        if t is not None and t.is_cuda:  # the call refuses others
+        if t is not None and t.get_device() >= 0:  # the call refuses others
+            if t.get_device() != stream.device.index:
+                raise ValueError("the stream and the tensors must be of one device")
             t.record_stream(stream)
     return torch.cuda.stream(stream)
 
@@ -158,6 +168,19 @@ def _current_stream(device: int) -> int:
     """The handle of the device's current stream; the plain handle spares building a Stream
     object (2 us of the call's 10)."""
     return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _run(device: int, call, *args):
+    """call(*args) with the tensors' device current: the library launches on the current one, and
+    the handle of a default stream means that device's."""
+    if device == _current_device():
+        return call(*args)
+    with torch.cuda.device(device):
+        return call(*args)
 
 
 def _workspace(nbytes: int, like):
@@ -256,8 +279,8 @@ def layer_norm(x, weight=None, bias=None, *, axis: int = -1, eps: float = 1e-5, 
     if return_stats:
         mean = torch.empty(p.stat_shape, dtype=torch.float32, device=x.device)
         rstd = torch.empty_like(mean)
-    p.forward_ptrs(x.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(), _ptr(mean), _ptr(rstd),
-                   _current_stream(device))
+    _run(device, p.forward_ptrs, x.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(),
+         _ptr(mean), _ptr(rstd), _current_stream(device))
     return (out, mean, rstd) if return_stats else out
 
 
@@ -289,8 +312,8 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, bias=None, *, axis: int 
     db = torch.empty_like(bias) if bias is not None and param_grads else None
     n = p.workspace_bytes if dw is not None or db is not None else 0
     ws = _workspace(n, x)
-    p.backward_ptrs(dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(),
-                    dx.data_ptr(), _ptr(dw), _ptr(db), _ptr(ws), n, _current_stream(device))
+    _run(device, p.backward_ptrs, dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(),
+         rstd.data_ptr(), dx.data_ptr(), _ptr(dw), _ptr(db), _ptr(ws), n, _current_stream(device))
     return dx, dw, db
 
 
@@ -381,8 +404,8 @@ def rope(q, k=None, *, positions, inv_freq, sections: Optional[Sequence[int]] = 
     if p is None:
         p = _rope_plans[key] = _rope_plan(q, k, positions, inv_freq, sections, pairing, inverse,
                                           out, k_out, device)
-    p.run_ptrs(q.data_ptr(), _ptr(k), positions.data_ptr(), inv_freq.data_ptr(), out.data_ptr(),
-               _ptr(k_out), _current_stream(device))
+    _run(device, p.run_ptrs, q.data_ptr(), _ptr(k), positions.data_ptr(), inv_freq.data_ptr(),
+         out.data_ptr(), _ptr(k_out), _current_stream(device))
     return out if k is None else (out, k_out)
 
 
@@ -534,8 +557,8 @@ def attention(q, k, v, *, causal: bool = False, scale: Optional[float] = None, q
         lse = torch.empty(p.lse_shape, dtype=torch.float32, device=q.device)
     n = p.forward_workspace
     ws = _workspace(n, q)
-    p.forward_ptrs(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(q_lens), _ptr(kv_lens),
-                   out.data_ptr(), _ptr(lse), _ptr(ws), n, _current_stream(device))
+    _run(device, p.forward_ptrs, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(q_lens),
+         _ptr(kv_lens), out.data_ptr(), _ptr(lse), _ptr(ws), n, _current_stream(device))
     return (out, lse) if return_lse else out
 
 
@@ -562,7 +585,7 @@ def attention_backward(dout, q, k, v, out, lse, *, causal: bool = False,
         raise ValueError("attention_backward: lse must be float32 (batch, heads, queries)")
     n = p.backward_workspace
     ws = _workspace(n, q)
-    p.backward_ptrs(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                    lse.data_ptr(), _ptr(q_lens), _ptr(kv_lens), dq.data_ptr(), dk.data_ptr(),
-                    dv.data_ptr(), _ptr(ws), n, _current_stream(device))
+    _run(device, p.backward_ptrs, dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+         out.data_ptr(), lse.data_ptr(), _ptr(q_lens), _ptr(kv_lens), dq.data_ptr(),
+         dk.data_ptr(), dv.data_ptr(), _ptr(ws), n, _current_stream(device))
     return dq, dk, dv

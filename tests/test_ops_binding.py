@@ -47,3 +47,87 @@ def test_positions_of_one_token_a_sequence():
         rope_plan(shape, None, batch=1, tokens=4)
     for shape in ((1,), (1, 1), (4, 1), (1, 1, 1), (4, 1, 1)):
         rope_plan(shape, None, batch=4, tokens=1)
+
+
+# ------------------------------------------------------------------- the tensors' own device
+
+class OnDevice1(torch.Tensor):
+    """A tensor that says it lies on the second GPU."""
+
+    def get_device(self):
+        return 1
+
+
+def on_device_1(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(OnDevice1)
+
+
+class Switch:
+    """Stands in for torch.cuda.device: notes the device that is current while it is entered."""
+    current = 0
+
+    def __init__(self, device):
+        self.device = device
+
+    def __enter__(self):
+        self.before, Switch.current = Switch.current, self.device
+
+    def __exit__(self, *a):
+        Switch.current = self.before
+
+
+def test_the_tensors_device_is_current_in_a_call(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "device", Switch)
+    monkeypatch.setattr(_ops, "_current_device", lambda: Switch.current)
+    seen = []
+    for device in (1, 0, 1):
+        _ops._run(device, lambda *a: seen.append((Switch.current, a)), 5, 6)
+    assert seen == [(1, (5, 6)), (0, (5, 6)), (1, (5, 6))] and Switch.current == 0
+
+
+def test_every_call_runs_on_its_tensors_device(monkeypatch):
+    calls = []
+    monkeypatch.setattr(_ops, "_run", lambda device, call, *a: calls.append((device, call.__name__)))
+    monkeypatch.setattr(_ops, "_current_stream", lambda device: 0)
+    x, w = on_device_1(4, 8), on_device_1(8)
+    stat = on_device_1(4)
+    _ops.layer_norm(x, w, w)
+    _ops.layer_norm_backward(x, x, stat, stat, w, w)
+    q = on_device_1(1, 3, 2, 8)
+    _ops.rope(q, q, positions=on_device_1(3, dtype=torch.int32), inv_freq=on_device_1(4))
+    _ops.attention(q, q, q)
+    _ops.attention_backward(q, q, q, q, q, on_device_1(1, 2, 3))
+    assert calls == [(1, "forward_ptrs"), (1, "backward_ptrs"), (1, "run_ptrs"),
+                     (1, "forward_ptrs"), (1, "backward_ptrs")]
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Stream:
+        device = torch.device("cuda", 0)
+
+    x = on_device_1(4, 8)
+    q = on_device_1(1, 3, 2, 8)
+    for call in (lambda: _ops.layer_norm(x, stream=Stream()),
+                 lambda: _ops.attention(q, q, q, stream=Stream())):
+        with pytest.raises(ValueError, match="stream"):
+            call()
+
+
+def test_check_device_looks_at_the_streams_device(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "device", Switch)
+    monkeypatch.setattr(_ops, "_current_device", lambda: Switch.current)
+    seen = []
+
+    class Lib:
+        @staticmethod
+        def fconv_ops_check_device(stream):
+            seen.append((Switch.current, stream))
+            return 0
+
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 77
+
+    monkeypatch.setattr(_ops, "load", lambda: Lib)
+    _ops.check_device(Stream())
+    _ops.check_device()
+    assert seen == [(1, 77), (0, None)]
