@@ -151,11 +151,17 @@ class FusedConvPlan:
         for t in (x, w, b, z, y):
             if t is not None and not t.is_contiguous():
                 raise ValueError("FusedConv tensors must be contiguous")
-        self.run_ptrs(x.data_ptr(), w.data_ptr(), 0 if b is None else b.data_ptr(),
-                      0 if z is None else z.data_ptr(), y.data_ptr(),
-                      0 if workspace is None else workspace.data_ptr(),
-                      0 if workspace is None else workspace.numel() * workspace.element_size(),
-                      stream.cuda_stream)
+        args = (x.data_ptr(), w.data_ptr(), 0 if b is None else b.data_ptr(),
+                0 if z is None else z.data_ptr(), y.data_ptr(),
+                0 if workspace is None else workspace.data_ptr(),
+                0 if workspace is None else workspace.numel() * workspace.element_size(),
+                stream.cuda_stream)
+        device = x.get_device()
+        if device < 0 or device == torch.cuda.current_device():
+            self.run_ptrs(*args)
+        else:  # the library launches on the current device
+            with torch.cuda.device(device):
+                self.run_ptrs(*args)
         return y
 
     def __del__(self):

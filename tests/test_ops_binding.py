@@ -131,3 +131,19 @@ def test_check_device_looks_at_the_streams_device(monkeypatch):
     _ops.check_device(Stream())
     _ops.check_device()
     assert seen == [(1, 77), (0, None)]
+
+
+def test_a_convolution_runs_on_its_tensors_device(monkeypatch):
+    from activation_implicit_gemm_gb300 import FusedConvPlan
+    monkeypatch.setattr(torch.cuda, "device", Switch)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: Switch.current)
+
+    class Stream:
+        cuda_stream = 5
+
+    x, w = on_device_1(1, 3, 8, 8), on_device_1(4, 3, 3, 3)
+    plan = FusedConvPlan(0, x.shape, w.shape)
+    seen = []
+    monkeypatch.setattr(plan, "run_ptrs", lambda *a: seen.append((Switch.current, a[-1])))
+    plan.run(x, w, stream=Stream())
+    assert seen == [(1, 5)] and Switch.current == 0
