@@ -523,13 +523,14 @@ def _attn_plan(who, q, k, v, out, causal, scale, q_lens, kv_lens, route, device,
     if grads is not None:
         strides = {n + "_stride": t.stride()[:3]
                    for n, t in zip(("dout", "dq", "dk", "dv"), grads)}
-    p = _attn_plans[key] = AttentionPlan(
+    p = AttentionPlan(
         _code(q.dtype), b, lq, k.shape[1], h, k.shape[2], d, q_stride=q.stride()[:3],
         k_stride=k.stride()[:3], v_stride=v.stride()[:3], out_stride=out.stride()[:3],
         scale=scale, causal=causal, has_q_lens=q_lens is not None,
         has_kv_lens=kv_lens is not None, training=grads is not None, route=route, device=device,
         **strides)
     p.lse_shape = (b, h, lq)
+    _attn_plans[key] = p  # whole: another thread may take it from here on
     return p
 
 

@@ -147,3 +147,33 @@ def test_a_convolution_runs_on_its_tensors_device(monkeypatch):
     monkeypatch.setattr(plan, "run_ptrs", lambda *a: seen.append((Switch.current, a[-1])))
     plan.run(x, w, stream=Stream())
     assert seen == [(1, 5)] and Switch.current == 0
+
+
+# ------------------------------------------------------------------------------ cached plans
+
+class Watched(dict):
+    """A plan cache that looks at what is put into it."""
+
+    def __init__(self, ready):
+        super().__init__()
+        self.ready = ready
+
+    def __setitem__(self, key, plan):
+        assert self.ready(plan)
+        super().__setitem__(key, plan)
+
+
+def attn_plan(keys, **kw):
+    q, k = torch.zeros(1, 2, 4, 16), torch.zeros(1, keys, 2, 16)
+    return _ops._attn_plan("attention", q, k, k, q, False, None, None, None, "auto", -1, **kw)
+
+
+def norm_plan(rows):
+    return _ops._norm_plan("layer_norm", torch.zeros(rows, 8), None, None, -1, 1e-5, -1)
+
+
+def test_a_plan_is_whole_when_other_threads_can_see_it(monkeypatch):
+    monkeypatch.setattr(_ops, "_attn_plans", Watched(lambda p: p.lse_shape == (1, 4, 2)))
+    monkeypatch.setattr(_ops, "_norm_plans", Watched(lambda p: p.param_shape and p.stat_shape))
+    assert attn_plan(5) is attn_plan(5) and len(_ops._attn_plans) == 1
+    assert norm_plan(3) is norm_plan(3) and len(_ops._norm_plans) == 1
