@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import threading
 from typing import Optional, Sequence
 
 from . import FconvError, _lib
@@ -142,6 +143,19 @@ class _Plan:
             pass
 
 
+_KEPT = 1024  # plans a cache holds; a step over ragged batches or a growing cache makes new ones
+_keeping = threading.Lock()
+
+
+def _keep(cache: dict, key, plan):
+    """Puts a plan into a cache, whose oldest ones make room."""
+    with _keeping:
+        while len(cache) >= _KEPT:
+            del cache[next(iter(cache))]
+        cache[key] = plan
+    return plan
+
+
 def _on_cuda(who: str, device: int, *tensors) -> None:
     """All tensors that are there lie on one CUDA device."""
     if device >= 0:
@@ -247,7 +261,7 @@ def _norm_plan(who, x, weight, bias, axis, eps, device):
                           device=device)
         p.param_shape = x.shape[axis:axis + 1]
         p.stat_shape = x.shape[:axis] + x.shape[axis + 1:]
-        _norm_plans[key] = p
+        _keep(_norm_plans, key, p)
     for t in (weight, bias):
         if t is not None and (t.shape != p.param_shape or not t.is_contiguous()):
             raise ValueError(f"{who}: weight and bias are vectors of {p.param_shape[0]} values")
@@ -402,8 +416,8 @@ def rope(q, k=None, *, positions, inv_freq, sections: Optional[Sequence[int]] = 
                 None if k_out is None else (k_out.dtype, k_out.shape, k_out.stride()))
     p = _rope_plans.get(key)
     if p is None:
-        p = _rope_plans[key] = _rope_plan(q, k, positions, inv_freq, sections, pairing, inverse,
-                                          out, k_out, device)
+        p = _keep(_rope_plans, key, _rope_plan(q, k, positions, inv_freq, sections, pairing,
+                                               inverse, out, k_out, device))
     _run(device, p.run_ptrs, q.data_ptr(), _ptr(k), positions.data_ptr(), inv_freq.data_ptr(),
          out.data_ptr(), _ptr(k_out), _current_stream(device))
     return out if k is None else (out, k_out)
@@ -530,8 +544,7 @@ def _attn_plan(who, q, k, v, out, causal, scale, q_lens, kv_lens, route, device,
         has_kv_lens=kv_lens is not None, training=grads is not None, route=route, device=device,
         **strides)
     p.lse_shape = (b, h, lq)
-    _attn_plans[key] = p  # whole: another thread may take it from here on
-    return p
+    return _keep(_attn_plans, key, p)  # whole: another thread may take it from here on
 
 
 def attention(q, k, v, *, causal: bool = False, scale: Optional[float] = None, q_lens=None,

@@ -177,3 +177,47 @@ def test_a_plan_is_whole_when_other_threads_can_see_it(monkeypatch):
     monkeypatch.setattr(_ops, "_norm_plans", Watched(lambda p: p.param_shape and p.stat_shape))
     assert attn_plan(5) is attn_plan(5) and len(_ops._attn_plans) == 1
     assert norm_plan(3) is norm_plan(3) and len(_ops._norm_plans) == 1
+
+
+def rope_call_plan(tokens):
+    """A plan as rope() makes and keeps it."""
+    q = on_device_1(1, tokens, 2, 8)
+    _ops.rope(q, positions=on_device_1(tokens, dtype=torch.int32), inv_freq=on_device_1(4))
+
+
+def test_the_caches_drop_their_oldest_plans(monkeypatch):
+    monkeypatch.setattr(_ops, "_run", lambda *a: None)
+    monkeypatch.setattr(_ops, "_current_stream", lambda device: 0)
+    monkeypatch.setattr(_ops, "_KEPT", 4)
+    for name in ("_attn_plans", "_norm_plans", "_rope_plans"):
+        monkeypatch.setattr(_ops, name, {})
+    for n in range(1, 12):  # keys that grow by one, as a decoder's do
+        attn_plan(n)
+        norm_plan(n)
+        rope_call_plan(n)
+    for cache in (_ops._attn_plans, _ops._norm_plans, _ops._rope_plans):
+        assert len(cache) == 4
+    newest = list(_ops._attn_plans.values())
+    assert [attn_plan(n) for n in range(8, 12)] == newest  # the newest are kept
+    assert attn_plan(1) is attn_plan(1) and len(_ops._attn_plans) == 4
+
+
+def test_threads_share_the_caches(monkeypatch):
+    import threading
+    monkeypatch.setattr(_ops, "_KEPT", 3)
+    monkeypatch.setattr(_ops, "_attn_plans", {})
+    failed = []
+
+    def work(seed):
+        try:
+            for i in range(200):
+                assert attn_plan(1 + (i * seed) % 13).lse_shape == (1, 4, 2)
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(s,)) for s in (1, 2, 3, 5, 7, 11)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed and len(_ops._attn_plans) <= 3
