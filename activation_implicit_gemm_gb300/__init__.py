@@ -24,11 +24,15 @@ __all__ = ["FconvError", "FusedConvPlan", "fused_conv", "conv_transpose", "plan_
 
 
 class FconvError(RuntimeError):
-    def __init__(self, status: int, where: str = ""):
+    """A status of the library. `text` is the call that gives a status its words; without one it
+    is the convolution's, and the token-side operators' for the statuses that only they have."""
+
+    def __init__(self, status: int, where: str = "", text=None):
         self.status = status
         self.code = STATUS.get(status, str(status))
-        lib = _lib.load()
-        text = lib.fconv_status_string if status < 32 else _ops.load().fconv_ops_status_string
+        if text is None:
+            lib = _lib.load() if status < 32 else _ops.load()
+            text = lib.fconv_status_string if status < 32 else lib.fconv_ops_status_string
         msg = text(status).decode()
         super().__init__(f"{where}: {self.code} ({msg})" if where else f"{self.code} ({msg})")
 

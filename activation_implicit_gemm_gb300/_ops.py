@@ -84,9 +84,13 @@ def load() -> ctypes.CDLL:
     return _ready
 
 
+def _error(status: int, where: str) -> FconvError:
+    return FconvError(status, where, load().fconv_ops_status_string)
+
+
 def _check(status: int, where: str):
     if status:
-        raise FconvError(status, where)
+        raise _error(status, where)
 
 
 def _start():
@@ -113,7 +117,7 @@ def check_device(stream=None) -> None:
 def _code(dtype) -> int:
     code = {torch.float32: _lib.F32, torch.float16: _lib.F16, torch.bfloat16: BF16}.get(dtype)
     if code is None:
-        raise FconvError(14, f"dtype {dtype}")
+        raise _error(14, f"dtype {dtype}")
     return code
 
 
@@ -427,7 +431,7 @@ def _rope_plan(q, k, positions, inv_freq, sections, pairing, inverse, out, k_out
     _heads("rope", "q", q)
     pos_type = {torch.int32: 0, torch.int64: 1, torch.float32: 2}.get(positions.dtype)
     if pos_type is None:
-        raise FconvError(14, f"positions of {positions.dtype}")
+        raise _error(14, f"positions of {positions.dtype}")
     if sections is None:
         sections = (inv_freq.numel(),)
     shape = tuple(positions.shape)

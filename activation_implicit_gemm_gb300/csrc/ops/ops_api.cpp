@@ -216,6 +216,8 @@ const char* fconv_ops_status_string(int s) {
     case FCONV_E_STRIDE: return "a stride is negative or makes elements of an output overlap";
     case FCONV_E_MASK: return "lengths were given that the plan does not have, or the reverse";
     case FCONV_E_ATTR_VALUE: return "an attribute has a value outside its range";
+    case FCONV_E_BIAS_SHAPE:
+      return "a weight, a bias or a gradient of one was given that the plan does not have";
     case FCONV_E_ALIGNMENT: return "a device pointer is not aligned as its type or route needs";
     case FCONV_E_ALIAS: return "an output must not be an input or another output";
     default: return fconv_status_string((fconv_status)s);

@@ -221,3 +221,32 @@ def test_threads_share_the_caches(monkeypatch):
     for t in threads:
         t.join()
     assert not failed and len(_ops._attn_plans) <= 3
+
+
+# -------------------------------------------------------------------------- texts of refusals
+
+def test_a_refusal_says_what_the_operators_call_it():
+    from activation_implicit_gemm_gb300 import AttentionPlan, FconvError, FusedConvPlan, LayerNormPlan
+
+    def text(call, *a, **kw):
+        with pytest.raises(FconvError) as e:
+            call(*a, **kw)
+        return e.value.code, str(e.value)
+
+    attribute = "an attribute has a value outside its range"
+    assert text(LayerNormPlan, 1, 3, 40, eps=-1.0) == (
+        "E_ATTR_VALUE", f"fconv_norm_plan_create: E_ATTR_VALUE ({attribute})")
+    s = dict(q_stride=(0, 0, 0), k_stride=(0, 0, 0), v_stride=(0, 0, 0), out_stride=(0, 0, 0))
+    assert attribute in text(AttentionPlan, 1, 1, 1, 1, 1, 1, 1, scale=-2.0, **s)[1]
+    A = 0x10000  # made-up addresses: never read on these paths
+    norm = LayerNormPlan(1, 3, 40)
+    assert "an output must not be an input" in text(
+        norm.forward_ptrs, A, 2 * A, 3 * A, 2 * A, None, None, None)[1]
+    assert "as its type or route needs" in text(
+        norm.forward_ptrs, A + 1, 2 * A, 3 * A, 4 * A, None, None, None)[1]
+    bare = LayerNormPlan(1, 3, 40, has_weight=False, has_bias=False)
+    assert "that the plan does not have" in text(
+        bare.forward_ptrs, A, 2 * A, None, 4 * A, None, None, None)[1]
+    # a convolution's refusals keep their own
+    assert "strides/dilations must be >= 1" in text(
+        FusedConvPlan, 1, (1, 3, 8, 8), (4, 3, 3, 3), strides=[0, 1])[1]
