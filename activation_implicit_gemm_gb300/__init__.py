@@ -7,7 +7,8 @@ raises.
 
 Beside it, the operators that follow a patch embedding (include/fconv_ops.h): layer_norm over
 rows or channels-first features, rope (rotary positions with one to three axes) and attention,
-each with its gradient.
+each with its gradient. Calls return when their work is enqueued; check_device waits for a
+stream's and raises if a kernel gave up a wait (its outputs are then not whole).
 """
 from __future__ import annotations
 
@@ -20,7 +21,7 @@ from ._lib import ROUTES, ROUTE_NAMES, STATUS
 __all__ = ["FconvError", "FusedConvPlan", "fused_conv", "conv_transpose", "plan_for", "load_library",
            "build", "LayerNormPlan", "RopePlan", "AttentionPlan", "layer_norm",
            "layer_norm_backward", "rope", "rope_frequencies", "attention",
-           "attention_backward"]
+           "attention_backward", "check_device"]
 
 
 class FconvError(RuntimeError):
@@ -231,4 +232,5 @@ def conv_transpose(x, w, b=None, z=None, *, group: int = 1, strides=None, dilati
 
 from . import _ops  # noqa: E402
 from ._ops import (AttentionPlan, LayerNormPlan, RopePlan, attention,  # noqa: E402
-                   attention_backward, layer_norm, layer_norm_backward, rope, rope_frequencies)
+                   attention_backward, check_device, layer_norm, layer_norm_backward, rope,
+                   rope_frequencies)

@@ -250,3 +250,26 @@ def test_a_refusal_says_what_the_operators_call_it():
     # a convolution's refusals keep their own
     assert "strides/dilations must be >= 1" in text(
         FusedConvPlan, 1, (1, 3, 8, 8), (4, 3, 3, 3), strides=[0, 1])[1]
+
+
+# ----------------------------------------------------------------- reports of waits given up
+
+def test_check_device_is_part_of_the_package():
+    import activation_implicit_gemm_gb300 as fc
+    assert fc.check_device is _ops.check_device and "check_device" in fc.__all__
+
+
+def test_check_device_raises_what_a_kernel_reported(monkeypatch):
+    import activation_implicit_gemm_gb300 as fc
+    lib = _ops.load()
+
+    class Lib:
+        fconv_ops_status_string = staticmethod(lib.fconv_ops_status_string)
+
+        @staticmethod
+        def fconv_ops_check_device(stream):
+            return 16
+
+    monkeypatch.setattr(_ops, "load", lambda: Lib)
+    with pytest.raises(fc.FconvError, match="E_DEVICE_TIMEOUT.*gave up a bounded wait"):
+        fc.check_device()
