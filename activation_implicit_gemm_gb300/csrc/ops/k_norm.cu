@@ -175,11 +175,8 @@ __global__ void __launch_bounds__(row_threads<TPR>(), row_blocks(E, TPR, false))
     float s[1] = {0.0f};
 #pragma unroll
     for (int e = 0; e < E; ++e) s[0] += f[e];
-    if (!row_sum<TPR, (VEC > 1)>(s, red, turn, ok)) {
-      feed.drain();
-      break;
-    }
-    feed.next();
+    ok = row_sum<TPR, (VEC > 1)>(s, red, turn, ok);
+    feed.next(ok);
     const float m = s[0] * inv;
     s[0] = 0.0f;
 #pragma unroll
@@ -189,14 +186,16 @@ __global__ void __launch_bounds__(row_threads<TPR>(), row_blocks(E, TPR, false))
     }
     row_sum<TPR, false>(s, red, turn, true);
     const float r = rsqrtf(s[0] * inv + g.eps);
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = fmaf(f[e] * r, w[e], b[e]);
+    if (!ok) break;  // here: before the row's arithmetic the branch cost up to a quarter
     if (t == 0) {
       if (g.mean) g.mean[row] = m;
       if (g.rstd) g.rstd[row] = r;
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) f[e] = fmaf(f[e] * r, w[e], b[e]);
     R::put((T*)g.y + row * C, f, t, C);
   }
+  if (abort_flag) feed.drain();
 }
 
 template <typename T, int VEC, int E, int TPR>
@@ -266,16 +265,15 @@ __global__ void __launch_bounds__(row_threads<TPR>(), row_blocks(E, TPR, true))
       s[0] += d[e];
       s[1] = fmaf(d[e], h[e], s[1]);
     }
-    if (!row_sum<TPR, (VEC > 1)>(s, red, turn, ok)) {
-      feed.drain();
-      break;
-    }
-    feed.next();
+    ok = row_sum<TPR, (VEC > 1)>(s, red, turn, ok);
+    feed.next(ok);
     const float a = s[0] * inv, c = s[1] * inv;
 #pragma unroll
     for (int e = 0; e < E; ++e) d[e] = r * (d[e] - a - h[e] * c);
+    if (!ok) break;
     R::put((T*)g.y + row * C, d, t, C);
   }
+  if (abort_flag) feed.drain();
   if (!g.part) return;
   float* part = g.part + (int64_t)blockIdx.x * 2 * C;
   if (TPR == 32) {  // the block's warps add up in order

@@ -12,6 +12,11 @@ namespace fconv {
 namespace ops {
 namespace {
 
+// A call of its own: with its loop inline in the kernels the backward ones spilled up to 552 bytes.
+__device__ __noinline__ bool wait_row(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return wait_bar(bar, parity, abort_flag);
+}
+
 // Rows on their way to a group of TPR threads: a ring of S stages in shared memory filled by
 // bulk copies (N tensors a stage), so that the loads in flight do not depend on registers or
 // on the group's barriers. Rows that are not whole 16-byte units do not use it (RING false).
@@ -55,22 +60,25 @@ struct Feed {
   }
   // All threads of the group wait for the current row; false when the wait was given up.
   __device__ __forceinline__ bool wait(volatile int* abort_flag) {
-    return !RING || wait_bar(bars + k % S * 8, (k / S) & 1, abort_flag);
+    const uint32_t bar = bars + k % S * 8, parity = (k / S) & 1;
+    return !RING || ptx::mbar_try_wait(bar, parity) || wait_row(bar, parity, abort_flag);
   }
-  // On the way out after that: the copies in flight land before the block's shared memory is
-  // given back (a stage that was not asked for again runs into the drain's short limit).
+  // On the way out after that, before next() or after it: the copies in flight land before the
+  // block's shared memory is given back (a stage that was not asked for again runs into the drain's
+  // short limit).
   __device__ __forceinline__ void drain() {
     if (RING && t == 0)
-      for (uint32_t i = 0; i < S; ++i) drain_bar(bars + (k + i) % S * 8, ((k + i) / S) & 1);
+      for (uint32_t i = k > 0 ? k - 1 : 0; i < k + S; ++i) drain_bar(bars + i % S * 8, (i / S) & 1);
   }
   // The current row of tensor n.
   __device__ __forceinline__ const T* row(const uint8_t* dsmem, int n) const {
     return reinterpret_cast<const T*>(dsmem + (ring - ptx::smem_addr(dsmem)) +
                                       (k % S * N + n) * bytes);
   }
-  // After a barrier of the group past the last read of the current row.
-  __device__ __forceinline__ void next() {
-    if (RING && t == 0 && left > 0) ask(k % S);
+  // After a barrier of the group past the last read of the current row; ok: its wait was not given
+  // up (else its stage is left alone).
+  __device__ __forceinline__ void next(bool ok = true) {
+    if (RING && t == 0 && ok && left > 0) ask(k % S);
     ++k;
   }
 };
