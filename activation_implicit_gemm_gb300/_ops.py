@@ -4,7 +4,9 @@ with several axes, and attention, each with its gradient.
 As with the convolution, PyTorch only provides device memory and streams: plans are cached by
 shape and strides, arguments are checked here and in the library, and every step runs in the
 library's CUDA kernels on the current stream of the tensors' device (or the one given), with that
-device made current for the call.
+device made current for the call. Outputs carry no gradient function: the backward calls are the
+gradients, to be called by hand or from a torch.autograd.Function. Plans are cached by shape: a
+program whose keys grow token by token passes one buffer and kv_lens, not a longer view each time.
 """
 from __future__ import annotations
 

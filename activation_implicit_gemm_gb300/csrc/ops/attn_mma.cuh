@@ -18,7 +18,7 @@
 // A block owns 64 rows (of queries, or of keys for dk and dv), a warp 16 of them and the columns
 // of a score tile in registers: all of them for dk and dv, half in the other kernels, whose
 // accumulators leave room for twice the warps (the halves are joined at the end; 528 -> 434 us a
-// training pass of the size below when it was made). The score accumulator is the next
+// training pass of the size below when that was made). The score accumulator is the next
 // product's A operand as it is: its column pair (2t, 2t + 1) of a lane takes the places of k = t
 // and k = t + 4, and the B operand is read with rows 2t and 2t + 1 to match. Tiles lie in shared
 // memory as f32 with rows of Dp + 4 floats, Dp a multiple of 8: both ways of reading a B operand
@@ -26,14 +26,15 @@
 // current one's products run. As in the other routes every gradient has one writer and no
 // atomics. dq needs nothing of dk and dv: its kernel is launched after theirs but takes the SMs as
 // their blocks leave them (it reads what the delta pass wrote, which theirs has waited for, from
-// L2) and waits for them only before it ends: 461 -> 383 us a training pass of the size below.
+// L2) and waits for them only before it ends: 461 -> 383 us a training pass of the size below when
+// that was made.
 //
 // Bound: latency. 3 x 333 queries x 777 keys, 16 heads of 72, f32 (one sequence without keys,
-// one cut short): forward 96 us, delta 9, dk and dv 230 and dq 133 by themselves, 383 for
-// the pass. A scheduler has four warps (two for dk and dv, whose two accumulators fill the
+// one cut short): 408 us for the pass; forward 101, delta 9, dk and dv 258 and dq 166 where each
+// is alone under the profiler, the last two overlapping in the pass. A scheduler has four warps (two for dk and dv, whose two accumulators fill the
 // registers) to cover the time of the products and of the shared-memory reads that feed them (a
 // 4-byte operand a lane for 1.5 instructions). Head lengths over 128, one block of eight warps an
-// SM: 4 x 1024 tokens of 8 heads of 256, f32, forward 0.77 ms (45 TFLOP/s), backward 3.3 ms (26
+// SM: 4 x 1024 tokens of 8 heads of 256, f32, forward 0.83 ms (41 TFLOP/s), backward 3.5 ms (24
 // counted; each half's warps of the dk, dv kernel make the scores for themselves).
 #pragma once
 
@@ -217,7 +218,7 @@ __device__ __forceinline__ void clear(float (&acc)[NT][4]) {
 
 // Columns of a tile in the gradient kernels. With 64 the four tiles of a head length of 128 leave
 // room for one block an SM, with 32 for two (4 x 1024 tokens of 8 heads of 128, f32, backward:
-// 2022 -> 1338 us); over 128 they would not fit at all.
+// 2022 -> 1338 us when that was made, 1438 now); over 128 they would not fit at all.
 template <int NT>
 constexpr int kColsOf = NT > 12 ? 32 : 64;
 

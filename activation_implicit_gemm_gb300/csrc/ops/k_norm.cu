@@ -18,8 +18,8 @@
 //    (or with odd 16-bit planes) a tile is read again from L2 in each pass.
 // dw and db: every block writes one partial sum, norm_dparam_join adds them in order.
 //
-// Measured: 32768 rows of 4096 in bf16, forward 85 us (6.3 TB/s) and backward 131 us with 4.5 for
-// the join (6.1 TB/s), 0.93 and 0.91 of the copy rate. 5001 rows of 1001 in f32 (no 16-byte units:
+// Measured: 32768 rows of 4096 in bf16, forward 85 us (6.3 TB/s) and backward 132 us with the join
+// (6.1 TB/s), 0.93 and 0.90 of the copy rate. 5001 rows of 1001 in f32 (no 16-byte units:
 // a row ahead in registers), 12 us, 16 and 5: the 2.7 MB of partial sums and the launches are as
 // long as the data. 32 x 128 channels x 56 x 56 in f16, forward 17 us, backward 27 and 3.7: the
 // data (51 and 77 MB) is largely in L2, and the conversions, sums and products of two positions a

@@ -35,8 +35,8 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   }
 }
 
-// Wait for operations this block has already issued (they always complete): goes on after its
-// limit, with the error word set.
+// On the way out: wait for operations this block has already issued (they always complete). Goes
+// on after its limit, with the error word set.
 __device__ __forceinline__ void drain_bar(uint32_t bar, uint32_t parity) {
   if (ptx::mbar_try_wait(bar, parity)) return;
   const uint64_t t0 = ptx::globaltimer_ns();

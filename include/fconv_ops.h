@@ -9,8 +9,12 @@
  * host nothing is launched and no output is written. No call aborts the process. A plan may be
  * used from several streams at once as long as each call has a workspace of its own.
  *
- * Every sum, softmax statistic and norm is held in f32; each output is rounded once. Results
- * do not depend on the order in which blocks run: there are no floating-point atomics.
+ * Every sum, softmax statistic and norm is held in f32; each output is rounded once. Beyond that
+ * only attention in f16 and bf16 rounds: on FCONV_ATTN_TC its probabilities and its score gradients
+ * are 16-bit operands of the products that follow, and on either route the gradient's delta comes
+ * from out as it was rounded. With FCONV_ATTN_TC its outputs are off by 1.2 to 1.5 times their own
+ * rounding, dq and dk over a few dozen keys by up to 1.8 times. Results do not depend on the order
+ * in which blocks run: there are no floating-point atomics.
  */
 #ifndef FCONV_OPS_H_
 #define FCONV_OPS_H_
@@ -115,7 +119,9 @@ void fconv_rope_destroy(fconv_rope_plan* plan);
  * causal: query i sees key j iff j <= i + (kv_len - q_len), so the last query sees every key.
  * A query that sees no key (or lies past q_len) has out 0, lse -inf and zero gradient.
  * A non-finite key or value that lies inside kv_len and is hidden from a query only by the
- * causal order can reach that query. */
+ * causal order can reach that query. Scores that come out as -inf (keys of f32's or bf16's lowest
+ * value, say) have probability 0, and a row that has no others counts as seeing no key; on
+ * FCONV_ATTN_TC such a key's value must still give a finite product with dout. */
 typedef struct {
   int dtype;
   int64_t batch, len_q, len_k, heads_q, heads_kv, head_dim;
