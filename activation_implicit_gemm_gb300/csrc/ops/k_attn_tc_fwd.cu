@@ -27,7 +27,7 @@
 // with a partial sum of its own.
 //
 // Bound: tensor (4 D FLOPs a pair) for long queries, HBM (K and V) for few, latency for short
-// sequences. 16384 tokens, 16 heads of 128, bf16: 1.35 to 1.40 ms from box to box, 1570 to 1630
+// sequences. 16384 tokens, 16 heads of 128, bf16: 1.35 to 1.40 ms from GPU to GPU, 1570 to 1630
 // TFLOP/s, 0.92 to 0.96 of what a long run of library products keeps up; head length 64 has the same exponentials for half the products
 // (4 x 4096 tokens, 16 heads: 280 us, 980 TFLOP/s). One query and up to 8192 keys of 16
 // sequences, 8 key heads of 128 for 32: 64 us and 6 for the join, 5.4 TB/s. 196 tokens of 12
