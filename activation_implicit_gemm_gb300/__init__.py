@@ -6,8 +6,9 @@ library's CUDA kernels. There is no CPU path: without the built library every ca
 raises.
 
 Beside it, the operators that follow a patch embedding (include/fconv_ops.h): layer_norm over
-rows or channels-first features, rope (rotary positions with one to three axes) and attention,
-each with its gradient. Calls return when their work is enqueued; check_device waits for a
+rows or channels-first features, rope (rotary positions with one to three axes), norm_rope (the
+same with a norm of each head), attention and gated_mlp (the gated feed-forward block), each with
+its gradient. Calls return when their work is enqueued; check_device waits for a
 stream's and raises if a kernel gave up a wait (its outputs are then not whole).
 """
 from __future__ import annotations
@@ -21,7 +22,8 @@ from ._lib import ROUTES, ROUTE_NAMES, STATUS
 __all__ = ["FconvError", "FusedConvPlan", "fused_conv", "conv_transpose", "plan_for", "load_library",
            "build", "LayerNormPlan", "RopePlan", "AttentionPlan", "layer_norm",
            "layer_norm_backward", "rope", "rope_frequencies", "attention",
-           "attention_backward", "check_device"]
+           "attention_backward", "check_device", "NormRopePlan", "norm_rope",
+           "norm_rope_backward", "MlpPlan", "gated_mlp", "gated_mlp_backward"]
 
 
 class FconvError(RuntimeError):
@@ -231,6 +233,7 @@ def conv_transpose(x, w, b=None, z=None, *, group: int = 1, strides=None, dilati
 
 
 from . import _ops  # noqa: E402
-from ._ops import (AttentionPlan, LayerNormPlan, RopePlan, attention,  # noqa: E402
-                   attention_backward, check_device, layer_norm, layer_norm_backward, rope,
+from ._ops import (AttentionPlan, LayerNormPlan, MlpPlan, NormRopePlan, RopePlan,  # noqa: E402
+                   attention, attention_backward, check_device, gated_mlp, gated_mlp_backward,
+                   layer_norm, layer_norm_backward, norm_rope, norm_rope_backward, rope,
                    rope_frequencies)

@@ -20,7 +20,8 @@ LIB = os.path.join(HERE, "libfconv.so")
 SOURCES = ["fconv_api.cpp", "k_direct.cu", "k_depthwise.cu", "k_grouped.cu", "k_igemm_tc.cu",
            "k_igemm_patch.cu", "k_igemm_tf32.cu", "k_transposed.cu", "fconv_noalloc.cu",
            "ops/ops_api.cpp", "ops/k_norm.cu", "ops/k_rope.cu", "ops/k_attn_mma.cu",
-           "ops/k_attn_mma_wide.cu", "ops/k_attn_tc_fwd.cu", "ops/k_attn_tc_bwd.cu"]
+           "ops/k_attn_mma_wide.cu", "ops/k_attn_tc_fwd.cu", "ops/k_attn_tc_bwd.cu",
+           "ops/block_api.cpp", "ops/k_norm_rope.cu", "ops/k_mlp_mma.cu", "ops/k_mlp_sums.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

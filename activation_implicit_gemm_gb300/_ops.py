@@ -1,5 +1,6 @@
 """Token-side operators over the C ABI in include/fconv_ops.h: layer norm, rotary positions
-with several axes, and attention, each with its gradient.
+with several axes, alone or with the norm of each head, attention, and the gated feed-forward
+block, each with its gradient.
 
 As with the convolution, PyTorch only provides device memory and streams: plans are cached by
 shape and strides, arguments are checked here and in the library, and every step runs in the
@@ -23,6 +24,8 @@ BF16 = 2
 PAIRINGS = {"interleaved": 0, "half": 1, "half_per_axis": 2}
 ATTN_ROUTES = {"auto": 0, "simple": 1, "tc": 2}
 ATTN_ROUTE_NAMES = {v: k for k, v in ATTN_ROUTES.items()}
+# Activations of the gated block by the convolution's names; Silu is QuickGelu with alpha 1.
+GATES = {None: 0, "Relu": 1, "Sigmoid": 3, "QuickGelu": 8, "Gelu": 10, "FastGelu": 11}
 
 
 class NormDesc(ctypes.Structure):
@@ -36,6 +39,23 @@ class RopeDesc(ctypes.Structure):
                 ("k_stride", I64 * 3), ("q_out_stride", I64 * 3), ("k_out_stride", I64 * 3),
                 ("axes", I32), ("section", I64 * 3), ("pairing", I32), ("pos_type", I32),
                 ("pos_batch", I64), ("inverse", I32)]
+
+
+class NormRopeDesc(ctypes.Structure):
+    _fields_ = [("dtype", I32), ("param_dtype", I32), ("batch", I64), ("len", I64),
+                ("heads_q", I64), ("heads_k", I64), ("head_dim", I64), ("q_stride", I64 * 3),
+                ("k_stride", I64 * 3), ("q_out_stride", I64 * 3), ("k_out_stride", I64 * 3),
+                ("dq_stride", I64 * 3), ("dk_stride", I64 * 3), ("has_weight", I32),
+                ("has_k_weight", I32), ("eps", F32), ("axes", I32), ("section", I64 * 3),
+                ("pairing", I32), ("pos_type", I32), ("pos_batch", I64), ("training", I32)]
+
+
+class MlpDesc(ctypes.Structure):
+    _fields_ = [("dtype", I32), ("tokens", I64), ("features", I64), ("hidden", I64),
+                ("out_features", I64), ("x_stride", I64), ("y_stride", I64),
+                ("gate_stride", I64), ("up_stride", I64), ("down_stride", I64),
+                ("dy_stride", I64), ("dx_stride", I64), ("has_b_gate", I32), ("has_b_up", I32),
+                ("has_b_down", I32), ("activation", I32), ("alpha", F32), ("training", I32)]
 
 
 class AttnDesc(ctypes.Structure):
@@ -63,6 +83,19 @@ _PROTOS = {
     "fconv_attn_forward": [VP] * 9 + [SZ, VP],
     "fconv_attn_backward": [VP] * 13 + [SZ, VP],
     "fconv_attn_destroy": [VP],
+    "fconv_norm_rope_plan_create": [ctypes.POINTER(NormRopeDesc), I32, ctypes.POINTER(VP)],
+    "fconv_norm_rope_workspace_size": [VP, ctypes.POINTER(SZ)],
+    "fconv_norm_rope_forward": [VP] * 10,
+    "fconv_norm_rope_backward": [VP] * 14 + [SZ, VP],
+    "fconv_norm_rope_destroy": [VP],
+    "fconv_mlp_plan_create": [ctypes.POINTER(MlpDesc), I32, I32, ctypes.POINTER(VP)],
+    "fconv_mlp_plan_route": [VP, ctypes.POINTER(I32)],
+    "fconv_mlp_forward_workspace": [VP, ctypes.POINTER(SZ)],
+    "fconv_mlp_backward_workspace": [VP, ctypes.POINTER(SZ)],
+    "fconv_mlp_saved_size": [VP, ctypes.POINTER(SZ)],
+    "fconv_mlp_forward": [VP] * 11 + [SZ, VP],
+    "fconv_mlp_backward": [VP] * 17 + [SZ, VP],
+    "fconv_mlp_destroy": [VP],
     "fconv_ops_check_device": [VP],
     "fconv_ops_status_string": [I32],
 }
@@ -79,8 +112,8 @@ def load() -> ctypes.CDLL:
             f = getattr(lib, name)
             f.argtypes = args
             f.restype = I32
-        for name in ("fconv_norm_destroy", "fconv_rope_destroy", "fconv_attn_destroy"):
-            getattr(lib, name).restype = None
+            if name.endswith("_destroy"):
+                f.restype = None
         lib.fconv_ops_status_string.restype = ctypes.c_char_p
         _ready = lib
     return _ready
@@ -429,8 +462,8 @@ def rope(q, k=None, *, positions, inv_freq, sections: Optional[Sequence[int]] = 
     return out if k is None else (out, k_out)
 
 
-def _rope_plan(q, k, positions, inv_freq, sections, pairing, inverse, out, k_out, device):
-    _heads("rope", "q", q)
+def _positions(who, q, positions, inv_freq, sections):
+    """(sections, code of the positions' type, batches of positions) once they fit q."""
     pos_type = {torch.int32: 0, torch.int64: 1, torch.float32: 2}.get(positions.dtype)
     if pos_type is None:
         raise _error(14, f"positions of {positions.dtype}")
@@ -443,27 +476,387 @@ def _rope_plan(q, k, positions, inv_freq, sections, pairing, inverse, out, k_out
         shape = (1,) + shape
     if (len(shape) != 3 or shape[0] not in (1, q.shape[0]) or shape[1] != q.shape[1]
             or shape[2] != len(sections) or not positions.is_contiguous()):
-        raise ValueError("rope: positions must be contiguous (1 or batch, tokens, axes)")
+        raise ValueError(f"{who}: positions must be contiguous (1 or batch, tokens, axes)")
     if (inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous()
             or inv_freq.numel() != sum(sections)):
-        raise ValueError("rope: inv_freq must be float32 with one value per pair")
+        raise ValueError(f"{who}: inv_freq must be float32 with one value per pair")
+    return sections, pos_type, shape[0]
+
+
+def _k_like_q(who, q, k):
+    _heads(who, "k", k)
+    if k.dtype != q.dtype or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3]:
+        raise ValueError(f"{who}: k must have q's type, batch, tokens and head_dim")
+
+
+def _like(who, name, t, like):
+    if like is None or t.shape != like.shape or t.dtype != like.dtype:
+        raise ValueError(f"{who}: {name} must be like its input")
+    _heads(who, name, t)
+
+
+def _rope_plan(q, k, positions, inv_freq, sections, pairing, inverse, out, k_out, device):
+    _heads("rope", "q", q)
+    sections, pos_type, pos_batch = _positions("rope", q, positions, inv_freq, sections)
     if k is not None:
-        _heads("rope", "k", k)
-        if k.dtype != q.dtype or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3]:
-            raise ValueError("rope: k must have q's type, batch, tokens and head_dim")
+        _k_like_q("rope", q, k)
     for name, t, like in (("out", out, q), ("k_out", k_out, k)):
         if t is not None:
-            if like is None or t.shape != like.shape or t.dtype != like.dtype:
-                raise ValueError(f"rope: {name} must be like its input")
-            _heads("rope", name, t)
+            _like("rope", name, t, like)
     b, t, h, d = q.shape
     none = (0, 0, 0)
     return RopePlan(_code(q.dtype), b, t, h, 0 if k is None else k.shape[2], d,
                     q_stride=q.stride()[:3], q_out_stride=out.stride()[:3],
                     k_stride=none if k is None else k.stride()[:3],
                     k_out_stride=none if k is None else k_out.stride()[:3], sections=sections,
-                    pairing=pairing, pos_type=pos_type, pos_batch=shape[0], inverse=inverse,
+                    pairing=pairing, pos_type=pos_type, pos_batch=pos_batch, inverse=inverse,
                     device=device)
+
+
+# ------------------------------------------------------------------ head norms with positions
+
+class NormRopePlan(_Plan):
+    """A validated norm of every head with rotary positions; strides are (batch, token, head) in
+    elements. With `training` it is of the backward pass: q_out_stride and k_out_stride are those
+    of the incoming gradients, dq_stride and dk_stride of the results."""
+
+    kind = "norm_rope"
+
+    def __init__(self, dtype: int, batch: int, length: int, heads_q: int, heads_k: int,
+                 head_dim: int, *, q_stride, q_out_stride, k_stride=(0, 0, 0),
+                 k_out_stride=(0, 0, 0), dq_stride=(0, 0, 0), dk_stride=(0, 0, 0),
+                 param_dtype: Optional[int] = None, has_weight: bool = True,
+                 has_k_weight: bool = False, eps: float = 1e-6, sections: Sequence[int] = (),
+                 pairing: str = "half", pos_type: int = 0, pos_batch: int = 1,
+                 training: bool = False, device: int = -1):
+        if pairing not in PAIRINGS:
+            raise ValueError(f"pairing must be one of {list(PAIRINGS)}")
+        sec = list(sections)
+        s3 = lambda s: (I64 * 3)(*s)  # noqa: E731
+        desc = NormRopeDesc(dtype, dtype if param_dtype is None else param_dtype, batch, length,
+                            heads_q, heads_k, head_dim, s3(q_stride), s3(k_stride),
+                            s3(q_out_stride), s3(k_out_stride), s3(dq_stride), s3(dk_stride),
+                            int(has_weight), int(has_k_weight), eps, len(sec),
+                            s3((sec + [0, 0, 0])[:3]), PAIRINGS[pairing], pos_type, pos_batch,
+                            int(training))
+        self._create(desc, device)
+        self.workspace_bytes = self._bytes("fconv_norm_rope_workspace_size")
+
+    def forward_ptrs(self, q, k, w, kw, positions, inv_freq, q_out, k_out, stream) -> None:
+        _check(self._lib.fconv_norm_rope_forward(self._ptr, q, k, w, kw, positions, inv_freq,
+                                                 q_out, k_out, stream), "fconv_norm_rope_forward")
+
+    def backward_ptrs(self, dq_out, dk_out, q, k, w, kw, positions, inv_freq, dq, dk, dw, dkw, ws,
+                      ws_bytes, stream) -> None:
+        _check(self._lib.fconv_norm_rope_backward(self._ptr, dq_out, dk_out, q, k, w, kw,
+                                                  positions, inv_freq, dq, dk, dw, dkw, ws,
+                                                  ws_bytes, stream), "fconv_norm_rope_backward")
+
+
+_norm_rope_plans: dict = {}
+
+
+def _form(t):
+    return None if t is None else (t.dtype, t.shape, t.stride())
+
+
+def _norm_rope_plan(who, q, k, weight, k_weight, positions, inv_freq, sections, pairing, eps,
+                    device, outs, grads=None):
+    """The cached plan of a call. outs: y of q and k, or in the backward pass their gradients;
+    grads: the results of the backward pass. Everything the checks look at is in the key."""
+    sections = None if sections is None else tuple(sections)
+    key = (q.dtype, q.shape, q.stride(), _form(k), _form(weight), _form(k_weight),
+           _form(positions), _form(inv_freq), sections, pairing, eps, device, _form(outs[0]),
+           _form(outs[1]), None if grads is None else (_form(grads[0]), _form(grads[1])))
+    p = _norm_rope_plans.get(key)
+    if p is not None:
+        return p
+    _heads(who, "q", q)
+    if k is not None:
+        _k_like_q(who, q, k)
+    if k is None and k_weight is not None:
+        raise ValueError(f"{who}: k_weight without k")
+    params = {w.dtype for w in (weight, k_weight) if w is not None}
+    if len(params) > 1:
+        raise ValueError(f"{who}: weight and k_weight must have one type")
+    for w in (weight, k_weight):
+        if w is not None and (w.shape != q.shape[3:] or not w.is_contiguous()):
+            raise ValueError(f"{who}: weights are vectors of {q.shape[3]} values")
+    pos_type, pos_batch = 0, 1
+    if positions is None:
+        if inv_freq is not None or sections:
+            raise ValueError(f"{who}: inv_freq and sections go with positions")
+        sections = ()
+    elif inv_freq is None:
+        raise ValueError(f"{who}: positions go with inv_freq")
+    else:
+        sections, pos_type, pos_batch = _positions(who, q, positions, inv_freq, sections)
+    pairs = [outs] if grads is None else [outs, grads]
+    for group in pairs:
+        for name, t, like in (("q", group[0], q), ("k", group[1], k)):
+            if (t is None) != (like is None):
+                raise ValueError(f"{who}: k and its gradient go together")
+            if t is not None:
+                _like(who, f"the output or gradient of {name}", t, like)
+    b, n, h, d = q.shape
+    st = lambda t: (0, 0, 0) if t is None else t.stride()[:3]  # noqa: E731
+    p = NormRopePlan(_code(q.dtype), b, n, h, 0 if k is None else k.shape[2], d,
+                     q_stride=st(q), k_stride=st(k), q_out_stride=st(outs[0]),
+                     k_out_stride=st(outs[1]),
+                     dq_stride=st(None if grads is None else grads[0]),
+                     dk_stride=st(None if grads is None else grads[1]),
+                     param_dtype=_code(params.pop()) if params else None,
+                     has_weight=weight is not None, has_k_weight=k_weight is not None, eps=eps,
+                     sections=sections, pairing=pairing, pos_type=pos_type, pos_batch=pos_batch,
+                     training=grads is not None, device=device)
+    return _keep(_norm_rope_plans, key, p)
+
+
+def norm_rope(q, k=None, *, weight=None, k_weight=None, positions=None, inv_freq=None,
+              sections: Optional[Sequence[int]] = None, pairing: str = "half", eps: float = 1e-6,
+              out=None, k_out=None, stream=None):
+    """Divide every head of q (batch, tokens, heads, head_dim), and of k in the same launch, by its
+    root mean square (sqrt(mean(x^2) + eps)), multiply it by a weight of head_dim values (of q's
+    type or float32, one for all heads of q, another for all of k) and turn its pairs by position
+    as `rope` does, whose positions, inv_freq, sections and pairing these are. Without positions
+    only the norm. head_dim is at most 512. q and k may be strided views with a contiguous last
+    axis; out and k_out may be q and k. Returns q', or (q', k')."""
+    if torch is None:
+        _start()
+    if stream is not None:
+        with _on_stream(stream, q, k, weight, k_weight, positions, inv_freq, out, k_out):
+            return norm_rope(q, k, weight=weight, k_weight=k_weight, positions=positions,
+                             inv_freq=inv_freq, sections=sections, pairing=pairing, eps=eps,
+                             out=out, k_out=k_out)
+    device = q.get_device()
+    _on_cuda("norm_rope", device, k, weight, k_weight, positions, inv_freq, out, k_out)
+    if out is None:
+        out = _new(q)
+    if k is not None and k_out is None:
+        k_out = _new(k)
+    p = _norm_rope_plan("norm_rope", q, k, weight, k_weight, positions, inv_freq, sections,
+                        pairing, eps, device, (out, k_out))
+    _run(device, p.forward_ptrs, q.data_ptr(), _ptr(k), _ptr(weight), _ptr(k_weight),
+         _ptr(positions), _ptr(inv_freq), out.data_ptr(), _ptr(k_out), _current_stream(device))
+    return out if k is None else (out, k_out)
+
+
+def norm_rope_backward(dout, q, dk_out=None, k=None, *, weight=None, k_weight=None, positions=None,
+                       inv_freq=None, sections: Optional[Sequence[int]] = None,
+                       pairing: str = "half", eps: float = 1e-6, dq=None, dk=None,
+                       param_grads: bool = True, stream=None):
+    """Gradients (dq, dk, dweight, dk_weight) of norm_rope from those of its outputs. q and k are
+    its inputs, which must still hold what they held then (so not after a call in place); dq and
+    dk may be given (dout and dk_out among others, or strided views of one buffer). dk is None
+    without k, a weight's gradient without the weight or without param_grads."""
+    if torch is None:
+        _start()
+    if stream is not None:
+        with _on_stream(stream, dout, q, dk_out, k, weight, k_weight, positions, inv_freq, dq, dk):
+            return norm_rope_backward(dout, q, dk_out, k, weight=weight, k_weight=k_weight,
+                                      positions=positions, inv_freq=inv_freq, sections=sections,
+                                      pairing=pairing, eps=eps, dq=dq, dk=dk,
+                                      param_grads=param_grads)
+    device = q.get_device()
+    _on_cuda("norm_rope_backward", device, dout, dk_out, k, weight, k_weight, positions, inv_freq,
+             dq, dk)
+    dq = _new(q) if dq is None else dq
+    if k is not None and dk is None:
+        dk = _new(k)
+    p = _norm_rope_plan("norm_rope_backward", q, k, weight, k_weight, positions, inv_freq,
+                        sections, pairing, eps, device, (dout, dk_out), (dq, dk))
+    dw = torch.empty_like(weight) if weight is not None and param_grads else None
+    dkw = torch.empty_like(k_weight) if k_weight is not None and param_grads else None
+    n = p.workspace_bytes if dw is not None or dkw is not None else 0
+    ws = _workspace(n, q)
+    _run(device, p.backward_ptrs, dout.data_ptr(), _ptr(dk_out), q.data_ptr(), _ptr(k),
+         _ptr(weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), dq.data_ptr(), _ptr(dk),
+         _ptr(dw), _ptr(dkw), _ptr(ws), n, _current_stream(device))
+    return dq, dk, dw, dkw
+
+
+# -------------------------------------------------------------------- gated feed-forward block
+
+class MlpPlan(_Plan):
+    """A validated gated feed-forward block; strides are those between rows, in elements. A plan
+    made with `training` also runs the backward pass."""
+
+    kind = "mlp"
+
+    def __init__(self, dtype: int, tokens: int, features: int, hidden: int, out_features: int, *,
+                 x_stride: int, y_stride: int, gate_stride: int, up_stride: int, down_stride: int,
+                 dy_stride: int = 0, dx_stride: int = 0, has_b_gate: bool = False,
+                 has_b_up: bool = False, has_b_down: bool = False, activation: int = 8,
+                 alpha: float = 1.0, training: bool = False, route: str = "auto",
+                 device: int = -1):
+        desc = MlpDesc(dtype, tokens, features, hidden, out_features, x_stride, y_stride,
+                       gate_stride, up_stride, down_stride, dy_stride, dx_stride,
+                       int(has_b_gate), int(has_b_up), int(has_b_down), activation, alpha,
+                       int(training))
+        self._create(desc, device, ATTN_ROUTES[route])
+        self.forward_workspace = self._bytes("fconv_mlp_forward_workspace")
+        self.backward_workspace = self._bytes("fconv_mlp_backward_workspace")
+        self.saved_bytes = self._bytes("fconv_mlp_saved_size")
+        r = I32()
+        _check(self._lib.fconv_mlp_plan_route(self._ptr, ctypes.byref(r)), "route")
+        self.route = ATTN_ROUTE_NAMES[r.value]
+
+    def forward_ptrs(self, x, wg, wu, wd, bg, bu, bd, y, saved, ws, ws_bytes, stream) -> None:
+        _check(self._lib.fconv_mlp_forward(self._ptr, x, wg, wu, wd, bg, bu, bd, y, saved, ws,
+                                           ws_bytes, stream), "fconv_mlp_forward")
+
+    def backward_ptrs(self, dy, x, wg, wu, wd, bg, bu, saved, dx, dwg, dwu, dwd, dbg, dbu, dbd,
+                      ws, ws_bytes, stream) -> None:
+        _check(self._lib.fconv_mlp_backward(self._ptr, dy, x, wg, wu, wd, bg, bu, saved, dx, dwg,
+                                            dwu, dwd, dbg, dbu, dbd, ws, ws_bytes, stream),
+               "fconv_mlp_backward")
+
+
+_mlp_plans: dict = {}
+
+
+def _row_stride(who, name, t):
+    """The stride between the rows of a tensor seen as (rows, last axis)."""
+    if t.dim() < 2 or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{who}: {name} must have rows that are contiguous")
+    if t.dim() > 2 and not t.is_contiguous():
+        try:
+            t = t.view(-1, t.shape[-1])
+        except RuntimeError:
+            raise ValueError(f"{who}: the rows of {name} must be one stride apart") from None
+    if t.dim() > 2:
+        return t.shape[-1]
+    return t.stride(0)
+
+
+def _gate(who, activation, params):
+    """(code, alpha) of an activation by its name."""
+    if activation == "Silu":
+        if params is not None:
+            raise ValueError(f"{who}: Silu takes no parameters")
+        return GATES["QuickGelu"], 1.0
+    if activation not in GATES:
+        raise ValueError(f"{who}: activation must be Silu or one of {list(GATES)}")
+    params = [] if params is None else list(params)
+    if len(params) > (activation == "QuickGelu"):
+        raise ValueError(f"{who}: {activation} takes fewer parameters")
+    return GATES[activation], float(params[0]) if params else 1.702
+
+
+def _mlp_plan(who, x, weights, biases, activation, params, route, device, y, grads=None):
+    """The cached plan of a call. grads: (dy, dx) of a backward pass (y is dy then)."""
+    key = (_form(x), *map(_form, weights), *map(_form, biases), activation,
+           None if params is None else tuple(params), route, device, _form(y),
+           None if grads is None else _form(grads))
+    p = _mlp_plans.get(key)
+    if p is not None:
+        return p
+    wg, wu, wd = weights
+    for name, w in (("w_gate", wg), ("w_up", wu), ("w_down", wd)):
+        if w.dim() != 2 or w.dtype != x.dtype:
+            raise ValueError(f"{who}: {name} must be a matrix of x's type")
+    if x.dim() < 2:
+        raise ValueError(f"{who}: x must be (..., tokens, features)")
+    hidden, features = wg.shape
+    if wu.shape != wg.shape or x.shape[-1] != features or wd.shape[1] != hidden:
+        raise ValueError(f"{who}: w_gate and w_up must be (hidden, {x.shape[-1]}) and w_down "
+                         "(out_features, hidden)")
+    for name, b, n in zip(("b_gate", "b_up", "b_down"), biases, (hidden, hidden, wd.shape[0])):
+        if b is not None and (b.shape != (n,) or b.dtype != x.dtype or not b.is_contiguous()):
+            raise ValueError(f"{who}: {name} must be a vector of {n} values of x's type")
+    if y.shape != x.shape[:-1] + wd.shape[:1] or y.dtype != x.dtype:
+        raise ValueError(f"{who}: the output and its gradient are "
+                         f"{tuple(x.shape[:-1] + wd.shape[:1])} of x's type")
+    if grads is not None and (grads.shape != x.shape or grads.dtype != x.dtype):
+        raise ValueError(f"{who}: dx must be like x")
+    code, alpha = _gate(who, activation, params)
+    if route not in ATTN_ROUTES:
+        raise ValueError(f"{who}: route must be one of {list(ATTN_ROUTES)}")
+    out_row = _row_stride(who, "y" if grads is None else "dy", y)
+    p = MlpPlan(_code(x.dtype), math.prod(x.shape[:-1]), features, hidden, wd.shape[0],
+                x_stride=_row_stride(who, "x", x),
+                y_stride=out_row if grads is None else wd.shape[0],
+                gate_stride=_row_stride(who, "w_gate", wg),
+                up_stride=_row_stride(who, "w_up", wu),
+                down_stride=_row_stride(who, "w_down", wd),
+                dy_stride=0 if grads is None else out_row,
+                dx_stride=0 if grads is None else _row_stride(who, "dx", grads),
+                has_b_gate=biases[0] is not None, has_b_up=biases[1] is not None,
+                has_b_down=biases[2] is not None, activation=code, alpha=alpha,
+                training=grads is not None, route=route, device=device)
+    return _keep(_mlp_plans, key, p)
+
+
+def gated_mlp(x, w_gate, w_up, w_down, *, b_gate=None, b_up=None, b_down=None,
+              activation: Optional[str] = "Silu", activation_params=None, out=None,
+              return_saved: bool = False, route: str = "auto", stream=None):
+    """(act(x w_gate^T + b_gate) * (x w_up^T + b_up)) w_down^T + b_down for x (..., features),
+    w_gate and w_up (hidden, features) and w_down (out_features, hidden). Rows are contiguous and
+    one stride apart, so gate and up may be halves of one packed weight. activation is Silu, Gelu
+    (erf), FastGelu (tanh), QuickGelu (activation_params: alpha), Relu, Sigmoid or None. With
+    return_saved also what the gradient takes: both projections in float32, 8 bytes a token and
+    hidden value, in an order of the library's own."""
+    if torch is None:
+        _start()
+    if stream is not None:
+        with _on_stream(stream, x, w_gate, w_up, w_down, b_gate, b_up, b_down, out):
+            return gated_mlp(x, w_gate, w_up, w_down, b_gate=b_gate, b_up=b_up, b_down=b_down,
+                             activation=activation, activation_params=activation_params, out=out,
+                             return_saved=return_saved, route=route)
+    device = x.get_device()
+    _on_cuda("gated_mlp", device, w_gate, w_up, w_down, b_gate, b_up, b_down, out)
+    if out is None:
+        out = torch.empty(x.shape[:-1] + w_down.shape[:1], dtype=x.dtype, device=x.device)
+    p = _mlp_plan("gated_mlp", x, (w_gate, w_up, w_down), (b_gate, b_up, b_down), activation,
+                  activation_params, route, device, out)
+    saved = None
+    if return_saved:
+        saved = torch.empty(p.saved_bytes // 4, dtype=torch.float32, device=x.device)
+    n = p.forward_workspace
+    ws = _workspace(n, x)
+    _run(device, p.forward_ptrs, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+         w_down.data_ptr(), _ptr(b_gate), _ptr(b_up), _ptr(b_down), out.data_ptr(), _ptr(saved),
+         _ptr(ws), n, _current_stream(device))
+    return (out, saved) if return_saved else out
+
+
+def gated_mlp_backward(dy, x, w_gate, w_up, w_down, saved=None, *, b_gate=None, b_up=None,
+                       b_down=None, activation: Optional[str] = "Silu", activation_params=None,
+                       dx=None, param_grads: bool = True, route: str = "auto", stream=None):
+    """Gradients (dx, dw_gate, dw_up, dw_down, db_gate, db_up, db_down) of gated_mlp. saved is what
+    it returned for these inputs; without it the projections are made again, for two more products
+    of x. Of b_down only its presence matters. The gradients of absent biases are None, and without
+    param_grads all but dx."""
+    if torch is None:
+        _start()
+    if stream is not None:
+        with _on_stream(stream, dy, x, w_gate, w_up, w_down, saved, b_gate, b_up, b_down, dx):
+            return gated_mlp_backward(dy, x, w_gate, w_up, w_down, saved, b_gate=b_gate,
+                                      b_up=b_up, b_down=b_down, activation=activation,
+                                      activation_params=activation_params, dx=dx,
+                                      param_grads=param_grads, route=route)
+    device = x.get_device()
+    _on_cuda("gated_mlp_backward", device, dy, w_gate, w_up, w_down, saved, b_gate, b_up, b_down,
+             dx)
+    dx = _new(x) if dx is None else dx
+    weights, biases = (w_gate, w_up, w_down), (b_gate, b_up, b_down)
+    p = _mlp_plan("gated_mlp_backward", x, weights, biases, activation, activation_params, route,
+                  device, dy, dx)
+    n = p.backward_workspace
+    if saved is not None:
+        if (saved.dtype != torch.float32 or saved.dim() != 1 or not saved.is_contiguous()
+                or saved.numel() * 4 != p.saved_bytes):
+            raise ValueError("gated_mlp_backward: saved must be what gated_mlp returned")
+        n -= p.saved_bytes
+    dw, db = [None] * 3, [None] * 3
+    if param_grads:
+        dw = [_new(w) for w in weights]
+        db = [None if b is None else _new(b) for b in biases]
+    ws = _workspace(n, x)
+    _run(device, p.backward_ptrs, dy.data_ptr(), x.data_ptr(), w_gate.data_ptr(),
+         w_up.data_ptr(), w_down.data_ptr(), _ptr(b_gate), _ptr(b_up), _ptr(saved), dx.data_ptr(),
+         *map(_ptr, dw), *map(_ptr, db), _ptr(ws), n, _current_stream(device))
+    return (dx, *dw, *db)
 
 
 # ---------------------------------------------------------------------------------- attention

@@ -41,6 +41,62 @@ struct RopeArgs {
 };
 int launch_rope(const fconv_rope_desc& d, int sms, const RopeArgs& a, cudaStream_t s);
 
+struct NormRopeArgs {
+  const void* q;
+  const void* k;
+  const void* w;
+  const void* kw;
+  const void* pos;
+  const float* inv_freq;
+  const void* q_out;  // written by the forward pass, the incoming gradient of the backward pass
+  const void* k_out;
+  void* dq;  // backward
+  void* dk;
+  void* dw;
+  void* dkw;
+  float* ws;  // null: no weight's gradient is wanted
+};
+constexpr int kNormRopeMostDim = 512;
+int launch_norm_rope_forward(const fconv_norm_rope_desc& d, int sms, const NormRopeArgs& a,
+                             cudaStream_t s);
+int launch_norm_rope_backward(const fconv_norm_rope_desc& d, int sms, const NormRopeArgs& a,
+                              cudaStream_t s);
+size_t norm_rope_workspace(const fconv_norm_rope_desc& d, int sms);
+
+struct MlpArgs {
+  const void* x;
+  const void* w_gate;
+  const void* w_up;
+  const void* w_down;
+  const void* b_gate;
+  const void* b_up;
+  const void* b_down;
+  void* y;
+  const void* dy;  // backward
+  void* dx;
+  void* dw_gate;
+  void* dw_up;
+  void* dw_down;
+  float* saved;  // g and u, or null
+  bool remake;   // backward: make g and u first
+  void* h;       // in the workspace, rows of `hidden` values, as are dg and du
+  void* dg;
+  void* du;
+};
+size_t mlp_saved_bytes(const fconv_mlp_desc& d);
+int launch_mlp_simple_forward(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s);
+int launch_mlp_simple_backward(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s);
+
+// Column sums of up to three matrices with the same rows (those without `out` are left out).
+struct SumsArgs {
+  const void* p;
+  int64_t row, cols;  // stride of the rows in elements
+  void* out;
+};
+size_t column_sums_workspace(const int64_t cols[3], int sms);
+int launch_column_sums(int dtype, const SumsArgs m[3], int64_t rows, float* part, int sms,
+                       cudaStream_t s);
+
 struct AttnArgs {
   const void* q;
   const void* k;

@@ -1,6 +1,7 @@
 /*
  * fconv_ops.h -- C ABI of the token-side operators in libfconv.so: layer norm, rotary
- * positions with several axes, and attention, each with its gradient.
+ * positions with several axes (alone, or with the norm of each head), attention, and the gated
+ * feed-forward block, each with its gradient.
  *
  * They follow the conventions of fconv.h: a descriptor is validated by *_plan_create before
  * anything is allocated or launched; a plan owns only host state; the caller owns every tensor
@@ -107,6 +108,50 @@ fconv_status fconv_rope_run(const fconv_rope_plan* plan, const void* q, const vo
                             void* k_out, void* stream);
 void fconv_rope_destroy(fconv_rope_plan* plan);
 
+/* ------------------------------------------- norm of each head, with rotary positions
+ * Every head of q (batch, len, heads_q, head_dim) and k (batch, len, heads_k, head_dim) is divided
+ * by its root mean square, multiplied by a weight of head_dim values and turned by its token's
+ * position, in one pass:
+ *   n = x * r,  r = 1 / sqrt(mean(x^2) + eps),  z = n * w,  y = z turned as by fconv_rope_run
+ * Strides and positions are those of fconv_rope_desc; axes = 0 leaves the rotation out (positions
+ * and inv_freq are then NULL). Weights have param_dtype, which is dtype or FCONV_F32; q and k have
+ * one each, both optional. heads_k = 0 for q alone. head_dim 1..512. */
+typedef struct {
+  int dtype, param_dtype;
+  int64_t batch, len, heads_q, heads_k, head_dim;
+  int64_t q_stride[3], k_stride[3];         /* of (batch, token, head), in elements */
+  int64_t q_out_stride[3], k_out_stride[3]; /* forward: y; backward: y's gradient */
+  int64_t dq_stride[3], dk_stride[3];       /* backward: x's gradient */
+  int has_weight, has_k_weight;
+  float eps; /* finite and > 0 */
+  int axes;  /* 0..3 */
+  int64_t section[3];
+  int pairing, pos_type;
+  int64_t pos_batch;
+  int training; /* 1: the plan is of the backward pass */
+} fconv_norm_rope_desc;
+typedef struct fconv_norm_rope_plan fconv_norm_rope_plan;
+
+fconv_status fconv_norm_rope_plan_create(const fconv_norm_rope_desc* desc, int device,
+                                         fconv_norm_rope_plan** out);
+/* Workspace of the backward pass where a weight's gradient is wanted. */
+fconv_status fconv_norm_rope_workspace_size(const fconv_norm_rope_plan* plan, size_t* bytes);
+/* q_out may be q with the same strides (in place), likewise k. */
+fconv_status fconv_norm_rope_forward(const fconv_norm_rope_plan* plan, const void* q,
+                                     const void* k, const void* weight, const void* k_weight,
+                                     const void* positions, const float* inv_freq, void* q_out,
+                                     void* k_out, void* stream);
+/* q and k are the forward pass's inputs; r is made again from them. dq may be dq_out with the same
+ * strides, likewise dk. dweight and dk_weight are sums over batch, tokens and heads, of
+ * param_dtype; they may be NULL (not wanted). */
+fconv_status fconv_norm_rope_backward(const fconv_norm_rope_plan* plan, const void* dq_out,
+                                      const void* dk_out, const void* q, const void* k,
+                                      const void* weight, const void* k_weight,
+                                      const void* positions, const float* inv_freq, void* dq,
+                                      void* dk, void* dweight, void* dk_weight, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+void fconv_norm_rope_destroy(fconv_norm_rope_plan* plan);
+
 /* ---------------------------------------------------------------------------- attention
  * q, out, dout, dq: (batch, len_q, heads_q, head_dim); k, v, dk, dv: (batch, len_k, heads_kv,
  * head_dim); any strides of the first three axes (in elements; 0 on an input broadcasts), the
@@ -162,6 +207,60 @@ fconv_status fconv_attn_backward(const fconv_attn_plan* plan, const void* dout, 
                                  void* dk, void* dv, void* workspace, size_t workspace_bytes,
                                  void* stream);
 void fconv_attn_destroy(fconv_attn_plan* plan);
+
+/* ---------------------------------------------------------- gated feed-forward block
+ *   g = x w_gate^T + b_gate,  u = x w_up^T + b_up,  h = act(g) * u,  y = h w_down^T + b_down
+ * x is (tokens, features), w_gate and w_up (hidden, features), w_down (out_features, hidden), y
+ * (tokens, out_features); all with contiguous rows a stride (in elements) apart, so that gate and
+ * up may be halves of one packed weight. Biases are contiguous, each optional, and of dtype.
+ * act is one of FCONV_ACT_NONE, RELU, SIGMOID, GELU (erf), FASTGELU (tanh) and QUICKGELU
+ * (v * sigmoid(alpha v); alpha = 1 is SiLU). With no tokens the weights' gradients are zero.
+ * g and u are f32; h, and in the backward pass the gradients of g and u, are rounded to dtype
+ * once as operands of the next product: in f16 they overflow past 65504 and lose bits under 6e-5.
+ * The 16-bit outputs are off by about 1.4 times their own rounding. */
+typedef struct {
+  int dtype;
+  int64_t tokens, features, hidden, out_features;
+  int64_t x_stride, y_stride, gate_stride, up_stride, down_stride;
+  int64_t dy_stride, dx_stride; /* backward only; weights' gradients are contiguous */
+  int has_b_gate, has_b_up, has_b_down;
+  int activation; /* fconv_act */
+  float alpha;    /* of QUICKGELU */
+  int training;   /* 1: the plan also runs the backward pass */
+} fconv_mlp_desc;
+typedef enum {
+  FCONV_MLP_AUTO = 0,
+  FCONV_MLP_SIMPLE = 1, /* every type, size and stride: warp-level tensor instructions */
+  FCONV_MLP_TC = 2      /* tcgen05 tensor cores: f16 and bf16, sizes and strides multiples of 8,
+                           16-byte addresses */
+} fconv_mlp_route;
+typedef struct fconv_mlp_plan fconv_mlp_plan;
+
+/* route: FCONV_MLP_AUTO, or one that must run the request (else FCONV_E_UNSUPPORTED). */
+fconv_status fconv_mlp_plan_create(const fconv_mlp_desc* desc, int device, int route,
+                                   fconv_mlp_plan** out);
+/* The route of a call whose device addresses are 16-byte aligned (a call with others runs on
+ * FCONV_MLP_SIMPLE, unless the plan was made for FCONV_MLP_TC: then FCONV_E_ALIGNMENT). */
+fconv_status fconv_mlp_plan_route(const fconv_mlp_plan* plan, int* route);
+fconv_status fconv_mlp_forward_workspace(const fconv_mlp_plan* plan, size_t* bytes);
+fconv_status fconv_mlp_backward_workspace(const fconv_mlp_plan* plan, size_t* bytes);
+/* Bytes of `saved`: g and u in f32, in an order of the library's own. */
+fconv_status fconv_mlp_saved_size(const fconv_mlp_plan* plan, size_t* bytes);
+/* saved may be NULL (inference, or a backward pass that makes g and u again). y must not be an
+ * input. */
+fconv_status fconv_mlp_forward(const fconv_mlp_plan* plan, const void* x, const void* w_gate,
+                               const void* w_up, const void* w_down, const void* b_gate,
+                               const void* b_up, const void* b_down, void* y, float* saved,
+                               void* workspace, size_t workspace_bytes, void* stream);
+/* saved is a forward pass's of the same x, w_gate, w_up and biases, or NULL: g and u are then made
+ * again from these. Every gradient may be NULL (not wanted). */
+fconv_status fconv_mlp_backward(const fconv_mlp_plan* plan, const void* dy, const void* x,
+                                const void* w_gate, const void* w_up, const void* w_down,
+                                const void* b_gate, const void* b_up, const float* saved, void* dx,
+                                void* dw_gate, void* dw_up, void* dw_down, void* db_gate,
+                                void* db_up, void* db_down, void* workspace,
+                                size_t workspace_bytes, void* stream);
+void fconv_mlp_destroy(fconv_mlp_plan* plan);
 
 #ifdef __cplusplus
 }
