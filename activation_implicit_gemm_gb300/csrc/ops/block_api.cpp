@@ -18,6 +18,7 @@ struct fconv_mlp_plan {
   fconv_mlp_desc d;
   int sms;
   int want;
+  bool tc;               // tensor cores for calls with aligned addresses
   size_t saved, matrix;  // bytes of g and u, and of a (tokens, hidden) operand
   size_t sums;           // of the bias gradients
   size_t fwd_ws, bwd_ws;
@@ -229,12 +230,14 @@ fconv_status fconv_mlp_plan_create(const fconv_mlp_desc* desc, int device, int r
   if (st != FCONV_OK) return st;
   fconv_mlp_plan* p = *out;
   const fconv_mlp_desc& d = p->d;
-  if (route < FCONV_MLP_AUTO || route > FCONV_MLP_TC || route == FCONV_MLP_TC) {
+  const bool tc = mlp_tc_supported(d);
+  if (route < FCONV_MLP_AUTO || route > FCONV_MLP_TC || (route == FCONV_MLP_TC && !tc)) {
     delete p;
     *out = nullptr;
     return FCONV_E_UNSUPPORTED;
   }
   p->want = route;
+  p->tc = tc && route != FCONV_MLP_SIMPLE;
   p->saved = mlp_saved_bytes(d);
   p->matrix = whole((size_t)d.tokens * (size_t)d.hidden * type_size(d.dtype));
   p->fwd_ws = p->matrix;
@@ -248,7 +251,7 @@ fconv_status fconv_mlp_plan_create(const fconv_mlp_desc* desc, int device, int r
 
 fconv_status fconv_mlp_plan_route(const fconv_mlp_plan* p, int* route) {
   if (!p || !route) return FCONV_E_NULL;
-  *route = FCONV_MLP_SIMPLE;
+  *route = p->tc ? FCONV_MLP_TC : FCONV_MLP_SIMPLE;
   return FCONV_OK;
 }
 
@@ -301,6 +304,13 @@ fconv_status fconv_mlp_forward(const fconv_mlp_plan* p, const void* x, const voi
   a.y = y;
   a.saved = saved;
   a.h = workspace;
+  if (p->tc) {
+    bool whole = true;
+    for (const void* v : {x, w_gate, w_up, w_down, b_gate, b_up, b_down, (const void*)y})
+      whole = whole && !misaligned(v, 16);
+    if (whole) return done(launch_mlp_tc_forward(d, p->sms, a, (cudaStream_t)stream));
+    if (p->want == FCONV_MLP_TC) return FCONV_E_ALIGNMENT;
+  }
   return done(launch_mlp_simple_forward(d, a, (cudaStream_t)stream));
 }
 
@@ -352,7 +362,15 @@ fconv_status fconv_mlp_backward(const fconv_mlp_plan* p, const void* dy, const v
   float* sums = (float*)(at + 3 * p->matrix);
   a.saved = saved ? const_cast<float*>(saved) : (float*)(at + 3 * p->matrix + p->sums);
   a.remake = !saved;
-  int err = launch_mlp_simple_backward(d, a, (cudaStream_t)stream);
+  bool tc = p->tc && d.tokens > 0;
+  if (tc) {
+    for (const void* v : {dy, x, w_gate, w_up, w_down, b_gate, b_up, (const void*)dx,
+                          (const void*)dw_gate, (const void*)dw_up, (const void*)dw_down})
+      tc = tc && !misaligned(v, 16);
+    if (!tc && p->want == FCONV_MLP_TC) return FCONV_E_ALIGNMENT;
+  }
+  const int err = tc ? launch_mlp_tc_backward(d, p->sms, a, (cudaStream_t)stream)
+                     : launch_mlp_simple_backward(d, a, (cudaStream_t)stream);
   if (err) return done(err);
   const SumsArgs m[3] = {{a.dg, d.hidden, d.hidden, db_gate},
                          {a.du, d.hidden, d.hidden, db_up},

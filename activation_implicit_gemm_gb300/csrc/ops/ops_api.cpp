@@ -159,12 +159,13 @@ const char* fconv_ops_status_string(int s) {
 }
 
 fconv_status fconv_ops_check_device(void* stream) {
-  unsigned n = 0, f = 0, b = 0;
+  unsigned n = 0, f = 0, b = 0, m = 0;
   if (read_and_clear_norm_error((cudaStream_t)stream, &n) != 0 ||
       read_and_clear_attn_forward_error((cudaStream_t)stream, &f) != 0 ||
-      read_and_clear_attn_backward_error((cudaStream_t)stream, &b) != 0)
+      read_and_clear_attn_backward_error((cudaStream_t)stream, &b) != 0 ||
+      read_and_clear_mlp_error((cudaStream_t)stream, &m) != 0)
     return FCONV_E_CUDA;
-  return n || f || b ? FCONV_E_DEVICE_TIMEOUT : FCONV_OK;
+  return n || f || b || m ? FCONV_E_DEVICE_TIMEOUT : FCONV_OK;
 }
 
 // ---------------------------------------------------------------------------- layer norm

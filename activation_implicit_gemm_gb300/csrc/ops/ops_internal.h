@@ -86,6 +86,11 @@ struct MlpArgs {
 size_t mlp_saved_bytes(const fconv_mlp_desc& d);
 int launch_mlp_simple_forward(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s);
 int launch_mlp_simple_backward(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s);
+// Tensor-core route (k_mlp_tc.cu): addresses must be 16-byte aligned, tokens > 0.
+bool mlp_tc_supported(const fconv_mlp_desc& d);
+int launch_mlp_tc_forward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s);
+int launch_mlp_tc_backward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s);
+int read_and_clear_mlp_error(cudaStream_t s, unsigned* value);
 
 // Column sums of up to three matrices with the same rows (those without `out` are left out).
 struct SumsArgs {

@@ -70,6 +70,14 @@ def test_forward_and_backward(n, c, f, o, dtype):
     check_all(both_passes(*ins), *ins)
 
 
+@pytest.mark.parametrize("dtype,n", [("f16", 2600), ("bf16", 2440)])
+def test_many_tiles(dtype, n):
+    """Enough tiles for the variants that fill the GPU, with ragged ends in every axis; the last
+    rows leave half of a 256-row tile empty, or part of it."""
+    ins = case(15, n, 1032, 1104, 1048, R.TYPES[dtype])
+    check_all(both_passes(*ins), *ins)
+
+
 @pytest.mark.parametrize("route", ["simple", "auto"])
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("activation,params", [
