@@ -11,7 +11,7 @@ namespace fconv {
 namespace ops {
 namespace {
 
-constexpr int kCols = 64, kRowsAtOnce = 16;  // 32 lanes of two columns each, 16 warps
+constexpr int kThreads = 256, kCols = 64;
 
 struct Sums {
   SumsArgs m[3];
@@ -24,31 +24,53 @@ __device__ __forceinline__ int matrix_of(const Sums& q, int block) {
   return block >= q.first[2] ? 2 : block >= q.first[1] ? 1 : 0;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(32 * kRowsAtOnce)
-    column_sums(const __grid_constant__ Sums q) {
-  __shared__ float sums[kRowsAtOnce][kCols + 1];
+// VEC columns a thread in one access, kCols / VEC threads a row, four rows on their way at a time.
+template <typename T, int VEC>
+__device__ __forceinline__ void sum_rows(const T* p, int64_t row, int64_t cols, int64_t c,
+                                         int64_t r, int64_t r1, float (&sum)[VEC]) {
+  constexpr int kRows = kThreads / (kCols / VEC), kAhead = 4;
+  if (c >= cols) return;  // cols is a multiple of VEC
+  p += c;
+  for (; r + (kAhead - 1) * kRows < r1; r += kAhead * kRows) {
+    float x[kAhead][VEC];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load_f<T, VEC>(p + (r + i * kRows) * row, x[i]);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) sum[e] += x[i][e];
+  }
+  for (; r < r1; r += kRows) {
+    float x[VEC];
+    load_f<T, VEC>(p + r * row, x);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) sum[e] += x[e];
+  }
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kThreads) column_sums(const __grid_constant__ Sums q) {
+  constexpr int kAcross = kCols / VEC, kRows = kThreads / kAcross;
+  __shared__ float sums[kRows][kCols + 1];
   ptx::pdl_wait();
   ptx::pdl_trigger();
   const int which = matrix_of(q, blockIdx.x);
   const SumsArgs& m = q.m[which];
   const int64_t c0 = (int64_t)(blockIdx.x - q.first[which]) * kCols;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c = c0 + 2 * lane;
+  const int across = threadIdx.x % kAcross, down = threadIdx.x / kAcross;
   const int64_t each = (q.rows + q.shares - 1) / q.shares;
   const int64_t r1 = min(((int64_t)blockIdx.y + 1) * each, q.rows);
-  float a = 0.0f, b = 0.0f;
-  const T* p = (const T*)m.p + c;
-  for (int64_t r = blockIdx.y * each + warp; r < r1; r += kRowsAtOnce) {
-    if (c < m.cols) a += to_f(p[r * m.row]);
-    if (c + 1 < m.cols) b += to_f(p[r * m.row + 1]);
-  }
-  sums[warp][2 * lane] = a;
-  sums[warp][2 * lane + 1] = b;
+  float sum[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) sum[e] = 0.0f;
+  sum_rows<T, VEC>((const T*)m.p, m.row, m.cols, c0 + across * VEC, blockIdx.y * each + down, r1,
+                   sum);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) sums[down][across * VEC + e] = sum[e];
   __syncthreads();
   if (threadIdx.x >= kCols) return;
   float v = 0.0f;
-  for (int i = 0; i < kRowsAtOnce; ++i) v += sums[i][threadIdx.x];
+  for (int i = 0; i < kRows; ++i) v += sums[i][threadIdx.x];
   q.part[((int64_t)blockIdx.y * q.first[3] + blockIdx.x) * kCols + threadIdx.x] = v;
 }
 
@@ -68,9 +90,9 @@ __global__ void __launch_bounds__(kCols) column_join(const __grid_constant__ Sum
 
 int64_t blocks_of(int64_t cols) { return (cols + kCols - 1) / kCols; }
 
-// Shares of the rows: about two blocks an SM, of 64 rows at least.
+// Shares of the rows: about four blocks an SM, of 64 rows at least.
 int shares_of(int64_t blocks, int64_t rows, int sms) {
-  int64_t n = (2 * sms + blocks - 1) / (blocks > 0 ? blocks : 1);
+  int64_t n = (4 * sms + blocks - 1) / (blocks > 0 ? blocks : 1);
   const int64_t most = (rows + 63) / 64;
   if (n > most) n = most;
   return n < 1 ? 1 : (int)n;
@@ -82,7 +104,7 @@ int shares_of(int64_t blocks, int64_t rows, int sms) {
 size_t column_sums_workspace(const int64_t cols[3], int sms) {
   int64_t blocks = 0;
   for (int i = 0; i < 3; ++i) blocks += blocks_of(cols[i]);
-  return (size_t)(2 * (int64_t)sms + 2 * blocks) * kCols * sizeof(float);
+  return (size_t)(4 * (int64_t)sms + 2 * blocks) * kCols * sizeof(float);
 }
 
 int launch_column_sums(int dtype, const SumsArgs m[3], int64_t rows, float* part, int sms,
@@ -96,10 +118,17 @@ int launch_column_sums(int dtype, const SumsArgs m[3], int64_t rows, float* part
   }
   if (q.first[3] == 0) return 0;
   q.shares = shares_of(q.first[3], rows, sms);
+  // 16-byte accesses where every row of every matrix starts on one
+  const int full = dtype == FCONV_F32 ? 4 : 8;
+  bool wide = true;
+  for (int i = 0; i < 3; ++i)
+    if (m[i].out)
+      wide = wide && m[i].cols % full == 0 && m[i].row % full == 0 && (uintptr_t)m[i].p % 16 == 0;
+  const dim3 grid((unsigned)q.first[3], (unsigned)q.shares);
   int e = 0;
-#define FCONV_M(T)                                                                            \
-  e = launch_pdl(column_sums<T>, dim3((unsigned)q.first[3], (unsigned)q.shares),              \
-                 dim3(32 * kRowsAtOnce), 0, s, q);                                            \
+#define FCONV_M(T)                                                                             \
+  e = wide ? launch_pdl(column_sums<T, 16 / (int)sizeof(T)>, grid, dim3(kThreads), 0, s, q)    \
+           : launch_pdl(column_sums<T, 1>, grid, dim3(kThreads), 0, s, q);                     \
   if (!e) e = launch_pdl(column_join<T>, dim3((unsigned)q.first[3]), dim3(kCols), 0, s, q)
   FCONV_OPS_TYPE(dtype, FCONV_M)
 #undef FCONV_M

@@ -262,6 +262,42 @@ __device__ __forceinline__ void as_floats(float (&x)[32], const uint32_t (&r)[32
   for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
 }
 
+// 32 values of h from g and u, two a word.
+template <int ACT>
+__device__ __forceinline__ void gate(uint32_t (&w)[16], const float (&g)[32], const float (&u)[32],
+                                     float alpha, bool bf16) {
+  float unused;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    w[i] = pack16(bf16, act_fast<ACT, false>(alpha, g[2 * i], unused) * u[2 * i],
+                  act_fast<ACT, false>(alpha, g[2 * i + 1], unused) * u[2 * i + 1]);
+}
+// 8 values of dg, du and h from those of dh, g and u.
+template <int ACT>
+__device__ __forceinline__ void gate_grad(uint32_t (&wg)[4], uint32_t (&wu)[4], uint32_t (&wh)[4],
+                                          const float* dh, const float4 (&g)[2],
+                                          const float4 (&u)[2], float alpha, bool bf16) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float gs[4] = {g[k].x, g[k].y, g[k].z, g[k].w}, us[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+    float dg[4], du[4], h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float slope;
+      const float a = act_fast<ACT, true>(alpha, gs[e], slope), d = dh[k * 4 + e];
+      dg[e] = d * us[e] * slope;
+      du[e] = d * a;
+      h[e] = a * us[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      wg[2 * k + e] = pack16(bf16, dg[2 * e], dg[2 * e + 1]);
+      wu[2 * k + e] = pack16(bf16, du[2 * e], du[2 * e + 1]);
+      wh[2 * k + e] = pack16(bf16, h[2 * e], h[2 * e + 1]);
+    }
+  }
+}
+
 template <int CG, bool AMN, bool BMN, int EPI>
 __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Job j) {
   constexpr int S = kStages<EPI>, BN = 128 * CG;
@@ -458,47 +494,31 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
             }
           }
           uint32_t w[16];
-          float unused;
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            w[i] = pack16(bf16, act_of<false>(act, alpha, g[2 * i], unused) * u[2 * i],
-                          act_of<false>(act, alpha, g[2 * i + 1], unused) * u[2 * i + 1]);
+#define FCONV_M(ACT) gate<ACT>(w, g, u, alpha, bf16)
+          FCONV_GATE_SWITCH(act, FCONV_M)
+#undef FCONV_M
           stage(slots + slot * kSlot, row, 0, w);
         } else {
           const float* from = saved + (int64_t)(col >> 2) * 256;
-#pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            uint32_t wg[4], wu[4], wh[4];
-            const bool there = grow < p.M && col + i < p.N;
-#pragma unroll
-            for (int k = 0; k < 8; k += 4) {
-              float4 g = make_float4(0, 0, 0, 0), u = g;
-              if (there) {
-                g = __ldcg(reinterpret_cast<const float4*>(from + (i + k) * 64));
-                u = __ldcg(reinterpret_cast<const float4*>(from + (i + k) * 64 + 128));
-              }
-              const float gs[4] = {g.x, g.y, g.z, g.w}, us[4] = {u.x, u.y, u.z, u.w};
-              float dg[4], du[4], h[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float dh = __uint_as_float(r0[i + k + e]);
-                float slope;
-                const float a = act_of<true>(act, alpha, gs[e], slope);
-                dg[e] = dh * us[e] * slope;
-                du[e] = dh * a;
-                h[e] = a * us[e];
-              }
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                wg[k / 2 + e] = pack16(bf16, dg[2 * e], dg[2 * e + 1]);
-                wu[k / 2 + e] = pack16(bf16, du[2 * e], du[2 * e + 1]);
-                wh[k / 2 + e] = pack16(bf16, h[2 * e], h[2 * e + 1]);
-              }
-            }
-            stage(slots, row, i / 2, wg);
-            stage(slots + kSlot, row, i / 2, wu);
-            stage(slots + 2 * kSlot, row, i / 2, wh);
-          }
+          float dh[32];
+          as_floats(dh, r0);
+#define FCONV_M(ACT)                                                                        \
+  _Pragma("unroll") for (int i = 0; i < 32; i += 8) {                                       \
+    uint32_t wg[4], wu[4], wh[4];                                                           \
+    float4 g[2] = {}, u[2] = {};                                                            \
+    if (grow < p.M && col + i < p.N) {                                                      \
+      _Pragma("unroll") for (int k = 0; k < 2; ++k) {                                       \
+        g[k] = __ldcg(reinterpret_cast<const float4*>(from + (i + 4 * k) * 64));            \
+        u[k] = __ldcg(reinterpret_cast<const float4*>(from + (i + 4 * k) * 64 + 128));      \
+      }                                                                                     \
+    }                                                                                       \
+    gate_grad<ACT>(wg, wu, wh, dh + i, g, u, alpha, bf16);                                  \
+    stage(slots, row, i / 2, wg);                                                           \
+    stage(slots + kSlot, row, i / 2, wu);                                                   \
+    stage(slots + 2 * kSlot, row, i / 2, wh);                                               \
+  }
+          FCONV_GATE_SWITCH(act, FCONV_M)
+#undef FCONV_M
         }
         ptx::fence_proxy_async_smem();
         ptx::bar_sync(1 + half, 128);
