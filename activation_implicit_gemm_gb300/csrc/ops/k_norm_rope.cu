@@ -8,8 +8,8 @@
 // G lanes (a power of two, so that sums over a head are shuffles) own a token: each lane has the
 // same VEC pairs of every head (two accesses of VEC elements, or one of 2 VEC where neighbours
 // pair up), makes their sines and cosines once and goes through its share of the heads with the
-// next one's values on their way. A block row (blockIdx.y) takes heads of q or of k only, so a
-// thread keeps one weight in registers. In the backward pass blocks stay for many tokens and keep
+// next one's values on their way. Blocks take heads of q or of k only, so a thread
+// keeps one weight in registers. In the backward pass blocks stay for many tokens and keep
 // their part of dw in registers; the parts are joined in a fixed order by a second kernel.
 #include "ops_common.cuh"
 #include "ops_internal.h"
@@ -30,7 +30,8 @@ struct Side {  // q or k
   void* out;  // y, or dx
   const void* w;
   void* dw;
-  int heads, per, groups;  // heads of a block row, block rows
+  int heads, per, groups;  // heads of a group, groups
+  int blocks;              // backward: of a group
   int64_t xs[3], ys[3], os[3];  // strides of x, dy and out
 };
 struct HeadGeom {
@@ -43,16 +44,19 @@ struct HeadGeom {
   float eps;
 };
 
-// Where a lane's chunk lies in a head and how its pairs turn.
-template <int VEC>
+template <typename T>
+constexpr bool kBf16 = false;
+template <>
+constexpr bool kBf16<__nv_bfloat16> = true;
+
+// Where a lane's chunk lies in a head.
 struct Chunk {
-  int lo, hi;       // first elements of its two accesses, hi < 0: no second one
+  int lo, hi;  // first elements of its two accesses, hi < 0: no second one
   bool turns;
-  float cs[VEC], sn[VEC];
 };
 
 template <int VEC, bool IL>
-__device__ __forceinline__ void place(Chunk<VEC>& c, const HeadGeom& g, int chunk) {
+__device__ __forceinline__ void place(Chunk& c, const HeadGeom& g, int chunk) {
   const int p0 = chunk * VEC;
   c.turns = chunk < g.pair_chunks;
   if (!c.turns) {
@@ -72,9 +76,10 @@ __device__ __forceinline__ void place(Chunk<VEC>& c, const HeadGeom& g, int chun
   }
 }
 
+// The sine and cosine of a chunk's pairs.
 template <int VEC>
-__device__ __forceinline__ void angles(Chunk<VEC>& c, const HeadGeom& g, int chunk, int64_t b,
-                                       int64_t t) {
+__device__ __forceinline__ void angles(float (&sn)[VEC], float (&cs)[VEC], const HeadGeom& g,
+                                       int chunk, int64_t b, int64_t t) {
   const int p0 = chunk * VEC;
   const int64_t at = ((g.pos_batch == 1 ? 0 : b) * g.len + t) * g.axes;
   float pos[3];
@@ -85,26 +90,28 @@ __device__ __forceinline__ void angles(Chunk<VEC>& c, const HeadGeom& g, int chu
     const int p = p0 + i;
     const float x = p < g.sec0 ? pos[0] : p < g.sec0 + g.sec1 ? pos[1] : pos[2];
     if (fabsf(x) <= kLongPosition) {
-      turn_of(x, g.inv_freq[p], c.sn[i], c.cs[i]);
+      turn_of(x, g.inv_freq[p], sn[i], cs[i]);
     } else {
       const int a = p < g.sec0 ? 0 : p < g.sec0 + g.sec1 ? 1 : 2;
       const float2 v = turn_of_long(long_position(g.pos, g.pos_type, at + a), g.inv_freq[p]);
-      c.sn[i] = v.x;
-      c.cs[i] = v.y;
+      sn[i] = v.x;
+      cs[i] = v.y;
     }
   }
 }
 
-// A chunk's 2 VEC elements of one head as they lie in memory. Element e of them is member e / VEC
-// of pair e % VEC, or with IL member e % 2 of pair e / 2.
+// A chunk's 2 VEC elements of one head, worked on as VEC packed pairs of f32: with both members
+// of a pair in one (kMembers: neighbours that turn with each other, or a chunk of one pair), else
+// VEC / 2 packed pairs of first members and as many of second ones.
 template <typename T, int VEC, bool IL>
 struct Raw {
+  static constexpr bool kMembers = IL || VEC == 1;
   Vec<T, IL ? 2 * VEC : VEC> a, b;
-  __device__ __forceinline__ void load(const T* p, const Chunk<VEC>& c) {
+  __device__ __forceinline__ void load(const T* p, const Chunk& c) {
     a = *reinterpret_cast<const decltype(a)*>(p + c.lo);
     if (!IL && c.hi >= 0) b = *reinterpret_cast<const decltype(b)*>(p + c.hi);
   }
-  __device__ __forceinline__ void store(T* p, const Chunk<VEC>& c) const {
+  __device__ __forceinline__ void store(T* p, const Chunk& c) const {
     *reinterpret_cast<decltype(a)*>(p + c.lo) = a;
     if (!IL && c.hi >= 0) *reinterpret_cast<decltype(b)*>(p + c.hi) = b;
   }
@@ -113,30 +120,50 @@ struct Raw {
     for (int i = 0; i < (IL ? 2 * VEC : VEC); ++i) a.v[i] = b.v[i] = from_f<T>(0.0f);
   }
   __device__ __forceinline__ T& at(int e) { return IL || e < VEC ? a.v[e] : b.v[e - VEC]; }
+  __device__ __forceinline__ uint64_t get(int i) {
+    if constexpr (sizeof(T) == 4) {
+      return pair((float)at(2 * i), (float)at(2 * i + 1));
+    } else if constexpr (VEC == 1) {
+      return pair(to_f(a.v[0]), to_f(b.v[0]));
+    } else if constexpr (kBf16<T>) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(&at(2 * i));
+      return pair(w << 16, w & 0xffff0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&at(2 * i)));
+      return pair(f.x, f.y);
+    }
+  }
+  __device__ __forceinline__ void set(int i, uint64_t v) {
+    if constexpr (sizeof(T) == 4) {
+      at(2 * i) = low(v);
+      at(2 * i + 1) = high(v);
+    } else if constexpr (VEC == 1) {
+      a.v[0] = from_f<T>(low(v));
+      b.v[0] = from_f<T>(high(v));
+    } else if constexpr (kBf16<T>) {
+      *reinterpret_cast<__nv_bfloat162*>(&at(2 * i)) = __floats2bfloat162_rn(low(v), high(v));
+    } else {
+      *reinterpret_cast<__half2*>(&at(2 * i)) = __floats2half2_rn(low(v), high(v));
+    }
+  }
 };
-// Positions of a pair's members among the 2 VEC elements.
-template <int VEC, bool IL>
-__device__ __forceinline__ constexpr int first(int i) { return IL ? 2 * i : i; }
-template <int VEC, bool IL>
-__device__ __forceinline__ constexpr int second(int i) { return IL ? 2 * i + 1 : VEC + i; }
+__device__ __forceinline__ uint64_t swapped(uint64_t v) { return pair(high(v), low(v)); }
 
 template <int VEC, bool IL>
-__device__ __forceinline__ int element(const Chunk<VEC>& c, int e) {  // -1: there is none
+__device__ __forceinline__ int element(const Chunk& c, int e) {  // -1: there is none
   if (IL || e < VEC) return c.lo + e;
   return c.hi < 0 ? -1 : c.hi + e - VEC;
 }
 
-template <int VEC, bool IL>
+// A chunk's weights in the order of its elements.
+template <typename T, int VEC, bool IL>
 __device__ __forceinline__ void load_weight(float (&w)[2 * VEC], const HeadGeom& g, const Side& s,
-                                            const Chunk<VEC>& c, int dtype_f32, bool f16) {
+                                            const Chunk& c) {
 #pragma unroll
   for (int e = 0; e < 2 * VEC; ++e) {
     const int at = element<VEC, IL>(c, e);
     w[e] = 1.0f;
-    if (s.w && at >= 0)
-      w[e] = dtype_f32 ? ((const float*)s.w)[at]
-             : f16     ? to_f(((const __half*)s.w)[at])
-                       : to_f(((const __nv_bfloat16*)s.w)[at]);
+    if (s.w && at >= 0) w[e] = g.f32_params ? ((const float*)s.w)[at] : to_f(((const T*)s.w)[at]);
   }
 }
 
@@ -145,16 +172,19 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
   return v;
 }
 
-template <typename T>
-constexpr bool kIsHalf = false;
-template <>
-constexpr bool kIsHalf<__half> = true;
+// Heads whose values are on their way while one is worked on: `bytes` of them a thread.
+template <typename T, int VEC, int R>
+__host__ __device__ constexpr int ahead(int bytes) {
+  const int each = 2 * VEC * R * (int)sizeof(T);
+  return R > 2 || each > bytes ? 1 : bytes / each;
+}
 
 // R: chunks of a lane (more than one only where a head has more than 32).
 template <typename T, int VEC, int R, bool IL>
-__global__ void __launch_bounds__(kThreads, VEC * R > 8 ? 1 : 3)
+__global__ void __launch_bounds__(kThreads, R > 2 ? 1 : R == 2 ? 2 : 3)
     norm_rope_forward(const __grid_constant__ HeadGeom g) {
   using Row = Raw<T, VEC, IL>;
+  constexpr int A = ahead<T, VEC, R>(64);
   ptx::pdl_wait();
   ptx::pdl_trigger();
   const bool is_k = (int)blockIdx.y >= g.side[0].groups;
@@ -168,143 +198,206 @@ __global__ void __launch_bounds__(kThreads, VEC * R > 8 ? 1 : 3)
   const int64_t b = token / g.len, t = token - b * g.len;
   const T* xp = (const T*)s.x + b * s.xs[0] + t * s.xs[1];
   T* yp = (T*)s.out + b * s.os[0] + t * s.os[1];
-  Chunk<VEC> c[R];
+  Chunk c[R];
   bool on[R];
-  Row row[R];
-  float w[R][2 * VEC];
+  Row row[A][R];
+  // The turn and the weights in one: y = r (x m + x' m'), x' the pairs' other members.
+  uint64_t m[R][VEC], mx[R][VEC];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     on[r] = here && lane + r * g.lanes < g.chunks;
-    row[r].zero();
+    if (on[r]) place<VEC, IL>(c[r], g, lane + r * g.lanes);
+#pragma unroll
+    for (int i = 0; i < A; ++i) {
+      row[i][r].zero();
+      if (on[r] && h0 + i < h1) row[i][r].load(xp + (h0 + i) * s.xs[2], c[r]);
+    }
     if (on[r]) {
-      place<VEC, IL>(c[r], g, lane + r * g.lanes);
-      row[r].load(xp + h0 * s.xs[2], c[r]);
-      if (c[r].turns) angles<VEC>(c[r], g, lane + r * g.lanes, b, t);
-      load_weight<VEC, IL>(w[r], g, s, c[r], g.f32_params, kIsHalf<T>);
-    }
-  }
-  for (int h = h0; h < h1; ++h) {
-    float x[R][2 * VEC], sum = 0.0f;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-#pragma unroll
-      for (int e = 0; e < 2 * VEC; ++e) {
-        x[r][e] = to_f(row[r].at(e));
-        sum = fmaf(x[r][e], x[r][e], sum);
-      }
-      if (on[r] && h + 1 < h1) row[r].load(xp + (h + 1) * s.xs[2], c[r]);
-    }
-    sum = lanes_sum(sum, g.lanes);
-    const float scale = rsqrtf(sum / (float)g.D + g.eps);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (!on[r]) continue;
-      Row y;
+      float sn[VEC], cs[VEC], w[2 * VEC];
+      load_weight<T, VEC, IL>(w, g, s, c[r]);
       if (c[r].turns) {
+        angles<VEC>(sn, cs, g, lane + r * g.lanes, b, t);
+      } else {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          constexpr auto F = first<VEC, IL>;
-          constexpr auto S = second<VEC, IL>;
-          const float u = x[r][F(i)] * scale * w[r][F(i)], v = x[r][S(i)] * scale * w[r][S(i)];
-          y.at(F(i)) = from_f<T>(u * c[r].cs[i] - v * c[r].sn[i]);
-          y.at(S(i)) = from_f<T>(v * c[r].cs[i] + u * c[r].sn[i]);
+        for (int k = 0; k < VEC; ++k) sn[k] = 0.0f, cs[k] = 1.0f;
+      }
+      if (Row::kMembers) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          m[r][k] = pair(w[2 * k] * cs[k], w[2 * k + 1] * cs[k]);
+          mx[r][k] = pair(-w[2 * k + 1] * sn[k], w[2 * k] * sn[k]);
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 2 * VEC; ++e) y.at(e) = from_f<T>(x[r][e] * scale * w[r][e]);
+        for (int k = 0; k < VEC / 2; ++k) {
+          const int e = 2 * k, f = VEC + 2 * k;
+          m[r][k] = pair(w[e] * cs[e], w[e + 1] * cs[e + 1]);
+          mx[r][k] = pair(-w[f] * sn[e], -w[f + 1] * sn[e + 1]);
+          m[r][VEC / 2 + k] = pair(w[f] * cs[e], w[f + 1] * cs[e + 1]);
+          mx[r][VEC / 2 + k] = pair(w[e] * sn[e], w[e + 1] * sn[e + 1]);
+        }
       }
-      y.store(yp + h * s.os[2], c[r]);
+    }
+  }
+  const float inv = 1.0f / (float)g.D;
+  const T* ahead_p = xp + (h0 + A) * s.xs[2];
+  yp += h0 * s.os[2];
+  for (int h = h0; h < h1; h += A) {
+#pragma unroll
+    for (int i = 0; i < A; ++i) {
+      if (h + i >= h1) break;
+      uint64_t x[R][VEC], sums = 0;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          x[r][k] = row[i][r].get(k);
+          sums = fma2(x[r][k], x[r][k], sums);
+        }
+        if (on[r] && h + i + A < h1) row[i][r].load(ahead_p, c[r]);
+      }
+      ahead_p += s.xs[2];
+      const float sum = lanes_sum(low(sums) + high(sums), g.lanes);
+      const float scale = rsqrtf(fmaf(sum, inv, g.eps));
+      const uint64_t both = pair(scale, scale);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (!on[r]) continue;
+        Row out;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          uint64_t y = mul2(x[r][k], m[r][k]);
+          if (c[r].turns) {
+            const uint64_t other = Row::kMembers ? swapped(x[r][k])
+                                                 : x[r][k < VEC / 2 ? k + VEC / 2 : k - VEC / 2];
+            y = fma2(other, mx[r][k], y);
+          }
+          out.set(k, mul2(y, both));
+        }
+        out.store(yp, c[r]);
+      }
+      yp += s.os[2];
     }
   }
 }
 
 template <typename T, int VEC, int R, bool IL>
-__global__ void __launch_bounds__(kThreads, VEC * R > 8 ? 1 : 2)
+__global__ void __launch_bounds__(kThreads, R > 2 ? 1 : 2)
     norm_rope_backward(const __grid_constant__ HeadGeom g) {
   using Row = Raw<T, VEC, IL>;
+  constexpr int A = ahead<T, VEC, R>(32);
   extern __shared__ float sums[];  // a row of D for each warp
   ptx::pdl_wait();
   ptx::pdl_trigger();
-  const bool is_k = (int)blockIdx.y >= g.side[0].groups;
+  const int of_q = g.side[0].groups * g.side[0].blocks;
+  const bool is_k = (int)blockIdx.x >= of_q;
   const Side& s = g.side[is_k];
-  const int h0 = ((int)blockIdx.y - (is_k ? g.side[0].groups : 0)) * s.per;
+  const int block = (int)blockIdx.x - (is_k ? of_q : 0);
+  const int h0 = block / s.blocks * s.per;
   const int h1 = min(h0 + s.per, s.heads);
   const int lane = threadIdx.x & (g.lanes - 1);
   const int64_t each = kThreads / g.lanes;  // tokens of a block at a time
-  Chunk<VEC> c[R];
-  float w[R][2 * VEC], dw[R][2 * VEC];
+  const float inv = 1.0f / (float)g.D;
+  Chunk c[R];
+  uint64_t w[R][VEC], dw[R][VEC];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-#pragma unroll
-    for (int e = 0; e < 2 * VEC; ++e) dw[r][e] = 0.0f;
     if (lane + r * g.lanes < g.chunks) {
+      float v[2 * VEC];
       place<VEC, IL>(c[r], g, lane + r * g.lanes);
-      load_weight<VEC, IL>(w[r], g, s, c[r], g.f32_params, kIsHalf<T>);
+      load_weight<T, VEC, IL>(v, g, s, c[r]);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) w[r][k] = pair(v[2 * k], v[2 * k + 1]);
     }
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) dw[r][k] = 0;
   }
-  for (int64_t t0 = blockIdx.x * each; t0 < g.tokens; t0 += gridDim.x * each) {
+  for (int64_t t0 = block % s.blocks * each; t0 < g.tokens; t0 += s.blocks * each) {
     int64_t token = t0 + threadIdx.x / g.lanes;
     const bool here = token < g.tokens;
     if (!here) token = 0;
     const int64_t b = token / g.len, t = token - b * g.len;
-    const T* xp = (const T*)s.x + b * s.xs[0] + t * s.xs[1];
-    const T* yp = (const T*)s.dy + b * s.ys[0] + t * s.ys[1];
-    T* op = (T*)s.out + b * s.os[0] + t * s.os[1];
+    const T* xp = (const T*)s.x + b * s.xs[0] + t * s.xs[1] + h0 * s.xs[2];
+    const T* yp = (const T*)s.dy + b * s.ys[0] + t * s.ys[1] + h0 * s.ys[2];
+    T* op = (T*)s.out + b * s.os[0] + t * s.os[1] + h0 * s.os[2];
     bool on[R];
-    Row rx[R], ry[R];
+    Row rx[A][R], ry[A][R];
+    float sn[R][VEC], cs[R][VEC];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       on[r] = here && lane + r * g.lanes < g.chunks;
-      rx[r].zero();
-      ry[r].zero();
-      if (on[r]) {
-        rx[r].load(xp + h0 * s.xs[2], c[r]);
-        ry[r].load(yp + h0 * s.ys[2], c[r]);
-        if (c[r].turns) angles<VEC>(c[r], g, lane + r * g.lanes, b, t);
+#pragma unroll
+      for (int i = 0; i < A; ++i) {
+        rx[i][r].zero();
+        ry[i][r].zero();
+        if (on[r] && h0 + i < h1) {
+          rx[i][r].load(xp + i * s.xs[2], c[r]);
+          ry[i][r].load(yp + i * s.ys[2], c[r]);
+        }
       }
+      if (on[r] && c[r].turns) angles<VEC>(sn[r], cs[r], g, lane + r * g.lanes, b, t);
     }
-    for (int h = h0; h < h1; ++h) {
-      float x[R][2 * VEC], a[R][2 * VEC], sum = 0.0f, dot = 0.0f;
+    xp += A * s.xs[2];
+    yp += A * s.ys[2];
+    for (int h = h0; h < h1; h += A) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
+      for (int i = 0; i < A; ++i) {
+        if (h + i >= h1) break;
+        uint64_t x[R][VEC], g2[R][VEC], squares = 0, dots = 0;
 #pragma unroll
-        for (int e = 0; e < 2 * VEC; ++e) {
-          x[r][e] = to_f(rx[r].at(e));
-          a[r][e] = to_f(ry[r].at(e));
-          sum = fmaf(x[r][e], x[r][e], sum);
-        }
-        if (!on[r]) continue;
-        if (h + 1 < h1) {
-          rx[r].load(xp + (h + 1) * s.xs[2], c[r]);
-          ry[r].load(yp + (h + 1) * s.ys[2], c[r]);
-        }
-        if (c[r].turns) {
+        for (int r = 0; r < R; ++r) {
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            constexpr auto F = first<VEC, IL>;
-            constexpr auto S = second<VEC, IL>;
-            const float u = a[r][F(i)], v = a[r][S(i)];
-            a[r][F(i)] = u * c[r].cs[i] + v * c[r].sn[i];
-            a[r][S(i)] = v * c[r].cs[i] - u * c[r].sn[i];
+          for (int k = 0; k < VEC; ++k) {
+            x[r][k] = rx[i][r].get(k);
+            g2[r][k] = ry[i][r].get(k);
+            squares = fma2(x[r][k], x[r][k], squares);
           }
+          if (!on[r]) continue;
+          if (h + i + A < h1) {
+            rx[i][r].load(xp, c[r]);
+            ry[i][r].load(yp, c[r]);
+          }
+          if (c[r].turns) {  // back
+            if (Row::kMembers) {
+#pragma unroll
+              for (int k = 0; k < VEC; ++k)
+                g2[r][k] = fma2(swapped(g2[r][k]), pair(sn[r][k], -sn[r][k]),
+                                mul2(g2[r][k], pair(cs[r][k], cs[r][k])));
+            } else {
+#pragma unroll
+              for (int k = 0; k < VEC / 2; ++k) {
+                const uint64_t cc = pair(cs[r][2 * k], cs[r][2 * k + 1]);
+                const uint64_t ss = pair(sn[r][2 * k], sn[r][2 * k + 1]);
+                const uint64_t u = g2[r][k], v = g2[r][VEC / 2 + k];
+                g2[r][k] = fma2(v, ss, mul2(u, cc));
+                const uint64_t vc = mul2(v, cc);
+                g2[r][VEC / 2 + k] = pair(fmaf(-low(u), sn[r][2 * k], low(vc)),
+                                          fmaf(-high(u), sn[r][2 * k + 1], high(vc)));
+              }
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) dots = fma2(mul2(g2[r][k], w[r][k]), x[r][k], dots);
         }
+        xp += s.xs[2];
+        yp += s.ys[2];
+        const float sum = lanes_sum(low(squares) + high(squares), g.lanes);
+        const float dot = lanes_sum(low(dots) + high(dots), g.lanes);
+        const float scale = rsqrtf(fmaf(sum, inv, g.eps));
+        const float along = -(dot * inv) * scale * scale;
+        const uint64_t scales = pair(scale, scale), alongs = pair(along, along);
 #pragma unroll
-        for (int e = 0; e < 2 * VEC; ++e) dot = fmaf(a[r][e] * w[r][e], x[r][e], dot);
-      }
-      sum = lanes_sum(sum, g.lanes);
-      dot = lanes_sum(dot, g.lanes);
-      const float scale = rsqrtf(sum / (float)g.D + g.eps);
-      const float along = dot / (float)g.D * scale * scale;
+        for (int r = 0; r < R; ++r) {
+          if (!on[r]) continue;
+          Row out;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (!on[r]) continue;
-        Row o;
-#pragma unroll
-        for (int e = 0; e < 2 * VEC; ++e) {
-          dw[r][e] = fmaf(a[r][e], x[r][e] * scale, dw[r][e]);
-          o.at(e) = from_f<T>(scale * (a[r][e] * w[r][e] - x[r][e] * along));
+          for (int k = 0; k < VEC; ++k) {
+            dw[r][k] = fma2(g2[r][k], mul2(x[r][k], scales), dw[r][k]);
+            out.set(k, mul2(fma2(x[r][k], alongs, mul2(g2[r][k], w[r][k])), scales));
+          }
+          out.store(op, c[r]);
         }
-        o.store(op + h * s.os[2], c[r]);
+        op += s.os[2];
       }
     }
   }
@@ -313,19 +406,17 @@ __global__ void __launch_bounds__(kThreads, VEC * R > 8 ? 1 : 2)
 #pragma unroll
   for (int r = 0; r < R; ++r) {
 #pragma unroll
-    for (int e = 0; e < 2 * VEC; ++e)
-      for (int o = g.lanes; o < 32; o <<= 1)
-        dw[r][e] += __shfl_xor_sync(0xffffffffu, dw[r][e], o);
-    if ((threadIdx.x & 31) < g.lanes && lane + r * g.lanes < g.chunks) {
-#pragma unroll
-      for (int e = 0; e < 2 * VEC; ++e) {
+    for (int e = 0; e < 2 * VEC; ++e) {
+      float v = e & 1 ? high(dw[r][e / 2]) : low(dw[r][e / 2]);
+      for (int o = g.lanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if ((threadIdx.x & 31) < g.lanes && lane + r * g.lanes < g.chunks) {
         const int at = element<VEC, IL>(c[r], e);
-        if (at >= 0) sums[(threadIdx.x >> 5) * g.D + at] = dw[r][e];
+        if (at >= 0) sums[(threadIdx.x >> 5) * g.D + at] = v;
       }
     }
   }
   __syncthreads();
-  float* part = g.part + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * g.D;
+  float* part = g.part + (int64_t)blockIdx.x * g.D;
   for (int e = threadIdx.x; e < g.D; e += kThreads) {
     float v = 0.0f;
     for (int i = 0; i < kThreads / 32; ++i) v += sums[i * g.D + e];
@@ -336,15 +427,15 @@ __global__ void __launch_bounds__(kThreads, VEC * R > 8 ? 1 : 2)
 // dw of q (blockIdx.y 0) or k: the parts of their blocks, 32 columns a block, in a fixed order.
 template <typename T>
 __global__ void __launch_bounds__(1024)
-    norm_rope_join(const __grid_constant__ HeadGeom g, int grid_x) {
+    norm_rope_join(const __grid_constant__ HeadGeom g) {
   __shared__ float sums[32][33];
   ptx::pdl_wait();
   ptx::pdl_trigger();
   const Side& s = g.side[blockIdx.y];
   if (!s.dw) return;
   const int col = blockIdx.x * 32 + (threadIdx.x & 31), row = threadIdx.x >> 5;
-  const int64_t begin = blockIdx.y ? (int64_t)g.side[0].groups * grid_x : 0;
-  const int64_t n = (int64_t)s.groups * grid_x;
+  const int64_t begin = blockIdx.y ? (int64_t)g.side[0].groups * g.side[0].blocks : 0;
+  const int64_t n = (int64_t)s.groups * s.blocks;
   float v = 0.0f;
   if (col < g.D)
     for (int64_t i = row; i < n; i += 32) v += __ldcg(g.part + (begin + i) * g.D + col);
@@ -387,7 +478,8 @@ struct Shape {
   bool il;
 };
 
-// The variants: accesses of 16 bytes, of 8 (16-bit rows that allow no more), and of one element.
+// The variants: accesses of 16 bytes, of 8 (16-bit rows that allow no more), of one element, and
+// more chunks a lane for heads that 32 lanes do not hold.
 template <typename T, typename Run>
 int by_shape(const Shape& v, Run run) {
   constexpr int kFull = 16 / sizeof(T);
@@ -420,18 +512,15 @@ struct RunBackward {
   }
 };
 
-// Heads of a block row, at most `most` and as even as they go.
+// Groups of heads, at most `most` in each and as even as they go.
 void share(Side& s, int most) {
   s.groups = s.heads ? (s.heads + most - 1) / most : 0;
   s.per = s.heads ? (s.heads + s.groups - 1) / s.groups : 0;
   s.groups = s.heads ? (s.heads + s.per - 1) / s.per : 0;
 }
 
-constexpr int kMostHeads = 8;  // of a block row in the backward pass
-int backward_rows(const fconv_norm_rope_desc& d) {
-  return (int)(d.heads_q + d.heads_k);  // at most
-}
-int backward_blocks(int sms) { return 4 * sms; }
+// Blocks of the backward pass: two an SM, shared out by the heads of a group, one a group at least.
+int backward_blocks(int sms) { return 2 * sms; }
 
 HeadGeom geometry(const fconv_norm_rope_desc& d, const NormRopeArgs& a, bool backward, Shape& v) {
   HeadGeom g{};
@@ -469,15 +558,13 @@ HeadGeom geometry(const fconv_norm_rope_desc& d, const NormRopeArgs& a, bool bac
   g.pos_type = d.pos_type;
   g.f32_params = d.param_dtype == FCONV_F32;
   g.eps = d.eps;
+  // il: 16 bytes hold whole pairs of neighbours
   const int n = width(d, a, g.pairs, backward), full = d.dtype == FCONV_F32 ? 4 : 8;
-  v.il = d.pairing == FCONV_ROPE_INTERLEAVED && g.pairs > 0 && n == full;
-  v.vec = v.il ? full / 2 : d.pairing == FCONV_ROPE_INTERLEAVED && g.pairs > 0 ? 1 : n;
-  if (v.vec != full && v.vec != 4 && !v.il) v.vec = 1;
-  auto count = [&](int vec) {
-    g.pair_chunks = g.pairs / vec;
-    g.chunks = g.pair_chunks + (g.D - 2 * g.pairs + 2 * vec - 1) / (2 * vec);
-  };
-  count(v.vec);
+  const bool neighbours = d.pairing == FCONV_ROPE_INTERLEAVED && g.pairs > 0;
+  v.il = neighbours && n == full;
+  v.vec = v.il ? full / 2 : neighbours || n < 4 ? 1 : n;
+  g.pair_chunks = g.pairs / v.vec;
+  g.chunks = g.pair_chunks + (g.D - 2 * g.pairs + 2 * v.vec - 1) / (2 * v.vec);
   g.lanes = 1;
   while (g.lanes < g.chunks && g.lanes < 32) g.lanes *= 2;
   v.r = (g.chunks + g.lanes - 1) / g.lanes;
@@ -487,7 +574,9 @@ HeadGeom geometry(const fconv_norm_rope_desc& d, const NormRopeArgs& a, bool bac
 }  // namespace
 
 size_t norm_rope_workspace(const fconv_norm_rope_desc& d, int sms) {
-  return (size_t)(backward_blocks(sms) + backward_rows(d)) * (size_t)d.head_dim * sizeof(float);
+  // groups * per stays under twice the heads, and a group has one block at least
+  const size_t most = 2 * (size_t)backward_blocks(sms) + (size_t)(d.heads_q + d.heads_k);
+  return most * (size_t)d.head_dim * sizeof(float);
 }
 
 int launch_norm_rope_forward(const fconv_norm_rope_desc& d, int sms, const NormRopeArgs& a,
@@ -516,29 +605,36 @@ int launch_norm_rope_backward(const fconv_norm_rope_desc& d, int sms, const Norm
   HeadGeom g = geometry(d, a, true, v);
   const int each = kThreads / g.lanes;
   const long long all = (g.tokens + each - 1) / each;  // blocks with one round of tokens
-  const int most = backward_blocks(sms);
-  int per = kMostHeads;  // fewer where the tokens alone do not fill the GPU
-  for (;;) {
+  const long long most = backward_blocks(sms);
+  int per = g.side[0].heads;  // fewer where the tokens alone do not fill the GPU
+  if (per < g.side[1].heads) per = g.side[1].heads;
+  for (;; per = (per + 1) / 2) {
     share(g.side[0], per);
     share(g.side[1], per);
     if (per == 1 || all * (g.side[0].groups + g.side[1].groups) >= most) break;
-    per /= 2;
   }
-  const int rows = g.side[0].groups + g.side[1].groups;
-  long long bx = most / rows;  // at most what the workspace holds
-  if (bx < 1) bx = 1;
-  if (bx > all) bx = all;
+  const int heads = g.side[0].heads + g.side[1].heads;
+  long long total = 0;
+  for (Side& side : g.side) {
+    long long n = most * side.per / heads;
+    if (n > all) n = all;
+    if (n < 1) n = 1;
+    side.blocks = (int)n;
+    total += n * side.groups;
+  }
   int e = 0;
-  if (bx > 0) {
-    v.grid = dim3((unsigned)bx, (unsigned)rows);
+  if (all > 0) {
+    v.grid = dim3((unsigned)total);
     const RunBackward run{g, v, s};
 #define FCONV_M(T) e = by_shape<T>(v, run)
     FCONV_OPS_TYPE(d.dtype, FCONV_M)
 #undef FCONV_M
+  } else {
+    g.side[0].groups = g.side[1].groups = 0;  // no parts: zero
   }
   if (e || (!a.dw && !a.dkw)) return e;
   const dim3 grid((unsigned)((g.D + 31) / 32), 2);
-#define FCONV_M(T) return launch_pdl(norm_rope_join<T>, grid, dim3(1024), 0, s, g, (int)bx)
+#define FCONV_M(T) return launch_pdl(norm_rope_join<T>, grid, dim3(1024), 0, s, g)
   FCONV_OPS_TYPE(d.dtype, FCONV_M)
 #undef FCONV_M
 }
