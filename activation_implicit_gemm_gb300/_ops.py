@@ -245,7 +245,7 @@ def _new(like):
     but keeps the strides of what is not contiguous)."""
     if like.is_contiguous():
         return torch.empty_like(like)
-    return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
 def _ptr(t):
@@ -561,13 +561,27 @@ def _form(t):
 
 
 def _norm_rope_plan(who, q, k, weight, k_weight, positions, inv_freq, sections, pairing, eps,
-                    device, outs, grads=None):
+                    device, outs, grads=None, given=True):
     """The cached plan of a call. outs: y of q and k, or in the backward pass their gradients;
-    grads: the results of the backward pass. Everything the checks look at is in the key."""
+    grads: the results of the backward pass. Everything the checks look at is in the key, but the
+    results where the call made them itself (not `given`): they follow from the inputs."""
     sections = None if sections is None else tuple(sections)
-    key = (q.dtype, q.shape, q.stride(), _form(k), _form(weight), _form(k_weight),
-           _form(positions), _form(inv_freq), sections, pairing, eps, device, _form(outs[0]),
-           _form(outs[1]), None if grads is None else (_form(grads[0]), _form(grads[1])))
+    key = (q.dtype, q.shape, q.stride(), sections, pairing, eps, device)
+    if k is not None:
+        key += (k.dtype, k.shape, k.stride())
+    for t in (weight, k_weight):
+        key += (None,) if t is None else (t.dtype, t.shape, t.is_contiguous())
+    if positions is not None and inv_freq is not None:
+        key += (positions.dtype, positions.shape, positions.is_contiguous(), inv_freq.dtype,
+                inv_freq.shape, inv_freq.is_contiguous())
+    else:
+        key += (positions is None, inv_freq is None)
+    if grads is not None:
+        key += ("grads", _form(outs[0]), _form(outs[1]))
+        if given:
+            key += (_form(grads[0]), _form(grads[1]))
+    elif given:
+        key += (_form(outs[0]), _form(outs[1]))
     p = _norm_rope_plans.get(key)
     if p is not None:
         return p
@@ -630,12 +644,13 @@ def norm_rope(q, k=None, *, weight=None, k_weight=None, positions=None, inv_freq
                              out=out, k_out=k_out)
     device = q.get_device()
     _on_cuda("norm_rope", device, k, weight, k_weight, positions, inv_freq, out, k_out)
+    given = out is not None or k_out is not None
     if out is None:
         out = _new(q)
     if k is not None and k_out is None:
         k_out = _new(k)
     p = _norm_rope_plan("norm_rope", q, k, weight, k_weight, positions, inv_freq, sections,
-                        pairing, eps, device, (out, k_out))
+                        pairing, eps, device, (out, k_out), given=given)
     _run(device, p.forward_ptrs, q.data_ptr(), _ptr(k), _ptr(weight), _ptr(k_weight),
          _ptr(positions), _ptr(inv_freq), out.data_ptr(), _ptr(k_out), _current_stream(device))
     return out if k is None else (out, k_out)
@@ -660,11 +675,12 @@ def norm_rope_backward(dout, q, dk_out=None, k=None, *, weight=None, k_weight=No
     device = q.get_device()
     _on_cuda("norm_rope_backward", device, dout, dk_out, k, weight, k_weight, positions, inv_freq,
              dq, dk)
+    given = dq is not None or dk is not None
     dq = _new(q) if dq is None else dq
     if k is not None and dk is None:
         dk = _new(k)
     p = _norm_rope_plan("norm_rope_backward", q, k, weight, k_weight, positions, inv_freq,
-                        sections, pairing, eps, device, (dout, dk_out), (dq, dk))
+                        sections, pairing, eps, device, (dout, dk_out), (dq, dk), given)
     dw = torch.empty_like(weight) if weight is not None and param_grads else None
     dkw = torch.empty_like(k_weight) if k_weight is not None and param_grads else None
     n = p.workspace_bytes if dw is not None or dkw is not None else 0
@@ -743,15 +759,22 @@ def _gate(who, activation, params):
     return GATES[activation], float(params[0]) if params else 1.702
 
 
-def _mlp_plan(who, x, weights, biases, activation, params, route, device, y, grads=None):
-    """The cached plan of a call. grads: (dy, dx) of a backward pass (y is dy then)."""
-    key = (_form(x), *map(_form, weights), *map(_form, biases), activation,
-           None if params is None else tuple(params), route, device, _form(y),
-           None if grads is None else _form(grads))
+def _mlp_plan(who, x, weights, biases, activation, params, route, device, y, dx=None, given=True):
+    """The cached plan of a call. With dx it is a backward pass's, whose dy is y. Everything the
+    checks look at is in the key, but a result that the call made itself (not `given`)."""
+    wg, wu, wd = weights
+    key = (x.dtype, x.shape, x.stride(), wg.dtype, wg.shape, wg.stride(), wu.dtype, wu.shape,
+           wu.stride(), wd.dtype, wd.shape, wd.stride(), activation,
+           None if params is None else tuple(params), route, device)
+    for b in biases:
+        key += (None,) if b is None else (b.dtype, b.shape, b.is_contiguous())
+    if dx is not None:
+        key += ("grads", _form(y), _form(dx) if given else None)
+    elif given:
+        key += (_form(y),)
     p = _mlp_plans.get(key)
     if p is not None:
         return p
-    wg, wu, wd = weights
     for name, w in (("w_gate", wg), ("w_up", wu), ("w_down", wd)):
         if w.dim() != 2 or w.dtype != x.dtype:
             raise ValueError(f"{who}: {name} must be a matrix of x's type")
@@ -767,23 +790,23 @@ def _mlp_plan(who, x, weights, biases, activation, params, route, device, y, gra
     if y.shape != x.shape[:-1] + wd.shape[:1] or y.dtype != x.dtype:
         raise ValueError(f"{who}: the output and its gradient are "
                          f"{tuple(x.shape[:-1] + wd.shape[:1])} of x's type")
-    if grads is not None and (grads.shape != x.shape or grads.dtype != x.dtype):
+    if dx is not None and (dx.shape != x.shape or dx.dtype != x.dtype):
         raise ValueError(f"{who}: dx must be like x")
     code, alpha = _gate(who, activation, params)
     if route not in ATTN_ROUTES:
         raise ValueError(f"{who}: route must be one of {list(ATTN_ROUTES)}")
-    out_row = _row_stride(who, "y" if grads is None else "dy", y)
+    out_row = _row_stride(who, "y" if dx is None else "dy", y)
     p = MlpPlan(_code(x.dtype), math.prod(x.shape[:-1]), features, hidden, wd.shape[0],
                 x_stride=_row_stride(who, "x", x),
-                y_stride=out_row if grads is None else wd.shape[0],
+                y_stride=out_row if dx is None else wd.shape[0],
                 gate_stride=_row_stride(who, "w_gate", wg),
                 up_stride=_row_stride(who, "w_up", wu),
                 down_stride=_row_stride(who, "w_down", wd),
-                dy_stride=0 if grads is None else out_row,
-                dx_stride=0 if grads is None else _row_stride(who, "dx", grads),
+                dy_stride=0 if dx is None else out_row,
+                dx_stride=0 if dx is None else _row_stride(who, "dx", dx),
                 has_b_gate=biases[0] is not None, has_b_up=biases[1] is not None,
                 has_b_down=biases[2] is not None, activation=code, alpha=alpha,
-                training=grads is not None, route=route, device=device)
+                training=dx is not None, route=route, device=device)
     return _keep(_mlp_plans, key, p)
 
 
@@ -805,10 +828,14 @@ def gated_mlp(x, w_gate, w_up, w_down, *, b_gate=None, b_up=None, b_down=None,
                              return_saved=return_saved, route=route)
     device = x.get_device()
     _on_cuda("gated_mlp", device, w_gate, w_up, w_down, b_gate, b_up, b_down, out)
+    given = out is not None
     if out is None:
-        out = torch.empty(x.shape[:-1] + w_down.shape[:1], dtype=x.dtype, device=x.device)
+        if w_down.shape[0] == x.shape[-1]:
+            out = _new(x)
+        else:
+            out = torch.empty(x.shape[:-1] + w_down.shape[:1], dtype=x.dtype, device=x.device)
     p = _mlp_plan("gated_mlp", x, (w_gate, w_up, w_down), (b_gate, b_up, b_down), activation,
-                  activation_params, route, device, out)
+                  activation_params, route, device, out, given=given)
     saved = None
     if return_saved:
         saved = torch.empty(p.saved_bytes // 4, dtype=torch.float32, device=x.device)
@@ -838,10 +865,11 @@ def gated_mlp_backward(dy, x, w_gate, w_up, w_down, saved=None, *, b_gate=None, 
     device = x.get_device()
     _on_cuda("gated_mlp_backward", device, dy, w_gate, w_up, w_down, saved, b_gate, b_up, b_down,
              dx)
+    given = dx is not None
     dx = _new(x) if dx is None else dx
     weights, biases = (w_gate, w_up, w_down), (b_gate, b_up, b_down)
     p = _mlp_plan("gated_mlp_backward", x, weights, biases, activation, activation_params, route,
-                  device, dy, dx)
+                  device, dy, dx, given)
     n = p.backward_workspace
     if saved is not None:
         if (saved.dtype != torch.float32 or saved.dim() != 1 or not saved.is_contiguous()

@@ -690,6 +690,13 @@ bool pairs_fill(int64_t M, int64_t N, int sms) {
   return ((M + 255) / 256) * ((N + 255) / 256) * 4 >= sms;
 }
 
+// g, u and h.
+int projections(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s) {
+  if (d.tokens <= kMlpFewTokens) return launch_mlp_few_gated(d, a, s);
+  return pairs_fill(d.tokens, 2 * d.hidden, sms) ? gated<2>(d, sms, a, a.h, s)
+                                                 : gated<1>(d, sms, a, a.h, s);
+}
+
 }  // namespace
 
 bool mlp_tc_supported(const fconv_mlp_desc& d) {
@@ -707,17 +714,15 @@ bool mlp_tc_supported(const fconv_mlp_desc& d) {
 }
 
 int launch_mlp_tc_forward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s) {
-  int e = pairs_fill(d.tokens, 2 * d.hidden, sms) ? gated<2>(d, sms, a, a.h, s)
-                                                  : gated<1>(d, sms, a, a.h, s);
-  if (e) return e;
+  if (const int e = projections(d, sms, a, s)) return e;
+  if (d.tokens <= kMlpFewTokens) return launch_mlp_few_down(d, a, s);
   return pairs_fill(d.tokens, d.out_features, sms) ? down<2>(d, sms, a, s) : down<1>(d, sms, a, s);
 }
 
 int launch_mlp_tc_backward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s) {
-  int e = 0;
   const int64_t T = d.tokens;
-  if (a.remake)  // h is written here too and again by the next kernel
-    e = pairs_fill(T, 2 * d.hidden, sms) ? gated<2>(d, sms, a, a.h, s) : gated<1>(d, sms, a, a.h, s);
+  // made again, the projections are the forward pass's bit by bit (h, too, is written again)
+  int e = a.remake ? projections(d, sms, a, s) : 0;
   if (!e)
     e = pairs_fill(T, d.hidden, sms) ? grads_of_projections<2>(d, sms, a, s)
                                      : grads_of_projections<1>(d, sms, a, s);
@@ -725,8 +730,9 @@ int launch_mlp_tc_backward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, c
     e = pairs_fill(T, d.features, sms) ? grad_of_input<2>(d, sms, a, s)
                                        : grad_of_input<1>(d, sms, a, s);
   if (!e && (a.dw_gate || a.dw_up || a.dw_down))
-    e = pairs_fill(2 * d.hidden + d.out_features, d.features, sms) ? grads_of_weights<2>(d, sms, a, s)
-                                                                   : grads_of_weights<1>(d, sms, a, s);
+    e = pairs_fill(2 * d.hidden + d.out_features, d.features, sms)
+            ? grads_of_weights<2>(d, sms, a, s)
+            : grads_of_weights<1>(d, sms, a, s);
   return e;
 }
 

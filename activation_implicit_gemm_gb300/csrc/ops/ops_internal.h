@@ -90,6 +90,10 @@ int launch_mlp_simple_backward(const fconv_mlp_desc& d, const MlpArgs& a, cudaSt
 bool mlp_tc_supported(const fconv_mlp_desc& d);
 int launch_mlp_tc_forward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s);
 int launch_mlp_tc_backward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s);
+// Up to kMlpFewTokens tokens of what the tensor-core route takes (k_mlp_few.cu).
+constexpr int kMlpFewTokens = 32;
+int launch_mlp_few_gated(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s);
+int launch_mlp_few_down(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s);
 int read_and_clear_mlp_error(cudaStream_t s, unsigned* value);
 
 // Column sums of up to three matrices with the same rows (those without `out` are left out).
