@@ -22,7 +22,8 @@ SOURCES = ["fconv_api.cpp", "k_direct.cu", "k_depthwise.cu", "k_grouped.cu", "k_
            "ops/ops_api.cpp", "ops/k_norm.cu", "ops/k_rope.cu", "ops/k_attn_mma.cu",
            "ops/k_attn_mma_wide.cu", "ops/k_attn_tc_fwd.cu", "ops/k_attn_tc_bwd.cu",
            "ops/block_api.cpp", "ops/k_norm_rope.cu", "ops/k_mlp_mma.cu", "ops/k_mlp_sums.cu",
-           "ops/k_mlp_tc.cu", "ops/k_mlp_few.cu"]
+           "ops/k_mlp_tc.cu", "ops/k_mlp_few.cu",
+           "ops/k_mlp_prep.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -18,10 +18,8 @@ struct fconv_mlp_plan {
   fconv_mlp_desc d;
   int sms;
   int want;
-  bool tc;               // tensor cores for calls with aligned addresses
-  size_t saved, matrix;  // bytes of g and u, and of a (tokens, hidden) operand
-  size_t sums;           // of the bias gradients
-  size_t fwd_ws, bwd_ws;
+  size_t saved;           // bytes of g and u
+  size_t fwd_ws, bwd_ws;  // bwd_ws without room for g and u
 };
 
 namespace {
@@ -64,7 +62,7 @@ fconv_status check_norm_rope(const fconv_norm_rope_desc& d) {
 fconv_status norm_rope_inputs(const fconv_norm_rope_desc& d, const void* q, const void* k,
                               const void* w, const void* kw, const void* positions,
                               const float* inv_freq) {
-  if (d.batch * d.len && (!q || (d.heads_k && !k) || (d.axes && (!positions || !inv_freq))))
+  if (d.batch * d.len > 0 && (!q || (d.heads_k && !k) || (d.axes && (!positions || !inv_freq))))
     return FCONV_E_NULL;
   if ((d.has_weight && !w) || (d.has_k_weight && !kw)) return FCONV_E_NULL;
   if ((!d.has_weight && w) || (!d.has_k_weight && kw)) return FCONV_E_BIAS_SHAPE;
@@ -103,6 +101,14 @@ fconv_status check_mlp(const fconv_mlp_desc& d) {
 }
 
 size_t whole(size_t bytes) { return (bytes + 255) / 256 * 256; }
+
+// The larger one of what the routes of a plan need.
+size_t mlp_workspace(const fconv_mlp_plan& p, bool backward) {
+  const size_t simple = mlp_simple_workspace(p.d, backward, p.sms);
+  const size_t tc =
+      p.want == FCONV_MLP_SIMPLE ? 0 : mlp_tc_workspace(p.d, backward, p.sms);
+  return whole(simple > tc ? simple : tc);
+}
 
 fconv_status mlp_inputs(const fconv_mlp_desc& d, const void* x, const void* w_gate,
                         const void* w_up, const void* w_down, const void* b_gate,
@@ -180,7 +186,7 @@ fconv_status fconv_norm_rope_backward(const fconv_norm_rope_plan* p, const void*
   if (!d.training) return FCONV_E_UNSUPPORTED;
   const fconv_status st = norm_rope_inputs(d, q, k, weight, k_weight, positions, inv_freq);
   if (st != FCONV_OK) return st;
-  if (d.batch * d.len && (!dq_out || !dq || (d.heads_k && (!dk_out || !dk)))) return FCONV_E_NULL;
+  if (d.batch * d.len > 0 && (!dq_out || !dq || (d.heads_k && (!dk_out || !dk)))) return FCONV_E_NULL;
   if (!d.heads_k && (dk_out || dk)) return FCONV_E_EXTENT;
   if ((!d.has_weight && dweight) || (!d.has_k_weight && dk_weight)) return FCONV_E_BIAS_SHAPE;
   const size_t e = type_size(d.dtype), pe = type_size(d.param_dtype);
@@ -230,28 +236,21 @@ fconv_status fconv_mlp_plan_create(const fconv_mlp_desc* desc, int device, int r
   if (st != FCONV_OK) return st;
   fconv_mlp_plan* p = *out;
   const fconv_mlp_desc& d = p->d;
-  const bool tc = mlp_tc_supported(d);
-  if (route < FCONV_MLP_AUTO || route > FCONV_MLP_TC || (route == FCONV_MLP_TC && !tc)) {
+  if (route < FCONV_MLP_AUTO || route > FCONV_MLP_TC) {
     delete p;
     *out = nullptr;
     return FCONV_E_UNSUPPORTED;
   }
   p->want = route;
-  p->tc = tc && route != FCONV_MLP_SIMPLE;
   p->saved = mlp_saved_bytes(d);
-  p->matrix = whole((size_t)d.tokens * (size_t)d.hidden * type_size(d.dtype));
-  p->fwd_ws = p->matrix;
-  if (d.training) {
-    const int64_t cols[3] = {d.hidden, d.hidden, d.out_features};
-    p->sums = whole(column_sums_workspace(cols, p->sms));
-    p->bwd_ws = 3 * p->matrix + p->sums + p->saved;
-  }
+  p->fwd_ws = mlp_workspace(*p, false);
+  if (d.training) p->bwd_ws = mlp_workspace(*p, true);
   return FCONV_OK;
 }
 
 fconv_status fconv_mlp_plan_route(const fconv_mlp_plan* p, int* route) {
   if (!p || !route) return FCONV_E_NULL;
-  *route = p->tc ? FCONV_MLP_TC : FCONV_MLP_SIMPLE;
+  *route = p->want == FCONV_MLP_SIMPLE ? FCONV_MLP_SIMPLE : FCONV_MLP_TC;
   return FCONV_OK;
 }
 
@@ -263,7 +262,7 @@ fconv_status fconv_mlp_forward_workspace(const fconv_mlp_plan* p, size_t* bytes)
 
 fconv_status fconv_mlp_backward_workspace(const fconv_mlp_plan* p, size_t* bytes) {
   if (!p || !bytes) return FCONV_E_NULL;
-  *bytes = p->bwd_ws;
+  *bytes = p->bwd_ws ? p->bwd_ws + p->saved : 0;
   return FCONV_OK;
 }
 
@@ -303,12 +302,10 @@ fconv_status fconv_mlp_forward(const fconv_mlp_plan* p, const void* x, const voi
   a.b_down = b_down;
   a.y = y;
   a.saved = saved;
-  a.h = workspace;
-  if (p->tc) {
-    bool whole = true;
-    for (const void* v : {x, w_gate, w_up, w_down, b_gate, b_up, b_down, (const void*)y})
-      whole = whole && !misaligned(v, 16);
-    if (whole) return done(launch_mlp_tc_forward(d, p->sms, a, (cudaStream_t)stream));
+  a.ws = workspace;
+  if (p->want != FCONV_MLP_SIMPLE) {
+    if (mlp_tc_supported(d, a, false))
+      return done(launch_mlp_tc_forward(d, p->sms, a, (cudaStream_t)stream));
     if (p->want == FCONV_MLP_TC) return FCONV_E_ALIGNMENT;
   }
   return done(launch_mlp_simple_forward(d, a, (cudaStream_t)stream));
@@ -341,8 +338,7 @@ fconv_status fconv_mlp_backward(const fconv_mlp_plan* p, const void* dy, const v
     for (int j = 0; j < i; ++j)
       if (outs[i] == outs[j]) return FCONV_E_ALIAS;
   }
-  if (!workspace || workspace_bytes < p->bwd_ws - (saved ? p->saved : 0))
-    return FCONV_E_WORKSPACE;
+  if (!workspace || workspace_bytes < p->bwd_ws + (saved ? 0 : p->saved)) return FCONV_E_WORKSPACE;
   MlpArgs a{};
   a.x = x;
   a.w_gate = w_gate;
@@ -355,27 +351,18 @@ fconv_status fconv_mlp_backward(const fconv_mlp_plan* p, const void* dy, const v
   a.dw_gate = dw_gate;
   a.dw_up = dw_up;
   a.dw_down = dw_down;
-  char* at = (char*)workspace;
-  a.dg = at;
-  a.du = at + p->matrix;
-  a.h = at + 2 * p->matrix;
-  float* sums = (float*)(at + 3 * p->matrix);
-  a.saved = saved ? const_cast<float*>(saved) : (float*)(at + 3 * p->matrix + p->sums);
+  a.db_gate = db_gate;
+  a.db_up = db_up;
+  a.db_down = db_down;
+  a.saved = saved ? const_cast<float*>(saved) : (float*)((char*)workspace + p->bwd_ws);
   a.remake = !saved;
-  bool tc = p->tc && d.tokens > 0;
-  if (tc) {
-    for (const void* v : {dy, x, w_gate, w_up, w_down, b_gate, b_up, (const void*)dx,
-                          (const void*)dw_gate, (const void*)dw_up, (const void*)dw_down})
-      tc = tc && !misaligned(v, 16);
-    if (!tc && p->want == FCONV_MLP_TC) return FCONV_E_ALIGNMENT;
+  a.ws = workspace;
+  if (p->want != FCONV_MLP_SIMPLE && d.tokens > 0) {  // no tokens: zeros, by the other route
+    if (mlp_tc_supported(d, a, true))
+      return done(launch_mlp_tc_backward(d, p->sms, a, (cudaStream_t)stream));
+    if (p->want == FCONV_MLP_TC) return FCONV_E_ALIGNMENT;
   }
-  const int err = tc ? launch_mlp_tc_backward(d, p->sms, a, (cudaStream_t)stream)
-                     : launch_mlp_simple_backward(d, a, (cudaStream_t)stream);
-  if (err) return done(err);
-  const SumsArgs m[3] = {{a.dg, d.hidden, d.hidden, db_gate},
-                         {a.du, d.hidden, d.hidden, db_up},
-                         {dy, d.dy_stride, d.out_features, db_down}};
-  return done(launch_column_sums(d.dtype, m, d.tokens, sums, p->sms, (cudaStream_t)stream));
+  return done(launch_mlp_simple_backward(d, p->sms, a, (cudaStream_t)stream));
 }
 
 void fconv_mlp_destroy(fconv_mlp_plan* p) { delete p; }

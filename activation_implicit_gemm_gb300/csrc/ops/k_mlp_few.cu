@@ -1,18 +1,24 @@
-// The gated feed-forward block for few tokens (include/fconv_ops.h): up to 32, f16 and bf16 with
-// sizes and strides of whole 16-byte units.
+// The gated feed-forward block for up to 32 tokens (include/fconv_ops.h), every type, size and
+// stride.
 //
 //   h = act(x Wg^T + bg) * (x Wu^T + bu),  y = h Wd^T + bd
 // Bound: HBM, every weight is read once for all tokens. Weights go from global memory straight
-// into the A operand of m16n8k16 instructions, tokens are the 8 columns of B. Lane (g, t) of a warp
-// takes 16 bytes of rows g and g + 8 and of token g, elements 8 t to 8 t + 7 of a step of 32; their
-// words 0 and 1 feed one instruction and 2 and 3 another, with the same order of K in both
+// into the A operand of warp-level tensor instructions, tokens are the 8 columns of B. Lane (g, t)
+// of a warp takes 16 bytes of rows g and g + 8 and of token g, of the 64 bytes of a step those from
+// 16 t on; words 0 and 1 feed one instruction and 2 and 3 another, with the same order of K in both
 // operands, so neither has to be moved between lanes. In the gated product rows 0 to 7 are the
-// gate's and 8 to 15 the up projection's of the same 8 hidden values.
+// gate's and 8 to 15 the up projection's of the same 8 hidden values. One token through 4096 x
+// 10240 in bf16: 41 us with the launches, 6.1 TB/s.
+//
+// f16 and bf16 are m16n8k16 operands as they are; f32 is split for m16n8k8 TF32 (hi + lo, three
+// products, sums of 16 products at a time as the instructions round towards zero). Where rows do
+// not start on 16 bytes the same bytes come an element at a time.
 //
 // The eight warps of a block share the same rows and split K; their f32 sums are joined through
 // shared memory in a fixed order, then come biases, gate and the one rounding. With more than 8
-// tokens a warp takes two row groups, so that tokens are read half as often.
+// 16-bit tokens a warp takes two row groups, so that tokens are read half as often.
 #include "mlp_math.cuh"
+#include "split_tf32.cuh"
 
 #include "../fconv_internal.h"
 #include "../ptx.cuh"
@@ -35,20 +41,37 @@ struct Few {
   float alpha;
 };
 
-__device__ __forceinline__ uint4 load_weight(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+// 16 bytes of a row from element k on, zeros past K.
+template <typename T, bool WIDE, bool WEIGHT>
+__device__ __forceinline__ uint4 load_row(const T* p, int k, int K) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if constexpr (WIDE) {
+    if (k < K) {
+      if (WEIGHT)
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(p + k));
+      else
+        v = *reinterpret_cast<const uint4*>(p + k);
+    }
+  } else {
+    constexpr int E = 16 / sizeof(T);
+    Vec<T, E> e;
+#pragma unroll
+    for (int i = 0; i < E; ++i) e.v[i] = k + i < K ? p[k + i] : from_f<T>(0.0f);
+    v = *reinterpret_cast<const uint4*>(&e);
+  }
   return v;
 }
+
 template <typename T>
 constexpr bool kIsBf16 = false;
 template <>
 constexpr bool kIsBf16<__nv_bfloat16> = true;
+
 template <typename T>
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                      uint32_t a3, uint32_t b0, uint32_t b1) {
   if constexpr (kIsBf16<T>) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -62,9 +85,39 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
   }
 }
 
+// acc += a step's products: rows a (g) and b (g + 8), tokens c.
+template <typename T>
+__device__ __forceinline__ void step(float (&acc)[4], const uint4& a, const uint4& b,
+                                     const uint4& c) {
+  if constexpr (sizeof(T) == 2) {
+    mma16<T>(acc, a.x, b.x, a.y, b.y, c.x, c.y);
+    mma16<T>(acc, a.z, b.z, a.w, b.w, c.z, c.w);
+  } else {
+    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+    const uint32_t cv[4] = {c.x, c.y, c.z, c.w};
+    float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      uint32_t ah[4], al[4], ch[2], cl[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        split_tf32(__uint_as_float(av[i + e]), ah[2 * e], al[2 * e]);
+        split_tf32(__uint_as_float(bv[i + e]), ah[2 * e + 1], al[2 * e + 1]);
+        split_tf32(__uint_as_float(cv[i + e]), ch[e], cl[e]);
+      }
+      mma_tf32(z, al, ch);
+      mma_tf32(z, ah, cl);
+      mma_tf32(z, ah, ch);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] += z[e];
+  }
+}
+
 // NT: groups of 8 tokens. MT: row groups of a warp. U: steps of K whose loads go out together.
-template <typename T, bool GATED, int NT, int MT, int U>
+template <typename T, bool WIDE, bool GATED, int NT, int MT, int U>
 __global__ void __launch_bounds__(kThreads, 2) mlp_few(const __grid_constant__ Few q) {
+  constexpr int kElems = 16 / sizeof(T), kStep = 4 * kElems;  // of a lane, of a step
   __shared__ float sums[kWarps][MT * 16][NT * 8 + 1];
   constexpr int kRows = GATED ? 8 : 16;  // outputs of a row group
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3;
@@ -77,14 +130,14 @@ __global__ void __launch_bounds__(kThreads, 2) mlp_few(const __grid_constant__ F
     for (int i = 0; i < 2; ++i) {
       const int which = GATED ? i : 0;
       const int row = min(n0 + m * kRows + (GATED ? 0 : i * 8) + gr, q.N - 1);
-      wp[m][i] = (const T*)q.w[which] + row * q.w_row[which] + t * 8;
+      wp[m][i] = (const T*)q.w[which] + row * q.w_row[which];
     }
   const T* xp[NT];
   bool there[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     there[n] = n * 8 + gr < q.tokens;
-    xp[n] = (const T*)q.x + (there[n] ? n * 8 + gr : 0) * q.x_row + t * 8;
+    xp[n] = (const T*)q.x + (there[n] ? n * 8 + gr : 0) * q.x_row;
   }
   float acc[MT][NT][4];
 #pragma unroll
@@ -96,31 +149,25 @@ __global__ void __launch_bounds__(kThreads, 2) mlp_few(const __grid_constant__ F
   ptx::pdl_wait();
   ptx::pdl_trigger();
 
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int k0 = warp * 32 * U; k0 < q.K; k0 += kWarps * 32 * U) {
+  for (int k0 = warp * kStep * U; k0 < q.K; k0 += kWarps * kStep * U) {
     uint4 w[U][MT][2], x[U][NT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = k0 + u * 32;
-      const bool in = k + t * 8 < q.K;
+      const int k = k0 + u * kStep + t * kElems;
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) w[u][m][i] = in ? load_weight(wp[m][i] + k) : zero;
+        for (int i = 0; i < 2; ++i) w[u][m][i] = load_row<T, WIDE, true>(wp[m][i], k, q.K);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        x[u][n] = in && there[n] ? *reinterpret_cast<const uint4*>(xp[n] + k) : zero;
+        x[u][n] = load_row<T, WIDE, false>(xp[n], there[n] ? k : q.K, q.K);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint4 a = w[u][m][0], b = w[u][m][1], c = x[u][n];
-          mma<T>(acc[m][n], a.x, b.x, a.y, b.y, c.x, c.y);
-          mma<T>(acc[m][n], a.z, b.z, a.w, b.w, c.z, c.w);
-        }
+        for (int n = 0; n < NT; ++n) step<T>(acc[m][n], w[u][m][0], w[u][m][1], x[u][n]);
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -152,34 +199,47 @@ __global__ void __launch_bounds__(kThreads, 2) mlp_few(const __grid_constant__ F
       float unused;
       v = act_of<false>(q.act, q.alpha, v, unused) * u;
     }
-    ((T*)q.out)[token * q.out_row + col] = from_f<T>(v);
+    if (q.out) ((T*)q.out)[token * q.out_row + col] = from_f<T>(v);
   }
 }
 
-template <typename T, bool GATED>
-int run(const Few& q, cudaStream_t s) {
+template <typename T, bool WIDE, bool GATED>
+int run_as(const Few& q, cudaStream_t s) {
+  constexpr int MT = sizeof(T) == 4 ? 1 : 2;
   const int rows = GATED ? 8 : 16;
   auto grid = [&](int mt) { return dim3((unsigned)((q.N + rows * mt - 1) / (rows * mt))); };
-  if (q.tokens <= 8) return launch_pdl(mlp_few<T, GATED, 1, 1, 4>, grid(1), dim3(kThreads), 0, s, q);
+  const dim3 block(kThreads);
+  if (q.tokens <= 8)
+    return launch_pdl(mlp_few<T, WIDE, GATED, 1, 1, 4>, grid(1), block, 0, s, q);
   if (q.tokens <= 16)
-    return launch_pdl(mlp_few<T, GATED, 2, 2, 2>, grid(2), dim3(kThreads), 0, s, q);
-  return launch_pdl(mlp_few<T, GATED, 4, 2, 2>, grid(2), dim3(kThreads), 0, s, q);
+    return launch_pdl(mlp_few<T, WIDE, GATED, 2, MT, 2>, grid(MT), block, 0, s, q);
+  return launch_pdl(mlp_few<T, WIDE, GATED, 4, MT, 2>, grid(MT), block, 0, s, q);
+}
+
+// 16-byte accesses where every row of weights and tokens starts on one and has no rest.
+template <typename T, bool GATED>
+int run(const Few& q, cudaStream_t s) {
+  constexpr int E = 16 / sizeof(T);
+  bool wide = q.K % E == 0 && (uintptr_t)q.x % 16 == 0 && (q.tokens == 1 || q.x_row % E == 0);
+  for (int i = 0; i < (GATED ? 2 : 1); ++i)
+    wide = wide && (uintptr_t)q.w[i] % 16 == 0 && (q.N == 1 || q.w_row[i] % E == 0);
+  return wide ? run_as<T, true, GATED>(q, s) : run_as<T, false, GATED>(q, s);
 }
 
 template <typename T>
-int gated(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s) {
+int gated(const fconv_mlp_desc& d, const MlpArgs& a, void* h, int64_t h_row, cudaStream_t s) {
   Few q{};
   q.x = a.x;
   q.w[0] = a.w_gate;
   q.w[1] = a.w_up;
   q.bias[0] = a.b_gate;
   q.bias[1] = a.b_up;
-  q.out = a.h;
+  q.out = h;
   q.saved = a.saved;
   q.x_row = d.x_stride;
   q.w_row[0] = d.gate_stride;
   q.w_row[1] = d.up_stride;
-  q.out_row = d.hidden;
+  q.out_row = h_row;
   q.quads = (d.hidden + 3) / 4;
   q.tokens = (int)d.tokens;
   q.K = (int)d.features;
@@ -190,13 +250,13 @@ int gated(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s) {
 }
 
 template <typename T>
-int down(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s) {
+int down(const fconv_mlp_desc& d, const MlpArgs& a, const void* h, int64_t h_row, cudaStream_t s) {
   Few q{};
-  q.x = a.h;
+  q.x = h;
   q.w[0] = a.w_down;
   q.bias[0] = a.b_down;
   q.out = a.y;
-  q.x_row = d.hidden;
+  q.x_row = h_row;
   q.w_row[0] = d.down_stride;
   q.out_row = d.y_stride;
   q.tokens = (int)d.tokens;
@@ -207,12 +267,18 @@ int down(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-int launch_mlp_few_gated(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s) {
-  return d.dtype == FCONV_BF16 ? gated<__nv_bfloat16>(d, a, s) : gated<__half>(d, a, s);
+int launch_mlp_few_gated(const fconv_mlp_desc& d, const MlpArgs& a, void* h, int64_t h_row,
+                         cudaStream_t s) {
+#define FCONV_M(T) return gated<T>(d, a, h, h_row, s)
+  FCONV_OPS_TYPE(d.dtype, FCONV_M)
+#undef FCONV_M
 }
 
-int launch_mlp_few_down(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s) {
-  return d.dtype == FCONV_BF16 ? down<__nv_bfloat16>(d, a, s) : down<__half>(d, a, s);
+int launch_mlp_few_down(const fconv_mlp_desc& d, const MlpArgs& a, const void* h, int64_t h_row,
+                        cudaStream_t s) {
+#define FCONV_M(T) return down<T>(d, a, h, h_row, s)
+  FCONV_OPS_TYPE(d.dtype, FCONV_M)
+#undef FCONV_M
 }
 
 }  // namespace ops

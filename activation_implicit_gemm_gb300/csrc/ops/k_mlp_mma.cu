@@ -13,6 +13,7 @@
 // the 64 columns are groups of 8 of the gate and 8 of the up projection in turn, so that a thread
 // has both values of its outputs.
 #include "mlp_math.cuh"
+#include "split_tf32.cuh"
 
 #include "../fconv_internal.h"
 #include "../ptx.cuh"
@@ -48,11 +49,9 @@ template <>
 struct Cell<true> {
   using Type = float2;
   static __device__ __forceinline__ float2 of(float v) {
-    const float largest = 3.4011621342146535e38f;  // of TF32; larger ones keep a rest, as lo
-    float c;
-    asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(c) : "f"(v), "f"(largest));
-    const float hi = __uint_as_float((__float_as_uint(c) + 0x1000u) & 0xffffe000u);
-    return make_float2(hi, v - hi);
+    uint32_t hi, lo;
+    split_tf32(v, hi, lo);
+    return make_float2(__uint_as_float(hi), __uint_as_float(lo));
   }
 };
 template <>
@@ -64,13 +63,6 @@ __device__ __forceinline__ uint32_t hi_of(float v) { return __float_as_uint(v); 
 __device__ __forceinline__ uint32_t hi_of(float2 v) { return __float_as_uint(v.x); }
 __device__ __forceinline__ uint32_t lo_of(float) { return 0; }
 __device__ __forceinline__ uint32_t lo_of(float2 v) { return __float_as_uint(v.y); }
-
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
 
 // A thread's part of a tile of ROWS x kK on its way from global memory.
 template <typename T, int ROWS>
@@ -186,12 +178,12 @@ __global__ void __launch_bounds__(kThreads, 2) mlp_mma(const __grid_constant__ P
         }
         if (SPLIT) {
 #pragma unroll
-          for (int n = 0; n < 4; ++n) mma(z[n], al, bh[k][n]);
+          for (int n = 0; n < 4; ++n) mma_tf32(z[n], al, bh[k][n]);
 #pragma unroll
-          for (int n = 0; n < 4; ++n) mma(z[n], ah, bl[k][n]);
+          for (int n = 0; n < 4; ++n) mma_tf32(z[n], ah, bl[k][n]);
         }
 #pragma unroll
-        for (int n = 0; n < 4; ++n) mma(z[n], ah, bh[k][n]);
+        for (int n = 0; n < 4; ++n) mma_tf32(z[n], ah, bh[k][n]);
       }
 #pragma unroll
       for (int n = 0; n < 4; ++n)
@@ -254,6 +246,15 @@ int run(const Product& q, cudaStream_t s) {
   return launch_pdl(mlp_mma<T, EPI>, dim3((unsigned)blocks), dim3(kThreads), smem, s, q);
 }
 
+// The workspace: h, and in the backward pass dg and du, rows of `hidden` values; then the sums.
+size_t matrix_bytes(const fconv_mlp_desc& d) {
+  const size_t n = (size_t)d.tokens * (size_t)d.hidden * (d.dtype == FCONV_F32 ? 4 : 2);
+  return (n + 255) / 256 * 256;
+}
+void* matrix(const fconv_mlp_desc& d, const MlpArgs& a, int i) {
+  return (char*)a.ws + i * matrix_bytes(d);
+}
+
 // The gated product: h (may be null) and, where `saved` is given, the projections.
 template <typename T>
 int gated(const fconv_mlp_desc& d, const MlpArgs& a, float* saved, void* h, cudaStream_t s) {
@@ -278,9 +279,10 @@ int gated(const fconv_mlp_desc& d, const MlpArgs& a, float* saved, void* h, cuda
 
 template <typename T>
 int forward(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s) {
-  if (const int e = gated<T>(d, a, a.saved, a.h, s)) return e;
+  void* h = matrix(d, a, 0);
+  if (const int e = gated<T>(d, a, a.saved, h, s)) return e;
   Product q{};
-  q.a[0] = {a.h, d.hidden, 1};
+  q.a[0] = {h, d.hidden, 1};
   q.b[0] = {a.w_down, d.down_stride, 1};
   q.terms = 1;
   q.M = d.tokens;
@@ -293,7 +295,8 @@ int forward(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s) {
 }
 
 template <typename T>
-int backward(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s) {
+int backward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s) {
+  void *h = matrix(d, a, 0), *dg = matrix(d, a, 1), *du = matrix(d, a, 2);
   int e = 0;
   if (a.remake) e = gated<T>(d, a, a.saved, nullptr, s);
   Product q{};
@@ -304,9 +307,9 @@ int backward(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s) {
     q.M = d.tokens;
     q.N = d.hidden;
     q.K = d.out_features;
-    q.out[0] = a.dg;
-    q.out[1] = a.du;
-    q.out[2] = a.h;
+    q.out[0] = dg;
+    q.out[1] = du;
+    q.out[2] = h;
     q.out_row = d.hidden;
     q.saved = a.saved;
     q.quads = (d.hidden + 3) / 4;
@@ -316,8 +319,8 @@ int backward(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s) {
   }
   if (!e && a.dx) {
     q = Product{};
-    q.a[0] = {a.dg, d.hidden, 1};
-    q.a[1] = {a.du, d.hidden, 1};
+    q.a[0] = {dg, d.hidden, 1};
+    q.a[1] = {du, d.hidden, 1};
     q.b[0] = {a.w_gate, 1, d.gate_stride};
     q.b[1] = {a.w_up, 1, d.up_stride};
     q.terms = 2;
@@ -343,10 +346,14 @@ int backward(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s) {
     q.out_row = n;
     e = run<T, kPlain>(q, s);
   };
-  weight(a.dg, d.hidden, d.hidden, a.x, d.x_stride, d.features, a.dw_gate);
-  weight(a.du, d.hidden, d.hidden, a.x, d.x_stride, d.features, a.dw_up);
-  weight(a.dy, d.dy_stride, d.out_features, a.h, d.hidden, d.hidden, a.dw_down);
-  return e;
+  weight(dg, d.hidden, d.hidden, a.x, d.x_stride, d.features, a.dw_gate);
+  weight(du, d.hidden, d.hidden, a.x, d.x_stride, d.features, a.dw_up);
+  weight(a.dy, d.dy_stride, d.out_features, h, d.hidden, d.hidden, a.dw_down);
+  if (e) return e;
+  const SumsArgs m[3] = {{dg, d.hidden, d.hidden, 0, a.db_gate},
+                         {du, d.hidden, d.hidden, 0, a.db_up},
+                         {a.dy, d.dy_stride, d.out_features, 0, a.db_down}};
+  return launch_column_sums(d.dtype, false, m, d.tokens, (float*)matrix(d, a, 3), sms, s);
 }
 
 }  // namespace
@@ -355,14 +362,20 @@ size_t mlp_saved_bytes(const fconv_mlp_desc& d) {
   return (size_t)saved_floats(d.tokens, d.hidden) * sizeof(float);
 }
 
+size_t mlp_simple_workspace(const fconv_mlp_desc& d, bool backward, int sms) {
+  if (!backward) return matrix_bytes(d);
+  const int64_t cols[3] = {d.hidden, d.hidden, d.out_features};
+  return 3 * matrix_bytes(d) + column_sums_workspace(cols, sms);
+}
+
 int launch_mlp_simple_forward(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s) {
 #define FCONV_M(T) return forward<T>(d, a, s)
   FCONV_OPS_TYPE(d.dtype, FCONV_M)
 #undef FCONV_M
 }
 
-int launch_mlp_simple_backward(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s) {
-#define FCONV_M(T) return backward<T>(d, a, s)
+int launch_mlp_simple_backward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s) {
+#define FCONV_M(T) return backward<T>(d, sms, a, s)
   FCONV_OPS_TYPE(d.dtype, FCONV_M)
 #undef FCONV_M
 }

@@ -29,7 +29,7 @@ template <typename T, int VEC>
 __device__ __forceinline__ void sum_rows(const T* p, int64_t row, int64_t cols, int64_t c,
                                          int64_t r, int64_t r1, float (&sum)[VEC]) {
   constexpr int kRows = kThreads / (kCols / VEC), kAhead = 4;
-  if (c >= cols) return;  // cols is a multiple of VEC
+  if (c >= cols) return;  // a row is whole accesses, the last columns may be no one's
   p += c;
   for (; r + (kAhead - 1) * kRows < r1; r += kAhead * kRows) {
     float x[kAhead][VEC];
@@ -48,7 +48,7 @@ __device__ __forceinline__ void sum_rows(const T* p, int64_t row, int64_t cols, 
   }
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, int PLANES>
 __global__ void __launch_bounds__(kThreads) column_sums(const __grid_constant__ Sums q) {
   constexpr int kAcross = kCols / VEC, kRows = kThreads / kAcross;
   __shared__ float sums[kRows][kCols + 1];
@@ -63,8 +63,10 @@ __global__ void __launch_bounds__(kThreads) column_sums(const __grid_constant__ 
   float sum[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) sum[e] = 0.0f;
-  sum_rows<T, VEC>((const T*)m.p, m.row, m.cols, c0 + across * VEC, blockIdx.y * each + down, r1,
-                   sum);
+#pragma unroll
+  for (int i = 0; i < PLANES; ++i)
+    sum_rows<T, VEC>((const T*)m.p + i * m.plane, m.row, m.cols, c0 + across * VEC,
+                     blockIdx.y * each + down, r1, sum);
 #pragma unroll
   for (int e = 0; e < VEC; ++e) sums[down][across * VEC + e] = sum[e];
   __syncthreads();
@@ -107,8 +109,8 @@ size_t column_sums_workspace(const int64_t cols[3], int sms) {
   return (size_t)(4 * (int64_t)sms + 2 * blocks) * kCols * sizeof(float);
 }
 
-int launch_column_sums(int dtype, const SumsArgs m[3], int64_t rows, float* part, int sms,
-                       cudaStream_t s) {
+int launch_column_sums(int dtype, bool planes, const SumsArgs m[3], int64_t rows, float* part,
+                       int sms, cudaStream_t s) {
   Sums q{};
   q.part = part;
   q.rows = rows;
@@ -118,18 +120,25 @@ int launch_column_sums(int dtype, const SumsArgs m[3], int64_t rows, float* part
   }
   if (q.first[3] == 0) return 0;
   q.shares = shares_of(q.first[3], rows, sms);
-  // 16-byte accesses where every row of every matrix starts on one
-  const int full = dtype == FCONV_F32 ? 4 : 8;
-  bool wide = true;
-  for (int i = 0; i < 3; ++i)
-    if (m[i].out)
-      wide = wide && m[i].cols % full == 0 && m[i].row % full == 0 && (uintptr_t)m[i].p % 16 == 0;
-  const dim3 grid((unsigned)q.first[3], (unsigned)q.shares);
+  const dim3 grid((unsigned)q.first[3], (unsigned)q.shares), block(kThreads);
   int e = 0;
-#define FCONV_M(T)                                                                             \
-  e = wide ? launch_pdl(column_sums<T, 16 / (int)sizeof(T)>, grid, dim3(kThreads), 0, s, q)    \
-           : launch_pdl(column_sums<T, 1>, grid, dim3(kThreads), 0, s, q);                     \
-  if (!e) e = launch_pdl(column_join<T>, dim3((unsigned)q.first[3]), dim3(kCols), 0, s, q)
+  if (planes) {  // rows of whole 16-byte units
+    e = launch_pdl(column_sums<__nv_bfloat16, 8, 3>, grid, block, 0, s, q);
+  } else {
+    // 16-byte accesses where every row of every matrix starts on one and has no rest
+    const int full = dtype == FCONV_F32 ? 4 : 8;
+    bool wide = true;
+    for (int i = 0; i < 3; ++i)
+      if (m[i].out)
+        wide = wide && m[i].cols % full == 0 && m[i].row % full == 0 && (uintptr_t)m[i].p % 16 == 0;
+#define FCONV_M(T)                                                                   \
+  e = wide ? launch_pdl(column_sums<T, 16 / (int)sizeof(T), 1>, grid, block, 0, s, q) \
+           : launch_pdl(column_sums<T, 1, 1>, grid, block, 0, s, q)
+    FCONV_OPS_TYPE(dtype, FCONV_M)
+#undef FCONV_M
+  }
+  if (e) return e;
+#define FCONV_M(T) e = launch_pdl(column_join<T>, dim3((unsigned)q.first[3]), dim3(kCols), 0, s, q)
   FCONV_OPS_TYPE(dtype, FCONV_M)
 #undef FCONV_M
   return e;

@@ -1,5 +1,4 @@
-// The gated feed-forward block on tcgen05 tensor cores (include/fconv_ops.h): f16 and bf16 with
-// sizes and strides of whole 16-byte units.
+// The gated feed-forward block on tcgen05 tensor cores (include/fconv_ops.h).
 //
 //   forward   h = act(x Wg^T + bg) * (x Wu^T + bu)      both products in one accumulator
 //             y = h Wd^T + bd
@@ -17,7 +16,14 @@
 // 32 KB stages full, an MMA warp issues, eight warps empty one accumulator while the next tile's
 // products fill the other. Blocks are persistent and take tiles in groups of 8 rows of tiles, so
 // that blocks at work at one time share operands in L2.
+//
+// f32 (F32) comes as three bf16 planes that add up to it (k_mlp_prep.cu; h, dg and du are split in
+// the epilogues). Six products of planes, the smallest first, leave out less than 2^-23 of a
+// product. The tensor core's f32 sums cut off instead of rounding (measured: 1.7e-8 of the result
+// for each instruction of 16 products, always towards zero), so after 512 of K they are added to
+// registers in plain f32.
 #include "mlp_math.cuh"
+#include "split_bf16.cuh"
 #include "tc_instr.cuh"
 #include "waits.cuh"
 
@@ -37,18 +43,23 @@ constexpr int kEpiWarps = 8, kFirstEpiWarp = 4;
 
 enum { kPlain, kGated, kGrad };
 
-template <int EPI>
-constexpr int kStages = EPI == kGrad ? 5 : 6;
-template <int EPI>
-constexpr int kSlots = EPI == kGrad ? 3 : 2;  // of each epilogue warpgroup
+constexpr int kPlanes = 3, kTerms = 6;  // of f32
+constexpr int kChunk = 8;               // steps of K whose sums stay in TMEM, f32
+
+template <int EPI, bool F32>
+constexpr int kSlots = EPI == kGrad || (F32 && EPI == kGated) ? 3 : 2;  // of an epilogue warpgroup
+template <int EPI, bool F32>
+constexpr int kStages = kSlots<EPI, F32> == 3 ? 5 : 6;
 
 struct Problem {
-  CUtensorMap a[2], b[2], c[3];  // terms of a sum (kGated: gate and up), outputs
-  int mt, nt, steps;             // tiles, steps of a term
-  int terms;
+  CUtensorMap a[2], b[2], c[3];  // products of a sum (kGated: gate and up), outputs as boxes
+  int mt, nt, steps;             // tiles, steps of a product
+  int products;
   int64_t M;
   int N;
   const void* bias[2];
+  void* out;                     // where boxes do not go: rows of any stride
+  int64_t out_row;
 };
 struct Job {
   Problem p[3];
@@ -140,22 +151,24 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 // A box into this block's shared memory, its bytes counted on a barrier of the first block.
 template <int CG>
 __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int c0, int c1,
-                                         uint32_t bar) {
+                                         int plane, uint32_t bar) {
   if (CG == 1) {
-    ptx::tma_load_2d(dst, map, c0, c1, bar);
+    ptx::tma_load_3d(dst, map, c0, c1, plane, bar);
   } else {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 "
-        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"((uint64_t)map), "r"(c0), "r"(c1), "r"(bar)
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"((uint64_t)map), "r"(c0), "r"(c1), "r"(plane), "r"(bar)
         : "memory");
   }
 }
-__device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, int c0, int c1) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::
-                   "l"((uint64_t)map),
-               "r"(src), "r"(c0), "r"(c1)
-               : "memory");
+__device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, int c0, int c1,
+                                          int plane) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          (uint64_t)map),
+      "r"(src), "r"(c0), "r"(c1), "r"(plane)
+      : "memory");
 }
 template <int N>
 __device__ __forceinline__ void bulk_wait_read_but() {
@@ -221,6 +234,43 @@ __device__ __forceinline__ Tile tile_of(const Job& j, int id) {
   return t;
 }
 
+// The steps of a tile in passes, each into an accumulator of its own: one for 16-bit types; for f32
+// one for every kChunk steps of a product, six terms each.
+struct Passes {
+  int chunks, count;
+};
+template <bool F32>
+__device__ __forceinline__ Passes passes_of(const Problem& p, int products) {
+  Passes v;
+  v.chunks = F32 ? (p.steps + kChunk - 1) / kChunk : 1;
+  v.count = F32 ? products * v.chunks : 1;
+  return v;
+}
+template <bool F32>
+__device__ __forceinline__ int steps_of(const Problem& p, int products, const Passes& v, int pass) {
+  if (!F32) return products * p.steps;
+  return kTerms * min(kChunk, p.steps - pass % v.chunks * kChunk);
+}
+struct Step {
+  int product, k, a_plane, b_plane;
+};
+template <bool F32>
+__device__ __forceinline__ Step step_of(const Problem& p, const Passes& v, int pass, int i) {
+  Step s;
+  if (!F32) {
+    s.product = i >= p.steps;
+    s.k = i - s.product * p.steps;
+    s.a_plane = s.b_plane = 0;
+  } else {
+    s.product = pass / v.chunks;
+    const int c0 = pass % v.chunks * kChunk, len = min(kChunk, p.steps - c0), term = i / len;
+    s.k = c0 + i - term * len;
+    s.a_plane = (0x001102 >> (4 * term)) & 3;  // 2 0 1 1 0 0
+    s.b_plane = (0x010120 >> (4 * term)) & 3;  // 0 2 1 0 1 0
+  }
+  return s;
+}
+
 __device__ __forceinline__ uint32_t pack16(bool bf16, float a, float b) {
   return bf16 ? pack2<true>(a, b) : pack2<false>(a, b);
 }
@@ -229,8 +279,7 @@ __device__ __forceinline__ float2 unpack16(bool bf16, uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
-// A row's 8 N / 4... values: N words of a 32-column row (64 bytes) of a staged box in the 64-byte
-// swizzle, from word w0 on.
+// N words of a row (64 bytes, 32 values) of a staged box in the 64-byte swizzle, from word w0 on.
 template <int N>
 __device__ __forceinline__ void stage(uint32_t slot, int row, int w0, const uint32_t (&w)[N]) {
 #pragma unroll
@@ -238,23 +287,57 @@ __device__ __forceinline__ void stage(uint32_t slot, int row, int w0, const uint
     ptx::st_shared_v4(slot + row * 64 + ((((w0 + i) >> 2) ^ ((row >> 1) & 3)) << 4), w[i], w[i + 1],
                       w[i + 2], w[i + 3]);
 }
-
-// x[i] += bias[col + i] for 32 columns, those past N left alone (N is a multiple of 8).
-__device__ __forceinline__ void add_bias(float (&x)[32], const void* bias, int col, int N,
-                                         bool bf16) {
-  if (!bias) return;
+// 8 f32 values from column c0 on as their three bf16 planes, in three slots.
+__device__ __forceinline__ void stage_planes(uint32_t slots, int row, int c0, const float* x) {
+  uint32_t w[kPlanes][4];
 #pragma unroll
-  for (int i = 0; i < 32; i += 8) {
-    if (col + i >= N) break;
-    const uint4 v = ptx::ldg_nc_v4((const uint16_t*)bias + col + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  for (int i = 0; i < 4; ++i) {
+    float a[kPlanes], b[kPlanes];
+    split_bf16(x[2 * i], a);
+    split_bf16(x[2 * i + 1], b);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = unpack16(bf16, w[k]);
-      x[i + 2 * k] += f.x;
-      x[i + 2 * k + 1] += f.y;
+    for (int q = 0; q < kPlanes; ++q) w[q][i] = pack2<true>(a[q], b[q]);
+  }
+#pragma unroll
+  for (int q = 0; q < kPlanes; ++q) stage(slots + q * kSlot, row, c0 / 2, w[q]);
+}
+// The staged rows of a warp to global memory, a row of 32 columns at a time, at any alignment.
+template <bool F32>
+__device__ __forceinline__ void store_rows(uint32_t slot, void* out, int64_t out_row, int64_t grow0,
+                                           int row0, int64_t M, int col, int N, int lane) {
+  __syncwarp();
+  const bool in = col + lane < N;
+#pragma unroll 4
+  for (int i = 0; i < 32; ++i) {
+    const int row = row0 + i;
+    if (grow0 + i >= M) break;
+    const int64_t at = (grow0 + i) * out_row + col + lane;
+    if (F32) {
+      const uint32_t v =
+          ptx::ld_shared_u32(slot + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4);
+      if (in) ((uint32_t*)out)[at] = v;
+    } else {
+      const uint32_t v = ptx::ld_shared_u16(slot + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) +
+                                            (lane & 7) * 2);
+      if (in) ((uint16_t*)out)[at] = (uint16_t)v;
     }
   }
+  __syncwarp();
+}
+
+// x[i] += bias[col + i] for 32 columns, those past N left alone. A lane reads one.
+template <bool F32>
+__device__ __forceinline__ void add_bias(float (&x)[32], const void* bias, int col, int N, bool bf16,
+                                         int lane) {
+  if (!bias) return;
+  float v = 0.0f;
+  if (col + lane < N) {
+    if (F32) v = ((const float*)bias)[col + lane];
+    else if (bf16) v = to_f(((const __nv_bfloat16*)bias)[col + lane]);
+    else v = to_f(((const __half*)bias)[col + lane]);
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) x[i] += __shfl_sync(0xffffffffu, v, i);
 }
 
 __device__ __forceinline__ void as_floats(float (&x)[32], const uint32_t (&r)[32]) {
@@ -298,9 +381,9 @@ __device__ __forceinline__ void gate_grad(uint32_t (&wg)[4], uint32_t (&wu)[4], 
   }
 }
 
-template <int CG, bool AMN, bool BMN, int EPI>
+template <int CG, bool AMN, bool BMN, int EPI, bool F32>
 __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Job j) {
-  constexpr int S = kStages<EPI>, BN = 128 * CG;
+  constexpr int S = kStages<EPI, F32>, BN = 128 * CG;
   constexpr int kCols = EPI == kGated ? BN / 2 : BN;  // of a tile of D
   constexpr uint32_t kStageBytes = 2 * kSide;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -344,33 +427,38 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
       const Problem& p = j.p[t.which];
       const int m0 = (t.m * CG + (int)rank) * 128;
       const int n0 = EPI == kGated ? t.n * kCols : t.n * BN + (int)rank * 128;
-      const int terms = EPI == kGated ? 1 : p.terms;
-      for (int term = 0; ok && term < terms; ++term) {
-        for (int k = 0; k < p.steps; ++k, ++it) {
+      const int products = EPI == kGated ? 1 : p.products;
+      const Passes v = passes_of<F32>(p, products);
+      for (int pass = 0; ok && pass < v.count; ++pass) {
+        const int steps = steps_of<F32>(p, products, v, pass);
+        for (int i = 0; i < steps; ++i, ++it) {
+          const Step st = step_of<F32>(p, v, pass, i);
           const int s = it % S;
           ok = all_lanes(wait_bar(ptx::smem_addr(&ctl.empty[s]), ((it / S) & 1) ^ 1, abort_flag));
           if (!ok) break;
           const uint32_t own = ptx::smem_addr(&ctl.full[s]);
           const uint32_t bar = CG == 1 ? own : in_first(own);
           const uint32_t sa = ring + s * kStageBytes, sb = sa + kSide;
+          const CUtensorMap *ma = &p.a[st.product], *mb = &p.b[st.product];
+          const int k = st.k * kStep, pa = st.a_plane, pb = st.b_plane;
           if (elect_lane()) {
             if (rank == 0) ptx::mbar_arrive_expect_tx(own, CG * kStageBytes);
             if (AMN) {
-              load_box<CG>(sa, &p.a[term], m0, k * kStep, bar);
-              load_box<CG>(sa + kBox, &p.a[term], m0 + 64, k * kStep, bar);
+              load_box<CG>(sa, ma, m0, k, pa, bar);
+              load_box<CG>(sa + kBox, ma, m0 + 64, k, pa, bar);
             } else {
-              load_box<CG>(sa, &p.a[term], k * kStep, m0, bar);
+              load_box<CG>(sa, ma, k, m0, pa, bar);
             }
             if (BMN) {
-              load_box<CG>(sb, &p.b[term], n0, k * kStep, bar);
-              load_box<CG>(sb + kBox, &p.b[term], n0 + 64, k * kStep, bar);
+              load_box<CG>(sb, mb, n0, k, pb, bar);
+              load_box<CG>(sb + kBox, mb, n0 + 64, k, pb, bar);
             } else if (EPI == kGated && CG == 1) {
-              load_box<CG>(sb, &p.b[0], k * kStep, n0, bar);
-              load_box<CG>(sb + kBox, &p.b[1], k * kStep, n0, bar);
+              load_box<CG>(sb, &p.b[0], k, n0, pb, bar);
+              load_box<CG>(sb + kBox, &p.b[1], k, n0, pb, bar);
             } else if (EPI == kGated) {
-              load_box<CG>(sb, &p.b[rank], k * kStep, n0, bar);
+              load_box<CG>(sb, &p.b[rank], k, n0, pb, bar);
             } else {
-              load_box<CG>(sb, &p.b[term], k * kStep, n0, bar);
+              load_box<CG>(sb, mb, k, n0, pb, bar);
             }
           }
           __syncwarp();
@@ -388,33 +476,38 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
     }
   } else if (warp == 1) {  // products
     if (rank == 0) {
-      const uint32_t idesc = idesc_16(j.bf16, 128 * CG, BN, BMN) | (AMN ? 1u << 15 : 0u);
+      const uint32_t idesc = idesc_16(F32 || j.bf16, 128 * CG, BN, BMN) | (AMN ? 1u << 15 : 0u);
       int it = 0, n = 0;
       bool ok = true;
-      for (int id = first; ok && id < j.tiles; id += stride, ++n) {
+      for (int id = first; ok && id < j.tiles; id += stride) {
         const Tile t = tile_of(j, id);
         const Problem& p = j.p[t.which];
-        const int steps = p.steps * (EPI == kGated ? 1 : p.terms);
-        const uint32_t d = tmem + (n & 1) * BN;
-        ok = all_lanes(
-            wait_cluster(ptx::smem_addr(&ctl.acc_empty[n & 1]), ((n >> 1) & 1) ^ 1, abort_flag));
-        ptx::tc_fence_after();
-        for (int k = 0; ok && k < steps; ++k, ++it) {
-          const int s = it % S;
-          ok = all_lanes(wait_bar(ptx::smem_addr(&ctl.full[s]), (it / S) & 1, abort_flag));
-          if (!ok) break;
+        const int products = EPI == kGated ? 1 : p.products;
+        const Passes v = passes_of<F32>(p, products);
+        for (int pass = 0; ok && pass < v.count; ++pass, ++n) {
+          const int steps = steps_of<F32>(p, products, v, pass);
+          const uint32_t d = tmem + (n & 1) * BN;
+          ok = all_lanes(wait_cluster(ptx::smem_addr(&ctl.acc_empty[n & 1]), ((n >> 1) & 1) ^ 1,
+                                      abort_flag));
           ptx::tc_fence_after();
-          const uint32_t sa = ring + s * kStageBytes, sb = sa + kSide;
-          const uint32_t a = uni(AMN ? desc_mn(sa, kBox) : desc_k(sa));
-          const uint32_t b = uni(BMN ? desc_mn(sb, kBox) : desc_k(sb));
-          if (elect_lane()) {
+          for (int k = 0; ok && k < steps; ++k, ++it) {
+            const int s = it % S;
+            ok = all_lanes(wait_bar(ptx::smem_addr(&ctl.full[s]), (it / S) & 1, abort_flag));
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint32_t sa = ring + s * kStageBytes, sb = sa + kSide;
+            const uint32_t a = uni(AMN ? desc_mn(sa, kBox) : desc_k(sa));
+            const uint32_t b = uni(BMN ? desc_mn(sb, kBox) : desc_k(sb));
+            if (elect_lane()) {
 #pragma unroll
-            for (int i = 0; i < kStep / 16; ++i)  // 16 elements of a row, or 16 rows
-              mma<CG>(d, a + i * (AMN ? 128 : 2), b + i * (BMN ? 128 : 2), idesc, k > 0 || i > 0);
-            commit<CG>(ptx::smem_addr(&ctl.empty[s]));
-            if (k + 1 == steps) commit<CG>(ptx::smem_addr(&ctl.acc_full[n & 1]));
+              for (int i = 0; i < kStep / 16; ++i)  // 16 elements of a row, or 16 rows
+                mma<CG>(d, a + i * (AMN ? 128 : 2), b + i * (BMN ? 128 : 2), idesc,
+                        k > 0 || i > 0);
+              commit<CG>(ptx::smem_addr(&ctl.empty[s]));
+              if (k + 1 == steps) commit<CG>(ptx::smem_addr(&ctl.acc_full[n & 1]));
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
       if (!ok) {  // the products issued so far read both blocks' shared memory
@@ -426,13 +519,15 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
   } else if (warp >= kFirstEpiWarp) {
     const int half = (warp - kFirstEpiWarp) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
-    const uint32_t slots = ring + S * kStageBytes + half * kSlots<EPI> * kSlot;
+    const uint32_t slots = ring + S * kStageBytes + half * kSlots<EPI, F32> * kSlot;
     const bool bf16 = j.bf16;
     const bool issues = threadIdx.x == (kFirstEpiWarp + 4 * half) * 32;
     const int act = j.act;
     const float alpha = j.alpha;
+    constexpr int kParts = kCols / 64;  // 32-column parts of a warp's half of the tile
     int n = 0, slot = 0;
-    for (int id = first; id < j.tiles; id += stride, ++n) {
+    bool ok = true;
+    for (int id = first; ok && id < j.tiles; id += stride) {
       const Tile t = tile_of(j, id);
       const Problem& p = j.p[t.which];
       const int m0 = (t.m * CG + (int)rank) * 128;
@@ -441,97 +536,193 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
       float* saved = nullptr;
       if (EPI != kPlain && j.saved)
         saved = j.saved + (grow >> 5) * j.quads * 256 + lane * 4;
-      // the warps of a group, which meet at barriers below, go on or give up together
-      if (!bar_and(1 + half, 128,
-                   wait_bar(ptx::smem_addr(&ctl.acc_full[n & 1]), (n >> 1) & 1, abort_flag)))
-        break;
-      ptx::tc_fence_after();
-      const uint32_t acc = tmem + (n & 1) * BN + ((uint32_t)(quarter * 32) << 16);
-#pragma unroll 1
-      for (int c = 0; c < kCols / 64; ++c) {
-        const int tcol = half * (kCols / 2) + c * 32, col = t.n * kCols + tcol;
-        uint32_t r0[32], r1[32];
+
+      // The warps of a group, which meet at barriers below, go on or give up together.
+      auto arrive = [&]() {
+        ok = bar_and(1 + half, 128, wait_bar(ptx::smem_addr(&ctl.acc_full[n & 1]), (n >> 1) & 1,
+                                             abort_flag));
+        ptx::tc_fence_after();
+        return ok;
+      };
+      auto release = [&]() {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t bar = ptx::smem_addr(&ctl.acc_empty[n & 1]);
+          if (CG == 1) ptx::mbar_arrive(bar);
+          else arrive_cluster(in_first(bar));
+        }
+      };
+      auto fetch = [&](int c, uint32_t (&r0)[32], uint32_t (&r1)[32]) {
+        const uint32_t acc = tmem + (n & 1) * BN + ((uint32_t)(quarter * 32) << 16);
+        const int tcol = half * (kCols / 2) + c * 32;
         tmem_fetch32(acc + tcol, r0);
         if (EPI == kGated) tmem_fetch32(acc + BN / 2 + tcol, r1);
         tmem_wait_ld();
         tmem_arrived(r0);
         if (EPI == kGated) tmem_arrived(r1);
-        if (c + 1 == kCols / 64) {  // the accumulator is free
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            const uint32_t bar = ptx::smem_addr(&ctl.acc_empty[n & 1]);
-            if (CG == 1) ptx::mbar_arrive(bar);
-            else arrive_cluster(in_first(bar));
-          }
-        }
-        if (col >= p.N) continue;  // the same for the whole warpgroup
-        if (issues) bulk_wait_read_but<EPI == kGrad ? 0 : kSlots<EPI> - 1>();
+      };
+      // Slots that may be written again, for all warps of the group.
+      auto reuse = [&]() {
+        if (issues) bulk_wait_read_but<kSlots<EPI, F32> == 3 ? 0 : 1>();
         ptx::bar_sync(1 + half, 128);
+      };
+      auto store = [&](const CUtensorMap* map, int col, int boxes, uint32_t from, bool planes) {
+        ptx::fence_proxy_async_smem();
+        ptx::bar_sync(1 + half, 128);
+        if (issues && m0 < p.M) {
+          for (int i = 0; i < boxes; ++i)
+            store_box(planes ? map : map + i, from + i * kSlot, col, m0, planes ? i : 0);
+          bulk_commit();
+        }
+      };
+      // 32 columns from `col` on; x (and with kGated u) are sums of products.
+      auto finish = [&](int c, float (&x)[32], float (&u)[32]) {
+        const int col = t.n * kCols + half * (kCols / 2) + c * 32;
+        if (col >= p.N) return;  // the same for the whole group
         if (EPI == kPlain) {
-          float x[32];
-          as_floats(x, r0);
-          add_bias(x, p.bias[0], col, p.N, bf16);
+          add_bias<F32>(x, p.bias[0], col, p.N, bf16, lane);
           uint32_t w[16];
+          if (F32) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = pack16(bf16, x[2 * i], x[2 * i + 1]);
-          stage(slots + slot * kSlot, row, 0, w);
+            for (int i = 0; i < 32; i += 4)
+              ptx::st_shared_v4(slots + row * 128 + (((i >> 2) ^ (row & 7)) << 4),
+                                __float_as_uint(x[i]), __float_as_uint(x[i + 1]),
+                                __float_as_uint(x[i + 2]), __float_as_uint(x[i + 3]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = pack16(bf16, x[2 * i], x[2 * i + 1]);
+          }
+          if (F32 || p.out) {  // a warp's own rows: no warp waits for another
+            if (!F32) {        // but for boxes of another problem's tile that may be on their way
+              if (issues) bulk_wait_read_but<0>();
+              ptx::bar_sync(1 + half, 128);
+              stage(slots, row, 0, w);
+            }
+            store_rows<F32>(slots, p.out, p.out_row, (int64_t)m0 + quarter * 32, quarter * 32, p.M,
+                            col, p.N, lane);
+          } else {
+            reuse();
+            stage(slots + slot * kSlot, row, 0, w);
+            store(&p.c[0], col, 1, slots + slot * kSlot, false);
+            slot ^= 1;
+          }
         } else if (EPI == kGated) {
-          float g[32], u[32];
-          as_floats(g, r0);
-          as_floats(u, r1);
-          add_bias(g, p.bias[0], col, p.N, bf16);
-          add_bias(u, p.bias[1], col, p.N, bf16);
+          add_bias<F32>(x, p.bias[0], col, p.N, bf16, lane);
+          add_bias<F32>(u, p.bias[1], col, p.N, bf16, lane);
           if (saved && grow < p.M) {
             float* to = saved + (int64_t)(col >> 2) * 256;
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
               if (col + i >= p.N) break;
               *reinterpret_cast<float4*>(to + i * 64) =
-                  make_float4(g[i], g[i + 1], g[i + 2], g[i + 3]);
+                  make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
               *reinterpret_cast<float4*>(to + i * 64 + 128) =
                   make_float4(u[i], u[i + 1], u[i + 2], u[i + 3]);
             }
           }
-          uint32_t w[16];
-#define FCONV_M(ACT) gate<ACT>(w, g, u, alpha, bf16)
-          FCONV_GATE_SWITCH(act, FCONV_M)
+          reuse();
+          if (F32) {
+            float unused;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = act_of<false>(act, alpha, x[i], unused) * u[i];
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) stage_planes(slots, row, i, x + i);
+            store(&p.c[0], col, kPlanes, slots, true);
+          } else {
+            uint32_t w[16];
+#define FCONV_M(ACT) gate<ACT>(w, x, u, alpha, bf16)
+            FCONV_GATE_SWITCH(act, FCONV_M)
 #undef FCONV_M
-          stage(slots + slot * kSlot, row, 0, w);
+            stage(slots + slot * kSlot, row, 0, w);
+            store(&p.c[0], col, 1, slots + slot * kSlot, false);
+            slot ^= 1;
+          }
         } else {
           const float* from = saved + (int64_t)(col >> 2) * 256;
-          float dh[32];
-          as_floats(dh, r0);
-#define FCONV_M(ACT)                                                                        \
-  _Pragma("unroll") for (int i = 0; i < 32; i += 8) {                                       \
-    uint32_t wg[4], wu[4], wh[4];                                                           \
-    float4 g[2] = {}, u[2] = {};                                                            \
-    if (grow < p.M && col + i < p.N) {                                                      \
-      _Pragma("unroll") for (int k = 0; k < 2; ++k) {                                       \
-        g[k] = __ldcg(reinterpret_cast<const float4*>(from + (i + 4 * k) * 64));            \
-        u[k] = __ldcg(reinterpret_cast<const float4*>(from + (i + 4 * k) * 64 + 128));      \
-      }                                                                                     \
-    }                                                                                       \
-    gate_grad<ACT>(wg, wu, wh, dh + i, g, u, alpha, bf16);                                  \
-    stage(slots, row, i / 2, wg);                                                           \
-    stage(slots + kSlot, row, i / 2, wu);                                                   \
-    stage(slots + 2 * kSlot, row, i / 2, wh);                                               \
-  }
-          FCONV_GATE_SWITCH(act, FCONV_M)
-#undef FCONV_M
-        }
-        ptx::fence_proxy_async_smem();
-        ptx::bar_sync(1 + half, 128);
-        if (issues && m0 < p.M) {
-          if (EPI == kGrad) {
+          auto load = [&](int i, float4& g, float4& v) {
+            g = v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (grow < p.M && col + i < p.N) {
+              g = __ldcg(reinterpret_cast<const float4*>(from + i * 64));
+              v = __ldcg(reinterpret_cast<const float4*>(from + i * 64 + 128));
+            }
+          };
+          if (F32) {
+#pragma unroll 1
+            for (int which = 0; which < 3; ++which) {  // dg, du, h: one after the other
+              reuse();
 #pragma unroll
-            for (int i = 0; i < 3; ++i) store_box(&p.c[i], slots + i * kSlot, col, m0);
+              for (int i = 0; i < 32; i += 8) {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; k += 4) {
+                  float4 g4, u4;
+                  load(i + k, g4, u4);
+                  const float gs[4] = {g4.x, g4.y, g4.z, g4.w}, us[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    float slope;
+                    const float a = act_of<true>(act, alpha, gs[e], slope), d = x[i + k + e];
+                    v[k + e] = which == 0 ? d * us[e] * slope : which == 1 ? d * a : a * us[e];
+                  }
+                }
+                stage_planes(slots, row, i, v);
+              }
+              store(&p.c[which], col, kPlanes, slots, true);
+            }
           } else {
-            store_box(&p.c[0], slots + slot * kSlot, col, m0);
+            reuse();
+#define FCONV_M(ACT)                                                 \
+  _Pragma("unroll") for (int i = 0; i < 32; i += 8) {                \
+    uint32_t wg[4], wu[4], wh[4];                                    \
+    float4 g[2], v[2];                                               \
+    load(i, g[0], v[0]);                                             \
+    load(i + 4, g[1], v[1]);                                         \
+    gate_grad<ACT>(wg, wu, wh, x + i, g, v, alpha, bf16);            \
+    stage(slots, row, i / 2, wg);                                    \
+    stage(slots + kSlot, row, i / 2, wu);                            \
+    stage(slots + 2 * kSlot, row, i / 2, wh);                        \
+  }
+            FCONV_GATE_SWITCH(act, FCONV_M)
+#undef FCONV_M
+            store(&p.c[0], col, 3, slots, false);
           }
-          bulk_commit();
         }
-        if (EPI != kGrad) slot ^= 1;
+      };
+
+      if constexpr (F32) {
+        float x[kParts][32], u[EPI == kGated ? kParts : 1][32];
+        const Passes v = passes_of<F32>(p, EPI == kGated ? 1 : p.products);
+        for (int pass = 0; pass < v.count; ++pass, ++n) {
+          if (!arrive()) break;
+#pragma unroll
+          for (int c = 0; c < kParts; ++c) {
+            uint32_t r0[32], r1[32];
+            fetch(c, r0, r1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              x[c][i] = (pass ? x[c][i] : 0.0f) + __uint_as_float(r0[i]);
+              if (EPI == kGated) u[c][i] = (pass ? u[c][i] : 0.0f) + __uint_as_float(r1[i]);
+            }
+          }
+          release();
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < kParts; ++c) finish(c, x[c], u[EPI == kGated ? c : 0]);
+      } else {
+        if (!arrive()) break;
+#pragma unroll 1
+        for (int c = 0; c < kParts; ++c) {
+          uint32_t r0[32], r1[32];
+          float x[32], u[32];
+          fetch(c, r0, r1);
+          if (c + 1 == kParts) release();
+          as_floats(x, r0);
+          if (EPI == kGated) as_floats(u, r1);
+          finish(c, x, u);
+        }
+        ++n;
       }
     }
     if (issues) bulk_wait_all();
@@ -545,30 +736,32 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
 
 // -------------------------------------------------------------------------- host side
 
-// A matrix of `rows` rows of `inner` elements `stride` apart, in boxes of box_inner x box_rows.
-bool map_of(EncodeTiledFn enc, CUtensorMap* m, const void* p, bool bf16, int64_t inner,
-            int64_t rows, int64_t stride, int box_inner, int box_rows) {
-  const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)(rows > 1 ? stride : inner) * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows};
-  const cuuint32_t one[2] = {1, 1};
-  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-             const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+// A matrix of 16-bit elements in `planes` planes: rows of `cols` elements `stride` apart.
+struct Matrix {
+  const void* p;
+  int64_t rows, cols, stride, plane;
+};
+bool map_of(EncodeTiledFn enc, CUtensorMap* m, const Matrix& x, bool bf16, int planes,
+            int box_inner, int box_rows) {
+  auto bytes = [](int64_t stride, int64_t extent) {
+    return (cuuint64_t)(extent > 1 ? stride * 2 : 16);
+  };
+  const cuuint64_t dims[3] = {(cuuint64_t)x.cols, (cuuint64_t)x.rows, (cuuint64_t)planes};
+  const cuuint64_t strides[2] = {bytes(x.stride, x.rows), bytes(x.plane, planes)};
+  const cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_rows, 1};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+             const_cast<void*>(x.p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
              box_inner == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-struct Matrix {
-  const void* p;
-  int64_t rows, cols, stride;
-};
-
-template <int CG, bool AMN, bool BMN, int EPI>
+template <int CG, bool AMN, bool BMN, int EPI, bool F32>
 struct Builder {
   EncodeTiledFn enc = tensor_map_encoder();
   Job j{};
-  bool ok = enc != nullptr;
+  bool ok = enc != nullptr, bf16;
   static constexpr int kCols = EPI == kGated ? 64 * CG : 128 * CG;
 
   Builder(const fconv_mlp_desc& d, float* saved) {
@@ -577,6 +770,7 @@ struct Builder {
     j.act = d.activation;
     j.alpha = d.alpha;
     j.bf16 = d.dtype == FCONV_BF16;
+    bf16 = F32 || j.bf16;
   }
   // A new problem, D of M x N as sums over K.
   Problem& add(int64_t M, int64_t N, int64_t K) {
@@ -584,28 +778,37 @@ struct Builder {
     p.mt = (int)((M + 128 * CG - 1) / (128 * CG));
     p.nt = (int)((N + kCols - 1) / kCols);
     p.steps = (int)((K + kStep - 1) / kStep);
-    p.terms = 0;
     p.M = M;
     p.N = (int)N;
     j.tiles += p.mt * p.nt;
     return p;
   }
   void operand(CUtensorMap* m, const Matrix& x, bool mn, int rows) {
-    ok = ok && map_of(enc, m, x.p, j.bf16, x.cols, x.rows, x.stride, 64, mn ? 64 : rows);
+    ok = ok && map_of(enc, m, x, bf16, F32 ? kPlanes : 1, 64, mn ? 64 : rows);
   }
-  void term(Problem& p, const Matrix& a, const Matrix& b) {
-    operand(&p.a[p.terms], a, AMN, 128);
-    operand(&p.b[p.terms], b, BMN, EPI == kGated && CG == 1 ? 64 : 128);
-    ++p.terms;
+  void product(Problem& p, const Matrix& a, const Matrix& b) {
+    operand(&p.a[p.products], a, AMN, 128);
+    operand(&p.b[p.products], b, BMN, EPI == kGated && CG == 1 ? 64 : 128);
+    ++p.products;
   }
-  void output(Problem& p, int i, const Matrix& c) {
-    ok = ok && map_of(enc, &p.c[i], c.p, j.bf16, c.cols, c.rows, c.stride, 32, 128);
+  // An operand of a later product.
+  void inner(Problem& p, int i, const Matrix& c) {
+    ok = ok && map_of(enc, &p.c[i], c, bf16, F32 ? kPlanes : 1, 32, 128);
+  }
+  // A result of the call: by boxes where its rows start on 16 bytes.
+  void result(Problem& p, void* out, int64_t rows, int64_t cols, int64_t stride) {
+    if (!F32 && (uintptr_t)out % 16 == 0 && (rows <= 1 || stride % 8 == 0)) {
+      inner(p, 0, {out, rows, cols, stride, 0});
+    } else {
+      p.out = out;
+      p.out_row = stride;
+    }
   }
   int launch(int sms, cudaStream_t s) {
     if (!ok) return (int)cudaErrorInvalidValue;
     if (j.tiles == 0) return 0;
-    const size_t smem = kStages<EPI> * 2 * kSide + 2 * kSlots<EPI> * kSlot;
-    auto kernel = mlp_tc<CG, AMN, BMN, EPI>;
+    const size_t smem = kStages<EPI, F32> * 2 * kSide + 2 * kSlots<EPI, F32> * kSlot;
+    auto kernel = mlp_tc<CG, AMN, BMN, EPI, F32>;
     if (const int e = allow_smem((const void*)kernel, smem)) return e;
     const int most = sms / CG;
     cudaLaunchConfig_t cfg = {};
@@ -625,63 +828,71 @@ struct Builder {
   }
 };
 
+// What the products read: the call's tensors, or their copies in the workspace.
+struct Inputs {
+  Matrix x, gate, up, down, dy;
+  Matrix h, dg, du;
+};
+
 // h, and where `saved` is given the projections.
-template <int CG>
-int gated(const fconv_mlp_desc& d, int sms, const MlpArgs& a, void* h, cudaStream_t s) {
-  Builder<CG, false, false, kGated> b(d, a.saved);
+template <int CG, bool F32>
+int gated(const fconv_mlp_desc& d, int sms, const MlpArgs& a, const Inputs& in, cudaStream_t s) {
+  Builder<CG, false, false, kGated, F32> b(d, a.saved);
   Problem& p = b.add(d.tokens, d.hidden, d.features);
-  b.term(p, {a.x, d.tokens, d.features, d.x_stride}, {a.w_gate, d.hidden, d.features, d.gate_stride});
-  b.operand(&p.b[1], {a.w_up, d.hidden, d.features, d.up_stride}, false, CG == 1 ? 64 : 128);
+  b.product(p, in.x, in.gate);
+  b.operand(&p.b[1], in.up, false, CG == 1 ? 64 : 128);
   p.bias[0] = a.b_gate;
   p.bias[1] = a.b_up;
-  b.output(p, 0, {h, d.tokens, d.hidden, d.hidden});
+  b.inner(p, 0, in.h);
   return b.launch(sms, s);
 }
 
-template <int CG>
-int down(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s) {
-  Builder<CG, false, false, kPlain> b(d, nullptr);
+template <int CG, bool F32>
+int down(const fconv_mlp_desc& d, int sms, const MlpArgs& a, const Inputs& in, cudaStream_t s) {
+  Builder<CG, false, false, kPlain, F32> b(d, nullptr);
   Problem& p = b.add(d.tokens, d.out_features, d.hidden);
-  b.term(p, {a.h, d.tokens, d.hidden, d.hidden}, {a.w_down, d.out_features, d.hidden, d.down_stride});
+  b.product(p, in.h, in.down);
   p.bias[0] = a.b_down;
-  b.output(p, 0, {a.y, d.tokens, d.out_features, d.y_stride});
+  b.result(p, a.y, d.tokens, d.out_features, d.y_stride);
   return b.launch(sms, s);
 }
 
-template <int CG>
-int grads_of_projections(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s) {
-  Builder<CG, false, true, kGrad> b(d, a.saved);
+template <int CG, bool F32>
+int grads_of_projections(const fconv_mlp_desc& d, int sms, const MlpArgs& a, const Inputs& in,
+                         cudaStream_t s) {
+  Builder<CG, false, true, kGrad, F32> b(d, a.saved);
   Problem& p = b.add(d.tokens, d.hidden, d.out_features);
-  b.term(p, {a.dy, d.tokens, d.out_features, d.dy_stride},
-         {a.w_down, d.out_features, d.hidden, d.down_stride});
-  const void* out[3] = {a.dg, a.du, a.h};
-  for (int i = 0; i < 3; ++i) b.output(p, i, {out[i], d.tokens, d.hidden, d.hidden});
+  b.product(p, in.dy, in.down);
+  b.inner(p, 0, in.dg);
+  b.inner(p, 1, in.du);
+  b.inner(p, 2, in.h);
   return b.launch(sms, s);
 }
 
-template <int CG>
-int grad_of_input(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s) {
-  Builder<CG, false, true, kPlain> b(d, nullptr);
+template <int CG, bool F32>
+int grad_of_input(const fconv_mlp_desc& d, int sms, const MlpArgs& a, const Inputs& in,
+                  cudaStream_t s) {
+  Builder<CG, false, true, kPlain, F32> b(d, nullptr);
   Problem& p = b.add(d.tokens, d.features, d.hidden);
-  b.term(p, {a.dg, d.tokens, d.hidden, d.hidden}, {a.w_gate, d.hidden, d.features, d.gate_stride});
-  b.term(p, {a.du, d.tokens, d.hidden, d.hidden}, {a.w_up, d.hidden, d.features, d.up_stride});
-  b.output(p, 0, {a.dx, d.tokens, d.features, d.dx_stride});
+  b.product(p, in.dg, in.gate);
+  b.product(p, in.du, in.up);
+  b.result(p, a.dx, d.tokens, d.features, d.dx_stride);
   return b.launch(sms, s);
 }
 
-template <int CG>
-int grads_of_weights(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s) {
-  Builder<CG, true, true, kPlain> b(d, nullptr);
-  auto one = [&](const Matrix& g, const Matrix& in, void* out) {
+template <int CG, bool F32>
+int grads_of_weights(const fconv_mlp_desc& d, int sms, const MlpArgs& a, const Inputs& in,
+                     cudaStream_t s) {
+  Builder<CG, true, true, kPlain, F32> b(d, nullptr);
+  auto one = [&](const Matrix& g, const Matrix& x, void* out) {
     if (!out) return;
-    Problem& p = b.add(g.cols, in.cols, d.tokens);
-    b.term(p, g, in);
-    b.output(p, 0, {out, g.cols, in.cols, in.cols});
+    Problem& p = b.add(g.cols, x.cols, d.tokens);
+    b.product(p, g, x);
+    b.result(p, out, g.cols, x.cols, x.cols);
   };
-  const Matrix x = {a.x, d.tokens, d.features, d.x_stride};
-  one({a.dg, d.tokens, d.hidden, d.hidden}, x, a.dw_gate);
-  one({a.du, d.tokens, d.hidden, d.hidden}, x, a.dw_up);
-  one({a.dy, d.tokens, d.out_features, d.dy_stride}, {a.h, d.tokens, d.hidden, d.hidden}, a.dw_down);
+  one(in.dg, in.x, a.dw_gate);
+  one(in.du, in.x, a.dw_up);
+  one(in.dy, in.h, a.dw_down);
   return b.launch(sms, s);
 }
 
@@ -689,51 +900,120 @@ int grads_of_weights(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStr
 bool pairs_fill(int64_t M, int64_t N, int sms) {
   return ((M + 255) / 256) * ((N + 255) / 256) * 4 >= sms;
 }
+#define FCONV_BY_SIZE(pairs, call, ...)                               \
+  (d.dtype == FCONV_F32 ? call<1, true>(d, sms, a, __VA_ARGS__)       \
+   : (pairs)            ? call<2, false>(d, sms, a, __VA_ARGS__)      \
+                        : call<1, false>(d, sms, a, __VA_ARGS__))
 
-// g, u and h.
-int projections(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s) {
-  if (d.tokens <= kMlpFewTokens) return launch_mlp_few_gated(d, a, s);
-  return pairs_fill(d.tokens, 2 * d.hidden, sms) ? gated<2>(d, sms, a, a.h, s)
-                                                 : gated<1>(d, sms, a, a.h, s);
+int64_t whole8(int64_t n) { return (n + 7) / 8 * 8; }
+size_t whole256(size_t n) { return (n + 255) / 256 * 256; }
+
+// A tensor of the call that TMA does not take as it is: f32, rows that do not start on 16 bytes or
+// that overlap.
+bool needs_copy(const fconv_mlp_desc& d, int64_t rows, int64_t cols, int64_t stride) {
+  if (d.dtype == FCONV_F32) return true;
+  return rows > 1 && (stride % 8 != 0 || stride < cols || stride >= (1LL << 39));
+}
+
+// The workspace, and the operands in it or where the call has them. Copies come in `prep`.
+struct Layout {
+  size_t bytes = 0;
+  Inputs in{};
+  PrepArgs prep{};
+  float* sums = nullptr;
+};
+Layout layout(const fconv_mlp_desc& d, const MlpArgs& a, bool backward, int sms) {
+  Layout l;
+  const int planes = d.dtype == FCONV_F32 ? kPlanes : 1;
+  char* base = (char*)a.ws;
+  auto take = [&](size_t bytes) {
+    char* p = base + l.bytes;
+    l.bytes += whole256(bytes);
+    return p;
+  };
+  auto fresh = [&](int64_t rows, int64_t cols) {
+    Matrix m{nullptr, rows, cols, whole8(cols), 0};
+    m.plane = rows * m.stride;
+    m.p = take((size_t)m.plane * planes * 2);
+    return m;
+  };
+  auto input = [&](const void* p, int64_t rows, int64_t cols, int64_t stride) {
+    if (!needs_copy(d, rows, cols, stride)) return Matrix{p, rows, cols, stride, 0};
+    const Matrix m = fresh(rows, cols);
+    l.prep.m[l.prep.count++] = {p, const_cast<void*>(m.p), rows, cols, stride, m.stride, m.plane};
+    return m;
+  };
+  l.in.h = fresh(d.tokens, d.hidden);
+  const bool few = d.tokens <= kMlpFewTokens;
+  if (backward) {
+    l.in.dg = fresh(d.tokens, d.hidden);
+    l.in.du = fresh(d.tokens, d.hidden);
+    const int64_t cols[3] = {d.hidden, d.hidden, d.out_features};
+    l.sums = (float*)take(column_sums_workspace(cols, sms));
+    l.in.dy = input(a.dy, d.tokens, d.out_features, d.dy_stride);
+  } else if (few) {
+    return l;  // the weight-streaming kernels read everything where it is
+  }
+  l.in.x = input(a.x, d.tokens, d.features, d.x_stride);
+  l.in.gate = input(a.w_gate, d.hidden, d.features, d.gate_stride);
+  l.in.up = input(a.w_up, d.hidden, d.features, d.up_stride);
+  l.in.down = input(a.w_down, d.out_features, d.hidden, d.down_stride);
+  return l;
+}
+
+// g, u and (unless h is null: not wanted) h.
+int projections(const fconv_mlp_desc& d, int sms, const MlpArgs& a, const Inputs& in, bool want_h,
+                cudaStream_t s) {
+  if (d.tokens <= kMlpFewTokens)
+    return launch_mlp_few_gated(d, a, want_h ? const_cast<void*>(in.h.p) : nullptr, in.h.stride, s);
+  return FCONV_BY_SIZE(pairs_fill(d.tokens, 2 * d.hidden, sms), gated, in, s);
 }
 
 }  // namespace
 
-bool mlp_tc_supported(const fconv_mlp_desc& d) {
-  if (d.dtype == FCONV_F32) return false;
-  auto whole = [](int64_t rows, int64_t cols, int64_t stride) {
-    if (cols % 8 != 0) return false;
-    return rows <= 1 || (stride % 8 == 0 && stride >= cols && stride < (1LL << 39));
+bool mlp_tc_supported(const fconv_mlp_desc& d, const MlpArgs& a, bool backward) {
+  if (d.tokens == 0) return false;
+  auto there = [&](const void* p, int64_t rows, int64_t cols, int64_t stride) {
+    return (uintptr_t)p % 16 == 0 || needs_copy(d, rows, cols, stride);
   };
-  if (!whole(d.tokens, d.features, d.x_stride) || !whole(d.tokens, d.out_features, d.y_stride) ||
-      !whole(d.hidden, d.features, d.gate_stride) || !whole(d.hidden, d.features, d.up_stride) ||
-      !whole(d.out_features, d.hidden, d.down_stride) || d.hidden % 8 != 0)
-    return false;
-  return !d.training || (whole(d.tokens, d.out_features, d.dy_stride) &&
-                         whole(d.tokens, d.features, d.dx_stride));
+  if (!backward && d.tokens <= kMlpFewTokens) return true;
+  return there(a.x, d.tokens, d.features, d.x_stride) &&
+         there(a.w_gate, d.hidden, d.features, d.gate_stride) &&
+         there(a.w_up, d.hidden, d.features, d.up_stride) &&
+         there(a.w_down, d.out_features, d.hidden, d.down_stride) &&
+         (!backward || there(a.dy, d.tokens, d.out_features, d.dy_stride));
+}
+
+size_t mlp_tc_workspace(const fconv_mlp_desc& d, bool backward, int sms) {
+  return layout(d, MlpArgs{}, backward, sms).bytes;
 }
 
 int launch_mlp_tc_forward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s) {
-  if (const int e = projections(d, sms, a, s)) return e;
-  if (d.tokens <= kMlpFewTokens) return launch_mlp_few_down(d, a, s);
-  return pairs_fill(d.tokens, d.out_features, sms) ? down<2>(d, sms, a, s) : down<1>(d, sms, a, s);
+  const Layout l = layout(d, a, false, sms);
+  int e = launch_mlp_prep(d.dtype, l.prep, s);
+  if (!e) e = projections(d, sms, a, l.in, true, s);
+  if (e) return e;
+  if (d.tokens <= kMlpFewTokens) return launch_mlp_few_down(d, a, l.in.h.p, l.in.h.stride, s);
+  return FCONV_BY_SIZE(pairs_fill(d.tokens, d.out_features, sms), down, l.in, s);
 }
 
 int launch_mlp_tc_backward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s) {
   const int64_t T = d.tokens;
-  // made again, the projections are the forward pass's bit by bit (h, too, is written again)
-  int e = a.remake ? projections(d, sms, a, s) : 0;
-  if (!e)
-    e = pairs_fill(T, d.hidden, sms) ? grads_of_projections<2>(d, sms, a, s)
-                                     : grads_of_projections<1>(d, sms, a, s);
-  if (!e && a.dx)
-    e = pairs_fill(T, d.features, sms) ? grad_of_input<2>(d, sms, a, s)
-                                       : grad_of_input<1>(d, sms, a, s);
+  const Layout l = layout(d, a, true, sms);
+  int e = launch_mlp_prep(d.dtype, l.prep, s);
+  // made again, the projections are the forward pass's bit by bit
+  if (!e && a.remake) e = projections(d, sms, a, l.in, false, s);
+  if (!e) e = FCONV_BY_SIZE(pairs_fill(T, d.hidden, sms), grads_of_projections, l.in, s);
+  if (!e && a.dx) e = FCONV_BY_SIZE(pairs_fill(T, d.features, sms), grad_of_input, l.in, s);
   if (!e && (a.dw_gate || a.dw_up || a.dw_down))
-    e = pairs_fill(2 * d.hidden + d.out_features, d.features, sms)
-            ? grads_of_weights<2>(d, sms, a, s)
-            : grads_of_weights<1>(d, sms, a, s);
-  return e;
+    e = FCONV_BY_SIZE(pairs_fill(2 * d.hidden + d.out_features, d.features, sms), grads_of_weights,
+                      l.in, s);
+  if (e) return e;
+  const Matrix* from[3] = {&l.in.dg, &l.in.du, &l.in.dy};
+  void* to[3] = {a.db_gate, a.db_up, a.db_down};
+  SumsArgs m[3];
+  for (int i = 0; i < 3; ++i) m[i] = {from[i]->p, from[i]->stride, from[i]->cols, from[i]->plane, to[i]};
+  return launch_column_sums(d.dtype, d.dtype == FCONV_F32, m, T, l.sums, sms, s);
 }
 
 int read_and_clear_mlp_error(cudaStream_t s, unsigned* value) {

@@ -77,34 +77,53 @@ struct MlpArgs {
   void* dw_gate;
   void* dw_up;
   void* dw_down;
+  void* db_gate;
+  void* db_up;
+  void* db_down;
   float* saved;  // g and u, or null
   bool remake;   // backward: make g and u first
-  void* h;       // in the workspace, rows of `hidden` values, as are dg and du
-  void* dg;
-  void* du;
+  void* ws;
 };
 size_t mlp_saved_bytes(const fconv_mlp_desc& d);
+size_t mlp_simple_workspace(const fconv_mlp_desc& d, bool backward, int sms);
 int launch_mlp_simple_forward(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s);
-int launch_mlp_simple_backward(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s);
-// Tensor-core route (k_mlp_tc.cu): addresses must be 16-byte aligned, tokens > 0.
-bool mlp_tc_supported(const fconv_mlp_desc& d);
+int launch_mlp_simple_backward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s);
+// Tensor-core route (k_mlp_tc.cu): whether it takes the addresses of a call, its workspace.
+bool mlp_tc_supported(const fconv_mlp_desc& d, const MlpArgs& a, bool backward);
+size_t mlp_tc_workspace(const fconv_mlp_desc& d, bool backward, int sms);
 int launch_mlp_tc_forward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s);
 int launch_mlp_tc_backward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s);
-// Up to kMlpFewTokens tokens of what the tensor-core route takes (k_mlp_few.cu).
-constexpr int kMlpFewTokens = 32;
-int launch_mlp_few_gated(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s);
-int launch_mlp_few_down(const fconv_mlp_desc& d, const MlpArgs& a, cudaStream_t s);
 int read_and_clear_mlp_error(cudaStream_t s, unsigned* value);
+// Its products for up to kMlpFewTokens tokens (k_mlp_few.cu); h has rows of h_row elements of the
+// call's type (gated: may be null).
+constexpr int kMlpFewTokens = 32;
+int launch_mlp_few_gated(const fconv_mlp_desc& d, const MlpArgs& a, void* h, int64_t h_row,
+                         cudaStream_t s);
+int launch_mlp_few_down(const fconv_mlp_desc& d, const MlpArgs& a, const void* h, int64_t h_row,
+                        cudaStream_t s);
 
-// Column sums of up to three matrices with the same rows (those without `out` are left out).
+// Tensors copied into rows of whole 16-byte units, f32 as three bf16 planes (k_mlp_prep.cu).
+struct PrepItem {
+  const void* src;
+  void* dst;
+  int64_t rows, cols, src_row, dst_row, plane;  // elements
+};
+struct PrepArgs {
+  PrepItem m[5];
+  int count;
+};
+int launch_mlp_prep(int dtype, const PrepArgs& a, cudaStream_t s);
+
+// Column sums of up to three matrices with the same rows (those without `out` are left out), of
+// dtype or, with `planes`, of f32 as three bf16 planes.
 struct SumsArgs {
   const void* p;
-  int64_t row, cols;  // stride of the rows in elements
+  int64_t row, cols, plane;  // strides of rows and planes in elements
   void* out;
 };
 size_t column_sums_workspace(const int64_t cols[3], int sms);
-int launch_column_sums(int dtype, const SumsArgs m[3], int64_t rows, float* part, int sms,
-                       cudaStream_t s);
+int launch_column_sums(int dtype, bool planes, const SumsArgs m[3], int64_t rows, float* part,
+                       int sms, cudaStream_t s);
 
 struct AttnArgs {
   const void* q;

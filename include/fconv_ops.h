@@ -215,9 +215,11 @@ void fconv_attn_destroy(fconv_attn_plan* plan);
  * up may be halves of one packed weight. Biases are contiguous, each optional, and of dtype.
  * act is one of FCONV_ACT_NONE, RELU, SIGMOID, GELU (erf), FASTGELU (tanh) and QUICKGELU
  * (v * sigmoid(alpha v); alpha = 1 is SiLU). With no tokens the weights' gradients are zero.
- * g and u are f32; h, and in the backward pass the gradients of g and u, are rounded to dtype
- * once as operands of the next product: in f16 they overflow past 65504 and lose bits under 6e-5.
- * The 16-bit outputs are off by about 1.4 times their own rounding. */
+ * g and u are f32; in f16 and bf16 h, and in the backward pass the gradients of g and u, are rounded
+ * to dtype once as operands of the next product: in f16 they overflow past 65504 and lose bits under
+ * 6e-5. The 16-bit outputs are off by about 1.4 times their own rounding. In f32 nothing is rounded
+ * to fewer bits (operands are split into parts that add up to them), but that an infinity may come
+ * out as NaN. */
 typedef struct {
   int dtype;
   int64_t tokens, features, hidden, out_features;
@@ -230,17 +232,19 @@ typedef struct {
 } fconv_mlp_desc;
 typedef enum {
   FCONV_MLP_AUTO = 0,
-  FCONV_MLP_SIMPLE = 1, /* every type, size and stride: warp-level tensor instructions */
-  FCONV_MLP_TC = 2      /* tcgen05 tensor cores: f16 and bf16, sizes and strides multiples of 8,
-                           16-byte addresses */
+  FCONV_MLP_SIMPLE = 1, /* one warp-level kernel for every call */
+  FCONV_MLP_TC = 2      /* tcgen05 tensor cores, and a kernel that streams the weights for the
+                           forward pass of up to 32 tokens. f32, and tensors whose rows do not
+                           start on 16 bytes, are copied into the workspace first. */
 } fconv_mlp_route;
 typedef struct fconv_mlp_plan fconv_mlp_plan;
 
 /* route: FCONV_MLP_AUTO, or one that must run the request (else FCONV_E_UNSUPPORTED). */
 fconv_status fconv_mlp_plan_create(const fconv_mlp_desc* desc, int device, int route,
                                    fconv_mlp_plan** out);
-/* The route of a call whose device addresses are 16-byte aligned (a call with others runs on
- * FCONV_MLP_SIMPLE, unless the plan was made for FCONV_MLP_TC: then FCONV_E_ALIGNMENT). */
+/* The route of a call with tokens whose device addresses are 16-byte aligned. One with others runs
+ * on FCONV_MLP_SIMPLE if TMA had to read them where they are, unless the plan was made for
+ * FCONV_MLP_TC: then FCONV_E_ALIGNMENT. */
 fconv_status fconv_mlp_plan_route(const fconv_mlp_plan* plan, int* route);
 fconv_status fconv_mlp_forward_workspace(const fconv_mlp_plan* plan, size_t* bytes);
 fconv_status fconv_mlp_backward_workspace(const fconv_mlp_plan* plan, size_t* bytes);

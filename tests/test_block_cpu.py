@@ -206,7 +206,8 @@ def test_mlp_refusals():
     assert code(mlp, training=True, dx_stride=63) == "E_STRIDE"
     assert code(mlp, training=True, dy_stride=-8) == "E_STRIDE"
     assert code(mlp, n=1 << 29, f=1 << 20) == "E_UNSUPPORTED"
-    assert code(mlp, F32, route="tc") == "E_UNSUPPORTED"
+    for dtype in (F32, F16, BF16):
+        assert mlp(dtype).route == "tc" and mlp(dtype, route="simple").route == "simple"
 
 
 def test_mlp_call_refusals():
@@ -227,6 +228,8 @@ def test_mlp_call_refusals():
     assert run(ws=None) == "E_WORKSPACE" and run(nbytes=p.forward_workspace - 1) == "E_WORKSPACE"
     for i, name in enumerate(("has_b_gate", "has_b_up", "has_b_down")):
         assert run(plan=mlp(**{name: False})) == "E_BIAS_SHAPE"
+    many = mlp(n=100, route="tc")  # TMA would read x where it is
+    assert run(plan=many, x=ok["x"] + 2) == "E_ALIGNMENT"
     empty = dict(ok, x=None, y=None, ws=None)
     mlp(n=0).forward_ptrs(*empty.values(), 0, None)
 
