@@ -41,27 +41,24 @@ struct Few {
   float alpha;
 };
 
-// 16 bytes of a row from element k on, zeros past K.
+// 16 bytes of a row from element k on where `in` (WIDE: a row has no rest), zeros past K.
 template <typename T, bool WIDE, bool WEIGHT>
-__device__ __forceinline__ uint4 load_row(const T* p, int k, int K) {
-  uint4 v = make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ uint4 load_row(const T* p, int k, int K, bool in) {
   if constexpr (WIDE) {
-    if (k < K) {
-      if (WEIGHT)
-        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "l"(p + k));
-      else
-        v = *reinterpret_cast<const uint4*>(p + k);
-    }
+    if (!in) return make_uint4(0, 0, 0, 0);
+    if (!WEIGHT) return *reinterpret_cast<const uint4*>(p + k);
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p + k));
+    return v;
   } else {
     constexpr int E = 16 / sizeof(T);
     Vec<T, E> e;
 #pragma unroll
-    for (int i = 0; i < E; ++i) e.v[i] = k + i < K ? p[k + i] : from_f<T>(0.0f);
-    v = *reinterpret_cast<const uint4*>(&e);
+    for (int i = 0; i < E; ++i) e.v[i] = in && k + i < K ? p[k + i] : from_f<T>(0.0f);
+    return *reinterpret_cast<const uint4*>(&e);
   }
-  return v;
 }
 
 template <typename T>
@@ -154,13 +151,14 @@ __global__ void __launch_bounds__(kThreads, 2) mlp_few(const __grid_constant__ F
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = k0 + u * kStep + t * kElems;
+      const bool in = k < q.K;
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) w[u][m][i] = load_row<T, WIDE, true>(wp[m][i], k, q.K);
+        for (int i = 0; i < 2; ++i) w[u][m][i] = load_row<T, WIDE, true>(wp[m][i], k, q.K, in);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        x[u][n] = load_row<T, WIDE, false>(xp[n], there[n] ? k : q.K, q.K);
+        x[u][n] = load_row<T, WIDE, false>(xp[n], k, q.K, in && there[n]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)

@@ -15,7 +15,9 @@
 // SM (CG 1) are for calls with too few of the others. Per block: a load warp keeps a ring of
 // 32 KB stages full, an MMA warp issues, eight warps empty one accumulator while the next tile's
 // products fill the other. Blocks are persistent and take tiles in groups of 8 rows of tiles, so
-// that blocks at work at one time share operands in L2.
+// that blocks at work at one time share operands in L2. Where one-SM tiles are few, a cluster of
+// blocks shares a tile (SPLIT): each takes a part of K, leaves its sums in shared memory and finishes
+// some of the columns, adding the blocks' parts in their order.
 //
 // f32 (F32) comes as three bf16 planes that add up to it (k_mlp_prep.cu; h, dg and du are split in
 // the epilogues). Six products of planes, the smallest first, leave out less than 2^-23 of a
@@ -64,6 +66,7 @@ struct Problem {
 struct Job {
   Problem p[3];
   int problems, tiles;
+  int splits;  // blocks of a tile, SPLIT
   float* saved;
   int64_t quads;
   float alpha;
@@ -89,6 +92,19 @@ __device__ __forceinline__ uint32_t in_first(uint32_t addr) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
   return r;
+}
+__device__ __forceinline__ uint32_t in_block(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 load_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
@@ -234,40 +250,36 @@ __device__ __forceinline__ Tile tile_of(const Job& j, int id) {
   return t;
 }
 
-// The steps of a tile in passes, each into an accumulator of its own: one for 16-bit types; for f32
-// one for every kChunk steps of a product, six terms each.
-struct Passes {
-  int chunks, count;
+// The steps [lo, hi) of a tile's products that a block takes, product by product.
+struct Range {
+  int lo, hi;
 };
-template <bool F32>
-__device__ __forceinline__ Passes passes_of(const Problem& p, int products) {
-  Passes v;
-  v.chunks = F32 ? (p.steps + kChunk - 1) / kChunk : 1;
-  v.count = F32 ? products * v.chunks : 1;
-  return v;
+__device__ __forceinline__ Range range_of(const Problem& p, int products, int rank, int splits) {
+  const int all = products * p.steps;
+  Range r;
+  r.lo = (int)((int64_t)all * rank / splits);
+  r.hi = (int)((int64_t)all * (rank + 1) / splits);
+  return r;
 }
+// They come in passes, each into an accumulator of its own: one for 16-bit types, for f32 one for
+// every kChunk steps (of one product), six terms each.
 template <bool F32>
-__device__ __forceinline__ int steps_of(const Problem& p, int products, const Passes& v, int pass) {
-  if (!F32) return products * p.steps;
-  return kTerms * min(kChunk, p.steps - pass % v.chunks * kChunk);
+__device__ __forceinline__ int pass_steps(const Problem& p, const Range& r, int at) {
+  if (!F32) return r.hi - at;
+  return min(min(kChunk, r.hi - at), p.steps - at % p.steps);
 }
 struct Step {
   int product, k, a_plane, b_plane;
 };
+// Load i of the pass of `len` steps from step `at` on.
 template <bool F32>
-__device__ __forceinline__ Step step_of(const Problem& p, const Passes& v, int pass, int i) {
+__device__ __forceinline__ Step step_of(const Problem& p, int at, int len, int i) {
+  const int term = F32 ? i / len : 0, g = at + i - term * len;
   Step s;
-  if (!F32) {
-    s.product = i >= p.steps;
-    s.k = i - s.product * p.steps;
-    s.a_plane = s.b_plane = 0;
-  } else {
-    s.product = pass / v.chunks;
-    const int c0 = pass % v.chunks * kChunk, len = min(kChunk, p.steps - c0), term = i / len;
-    s.k = c0 + i - term * len;
-    s.a_plane = (0x001102 >> (4 * term)) & 3;  // 2 0 1 1 0 0
-    s.b_plane = (0x010120 >> (4 * term)) & 3;  // 0 2 1 0 1 0
-  }
+  s.product = g >= p.steps;
+  s.k = g - s.product * p.steps;
+  s.a_plane = F32 ? (0x001102 >> (4 * term)) & 3 : 0;  // 2 0 1 1 0 0
+  s.b_plane = F32 ? (0x010120 >> (4 * term)) & 3 : 0;  // 0 2 1 0 1 0
   return s;
 }
 
@@ -381,7 +393,7 @@ __device__ __forceinline__ void gate_grad(uint32_t (&wg)[4], uint32_t (&wu)[4], 
   }
 }
 
-template <int CG, bool AMN, bool BMN, int EPI, bool F32>
+template <int CG, bool AMN, bool BMN, int EPI, bool F32, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Job j) {
   constexpr int S = kStages<EPI, F32>, BN = 128 * CG;
   constexpr int kCols = EPI == kGated ? BN / 2 : BN;  // of a tile of D
@@ -395,6 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
   }
   const int warp = uni((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
   const uint32_t rank = CG == 1 ? 0 : block_rank();
+  const int splits = SPLIT ? j.splits : 1, part = SPLIT ? (int)block_rank() : 0;
   volatile int* abort_flag = &ctl.abort_flag;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
@@ -409,6 +422,12 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
     ctl.abort_flag = 0;
     ptx::fence_mbar_init();
   }
+  if (threadIdx.x == 32) {
+    const Problem& p = j.p[0];
+    ptx::prefetch_tmap(&p.a[0]);
+    ptx::prefetch_tmap(&p.b[0]);
+    if (EPI == kGated) ptx::prefetch_tmap(&p.b[1]);
+  }
   if (warp == 2) tmem_take<CG>(ptx::smem_addr(&ctl.tmem), 2 * BN);
   ptx::tc_fence_before();
   __syncthreads();
@@ -417,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
   const uint32_t tmem = ctl.tmem;
   ptx::pdl_wait();
   ptx::pdl_trigger();
-  const int first = (int)blockIdx.x / CG, stride = (int)gridDim.x / CG;
+  const int first = (int)blockIdx.x / (CG * splits), stride = (int)gridDim.x / (CG * splits);
 
   if (warp == 0) {  // loads
     int it = 0;
@@ -427,12 +446,12 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
       const Problem& p = j.p[t.which];
       const int m0 = (t.m * CG + (int)rank) * 128;
       const int n0 = EPI == kGated ? t.n * kCols : t.n * BN + (int)rank * 128;
-      const int products = EPI == kGated ? 1 : p.products;
-      const Passes v = passes_of<F32>(p, products);
-      for (int pass = 0; ok && pass < v.count; ++pass) {
-        const int steps = steps_of<F32>(p, products, v, pass);
+      const Range r = range_of(p, EPI == kGated ? 1 : p.products, part, splits);
+      for (int at = r.lo, len; ok && at < r.hi; at += len) {
+        len = pass_steps<F32>(p, r, at);
+        const int steps = len * (F32 ? kTerms : 1);
         for (int i = 0; i < steps; ++i, ++it) {
-          const Step st = step_of<F32>(p, v, pass, i);
+          const Step st = step_of<F32>(p, at, len, i);
           const int s = it % S;
           ok = all_lanes(wait_bar(ptx::smem_addr(&ctl.empty[s]), ((it / S) & 1) ^ 1, abort_flag));
           if (!ok) break;
@@ -482,10 +501,10 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
       for (int id = first; ok && id < j.tiles; id += stride) {
         const Tile t = tile_of(j, id);
         const Problem& p = j.p[t.which];
-        const int products = EPI == kGated ? 1 : p.products;
-        const Passes v = passes_of<F32>(p, products);
-        for (int pass = 0; ok && pass < v.count; ++pass, ++n) {
-          const int steps = steps_of<F32>(p, products, v, pass);
+        const Range r = range_of(p, EPI == kGated ? 1 : p.products, part, splits);
+        for (int at = r.lo, len; ok && at < r.hi; at += len, ++n) {
+          len = pass_steps<F32>(p, r, at);
+          const int steps = len * (F32 ? kTerms : 1);
           const uint32_t d = tmem + (n & 1) * BN;
           ok = all_lanes(wait_cluster(ptx::smem_addr(&ctl.acc_empty[n & 1]), ((n >> 1) & 1) ^ 1,
                                       abort_flag));
@@ -525,6 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
     const int act = j.act;
     const float alpha = j.alpha;
     constexpr int kParts = kCols / 64;  // 32-column parts of a warp's half of the tile
+    constexpr int kUps = EPI == kGated ? kParts : 1;
     int n = 0, slot = 0;
     bool ok = true;
     for (int id = first; ok && id < j.tiles; id += stride) {
@@ -576,9 +596,9 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
           bulk_commit();
         }
       };
-      // 32 columns from `col` on; x (and with kGated u) are sums of products.
+      // 32 columns of the tile; x (and with kGated u) are sums of products.
       auto finish = [&](int c, float (&x)[32], float (&u)[32]) {
-        const int col = t.n * kCols + half * (kCols / 2) + c * 32;
+        const int col = t.n * kCols + c * 32;
         if (col >= p.N) return;  // the same for the whole group
         if (EPI == kPlain) {
           add_bias<F32>(x, p.bias[0], col, p.N, bf16, lane);
@@ -690,26 +710,79 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
         }
       };
 
-      if constexpr (F32) {
-        float x[kParts][32], u[EPI == kGated ? kParts : 1][32];
-        const Passes v = passes_of<F32>(p, EPI == kGated ? 1 : p.products);
-        for (int pass = 0; pass < v.count; ++pass, ++n) {
-          if (!arrive()) break;
+      // All sums of this warp's part of the tile.
+      auto collect = [&](float (&x)[kParts][32], float (&u)[kUps][32]) {
+        const Range r = range_of(p, EPI == kGated ? 1 : p.products, part, splits);
+        for (int at = r.lo; at < r.hi; at += pass_steps<F32>(p, r, at), ++n) {
+          if (!arrive()) return;
 #pragma unroll
           for (int c = 0; c < kParts; ++c) {
             uint32_t r0[32], r1[32];
             fetch(c, r0, r1);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              x[c][i] = (pass ? x[c][i] : 0.0f) + __uint_as_float(r0[i]);
-              if (EPI == kGated) u[c][i] = (pass ? u[c][i] : 0.0f) + __uint_as_float(r1[i]);
+              x[c][i] = (at > r.lo ? x[c][i] : 0.0f) + __uint_as_float(r0[i]);
+              if (EPI == kGated) u[c][i] = (at > r.lo ? u[c][i] : 0.0f) + __uint_as_float(r1[i]);
             }
           }
           release();
         }
+      };
+
+      if constexpr (SPLIT) {
+        // columns c of 32 of the tile: rows of 16 bytes, a row a lane, 128 rows after each other
+        auto sums_at = [&](int c, int which) {
+          return (uint32_t)((c * (EPI == kGated ? 2 : 1) + which) * 128 * 32 * 4 + row * 16);
+        };
+        {
+          float x[kParts][32], u[kUps][32];
+          collect(x, u);
+          if (ok) {  // the ring is free: nothing more is loaded, and what was has been read
+#pragma unroll
+            for (int c = 0; c < kParts; ++c)
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const uint32_t to = ring + sums_at(half * kParts + c, 0) + i * 512;
+                ptx::st_shared_v4(to, __float_as_uint(x[c][i]), __float_as_uint(x[c][i + 1]),
+                                  __float_as_uint(x[c][i + 2]), __float_as_uint(x[c][i + 3]));
+                if (EPI == kGated) {
+                  const uint32_t at = ring + sums_at(half * kParts + c, 1) + i * 512;
+                  ptx::st_shared_v4(at, __float_as_uint(u[c][i]), __float_as_uint(u[c][i + 1]),
+                                    __float_as_uint(u[c][i + 2]), __float_as_uint(u[c][i + 3]));
+                }
+              }
+          }
+        }
+        __syncwarp();
+        cluster_sync();  // with the other warps, below
+        // columns c go to block c % splits, there to group c / splits
+        const int c = half * splits + part;
+        if (ok && c < 2 * kParts && part < splits) {
+          float x[32], u[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = u[i] = 0.0f;
+          for (int b = 0; b < splits; ++b) {
+            const uint32_t from = in_block(ring, b);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 v = load_cluster(from + sums_at(c, 0) + i * 512);
+              x[i] += v.x, x[i + 1] += v.y, x[i + 2] += v.z, x[i + 3] += v.w;
+              if (EPI == kGated) {
+                const float4 w = load_cluster(from + sums_at(c, 1) + i * 512);
+                u[i] += w.x, u[i + 1] += w.y, u[i + 2] += w.z, u[i + 3] += w.w;
+              }
+            }
+          }
+          finish(c, x, u);
+        }
+        break;  // one tile
+      } else if constexpr (F32) {
+        float x[kParts][32], u[kUps][32];
+        collect(x, u);
         if (!ok) break;
 #pragma unroll
-        for (int c = 0; c < kParts; ++c) finish(c, x[c], u[EPI == kGated ? c : 0]);
+        for (int c = 0; c < kParts; ++c)
+          finish(half * kParts + c, x[c], u[EPI == kGated ? c : 0]);
       } else {
         if (!arrive()) break;
 #pragma unroll 1
@@ -720,16 +793,21 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
           if (c + 1 == kParts) release();
           as_floats(x, r0);
           if (EPI == kGated) as_floats(u, r1);
-          finish(c, x, u);
+          finish(half * kParts + c, x, u);
         }
         ++n;
       }
     }
     if (issues) bulk_wait_all();
   }
+  if (SPLIT && warp < kFirstEpiWarp) {  // the sums of all blocks are in shared memory
+    __syncwarp();
+    cluster_sync();
+  }
   __syncthreads();
   ptx::tc_fence_before();
-  if (CG == 2) cluster_sync();  // nothing of the other block is on its way here any more
+  // nothing of the other blocks is on its way here any more, and they have read what they need
+  if (CG == 2 || SPLIT) cluster_sync();
   ptx::tc_fence_after();
   if (warp == 2) tmem_give<CG>(tmem, 2 * BN);
 }
@@ -756,6 +834,11 @@ bool map_of(EncodeTiledFn enc, CUtensorMap* m, const Matrix& x, bool bf16, int p
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+// Blocks of a call: pairs of SMs (CG 2), single ones, or clusters of `splits` for each tile.
+struct Shape {
+  int cg, splits;
+};
 
 template <int CG, bool AMN, bool BMN, int EPI, bool F32>
 struct Builder {
@@ -804,15 +887,23 @@ struct Builder {
       p.out_row = stride;
     }
   }
-  int launch(int sms, cudaStream_t s) {
+  int launch(int sms, int splits, cudaStream_t s) {
     if (!ok) return (int)cudaErrorInvalidValue;
     if (j.tiles == 0) return 0;
-    const size_t smem = kStages<EPI, F32> * 2 * kSide + 2 * kSlots<EPI, F32> * kSlot;
-    auto kernel = mlp_tc<CG, AMN, BMN, EPI, F32>;
-    if (const int e = allow_smem((const void*)kernel, smem)) return e;
+    j.splits = splits;
+    if constexpr (CG == 1) {
+      if (splits > 1) return start<true>(j.tiles * splits, splits, s);
+    }
     const int most = sms / CG;
+    return start<false>((j.tiles < most ? j.tiles : most) * CG, CG, s);
+  }
+  template <bool SPLIT>
+  int start(int blocks, int cluster, cudaStream_t s) {
+    const size_t smem = kStages<EPI, F32> * 2 * kSide + 2 * kSlots<EPI, F32> * kSlot;
+    auto kernel = mlp_tc<CG, AMN, BMN, EPI, F32, SPLIT>;
+    if (const int e = allow_smem((const void*)kernel, smem)) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((j.tiles < most ? j.tiles : most) * CG));
+    cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -820,10 +911,10 @@ struct Builder {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG == 2 ? 2 : 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return (int)cudaLaunchKernelEx(&cfg, kernel, j);
   }
 };
@@ -836,7 +927,7 @@ struct Inputs {
 
 // h, and where `saved` is given the projections.
 template <int CG, bool F32>
-int gated(const fconv_mlp_desc& d, int sms, const MlpArgs& a, const Inputs& in, cudaStream_t s) {
+int gated(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const Inputs& in, cudaStream_t s) {
   Builder<CG, false, false, kGated, F32> b(d, a.saved);
   Problem& p = b.add(d.tokens, d.hidden, d.features);
   b.product(p, in.x, in.gate);
@@ -844,21 +935,21 @@ int gated(const fconv_mlp_desc& d, int sms, const MlpArgs& a, const Inputs& in, 
   p.bias[0] = a.b_gate;
   p.bias[1] = a.b_up;
   b.inner(p, 0, in.h);
-  return b.launch(sms, s);
+  return b.launch(sms, splits, s);
 }
 
 template <int CG, bool F32>
-int down(const fconv_mlp_desc& d, int sms, const MlpArgs& a, const Inputs& in, cudaStream_t s) {
+int down(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const Inputs& in, cudaStream_t s) {
   Builder<CG, false, false, kPlain, F32> b(d, nullptr);
   Problem& p = b.add(d.tokens, d.out_features, d.hidden);
   b.product(p, in.h, in.down);
   p.bias[0] = a.b_down;
   b.result(p, a.y, d.tokens, d.out_features, d.y_stride);
-  return b.launch(sms, s);
+  return b.launch(sms, splits, s);
 }
 
 template <int CG, bool F32>
-int grads_of_projections(const fconv_mlp_desc& d, int sms, const MlpArgs& a, const Inputs& in,
+int grads_of_projections(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const Inputs& in,
                          cudaStream_t s) {
   Builder<CG, false, true, kGrad, F32> b(d, a.saved);
   Problem& p = b.add(d.tokens, d.hidden, d.out_features);
@@ -866,22 +957,22 @@ int grads_of_projections(const fconv_mlp_desc& d, int sms, const MlpArgs& a, con
   b.inner(p, 0, in.dg);
   b.inner(p, 1, in.du);
   b.inner(p, 2, in.h);
-  return b.launch(sms, s);
+  return b.launch(sms, splits, s);
 }
 
 template <int CG, bool F32>
-int grad_of_input(const fconv_mlp_desc& d, int sms, const MlpArgs& a, const Inputs& in,
+int grad_of_input(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const Inputs& in,
                   cudaStream_t s) {
   Builder<CG, false, true, kPlain, F32> b(d, nullptr);
   Problem& p = b.add(d.tokens, d.features, d.hidden);
   b.product(p, in.dg, in.gate);
   b.product(p, in.du, in.up);
   b.result(p, a.dx, d.tokens, d.features, d.dx_stride);
-  return b.launch(sms, s);
+  return b.launch(sms, splits, s);
 }
 
 template <int CG, bool F32>
-int grads_of_weights(const fconv_mlp_desc& d, int sms, const MlpArgs& a, const Inputs& in,
+int grads_of_weights(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const Inputs& in,
                      cudaStream_t s) {
   Builder<CG, true, true, kPlain, F32> b(d, nullptr);
   auto one = [&](const Matrix& g, const Matrix& x, void* out) {
@@ -893,17 +984,46 @@ int grads_of_weights(const fconv_mlp_desc& d, int sms, const MlpArgs& a, const I
   one(in.dg, in.x, a.dw_gate);
   one(in.du, in.x, a.dw_up);
   one(in.dy, in.h, a.dw_down);
-  return b.launch(sms, s);
+  return b.launch(sms, splits, s);
 }
 
-// Pairs of SMs where their tiles of 256 x (256, gated: 128) fill half of the GPU at least.
-bool pairs_fill(int64_t M, int64_t N, int sms) {
-  return ((M + 255) / 256) * ((N + 255) / 256) * 4 >= sms;
+// The blocks of a product of M x N (in columns of accumulators: gated ones have two for each of
+// D) with `steps` steps of K, or of several with their tiles together: what takes the least time,
+// counted in steps of a single SM's tile (0.19 us where operands come from HBM). A step of a pair of
+// SMs takes 1.2 of them, a round of tiles 4 to 6 more, a cluster's start and its exchange of sums 12
+// to 24 (196 tokens, 2048 to 768: 13.7 us with 12 blocks, 12.2, 10.9 and 12.0 with 2, 4 and 8 times
+// as many; 768 to 2048 in 64 tiles: 9.9 and 11.4). Clusters of 4 and 8 leave SMs of a GPC unused.
+Shape shape_of(const fconv_mlp_desc& d, int64_t tiles1, int64_t tiles2, int64_t steps, int sms) {
+  constexpr double kRound = 4.0, kSplitRound = 6.0, kPair = 1.2, kGain = 0.93;
+  const double terms = d.dtype == FCONV_F32 ? kTerms : 1;
+  auto rounds = [](int64_t tiles, int64_t slots) { return (double)((tiles + slots - 1) / slots); };
+  Shape best{1, 1};
+  double least = rounds(tiles1, sms) * (kRound + terms * steps);
+  for (int splits = 2; splits <= 8; splits *= 2) {
+    const int64_t slots = sms / splits - (splits == 8 ? 3 : splits == 4 ? 2 : 0);
+    if (slots < 1 || steps < 2 * splits || tiles1 * splits > (1 << 30)) break;
+    const double each = kSplitRound + terms * ((steps + splits - 1) / splits);
+    const double cost = 8 + 2 * splits + rounds(tiles1, slots) * each;
+    if (cost < kGain * least) {
+      least = cost;
+      best.splits = splits;
+    }
+  }
+  if (d.dtype != FCONV_F32 && rounds(tiles2, sms / 2) * (kRound + kPair * steps) <= least)
+    best = Shape{2, 1};
+  return best;
 }
-#define FCONV_BY_SIZE(pairs, call, ...)                               \
-  (d.dtype == FCONV_F32 ? call<1, true>(d, sms, a, __VA_ARGS__)       \
-   : (pairs)            ? call<2, false>(d, sms, a, __VA_ARGS__)      \
-                        : call<1, false>(d, sms, a, __VA_ARGS__))
+int64_t tiles_of(int64_t M, int64_t N, int side) {
+  return ((M + side - 1) / side) * ((N + side - 1) / side);
+}
+Shape shape_of(const fconv_mlp_desc& d, int64_t M, int64_t N, int64_t K, int products, int sms) {
+  return shape_of(d, tiles_of(M, N, 128), tiles_of(M, N, 256),
+                  products * ((K + kStep - 1) / kStep), sms);
+}
+#define FCONV_BY_SHAPE(v, call)                                          \
+  (d.dtype == FCONV_F32 ? call<1, true>(d, sms, (v).splits, a, l.in, s)  \
+   : (v).cg == 2        ? call<2, false>(d, sms, 1, a, l.in, s)          \
+                        : call<1, false>(d, sms, (v).splits, a, l.in, s))
 
 int64_t whole8(int64_t n) { return (n + 7) / 8 * 8; }
 size_t whole256(size_t n) { return (n + 255) / 256 * 256; }
@@ -961,12 +1081,13 @@ Layout layout(const fconv_mlp_desc& d, const MlpArgs& a, bool backward, int sms)
   return l;
 }
 
-// g, u and (unless h is null: not wanted) h.
-int projections(const fconv_mlp_desc& d, int sms, const MlpArgs& a, const Inputs& in, bool want_h,
+// g, u and h (few tokens: if wanted).
+int projections(const fconv_mlp_desc& d, int sms, const MlpArgs& a, const Layout& l, bool want_h,
                 cudaStream_t s) {
   if (d.tokens <= kMlpFewTokens)
-    return launch_mlp_few_gated(d, a, want_h ? const_cast<void*>(in.h.p) : nullptr, in.h.stride, s);
-  return FCONV_BY_SIZE(pairs_fill(d.tokens, 2 * d.hidden, sms), gated, in, s);
+    return launch_mlp_few_gated(d, a, want_h ? const_cast<void*>(l.in.h.p) : nullptr,
+                                l.in.h.stride, s);
+  return FCONV_BY_SHAPE(shape_of(d, d.tokens, 2 * d.hidden, d.features, 1, sms), gated);
 }
 
 }  // namespace
@@ -991,23 +1112,30 @@ size_t mlp_tc_workspace(const fconv_mlp_desc& d, bool backward, int sms) {
 int launch_mlp_tc_forward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s) {
   const Layout l = layout(d, a, false, sms);
   int e = launch_mlp_prep(d.dtype, l.prep, s);
-  if (!e) e = projections(d, sms, a, l.in, true, s);
+  if (!e) e = projections(d, sms, a, l, true, s);
   if (e) return e;
   if (d.tokens <= kMlpFewTokens) return launch_mlp_few_down(d, a, l.in.h.p, l.in.h.stride, s);
-  return FCONV_BY_SIZE(pairs_fill(d.tokens, d.out_features, sms), down, l.in, s);
+  return FCONV_BY_SHAPE(shape_of(d, d.tokens, d.out_features, d.hidden, 1, sms), down);
 }
 
 int launch_mlp_tc_backward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s) {
-  const int64_t T = d.tokens;
+  const int64_t T = d.tokens, D = d.features, F = d.hidden, O = d.out_features;
   const Layout l = layout(d, a, true, sms);
   int e = launch_mlp_prep(d.dtype, l.prep, s);
   // made again, the projections are the forward pass's bit by bit
-  if (!e && a.remake) e = projections(d, sms, a, l.in, false, s);
-  if (!e) e = FCONV_BY_SIZE(pairs_fill(T, d.hidden, sms), grads_of_projections, l.in, s);
-  if (!e && a.dx) e = FCONV_BY_SIZE(pairs_fill(T, d.features, sms), grad_of_input, l.in, s);
-  if (!e && (a.dw_gate || a.dw_up || a.dw_down))
-    e = FCONV_BY_SIZE(pairs_fill(2 * d.hidden + d.out_features, d.features, sms), grads_of_weights,
-                      l.in, s);
+  if (!e && a.remake) e = projections(d, sms, a, l, false, s);
+  if (!e) e = FCONV_BY_SHAPE(shape_of(d, T, F, O, 1, sms), grads_of_projections);
+  if (!e && a.dx) e = FCONV_BY_SHAPE(shape_of(d, T, D, F, 2, sms), grad_of_input);
+  if (!e && (a.dw_gate || a.dw_up || a.dw_down)) {
+    int64_t tiles[2];
+    for (int i = 0; i < 2; ++i) {
+      const int side = 128 * (i + 1);
+      tiles[i] = ((a.dw_gate != nullptr) + (a.dw_up != nullptr)) * tiles_of(F, D, side) +
+                 (a.dw_down != nullptr) * tiles_of(O, F, side);
+    }
+    e = FCONV_BY_SHAPE(shape_of(d, tiles[0], tiles[1], (T + kStep - 1) / kStep, sms),
+                       grads_of_weights);
+  }
   if (e) return e;
   const Matrix* from[3] = {&l.in.dg, &l.in.du, &l.in.dy};
   void* to[3] = {a.db_gate, a.db_up, a.db_down};
