@@ -92,9 +92,9 @@ __global__ void __launch_bounds__(kCols) column_join(const __grid_constant__ Sum
 
 int64_t blocks_of(int64_t cols) { return (cols + kCols - 1) / kCols; }
 
-// Shares of the rows: about four blocks an SM, of 64 rows at least.
+// Shares of the rows: about eight blocks an SM, of 64 rows at least.
 int shares_of(int64_t blocks, int64_t rows, int sms) {
-  int64_t n = (4 * sms + blocks - 1) / (blocks > 0 ? blocks : 1);
+  int64_t n = (8 * sms + blocks - 1) / (blocks > 0 ? blocks : 1);
   const int64_t most = (rows + 63) / 64;
   if (n > most) n = most;
   return n < 1 ? 1 : (int)n;
@@ -106,7 +106,7 @@ int shares_of(int64_t blocks, int64_t rows, int sms) {
 size_t column_sums_workspace(const int64_t cols[3], int sms) {
   int64_t blocks = 0;
   for (int i = 0; i < 3; ++i) blocks += blocks_of(cols[i]);
-  return (size_t)(4 * (int64_t)sms + 2 * blocks) * kCols * sizeof(float);
+  return (size_t)(8 * (int64_t)sms + 2 * blocks) * kCols * sizeof(float);
 }
 
 int launch_column_sums(int dtype, bool planes, const SumsArgs m[3], int64_t rows, float* part,

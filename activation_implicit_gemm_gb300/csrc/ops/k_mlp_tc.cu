@@ -39,7 +39,7 @@ namespace {
 constexpr int kStep = 64;                  // K of a stage
 constexpr uint32_t kSide = 128 * kStep * 2;  // bytes of 128 rows (or columns) of one operand
 constexpr uint32_t kBox = kSide / 2;       // 64 of them where they run along M or N
-constexpr uint32_t kSlot = 128 * 64;       // staged output: 128 rows of 32 values
+constexpr uint32_t kSlot = 32 * 64;        // staged output of a warp: 32 rows of 32 values
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8, kFirstEpiWarp = 4;
 
@@ -49,7 +49,7 @@ constexpr int kPlanes = 3, kTerms = 6;  // of f32
 constexpr int kChunk = 8;               // steps of K whose sums stay in TMEM, f32
 
 template <int EPI, bool F32>
-constexpr int kSlots = EPI == kGrad || (F32 && EPI == kGated) ? 3 : 2;  // of an epilogue warpgroup
+constexpr int kSlots = EPI == kGrad || (F32 && EPI == kGated) ? 3 : 2;  // of an epilogue warp
 template <int EPI, bool F32>
 constexpr int kStages = kSlots<EPI, F32> == 3 ? 5 : 6;
 
@@ -190,19 +190,6 @@ template <int N>
 __device__ __forceinline__ void bulk_wait_read_but() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
-// The same answer for `count` threads (whole warps): whether all of them have `ok`.
-__device__ __forceinline__ bool bar_and(uint32_t id, uint32_t count, bool ok) {
-  uint32_t all;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %3, 0;\n\t"
-      "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
-      "selp.b32 %0, 1, 0, q;\n\t}"
-      : "=r"(all)
-      : "r"(id), "r"(count), "r"((uint32_t)ok)
-      : "memory");
-  return all != 0;
-}
 // A wait for arrivals from the other block too.
 __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity,
                                              volatile int* abort_flag) {
@@ -316,20 +303,19 @@ __device__ __forceinline__ void stage_planes(uint32_t slots, int row, int c0, co
 // The staged rows of a warp to global memory, a row of 32 columns at a time, at any alignment.
 template <bool F32>
 __device__ __forceinline__ void store_rows(uint32_t slot, void* out, int64_t out_row, int64_t grow0,
-                                           int row0, int64_t M, int col, int N, int lane) {
+                                           int64_t M, int col, int N, int lane) {
   __syncwarp();
   const bool in = col + lane < N;
 #pragma unroll 4
   for (int i = 0; i < 32; ++i) {
-    const int row = row0 + i;
     if (grow0 + i >= M) break;
     const int64_t at = (grow0 + i) * out_row + col + lane;
     if (F32) {
       const uint32_t v =
-          ptx::ld_shared_u32(slot + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4);
+          ptx::ld_shared_u32(slot + i * 128 + (((lane >> 2) ^ (i & 7)) << 4) + (lane & 3) * 4);
       if (in) ((uint32_t*)out)[at] = v;
     } else {
-      const uint32_t v = ptx::ld_shared_u16(slot + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) +
+      const uint32_t v = ptx::ld_shared_u16(slot + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) +
                                             (lane & 7) * 2);
       if (in) ((uint16_t*)out)[at] = (uint16_t)v;
     }
@@ -536,11 +522,13 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
       }
     }
   } else if (warp >= kFirstEpiWarp) {
+    // Each warp for itself: a quarter of the rows (its TMEM lanes) of half of the columns, its own
+    // slots and its own stores.
     const int half = (warp - kFirstEpiWarp) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
-    const uint32_t slots = ring + S * kStageBytes + half * kSlots<EPI, F32> * kSlot;
+    const uint32_t slots =
+        ring + S * kStageBytes + (uint32_t)((warp - kFirstEpiWarp) * kSlots<EPI, F32>) * kSlot;
     const bool bf16 = j.bf16;
-    const bool issues = threadIdx.x == (kFirstEpiWarp + 4 * half) * 32;
     const int act = j.act;
     const float alpha = j.alpha;
     constexpr int kParts = kCols / 64;  // 32-column parts of a warp's half of the tile
@@ -550,17 +538,34 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
     for (int id = first; ok && id < j.tiles; id += stride) {
       const Tile t = tile_of(j, id);
       const Problem& p = j.p[t.which];
-      const int m0 = (t.m * CG + (int)rank) * 128;
-      const int64_t grow = (int64_t)m0 + row;
+      const int m0 = (t.m * CG + (int)rank) * 128 + quarter * 32;  // this warp's first row
+      const int64_t grow = (int64_t)m0 + lane;
+      const int first_part = SPLIT ? half * splits + part : half * kParts;
       // saved values of this warp's rows: block of 32 rows, a row a lane
       float* saved = nullptr;
       if (EPI != kPlain && j.saved)
         saved = j.saved + (grow >> 5) * j.quads * 256 + lane * 4;
+      // kGrad: those of 32 columns, in 16-bit types on their way since the part before (f32 has no
+      // registers for that)
+      constexpr bool kEarly = EPI == kGrad && !F32;
+      float4 gs[kEarly ? 8 : 1], us[kEarly ? 8 : 1];
+      auto load_saved = [&](int c, int i, float4& g, float4& v) {
+        g = v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int col = t.n * kCols + c * 32 + 4 * i;
+        if (grow < p.M && col < p.N) {
+          const float* from = saved + (int64_t)(col >> 2) * 256;
+          g = __ldcg(reinterpret_cast<const float4*>(from));
+          v = __ldcg(reinterpret_cast<const float4*>(from + 128));
+        }
+      };
+      if (kEarly) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) load_saved(first_part, i, gs[i], us[i]);
+      }
 
-      // The warps of a group, which meet at barriers below, go on or give up together.
       auto arrive = [&]() {
-        ok = bar_and(1 + half, 128, wait_bar(ptx::smem_addr(&ctl.acc_full[n & 1]), (n >> 1) & 1,
-                                             abort_flag));
+        ok = all_lanes(
+            wait_bar(ptx::smem_addr(&ctl.acc_full[n & 1]), (n >> 1) & 1, abort_flag));
         ptx::tc_fence_after();
         return ok;
       };
@@ -582,55 +587,75 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
         tmem_arrived(r0);
         if (EPI == kGated) tmem_arrived(r1);
       };
-      // Slots that may be written again, for all warps of the group.
+      // Slots that may be written again.
       auto reuse = [&]() {
-        if (issues) bulk_wait_read_but<kSlots<EPI, F32> == 3 ? 0 : 1>();
-        ptx::bar_sync(1 + half, 128);
+        if (lane == 0) bulk_wait_read_but<kSlots<EPI, F32> == 3 ? 0 : 1>();
+        __syncwarp();
       };
       auto store = [&](const CUtensorMap* map, int col, int boxes, uint32_t from, bool planes) {
         ptx::fence_proxy_async_smem();
-        ptx::bar_sync(1 + half, 128);
-        if (issues && m0 < p.M) {
+        __syncwarp();
+        if (lane == 0 && m0 < p.M) {
           for (int i = 0; i < boxes; ++i)
             store_box(planes ? map : map + i, from + i * kSlot, col, m0, planes ? i : 0);
           bulk_commit();
         }
       };
-      // 32 columns of the tile; x (and with kGated u) are sums of products.
-      auto finish = [&](int c, float (&x)[32], float (&u)[32]) {
+      // 32 columns of the tile, of which this warp takes `next` after them; x (and with kGated u)
+      // are sums of products.
+      auto finish = [&](int c, int next, float (&x)[32], float (&u)[32]) {
         const int col = t.n * kCols + c * 32;
-        if (col >= p.N) return;  // the same for the whole group
+        if (col >= p.N) return;
         if (EPI == kPlain) {
           add_bias<F32>(x, p.bias[0], col, p.N, bf16, lane);
           uint32_t w[16];
           if (F32) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              ptx::st_shared_v4(slots + row * 128 + (((i >> 2) ^ (row & 7)) << 4),
+              ptx::st_shared_v4(slots + lane * 128 + (((i >> 2) ^ (lane & 7)) << 4),
                                 __float_as_uint(x[i]), __float_as_uint(x[i + 1]),
                                 __float_as_uint(x[i + 2]), __float_as_uint(x[i + 3]));
           } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = pack16(bf16, x[2 * i], x[2 * i + 1]);
           }
-          if (F32 || p.out) {  // a warp's own rows: no warp waits for another
-            if (!F32) {        // but for boxes of another problem's tile that may be on their way
-              if (issues) bulk_wait_read_but<0>();
-              ptx::bar_sync(1 + half, 128);
-              stage(slots, row, 0, w);
+          if (F32 || p.out) {
+            if (!F32) {  // boxes of another problem's tile may be on their way
+              if (lane == 0) bulk_wait_read_but<0>();
+              __syncwarp();
+              stage(slots, lane, 0, w);
             }
-            store_rows<F32>(slots, p.out, p.out_row, (int64_t)m0 + quarter * 32, quarter * 32, p.M,
-                            col, p.N, lane);
+            store_rows<F32>(slots, p.out, p.out_row, m0, p.M, col, p.N, lane);
           } else {
             reuse();
-            stage(slots + slot * kSlot, row, 0, w);
+            stage(slots + slot * kSlot, lane, 0, w);
             store(&p.c[0], col, 1, slots + slot * kSlot, false);
             slot ^= 1;
           }
         } else if (EPI == kGated) {
           add_bias<F32>(x, p.bias[0], col, p.N, bf16, lane);
           add_bias<F32>(u, p.bias[1], col, p.N, bf16, lane);
-          if (saved && grow < p.M) {
+          reuse();
+          if (F32) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              float h[8], unused;
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                h[e] = act_of<false>(act, alpha, x[i + e], unused) * u[i + e];
+              stage_planes(slots, lane, i, h);
+            }
+            store(&p.c[0], col, kPlanes, slots, true);
+          } else {
+            uint32_t w[16];
+#define FCONV_M(ACT) gate<ACT>(w, x, u, alpha, bf16)
+            FCONV_GATE_SWITCH(act, FCONV_M)
+#undef FCONV_M
+            stage(slots + slot * kSlot, lane, 0, w);
+            store(&p.c[0], col, 1, slots + slot * kSlot, false);
+            slot ^= 1;
+          }
+          if (saved && grow < p.M) {  // after the fence, which would wait for them
             float* to = saved + (int64_t)(col >> 2) * 256;
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
@@ -641,72 +666,47 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
                   make_float4(u[i], u[i + 1], u[i + 2], u[i + 3]);
             }
           }
-          reuse();
-          if (F32) {
-            float unused;
+        } else if (F32) {
+#pragma unroll 1
+          for (int which = 0; which < 3; ++which) {  // dg, du, h: one after the other
+            reuse();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = act_of<false>(act, alpha, x[i], unused) * u[i];
+            for (int i = 0; i < 32; i += 8) {
+              float v[8];
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) stage_planes(slots, row, i, x + i);
-            store(&p.c[0], col, kPlanes, slots, true);
-          } else {
-            uint32_t w[16];
-#define FCONV_M(ACT) gate<ACT>(w, x, u, alpha, bf16)
-            FCONV_GATE_SWITCH(act, FCONV_M)
-#undef FCONV_M
-            stage(slots + slot * kSlot, row, 0, w);
-            store(&p.c[0], col, 1, slots + slot * kSlot, false);
-            slot ^= 1;
+              for (int k = 0; k < 8; k += 4) {
+                float4 g4, u4;
+                load_saved(c, (i + k) / 4, g4, u4);
+                const float gv[4] = {g4.x, g4.y, g4.z, g4.w}, uv[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  float slope;
+                  const float a = act_of<true>(act, alpha, gv[e], slope), d = x[i + k + e];
+                  v[k + e] = which == 0 ? d * uv[e] * slope : which == 1 ? d * a : a * uv[e];
+                }
+              }
+              stage_planes(slots, lane, i, v);
+            }
+            store(&p.c[which], col, kPlanes, slots, true);
           }
         } else {
-          const float* from = saved + (int64_t)(col >> 2) * 256;
-          auto load = [&](int i, float4& g, float4& v) {
-            g = v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (grow < p.M && col + i < p.N) {
-              g = __ldcg(reinterpret_cast<const float4*>(from + i * 64));
-              v = __ldcg(reinterpret_cast<const float4*>(from + i * 64 + 128));
-            }
-          };
-          if (F32) {
-#pragma unroll 1
-            for (int which = 0; which < 3; ++which) {  // dg, du, h: one after the other
-              reuse();
-#pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                float v[8];
-#pragma unroll
-                for (int k = 0; k < 8; k += 4) {
-                  float4 g4, u4;
-                  load(i + k, g4, u4);
-                  const float gs[4] = {g4.x, g4.y, g4.z, g4.w}, us[4] = {u4.x, u4.y, u4.z, u4.w};
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    float slope;
-                    const float a = act_of<true>(act, alpha, gs[e], slope), d = x[i + k + e];
-                    v[k + e] = which == 0 ? d * us[e] * slope : which == 1 ? d * a : a * us[e];
-                  }
-                }
-                stage_planes(slots, row, i, v);
-              }
-              store(&p.c[which], col, kPlanes, slots, true);
-            }
-          } else {
-            reuse();
-#define FCONV_M(ACT)                                                 \
-  _Pragma("unroll") for (int i = 0; i < 32; i += 8) {                \
-    uint32_t wg[4], wu[4], wh[4];                                    \
-    float4 g[2], v[2];                                               \
-    load(i, g[0], v[0]);                                             \
-    load(i + 4, g[1], v[1]);                                         \
-    gate_grad<ACT>(wg, wu, wh, x + i, g, v, alpha, bf16);            \
-    stage(slots, row, i / 2, wg);                                    \
-    stage(slots + kSlot, row, i / 2, wu);                            \
-    stage(slots + 2 * kSlot, row, i / 2, wh);                        \
+          reuse();
+#define FCONV_M(ACT)                                                                             \
+  _Pragma("unroll") for (int i = 0; i < 32; i += 8) {                                            \
+    uint32_t wg[4], wu[4], wh[4];                                                                \
+    const float4 g[2] = {gs[i / 4], gs[i / 4 + 1]}, v[2] = {us[i / 4], us[i / 4 + 1]};           \
+    if (next >= 0) {                                                                             \
+      load_saved(next, i / 4, gs[i / 4], us[i / 4]);                                             \
+      load_saved(next, i / 4 + 1, gs[i / 4 + 1], us[i / 4 + 1]);                                 \
+    }                                                                                            \
+    gate_grad<ACT>(wg, wu, wh, x + i, g, v, alpha, bf16);                                        \
+    stage(slots, lane, i / 2, wg);                                                               \
+    stage(slots + kSlot, lane, i / 2, wu);                                                       \
+    stage(slots + 2 * kSlot, lane, i / 2, wh);                                                   \
   }
-            FCONV_GATE_SWITCH(act, FCONV_M)
+          FCONV_GATE_SWITCH(act, FCONV_M)
 #undef FCONV_M
-            store(&p.c[0], col, 3, slots, false);
-          }
+          store(&p.c[0], col, 3, slots, false);
         }
       };
 
@@ -755,9 +755,9 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
         }
         __syncwarp();
         cluster_sync();  // with the other warps, below
-        // columns c go to block c % splits, there to group c / splits
-        const int c = half * splits + part;
-        if (ok && c < 2 * kParts && part < splits) {
+        // columns c go to block c % splits, there to half c / splits of the warps
+        const int c = first_part;
+        if (ok && c < 2 * kParts) {
           float x[32], u[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = u[i] = 0.0f;
@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
               }
             }
           }
-          finish(c, x, u);
+          finish(c, -1, x, u);
         }
         break;  // one tile
       } else if constexpr (F32) {
@@ -782,7 +782,8 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
         if (!ok) break;
 #pragma unroll
         for (int c = 0; c < kParts; ++c)
-          finish(half * kParts + c, x[c], u[EPI == kGated ? c : 0]);
+          finish(first_part + c, c + 1 < kParts ? first_part + c + 1 : -1, x[c],
+                 u[EPI == kGated ? c : 0]);
       } else {
         if (!arrive()) break;
 #pragma unroll 1
@@ -793,12 +794,13 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
           if (c + 1 == kParts) release();
           as_floats(x, r0);
           if (EPI == kGated) as_floats(u, r1);
-          finish(half * kParts + c, x, u);
+          finish(first_part + c, c + 1 < kParts ? first_part + c + 1 : -1, x, u);
         }
         ++n;
       }
     }
-    if (issues) bulk_wait_all();
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   }
   if (SPLIT && warp < kFirstEpiWarp) {  // the sums of all blocks are in shared memory
     __syncwarp();
@@ -876,7 +878,7 @@ struct Builder {
   }
   // An operand of a later product.
   void inner(Problem& p, int i, const Matrix& c) {
-    ok = ok && map_of(enc, &p.c[i], c, bf16, F32 ? kPlanes : 1, 32, 128);
+    ok = ok && map_of(enc, &p.c[i], c, bf16, F32 ? kPlanes : 1, 32, 32);
   }
   // A result of the call: by boxes where its rows start on 16 bytes.
   void result(Problem& p, void* out, int64_t rows, int64_t cols, int64_t stride) {
@@ -899,7 +901,7 @@ struct Builder {
   }
   template <bool SPLIT>
   int start(int blocks, int cluster, cudaStream_t s) {
-    const size_t smem = kStages<EPI, F32> * 2 * kSide + 2 * kSlots<EPI, F32> * kSlot;
+    const size_t smem = kStages<EPI, F32> * 2 * kSide + kEpiWarps * kSlots<EPI, F32> * kSlot;
     auto kernel = mlp_tc<CG, AMN, BMN, EPI, F32, SPLIT>;
     if (const int e = allow_smem((const void*)kernel, smem)) return e;
     cudaLaunchConfig_t cfg = {};
