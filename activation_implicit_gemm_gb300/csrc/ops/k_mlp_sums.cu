@@ -1,6 +1,7 @@
 // Sums over the rows of up to three matrices at once: the bias gradients of the gated
-// feed-forward block. Bound: HBM, each matrix read once. A block adds 64 columns of its share of
-// the rows; the shares' f32 sums are joined in order by a second launch.
+// feed-forward block. Bound: HBM, each matrix read once. A block adds 128 columns of its share of
+// the rows (256 bytes of a 16-bit row at a time); the shares' f32 sums are joined in order by a
+// second launch.
 #include "ops_common.cuh"
 #include "ops_internal.h"
 
@@ -11,13 +12,13 @@ namespace fconv {
 namespace ops {
 namespace {
 
-constexpr int kThreads = 256, kCols = 64;
+constexpr int kThreads = 256, kCols = 128;
 
 struct Sums {
   SumsArgs m[3];
   float* part;
   int64_t rows;
-  int first[4];  // first block of 64 columns of each matrix
+  int first[4];  // first block of kCols columns of each matrix
   int shares;
 };
 __device__ __forceinline__ int matrix_of(const Sums& q, int block) {
@@ -72,30 +73,40 @@ __global__ void __launch_bounds__(kThreads) column_sums(const __grid_constant__ 
   __syncthreads();
   if (threadIdx.x >= kCols) return;
   float v = 0.0f;
+#pragma unroll
   for (int i = 0; i < kRows; ++i) v += sums[i][threadIdx.x];
   q.part[((int64_t)blockIdx.y * q.first[3] + blockIdx.x) * kCols + threadIdx.x] = v;
 }
 
+// 32 columns a block, 32 shares at a time.
 template <typename T>
-__global__ void __launch_bounds__(kCols) column_join(const __grid_constant__ Sums q) {
+__global__ void __launch_bounds__(1024) column_join(const __grid_constant__ Sums q) {
+  __shared__ float sums[32][33];
   ptx::pdl_wait();
   ptx::pdl_trigger();
-  const int which = matrix_of(q, blockIdx.x);
+  const int block = blockIdx.x / (kCols / 32), which = matrix_of(q, block);
   const SumsArgs& m = q.m[which];
-  const int64_t c = (int64_t)(blockIdx.x - q.first[which]) * kCols + threadIdx.x;
-  if (c >= m.cols) return;
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+  const int in_block = blockIdx.x % (kCols / 32) * 32 + lane;
+  const int64_t c = (int64_t)(block - q.first[which]) * kCols + in_block;
   float v = 0.0f;
-  for (int i = 0; i < q.shares; ++i)
-    v += __ldcg(q.part + ((int64_t)i * q.first[3] + blockIdx.x) * kCols + threadIdx.x);
+  for (int i = row; i < q.shares; i += 32)
+    v += __ldcg(q.part + ((int64_t)i * q.first[3] + block) * kCols + in_block);
+  sums[row][lane] = v;
+  __syncthreads();
+  if (row > 0 || c >= m.cols) return;
+  v = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v += sums[i][lane];
   ((T*)m.out)[c] = from_f<T>(v);
 }
 
 int64_t blocks_of(int64_t cols) { return (cols + kCols - 1) / kCols; }
 
-// Shares of the rows: about eight blocks an SM, of 64 rows at least.
+// Shares of the rows: about eight blocks an SM, of 32 rows at least.
 int shares_of(int64_t blocks, int64_t rows, int sms) {
   int64_t n = (8 * sms + blocks - 1) / (blocks > 0 ? blocks : 1);
-  const int64_t most = (rows + 63) / 64;
+  const int64_t most = (rows + 31) / 32;
   if (n > most) n = most;
   return n < 1 ? 1 : (int)n;
 }
@@ -138,7 +149,7 @@ int launch_column_sums(int dtype, bool planes, const SumsArgs m[3], int64_t rows
 #undef FCONV_M
   }
   if (e) return e;
-#define FCONV_M(T) e = launch_pdl(column_join<T>, dim3((unsigned)q.first[3]), dim3(kCols), 0, s, q)
+#define FCONV_M(T) e = launch_pdl(column_join<T>, dim3((unsigned)q.first[3] * (kCols / 32)), dim3(1024), 0, s, q)
   FCONV_OPS_TYPE(dtype, FCONV_M)
 #undef FCONV_M
   return e;
