@@ -22,8 +22,8 @@
 // f32 (F32) comes as three bf16 planes that add up to it (k_mlp_prep.cu; h, dg and du are split in
 // the epilogues). Six products of planes, the smallest first, leave out less than 2^-23 of a
 // product. The tensor core's f32 sums cut off instead of rounding (measured: 1.7e-8 of the result
-// for each instruction of 16 products, always towards zero), so after 512 of K they are added to
-// registers in plain f32.
+// for each instruction of 16 products, always towards zero), so after 128 of K they are added to
+// registers in plain f32 (after 512 the errors were twice as large, at the same speed).
 #include "mlp_math.cuh"
 #include "split_bf16.cuh"
 #include "tc_instr.cuh"
@@ -46,12 +46,12 @@ constexpr int kEpiWarps = 8, kFirstEpiWarp = 4;
 enum { kPlain, kGated, kGrad };
 
 constexpr int kPlanes = 3, kTerms = 6;  // of f32
-constexpr int kChunk = 8;               // steps of K whose sums stay in TMEM, f32
+constexpr int kChunk = 2;               // steps of K whose sums stay in TMEM, f32
 
+template <int EPI, bool F32>  // of an epilogue warp
+constexpr int kSlots = EPI == kPlain ? 2 : EPI == kGated ? (F32 ? kPlanes : 2) : F32 ? 2 * kPlanes : 3;
 template <int EPI, bool F32>
-constexpr int kSlots = EPI == kGrad || (F32 && EPI == kGated) ? 3 : 2;  // of an epilogue warp
-template <int EPI, bool F32>
-constexpr int kStages = kSlots<EPI, F32> == 3 ? 5 : 6;
+constexpr int kStages = kSlots<EPI, F32> > 3 ? 4 : kSlots<EPI, F32> == 3 ? 5 : 6;
 
 struct Problem {
   CUtensorMap a[2], b[2], c[3];  // products of a sum (kGated: gate and up), outputs as boxes
@@ -379,6 +379,34 @@ __device__ __forceinline__ void gate_grad(uint32_t (&wg)[4], uint32_t (&wu)[4], 
   }
 }
 
+// The same for f32, staged as planes: 32 values of h; 8 of dg, or of du and h.
+template <int ACT>
+__device__ __forceinline__ void gate_planes(uint32_t slots, int row, const float (&g)[32],
+                                            const float (&u)[32], float alpha) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8) {
+    float h[8], unused;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = act_exact<ACT, false>(alpha, g[i + e], unused) * u[i + e];
+    stage_planes(slots, row, i, h);
+  }
+}
+template <int ACT, bool GATE>
+__device__ __forceinline__ void gate_grad_planes(uint32_t slots, int row, int c0, const float* dh,
+                                                 const float (&g)[8], const float (&u)[8],
+                                                 float alpha) {
+  float v[8], h[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float slope = 0.0f;
+    const float a = act_exact<ACT, GATE>(alpha, g[e], slope);
+    v[e] = GATE ? dh[e] * u[e] * slope : dh[e] * a;
+    h[e] = a * u[e];
+  }
+  stage_planes(slots, row, c0, v);
+  if (!GATE) stage_planes(slots + kPlanes * kSlot, row, c0, h);
+}
+
 template <int CG, bool AMN, bool BMN, int EPI, bool F32, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Job j) {
   constexpr int S = kStages<EPI, F32>, BN = 128 * CG;
@@ -589,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
       };
       // Slots that may be written again.
       auto reuse = [&]() {
-        if (lane == 0) bulk_wait_read_but<kSlots<EPI, F32> == 3 ? 0 : 1>();
+        if (lane == 0) bulk_wait_read_but<kSlots<EPI, F32> == 2 ? 1 : 0>();
         __syncwarp();
       };
       auto store = [&](const CUtensorMap* map, int col, int boxes, uint32_t from, bool planes) {
@@ -637,14 +665,9 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
           add_bias<F32>(u, p.bias[1], col, p.N, bf16, lane);
           reuse();
           if (F32) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              float h[8], unused;
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                h[e] = act_of<false>(act, alpha, x[i + e], unused) * u[i + e];
-              stage_planes(slots, lane, i, h);
-            }
+#define FCONV_M(ACT) gate_planes<ACT>(slots, lane, x, u, alpha)
+            FCONV_GATE_SWITCH(act, FCONV_M)
+#undef FCONV_M
             store(&p.c[0], col, kPlanes, slots, true);
           } else {
             uint32_t w[16];
@@ -667,28 +690,34 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
             }
           }
         } else if (F32) {
-#pragma unroll 1
-          for (int which = 0; which < 3; ++which) {  // dg, du, h: one after the other
-            reuse();
+          auto values = [&](int i, float (&g)[8], float (&v)[8]) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              float v[8];
-#pragma unroll
-              for (int k = 0; k < 8; k += 4) {
-                float4 g4, u4;
-                load_saved(c, (i + k) / 4, g4, u4);
-                const float gv[4] = {g4.x, g4.y, g4.z, g4.w}, uv[4] = {u4.x, u4.y, u4.z, u4.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  float slope;
-                  const float a = act_of<true>(act, alpha, gv[e], slope), d = x[i + k + e];
-                  v[k + e] = which == 0 ? d * uv[e] * slope : which == 1 ? d * a : a * uv[e];
-                }
-              }
-              stage_planes(slots, lane, i, v);
+            for (int k = 0; k < 8; k += 4) {
+              float4 g4, v4;
+              load_saved(c, (i + k) / 4, g4, v4);
+              g[k] = g4.x, g[k + 1] = g4.y, g[k + 2] = g4.z, g[k + 3] = g4.w;
+              v[k] = v4.x, v[k + 1] = v4.y, v[k + 2] = v4.z, v[k + 3] = v4.w;
             }
-            store(&p.c[which], col, kPlanes, slots, true);
-          }
+          };
+          // dg, then du and h: there is no room for nine planes at once
+#define FCONV_M(ACT)                                                     \
+  reuse();                                                               \
+  _Pragma("unroll") for (int i = 0; i < 32; i += 8) {                    \
+    float g[8], v[8];                                                    \
+    values(i, g, v);                                                     \
+    gate_grad_planes<ACT, true>(slots, lane, i, x + i, g, v, alpha);     \
+  }                                                                      \
+  store(&p.c[0], col, kPlanes, slots, true);                             \
+  reuse();                                                               \
+  _Pragma("unroll") for (int i = 0; i < 32; i += 8) {                    \
+    float g[8], v[8];                                                    \
+    values(i, g, v);                                                     \
+    gate_grad_planes<ACT, false>(slots, lane, i, x + i, g, v, alpha);    \
+  }                                                                      \
+  store(&p.c[1], col, kPlanes, slots, true);                             \
+  store(&p.c[2], col, kPlanes, slots + kPlanes * kSlot, true)
+          FCONV_GATE_SWITCH(act, FCONV_M)
+#undef FCONV_M
         } else {
           reuse();
 #define FCONV_M(ACT)                                                                             \

@@ -13,39 +13,52 @@ namespace fconv {
 namespace ops {
 namespace {
 
-// act(v) in f32, and with SLOPE its derivative. The activation is the same in all threads.
+// act(v) in f32, and with SLOPE its derivative.
+template <int ACT, bool SLOPE>
+__device__ __forceinline__ float act_exact(float alpha, float v, float& slope) {
+  if (ACT == FCONV_ACT_RELU) {  // NaN goes through
+    if (SLOPE) slope = v > 0.0f ? 1.0f : 0.0f;
+    return v < 0.0f ? 0.0f : v;
+  } else if (ACT == FCONV_ACT_SIGMOID) {
+    const float p = 1.0f / (1.0f + expf(-v));
+    if (SLOPE) slope = p * (1.0f / (1.0f + expf(v)));  // 1 - p loses its bits for large v
+    return p;
+  } else if (ACT == FCONV_ACT_QUICKGELU) {
+    const float p = 1.0f / (1.0f + expf(-alpha * v));
+    if (SLOPE) slope = p * (1.0f + alpha * v * (1.0f - p));
+    return v * p;
+  } else if (ACT == FCONV_ACT_GELU) {
+    const float p = 0.5f * erfcf(v * -0.7071067811865476f);
+    if (SLOPE) slope = p + v * 0.3989422804014327f * expf(-0.5f * v * v);
+    return v * p;
+  } else if (ACT == FCONV_ACT_FASTGELU) {
+    constexpr float k = 0.7978845608028654f, c = 0.044715f;  // sqrt(2 / pi)
+    const float th = tanhf(k * (v + c * v * v * v));
+    if (SLOPE)
+      slope = 0.5f * (1.0f + th) + 0.5f * v * (1.0f - th * th) * k * (1.0f + 3.0f * c * v * v);
+    return 0.5f * v * (1.0f + th);
+  } else {
+    if (SLOPE) slope = 1.0f;
+    return v;
+  }
+}
+
+// Calls M(ACT) with ACT the compile-time code of the activation, which is the same in all threads.
+#define FCONV_GATE_SWITCH(act, M)                                  \
+  switch (act) {                                                   \
+    case FCONV_ACT_RELU: { M(FCONV_ACT_RELU); break; }             \
+    case FCONV_ACT_SIGMOID: { M(FCONV_ACT_SIGMOID); break; }       \
+    case FCONV_ACT_QUICKGELU: { M(FCONV_ACT_QUICKGELU); break; }   \
+    case FCONV_ACT_GELU: { M(FCONV_ACT_GELU); break; }             \
+    case FCONV_ACT_FASTGELU: { M(FCONV_ACT_FASTGELU); break; }     \
+    default: { M(FCONV_ACT_NONE); break; }                         \
+  }
+
 template <bool SLOPE>
 __device__ __forceinline__ float act_of(int act, float alpha, float v, float& slope) {
-  switch (act) {
-    case FCONV_ACT_RELU:  // NaN goes through
-      if (SLOPE) slope = v > 0.0f ? 1.0f : 0.0f;
-      return v < 0.0f ? 0.0f : v;
-    case FCONV_ACT_SIGMOID: {
-      const float p = 1.0f / (1.0f + expf(-v));
-      if (SLOPE) slope = p * (1.0f / (1.0f + expf(v)));  // 1 - p loses its bits for large v
-      return p;
-    }
-    case FCONV_ACT_QUICKGELU: {
-      const float p = 1.0f / (1.0f + expf(-alpha * v));
-      if (SLOPE) slope = p * (1.0f + alpha * v * (1.0f - p));
-      return v * p;
-    }
-    case FCONV_ACT_GELU: {
-      const float p = 0.5f * erfcf(v * -0.7071067811865476f);
-      if (SLOPE) slope = p + v * 0.3989422804014327f * expf(-0.5f * v * v);
-      return v * p;
-    }
-    case FCONV_ACT_FASTGELU: {
-      constexpr float k = 0.7978845608028654f, c = 0.044715f;  // sqrt(2 / pi)
-      const float th = tanhf(k * (v + c * v * v * v));
-      if (SLOPE)
-        slope = 0.5f * (1.0f + th) + 0.5f * v * (1.0f - th * th) * k * (1.0f + 3.0f * c * v * v);
-      return 0.5f * v * (1.0f + th);
-    }
-    default:
-      if (SLOPE) slope = 1.0f;
-      return v;
-  }
+#define FCONV_M(ACT) return act_exact<ACT, SLOPE>(alpha, v, slope)
+  FCONV_GATE_SWITCH(act, FCONV_M)
+#undef FCONV_M
 }
 
 // The same with the special-function unit's exponential and reciprocal (each within 2 ulp of f32),
@@ -104,17 +117,6 @@ __device__ __forceinline__ float act_fast(float alpha, float v, float& slope) {
     return v;
   }
 }
-
-// Calls M(ACT) with ACT the compile-time code of the activation.
-#define FCONV_GATE_SWITCH(act, M)                                  \
-  switch (act) {                                                   \
-    case FCONV_ACT_RELU: { M(FCONV_ACT_RELU); break; }             \
-    case FCONV_ACT_SIGMOID: { M(FCONV_ACT_SIGMOID); break; }       \
-    case FCONV_ACT_QUICKGELU: { M(FCONV_ACT_QUICKGELU); break; }   \
-    case FCONV_ACT_GELU: { M(FCONV_ACT_GELU); break; }             \
-    case FCONV_ACT_FASTGELU: { M(FCONV_ACT_FASTGELU); break; }     \
-    default: { M(FCONV_ACT_NONE); break; }                         \
-  }
 
 // The projections g and u of a training pass, f32: blocks of 32 rows by 4 columns, g's before
 // u's, so that a warp with a row a lane (as accumulators come out of TMEM) moves 512 consecutive
