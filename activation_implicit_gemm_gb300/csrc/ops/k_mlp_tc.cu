@@ -1056,7 +1056,8 @@ Shape shape_of(const fconv_mlp_desc& d, int64_t M, int64_t N, int64_t K, int pro
    : (v).cg == 2        ? call<2, false>(d, sms, 1, a, l.in, s)          \
                         : call<1, false>(d, sms, (v).splits, a, l.in, s))
 
-int64_t whole8(int64_t n) { return (n + 7) / 8 * 8; }
+// Rows in the workspace start on 128 bytes: a box's row then is one line of L2, not parts of two.
+int64_t whole_row(int64_t cols) { return (cols + 63) / 64 * 64; }
 size_t whole256(size_t n) { return (n + 255) / 256 * 256; }
 
 // A tensor of the call that TMA does not take as it is: f32, rows that do not start on 16 bytes or
@@ -1083,7 +1084,7 @@ Layout layout(const fconv_mlp_desc& d, const MlpArgs& a, bool backward, int sms)
     return p;
   };
   auto fresh = [&](int64_t rows, int64_t cols) {
-    Matrix m{nullptr, rows, cols, whole8(cols), 0};
+    Matrix m{nullptr, rows, cols, whole_row(cols), 0};
     m.plane = rows * m.stride;
     m.p = take((size_t)m.plane * planes * 2);
     return m;
