@@ -15,8 +15,9 @@
 // not start on 16 bytes the same bytes come an element at a time.
 //
 // The eight warps of a block share the same rows and split K; their f32 sums are joined through
-// shared memory in a fixed order, then come biases, gate and the one rounding. With more than 8
-// 16-bit tokens a warp takes two row groups, so that tokens are read half as often.
+// shared memory in a fixed order, then come biases, gate and the one rounding. Tokens are read from
+// L1 for every row group; with two row groups a warp, which reads them half as often, 16 tokens took
+// 67 us instead of 58 (fewer blocks than the SMs hold), 32 tokens 83 instead of 81.
 #include "mlp_math.cuh"
 #include "split_tf32.cuh"
 
@@ -41,12 +42,22 @@ struct Few {
   float alpha;
 };
 
+__device__ __forceinline__ float load_l2(const float* p) { return __ldcg(p); }
+__device__ __forceinline__ __half load_l2(const __half* p) { return __ldcg(p); }
+__device__ __forceinline__ __nv_bfloat16 load_l2(const __nv_bfloat16* p) { return __ldcg(p); }
+
+// How a row is read: weights once (a plain load that leaves L1 alone takes 51 us for one token
+// through 4096 x 10240, one through L2 only 60, with L2 full of other data); EARLY ones through L2
+// only, as nothing orders this SM's L1 before the wait; tokens through L1.
+enum { kTokens, kWeights, kEarly };
+
 // 16 bytes of a row from element k on where `in` (WIDE: a row has no rest), zeros past K.
-template <typename T, bool WIDE, bool WEIGHT>
+template <typename T, bool WIDE, int HOW>
 __device__ __forceinline__ uint4 load_row(const T* p, int k, int K, bool in) {
   if constexpr (WIDE) {
     if (!in) return make_uint4(0, 0, 0, 0);
-    if (!WEIGHT) return *reinterpret_cast<const uint4*>(p + k);
+    if (HOW == kTokens) return *reinterpret_cast<const uint4*>(p + k);
+    if (HOW == kEarly) return __ldcg(reinterpret_cast<const uint4*>(p + k));
     uint4 v;
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
@@ -56,7 +67,10 @@ __device__ __forceinline__ uint4 load_row(const T* p, int k, int K, bool in) {
     constexpr int E = 16 / sizeof(T);
     Vec<T, E> e;
 #pragma unroll
-    for (int i = 0; i < E; ++i) e.v[i] = in && k + i < K ? p[k + i] : from_f<T>(0.0f);
+    for (int i = 0; i < E; ++i) {
+      e.v[i] = from_f<T>(0.0f);
+      if (in && k + i < K) e.v[i] = HOW == kEarly ? load_l2(p + k + i) : p[k + i];
+    }
     return *reinterpret_cast<const uint4*>(&e);
   }
 }
@@ -111,24 +125,22 @@ __device__ __forceinline__ void step(float (&acc)[4], const uint4& a, const uint
   }
 }
 
-// NT: groups of 8 tokens. MT: row groups of a warp. U: steps of K whose loads go out together.
-template <typename T, bool WIDE, bool GATED, int NT, int MT, int U>
+// NT: groups of 8 tokens. U: steps of K whose loads go out together.
+template <typename T, bool WIDE, bool GATED, int NT, int U>
 __global__ void __launch_bounds__(kThreads, 2) mlp_few(const __grid_constant__ Few q) {
   constexpr int kElems = 16 / sizeof(T), kStep = 4 * kElems;  // of a lane, of a step
-  __shared__ float sums[kWarps][MT * 16][NT * 8 + 1];
-  constexpr int kRows = GATED ? 8 : 16;  // outputs of a row group
+  __shared__ float sums[kWarps][16][NT * 8 + 1];
+  constexpr int kRows = GATED ? 8 : 16;  // outputs of a block
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * kRows * MT;
+  const int n0 = blockIdx.x * kRows;
   // this lane's rows of weights; rows past the end read the last one, for outputs no one writes
-  const T* wp[MT][2];
+  const T* wp[2];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int which = GATED ? i : 0;
-      const int row = min(n0 + m * kRows + (GATED ? 0 : i * 8) + gr, q.N - 1);
-      wp[m][i] = (const T*)q.w[which] + row * q.w_row[which];
-    }
+  for (int i = 0; i < 2; ++i) {
+    const int which = GATED ? i : 0;
+    const int row = min(n0 + (GATED ? 0 : i * 8) + gr, q.N - 1);
+    wp[i] = (const T*)q.w[which] + row * q.w_row[which];
+  }
   const T* xp[NT];
   bool there[NT];
 #pragma unroll
@@ -136,56 +148,61 @@ __global__ void __launch_bounds__(kThreads, 2) mlp_few(const __grid_constant__ F
     there[n] = n * 8 + gr < q.tokens;
     xp[n] = (const T*)q.x + (there[n] ? n * 8 + gr : 0) * q.x_row;
   }
-  float acc[MT][NT][4];
+  float acc[NT][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
+  uint4 w[U][2];
+  auto load_weights = [&](int k0, bool early) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[m][n][e] = 0.0f;
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * kStep + t * kElems;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        w[u][i] = early ? load_row<T, WIDE, kEarly>(wp[i], k, q.K, k < q.K)
+                        : load_row<T, WIDE, kWeights>(wp[i], k, q.K, k < q.K);
+    }
+  };
+  const int first = warp * kStep * U;
+  // The second product's first weights do not wait for the first product: that has waited for all
+  // that came before it when this kernel may start.
+  if (!GATED) load_weights(first, true);
   ptx::pdl_wait();
   ptx::pdl_trigger();
 
-  for (int k0 = warp * kStep * U; k0 < q.K; k0 += kWarps * kStep * U) {
-    uint4 w[U][MT][2], x[U][NT];
+  for (int k0 = first; k0 < q.K; k0 += kWarps * kStep * U) {
+    uint4 x[U][NT];
+    if (GATED || k0 != first) load_weights(k0, false);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = k0 + u * kStep + t * kElems;
       const bool in = k < q.K;
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) w[u][m][i] = load_row<T, WIDE, true>(wp[m][i], k, q.K, in);
-#pragma unroll
       for (int n = 0; n < NT; ++n)
-        x[u][n] = load_row<T, WIDE, false>(xp[n], k, q.K, in && there[n]);
+        x[u][n] = load_row<T, WIDE, kTokens>(xp[n], k, q.K, in && there[n]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) step<T>(acc[m][n], w[u][m][0], w[u][m][1], x[u][n]);
+      for (int n = 0; n < NT; ++n) step<T>(acc[n], w[u][0], w[u][1], x[u][n]);
   }
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        sums[warp][m * 16 + gr + (e >> 1) * 8][n * 8 + 2 * t + (e & 1)] = acc[m][n][e];
+    for (int e = 0; e < 4; ++e)
+      sums[warp][gr + (e >> 1) * 8][n * 8 + 2 * t + (e & 1)] = acc[n][e];
   __syncthreads();
 
   // outputs: neighbouring threads have neighbouring rows of one token
-  for (int i = threadIdx.x; i < kRows * MT * NT * 8; i += kThreads) {
-    const int r = i % (kRows * MT), token = i / (kRows * MT), col = n0 + r;
+  for (int i = threadIdx.x; i < kRows * NT * 8; i += kThreads) {
+    const int r = i % kRows, token = i / kRows, col = n0 + r;
     if (token >= q.tokens || col >= q.N) continue;
-    const int at = GATED ? r / 8 * 16 + r % 8 : r;
     float v = 0.0f, u = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      v += sums[w][at][token];
-      if (GATED) u += sums[w][at + 8][token];
+      v += sums[w][r][token];
+      if (GATED) u += sums[w][r + 8][token];
     }
     if (q.bias[0]) v += to_f(((const T*)q.bias[0])[col]);
     if (GATED) {
@@ -203,15 +220,11 @@ __global__ void __launch_bounds__(kThreads, 2) mlp_few(const __grid_constant__ F
 
 template <typename T, bool WIDE, bool GATED>
 int run_as(const Few& q, cudaStream_t s) {
-  constexpr int MT = sizeof(T) == 4 ? 1 : 2;
   const int rows = GATED ? 8 : 16;
-  auto grid = [&](int mt) { return dim3((unsigned)((q.N + rows * mt - 1) / (rows * mt))); };
-  const dim3 block(kThreads);
-  if (q.tokens <= 8)
-    return launch_pdl(mlp_few<T, WIDE, GATED, 1, 1, 4>, grid(1), block, 0, s, q);
-  if (q.tokens <= 16)
-    return launch_pdl(mlp_few<T, WIDE, GATED, 2, MT, 2>, grid(MT), block, 0, s, q);
-  return launch_pdl(mlp_few<T, WIDE, GATED, 4, MT, 2>, grid(MT), block, 0, s, q);
+  const dim3 grid((unsigned)((q.N + rows - 1) / rows)), block(kThreads);
+  if (q.tokens <= 8) return launch_pdl(mlp_few<T, WIDE, GATED, 1, 4>, grid, block, 0, s, q);
+  if (q.tokens <= 16) return launch_pdl(mlp_few<T, WIDE, GATED, 2, 4>, grid, block, 0, s, q);
+  return launch_pdl(mlp_few<T, WIDE, GATED, 4, 2>, grid, block, 0, s, q);
 }
 
 // 16-byte accesses where every row of weights and tokens starts on one and has no rest.

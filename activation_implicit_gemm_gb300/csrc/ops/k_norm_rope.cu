@@ -184,7 +184,7 @@ template <typename T, int VEC, int R, bool IL>
 __global__ void __launch_bounds__(kThreads, R > 2 ? 1 : R == 2 ? 2 : 3)
     norm_rope_forward(const __grid_constant__ HeadGeom g) {
   using Row = Raw<T, VEC, IL>;
-  constexpr int A = ahead<T, VEC, R>(64);
+  constexpr int A = ahead<T, VEC, R>(VEC == 8 ? 32 : 64);
   ptx::pdl_wait();
   ptx::pdl_trigger();
   const bool is_k = (int)blockIdx.y >= g.side[0].groups;
