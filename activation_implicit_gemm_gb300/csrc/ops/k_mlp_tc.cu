@@ -1040,7 +1040,8 @@ Shape shape_of(const fconv_mlp_desc& d, int64_t tiles1, int64_t tiles2, int64_t 
       best.splits = splits;
     }
   }
-  if (d.dtype != FCONV_F32 && rounds(tiles2, sms / 2) * (kRound + kPair * steps) <= least)
+  if (d.dtype != FCONV_F32 && sms > 1 &&
+      rounds(tiles2, sms / 2) * (kRound + kPair * steps) <= least)
     best = Shape{2, 1};
   return best;
 }

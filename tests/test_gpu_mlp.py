@@ -254,3 +254,85 @@ def test_offsets_past_32_bits():
     for route in ("auto", "simple"):
         got = fc.gated_mlp(wide, wg.cuda(), wu.cuda(), wd.cuda(), route=route)
         R.check(got, val, tol, route)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n,c,f", [(1, 256, 640), (12, 264, 328), (3, 33, 47), (40, 96, 200)])
+def test_passes_that_follow_each_other(n, c, f, dtype):
+    """Inputs and weights are written in place right before each pass, and passes are not waited
+    for: kernels that start beside the ones before them read what those wrote."""
+    T = R.TYPES[dtype]
+    sets = []
+    for i in range(3):
+        x, wg, wu, wd, b, dy = case(140 + 10 * i, n, c, f, c, T)
+        sets.append([t.cuda() for t in (x, wg, wu, wd, *b, dy)])
+
+    def run(x, wg, wu, wd, bg, bu, bd, dy):
+        how = dict(b_gate=bg, b_up=bu, b_down=bd)
+        y, saved = fc.gated_mlp(x, wg, wu, wd, **how, return_saved=True)
+        return (y, *fc.gated_mlp_backward(dy, x, wg, wu, wd, saved, **how))
+
+    want = []
+    for s in sets:
+        want.append(run(*s))
+        torch.cuda.synchronize()
+    buffers = [t.clone() for t in sets[0]]
+    got = []
+    for i in range(30):
+        for b, t in zip(buffers, sets[i % 3]):
+            b.copy_(t)
+        got.append(run(*buffers))
+    torch.cuda.synchronize()
+    for i, outs in enumerate(got):
+        for a, b in zip(outs, want[i % 3]):
+            assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("n", [16, 32, 33])
+def test_two_streams_at_once(n):
+    """Calls of two streams, each with a workspace of its own, beside each other."""
+    ins = [case(170 + 10 * i, n, 320, 648, 320, torch.bfloat16) for i in range(2)]
+    dev = [[t.cuda() for t in (*v[:4], v[5])] for v in ins]
+
+    def run(x, wg, wu, wd, dy):
+        y, saved = fc.gated_mlp(x, wg, wu, wd, return_saved=True)
+        return (y, *fc.gated_mlp_backward(dy, x, wg, wu, wd, saved)[:4])
+
+    want = [run(*d) for d in dev]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(run(*dev[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for outs in got[i]:
+            for a, b in zip(outs, want[i]):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n", [40, 700])
+def test_unaligned_rows_in_16_bits(n):
+    """Odd sizes and odd strides, which are copied first, and results at odd strides."""
+    c, f, o, T = 77, 131, 59, torch.bfloat16
+    x, wg, wu, wd, b, dy = case(180, n, c, f, o, T)
+    wide = [torch.full((t.shape[0], t.shape[1] + 5), 9.0, dtype=T).cuda() for t in (x, wg, wu, wd, dy)]
+    views = []
+    for t, w in zip((x, wg, wu, wd, dy), wide):
+        w[:, 2:2 + t.shape[1]] = t.cuda()
+        views.append(w[:, 2:2 + t.shape[1]])
+    how = dict(b_gate=b[0].cuda(), b_up=b[1].cuda(), b_down=b[2].cuda())
+    ybuf, dxbuf = torch.full((n, o + 3), 9.0, dtype=T).cuda(), torch.full((n, c + 1), 9.0, dtype=T).cuda()
+    y, saved = fc.gated_mlp(*views[:4], **how, return_saved=True, out=ybuf[:, 1:1 + o])
+    grads = fc.gated_mlp_backward(views[4], *views[:4], saved, **how, dx=dxbuf[:, :c])
+    check_all({"y": y, **dict(zip(NAMES, grads))}, x, wg, wu, wd, b, dy)
+    assert (ybuf[:, 0] == 9).all() and (ybuf[:, 1 + o:] == 9).all() and (dxbuf[:, c:] == 9).all()
+
+
+@pytest.mark.parametrize("n,c,f,o", [(700, 1030, 500, 300), (60, 2000, 130, 90), (150, 90, 1500, 80)])
+def test_long_sums_in_f32(n, c, f, o):
+    """Sums that are split over passes and over blocks, of every product."""
+    ins = case(190, n, c, f, o, torch.float32)
+    check_all(both_passes(*ins, activation="Gelu"), *ins, activation="Gelu")
