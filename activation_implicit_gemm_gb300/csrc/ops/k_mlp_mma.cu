@@ -353,7 +353,7 @@ int backward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s)
   const SumsArgs m[3] = {{dg, d.hidden, d.hidden, 0, a.db_gate},
                          {du, d.hidden, d.hidden, 0, a.db_up},
                          {a.dy, d.dy_stride, d.out_features, 0, a.db_down}};
-  return launch_column_sums(d.dtype, false, m, d.tokens, (float*)matrix(d, a, 3), sms, s);
+  return launch_column_sums(d.dtype, false, false, m, d.tokens, (float*)matrix(d, a, 3), sms, s);
 }
 
 }  // namespace

@@ -1174,7 +1174,8 @@ int launch_mlp_tc_backward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, c
   void* to[3] = {a.db_gate, a.db_up, a.db_down};
   SumsArgs m[3];
   for (int i = 0; i < 3; ++i) m[i] = {from[i]->p, from[i]->stride, from[i]->cols, from[i]->plane, to[i]};
-  return launch_column_sums(d.dtype, d.dtype == FCONV_F32, m, T, l.sums, sms, s);
+  const bool early = a.dx || a.dw_gate || a.dw_up || a.dw_down;  // which waited for dg, du and dy
+  return launch_column_sums(d.dtype, d.dtype == FCONV_F32, early, m, T, l.sums, sms, s);
 }
 
 int read_and_clear_mlp_error(cudaStream_t s, unsigned* value) {

@@ -115,15 +115,16 @@ struct PrepArgs {
 int launch_mlp_prep(int dtype, const PrepArgs& a, cudaStream_t s);
 
 // Column sums of up to three matrices with the same rows (those without `out` are left out), of
-// dtype or, with `planes`, of f32 as three bf16 planes.
+// dtype or, with `planes`, of f32 as three bf16 planes. `early`: the launch before it has waited for
+// what made the matrices.
 struct SumsArgs {
   const void* p;
   int64_t row, cols, plane;  // strides of rows and planes in elements
   void* out;
 };
 size_t column_sums_workspace(const int64_t cols[3], int sms);
-int launch_column_sums(int dtype, bool planes, const SumsArgs m[3], int64_t rows, float* part,
-                       int sms, cudaStream_t s);
+int launch_column_sums(int dtype, bool planes, bool early, const SumsArgs m[3], int64_t rows,
+                       float* part, int sms, cudaStream_t s);
 
 struct AttnArgs {
   const void* q;
