@@ -4,7 +4,7 @@
 //             y = h Wd^T + bd
 //   backward  dh = dy Wd;  dg = dh u act'(g), du = dh act(g), h = act(g) u   in its epilogue
 //             dx = dg Wg + du Wu                         one sum over both
-//             dWg = dg^T x, dWu = du^T x, dWd = dy^T h   one launch
+//             dWg = dg^T x, dWu = du^T x, dWd = dy^T h   one launch, with dx where that is quicker
 // All of them are one kernel, D = A B^T with operands that run along K or along M and N in memory
 // (the descriptors transpose, nothing is copied), f32 sums in TMEM and an epilogue that adds
 // biases, gates, and rounds once.
@@ -57,6 +57,7 @@ struct Problem {
   CUtensorMap a[2], b[2], c[3];  // products of a sum (kGated: gate and up), outputs as boxes
   int mt, nt, steps;             // tiles, steps of a product
   int products;
+  int a_mn, b_mn;                // whether operands run along M or N in memory, not along K
   int64_t M;
   int N;
   const void* bias[2];
@@ -64,7 +65,7 @@ struct Problem {
   int64_t out_row;
 };
 struct Job {
-  Problem p[3];
+  Problem p[4];
   int problems, tiles;
   int splits;  // blocks of a tile, SPLIT
   float* saved;
@@ -273,11 +274,6 @@ __device__ __forceinline__ Step step_of(const Problem& p, int at, int len, int i
 __device__ __forceinline__ uint32_t pack16(bool bf16, float a, float b) {
   return bf16 ? pack2<true>(a, b) : pack2<false>(a, b);
 }
-__device__ __forceinline__ float2 unpack16(bool bf16, uint32_t v) {
-  if (bf16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-  return __half22float2(*reinterpret_cast<const __half2*>(&v));
-}
-
 // N words of a row (64 bytes, 32 values) of a staged box in the 64-byte swizzle, from word w0 on.
 template <int N>
 __device__ __forceinline__ void stage(uint32_t slot, int row, int w0, const uint32_t (&w)[N]) {
@@ -407,7 +403,7 @@ __device__ __forceinline__ void gate_grad_planes(uint32_t slots, int row, int c0
   if (!GATE) stage_planes(slots + kPlanes * kSlot, row, c0, h);
 }
 
-template <int CG, bool AMN, bool BMN, int EPI, bool F32, bool SPLIT>
+template <int CG, int EPI, bool F32, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Job j) {
   constexpr int S = kStages<EPI, F32>, BN = 128 * CG;
   constexpr int kCols = EPI == kGated ? BN / 2 : BN;  // of a tile of D
@@ -476,13 +472,13 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
           const int k = st.k * kStep, pa = st.a_plane, pb = st.b_plane;
           if (elect_lane()) {
             if (rank == 0) ptx::mbar_arrive_expect_tx(own, CG * kStageBytes);
-            if (AMN) {
+            if (EPI == kPlain && p.a_mn) {
               load_box<CG>(sa, ma, m0, k, pa, bar);
               load_box<CG>(sa + kBox, ma, m0 + 64, k, pa, bar);
             } else {
               load_box<CG>(sa, ma, k, m0, pa, bar);
             }
-            if (BMN) {
+            if (EPI != kGated && p.b_mn) {
               load_box<CG>(sb, mb, n0, k, pb, bar);
               load_box<CG>(sb + kBox, mb, n0 + 64, k, pb, bar);
             } else if (EPI == kGated && CG == 1) {
@@ -509,12 +505,16 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
     }
   } else if (warp == 1) {  // products
     if (rank == 0) {
-      const uint32_t idesc = idesc_16(F32 || j.bf16, 128 * CG, BN, BMN) | (AMN ? 1u << 15 : 0u);
       int it = 0, n = 0;
       bool ok = true;
       for (int id = first; ok && id < j.tiles; id += stride) {
         const Tile t = tile_of(j, id);
         const Problem& p = j.p[t.which];
+        const bool amn = EPI == kPlain && p.a_mn, bmn = EPI != kGated && p.b_mn;
+        const uint32_t idesc =
+            uni(idesc_16(F32 || j.bf16, 128 * CG, BN, bmn) | (amn ? 1u << 15 : 0u));
+        // a step of 16 of K: 32 bytes of a row, or 16 rows
+        const uint32_t a_next = uni(amn ? 128u : 2u), b_next = uni(bmn ? 128u : 2u);
         const Range r = range_of(p, EPI == kGated ? 1 : p.products, part, splits);
         for (int at = r.lo, len; ok && at < r.hi; at += len, ++n) {
           len = pass_steps<F32>(p, r, at);
@@ -529,13 +529,12 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
             if (!ok) break;
             ptx::tc_fence_after();
             const uint32_t sa = ring + s * kStageBytes, sb = sa + kSide;
-            const uint32_t a = uni(AMN ? desc_mn(sa, kBox) : desc_k(sa));
-            const uint32_t b = uni(BMN ? desc_mn(sb, kBox) : desc_k(sb));
+            const uint32_t a = uni(amn ? desc_mn(sa, kBox) : desc_k(sa));
+            const uint32_t b = uni(bmn ? desc_mn(sb, kBox) : desc_k(sb));
             if (elect_lane()) {
 #pragma unroll
-              for (int i = 0; i < kStep / 16; ++i)  // 16 elements of a row, or 16 rows
-                mma<CG>(d, a + i * (AMN ? 128 : 2), b + i * (BMN ? 128 : 2), idesc,
-                        k > 0 || i > 0);
+              for (int i = 0; i < kStep / 16; ++i)
+                mma<CG>(d, a + i * a_next, b + i * b_next, idesc, k > 0 || i > 0);
               commit<CG>(ptx::smem_addr(&ctl.empty[s]));
               if (k + 1 == steps) commit<CG>(ptx::smem_addr(&ctl.acc_full[n & 1]));
             }
@@ -869,9 +868,10 @@ bool map_of(EncodeTiledFn enc, CUtensorMap* m, const Matrix& x, bool bf16, int p
 // Blocks of a call: pairs of SMs (CG 2), single ones, or clusters of `splits` for each tile.
 struct Shape {
   int cg, splits;
+  double cost;
 };
 
-template <int CG, bool AMN, bool BMN, int EPI, bool F32>
+template <int CG, int EPI, bool F32>
 struct Builder {
   EncodeTiledFn enc = tensor_map_encoder();
   Job j{};
@@ -886,9 +886,11 @@ struct Builder {
     j.bf16 = d.dtype == FCONV_BF16;
     bf16 = F32 || j.bf16;
   }
-  // A new problem, D of M x N as sums over K.
-  Problem& add(int64_t M, int64_t N, int64_t K) {
+  // A new problem, D of M x N as sums over K, and how its operands lie.
+  Problem& add(int64_t M, int64_t N, int64_t K, bool a_mn, bool b_mn) {
     Problem& p = j.p[j.problems++];
+    p.a_mn = a_mn;
+    p.b_mn = b_mn;
     p.mt = (int)((M + 128 * CG - 1) / (128 * CG));
     p.nt = (int)((N + kCols - 1) / kCols);
     p.steps = (int)((K + kStep - 1) / kStep);
@@ -901,8 +903,8 @@ struct Builder {
     ok = ok && map_of(enc, m, x, bf16, F32 ? kPlanes : 1, 64, mn ? 64 : rows);
   }
   void product(Problem& p, const Matrix& a, const Matrix& b) {
-    operand(&p.a[p.products], a, AMN, 128);
-    operand(&p.b[p.products], b, BMN, EPI == kGated && CG == 1 ? 64 : 128);
+    operand(&p.a[p.products], a, p.a_mn, 128);
+    operand(&p.b[p.products], b, p.b_mn, EPI == kGated && CG == 1 ? 64 : 128);
     ++p.products;
   }
   // An operand of a later product.
@@ -931,7 +933,7 @@ struct Builder {
   template <bool SPLIT>
   int start(int blocks, int cluster, cudaStream_t s) {
     const size_t smem = kStages<EPI, F32> * 2 * kSide + kEpiWarps * kSlots<EPI, F32> * kSlot;
-    auto kernel = mlp_tc<CG, AMN, BMN, EPI, F32, SPLIT>;
+    auto kernel = mlp_tc<CG, EPI, F32, SPLIT>;
     if (const int e = allow_smem((const void*)kernel, smem)) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
@@ -959,8 +961,8 @@ struct Inputs {
 // h, and where `saved` is given the projections.
 template <int CG, bool F32>
 int gated(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const Inputs& in, cudaStream_t s) {
-  Builder<CG, false, false, kGated, F32> b(d, a.saved);
-  Problem& p = b.add(d.tokens, d.hidden, d.features);
+  Builder<CG, kGated, F32> b(d, a.saved);
+  Problem& p = b.add(d.tokens, d.hidden, d.features, false, false);
   b.product(p, in.x, in.gate);
   b.operand(&p.b[1], in.up, false, CG == 1 ? 64 : 128);
   p.bias[0] = a.b_gate;
@@ -971,8 +973,8 @@ int gated(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const 
 
 template <int CG, bool F32>
 int down(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const Inputs& in, cudaStream_t s) {
-  Builder<CG, false, false, kPlain, F32> b(d, nullptr);
-  Problem& p = b.add(d.tokens, d.out_features, d.hidden);
+  Builder<CG, kPlain, F32> b(d, nullptr);
+  Problem& p = b.add(d.tokens, d.out_features, d.hidden, false, false);
   b.product(p, in.h, in.down);
   p.bias[0] = a.b_down;
   b.result(p, a.y, d.tokens, d.out_features, d.y_stride);
@@ -982,8 +984,8 @@ int down(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const I
 template <int CG, bool F32>
 int grads_of_projections(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const Inputs& in,
                          cudaStream_t s) {
-  Builder<CG, false, true, kGrad, F32> b(d, a.saved);
-  Problem& p = b.add(d.tokens, d.hidden, d.out_features);
+  Builder<CG, kGrad, F32> b(d, a.saved);
+  Problem& p = b.add(d.tokens, d.hidden, d.out_features, false, true);
   b.product(p, in.dy, in.down);
   b.inner(p, 0, in.dg);
   b.inner(p, 1, in.du);
@@ -991,66 +993,83 @@ int grads_of_projections(const fconv_mlp_desc& d, int sms, int splits, const Mlp
   return b.launch(sms, splits, s);
 }
 
+// dx and the weights' gradients, of which `a` may leave some out.
 template <int CG, bool F32>
-int grad_of_input(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const Inputs& in,
-                  cudaStream_t s) {
-  Builder<CG, false, true, kPlain, F32> b(d, nullptr);
-  Problem& p = b.add(d.tokens, d.features, d.hidden);
-  b.product(p, in.dg, in.gate);
-  b.product(p, in.du, in.up);
-  b.result(p, a.dx, d.tokens, d.features, d.dx_stride);
-  return b.launch(sms, splits, s);
-}
-
-template <int CG, bool F32>
-int grads_of_weights(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const Inputs& in,
-                     cudaStream_t s) {
-  Builder<CG, true, true, kPlain, F32> b(d, nullptr);
-  auto one = [&](const Matrix& g, const Matrix& x, void* out) {
+int gradients(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const Inputs& in,
+              cudaStream_t s) {
+  Builder<CG, kPlain, F32> b(d, nullptr);
+  if (a.dx) {
+    Problem& p = b.add(d.tokens, d.features, d.hidden, false, true);
+    b.product(p, in.dg, in.gate);
+    b.product(p, in.du, in.up);
+    b.result(p, a.dx, d.tokens, d.features, d.dx_stride);
+  }
+  auto weight = [&](const Matrix& g, const Matrix& x, void* out) {
     if (!out) return;
-    Problem& p = b.add(g.cols, x.cols, d.tokens);
+    Problem& p = b.add(g.cols, x.cols, d.tokens, true, true);
     b.product(p, g, x);
     b.result(p, out, g.cols, x.cols, x.cols);
   };
-  one(in.dg, in.x, a.dw_gate);
-  one(in.du, in.x, a.dw_up);
-  one(in.dy, in.h, a.dw_down);
+  weight(in.dg, in.x, a.dw_gate);
+  weight(in.du, in.x, a.dw_up);
+  weight(in.dy, in.h, a.dw_down);
   return b.launch(sms, splits, s);
 }
 
-// The blocks of a product of M x N (in columns of accumulators: gated ones have two for each of
-// D) with `steps` steps of K, or of several with their tiles together: what takes the least time,
-// counted in steps of a single SM's tile (0.19 us where operands come from HBM). A step of a pair of
-// SMs takes 1.2 of them, a round of tiles 4 to 6 more, a cluster's start and its exchange of sums 12
-// to 24 (196 tokens, 2048 to 768: 13.7 us with 12 blocks, 12.2, 10.9 and 12.0 with 2, 4 and 8 times
-// as many; 768 to 2048 in 64 tiles: 9.9 and 11.4). Clusters of 4 and 8 leave SMs of a GPC unused.
-Shape shape_of(const fconv_mlp_desc& d, int64_t tiles1, int64_t tiles2, int64_t steps, int sms) {
+// Tiles of one length: those of a product of M x N (in columns of accumulators: gated ones have two
+// for each of D), of one SM and of a pair, and their steps of K.
+struct Group {
+  int64_t tiles1, tiles2, steps;
+};
+Group group_of(int64_t M, int64_t N, int64_t K, int products) {
+  auto tiles = [&](int side) { return ((M + side - 1) / side) * ((N + side - 1) / side); };
+  return Group{tiles(128), tiles(256), products * ((K + kStep - 1) / kStep)};
+}
+
+// The blocks of a launch: what takes the least time, counted in steps of a single SM's tile (0.19 us
+// where operands come from HBM). A step of a pair of SMs takes 1.2 of them, a round of tiles 4 to 6
+// more, a cluster's start and its exchange of sums 12 to 24 (196 tokens, 2048 to 768: 13.7 us with 12
+// blocks, 12.2, 10.9 and 12.0 with 2, 4 and 8 times as many; 768 to 2048 in 64 tiles: 9.9 and 11.4).
+// Clusters of 4 and 8 leave SMs of a GPC unused.
+Shape shape_of(const fconv_mlp_desc& d, const Group* g, int n, int sms) {
   constexpr double kRound = 4.0, kSplitRound = 6.0, kPair = 1.2, kGain = 0.93;
   const double terms = d.dtype == FCONV_F32 ? kTerms : 1;
-  auto rounds = [](int64_t tiles, int64_t slots) { return (double)((tiles + slots - 1) / slots); };
-  Shape best{1, 1};
-  double least = rounds(tiles1, sms) * (kRound + terms * steps);
+  // rounds of `slots` tiles, each as long as the longest of them
+  auto cost = [&](bool pairs, int64_t slots, double round, double step, int splits) {
+    double sum = 0.0;
+    int64_t over = 0;  // slots of the last round that the next group can use
+    for (int i = 0; i < n; ++i) {
+      int64_t tiles = pairs ? g[i].tiles2 : g[i].tiles1;
+      const int64_t used = tiles < over ? tiles : over;
+      over -= used;
+      tiles -= used;
+      const int64_t rounds = (tiles + slots - 1) / slots;
+      sum += (double)rounds * (round + step * (double)((g[i].steps + splits - 1) / splits));
+      if (rounds > 0) over = rounds * slots - tiles;
+    }
+    return sum;
+  };
+  int64_t least_steps = g[0].steps, tiles = 0;
+  for (int i = 0; i < n; ++i) {
+    if (g[i].steps < least_steps) least_steps = g[i].steps;
+    tiles += g[i].tiles1;
+  }
+  Shape best{1, 1, cost(false, sms, kRound, terms, 1)};
   for (int splits = 2; splits <= 8; splits *= 2) {
     const int64_t slots = sms / splits - (splits == 8 ? 3 : splits == 4 ? 2 : 0);
-    if (slots < 1 || steps < 2 * splits || tiles1 * splits > (1 << 30)) break;
-    const double each = kSplitRound + terms * ((steps + splits - 1) / splits);
-    const double cost = 8 + 2 * splits + rounds(tiles1, slots) * each;
-    if (cost < kGain * least) {
-      least = cost;
-      best.splits = splits;
-    }
+    if (slots < 1 || least_steps < 2 * splits || tiles * splits > (1 << 30)) break;
+    const double c = 8 + 2 * splits + cost(false, slots, kSplitRound, terms, splits);
+    if (c < kGain * best.cost) best = Shape{1, splits, c};
   }
-  if (d.dtype != FCONV_F32 && sms > 1 &&
-      rounds(tiles2, sms / 2) * (kRound + kPair * steps) <= least)
-    best = Shape{2, 1};
+  if (d.dtype != FCONV_F32 && sms > 1) {
+    const double c = cost(true, sms / 2, kRound, kPair, 1);
+    if (c <= best.cost) best = Shape{2, 1, c};
+  }
   return best;
 }
-int64_t tiles_of(int64_t M, int64_t N, int side) {
-  return ((M + side - 1) / side) * ((N + side - 1) / side);
-}
-Shape shape_of(const fconv_mlp_desc& d, int64_t M, int64_t N, int64_t K, int products, int sms) {
-  return shape_of(d, tiles_of(M, N, 128), tiles_of(M, N, 256),
-                  products * ((K + kStep - 1) / kStep), sms);
+Shape shape_of(const fconv_mlp_desc& d, int64_t M, int64_t N, int64_t K, int sms) {
+  const Group g = group_of(M, N, K, 1);
+  return shape_of(d, &g, 1, sms);
 }
 #define FCONV_BY_SHAPE(v, call)                                          \
   (d.dtype == FCONV_F32 ? call<1, true>(d, sms, (v).splits, a, l.in, s)  \
@@ -1114,13 +1133,27 @@ Layout layout(const fconv_mlp_desc& d, const MlpArgs& a, bool backward, int sms)
   return l;
 }
 
+int gradients_by_shape(const fconv_mlp_desc& d, int sms, const Shape& v, const MlpArgs& a,
+                       const Layout& l, cudaStream_t s) {
+  return FCONV_BY_SHAPE(v, gradients);
+}
+// A call that wants dx alone, or the weights' gradients alone.
+MlpArgs only(const MlpArgs& a, bool dx) {
+  MlpArgs v = a;
+  if (dx)
+    v.dw_gate = v.dw_up = v.dw_down = nullptr;
+  else
+    v.dx = nullptr;
+  return v;
+}
+
 // g, u and h (few tokens: if wanted).
 int projections(const fconv_mlp_desc& d, int sms, const MlpArgs& a, const Layout& l, bool want_h,
                 cudaStream_t s) {
   if (d.tokens <= kMlpFewTokens)
     return launch_mlp_few_gated(d, a, want_h ? const_cast<void*>(l.in.h.p) : nullptr,
                                 l.in.h.stride, s);
-  return FCONV_BY_SHAPE(shape_of(d, d.tokens, 2 * d.hidden, d.features, 1, sms), gated);
+  return FCONV_BY_SHAPE(shape_of(d, d.tokens, 2 * d.hidden, d.features, sms), gated);
 }
 
 }  // namespace
@@ -1148,7 +1181,7 @@ int launch_mlp_tc_forward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cu
   if (!e) e = projections(d, sms, a, l, true, s);
   if (e) return e;
   if (d.tokens <= kMlpFewTokens) return launch_mlp_few_down(d, a, l.in.h.p, l.in.h.stride, s);
-  return FCONV_BY_SHAPE(shape_of(d, d.tokens, d.out_features, d.hidden, 1, sms), down);
+  return FCONV_BY_SHAPE(shape_of(d, d.tokens, d.out_features, d.hidden, sms), down);
 }
 
 int launch_mlp_tc_backward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s) {
@@ -1157,24 +1190,38 @@ int launch_mlp_tc_backward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, c
   int e = launch_mlp_prep(d.dtype, l.prep, s);
   // made again, the projections are the forward pass's bit by bit
   if (!e && a.remake) e = projections(d, sms, a, l, false, s);
-  if (!e) e = FCONV_BY_SHAPE(shape_of(d, T, F, O, 1, sms), grads_of_projections);
-  if (!e && a.dx) e = FCONV_BY_SHAPE(shape_of(d, T, D, F, 2, sms), grad_of_input);
-  if (!e && (a.dw_gate || a.dw_up || a.dw_down)) {
-    int64_t tiles[2];
-    for (int i = 0; i < 2; ++i) {
-      const int side = 128 * (i + 1);
-      tiles[i] = ((a.dw_gate != nullptr) + (a.dw_up != nullptr)) * tiles_of(F, D, side) +
-                 (a.dw_down != nullptr) * tiles_of(O, F, side);
+  if (!e) e = FCONV_BY_SHAPE(shape_of(d, T, F, O, sms), grads_of_projections);
+  // Nothing of dx goes into the weights' gradients or back, so tiles of all may share the GPU in one
+  // launch of persistent blocks, unless their lengths want shapes of their own (few tokens: long sums
+  // for dx, short ones for the weights). Both passes of 6304 x 768 x 2048 in f16: 186 us with two
+  // launches, 182 with one; the gradients of 100 x 3000 x 4000 in f32: 259 and 406 us; clusters that
+  // took both gained nothing (999 x 333 x 777, f32, both passes: 123 and 130).
+  Group g[4];
+  int n = 0;  // in the order of the launch's problems
+  if (a.dx) g[n++] = group_of(T, D, F, 2);
+  const int after_dx = n;
+  if (a.dw_gate) g[n++] = group_of(F, D, T, 1);
+  if (a.dw_up) g[n++] = group_of(F, D, T, 1);
+  if (a.dw_down) g[n++] = group_of(O, F, T, 1);
+  if (!e && n > 0) {
+    constexpr double kLaunch = 10.0;  // steps that a launch of its own costs
+    const Shape all = shape_of(d, g, n, sms);
+    const Shape first = after_dx > 0 ? shape_of(d, g, after_dx, sms) : all;
+    const Shape rest = n > after_dx ? shape_of(d, g + after_dx, n - after_dx, sms) : all;
+    if (after_dx > 0 && n > after_dx &&
+        (all.splits > 1 || first.cost + rest.cost + kLaunch < all.cost)) {
+      e = gradients_by_shape(d, sms, first, only(a, true), l, s);
+      if (!e) e = gradients_by_shape(d, sms, rest, only(a, false), l, s);
+    } else {
+      e = gradients_by_shape(d, sms, all, a, l, s);
     }
-    e = FCONV_BY_SHAPE(shape_of(d, tiles[0], tiles[1], (T + kStep - 1) / kStep, sms),
-                       grads_of_weights);
   }
   if (e) return e;
   const Matrix* from[3] = {&l.in.dg, &l.in.du, &l.in.dy};
   void* to[3] = {a.db_gate, a.db_up, a.db_down};
   SumsArgs m[3];
   for (int i = 0; i < 3; ++i) m[i] = {from[i]->p, from[i]->stride, from[i]->cols, from[i]->plane, to[i]};
-  const bool early = a.dx || a.dw_gate || a.dw_up || a.dw_down;  // which waited for dg, du and dy
+  const bool early = n > 0;  // the launch before has waited for dg, du and dy
   return launch_column_sums(d.dtype, d.dtype == FCONV_F32, early, m, T, l.sums, sms, s);
 }
 

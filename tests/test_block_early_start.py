@@ -39,7 +39,7 @@ def test_bias_sums_come_from_l2_and_end_last():
     assert "__shared__" not in kernel
     # `early` only after a product that has waited for dg, du and dy
     back = body(source("k_mlp_tc.cu"), "launch_mlp_tc_backward")
-    assert "early = a.dx || a.dw_gate || a.dw_up || a.dw_down" in back
+    assert "early = n > 0" in back and "if (!e && n > 0) {" in back
     tc = body(source("k_mlp_tc.cu"), "mlp_tc")
     assert tc.index("ptx::pdl_wait();") < tc.index("ptx::pdl_trigger();")
     assert "launch_column_sums(d.dtype, false, false," in source("k_mlp_mma.cu")
