@@ -911,9 +911,10 @@ struct Builder {
   void inner(Problem& p, int i, const Matrix& c) {
     ok = ok && map_of(enc, &p.c[i], c, bf16, F32 ? kPlanes : 1, 32, 32);
   }
-  // A result of the call: by boxes where its rows start on 16 bytes.
+  // A result of the call: by boxes where its rows are whole 16-byte units (a box writes the unit that
+  // a row ends in as a whole) and start on one.
   void result(Problem& p, void* out, int64_t rows, int64_t cols, int64_t stride) {
-    if (!F32 && (uintptr_t)out % 16 == 0 && (rows <= 1 || stride % 8 == 0)) {
+    if (!F32 && cols % 8 == 0 && (uintptr_t)out % 16 == 0 && (rows <= 1 || stride % 8 == 0)) {
       inner(p, 0, {out, rows, cols, stride, 0});
     } else {
       p.out = out;

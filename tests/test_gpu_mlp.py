@@ -336,3 +336,63 @@ def test_long_sums_in_f32(n, c, f, o):
     """Sums that are split over passes and over blocks, of every product."""
     ins = case(190, n, c, f, o, torch.float32)
     check_all(both_passes(*ins, activation="Gelu"), *ins, activation="Gelu")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("n", [7, 140])
+def test_odd_sizes_in_aligned_rows(n, dtype):
+    """Rows that start on 16 bytes but do not fill them are read and written where they are."""
+    c, f, o, T = 77, 131, 59, R.TYPES[dtype]
+    x, wg, wu, wd, b, dy = case(210, n, c, f, o, T)
+    views = []
+    for t in (x, wg, wu, wd, dy):
+        wide = torch.full((t.shape[0], (t.shape[1] + 15) // 8 * 8), float("nan"), dtype=T).cuda()
+        wide[:, :t.shape[1]] = t.cuda()
+        views.append(wide[:, :t.shape[1]])
+    how = dict(b_gate=b[0].cuda(), b_up=b[1].cuda(), b_down=b[2].cuda())
+    ybuf, dxbuf = (torch.full((n, m), 9.0, dtype=T).cuda() for m in (64, 80))
+    y, saved = fc.gated_mlp(*views[:4], **how, return_saved=True, out=ybuf[:, :o])
+    grads = fc.gated_mlp_backward(views[4], *views[:4], saved, **how, dx=dxbuf[:, :c])
+    check_all({"y": y, **dict(zip(NAMES, grads))}, x, wg, wu, wd, b, dy)
+    assert (ybuf[:, o:] == 9).all() and (dxbuf[:, c:] == 9).all()
+
+
+@pytest.mark.parametrize("route", ["simple", "auto"])
+@pytest.mark.parametrize("n", [4, 60])
+def test_largest_values_in_f32(n, route):
+    """Values up to f32's largest, whose first plane would round to an infinity, against weights that
+    bring them back."""
+    x, wg, wu, wd, b, dy = case(220, n, 64, 72, 40, torch.float32)
+    top = torch.finfo(torch.float32).max
+    x = (x.double() * 2e38).clamp(-top, top).float()
+    x[0, :5] = top
+    wg, wu, wd = wg * 1e-33, wu * 1e-33, wd * 1e-9
+    b = [t * 1e3 for t in b]
+    got = both_passes(x, wg, wu, wd, b, dy, activation="Relu", route=route)
+    for name in ("y", "dx", "db_down"):  # the weights' gradients pass the type's largest
+        R.check(got[name], *B.gated_mlp(x, wg, wu, wd, *b, "Relu", dy=dy)[name], name)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [40, 300])
+def test_each_gradient_alone(n, dtype):
+    """Any subset of the gradients through the plan, with the bits of the whole call."""
+    x, wg, wu, wd, b, dy = case(230, n, 96, 136, 64, R.TYPES[dtype])
+    whole = both_passes(x, wg, wu, wd, b, dy)
+    dev = [t.cuda() for t in (dy, x, wg, wu, wd, b[0], b[1])]
+    p = fc.MlpPlan(_ops._code(x.dtype), n, 96, 136, 64, x_stride=96, y_stride=64, gate_stride=96,
+                   up_stride=96, down_stride=136, dy_stride=64, dx_stride=96, has_b_gate=True,
+                   has_b_up=True, has_b_down=True, training=True)
+    ws = torch.empty(p.backward_workspace, dtype=torch.uint8, device="cuda")
+    shapes = [(n, 96), (136, 96), (136, 96), (64, 136), (136,), (136,), (64,)]
+    for which in ((0,), (1,), (2, 3), (4,), (0, 4, 5, 6), (3, 6), ()):
+        outs = [torch.empty(s, dtype=x.dtype, device="cuda") if i in which else None
+                for i, s in enumerate(shapes)]
+        p.backward_ptrs(*(t.data_ptr() for t in dev), None, *map(_ops._ptr, outs), ws.data_ptr(),
+                        ws.numel(), torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        for i in which:
+            a, ref = outs[i], whole[NAMES[i]]
+            # a launch of fewer products may take another shape, whose sums come in another order
+            assert torch.equal(a, ref) or torch.allclose(a.double(), ref.double(), rtol=0.02,
+                                                         atol=0.02 * ref.double().abs().max().item())
