@@ -966,7 +966,8 @@ struct Inputs {
 
 // h, and where `saved` is given the projections.
 template <int CG, bool F32>
-int gated(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const Inputs& in, cudaStream_t s) {
+int gated(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const Inputs& in,
+          cudaStream_t s) {
   Builder<CG, kGated, F32> b(d, a.saved);
   Problem& p = b.add(d.tokens, d.hidden, d.features, false, false);
   b.product(p, in.x, in.gate);
@@ -978,7 +979,8 @@ int gated(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const 
 }
 
 template <int CG, bool F32>
-int down(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const Inputs& in, cudaStream_t s) {
+int down(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const Inputs& in,
+         cudaStream_t s) {
   Builder<CG, kPlain, F32> b(d, nullptr);
   Problem& p = b.add(d.tokens, d.out_features, d.hidden, false, false);
   b.product(p, in.h, in.down);
@@ -988,8 +990,8 @@ int down(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const I
 }
 
 template <int CG, bool F32>
-int grads_of_projections(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const Inputs& in,
-                         cudaStream_t s) {
+int grads_of_projections(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a,
+                         const Inputs& in, cudaStream_t s) {
   Builder<CG, kGrad, F32> b(d, a.saved);
   Problem& p = b.add(d.tokens, d.hidden, d.out_features, false, true);
   b.product(p, in.dy, in.down);

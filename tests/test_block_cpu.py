@@ -301,6 +301,40 @@ def test_mlp_arguments(monkeypatch):
     assert len(calls) == done
 
 
+def test_a_stream_of_another_device_is_refused():
+    class Stream:
+        device = torch.device("cuda", 0)
+
+    class There(torch.Tensor):
+        def get_device(self):
+            return 1
+
+    q = torch.zeros(1, 2, 2, 8).as_subclass(There)
+    w = torch.zeros(8, 8).as_subclass(There)
+    for call in (lambda: _ops.norm_rope(q, stream=Stream()),
+                 lambda: _ops.norm_rope_backward(q, q, stream=Stream()),
+                 lambda: _ops.gated_mlp(w, w, w, w, stream=Stream()),
+                 lambda: _ops.gated_mlp_backward(w, w, w, w, w, stream=Stream())):
+        with pytest.raises(ValueError, match="stream"):
+            call()
+
+
+def test_plan_caches_drop_their_oldest(monkeypatch):
+    monkeypatch.setattr(_ops, "_run", lambda *a: None)
+    monkeypatch.setattr(_ops, "_on_cuda", lambda *a: None)
+    monkeypatch.setattr(_ops, "_current_stream", lambda device: 0)
+    monkeypatch.setattr(_ops, "_KEPT", 4)
+    for cache in (_ops._norm_rope_plans, _ops._mlp_plans):
+        cache.clear()
+    w = torch.zeros(8, 8)
+    for n in range(1, 10):
+        _ops.norm_rope(torch.zeros(1, n, 2, 8))
+        _ops.gated_mlp(torch.zeros(n, 8), w, w, w)
+    assert len(_ops._norm_rope_plans) == 4 and len(_ops._mlp_plans) == 4
+    for cache in (_ops._norm_rope_plans, _ops._mlp_plans):
+        cache.clear()
+
+
 # --------------------------------------------------------------------------- 64-bit forms
 
 @pytest.mark.parametrize("pairing", ["half", "interleaved", "half_per_axis"])
