@@ -32,11 +32,12 @@ __device__ __forceinline__ float act_exact(float alpha, float v, float& slope) {
     if (SLOPE) slope = p + v * 0.3989422804014327f * expf(-0.5f * v * v);
     return v * p;
   } else if (ACT == FCONV_ACT_FASTGELU) {
-    constexpr float k = 0.7978845608028654f, c = 0.044715f;  // sqrt(2 / pi)
-    const float th = tanhf(k * (v + c * v * v * v));
-    if (SLOPE)
-      slope = 0.5f * (1.0f + th) + 0.5f * v * (1.0f - th * th) * k * (1.0f + 3.0f * c * v * v);
-    return 0.5f * v * (1.0f + th);
+    // (1 + tanh z) / 2 is the logistic function of 2 z; 1 + tanh z itself would cancel for v < 0
+    constexpr float k = 1.5957691216057308f, c = 0.044715f;  // sqrt(8 / pi)
+    const float v2 = v * v, w = v * fmaf(k * c, v2, k);
+    const float p = 1.0f / (1.0f + expf(-w));
+    if (SLOPE) slope = p + v * fmaf(3.0f * k * c, v2, k) * p * (1.0f / (1.0f + expf(w)));
+    return v * p;
   } else {
     if (SLOPE) slope = 1.0f;
     return v;
