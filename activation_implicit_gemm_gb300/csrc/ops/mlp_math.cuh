@@ -13,6 +13,16 @@ namespace fconv {
 namespace ops {
 namespace {
 
+// v, held within -most and most; NaN stays.
+__device__ __forceinline__ float within(float v, float most) {
+  float y;
+  asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(y) : "f"(v), "f"(most));
+  return y;
+}
+// Past it FastGelu is v or 0 and its slope 1 or 0 in f32 (from |v| = 6 and 12 on): held there, the
+// powers of v that meet them stay finite.
+constexpr float kFastGeluEnd = 32.0f;
+
 // act(v) in f32, and with SLOPE its derivative.
 template <int ACT, bool SLOPE>
 __device__ __forceinline__ float act_exact(float alpha, float v, float& slope) {
@@ -34,9 +44,9 @@ __device__ __forceinline__ float act_exact(float alpha, float v, float& slope) {
   } else if (ACT == FCONV_ACT_FASTGELU) {
     // (1 + tanh z) / 2 is the logistic function of 2 z; 1 + tanh z itself would cancel for v < 0
     constexpr float k = 1.5957691216057308f, c = 0.044715f;  // sqrt(8 / pi)
-    const float v2 = v * v, w = v * fmaf(k * c, v2, k);
+    const float x = within(v, kFastGeluEnd), x2 = x * x, w = x * fmaf(k * c, x2, k);
     const float p = 1.0f / (1.0f + expf(-w));
-    if (SLOPE) slope = p + v * fmaf(3.0f * k * c, v2, k) * p * (1.0f / (1.0f + expf(w)));
+    if (SLOPE) slope = p + x * fmaf(3.0f * k * c, x2, k) * p * (1.0f / (1.0f + expf(w)));
     return v * p;
   } else {
     if (SLOPE) slope = 1.0f;
@@ -114,9 +124,9 @@ __device__ __forceinline__ float act_fast(float alpha, float v, float& slope) {
     return v * p;
   } else if (ACT == FCONV_ACT_FASTGELU) {  // (1 + tanh z) / 2 is the logistic function of 2 z
     constexpr float k = 0.7978845608028654f, c = 0.044715f;
-    const float v2 = v * v, z = v * fmaf(k * c, v2, k);
+    const float x = within(v, kFastGeluEnd), x2 = x * x, z = x * fmaf(k * c, x2, k);
     const float p = logistic2(z * (2.0f * kLog2e));
-    if (SLOPE) slope = p * fmaf(2.0f * v * (1.0f - p), fmaf(3.0f * k * c, v2, k), 1.0f);
+    if (SLOPE) slope = p * fmaf(2.0f * x * (1.0f - p), fmaf(3.0f * k * c, x2, k), 1.0f);
     return v * p;
   } else {
     if (SLOPE) slope = 1.0f;

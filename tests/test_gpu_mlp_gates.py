@@ -106,3 +106,31 @@ def test_each_gate_value_relative_to_itself(kind, params, dtype, n, route):
     scaled = back(scale)
     for name, got in (("dw_up", scaled[2][:, 0]), ("db_up", scaled[5])):
         R.check(got, h, rel * h.abs() + 2 * TINY[T], name)
+
+
+@pytest.mark.parametrize("route", ["auto", "simple"])
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["Silu", "Gelu", "FastGelu", "Sigmoid"])
+def test_gates_of_any_size(kind, dtype, n, route):
+    """Gates whose square or cube no f32 holds: act(g) is g or 0 (Sigmoid 1 or 0), its slope 1 or 0
+    (Sigmoid 0)."""
+    T = R.TYPES[dtype]
+    values = torch.cat([torch.logspace(2, 38, F // 2), -torch.logspace(2, 38, F // 2)]).to(T)
+    x, g, u = torch.zeros(n, 8, dtype=T), torch.zeros(F, 8, dtype=T), torch.zeros(F, 8, dtype=T)
+    x[:, 0], g[:, 0], u[:, 0] = 1.0, values, 1.0
+    # half an identity: sums hold no more than one value, and none of them passes the type
+    dev = [t.cuda() for t in (x, g, u, (torch.eye(F) / 2).to(T))]
+    y, saved = fc.gated_mlp(*dev, activation=kind, route=route, return_saved=True)
+    dy = torch.zeros(n, F, dtype=T)
+    dy[-1] = 2.0
+    grads = fc.gated_mlp_backward(dy.cuda(), *dev, saved, activation=kind, route=route)
+    v = values.double()
+    on = (v > 0).double()
+    a = on if kind == "Sigmoid" else v.clamp(min=0.0)
+    slope = torch.zeros_like(v) if kind == "Sigmoid" else on
+    # at -100 all but Sigmoid's and Silu's exponentials are 0 in f32, and those are under 4e-42
+    tiny, rel = 1e-40, 2.02 * U[T] + 32 * E32
+    R.check(y[-1], a / 2, rel * a + tiny, "y")
+    R.check(grads[2][:, 0], a, rel * a + tiny, "dw_up")
+    R.check(grads[1][:, 0], slope, rel * slope + tiny, "dw_gate")
