@@ -1104,7 +1104,9 @@ struct Layout {
 };
 Layout layout(const fconv_mlp_desc& d, const MlpArgs& a, bool backward, int sms) {
   Layout l;
-  const int planes = d.dtype == FCONV_F32 ? kPlanes : 1;
+  const bool few = d.tokens <= kMlpFewTokens;
+  // of what the workspace holds: f32 operands in three parts, 16-bit h of few tokens in two
+  const int planes = d.dtype == FCONV_F32 ? kPlanes : few && !backward ? 2 : 1;
   char* base = (char*)a.ws;
   auto take = [&](size_t bytes) {
     char* p = base + l.bytes;
@@ -1124,7 +1126,6 @@ Layout layout(const fconv_mlp_desc& d, const MlpArgs& a, bool backward, int sms)
     return m;
   };
   l.in.h = fresh(d.tokens, d.hidden);
-  const bool few = d.tokens <= kMlpFewTokens;
   if (backward) {
     l.in.dg = fresh(d.tokens, d.hidden);
     l.in.du = fresh(d.tokens, d.hidden);
@@ -1160,7 +1161,7 @@ int projections(const fconv_mlp_desc& d, int sms, const MlpArgs& a, const Layout
                 cudaStream_t s) {
   if (d.tokens <= kMlpFewTokens)
     return launch_mlp_few_gated(d, a, want_h ? const_cast<void*>(l.in.h.p) : nullptr,
-                                l.in.h.stride, s);
+                                l.in.h.stride, l.in.h.plane, s);
   return FCONV_BY_SHAPE(shape_of(d, d.tokens, 2 * d.hidden, d.features, sms), gated);
 }
 
@@ -1188,7 +1189,7 @@ int launch_mlp_tc_forward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cu
   int e = launch_mlp_prep(d.dtype, l.prep, s);
   if (!e) e = projections(d, sms, a, l, true, s);
   if (e) return e;
-  if (d.tokens <= kMlpFewTokens) return launch_mlp_few_down(d, a, l.in.h.p, l.in.h.stride, s);
+  if (d.tokens <= kMlpFewTokens) return launch_mlp_few_down(d, a, l.in.h.p, l.in.h.stride, l.in.h.plane, s);
   return FCONV_BY_SHAPE(shape_of(d, d.tokens, d.out_features, d.hidden, sms), down);
 }
 

@@ -95,12 +95,12 @@ int launch_mlp_tc_forward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cu
 int launch_mlp_tc_backward(const fconv_mlp_desc& d, int sms, const MlpArgs& a, cudaStream_t s);
 int read_and_clear_mlp_error(cudaStream_t s, unsigned* value);
 // Its products for up to kMlpFewTokens tokens (k_mlp_few.cu); h has rows of h_row elements of the
-// call's type (gated: may be null).
+// call's type (gated: may be null), in 16-bit types twice, its second part h_plane elements on.
 constexpr int kMlpFewTokens = 32;
 int launch_mlp_few_gated(const fconv_mlp_desc& d, const MlpArgs& a, void* h, int64_t h_row,
-                         cudaStream_t s);
+                         int64_t h_plane, cudaStream_t s);
 int launch_mlp_few_down(const fconv_mlp_desc& d, const MlpArgs& a, const void* h, int64_t h_row,
-                        cudaStream_t s);
+                        int64_t h_plane, cudaStream_t s);
 
 // Tensors copied into rows of whole 16-byte units, f32 as three bf16 planes (k_mlp_prep.cu).
 struct PrepItem {
