@@ -753,7 +753,7 @@ def _gate(who, activation, params):
         return GATES["QuickGelu"], 1.0
     if activation not in GATES:
         raise ValueError(f"{who}: activation must be Silu or one of {list(GATES)}")
-    params = [] if params is None else list(params)
+    params = params or ()
     if len(params) > (activation == "QuickGelu"):
         raise ValueError(f"{who}: {activation} takes fewer parameters")
     return GATES[activation], float(params[0]) if params else 1.702
@@ -763,9 +763,9 @@ def _mlp_plan(who, x, weights, biases, activation, params, route, device, y, dx=
     """The cached plan of a call. With dx it is a backward pass's, whose dy is y. Everything the
     checks look at is in the key, but a result that the call made itself (not `given`)."""
     wg, wu, wd = weights
+    params = None if params is None else tuple(params)  # once: an iterator has no second time
     key = (x.dtype, x.shape, x.stride(), wg.dtype, wg.shape, wg.stride(), wu.dtype, wu.shape,
-           wu.stride(), wd.dtype, wd.shape, wd.stride(), activation,
-           None if params is None else tuple(params), route, device)
+           wu.stride(), wd.dtype, wd.shape, wd.stride(), activation, params, route, device)
     for b in biases:
         key += (None,) if b is None else (b.dtype, b.shape, b.is_contiguous())
     if dx is not None:
