@@ -818,7 +818,9 @@ def gated_mlp(x, w_gate, w_up, w_down, *, b_gate=None, b_up=None, b_down=None,
     one stride apart, so gate and up may be halves of one packed weight. activation is Silu, Gelu
     (erf), FastGelu (tanh), QuickGelu (activation_params: alpha), Relu, Sigmoid or None. With
     return_saved also what the gradient takes: both projections in float32, 8 bytes a token and
-    hidden value, in an order of the library's own."""
+    hidden value, in an order of the library's own. Over 32 tokens in float16 or bfloat16, tensors
+    whose rows are whole units of 16 bytes should start on one: a base off it takes a kernel without
+    tcgen05, up to 50 times as long."""
     if torch is None:
         _start()
     if stream is not None:

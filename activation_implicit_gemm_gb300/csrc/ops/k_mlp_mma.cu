@@ -1,5 +1,8 @@
-// The gated feed-forward block without tcgen05 (include/fconv_ops.h): f32, and f16 and bf16 calls
-// whose sizes, strides or addresses TMA does not take.
+// The gated feed-forward block without tcgen05 (include/fconv_ops.h), every type, size, stride and
+// address: all calls of a plan made for it. Others come here only with an f16 or bf16 operand in rows
+// that TMA takes at an address off 16 bytes, which it does not (operands in other rows, and f32, are
+// copied first), and without tokens, for gradients of zero. 16384 x 4096 x 10240 in bf16, forward:
+// 122 ms, against 2.4 ms on tcgen05.
 //
 // Every product is one kernel, D = A B^T with any strides of both, on m16n8k8 TF32 instructions.
 // An f32 value is hi (rounded to TF32) + lo; a product is lo hi + hi lo + hi hi, which drops about

@@ -11,11 +11,12 @@
  * used from several streams at once as long as each call has a workspace of its own.
  *
  * Every sum, softmax statistic and norm is held in f32; each output is rounded once. Beyond that
- * only attention in f16 and bf16 rounds: on FCONV_ATTN_TC its probabilities and its score gradients
- * are 16-bit operands of the products that follow, and on either route the gradient's delta comes
- * from out as it was rounded. With FCONV_ATTN_TC its outputs are off by 1.2 to 1.5 times their own
- * rounding, dq and dk over a few dozen keys by up to 1.8 times. Results do not depend on the order
- * in which blocks run: there are no floating-point atomics.
+ * two operators round in f16 and bf16. Attention on FCONV_ATTN_TC: its probabilities and its score
+ * gradients are 16-bit operands of the products that follow, and on either route the gradient's
+ * delta comes from out as it was rounded. With FCONV_ATTN_TC its outputs are off by 1.2 to 1.5 times
+ * their own rounding, dq and dk over a few dozen keys by up to 1.8 times. The gated feed-forward
+ * block: its hidden values and their gradients, as its section says. Results do not depend on the
+ * order in which blocks run: there are no floating-point atomics.
  */
 #ifndef FCONV_OPS_H_
 #define FCONV_OPS_H_
@@ -115,7 +116,9 @@ void fconv_rope_destroy(fconv_rope_plan* plan);
  *   n = x * r,  r = 1 / sqrt(mean(x^2) + eps),  z = n * w,  y = z turned as by fconv_rope_run
  * Strides and positions are those of fconv_rope_desc; axes = 0 leaves the rotation out (positions
  * and inv_freq are then NULL). Weights have param_dtype, which is dtype or FCONV_F32; q and k have
- * one each, both optional. heads_k = 0 for q alone. head_dim 1..512. */
+ * one each, both optional. heads_k = 0 for q alone. head_dim 1..512. The squares are summed in f32:
+ * a head whose sum passes the type (values of f32 and bf16 past about 1e18) comes out as zeros, its
+ * gradient as zeros or NaN. */
 typedef struct {
   int dtype, param_dtype;
   int64_t batch, len, heads_q, heads_k, head_dim;
@@ -220,8 +223,8 @@ void fconv_attn_destroy(fconv_attn_plan* plan);
  * 6e-5. The 16-bit outputs are off by about 1.4 times their own rounding, over a few dozen hidden
  * values by up to 1.8 in single calls. The forward pass of up to 32 tokens (but on FCONV_MLP_SIMPLE)
  * keeps h to 2^-16 of itself (f16: 2^-22, 2^-36 under 6e-5, up to 65504) and rounds y alone. In f32
- * nothing is rounded to fewer bits (operands are split into parts that add up to them), but that an
- * infinity may come out as NaN. */
+ * nothing is rounded to fewer bits (operands are split into parts that add up to them), but that
+ * values under 2^-110 may lose their last parts and an infinity may come out as NaN. */
 typedef struct {
   int dtype;
   int64_t tokens, features, hidden, out_features;
