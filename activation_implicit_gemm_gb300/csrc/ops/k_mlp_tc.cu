@@ -29,6 +29,14 @@
 // product. The tensor core's f32 sums cut off instead of rounding (measured: 1.7e-8 of the result
 // for each instruction of 16 products, always towards zero), so after 128 of K they are added to
 // registers in plain f32 (after 512 the errors were twice as large, at the same speed).
+//
+// What is cut adds up where terms have one sign: 1.0e-7 of the result for each instruction (measured,
+// positive values), 1.7e-3 for a weight's gradient over 2^18 tokens, 3.5 times f16's rounding. So in
+// 16-bit types, too, a sum of more than kLong steps comes in passes of at most 16384 products (1.0e-4).
+// A thread's part of a tile does not fit its registers there: the sums so far lie in the workspace,
+// each thread reads and writes its own, and all blocks' 20 MB stay in L2. Passes of at most 4096, 8192
+// and 16384: 2122, 2105 and 2067 us for 16384 x 4096 x 10240 forward (its down projection sums 10240
+// values), 950, 915 and 866 us for 2048 x 16384 x 8192; 2070 and 870 without passes.
 #include "mlp_math.cuh"
 #include "split_bf16.cuh"
 #include "tc_instr.cuh"
@@ -52,6 +60,7 @@ enum { kPlain, kGated, kGrad };
 
 constexpr int kPlanes = 3, kTerms = 6;  // of f32
 constexpr int kChunk = 2;               // steps of K whose sums stay in TMEM, f32
+constexpr int kLong = 256;              // and in 16-bit types
 
 template <int EPI, bool F32>  // of an epilogue warp
 constexpr int kSlots = EPI == kPlain ? 2 : EPI == kGated ? (F32 ? kPlanes : 2) : F32 ? 2 * kPlanes : 3;
@@ -74,6 +83,7 @@ struct Job {
   int problems, tiles;
   int splits;  // blocks of a tile, SPLIT
   float* saved;
+  float* sums;  // of passes, 128 rows of each block's columns
   int64_t quads;
   float alpha;
   int act, bf16;
@@ -254,11 +264,16 @@ __device__ __forceinline__ Range range_of(const Problem& p, int products, int ra
   r.hi = (int)((int64_t)all * (rank + 1) / splits);
   return r;
 }
-// They come in passes, each into an accumulator of its own: one for 16-bit types, for f32 one for
-// every kChunk steps (of one product), six terms each.
+// They come in passes, each into an accumulator of its own: for 16-bit types as few and as even ones
+// as kLong allows, for f32 one for every kChunk steps (of one product), six terms each.
 template <bool F32>
 __device__ __forceinline__ int pass_steps(const Problem& p, const Range& r, int at) {
-  if (!F32) return r.hi - at;
+  if (!F32) {
+    const int all = r.hi - r.lo;
+    if (all <= kLong) return all;
+    const int passes = (all + kLong - 1) / kLong;
+    return min((all + passes - 1) / passes, r.hi - at);
+  }
   return min(min(kChunk, r.hi - at), p.steps - at % p.steps);
 }
 struct Step {
@@ -743,6 +758,36 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
         }
       };
 
+      // The sums of the passes so far, each thread's own, 16 bytes a lane (16-bit types: the columns
+      // of a row that a thread has do not fit its registers).
+      auto sums_of = [&](int c) {
+        constexpr int kEach = EPI == kGated ? 16 : 8;  // accesses of a part
+        const int64_t first_access =
+            ((int64_t)blockIdx.x * kEpiWarps + (warp - kFirstEpiWarp)) * kParts + c;
+        return reinterpret_cast<float4*>(j.sums) + first_access * kEach * 32 + lane;
+      };
+      auto add_sums = [&](int c, float (&x)[32], float (&u)[32]) {
+        const float4* from = sums_of(c);
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const float4 v = __ldcg(from + i / 4 * 32);
+          x[i] += v.x, x[i + 1] += v.y, x[i + 2] += v.z, x[i + 3] += v.w;
+          if (EPI == kGated) {
+            const float4 w = __ldcg(from + (8 + i / 4) * 32);
+            u[i] += w.x, u[i + 1] += w.y, u[i + 2] += w.z, u[i + 3] += w.w;
+          }
+        }
+      };
+      auto put_sums = [&](int c, const float (&x)[32], const float (&u)[32]) {
+        float4* to = sums_of(c);
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          __stcg(to + i / 4 * 32, make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
+          if (EPI == kGated)
+            __stcg(to + (8 + i / 4) * 32, make_float4(u[i], u[i + 1], u[i + 2], u[i + 3]));
+        }
+      };
+
       // All sums of this warp's part of the tile.
       auto collect = [&](float (&x)[kParts][32], float (&u)[kUps][32]) {
         const Range r = range_of(p, EPI == kGated ? 1 : p.products, part, splits);
@@ -818,18 +863,26 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
           finish(first_part + c, c + 1 < kParts ? first_part + c + 1 : -1, x[c],
                  u[EPI == kGated ? c : 0]);
       } else {
-        if (!arrive()) break;
+        const Range r = range_of(p, EPI == kGated ? 1 : p.products, part, splits);
+        for (int at = r.lo, len; at < r.hi; at += len, ++n) {
+          len = pass_steps<F32>(p, r, at);
+          if (!arrive()) break;
 #pragma unroll 1
-        for (int c = 0; c < kParts; ++c) {
-          uint32_t r0[32], r1[32];
-          float x[32], u[32];
-          fetch(c, r0, r1);
-          if (c + 1 == kParts) release();
-          as_floats(x, r0);
-          if (EPI == kGated) as_floats(u, r1);
-          finish(first_part + c, c + 1 < kParts ? first_part + c + 1 : -1, x, u);
+          for (int c = 0; c < kParts; ++c) {
+            uint32_t r0[32], r1[32];
+            float x[32], u[32];
+            fetch(c, r0, r1);
+            if (c + 1 == kParts) release();
+            as_floats(x, r0);
+            if (EPI == kGated) as_floats(u, r1);
+            if (at > r.lo) add_sums(c, x, u);
+            if (at + len < r.hi)
+              put_sums(c, x, u);
+            else
+              finish(first_part + c, c + 1 < kParts ? first_part + c + 1 : -1, x, u);
+          }
         }
-        ++n;
+        if (!ok) break;
       }
     }
     if (lane == 0) bulk_wait_all();
@@ -883,8 +936,9 @@ struct Builder {
   bool ok = enc != nullptr, bf16;
   static constexpr int kCols = EPI == kGated ? 64 * CG : 128 * CG;
 
-  Builder(const fconv_mlp_desc& d, float* saved) {
+  Builder(const fconv_mlp_desc& d, float* saved, float* pass_sums) {
     j.saved = saved;
+    j.sums = pass_sums;
     j.quads = (d.hidden + 3) / 4;
     j.act = d.activation;
     j.alpha = d.alpha;
@@ -928,6 +982,9 @@ struct Builder {
   }
   int launch(int sms, int splits, cudaStream_t s) {
     if (!ok) return (int)cudaErrorInvalidValue;
+    for (int i = 0; i < j.problems; ++i)  // a layout without room for what it needs
+      if (!F32 && !j.sums && j.p[i].products * j.p[i].steps > kLong)
+        return (int)cudaErrorInvalidValue;
     if (j.tiles == 0) return 0;
     j.splits = splits;
     if constexpr (CG == 1) {
@@ -962,13 +1019,14 @@ struct Builder {
 struct Inputs {
   Matrix x, gate, up, down, dy;
   Matrix h, dg, du;
+  float* pass_sums;  // of 16-bit types where a sum is long, else null
 };
 
 // h, and where `saved` is given the projections.
 template <int CG, bool F32>
 int gated(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const Inputs& in,
           cudaStream_t s) {
-  Builder<CG, kGated, F32> b(d, a.saved);
+  Builder<CG, kGated, F32> b(d, a.saved, in.pass_sums);
   Problem& p = b.add(d.tokens, d.hidden, d.features, false, false);
   b.product(p, in.x, in.gate);
   b.operand(&p.b[1], in.up, false, CG == 1 ? 64 : 128);
@@ -981,7 +1039,7 @@ int gated(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const 
 template <int CG, bool F32>
 int down(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const Inputs& in,
          cudaStream_t s) {
-  Builder<CG, kPlain, F32> b(d, nullptr);
+  Builder<CG, kPlain, F32> b(d, nullptr, in.pass_sums);
   Problem& p = b.add(d.tokens, d.out_features, d.hidden, false, false);
   b.product(p, in.h, in.down);
   p.bias[0] = a.b_down;
@@ -992,7 +1050,7 @@ int down(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const I
 template <int CG, bool F32>
 int grads_of_projections(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a,
                          const Inputs& in, cudaStream_t s) {
-  Builder<CG, kGrad, F32> b(d, a.saved);
+  Builder<CG, kGrad, F32> b(d, a.saved, in.pass_sums);
   Problem& p = b.add(d.tokens, d.hidden, d.out_features, false, true);
   b.product(p, in.dy, in.down);
   b.inner(p, 0, in.dg);
@@ -1005,7 +1063,7 @@ int grads_of_projections(const fconv_mlp_desc& d, int sms, int splits, const Mlp
 template <int CG, bool F32>
 int gradients(const fconv_mlp_desc& d, int sms, int splits, const MlpArgs& a, const Inputs& in,
               cudaStream_t s) {
-  Builder<CG, kPlain, F32> b(d, nullptr);
+  Builder<CG, kPlain, F32> b(d, nullptr, in.pass_sums);
   if (a.dx) {
     Problem& p = b.add(d.tokens, d.features, d.hidden, false, true);
     b.product(p, in.dg, in.gate);
@@ -1126,6 +1184,13 @@ Layout layout(const fconv_mlp_desc& d, const MlpArgs& a, bool backward, int sms)
     return m;
   };
   l.in.h = fresh(d.tokens, d.hidden);
+  // each block's share of the largest tile: 128 rows of 256 columns (few tokens: of the backward pass)
+  int64_t longest = d.features > d.hidden ? d.features : d.hidden;
+  if (backward) {  // over tokens and outputs too, and over both projections of hidden values
+    for (int64_t k : {2 * d.hidden, d.tokens, d.out_features}) longest = k > longest ? k : longest;
+  }
+  if (planes == 1 && longest > kLong * kStep)
+    l.in.pass_sums = (float*)take((size_t)sms * 128 * 256 * sizeof(float));
   if (backward) {
     l.in.dg = fresh(d.tokens, d.hidden);
     l.in.du = fresh(d.tokens, d.hidden);
