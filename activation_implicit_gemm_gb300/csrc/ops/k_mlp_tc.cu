@@ -19,8 +19,8 @@
 // blocks shares a tile (SPLIT): each takes a part of K, leaves its sums in shared memory and finishes
 // some of the columns, adding the blocks' parts in their order.
 //
-// Bound: the tensor pipe, busy throughout at 16384 x 4096 x 10240 in bf16 (1388 and 728 us alone, 1.9
-// to 2.0 PFLOP/s; 2.34 to 2.41 ms in passes under the power cap). Short sums (768 of K) leave the
+// Bound: the tensor pipe, busy throughout at 16384 x 4096 x 10240 in bf16 (1390 to 1420 and 730 to 740 us
+// alone, 1.9 to 2.0 PFLOP/s; 2.34 to 2.41 ms in passes under the power cap). Short sums (768 of K) leave the
 // epilogues and their traffic to bound it: 48 us for the gated product of 6304 x 768 x 2048 with g
 // and u going out in f32, 27 without.
 //
@@ -1094,8 +1094,9 @@ Group group_of(int64_t M, int64_t N, int64_t K, int products) {
 
 // The blocks of a launch: what takes the least time, counted in steps of a single SM's tile (0.19 us
 // where operands come from HBM). A step of a pair of SMs takes 1.2 of them, a round of tiles 4 to 6
-// more, a cluster's start and its exchange of sums 12 to 24 (196 tokens, 2048 to 768: 13.7 us with 12
-// blocks, 12.2, 10.9 and 12.0 with 2, 4 and 8 times as many; 768 to 2048 in 64 tiles: 9.9 and 11.4).
+// more, a cluster's start and its exchange of sums 12 to 24 (196 tokens, each product launched by itself:
+// 2048 to 768 takes 13.7 us with 12 blocks, 12.2, 10.9 and 12.0 with 2, 4 and 8 times as many, 768 to 2048
+// in 64 tiles 9.9 and 11.4; in a captured graph, where one starts as the other ends, both take 15).
 // Clusters of 4 and 8 leave SMs of a GPC unused.
 Shape shape_of(const fconv_mlp_desc& d, const Group* g, int n, int sms) {
   constexpr double kRound = 4.0, kSplitRound = 6.0, kPair = 1.2, kGain = 0.93;

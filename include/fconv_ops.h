@@ -223,9 +223,9 @@ void fconv_attn_destroy(fconv_attn_plan* plan);
  * 6e-5. The 16-bit outputs are off by about 1.4 times their own rounding, over a few dozen hidden
  * values by up to 1.8 in single calls. The forward pass of up to 32 tokens (but on FCONV_MLP_SIMPLE)
  * keeps h to 2^-16 of itself (f16: 2^-22, 2^-36 under 6e-5, up to 65504) and rounds y alone. 16-bit
- * sums on tensor cores lose up to 1e-4 of themselves where all terms have one sign, however long. In f32
- * nothing is rounded to fewer bits (operands are split into parts that add up to them), but that
- * values under 2^-110 may lose their last parts and an infinity may come out as NaN. */
+ * sums on tensor cores lose up to 1e-4 of themselves where all terms have one sign, however long.
+ * In f32 nothing is rounded to fewer bits (operands are split into parts that add up to them), but
+ * that values under 2^-110 may lose their last parts and an infinity may come out as NaN. */
 typedef struct {
   int dtype;
   int64_t tokens, features, hidden, out_features;
