@@ -75,3 +75,20 @@ def test_strided_rows():
                      out=out[:, 1:1 + o])
         check(out[:, 1:1 + o], x, wg, wu, wd, b, "Silu")
         assert (out[:, 0] == 9).all() and (out[:, 1 + o:] == 9).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("n,f", [(1, 5), (9, 517), (30, 775), (3, 64)])
+def test_what_the_workspace_held_is_not_read(n, f, dtype):
+    """A workspace of NaN: rows of hidden values end inside a unit of 16 bytes."""
+    c, o, T = 40, 24, R.TYPES[dtype]
+    x, wg, wu, wd, b, _ = case(430, n, c, f, o, T)
+    dev = [t.contiguous().cuda() for t in (x, wg, wu, wd, *b)]
+    p = fc.MlpPlan(_ops._code(T), n, c, f, o, x_stride=c, y_stride=o, gate_stride=c, up_stride=c,
+                   down_stride=f, has_b_gate=True, has_b_up=True, has_b_down=True)
+    ws = torch.full((p.forward_workspace,), 255, dtype=torch.uint8, device="cuda")
+    y = torch.empty((n, o), dtype=T, device="cuda")
+    p.forward_ptrs(*(t.data_ptr() for t in dev), y.data_ptr(), None, ws.data_ptr(), ws.numel(),
+                   torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    check(y, x, wg, wu, wd, b, "Silu")
