@@ -22,6 +22,7 @@ def cuda_lib():
     if not torch.cuda.is_available():
         pytest.skip("needs a CUDA GPU")
     _build.build()
+    _ops._start()
     yield
     _ops.check_device()
 
