@@ -19,8 +19,8 @@
 // blocks shares a tile (SPLIT): each takes a part of K, leaves its sums in shared memory and finishes
 // some of the columns, adding the blocks' parts in their order.
 //
-// Bound: the tensor pipe, busy throughout at 16384 x 4096 x 10240 in bf16 (1390 to 1420 and 730 to 740 us
-// alone, 1.9 to 2.0 PFLOP/s; 2.34 to 2.41 ms in passes under the power cap). Short sums (768 of K) leave the
+// Bound: the tensor pipe, busy throughout at 16384 x 4096 x 10240 in bf16 (1375 to 1390 and 718 to 728 us
+// alone, 1.9 to 2.0 PFLOP/s; 2.31 to 2.41 ms in passes under the power cap). Short sums (768 of K) leave the
 // epilogues and their traffic to bound it: 48 us for the gated product of 6304 x 768 x 2048 with g
 // and u going out in f32, 27 without.
 //
@@ -36,7 +36,9 @@
 // A thread's part of a tile does not fit its registers there: the sums so far lie in the workspace,
 // each thread reads and writes its own, and all blocks' 20 MB stay in L2. Passes of at most 4096, 8192
 // and 16384: 2122, 2105 and 2067 us for 16384 x 4096 x 10240 forward (its down projection sums 10240
-// values), 950, 915 and 866 us for 2048 x 16384 x 8192; 2070 and 870 without passes.
+// values), 950, 915 and 866 us for 2048 x 16384 x 8192; 2070 and 870 without passes. Calls whose sums
+// take one pass have kernels without that code (LONG), which costs them 1 %: 2380 and 2402 us for the
+// first shape in passes under the power cap, 184 and 185.6 for both passes of 6304 x 768 x 2048.
 #include "mlp_math.cuh"
 #include "split_bf16.cuh"
 #include "tc_instr.cuh"
@@ -423,7 +425,8 @@ __device__ __forceinline__ void gate_grad_planes(uint32_t slots, int row, int c0
   if (!GATE) stage_planes(slots + kPlanes * kSlot, row, c0, h);
 }
 
-template <int CG, int EPI, bool F32, bool SPLIT>
+// LONG: a 16-bit tile's sums may come in several passes (without SPLIT).
+template <int CG, int EPI, bool F32, bool SPLIT, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Job j) {
   constexpr int S = kStages<EPI, F32>, BN = 128 * CG;
   constexpr int kCols = EPI == kGated ? BN / 2 : BN;  // of a tile of D
@@ -865,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
       } else {
         const Range r = range_of(p, EPI == kGated ? 1 : p.products, part, splits);
         for (int at = r.lo, len; at < r.hi; at += len, ++n) {
-          len = pass_steps<F32>(p, r, at);
+          len = LONG ? pass_steps<F32>(p, r, at) : r.hi - at;
           if (!arrive()) break;
 #pragma unroll 1
           for (int c = 0; c < kParts; ++c) {
@@ -875,8 +878,8 @@ __global__ void __launch_bounds__(kThreads, 1) mlp_tc(const __grid_constant__ Jo
             if (c + 1 == kParts) release();
             as_floats(x, r0);
             if (EPI == kGated) as_floats(u, r1);
-            if (at > r.lo) add_sums(c, x, u);
-            if (at + len < r.hi)
+            if (LONG && at > r.lo) add_sums(c, x, u);
+            if (LONG && at + len < r.hi)
               put_sums(c, x, u);
             else
               finish(first_part + c, c + 1 < kParts ? first_part + c + 1 : -1, x, u);
@@ -982,21 +985,25 @@ struct Builder {
   }
   int launch(int sms, int splits, cudaStream_t s) {
     if (!ok) return (int)cudaErrorInvalidValue;
-    for (int i = 0; i < j.problems; ++i)  // a layout without room for what it needs
-      if (!F32 && !j.sums && j.p[i].products * j.p[i].steps > kLong)
-        return (int)cudaErrorInvalidValue;
     if (j.tiles == 0) return 0;
     j.splits = splits;
     if constexpr (CG == 1) {
-      if (splits > 1) return start<true>(j.tiles * splits, splits, s);
+      if (splits > 1) return start<true, false>(j.tiles * splits, splits, s);
     }
-    const int most = sms / CG;
-    return start<false>((j.tiles < most ? j.tiles : most) * CG, CG, s);
+    const int most = sms / CG, blocks = (j.tiles < most ? j.tiles : most) * CG;
+    if constexpr (!F32) {
+      bool passes = false;
+      for (int i = 0; i < j.problems; ++i)
+        passes = passes || j.p[i].products * j.p[i].steps > kLong;
+      if (passes && !j.sums) return (int)cudaErrorInvalidValue;  // the layout has no room for them
+      if (passes) return start<false, true>(blocks, CG, s);
+    }
+    return start<false, false>(blocks, CG, s);
   }
-  template <bool SPLIT>
+  template <bool SPLIT, bool LONG>
   int start(int blocks, int cluster, cudaStream_t s) {
     const size_t smem = kStages<EPI, F32> * 2 * kSide + kEpiWarps * kSlots<EPI, F32> * kSlot;
-    auto kernel = mlp_tc<CG, EPI, F32, SPLIT>;
+    auto kernel = mlp_tc<CG, EPI, F32, SPLIT, LONG>;
     if (const int e = allow_smem((const void*)kernel, smem)) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
